@@ -12,7 +12,10 @@ import ctypes
 import os
 from typing import Optional
 
+from . import kv_cache as _kv
 from . import plan  # noqa: F401  (host-side sizing rules)
+from .kv_cache import (KV_STATUS_BITS, KVCache, alloc_kv_cache, alloc_kv_workspace, kv_append, kv_attention,  # noqa: F401
+                       kv_compact, kv_copy_pages, kv_fork, kv_free, kv_reserve, kv_scratch_bytes, kv_status)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmqatopk.so")
@@ -89,6 +92,7 @@ def lib():
     L.mqa_topk_strerror.restype = ctypes.c_char_p
     for name in EXPORTS[:-1]:
         getattr(L, name).restype = I
+    _kv.declare(L)
     _lib = L
     return L
 

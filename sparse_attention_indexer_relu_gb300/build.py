@@ -30,8 +30,11 @@ SOURCES = [("mqa_fused.cu", "mqa_fused.o", []), ("mqa_fused.cu", "mqa_fused_fold
            ("mqa_fused.cu", "mqa_fused_masked.o", ["-DMQA_MASKED=1", "-DMQA_RELU_ALU_CHUNKS=0"]),
            ("mqa_fused.cu", "mqa_fused_pairs.o", ["-DMQA_PAIR_HELPERS=1"]),
            ("mqa_gather.cu", "mqa_gather.o", []), ("mqa_aux.cu", "mqa_aux.o", []),
-           ("mqatopk_api.cu", "mqatopk_api.o", [])]
-HEADERS = ["mqa_internal.h", "ptx.cuh", "mqa_fold.h"]
+           ("mqatopk_api.cu", "mqatopk_api.o", []),
+           # the paged key/value cache
+           ("kv_attn.cu", "kv_attn.o", []), ("kv_append.cu", "kv_append.o", []), ("kv_pages.cu", "kv_pages.o", []),
+           ("kv_api.cu", "kv_api.o", [])]
+HEADERS = ["mqa_internal.h", "ptx.cuh", "mqa_fold.h", "kv_internal.h", "kv_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -56,6 +59,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     # the compile flags live in this file: a change to it rebuilds every object
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "mqatopk.h"),
+                                                       os.path.join(ROOT, "include", "mqakv.h"),
                                                        os.path.abspath(__file__)]
     objs, jobs = [], []
     for src, obj, defs in SOURCES:

@@ -1,0 +1,277 @@
+// C ABI of the paged key/value cache (include/mqakv.h): argument checks,
+// workspace sizing and launches.  Host code only.
+#include "kv_internal.h"
+
+#include <climits>
+#include <cstring>
+
+namespace {
+
+using namespace mqa;
+
+inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }
+
+int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1; }
+
+// What a call needs of the cache beside its codes, exponents and scratch.
+enum Needs { kTables = 1, kRefs = 2 };
+
+int check_cache(const mqa_kv_cache *c, int needs) {
+  if (!c) return MQA_ERR_INVALID_ARGUMENT;
+  if (c->num_pages < 1 || log2_of(c->page_size) < 0 || c->kv_heads < 1 || c->kv_heads > 256 ||
+      (c->head_dim != 64 && c->head_dim != 128) || c->max_seqs < 1 || c->max_seqs > MQA_KV_MAX_SEQS ||
+      c->max_pages < 1 || c->n_extra < 0 || c->n_extra > MQA_KV_MAX_EXTRA)
+    return MQA_ERR_INVALID_ARGUMENT;
+  if ((long long)c->num_pages * c->kv_heads * c->page_size > INT_MAX ||
+      (long long)c->max_pages * c->page_size > INT_MAX)
+    return MQA_ERR_INVALID_ARGUMENT;
+  if (!c->k || !c->v || !c->k_exps || !c->v_exps || !c->scratch) return MQA_ERR_INVALID_ARGUMENT;
+  if ((needs & kTables) && (!c->page_table || !c->seq_lens)) return MQA_ERR_INVALID_ARGUMENT;
+  if ((needs & kRefs) && !c->refcounts) return MQA_ERR_INVALID_ARGUMENT;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->scratch, 256) || !aligned(c->page_table, 4) ||
+      !aligned(c->seq_lens, 4) || !aligned(c->refcounts, 4))
+    return MQA_ERR_MISALIGNED;
+  for (int i = 0; i < c->n_extra; ++i)
+    if (!c->extra[i].data || c->extra[i].page_bytes == 0) return MQA_ERR_INVALID_ARGUMENT;
+  if (c->scratch_bytes < kv_scratch(c->num_pages, c->max_seqs).total) return MQA_ERR_WORKSPACE_TOO_SMALL;
+  return MQA_OK;
+}
+
+KvView view_of(const mqa_kv_cache *c) {
+  KvView v;
+  v.k = c->k;
+  v.v = c->v;
+  v.k_exps = c->k_exps;
+  v.v_exps = c->v_exps;
+  v.table = c->page_table;
+  v.lens = c->seq_lens;
+  v.refs = c->refcounts;
+  v.status = reinterpret_cast<int32_t *>(c->scratch) + kKvStatus;
+  v.pages = c->num_pages;
+  v.page = c->page_size;
+  v.page_log2 = log2_of(c->page_size);
+  v.heads = c->kv_heads;
+  v.dim = c->head_dim;
+  v.seqs = c->max_seqs;
+  v.max_pages = c->max_pages;
+  return v;
+}
+
+KvLists lists_of(const mqa_kv_cache *c) {
+  const KvScratch s = kv_scratch(c->num_pages, c->max_seqs);
+  uint8_t *b = reinterpret_cast<uint8_t *>(c->scratch);
+  auto at = [&](size_t off) { return reinterpret_cast<int32_t *>(b + off); };
+  return KvLists{at(0), at(s.src), at(s.dst), at(s.rank), at(s.seq_a), at(s.seq_b), at(s.sums)};
+}
+
+KvPools pools_of(const mqa_kv_cache *c) {
+  KvPools p;
+  std::memset(&p, 0, sizeof p);
+  auto add = [&](void *data, size_t bytes) {
+    p.data[p.n] = reinterpret_cast<uint8_t *>(data);
+    p.bytes[p.n++] = bytes;
+  };
+  const size_t codes = (size_t)c->kv_heads * c->page_size * c->head_dim;
+  add(c->k, codes);
+  add(c->v, codes);
+  add(c->k_exps, (size_t)c->kv_heads);
+  add(c->v_exps, (size_t)c->kv_heads);
+  for (int i = 0; i < c->n_extra; ++i) add(c->extra[i].data, c->extra[i].page_bytes);
+  return p;
+}
+
+int code(cudaError_t e) {
+  if (e == cudaSuccess) return MQA_OK;
+  cudaGetLastError();
+  return MQA_ERR_CUDA;
+}
+
+// Column blocks of the split kernel: 8, 16 or 32 columns.
+struct AttnPlan {
+  int nb, ctas;
+  size_t slots_off, bytes;
+};
+AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, int q_heads, bool selected) {
+  const int group = q_heads / c->kv_heads;
+  if (max_rows <= 0 || max_rows > rows) max_rows = rows;
+  const long long cols = selected ? group : (long long)group * max_rows;
+  AttnPlan p;
+  p.nb = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+  p.ctas = sms * attn_ctas_per_sm(p.nb);
+  p.slots_off = ((size_t)p.ctas * sizeof(int4) + 255) / 256 * 256;
+  p.bytes = p.slots_off + (size_t)p.ctas * 2 * attn_slot_floats(p.nb, c->head_dim) * sizeof(float);
+  return p;
+}
+
+int check_attention(const mqa_kv_cache *c, int rows, int q_heads) {
+  const int rc = check_cache(c, kTables);
+  if (rc != MQA_OK) return rc;
+  if (rows < 0 || q_heads < 1 || q_heads % c->kv_heads != 0 || q_heads > 65536) return MQA_ERR_INVALID_ARGUMENT;
+  return MQA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mqa_kv_scratch_bytes(int num_pages, int max_seqs, size_t *bytes) {
+  if (!bytes || num_pages < 1 || max_seqs < 1 || max_seqs > MQA_KV_MAX_SEQS) return MQA_ERR_INVALID_ARGUMENT;
+  *bytes = kv_scratch(num_pages, max_seqs).total;
+  return MQA_OK;
+}
+
+int mqa_kv_append(const mqa_kv_cache *cache, const void *k, const void *v, long long k_row_stride,
+                  long long v_row_stride, int type, const int32_t *row_starts, int rows, void *stream) {
+  int rc = check_cache(cache, kTables);
+  if (rc != MQA_OK) return rc;
+  if (rows < 0 || type < MQA_KV_BF16 || type > MQA_KV_FP32) return MQA_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return MQA_OK;
+  const long long width = (long long)cache->kv_heads * cache->head_dim;
+  if (!k || !v || !row_starts || (rows > 1 && (k_row_stride < width || v_row_stride < width)))
+    return MQA_ERR_INVALID_ARGUMENT;
+  const int per16 = type == MQA_KV_FP32 ? 4 : 8;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(row_starts, 4) || k_row_stride % per16 || v_row_stride % per16)
+    return MQA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = require_device(&sms);
+  if (rc != MQA_OK) return rc;
+  return code(launch_kv_append(view_of(cache), k, v, k_row_stride, v_row_stride, type, row_starts, rows, sms,
+                               as_stream(stream)));
+}
+
+int mqa_kv_attention_workspace_bytes(int device, const mqa_kv_cache *cache, int rows, int q_heads, size_t *bytes) {
+  int rc = check_attention(cache, rows, q_heads);
+  if (rc != MQA_OK) return rc;
+  if (!bytes) return MQA_ERR_INVALID_ARGUMENT;
+  int sms = 0;
+  rc = device_sms(device, &sms);
+  if (rc != MQA_OK) return rc;
+  // the largest of the forms that a call with these sizes may take
+  size_t most = 0;
+  for (const int nb_rows : {1, rows}) {
+    const size_t a = plan_attention(sms, cache, rows, nb_rows, q_heads, false).bytes;
+    most = a > most ? a : most;
+  }
+  *bytes = most;
+  return MQA_OK;
+}
+
+int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_stride, int type, int q_heads,
+                     const int32_t *row_starts, int rows, int max_rows, const int32_t *selected, int n_selected,
+                     int causal, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+  int rc = check_attention(cache, rows, q_heads);
+  if (rc != MQA_OK) return rc;
+  if ((type != MQA_KV_BF16 && type != MQA_KV_FP16) || n_selected < 0 || (!selected && n_selected > 0) ||
+      !(scale > 0.f && scale < 3.4e38f))
+    return MQA_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return MQA_OK;
+  if (!q || !out || !row_starts || !workspace ||
+      (rows > 1 && q_row_stride < (long long)q_heads * cache->head_dim))
+    return MQA_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(out, 16) || q_row_stride % 8 || !aligned(row_starts, 4) || !aligned(selected, 4) ||
+      !aligned(lse, 4) || !aligned(workspace, 256))
+    return MQA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = require_device(&sms);
+  if (rc != MQA_OK) return rc;
+  const AttnPlan P = plan_attention(sms, cache, rows, max_rows, q_heads, selected != nullptr);
+  if (workspace_bytes < P.bytes) return MQA_ERR_WORKSPACE_TOO_SMALL;
+  AttnParams p;
+  std::memset(&p, 0, sizeof p);
+  p.c = view_of(cache);
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.starts = row_starts;
+  p.selected = selected;
+  p.q_stride = q_row_stride;
+  p.rows = rows;
+  p.q_heads = q_heads;
+  p.group = q_heads / cache->kv_heads;
+  p.n_selected = n_selected;
+  p.causal = causal != 0;
+  p.bf16 = type == MQA_KV_BF16;
+  p.scale_log2 = scale * 1.44269504088896341f;
+  p.max_cols = INT_MAX;
+  p.desc = reinterpret_cast<int4 *>(workspace);
+  p.slots = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + P.slots_off);
+  return code(launch_kv_attention(p, P.nb, P.ctas, as_stream(stream)));
+}
+
+int mqa_kv_reserve(const mqa_kv_cache *cache, const int32_t *counts, void *stream) {
+  int rc = check_cache(cache, kTables | kRefs);
+  if (rc != MQA_OK) return rc;
+  if (!counts) return MQA_ERR_INVALID_ARGUMENT;
+  if (!aligned(counts, 4)) return MQA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = require_device(&sms);
+  if (rc != MQA_OK) return rc;
+  return code(launch_kv_reserve(view_of(cache), lists_of(cache), counts, as_stream(stream)));
+}
+
+int mqa_kv_fork(const mqa_kv_cache *cache, const int32_t *parents, const int32_t *children, int n, void *stream) {
+  int rc = check_cache(cache, kTables | kRefs);
+  if (rc != MQA_OK) return rc;
+  if (n < 0 || n > cache->max_seqs) return MQA_ERR_INVALID_ARGUMENT;  // children are distinct sequences
+  if (n == 0) return MQA_OK;
+  if (!parents || !children) return MQA_ERR_INVALID_ARGUMENT;
+  if (!aligned(parents, 4) || !aligned(children, 4)) return MQA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = require_device(&sms);
+  if (rc != MQA_OK) return rc;
+  return code(launch_kv_fork(view_of(cache), lists_of(cache), pools_of(cache), parents, children, n, sms,
+                             as_stream(stream)));
+}
+
+int mqa_kv_free(const mqa_kv_cache *cache, const int32_t *seqs, int n, void *stream) {
+  int rc = check_cache(cache, kTables | kRefs);
+  if (rc != MQA_OK) return rc;
+  if (n < 0) return MQA_ERR_INVALID_ARGUMENT;
+  if (n == 0) return MQA_OK;
+  if (!seqs) return MQA_ERR_INVALID_ARGUMENT;
+  if (!aligned(seqs, 4)) return MQA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = require_device(&sms);
+  if (rc != MQA_OK) return rc;
+  return code(launch_kv_free(view_of(cache), seqs, n, as_stream(stream)));
+}
+
+int mqa_kv_compact(const mqa_kv_cache *cache, void *stream) {
+  int rc = check_cache(cache, kTables | kRefs);
+  if (rc != MQA_OK) return rc;
+  int sms = 0;
+  rc = require_device(&sms);
+  if (rc != MQA_OK) return rc;
+  return code(launch_kv_compact(view_of(cache), lists_of(cache), pools_of(cache), sms, as_stream(stream)));
+}
+
+int mqa_kv_copy_pages(const mqa_kv_cache *cache, const int32_t *src, const int32_t *dst, int n, void *stream) {
+  int rc = check_cache(cache, 0);
+  if (rc != MQA_OK) return rc;
+  if (n < 0 || n > cache->num_pages) return MQA_ERR_INVALID_ARGUMENT;  // targets are distinct pages
+  if (n == 0) return MQA_OK;
+  if (!src || !dst) return MQA_ERR_INVALID_ARGUMENT;
+  if (!aligned(src, 4) || !aligned(dst, 4)) return MQA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = require_device(&sms);
+  if (rc != MQA_OK) return rc;
+  return code(launch_kv_copy(view_of(cache), lists_of(cache), pools_of(cache), src, dst, n, sms, as_stream(stream)));
+}
+
+int mqa_kv_get_status(const mqa_kv_cache *cache, int32_t *status, void *stream) {
+  int rc = check_cache(cache, 0);
+  if (rc != MQA_OK) return rc;
+  if (!status) return MQA_ERR_INVALID_ARGUMENT;
+  int sms = 0;
+  rc = require_device(&sms);
+  if (rc != MQA_OK) return rc;
+  int32_t *word = reinterpret_cast<int32_t *>(cache->scratch) + kKvStatus;
+  cudaError_t e = cudaMemcpyAsync(status, word, sizeof(int32_t), cudaMemcpyDeviceToHost, as_stream(stream));
+  if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof(int32_t), as_stream(stream));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(as_stream(stream));
+  return code(e);
+}
+
+}  // extern "C"

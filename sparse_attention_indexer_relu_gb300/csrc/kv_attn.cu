@@ -1,0 +1,739 @@
+// Attention over the paged 8-bit cache for few query columns per key/value
+// head: single tokens, short runs of them, and rows that each read their own
+// selected keys.  (include/mqakv.h, mqa_kv_attention.)
+//
+// Mathematics.  The columns of an item are (query row, query head) pairs that
+// read the same key/value head.  With c = scale * log2(e) and s = c * 2^(ke -
+// 127) * q . E(k), in base 2,
+//     out = sum_t 2^(s_t - m) 2^(ve_t - 127) E(v_t) / sum_t 2^(s_t - m).
+// The codes are exact in fp16, so both products run on the tensor cores in
+// fp16 with fp32 accumulation: q enters times a power of two that brings its
+// column's largest magnitude to 2^10 (exact for bf16 and fp16 down to 2^-34 of
+// it), and the weights enter as p' = 2^(s + lv - w), lv = ve - 127, with a
+// running reference w of their own, so that a weight is rounded to fp16
+// relative to the largest weight TIMES scale that its column has seen (11
+// bits; a weight 2^-24 below it still has one).  The sum of the softmax is
+// kept in fp32 from unrounded weights against a second reference m.  Both
+// references move only when a value passes them by 2^8.
+//
+// Layout.  S^T = K Q^T and O^T = V^T P^T: keys are the M dimension of the
+// first product and head components that of the second, so 8 columns fill an
+// MMA's N.  The order of the contraction index is free as long as both
+// operands agree, so a lane takes 32 contiguous bytes of a key row (K) and 16
+// contiguous components of 4 keys (V), converts them in registers and needs no
+// transposed loads; P passes from one product to the other by an 8 x 8
+// transpose of registers.
+//
+// Split.  All items' key tiles form one line that is cut evenly between the
+// CTAs of a fixed grid, whatever the lengths; a CTA's range begins and ends
+// inside items, for which it leaves partial results in its two workspace
+// slots, and a second kernel joins them in CTA order.
+#include "kv_internal.h"
+#include "kv_ptx.cuh"
+
+#include <cfloat>
+
+namespace mqa {
+
+namespace {
+
+constexpr int kWarps = kAttnThreads / 32;
+constexpr int kTile = 16 * kWarps;  // keys per unit of work: one 16-key sub-tile per warp
+constexpr float kSlack = 8.0f;      // a reference moves when a value passes it by 2^8: p' <= 2^8 in fp16
+constexpr int kStages = 3;          // sub-tiles in flight per warp: 2 x 16 warps x 4 KB ahead on an SM
+
+template <int NB>
+struct Cfg {
+  static constexpr int ctas = NB == 1 ? 4 : NB == 2 ? 3 : 2;
+};
+
+template <int D>
+__host__ __device__ constexpr int stage_bytes() {
+  return 2 * 16 * D;
+}
+
+// Per-warp stage descriptions: scale, exponent and position of its keys.
+struct Meta {
+  float ks[kStages][16];
+  float lv[kStages][16];
+  int pos[kStages][16];
+};
+
+template <int D, int NB>
+struct Smem {
+  union {
+    uint8_t ring[kWarps][kStages][2 * 16 * D];
+    float merge[8 * NB][D + 4];
+  };
+  Meta meta[kWarps];
+  float cs[8 * NB];             // per column: scale * log2(e) / (power of two q was multiplied with)
+  int lim[8 * NB];              // positions the column sees: [0, lim)
+  float wm[kWarps][8 * NB], ww[kWarps][8 * NB], wl[kWarps][8 * NB];
+  uint32_t qf[NB > 2 ? NB : 1][D / 8][32];  // q fragments (NB > 2)
+  long long scan[kWarps];
+  int found[2];
+  long long found_at;
+};
+
+struct Item {
+  int seq, head, cb;   // sequence (or row, for selected keys), key/value head, column block
+  int tiles;           // key tiles of the item
+};
+
+}  // namespace
+
+int attn_ctas_per_sm(int nb) { return nb == 1 ? Cfg<1>::ctas : nb == 2 ? Cfg<2>::ctas : Cfg<4>::ctas; }
+size_t attn_slot_floats(int nb, int dim) { return (size_t)8 * nb * (dim + 4); }
+
+namespace {
+
+// e4m3 code pair (low 16 bits) to fp16 pair.
+__device__ __forceinline__ uint32_t cvt2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t cvt2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// Bytes of w that hold a NaN code (0x7F or 0xFF), as 0x80 bits.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+template <int D, int NB, bool SEL>
+__global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(const AttnParams p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  using S = Smem<D, NB>;
+  S &sm = *reinterpret_cast<S *>(smem_raw);
+  constexpr int CB = 8 * NB;
+  constexpr int KW = D / 16;   // words of a K row per lane (8 or 4)
+  constexpr int VW = D / 32;   // words of a V row per lane (4 or 2)
+  constexpr int MT = D / 16;   // 16-component tiles of O^T
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int heads = p.c.heads, group = p.group;
+  const int nsel_tiles = SEL ? max(1, (p.n_selected + kTile - 1) / kTile) : 1;
+  const int ncb_sel = (group + CB - 1) / CB;
+
+  // ---- this CTA's range of the line of work
+  // sequence s: rows [r0, r1), length; units = heads * column blocks * tiles
+  auto rows_of = [&](int s, int &r0, int &n) {
+    r0 = min(max(p.starts[s], 0), p.rows);
+    n = max(min(p.starts[s + 1], p.rows) - r0, 0);
+  };
+  auto length_of = [&](int s) { return min(max(p.c.lens[s], 0), p.c.max_pages << p.c.page_log2); };
+  auto shape_of = [&](int s, int &ncb, int &tiles) {  // column blocks and tiles per item of sequence s
+    int r0, n;
+    rows_of(s, r0, n);
+    const long long cols = (long long)n * group;
+    ncb = cols > p.max_cols ? 0 : (int)((cols + CB - 1) / CB);
+    tiles = ncb ? max(1, (length_of(s) + kTile - 1) / kTile) : 0;
+  };
+  long long total;
+  const int per_thread = (p.c.seqs + kAttnThreads - 1) / kAttnThreads;
+  long long mine = 0, before = 0;
+  if (SEL) {
+    int last = min(max(p.starts[p.c.seqs], 0), p.rows);
+    total = (long long)last * heads * ncb_sel * nsel_tiles;
+  } else {
+    for (int i = 0; i < per_thread; ++i) {
+      const int s = tid * per_thread + i;
+      if (s >= p.c.seqs) break;
+      int ncb, tiles;
+      shape_of(s, ncb, tiles);
+      mine += (long long)heads * ncb * tiles;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sm.scan[warp] = incl;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sm.scan[w];
+      total += sm.scan[w];
+    }
+    before += incl - mine;
+  }
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  long long at = blockIdx.x * per;
+  const long long end = min(total, at + per);
+  if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (at >= end) return;  // the whole CTA leaves together
+  Item it;
+  int tile;  // first tile of the current segment
+  if (SEL) {
+    const long long item = at / nsel_tiles;
+    it.tiles = nsel_tiles;
+    tile = (int)(at - item * nsel_tiles);
+    it.cb = (int)(item % ncb_sel);
+    it.head = (int)(item / ncb_sel % heads);
+    it.seq = (int)(item / ((long long)ncb_sel * heads));  // the row
+  } else {
+    if (at >= before && at < before + mine) {
+      long long b = before;
+      for (int i = 0; i < per_thread; ++i) {
+        const int s = tid * per_thread + i;
+        int ncb, tiles;
+        shape_of(s, ncb, tiles);
+        const long long u = (long long)heads * ncb * tiles;
+        if (at < b + u) {
+          sm.found[0] = s;
+          sm.found_at = at - b;
+          break;
+        }
+        b += u;
+      }
+    }
+    __syncthreads();
+    it.seq = sm.found[0];
+    int ncb;
+    shape_of(it.seq, ncb, it.tiles);
+    const long long item = sm.found_at / it.tiles;
+    tile = (int)(sm.found_at - item * it.tiles);
+    it.cb = (int)(item % ncb);
+    it.head = (int)(item / ncb);
+  }
+
+  Meta &meta = sm.meta[warp];
+  while (at < end) {
+    const int t0 = tile, t1 = (int)min((long long)it.tiles, t0 + (end - at));
+    // ---- the item's rows, columns and limits
+    int r0, n, seq = it.seq, ncb;
+    if (SEL) {
+      int lo = 0, hi = p.c.seqs;  // the last sequence that starts at or before the row
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.starts[mid] <= it.seq) lo = mid; else hi = mid;
+      }
+      seq = lo;
+      ncb = ncb_sel;
+    }
+    rows_of(seq, r0, n);
+    const int len = length_of(seq);
+    if (!SEL) ncb = (int)(((long long)n * group + CB - 1) / CB);
+    const int32_t *table = p.c.table + (size_t)seq * p.c.max_pages;
+    const int c0 = it.cb * CB;                          // first column of the block
+    const int ncols = min(CB, (SEL ? group : n * group) - c0);
+    if (tid == 0 && p.c.lens[seq] != len) atomicOr(p.c.status, MQA_KV_DEV_BAD_LENGTH);
+    __syncthreads();  // the previous segment's readers of cs / lim / merge are done
+    if (tid < CB) {
+      int lim = 0;
+      if (tid < ncols) {
+        const int i = SEL ? it.seq - r0 : (c0 + tid) / group;
+        lim = p.causal ? min(max(len - n + i + 1, 0), len) : len;
+        if (SEL && (i < 0 || i >= n)) lim = 0;
+      }
+      sm.lim[tid] = lim;
+    }
+    __syncthreads();
+    int lim_max = 0, lim_min = INT32_MAX;
+#pragma unroll
+    for (int i = 0; i < CB; ++i) {
+      lim_max = max(lim_max, sm.lim[i]);
+      lim_min = min(lim_min, i < ncols ? sm.lim[i] : INT32_MAX);
+    }
+    // ---- q: column g of each 8-column block, the lane's components
+    // k-step j: b0 = components KW*4*t + 4j, +1; b1 = +2, +3 (t's 4*KW bytes of a key row)
+    uint32_t qr[NB > 2 ? 1 : NB][2 * KW];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      if (NB > 2 && (nb & (kWarps - 1)) != warp) continue;  // shared through memory: one warp loads it
+      const int col = nb * 8 + g;
+      float f[4 * KW];
+      float amax = 0.f;
+      if (col < ncols) {
+        const int row = SEL ? it.seq : r0 + (c0 + col) / group;
+        const int h = it.head * group + (SEL ? c0 + col : (c0 + col) % group);
+        const size_t off = (size_t)row * p.q_stride + (size_t)h * D + 4 * KW * t;
+        const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + off);
+#pragma unroll
+        for (int j = 0; j < KW / 2; ++j) {
+          const uint4 w = __ldg(src + j);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            float2 x = p.bf16 ? bf16x2_to_float2(ws[b]) : half2_to_float2(ws[b]);
+            f[8 * j + 2 * b] = x.x;
+            f[8 * j + 2 * b + 1] = x.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4 * KW; ++j) f[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4 * KW; ++j) amax = fmaxf(amax, fabsf(f[j]));
+      amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+      // power of two that brings the column's largest magnitude to [2^10, 2^11)
+      int e = 0;
+      if (amax > 0.f && amax <= FLT_MAX) e = 10 - exponent_of(amax);
+      e = max(-100, min(100, e));
+      const float up = pow2i(e);
+      if (t == 0) sm.cs[col] = p.scale_log2 * pow2i(-e);  // every warp writes the same value
+#pragma unroll
+      for (int j = 0; j < 2 * KW; ++j) {
+        const uint32_t h2 = float2_to_half2(f[2 * j] * up, f[2 * j + 1] * up);
+        if (NB > 2) sm.qf[NB > 2 ? nb : 0][j][lane] = h2;
+        else qr[NB > 2 ? 0 : nb][j] = h2;
+      }
+    }
+    __syncthreads();
+    float cs[NB][2];
+    int lim[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        cs[nb][c] = sm.cs[nb * 8 + 2 * t + c];
+        lim[nb][c] = sm.lim[nb * 8 + 2 * t + c];
+      }
+    const int32_t *sel = SEL ? p.selected + (size_t)it.seq * p.n_selected : nullptr;
+
+    float m[NB][2], w[NB][2], l[NB][2];
+    float o[MT][NB][4];
+    // the tiles this item needs: later ones hold no key that a column sees
+    const int t1e = SEL ? t1 : min(t1, (lim_max + kTile - 1) / kTile);
+    const int iters = max(0, t1e - t0);
+
+    // A masked weight is zero, but zero times a NaN value is NaN: where the
+    // result has one, the segment runs again with NaN codes of V taken out and
+    // every visible key that has one scored NaN.
+    for (int careful = 0; careful < 2; ++careful) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) m[nb][c] = w[nb][c] = -INFINITY, l[nb][c] = 0.f;
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][nb][i] = 0.f;
+
+      // ---- loads.  Rows of D bytes; 16-byte chunks exchanged within 128 bytes
+      // so that both products' reads spread over the banks.
+      // Dense: lane j holds sub-tile it + j's first row, scale and exponent.
+      int d_row = -1;
+      float d_ks = 0.f, d_lv = 0.f;
+      // Selected: a chain three refreshes deep (position, page, exponents), 32 keys each.
+      int s_pos0 = -1, s_pos1 = -1, s_pos2 = -1, s_pos = -1;
+      int s_pg1 = -1, s_row2 = -1, s_row = -1;
+      uint32_t s_e2 = 0;
+      float s_ks = 0.f, s_lv = 0.f;
+      auto load_pos = [&](int i) -> int {  // position of the lane's key among sub-tiles i, i + 1
+        const int k = (t0 + i + (lane >> 4)) * kTile + warp * 16 + (lane & 15);
+        if (i + (lane >> 4) >= iters || k >= p.n_selected) return -1;
+        const int x = __ldg(sel + k);
+        return (unsigned)x < (unsigned)lim_max ? x : -1;
+      };
+      auto load_page = [&](int pos) -> int { return pos < 0 ? -1 : __ldg(table + (pos >> p.c.page_log2)); };
+      auto row_of = [&](int pos, int pg) -> int {
+        if (pos < 0) return -1;
+        if ((unsigned)pg >= (unsigned)p.c.pages) {
+          atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
+          return -1;
+        }
+        return ((pg * heads + it.head) << p.c.page_log2) + (pos & (p.c.page - 1));
+      };
+      auto load_exps = [&](int row) -> uint32_t {
+        if (row < 0) return 127u | 127u << 8;
+        const int ph = row >> p.c.page_log2;
+        return (uint32_t)__ldg(p.c.k_exps + ph) | (uint32_t)__ldg(p.c.v_exps + ph) << 8;
+      };
+      auto refresh_sel = [&](int i) {  // sub-tiles i, i + 1 become current
+        s_pos = s_pos2, s_row = s_row2;
+        s_ks = exp_byte(s_e2 & 255u), s_lv = (float)(int)(s_e2 >> 8) - 127.f;
+        s_pos2 = s_pos1, s_row2 = row_of(s_pos1, s_pg1), s_e2 = load_exps(s_row2);
+        s_pos1 = s_pos0, s_pg1 = load_page(s_pos0);
+        s_pos0 = load_pos(i + 6);
+      };
+      if (SEL) {
+        s_pos0 = load_pos(0);
+        s_pos1 = s_pos0, s_pg1 = load_page(s_pos0), s_pos0 = load_pos(2);
+        s_pos2 = s_pos1, s_row2 = row_of(s_pos1, s_pg1), s_e2 = load_exps(s_row2);
+        s_pos1 = s_pos0, s_pg1 = load_page(s_pos0), s_pos0 = load_pos(4);
+      }
+      auto issue = [&](int i) {
+        if (i < iters) {
+          const int stage = i % kStages;
+          const int base = (t0 + i) * kTile + warp * 16;
+          if (SEL) {
+            if ((i & 1) == 0) refresh_sel(i);
+            if ((lane >> 4) == (i & 1)) {
+              meta.ks[stage][lane & 15] = s_ks;
+              meta.lv[stage][lane & 15] = s_lv;
+              meta.pos[stage][lane & 15] = s_row < 0 ? INT32_MAX : s_pos;
+            }
+          } else {
+            if ((i & 31) == 0) {
+              const int pos = base + lane * kTile;
+              const bool want = i + lane < iters && pos < lim_max;
+              d_row = want ? row_of(pos, load_page(pos)) : -1;
+              const uint32_t e = load_exps(d_row);
+              d_ks = exp_byte(e & 255u), d_lv = (float)(int)(e >> 8) - 127.f;
+            }
+            if (lane == (i & 31)) {
+              meta.ks[stage][0] = d_ks;
+              meta.lv[stage][0] = d_lv;
+              meta.pos[stage][0] = d_row < 0 ? INT32_MAX - 16 : base;
+            }
+          }
+          const int first = SEL ? 0 : __shfl_sync(~0u, d_row, i & 31);
+          constexpr int CH = D / 16;  // chunks per row
+          uint8_t *kd = sm.ring[warp][stage], *vd = kd + 16 * D;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const int id = c * 32 + lane, r = id / CH, ch = id % CH;
+            const int row = SEL ? __shfl_sync(~0u, s_row, r + 16 * (i & 1)) : first + r;
+            const bool ok = SEL ? row >= 0 : first >= 0 && base + r < lim_max;
+            const size_t src = ok ? (size_t)row * D + ch * 16 : 0;
+            const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+            const int dst = r * D + ((ch ^ sw) << 4);
+            cp_async16(kd + dst, p.c.k + src, ok);
+            cp_async16(vd + dst, p.c.v + src, ok);
+          }
+        }
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+      for (int i = 0; i < iters; ++i) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        const int stage = i % kStages;
+        const uint8_t *kd = sm.ring[warp][stage], *vd = kd + 16 * D;
+        // ---- S^T = K Q^T
+        float acc[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[nb][j] = 0.f;
+        uint32_t ka[KW], kb[KW];  // rows g and g + 8
+#pragma unroll
+        for (int h = 0; h < KW / 4; ++h) {
+          const int ch = t * (KW / 4) + h;
+          const int sa = D == 128 ? (g & 7) : ((g >> 1) & 3), sb = D == 128 ? (g & 7) : (((g + 8) >> 1) & 3);
+          const uint4 x = *reinterpret_cast<const uint4 *>(kd + g * D + ((ch ^ sa) << 4));
+          const uint4 y = *reinterpret_cast<const uint4 *>(kd + (g + 8) * D + ((ch ^ sb) << 4));
+          ka[4 * h] = x.x, ka[4 * h + 1] = x.y, ka[4 * h + 2] = x.z, ka[4 * h + 3] = x.w;
+          kb[4 * h] = y.x, kb[4 * h + 1] = y.y, kb[4 * h + 2] = y.z, kb[4 * h + 3] = y.w;
+        }
+#pragma unroll
+        for (int j = 0; j < KW; ++j) {
+          const uint32_t a[4] = {cvt2(ka[j]), cvt2(kb[j]), cvt2_hi(ka[j]), cvt2_hi(kb[j])};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            if (NB > 2) {
+              const uint32_t b0 = sm.qf[NB > 2 ? nb : 0][2 * j][lane], b1 = sm.qf[NB > 2 ? nb : 0][2 * j + 1][lane];
+              mma_f16(acc[nb], a, b0, b1);
+            } else {
+              mma_f16(acc[nb], a, qr[NB > 2 ? 0 : nb][2 * j], qr[NB > 2 ? 0 : nb][2 * j + 1]);
+            }
+          }
+        }
+        // ---- V words: keys 2t, 2t + 1, 2t + 8, 2t + 9, components 4 * VW * g ...
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const int r = 2 * t + (kk & 1) + 8 * (kk >> 1);
+          const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(vd + r * D + ((g ^ sw) << 4));
+            v[kk][0] = x.x, v[kk][1] = x.y, v[kk][VW - 2] = x.z, v[kk][VW - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(vd + r * D + (((g >> 1) ^ sw) << 4) + 8 * (g & 1));
+            v[kk][0] = x.x, v[kk][1] = x.y;
+          }
+        }
+        uint32_t bad_keys = 0;
+        if (careful) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+              const uint32_t nb8 = nan_bytes(v[kk][j]);
+              if (nb8) {
+                bad_keys |= 1u << (2 * t + (kk & 1) + 8 * (kk >> 1));
+                v[kk][j] &= ~((nb8 >> 7) * 255u);
+              }
+            }
+          bad_keys = __reduce_or_sync(~0u, bad_keys);
+        }
+        // ---- weights
+        float s[NB][4], lv[2];
+        {
+          float ks[2];
+          int pos[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int k = SEL ? g + 8 * r : 0;
+            ks[r] = meta.ks[stage][k];
+            lv[r] = meta.lv[stage][k];
+            pos[r] = meta.pos[stage][k] + (SEL ? 0 : g + 8 * r);
+          }
+          bool move = false;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float x = acc[nb][2 * r + c] * (cs[nb][c] * ks[r]);
+                if (bad_keys >> (g + 8 * r) & 1) x = NAN;
+                x = pos[r] < lim[nb][c] ? x : -INFINITY;
+                s[nb][2 * r + c] = x;
+                move |= x > m[nb][c] + kSlack || x + lv[r] > w[nb][c] + kSlack;
+              }
+          if (__any_sync(~0u, move)) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float a = fmaxf(s[nb][c], s[nb][2 + c]), b = fmaxf(s[nb][c] + lv[0], s[nb][2 + c] + lv[1]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                  a = fmaxf(a, __shfl_xor_sync(~0u, a, x));
+                  b = fmaxf(b, __shfl_xor_sync(~0u, b, x));
+                }
+                a = fmaxf(a, m[nb][c]), b = fmaxf(b, w[nb][c]);
+                const float fl = m[nb][c] == a ? 1.f : ex2(m[nb][c] - a), fo = w[nb][c] == b ? 1.f : ex2(w[nb][c] - b);
+                m[nb][c] = a, w[nb][c] = b;
+                l[nb][c] *= fl;
+#pragma unroll
+                for (int j = 0; j < MT; ++j) o[j][nb][c] *= fo, o[j][nb][2 + c] *= fo;
+              }
+          }
+        }
+        uint32_t pf[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float mr[2], wr[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            mr[c] = m[nb][c] == -INFINITY ? 0.f : m[nb][c];
+            wr[c] = w[nb][c] == -INFINITY ? 0.f : w[nb][c];
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            l[nb][0] += ex2(s[nb][2 * r] - mr[0]);
+            l[nb][1] += ex2(s[nb][2 * r + 1] - mr[1]);
+            pf[nb][r] = transpose8x8(float2_to_half2(ex2(s[nb][2 * r] + (lv[r] - wr[0])),
+                                                     ex2(s[nb][2 * r + 1] + (lv[r] - wr[1]))));
+          }
+        }
+        // ---- O^T += V^T P^T; tile j holds components 4 * VW * g + 2j and + 2j + 1 in rows g and g + 8
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          const uint32_t a01 = __byte_perm(v[0][j], v[1][j], 0x5140), b01 = __byte_perm(v[0][j], v[1][j], 0x7362);
+          const uint32_t a23 = __byte_perm(v[2][j], v[3][j], 0x5140), b23 = __byte_perm(v[2][j], v[3][j], 0x7362);
+          const uint32_t x[4] = {cvt2(a01), cvt2_hi(a01), cvt2(a23), cvt2_hi(a23)};
+          const uint32_t y[4] = {cvt2(b01), cvt2_hi(b01), cvt2(b23), cvt2_hi(b23)};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma_f16(o[2 * j][nb], x, pf[nb][0], pf[nb][1]);
+            mma_f16(o[2 * j + 1][nb], y, pf[nb][0], pf[nb][1]);
+          }
+        }
+        __syncwarp();
+        issue(i + kStages - 1);
+      }
+      cp_async_wait<0>();
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bad |= o[j][nb][i] != o[j][nb][i];
+      if (careful || !__any_sync(~0u, bad)) break;
+    }
+
+    // ---- join the warps: common references, then sums in warp order
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nb][c] += __shfl_xor_sync(~0u, l[nb][c], x);
+        if (g == 0) {
+          sm.wm[warp][nb * 8 + 2 * t + c] = m[nb][c];
+          sm.ww[warp][nb * 8 + 2 * t + c] = w[nb][c];
+          sm.wl[warp][nb * 8 + 2 * t + c] = l[nb][c];
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) top = fmaxf(top, sm.ww[x][nb * 8 + 2 * t + c]);
+        const float f = w[nb][c] == top ? 1.f : ex2(w[nb][c] - top);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) o[j][nb][c] *= f, o[j][nb][2 + c] *= f;
+      }
+    for (int x = 0; x < kWarps; ++x) {
+      if (warp == x) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float2 *d = reinterpret_cast<float2 *>(&sm.merge[nb * 8 + 2 * t + c][4 * VW * g + 2 * j]);
+              float2 val = make_float2(o[j][nb][c], o[j][nb][2 + c]);
+              if (x) {
+                const float2 was = *d;
+                val.x += was.x, val.y += was.y;
+              }
+              *d = val;
+            }
+      }
+      __syncthreads();
+    }
+    const bool whole = t0 == 0 && t1 == it.tiles;
+    float *slot = p.slots + ((size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * attn_slot_floats_dev<CB, D>();
+    for (int col = warp; col < ncols; col += kWarps) {
+      float mx = -INFINITY, wx = -INFINITY, ls = 0.f;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) mx = fmaxf(mx, sm.wm[x][col]), wx = fmaxf(wx, sm.ww[x][col]);
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x)
+        ls += sm.wl[x][col] * (sm.wm[x][col] == mx ? 1.f : ex2(sm.wm[x][col] - mx));
+      if (whole) {
+        const int row = SEL ? it.seq : r0 + (c0 + col) / group;
+        const int h = it.head * group + (SEL ? c0 + col : (c0 + col) % group);
+        finish<D>(p, row, h, lane, sm.merge[col], mx, wx, ls);
+      } else {
+        for (int d = lane; d < D; d += 32) slot[col * D + d] = sm.merge[col][d];
+        if (lane == 0) {
+          slot[CB * D + col] = mx;
+          slot[CB * D + CB + col] = wx;
+          slot[CB * D + 2 * CB + col] = ls;
+        }
+      }
+    }
+    if (!whole && t0 == 0 && tid == 0) {
+      // the CTAs that hold the item's other parts follow this one
+      const long long rest = it.tiles - (t1 - t0);
+      p.desc[blockIdx.x] = make_int4(SEL ? it.seq : r0, it.head, SEL ? -c0 - 1 : c0, (int)((rest + per - 1) / per) |
+                                     ncols << 20);
+    }
+    // ---- next item
+    at += t1 - t0;
+    tile = 0;
+    if (at >= end) break;
+    if (++it.cb == ncb) {
+      it.cb = 0;
+      if (++it.head == heads) {
+        it.head = 0;
+        if (SEL) {
+          ++it.seq;
+        } else {
+          int nn = 0;
+          do {
+            ++it.seq;
+            shape_of(it.seq, nn, it.tiles);
+          } while (nn == 0);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+// Join split items: block (c, col) adds the parts of the item that CTA c
+// began, its own first, then the following CTAs' in order.
+namespace {
+template <int D>
+__global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int cb) {
+  const int4 d = p.desc[blockIdx.x];
+  const int more = d.w & 0xFFFFF, ncols = d.w >> 20;
+  const int col = blockIdx.y;
+  if (more == 0 || col >= ncols) return;
+  __shared__ float acc[4][D];
+  __shared__ float red[4][3];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t pitch = (size_t)cb * (D + 4);
+  auto slot = [&](int i) { return p.slots + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * pitch; };
+  float mx = -INFINITY, wx = -INFINITY;
+  for (int i = lane; i <= more; i += 32) {
+    const float *s = slot(i) + cb * D;
+    mx = fmaxf(mx, s[col]);
+    wx = fmaxf(wx, s[cb + col]);
+  }
+#pragma unroll
+  for (int x = 16; x; x >>= 1) {
+    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
+    wx = fmaxf(wx, __shfl_xor_sync(~0u, wx, x));
+  }
+  constexpr int E = D / 32;
+  float o[E], ls = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i <= more; i += 4) {
+    const float *s = slot(i);
+    const float m = s[cb * D + col], w = s[cb * D + cb + col];
+    ls += s[cb * D + 2 * cb + col] * (m == mx ? 1.f : ex2(m - mx));
+    const float f = w == wx ? 1.f : ex2(w - wx);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] += f * s[col * D + lane + 32 * e];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = o[e];
+  if (lane == 0) red[warp][0] = ls;
+  __syncthreads();
+  if (warp) return;
+  ls = red[0][0] + red[1][0] + red[2][0] + red[3][0];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int x = lane + 32 * e;
+    acc[0][x] = acc[0][x] + acc[1][x] + acc[2][x] + acc[3][x];
+  }
+  __syncwarp();
+  const bool sel = d.z < 0;
+  const int c = (sel ? -d.z - 1 : d.z) + col;
+  const int row = sel ? d.x : d.x + c / p.group, h = d.y * p.group + (sel ? c : c % p.group);
+  finish<D>(p, row, h, lane, acc[0], mx, wx, ls);
+}
+
+template <int D, int NB, bool SEL>
+cudaError_t launch(const AttnParams &p, int ctas, cudaStream_t stream) {
+  constexpr size_t bytes = sizeof(Smem<D, NB>);
+  auto *k = kv_attn_kernel<D, NB, SEL>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  k<<<ctas, kAttnThreads, bytes, stream>>>(p);
+  const cudaError_t le = cudaGetLastError();
+  if (le != cudaSuccess) return le;
+  kv_join_kernel<D><<<dim3(ctas, 8 * NB), 128, 0, stream>>>(p, 8 * NB);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const AttnParams &p, int nb, int ctas, cudaStream_t stream) {
+  const bool sel = p.selected != nullptr;
+  switch (nb) {
+    case 1: return sel ? launch<D, 1, true>(p, ctas, stream) : launch<D, 1, false>(p, ctas, stream);
+    case 2: return sel ? launch<D, 2, true>(p, ctas, stream) : launch<D, 2, false>(p, ctas, stream);
+    default: return sel ? launch<D, 4, true>(p, ctas, stream) : launch<D, 4, false>(p, ctas, stream);
+  }
+}
+}  // namespace
+
+cudaError_t launch_kv_attention(const AttnParams &p, int nb, int ctas, cudaStream_t stream) {
+  return p.c.dim == 64 ? launch_d<64>(p, nb, ctas, stream) : launch_d<128>(p, nb, ctas, stream);
+}
+
+}  // namespace mqa

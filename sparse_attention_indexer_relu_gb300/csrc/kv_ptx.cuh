@@ -1,0 +1,97 @@
+// Device helpers of the paged key/value cache's kernels: asynchronous copies,
+// fp16 matrix products, powers of two and row conversions.
+#pragma once
+#include "kv_internal.h"
+#include "ptx.cuh"
+
+#include <cmath>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace mqa {
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// floor(log2 |x|) of a finite nonzero fp32 (subnormals read as -127).
+__device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
+// Scale of a UE8M0 byte: the fp32 with bit pattern e << 23.
+__device__ __forceinline__ float exp_byte(uint32_t e) { return __uint_as_float(e << 23); }
+
+// 16 bytes global -> shared without registers; zeros where !ok (nothing is read then).
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+               "l"(__cvta_generic_to_global(src)), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16 operands.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit values held two per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 half2_to_float2(uint32_t w) {
+  __half2 h;
+  memcpy(&h, &w, 4);
+  return __half22float2(h);
+}
+__device__ __forceinline__ uint32_t float2_to_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+__device__ __forceinline__ uint32_t float2_to_bf162(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+
+template <int CB, int D>
+__host__ __device__ constexpr size_t attn_slot_floats_dev() {
+  return (size_t)CB * (D + 4);
+}
+
+// One warp writes a row of a head: acc = sum 2^(s + lv - w) E(v), ls = sum
+// 2^(s - m), so the result is acc / ls * 2^(w - m); zeros where nothing was
+// seen (m = -inf and no NaN).
+template <int D>
+__device__ __forceinline__ void finish(const AttnParams &p, int row, int head, int lane, const float *acc, float m,
+                                       float w, float ls) {
+  const bool none = m == -INFINITY && ls == 0.f;
+  const float f = none ? 0.f : ls != ls ? NAN : ex2(w - m) / ls;
+  const size_t at = ((size_t)row * p.q_heads + head) * D;
+  uint32_t *o = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.out) + at);
+#pragma unroll
+  for (int d = lane; d < D / 2; d += 32) {
+    const float a = none ? 0.f : acc[2 * d] * f, b = none ? 0.f : acc[2 * d + 1] * f;
+    o[d] = p.bf16 ? float2_to_bf162(a, b) : float2_to_half2(a, b);
+  }
+  if (p.lse && lane == 0)
+    p.lse[(size_t)row * p.q_heads + head] = none ? -INFINITY : (m + log2f(ls)) * 0.693147180559945309f;
+}
+
+}  // namespace mqa

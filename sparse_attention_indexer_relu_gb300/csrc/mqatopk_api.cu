@@ -1,6 +1,7 @@
 // C ABI of the library (include/mqatopk.h): argument checks, workspace sizing,
 // TMA descriptor encoding and launches.  Host code only.
 #include "../../include/mqatopk.h"
+#include "kv_internal.h"
 #include "mqa_fold.h"
 #include "mqa_internal.h"
 
@@ -156,6 +157,20 @@ int split_max_blocks(int ctas, int rows, int brows) {
 }
 
 }  // namespace
+
+int mqa::require_device(int *sms) {
+  DeviceInfo d;
+  const int rc = current_device_info(&d);
+  if (rc == MQA_OK) *sms = d.sms;
+  return rc;
+}
+
+int mqa::device_sms(int device, int *sms) {
+  DeviceInfo d;
+  const int rc = device_info(device, &d);
+  if (rc == MQA_OK) *sms = d.sms;
+  return rc;
+}
 
 FusedLayout mqa::fused_layout(int ctas, int cap, int split_max, int brows, int fold_rows) {
   FusedLayout L;

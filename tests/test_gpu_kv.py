@@ -1,0 +1,533 @@
+"""The paged 8-bit cache on the GPU, against the plain 64-bit forms of kv_reference.py."""
+import numpy as np
+import pytest
+
+import kv_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": "bfloat16", "fp16": "float16", "fp32": "float32"}
+
+
+@pytest.fixture(scope="module")
+def mqa():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import sparse_attention_indexer_relu_gb300 as m
+    m.lib()
+    return m
+
+
+def ints(a):
+    import torch
+    return torch.from_numpy(np.asarray(a, dtype=np.int32).copy()).cuda()
+
+
+def rows_of(rng, n, heads, dim, dtype, scale=1.5):
+    """Random rows of a type, and their values in 64 bits."""
+    import torch
+    t = (torch.from_numpy(rng.standard_normal((n, heads, dim))) * scale).to(getattr(torch, TYPES[dtype])).cuda()
+    return t, t.double().cpu().numpy()
+
+
+def starts_of(rows):
+    return np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+
+
+def check(got, lse, want, what=""):
+    """Against (out, lse, bound of out, bound of lse): NaN where NaN, else within the bound."""
+    out, l, tol, ltol = want
+    g = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(g), np.isnan(out)), what
+    bad = np.abs(np.nan_to_num(g - out)) > tol
+    assert not bad.any(), (what, np.argwhere(bad)[:5], np.abs(g - out)[bad][:5], tol[bad][:5])
+    if lse is not None:
+        gl = lse.double().cpu().numpy()
+        assert np.array_equal(np.isnan(gl), np.isnan(l)) and np.array_equal(np.isneginf(gl), np.isneginf(l)), what
+        d = np.abs(np.where(np.isfinite(l), gl, 0) - np.where(np.isfinite(l), l, 0))
+        assert (d <= ltol + 1e-30).all(), (what, d.max())
+
+
+def attend(mqa, c, rng, rows, group, dtype="bf16", causal=True, selected=None, max_rows=None, q_scale=1.5, scale=None,
+           extra_rows=0):
+    import torch
+    st = starts_of(rows)
+    n = int(st[-1]) + extra_rows
+    q, qd = rows_of(rng, n, c.heads * group, c.dim, dtype, q_scale)
+    dev = ref.to_device(c, mqa)
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    sel = None if selected is None else ints(selected)
+    scale = c.dim ** -0.5 if scale is None else scale
+    mqa.kv_attention(q, dev, ints(st), selected=sel, causal=causal, scale=scale, max_rows=max_rows, out=out, lse=lse)
+    assert mqa.kv_status(dev) == 0
+    m = int(st[-1])
+    assert (out[m:] == 7).all() and (lse[m:] == 7).all()  # rows behind the last sequence
+    want = c.attention(qd[:m], st, scale, dtype, None if selected is None else selected[:m], causal)
+    check(out[:m], lse[:m], want)
+    return out, dev, q, st
+
+
+# ---------------------------------------------------------------- attention
+CASES = [  # page, heads, group, dim, lens, rows
+    (16, 1, 1, 128, [1], [1]),
+    (64, 2, 4, 128, [0, 1, 63, 64, 65, 200], [1, 1, 1, 1, 1, 1]),
+    (32, 2, 8, 64, [0, 5, 333, 0], [0, 3, 2, 1]),
+    (16, 3, 3, 64, [100, 257], [5, 7]),
+    (128, 1, 16, 128, [129, 1000], [1, 2]),
+    (64, 2, 5, 128, [700], [9]),
+    (64, 1, 32, 128, [300, 31], [1, 3]),
+    (16, 1, 71, 64, [90], [2]),
+    (32, 2, 2, 128, [2, 40], [5, 40]),          # more rows than positions: the first see nothing
+    (64, 1, 4, 128, [130, 77, 64], [130, 77, 1]),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_attention(mqa, case, dtype, causal):
+    page, heads, group, dim, lens, rows = case
+    rng = np.random.default_rng(len(lens) * 100 + group)
+    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 2, heads, page, dim, lens, 20)
+    attend(mqa, c, rng, rows, group, dtype, causal, extra_rows=3)
+
+
+@pytest.mark.parametrize("max_rows", [None, 1, 4, 100])
+def test_attention_answers_for_any_max_rows(mqa, max_rows):
+    rng = np.random.default_rng(7)
+    c = ref.random_cache(rng, 40, 2, 16, 128, [150, 90, 33], 12)
+    attend(mqa, c, rng, [40, 1, 7], 4, max_rows=max_rows)
+
+
+def test_attention_long_context_is_split_and_joined(mqa):
+    rng = np.random.default_rng(8)
+    c = ref.random_cache(rng, 700, 1, 64, 128, [40001], 640)
+    attend(mqa, c, rng, [2], 8)
+
+
+def test_attention_sharp_and_flat_softmax(mqa):
+    """Scores of thousands (one key takes all) and of almost zero (all alike)."""
+    rng = np.random.default_rng(9)
+    c = ref.random_cache(rng, 30, 2, 32, 64, [500, 300], 20)
+    attend(mqa, c, rng, [2, 2], 4, "fp16", q_scale=200.0)
+    attend(mqa, c, rng, [2, 2], 4, "bf16", q_scale=1e-30)
+
+
+def test_attention_scales_far_apart(mqa):
+    """Blocks whose scales span 2^120: keys stay within reach of the softmax, values do not."""
+    rng = np.random.default_rng(10)
+    c = ref.random_cache(rng, 20, 2, 16, 128, [200], 16)
+    c.ve[:] = rng.integers(60, 180, c.ve.shape)
+    c.ke[:] = rng.integers(90, 128, c.ke.shape)
+    rng2 = np.random.default_rng(11)
+    q, qd = rows_of(rng2, 3, 8, 128, "bf16")
+    dev = ref.to_device(c, mqa)
+    got = mqa.kv_attention(q, dev, ints([0, 3]), scale=0.01)
+    want = c.attention(qd, np.array([0, 3]), 0.01, "bf16")
+    out, _, tol, _ = want
+    fine = np.abs(out) < 3e38  # the rest leave bf16's range
+    assert fine.any() and (np.abs(got.double().cpu().numpy() - out)[fine] <= tol[fine]).all()
+
+
+def test_small_scale_block_with_all_the_weight(mqa):
+    """The key with all the softmax weight sits in a block whose value scale is 2^30 below the others'."""
+    rng = np.random.default_rng(12)
+    c = ref.random_cache(rng, 8, 1, 16, 64, [96], 8)
+    c.ve[:] = 127
+    c.ve[c.table[0, 2], 0] = 97
+    c.k[c.table[0, 2], 0, 5] = ref.round_e4m3(np.full(64, 400.0))
+    import torch
+    q = torch.ones((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    dev = ref.to_device(c, mqa)
+    got = mqa.kv_attention(q, dev, ints([0, 1]), scale=0.125)
+    out, l, tol, ltol = c.attention(np.ones((1, 2, 64)), np.array([0, 1]), 0.125, "bf16")
+    check(got, None, (out, l, tol, ltol))
+
+
+def test_nan_codes_count_only_where_they_are_seen(mqa):
+    rng = np.random.default_rng(13)
+    c = ref.random_cache(rng, 20, 2, 16, 128, [100, 60], 10)
+    c.v[c.table[0, 97 // 16], 0, 97 % 16, 3] = 127    # a value of position 97, head 0
+    c.k[c.table[1, 58 // 16], 1, 58 % 16, 100] = 255  # a key of position 58, head 1
+    for rows in ([5, 4], [100, 60]):
+        out, _, _, st = attend(mqa, c, np.random.default_rng(14), rows, 4)
+        o = out.float().cpu().numpy()
+        first = int(st[1])
+        assert np.isnan(o[first - 3:first, :4]).all() and not np.isnan(o[:first - 3]).any()
+        assert not np.isnan(o[:first, 4:]).any()
+
+
+def test_infinite_and_nan_queries(mqa):
+    import torch
+    rng = np.random.default_rng(15)
+    c = ref.random_cache(rng, 20, 2, 16, 64, [100], 10)
+    q, qd = rows_of(rng, 3, 8, 64, "bf16")
+    q[1, 2, 5] = float("nan")
+    q[2, 4, 0] = float("inf")
+    out = mqa.kv_attention(q, ref.to_device(c, mqa), ints([0, 3])).float().cpu().numpy()
+    qd[1, 2], qd[2, 4] = 0, 0
+    want = c.attention(qd, np.array([0, 3]), 0.125, "bf16")
+    assert np.isnan(out[1, 2]).all()
+    keep = np.ones((3, 8), bool)
+    keep[1, 2] = keep[2, 4] = False
+    assert (np.abs(out - want[0])[keep] <= want[2][keep]).all() and not np.isnan(out[keep]).any()
+    assert torch.cuda.current_stream() is not None
+
+
+def test_strided_queries(mqa):
+    import torch
+    rng = np.random.default_rng(16)
+    c = ref.random_cache(rng, 12, 2, 32, 64, [150], 6)
+    wide = torch.from_numpy(rng.standard_normal((4, 12, 64))).to(torch.bfloat16).cuda()
+    q = wide[:, 2:10]
+    got = mqa.kv_attention(q, ref.to_device(c, mqa), ints([0, 4]))
+    check(got, None, c.attention(q.double().cpu().numpy(), np.array([0, 4]), 0.125, "bf16"))
+
+
+def test_bad_tables_are_not_followed(mqa):
+    """A page index outside the pool: its keys are not seen; the status word tells."""
+    rng = np.random.default_rng(17)
+    c = ref.random_cache(rng, 12, 2, 16, 64, [100, 40], 8)
+    dev = ref.to_device(c, mqa)
+    dev.page_table[0, 2] = 1 << 30
+    dev.page_table[1, 0] = -5
+    q, qd = rows_of(rng, 2, 4, 64, "fp16")
+    sel = np.full((2, 128), -1, np.int32)
+    sel[0, :84] = [t for t in range(100) if not 32 <= t < 48]
+    sel[1, :24] = range(16, 40)
+    got = mqa.kv_attention(q, dev, ints([0, 1, 2]))
+    assert mqa.kv_status(dev) == 2
+    check(got, None, c.attention(qd, np.array([0, 1, 2]), 0.125, "fp16", sel))
+    dev.seq_lens[0] = 10 ** 6
+    mqa.kv_attention(q, dev, ints([0, 1, 2]))
+    assert mqa.kv_status(dev) & 8
+    assert mqa.kv_status(dev) == 0
+
+
+def test_row_starts_outside_the_rows(mqa):
+    """Bounds that leave the call's rows are cut to them; decreasing ones give a sequence no rows."""
+    import torch
+    rng = np.random.default_rng(18)
+    c = ref.random_cache(rng, 30, 1, 16, 64, [50, 40, 30], 8)
+    q, qd = rows_of(rng, 4, 4, 64, "bf16")
+    out = torch.zeros_like(q)
+    mqa.kv_attention(q, ref.to_device(c, mqa), ints([-3, 2, 2, 1000]), out=out)
+    want = c.attention(qd, np.array([0, 2, 2, 4]), 0.125, "bf16")
+    check(out, None, want)
+    mqa.kv_attention(q, ref.to_device(c, mqa), ints([3, 1, 4, 4]), out=out)
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- selected keys
+def random_selection(rng, c, rows, k, seen_only=False):
+    sel = []
+    for n, r in zip(c.lens, rows):
+        for i in range(r):
+            last = int(n) - r + i
+            hi = max(1, last + 1 if seen_only else int(n) + 5)
+            x = rng.permutation(hi)[:k]
+            x = np.concatenate([x, np.full(k - len(x), -1)]) if len(x) < k else x
+            if not seen_only:
+                x[rng.random(k) < 0.1] = rng.integers(-5, 0)
+            sel.append(x)
+    return np.array(sel, np.int32).reshape(-1, k)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", [(16, 1, 1, 128, [1], [1], 4), (64, 2, 4, 128, [500, 0, 90], [3, 2, 2], 100),
+                                  (32, 1, 32, 64, [700, 64], [2, 5], 65), (128, 2, 9, 128, [1200], [3], 512),
+                                  (16, 4, 16, 64, [33, 400], [33, 1], 48)], ids=str)
+def test_selected_attention(mqa, case, dtype):
+    page, heads, group, dim, lens, rows, k = case
+    rng = np.random.default_rng(k)
+    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 1, heads, page, dim, lens, 30)
+    sel = random_selection(rng, c, rows, k)
+    sel = np.concatenate([sel, np.full((2, k), 3, np.int32)])  # rows of no sequence
+    attend(mqa, c, rng, rows, group, dtype, True, sel, extra_rows=2)
+
+
+def test_selected_all_entries_and_none(mqa):
+    """A list of every visible position gives the dense answer's value; an empty one and one of -1 give zeros; a
+    position listed twice counts twice."""
+    rng = np.random.default_rng(20)
+    c = ref.random_cache(rng, 20, 2, 16, 128, [150], 12)
+    allk = np.stack([np.where(np.arange(150) <= 145 + i, np.arange(150), -1) for i in range(5)]).astype(np.int32)
+    attend(mqa, c, rng, [5], 4, selected=allk)
+    attend(mqa, c, rng, [5], 4, selected=np.full((5, 7), -1, np.int32))
+    attend(mqa, c, rng, [5], 4, selected=np.zeros((5, 0), np.int32))
+    attend(mqa, c, rng, [5], 4, selected=np.tile(np.array([[9, 3, 9, 9]], np.int32), (5, 1)))
+
+
+def test_selected_long(mqa):
+    rng = np.random.default_rng(21)
+    c = ref.random_cache(rng, 330, 1, 64, 128, [20000], 320)
+    attend(mqa, c, rng, [3], 8, selected=random_selection(rng, c, [3], 2048, True))
+
+
+# ---------------------------------------------------------------- streams, graphs
+def test_attention_in_a_graph_on_a_side_stream(mqa):
+    import torch
+    rng = np.random.default_rng(22)
+    c = ref.random_cache(rng, 60, 2, 16, 128, [300, 120], 24)
+    dev = ref.to_device(c, mqa)
+    q, qd = rows_of(rng, 4, 8, 128, "bf16")
+    st = ints([0, 2, 4])
+    ws = mqa.alloc_kv_workspace(dev, 4, 8)
+    out = torch.zeros_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    mqa.kv_attention(q, dev, st, workspace=ws, out=out, stream=side)
+    side.synchronize()
+    check(out, None, c.attention(qd, np.array([0, 2, 4]), 128 ** -0.5, "bf16"))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mqa.kv_attention(q, dev, st, workspace=ws, out=out)
+    for lens in ([300, 120], [17, 1], [0, 64]):
+        c.lens[:] = lens
+        dev.seq_lens.copy_(ints(lens))
+        out.fill_(3)
+        g.replay()
+        torch.cuda.synchronize()
+        check(out, None, c.attention(qd, np.array([0, 2, 4]), 128 ** -0.5, "bf16"), lens)
+
+
+def test_two_streams_with_a_workspace_each(mqa):
+    import torch
+    rng = np.random.default_rng(23)
+    c = ref.random_cache(rng, 340, 2, 32, 128, [9000, 500], 300)
+    dev = ref.to_device(c, mqa)
+    q, _ = rows_of(rng, 2, 8, 128, "fp16")
+    st = ints([0, 1, 2])
+    want = mqa.kv_attention(q, dev, st)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [mqa.kv_attention(q, dev, st, stream=s) for _ in range(10) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)  # and the same bits every time
+
+
+# ---------------------------------------------------------------- appending
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("case", [(16, 1, 128, [1], [1]), (64, 2, 64, [64, 65, 200, 5], [1, 2, 130, 0]),
+                                  (32, 3, 128, [31, 33, 400], [31, 33, 77]), (128, 2, 64, [300, 0, 4], [2, 0, 9]),
+                                  (16, 8, 128, [17, 18, 19, 20, 40, 16, 1, 2], [1] * 8)], ids=str)
+def test_append_bit_exact(mqa, case, dtype):
+    import torch
+    page, heads, dim, lens, rows = case
+    rng = np.random.default_rng(dim + len(lens))
+    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 2, heads, page, dim, lens, 14)
+    dev = ref.to_device(c, mqa)
+    st = starts_of(rows)
+    n = int(st[-1]) + 2
+    size = torch.from_numpy(2.0 ** rng.integers(-6, 14, (n, heads, 1))).cuda()  # some blocks' scales grow
+    k, v = (rows_of(rng, n, heads, dim, dtype)[0] * size for _ in range(2))
+    k, v = (x.clamp(-6e4, 6e4).to(getattr(torch, TYPES[dtype])) for x in (k, v))
+    mqa.kv_append(dev, k, v, ints(st))
+    c.append(k.double().cpu().numpy(), v.double().cpu().numpy(), st)
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+
+
+def test_append_extremes(mqa):
+    """Zeros, the smallest and largest values, infinities and NaN, and a block of a given, larger scale."""
+    import torch
+    rng = np.random.default_rng(31)
+    c = ref.random_cache(rng, 12, 2, 16, 64, [40, 20, 16, 9], 4)
+    c.ke[c.table[1, 1]] = 200
+    dev = ref.to_device(c, mqa)
+    st = starts_of([20, 4, 16, 5])
+    k = torch.from_numpy(rng.standard_normal((45, 2, 64))).float().cuda()
+    k[3] = 0
+    k[4:12] *= 1e38
+    k[22:24] = 1e-44
+    k[24:40] = 0
+    v = k.clone()
+    v[1, 0, 5], v[2, 1, 6], v[41, 0, 0] = float("inf"), float("-inf"), float("nan")
+    v[40:45, 1] = float("nan")
+    mqa.kv_append(dev, k, v, ints(st))
+    c.append(k.double().cpu().numpy(), v.double().cpu().numpy(), st)
+    bad = ref.same(c, dev)
+    if bad:  # a NaN's sign is not kept by every path
+        for n, a in (("k", c.k), ("v", c.v)):
+            g = getattr(dev, n).cpu().numpy()
+            nan = np.isnan(ref.E4M3[a])
+            assert np.array_equal(np.isnan(ref.E4M3[g]), nan) and np.array_equal(g[~nan], a[~nan])
+    assert [n for n in bad if n not in ("k", "v")] == []
+
+
+def test_append_strided_and_refused_rows(mqa):
+    import torch
+    rng = np.random.default_rng(32)
+    c = ref.random_cache(rng, 12, 2, 16, 64, [3, 40], 4)
+    dev = ref.to_device(c, mqa)
+    wide = torch.from_numpy(rng.standard_normal((9, 6, 64))).to(torch.bfloat16).cuda()
+    k, v = wide[:, 1:3], wide[:, 4:6]
+    st = starts_of([5, 4])  # five rows for a sequence of three: two lie before it
+    mqa.kv_append(dev, k, v, ints(st))
+    kd, vd = k.double().cpu().numpy(), v.double().cpu().numpy()
+    c.append(np.concatenate([kd[2:], kd[:2]]), np.concatenate([vd[2:], vd[:2]]), starts_of([3, 4]))
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+    dev.page_table[1, 2] = 99  # positions 36 .. 39 have no page now
+    before = dev.k.clone()
+    mqa.kv_append(dev, k[5:], v[5:], ints([0, 0, 4]))
+    assert mqa.kv_status(dev) == 2 and torch.equal(before, dev.k)
+    dev.seq_lens[1] = 1000
+    mqa.kv_append(dev, k[5:], v[5:], ints([0, 0, 4]))
+    assert mqa.kv_status(dev) == 8 and torch.equal(before, dev.k)
+
+
+# ---------------------------------------------------------------- pages
+def test_random_page_operations(mqa):
+    import torch
+    rng = np.random.default_rng(40)
+    pages, heads, page, dim, seqs, width = 90, 2, 16, 64, 12, 9
+    c = ref.random_cache(rng, pages, heads, page, dim, [0] * seqs, width, shuffle=False)
+    c.table[:] = -1
+    index = torch.from_numpy(rng.integers(0, 255, (pages, page, 5)).astype(np.uint8)).cuda()
+    plain_index = index.cpu().numpy().copy()
+    dev = ref.to_device(c, mqa, extra=(index,))
+    plain_copy = c.copy_pages
+
+    def copy_all(src, dst):
+        plain_copy(src, dst)
+        plain_index[dst] = plain_index[src]
+    c.copy_pages = copy_all
+    seen = set()
+    for step in range(300):
+        op = rng.choice(["reserve", "reserve", "fork", "fork", "free", "compact"])
+        live = np.nonzero(c.lens)[0]
+        empty = np.nonzero(c.lens == 0)[0]
+        want = 0
+        if op == "reserve":
+            counts = np.where(rng.random(seqs) < 0.4, rng.integers(0, 40, seqs), 0).astype(np.int32)
+            # a shared partial page cannot arise: fork copies it
+            mqa.kv_reserve(dev, ints(counts))
+            want = c.reserve(counts)
+        elif op == "fork":
+            n = int(rng.integers(1, 4))
+            parents = rng.integers(0, seqs, n).astype(np.int32)
+            children = rng.permutation(empty)[:n].astype(np.int32)
+            if len(children) < n or rng.random() < 0.1:
+                children = rng.integers(0, seqs, n).astype(np.int32)
+            mqa.kv_fork(dev, ints(parents), ints(children))
+            want = c.fork(parents, children)
+        elif op == "free":
+            gone = rng.permutation(live)[:2].astype(np.int32)
+            mqa.kv_free(dev, ints(np.concatenate([gone, gone[:1]])))  # one of them listed twice
+            c.free(gone)
+        else:
+            mqa.kv_compact(dev)
+            c.compact()
+        seen.add((op, want))
+        assert mqa.kv_status(dev) == want, (step, op)
+        assert ref.same(c, dev) == [], (step, op, ref.same(c, dev))
+        assert np.array_equal(index.cpu().numpy(), plain_index)
+    assert {("reserve", 0), ("reserve", 8), ("fork", 0), ("fork", 4), ("free", 0), ("compact", 0)} <= seen, seen
+
+
+def test_too_few_pages_change_nothing(mqa):
+    rng = np.random.default_rng(42)
+    c = ref.random_cache(rng, 10, 1, 16, 64, [70, 40, 0, 0, 0], 9)  # two free pages
+    dev = ref.to_device(c, mqa)
+    for counts, want in (([0, 9, 33, 0, 0], 1), ([0, 0, 17, 16, 0], 1), ([10, 8, 16, 16, 0], 0), ([0, 0, 1, 0, 0], 1)):
+        counts = np.array(counts, np.int32)
+        mqa.kv_reserve(dev, ints(counts))
+        assert c.reserve(counts) == want and mqa.kv_status(dev) == want and ref.same(c, dev) == []
+    c = ref.random_cache(rng, 10, 1, 16, 64, [70, 40, 0, 0, 0], 9)
+    dev = ref.to_device(c, mqa)
+    for parents, children, want in (([0, 1, 0], [2, 3, 4], 1), ([0, 1], [2, 3], 0), ([1], [4], 1)):
+        parents, children = np.array(parents), np.array(children)
+        mqa.kv_fork(dev, ints(parents), ints(children))
+        assert c.fork(parents, children) == want and mqa.kv_status(dev) == want and ref.same(c, dev) == []
+
+
+@pytest.mark.parametrize("pages", [1, 7, 4096, 5000, 12289])
+def test_compact_sizes(mqa, pages):
+    rng = np.random.default_rng(pages)
+    lens, left = [], pages
+    while left > 0 and len(lens) < 40:
+        n = int(rng.integers(1, max(2, min(left, 700) + 1)))
+        n = min(n, left)
+        lens.append(16 * n - int(rng.integers(0, 16)))
+        left -= n
+    c = ref.random_cache(rng, pages, 1, 16, 64, lens, 700)
+    c.table[c.table < 0] = 0
+    dev = ref.to_device(c, mqa)
+    gone = np.nonzero(rng.random(len(lens)) < 0.5)[0].astype(np.int32)
+    c.free(gone)
+    mqa.kv_free(dev, ints(gone))
+    mqa.kv_compact(dev)
+    c.compact()
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+    mqa.kv_compact(dev)  # nothing left to move
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+
+
+def test_page_lists_that_are_refused(mqa):
+    rng = np.random.default_rng(41)
+    c = ref.random_cache(rng, 20, 2, 16, 64, [40, 33, 0, 0], 8)
+    dev = ref.to_device(c, mqa)
+    for src, dst in (([1, 2], [3, 3]), ([1, 2], [2, 3]), ([1], [20]), ([-1], [3]), ([4], [4])):
+        mqa.kv_copy_pages(dev, ints(src), ints(dst))
+        assert mqa.kv_status(dev) == 4 and ref.same(c, dev) == [], (src, dst)
+    mqa.kv_copy_pages(dev, ints([1, 1, 5]), ints([3, 4, 6]))
+    c.copy_pages([1, 1, 5], [3, 4, 6])
+    assert mqa.kv_status(dev) == 0 and ref.same(c, dev) == []
+    for parents, children in (([0], [1]), ([0, 1], [2, 2]), ([4], [2]), ([0], [-1])):
+        mqa.kv_fork(dev, ints(parents), ints(children))
+        assert mqa.kv_status(dev) == 4 and ref.same(c, dev) == []
+    mqa.kv_free(dev, ints([7, -1]))
+    assert mqa.kv_status(dev) == 2 and ref.same(c, dev) == []
+    mqa.kv_reserve(dev, ints([0, 0, 16 * 9, 0]))
+    assert mqa.kv_status(dev) == 8 and ref.same(c, dev) == []
+    mqa.kv_reserve(dev, ints([0, -1, 0, 0]))
+    assert mqa.kv_status(dev) == 4 and ref.same(c, dev) == []
+
+
+# ---------------------------------------------------------------- together
+def test_prompt_selection_attention_fork_and_decode(mqa):
+    """A prompt is written, the indexer selects keys for its rows, attention reads them; two samples are forked, each
+    gets a token of its own, the prompt's sequence is freed, the pool compacted, and the samples answer as before."""
+    import torch
+    rng = np.random.default_rng(50)
+    heads, group, dim, page, n = 2, 8, 128, 64, 1000
+    dev = mqa.alloc_kv_cache(60, page, heads, dim, 3, 20)
+    c = ref.Cache(*(t.cpu().numpy().copy() for t in (dev.k, dev.v, dev.k_exps, dev.v_exps, dev.page_table,
+                                                     dev.seq_lens, dev.refcounts)))
+
+    def grow(counts):
+        counts = np.array(counts, np.int32)
+        st = starts_of(counts)
+        k, kd = rows_of(rng, int(st[-1]), heads, dim, "bf16")
+        v, vd = rows_of(rng, int(st[-1]), heads, dim, "bf16")
+        mqa.kv_reserve(dev, ints(counts))
+        mqa.kv_append(dev, k, v, ints(st))
+        assert c.reserve(counts) == 0
+        c.append(kd, vd, st)
+        return st
+
+    st = grow([n, 0, 0])
+    # the indexer over the prompt's own index keys
+    rows = 6
+    iq = torch.from_numpy(ref.round_e4m3(rng.standard_normal((rows, 32, 128)))).cuda()
+    ik = torch.from_numpy(ref.round_e4m3(rng.standard_normal((n, 128)))).cuda()
+    ends = ints(n - rows + 1 + np.arange(rows))
+    idx = mqa.mqa_topk_prefill(iq, ik, torch.ones(n, device="cuda"), torch.rand((rows, 32), device="cuda"),
+                               torch.zeros_like(ends), ends, 512)
+    q, qd = rows_of(rng, rows, heads * group, dim, "bf16")
+    last = np.array([0, rows, rows, rows])
+    got = mqa.kv_attention(q, dev, ints(last), selected=idx)
+    check(got, None, c.attention(qd, last, dim ** -0.5, "bf16", idx.cpu().numpy()))
+    mqa.kv_fork(dev, ints([0, 0]), ints([1, 2]))
+    assert c.fork(np.array([0, 0]), np.array([1, 2])) == 0
+    st = grow([0, 1, 1])
+    assert ref.same(c, dev) == []
+    q, qd = rows_of(rng, 2, heads * group, dim, "bf16")
+    want = mqa.kv_attention(q, dev, ints(st))
+    check(want, None, c.attention(qd, st, dim ** -0.5, "bf16"))
+    mqa.kv_free(dev, ints([0]))
+    mqa.kv_compact(dev)
+    c.free([0])
+    c.compact()
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+    assert torch.equal(mqa.kv_attention(q, dev, ints(st)), want)
