@@ -87,20 +87,33 @@ int code(cudaError_t e) {
   return MQA_ERR_CUDA;
 }
 
-// Column blocks of the split kernel: 8, 16 or 32 columns.
+// Which kernels a call runs and where their parts of the workspace lie.  The
+// split kernel (kv_attn.cu) takes blocks of 8, 16 or 32 columns; calls in which
+// a sequence may have more than kTiledFrom columns run the tiled kernel
+// (kv_prefill.cu), and leave sequences of up to kSplitCols to the split kernel.
+constexpr int kTiledFrom = 64;
+constexpr int kSplitCols = 16;
 struct AttnPlan {
-  int nb, ctas;
-  size_t slots_off, bytes;
+  bool split, tiled;
+  int nb, ctas, tiled_ctas;
+  size_t slots_off, tiled_off, tiled_slots_off, bytes;
 };
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, int q_heads, bool selected) {
   const int group = q_heads / c->kv_heads;
   if (max_rows <= 0 || max_rows > rows) max_rows = rows;
   const long long cols = selected ? group : (long long)group * max_rows;
   AttnPlan p;
-  p.nb = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+  p.tiled = !selected && cols > kTiledFrom;
+  p.split = !p.tiled || c->max_seqs > 1;
+  p.nb = cols <= 8 ? 1 : cols <= 16 || p.tiled ? 2 : 4;
   p.ctas = sms * attn_ctas_per_sm(p.nb);
-  p.slots_off = ((size_t)p.ctas * sizeof(int4) + 255) / 256 * 256;
-  p.bytes = p.slots_off + (size_t)p.ctas * 2 * attn_slot_floats(p.nb, c->head_dim) * sizeof(float);
+  p.slots_off = up256((size_t)p.ctas * sizeof(int4));
+  p.tiled_off = up256(p.slots_off + (size_t)p.ctas * 2 * attn_slot_floats(p.nb, c->head_dim) * sizeof(float));
+  p.tiled_ctas = sms;
+  p.tiled_slots_off = p.tiled_off + up256((size_t)sms * sizeof(int4));
+  p.bytes = p.tiled ? p.tiled_slots_off + (size_t)sms * 2 * kTiledCols * (c->head_dim + 4) * sizeof(float)
+                    : p.tiled_off;
   return p;
 }
 
@@ -147,13 +160,8 @@ int mqa_kv_attention_workspace_bytes(int device, const mqa_kv_cache *cache, int 
   int sms = 0;
   rc = device_sms(device, &sms);
   if (rc != MQA_OK) return rc;
-  // the largest of the forms that a call with these sizes may take
-  size_t most = 0;
-  for (const int nb_rows : {1, rows}) {
-    const size_t a = plan_attention(sms, cache, rows, nb_rows, q_heads, false).bytes;
-    most = a > most ? a : most;
-  }
-  *bytes = most;
+  // the form for the most columns needs the most, whatever max_rows a call gives
+  *bytes = plan_attention(sms, cache, rows, rows, q_heads, false).bytes;
   return MQA_OK;
 }
 
@@ -194,9 +202,17 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
   p.causal = causal != 0;
   p.bf16 = type == MQA_KV_BF16;
   p.scale_log2 = scale * 1.44269504088896341f;
-  p.max_cols = INT_MAX;
-  p.desc = reinterpret_cast<int4 *>(workspace);
-  p.slots = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + P.slots_off);
+  uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
+  if (P.tiled) {
+    p.max_cols = P.split ? kSplitCols : 0;
+    p.desc = reinterpret_cast<int4 *>(ws + P.tiled_off);
+    p.slots = reinterpret_cast<float *>(ws + P.tiled_slots_off);
+    rc = code(launch_kv_prefill(p, P.tiled_ctas, as_stream(stream)));
+    if (rc != MQA_OK || !P.split) return rc;
+  }
+  p.max_cols = P.tiled ? kSplitCols : INT_MAX;
+  p.desc = reinterpret_cast<int4 *>(ws);
+  p.slots = reinterpret_cast<float *>(ws + P.slots_off);
   return code(launch_kv_attention(p, P.nb, P.ctas, as_stream(stream)));
 }
 

@@ -67,6 +67,11 @@ struct AttnParams {
 constexpr int kAttnThreads = 128;
 int attn_ctas_per_sm(int nb);
 size_t attn_slot_floats(int nb, int dim);
+// Columns per item of the tiled kernel (p.max_cols: it takes the sequences of
+// more columns), and the fewest key tiles a CTA's part holds.
+constexpr int kTiledCols = 256;
+constexpr int kTiledMinTiles = 4;
+cudaError_t launch_kv_prefill(const AttnParams &p, int ctas, cudaStream_t stream);
 cudaError_t launch_kv_attention(const AttnParams &p, int nb, int ctas, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,

@@ -219,6 +219,67 @@ def test_row_starts_outside_the_rows(mqa):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_attention_with_few_rows_announced(mqa, case, causal):
+    """max_rows = 1 keeps every sequence on the split kernel."""
+    page, heads, group, dim, lens, rows = case
+    rng = np.random.default_rng(len(lens) * 100 + group)
+    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 2, heads, page, dim, lens, 20)
+    attend(mqa, c, rng, rows, group, "fp16", causal, max_rows=1)
+
+
+TILED = [  # page, heads, group, dim, lens, rows: 17 to thousands of columns per sequence
+    (64, 1, 4, 128, [128], [32]),                 # one 128-column half, one full tile of keys
+    (64, 1, 4, 128, [129], [33]),
+    (16, 2, 8, 128, [700], [70]),                 # two full halves and a rest
+    (32, 2, 8, 64, [700], [70]),
+    (128, 1, 3, 64, [400, 0, 90, 513], [200, 0, 90, 9]),
+    (16, 1, 16, 128, [300, 5, 1100], [17, 2, 40]),
+    (64, 2, 1, 128, [3000], [600]),
+    (64, 1, 7, 64, [100, 260], [150, 200]),       # more rows than positions, then a chunk
+    (32, 1, 32, 128, [2500], [9]),                # split along the keys
+    (16, 3, 5, 64, [257, 256, 255], [255, 256, 100]),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", TILED, ids=str)
+def test_tiled_attention(mqa, case, dtype, causal):
+    page, heads, group, dim, lens, rows = case
+    rng = np.random.default_rng(sum(lens) + dim)
+    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 2, heads, page, dim, lens, 190)
+    attend(mqa, c, rng, rows, group, dtype, causal, extra_rows=5)
+
+
+def test_tiled_attention_scales_far_apart_and_sharp(mqa):
+    rng = np.random.default_rng(25)
+    c = ref.random_cache(rng, 30, 1, 16, 64, [400], 30, spread=20)
+    attend(mqa, c, rng, [60], 4, "fp16", scale=1e-6)
+    c.ke[:] = 127
+    attend(mqa, c, rng, [60], 4, "bf16", q_scale=200.0)
+    c.ve[:] = 127
+    c.ve[c.table[0, 3], 0] = 27  # values 2^100 below the others', in the block that has all the weight
+    c.k[c.table[0, 3], 0, 5] = ref.round_e4m3(np.full(64, 440.0))
+    import torch
+    q = torch.ones((60, 4, 64), dtype=torch.bfloat16, device="cuda")
+    got = mqa.kv_attention(q, ref.to_device(c, mqa), ints([0, 60]), scale=0.5)
+    check(got, None, c.attention(np.ones((60, 4, 64)), np.array([0, 60]), 0.5, "bf16"))
+
+
+def test_tiled_attention_bad_page(mqa):
+    rng = np.random.default_rng(26)
+    c = ref.random_cache(rng, 40, 2, 16, 64, [300], 30)
+    dev = ref.to_device(c, mqa)
+    dev.page_table[0, 7] = 40
+    q, qd = rows_of(rng, 50, 8, 64, "fp16")
+    sel = np.array([[t for t in range(300) if t // 16 != 7]] * 50, np.int32)
+    got = mqa.kv_attention(q, dev, ints([0, 50]))
+    assert mqa.kv_status(dev) == 2
+    check(got, None, c.attention(qd, np.array([0, 50]), 0.125, "fp16", sel))
+
+
 # ---------------------------------------------------------------- selected keys
 def random_selection(rng, c, rows, k, seen_only=False):
     sel = []
