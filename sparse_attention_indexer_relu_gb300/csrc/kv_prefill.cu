@@ -10,9 +10,9 @@
 // While one tile's scores are turned into weights the tensor cores work on the
 // other tile.  Roles: 2 x 4 softmax warps (a thread per column; it also moves
 // its references and rescales its row of O when a score passes them by 2^8),
-// 4 converter warps (codes from global memory to fp16 in the swizzled layouts
-// that the MMAs read: K with its components contiguous, V as it lies, which
-// the MMA reads transposed), one issuing warp.
+// 2 x 4 converter warps (codes from global memory to fp16 in the swizzled
+// layouts that the MMAs read: K with its components contiguous, V as it lies,
+// which the MMA reads transposed), one issuing warp.
 // Every wait has a time limit; once one has run out, all of them return at
 // once and the kernel runs to its end on whatever it finds in shared memory.
 //
@@ -28,7 +28,7 @@ namespace mqa {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kKeys = 128;                // keys per tile
 constexpr int kCols = kTiledCols;         // columns per item
 constexpr int kStagesKV = 2;
@@ -36,7 +36,7 @@ constexpr int kMeta = 4;                  // tile descriptions in flight (softma
 constexpr float kSlack = 8.0f;
 constexpr long long kWaitNs = 2000000000LL;
 constexpr int kConverters = 128;
-constexpr int kBarConv = 1;               // named barrier of the converters
+constexpr int kBarConv = 1;               // named barriers of the two converter groups
 
 struct TileMeta {
   float ks[8], lv[8];    // per 16 keys: key scale, log2 of the value scale
@@ -51,7 +51,7 @@ struct Smem {
   uint8_t v[kStagesKV][kKeys * D * 2];
   float cs[2][kCols];
   TileMeta meta[kMeta];
-  int row[kMeta][8];     // first row of each 16 keys in the pool, -1: none
+  int row[2][kMeta][8];  // keys', values': first row of each 16 keys in the pool, below 0: none
   uint64_t q_full, q_empty, k_full[kStagesKV], k_empty[kStagesKV], v_full[kStagesKV], v_empty[kStagesKV];
   uint64_t s_full[2], p_full[2], o_full[2], done;
   uint32_t tmem;
@@ -62,20 +62,27 @@ struct Smem {
 
 // sum over 0 <= i < n of floor((a i + b) / m); a, b >= 0, m > 0.  Whole parts
 // first; what is left below the line is counted along the other axis.
-__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+template <typename T>
+__device__ __forceinline__ long long floor_sum_as(long long n, T m, T a, T b) {
   long long sum = 0;
   while (true) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long top = a * n + b;
+    const T qa = a / m, qb = b / m;
+    sum += n * (n - 1) / 2 * (long long)qa + n * (long long)qb;
+    a -= qa * m;
+    b -= qb * m;
+    const T top = a * (T)n + b;
     if (top < m) return sum;
-    n = top / m;
-    b = top % m;
-    const long long x = a;
+    n = (long long)(top / m);
+    b = top - (T)n * m;
+    const T x = a;
     a = m;
     m = x;
   }
+}
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  // all that is divided is at most a n + b: 32-bit division where that fits
+  if (n < (1 << 20) && a * n + b < (1LL << 32)) return floor_sum_as<uint32_t>(n, (uint32_t)m, (uint32_t)a, (uint32_t)b);
+  return floor_sum_as<unsigned long long>(n, m, a, b);
 }
 
 // Shape of a sequence's work.
@@ -198,17 +205,6 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -240,14 +236,23 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 }
 
 // ------------------------------------------------------------------ converters
-template <int D>
+// One group of 4 warps converts the keys, another the values; each also loads
+// half of an item's queries.  A warp's load covers whole 128-byte lines; its
+// lanes are laid out so that 8 of them store to 8 different bank groups (4
+// chunks of two rows whose exchanges differ in the lowest bit).
+template <int D, bool VALUES>
 __device__ void convert_role(const AttnParams &p, Smem<D> &sm, Walk w) {
-  constexpr int CH = D / 16;            // 16-byte chunks of a code row
-  constexpr int RPS = kConverters / CH; // rows per step
-  constexpr int STEPS = kKeys / RPS;    // 8 (D = 128) or 4
-  const int tid = threadIdx.x & (kConverters - 1);
-  const int ch = tid % CH, r0 = tid / CH;
+  constexpr int CH = D / 16;              // 16-byte chunks of a code row
+  constexpr int RPS = kConverters / CH;   // rows per step: 16 (D = 128) or 32
+  constexpr int STEPS = kKeys / RPS;
+  const int tid = threadIdx.x & (kConverters - 1), lane = tid & 31;
+  const int ch = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3;
+  const int r0 = D == 128 ? (tid >> 5) * 4 + (lane >> 2 & 3) : (tid >> 5) * 8 + (lane >> 2);
   const int heads = p.c.heads;
+  const uint8_t *codes = VALUES ? p.c.v : p.c.k;
+  uint64_t *full = VALUES ? sm.v_full : sm.k_full, *empty = VALUES ? sm.v_empty : sm.k_empty;
+  int(*rows)[8] = sm.row[VALUES];
+  constexpr int kBar = kBarConv + VALUES;
   uint32_t tile_no = 0, q_no = 0;
   for (; w.valid(); w.next(p)) {
     const int nt = w.needed(p), ncols = w.cols(p);
@@ -263,138 +268,128 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm, Walk w) {
       const int pos = (w.x.t0 + t) * kKeys + tid * 16;
       if (tid >= 8 || t >= nt || pos >= lim) return -2;  // nothing there
       if ((unsigned)page >= (unsigned)p.c.pages) {
-        atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
+        if (VALUES) atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
         return -1;
       }
       return ((page * heads + w.x.head) << p.c.page_log2) + (pos & (p.c.page - 1));
     };
-    auto load_exps = [&](int row) -> uint32_t {
-      if (row < 0) return 127u | 127u << 8;
+    // nothing is computed from a loaded value before it is published, an iteration later
+    uint32_t ke1 = 127, ve1 = 127;
+    auto load_exps = [&](int row) {
+      if (!VALUES || row < 0) return;
       const int ph = row >> p.c.page_log2;
-      return (uint32_t)__ldg(p.c.k_exps + ph) | (uint32_t)__ldg(p.c.v_exps + ph) << 8;
+      ke1 = __ldg(p.c.k_exps + ph);
+      ve1 = __ldg(p.c.v_exps + ph);
     };
-    auto publish = [&](uint32_t no, int row, uint32_t e) {
+    auto publish = [&](uint32_t no, int row) {
       const int m = no % kMeta;
       if (tid < 8) {
-        sm.meta[m].ks[tid] = exp_byte(e & 255u);
-        sm.meta[m].lv[tid] = (float)(int)(e >> 8) - 127.f;
-        sm.row[m][tid] = row;
-        const uint32_t bad = __ballot_sync(0xFFu, row == -1);
-        if (tid < 4) {
-          sm.meta[m].hide[tid] = (bad >> (2 * tid) & 1 ? 0xFFFFu : 0u) | (bad >> (2 * tid + 1) & 1 ? 0xFFFF0000u : 0u);
-          sm.meta[m].nan[tid] = 0;
+        rows[m][tid] = row;
+        if (VALUES) {
+          sm.meta[m].ks[tid] = exp_byte(ke1);
+          sm.meta[m].lv[tid] = (float)(int)ve1 - 127.f;
+          const uint32_t bad = __ballot_sync(0xFFu, row == -1);
+          if (tid < 4) {
+            sm.meta[m].hide[tid] = (bad >> (2 * tid) & 1 ? 0xFFFFu : 0u) | (bad >> (2 * tid + 1) & 1 ? 0xFFFF0000u : 0u);
+            sm.meta[m].nan[tid] = 0;
+          }
         }
       }
     };
-    uint4 kr[STEPS], vr[STEPS];
-    auto load = [&](uint32_t no, const uint8_t *codes, uint4 (&x)[STEPS]) {
+    uint4 x[STEPS];
+    auto load = [&](uint32_t no) {
       const int m = no % kMeta;
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
         const int r = i * RPS + r0;
-        const int row = sm.row[m][r >> 4];
+        const int row = rows[m][r >> 4];
         x[i] = make_uint4(0, 0, 0, 0);
-        if (row >= 0)
-          x[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)(row + (r & 15)) * D + ch * 16));
+        if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)(row + (r & 15)) * D + ch * 16));
       }
     };
     int pg2 = load_page(0);
     int row1 = row_of(0, pg2);
-    uint32_t e1 = load_exps(row1);
+    load_exps(row1);
     pg2 = load_page(1);
-    // tile 0 is published before any converter of the previous part could still read its slot
-    named_bar(kBarConv, kConverters);
-    publish(tile_no, row1, e1);
-    row1 = row_of(1, pg2), e1 = load_exps(row1), pg2 = load_page(2);
-    named_bar(kBarConv, kConverters);
-    load(tile_no, p.c.k, kr);
-    load(tile_no, p.c.v, vr);
+    publish(tile_no, row1);
+    row1 = row_of(1, pg2), load_exps(row1), pg2 = load_page(2);
+    named_bar(kBar, kConverters);
+    load(tile_no);
 
     for (int t = 0; t < nt; ++t, ++tile_no) {
       const int stage = tile_no % kStagesKV;
       const uint32_t round = tile_no / kStagesKV;
-      if (t + 1 < nt) publish(tile_no + 1, row1, e1);
-      row1 = row_of(t + 2, pg2), e1 = load_exps(row1), pg2 = load_page(t + 3);
-      named_bar(kBarConv, kConverters);
-      // K
-      wait(sm, &sm.k_empty[stage], (round & 1) ^ 1, p.c.status);
+      if (t + 1 < nt) publish(tile_no + 1, row1);
+      row1 = row_of(t + 2, pg2), load_exps(row1), pg2 = load_page(t + 3);
+      named_bar(kBar, kConverters);
+      wait(sm, &empty[stage], (round & 1) ^ 1, p.c.status);
+      uint8_t *dst = VALUES ? sm.v[stage] : sm.k[stage];
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
         const int r = i * RPS + r0;
-        const uint32_t ws[4] = {kr[i].x, kr[i].y, kr[i].z, kr[i].w};
-        const uint4 a = make_uint4(cvt2(ws[0]), cvt2_hi(ws[0]), cvt2(ws[1]), cvt2_hi(ws[1]));
-        const uint4 b = make_uint4(cvt2(ws[2]), cvt2_hi(ws[2]), cvt2(ws[3]), cvt2_hi(ws[3]));
-        // the second half's lanes store in the other order: all banks at once
-        const bool sw = ch & 4;
-        *reinterpret_cast<uint4 *>(sm.k[stage] + chunk_at(r, 2 * ch + (sw ? 1 : 0))) = sw ? b : a;
-        *reinterpret_cast<uint4 *>(sm.k[stage] + chunk_at(r, 2 * ch + (sw ? 0 : 1))) = sw ? a : b;
+        uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        if (VALUES) {
+          const uint32_t odd = nan_bytes(ws[0]) | nan_bytes(ws[1]) | nan_bytes(ws[2]) | nan_bytes(ws[3]);
+          if (odd) {  // taken out here; the scores of the columns that see the key become NaN
+            atomicOr(&sm.meta[tile_no % kMeta].nan[r >> 5], 1u << (r & 31));
+#pragma unroll
+            for (int b = 0; b < 4; ++b) ws[b] &= ~((nan_bytes(ws[b]) >> 7) * 255u);
+          }
+        }
+        *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * ch)) =
+            make_uint4(cvt2(ws[0]), cvt2_hi(ws[0]), cvt2(ws[1]), cvt2_hi(ws[1]));
+        *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * ch + 1)) =
+            make_uint4(cvt2(ws[2]), cvt2_hi(ws[2]), cvt2(ws[3]), cvt2_hi(ws[3]));
       }
       fence_async_smem();
-      mbar_arrive(&sm.k_full[stage]);
-      if (t + 1 < nt) load(tile_no + 1, p.c.k, kr);
+      mbar_arrive(&full[stage]);
+      if (t + 1 < nt) load(tile_no + 1);
       if (t == 0) {
-        // ---- Q: rows tid and tid + 128; the previous part's last scores must be done
+        // ---- this group's 128 query rows (the previous part's last scores must be
+        // done): 8 components per lane, a row's largest magnitude by exchange
         wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p.c.status);
+        constexpr int LPR = D / 8, QR = 32 / LPR;  // lanes per row, rows per warp step
+        const int part = lane % LPR;
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          const int col = x * 128 + tid;
-          uint8_t *dst = sm.q[x];
-          const int cc = w.x.block * kCols + col;
-          const size_t off = col < ncols ? (size_t)(w.x.q.r0 + cc / p.group) * p.q_stride +
-                                               (size_t)(w.x.head * p.group + cc % p.group) * D
-                                         : 0;
-          const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + off);
-          float amax = 0.f;
-          for (int j = 0; j < D / 8; ++j) {
-            const uint4 u = col < ncols ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-            const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+        for (int b = 0; b < 32 / QR; b += 8) {
+          uint4 u[8];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const float2 f = p.bf16 ? bf16x2_to_float2(ws[b]) : half2_to_float2(ws[b]);
-              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
+          for (int i = 0; i < 8; ++i) {
+            const int r = (tid >> 5) * 32 + (b + i) * QR + lane / LPR, col = VALUES * 128 + r;
+            const int cc = w.x.block * kCols + col;
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (col < ncols)
+              u[i] = __ldg(reinterpret_cast<const uint4 *>(
+                  reinterpret_cast<const uint16_t *>(p.q) + (size_t)(w.x.q.r0 + cc / p.group) * p.q_stride +
+                  (size_t)(w.x.head * p.group + cc % p.group) * D + part * 8));
           }
-          int e = 0;
-          if (amax > 0.f && amax <= FLT_MAX) e = 10 - exponent_of(amax);
-          e = max(-100, min(100, e));
-          const float up = pow2i(e);
-          sm.cs[q_no & 1][col] = p.scale_log2 * pow2i(-e);
-          for (int j = 0; j < D / 8; ++j) {
-            const uint4 u = col < ncols ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-            const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = (tid >> 5) * 32 + (b + i) * QR + lane / LPR;
+            const uint32_t ws[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+            float2 f[4];
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              f[j] = p.bf16 ? bf16x2_to_float2(ws[j]) : half2_to_float2(ws[j]);
+              amax = fmaxf(amax, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
+            }
+#pragma unroll
+            for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+            int e = 0;
+            if (amax > 0.f && amax <= FLT_MAX) e = 10 - exponent_of(amax);
+            e = max(-100, min(100, e));
+            const float up = pow2i(e);
+            if (part == 0) sm.cs[q_no & 1][VALUES * 128 + r] = p.scale_log2 * pow2i(-e);
             uint32_t h[4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const float2 f = p.bf16 ? bf16x2_to_float2(ws[b]) : half2_to_float2(ws[b]);
-              h[b] = float2_to_half2(f.x * up, f.y * up);
-            }
-            *reinterpret_cast<uint4 *>(dst + chunk_at(tid, j)) = make_uint4(h[0], h[1], h[2], h[3]);
+            for (int j = 0; j < 4; ++j) h[j] = float2_to_half2(f[j].x * up, f[j].y * up);
+            *reinterpret_cast<uint4 *>(sm.q[VALUES] + chunk_at(r, part)) = make_uint4(h[0], h[1], h[2], h[3]);
           }
         }
         fence_async_smem();
         mbar_arrive(&sm.q_full);
       }
-      // V
-      wait(sm, &sm.v_empty[stage], (round & 1) ^ 1, p.c.status);
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int r = i * RPS + r0;
-        uint32_t ws[4] = {vr[i].x, vr[i].y, vr[i].z, vr[i].w};
-        const uint32_t odd = nan_bytes(ws[0]) | nan_bytes(ws[1]) | nan_bytes(ws[2]) | nan_bytes(ws[3]);
-        if (odd) {  // taken out here; the scores of the columns that see the key become NaN
-          atomicOr(&sm.meta[tile_no % kMeta].nan[r >> 5], 1u << (r & 31));
-#pragma unroll
-          for (int b = 0; b < 4; ++b) ws[b] &= ~((nan_bytes(ws[b]) >> 7) * 255u);
-        }
-        const uint4 a = make_uint4(cvt2(ws[0]), cvt2_hi(ws[0]), cvt2(ws[1]), cvt2_hi(ws[1]));
-        const uint4 b = make_uint4(cvt2(ws[2]), cvt2_hi(ws[2]), cvt2(ws[3]), cvt2_hi(ws[3]));
-        const bool sw = ch & 4;
-        *reinterpret_cast<uint4 *>(sm.v[stage] + chunk_at(r, 2 * ch + (sw ? 1 : 0))) = sw ? b : a;
-        *reinterpret_cast<uint4 *>(sm.v[stage] + chunk_at(r, 2 * ch + (sw ? 0 : 1))) = sw ? a : b;
-      }
-      fence_async_smem();
-      mbar_arrive(&sm.v_full[stage]);
-      if (t + 1 < nt) load(tile_no + 1, p.c.v, vr);
     }
     ++q_no;
   }
@@ -469,6 +464,125 @@ __device__ void mma_role(const AttnParams &p, Smem<D> &sm, Walk w) {
 }
 
 // ------------------------------------------------------------------ softmax
+// How a tile's scores are read: as they are; cut at the keys the column sees;
+// or with every rare case (pages outside the pool, NaN values, scales far apart).
+enum Mode { kPlain, kCut, kRare };
+
+template <int MODE>
+__device__ __forceinline__ void hide_keys(uint32_t (&s)[32], const TileMeta &meta, int j, int room) {
+  if (MODE == kPlain) return;
+  if (MODE == kRare) {
+    const uint32_t hide = meta.hide[j], nan = meta.nan[j];
+#pragma unroll
+    for (int b = 0; b < 32; ++b) {
+      if (nan >> b & 1) s[b] = 0x7FC00000u;
+      if (hide >> b & 1) s[b] = 0xFF800000u;  // -inf
+    }
+  }
+  const int n = room - 32 * j;
+#pragma unroll
+  for (int b = 0; b < 32; ++b)
+    if (b >= n) s[b] = 0xFF800000u;
+}
+
+// A column's largest score of the tile, and largest score plus value exponent.
+// The next 32 columns are on their way from TMEM while 32 are looked at.
+template <int MODE>
+__device__ __forceinline__ void scan_scores(uint32_t ts, const TileMeta &meta, int room, float cs, float &top,
+                                            float &topw) {
+  auto look = [&](uint32_t(&s)[32], int j) {
+    hide_keys<MODE>(s, meta, j, room);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      float a[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) a[b] = __uint_as_float(s[16 * g + b]);
+#pragma unroll
+      for (int b = 4; b < 16; ++b) a[b & 3] = fmaxf(a[b & 3], __uint_as_float(s[16 * g + b]));
+      const float x = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * (cs * meta.ks[2 * j + g]);
+      top = fmaxf(top, x);
+      topw = fmaxf(topw, x + meta.lv[2 * j + g]);
+    }
+  };
+  uint32_t s0[32], s1[32];
+  tmem_ld_32x32b_x32(ts, s0);
+#pragma unroll 1
+  for (int j = 0; j < 4; j += 2) {
+    tmem_ld_wait();
+    tmem_ld_32x32b_x32(ts + 32 * j + 32, s1);
+    look(s0, j);
+    tmem_ld_wait();
+    if (j == 0) tmem_ld_32x32b_x32(ts + 64, s0);
+    look(s1, j + 1);
+  }
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Scores to weights, in place (fp16 over the first half of the fp32 columns);
+// returns the column's sum with this tile's.  A weight in the sum is 2^back of
+// the one that enters the product.
+template <int MODE>
+__device__ __forceinline__ float weigh(uint32_t ts, const TileMeta &meta, int room, float cs, float mr, float ww,
+                                       float l) {
+  auto turn = [&](uint32_t(&s)[32], int j) {
+    hide_keys<MODE>(s, meta, j, room);
+    uint32_t h[16];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float f = cs * meta.ks[2 * j + g], lv = meta.lv[2 * j + g];
+      const float b = lv - ww, back = ww - lv - mr;
+      const uint64_t f2 = pack2(f, f), b2 = pack2(b, b);
+      if (MODE == kRare && back > 64.f) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) l += ex2(__uint_as_float(s[16 * g + k]) * f - mr);
+      }
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float y, z;
+        unpack2(fma2(pack2(__uint_as_float(s[16 * g + 2 * k]), __uint_as_float(s[16 * g + 2 * k + 1])), f2, b2), y, z);
+        y = ex2(y), z = ex2(z);
+        sum[k & 1] = add2(sum[k & 1], pack2(y, z));
+        h[8 * g + k] = float2_to_half2(y, z);
+      }
+      float y, z;
+      unpack2(add2(sum[0], sum[1]), y, z);
+      if (MODE != kRare || !(back > 64.f)) l = fmaf(y + z, ex2(back), l);
+    }
+    tmem_st16(ts + 16 * j, h);
+  };
+  uint32_t s0[32], s1[32];
+  tmem_ld_32x32b_x32(ts, s0);
+#pragma unroll 1
+  for (int j = 0; j < 4; j += 2) {
+    tmem_ld_wait();
+    tmem_ld_32x32b_x32(ts + 32 * j + 32, s1);
+    turn(s0, j);
+    tmem_ld_wait();
+    if (j == 0) tmem_ld_32x32b_x32(ts + 64, s0);
+    turn(s1, j + 1);
+  }
+  return l;
+}
+
 template <int D>
 __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, Walk w, long long per) {
   const int x = threadIdx.x >> 7;        // tile of columns
@@ -505,38 +619,16 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, Walk w, long long
       __syncwarp();
       tc_fence_after();
       const TileMeta &meta = sm.meta[tile_no % kMeta];
-      uint32_t s[128];
-      tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(s));
-      tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-      tmem_ld_32x32b_x32(ts + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 64));
-      tmem_ld_32x32b_x32(ts + 96, *reinterpret_cast<uint32_t(*)[32]>(s + 96));
-      tmem_ld_wait();
       const int room = lim - (w.x.t0 + t) * kKeys;  // keys of the tile that the column sees
       uint32_t odd = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) odd |= meta.hide[j] | meta.nan[j];
-      if (__any_sync(~0u, room < kKeys) || odd) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t hide = meta.hide[j], nan = meta.nan[j];
-#pragma unroll
-          for (int b = 0; b < 32; ++b) {
-            if (nan >> b & 1) s[32 * j + b] = 0x7FC00000u;
-            if (32 * j + b >= room || (hide >> b & 1)) s[32 * j + b] = 0xFF800000u;  // -inf
-          }
-        }
-      }
+      const bool cut = __any_sync(~0u, room < kKeys);
       // largest score, and largest score with the value scale
       float top = -INFINITY, topw = -INFINITY;
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        float a = __uint_as_float(s[16 * g]);
-#pragma unroll
-        for (int j = 1; j < 16; ++j) a = fmaxf(a, __uint_as_float(s[16 * g + j]));
-        a *= cs * meta.ks[g];
-        top = fmaxf(top, a);
-        topw = fmaxf(topw, a + meta.lv[g]);
-      }
+      if (odd) scan_scores<kRare>(ts, meta, room, cs, top, topw);
+      else if (cut) scan_scores<kCut>(ts, meta, room, cs, top, topw);
+      else scan_scores<kPlain>(ts, meta, room, cs, top, topw);
       const bool move = top > m + kSlack || topw > wr + kSlack;
       if (__any_sync(~0u, move)) {
         const float mn = fmaxf(m, top), wn = fmaxf(wr, topw);
@@ -556,30 +648,14 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, Walk w, long long
         }
       }
       const float mr = m == -INFINITY ? 0.f : m, ww = wr == -INFINITY ? 0.f : wr;
+      // values so small that their weights would leave fp32's range before they
+      // are scaled back: the sum takes a power of two of its own
+      bool far = false;
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const float f = cs * meta.ks[g], lv = meta.lv[g];
-        const float b = lv - ww, back = ww - lv - mr;  // a weight is 2^back times what enters the product
-        float sum = 0.f;
-        if (back > 64.f) {  // values so small that their weights would leave fp32's range here
-#pragma unroll
-          for (int j = 0; j < 16; ++j) l += ex2(__uint_as_float(s[16 * g + j]) * f - mr);
-        }
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float y = ex2(fmaf(__uint_as_float(s[16 * g + 2 * j]), f, b));
-          const float z = ex2(fmaf(__uint_as_float(s[16 * g + 2 * j + 1]), f, b));
-          sum += y;
-          sum += z;
-          h[j] = float2_to_half2(y, z);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[8 * g + j] = h[j];
-        if (!(back > 64.f)) l = fmaf(sum, ex2(back), l);
-      }
-      tmem_st32(ts, s);
-      tmem_st32(ts + 32, s + 32);
+      for (int g = 0; g < 8; ++g) far |= ww - meta.lv[g] - mr > 64.f;
+      if (odd || __any_sync(~0u, far)) l = weigh<kRare>(ts, meta, room, cs, mr, ww, l);
+      else if (cut) l = weigh<kCut>(ts, meta, room, cs, mr, ww, l);
+      else l = weigh<kPlain>(ts, meta, room, cs, mr, ww, l);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&sm.p_full[x]);
@@ -692,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const AttnParam
   }
   if (tid == 0) {
     sm.dead = 0;
-    mbar_init(&sm.q_full, kConverters);
+    mbar_init(&sm.q_full, 2 * kConverters);
     mbar_init(&sm.q_empty, 1);
     for (int i = 0; i < kStagesKV; ++i) {
       mbar_init(&sm.k_full[i], kConverters);
@@ -708,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const AttnParam
     mbar_init(&sm.done, 1);
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
@@ -731,20 +807,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const AttnParam
     w.x.t0 = (int)(rest - tiles_before(p, w.x.q, lo));
     w.fit();
   }
-  // registers: 256 x 176 + 128 x 112 + 128 x 48 = 512 x 128, what the block was launched with
+  // registers: 256 x 128 + 256 x 88 + 128 x 48 = 640 x 96, what the block was launched with
   if (warp < 8) {
-    reg_inc<176>();
+    reg_inc<128>();
     softmax_role<D>(p, sm, w, per);
   } else if (warp < 12) {
-    reg_dec<112>();
-    convert_role<D>(p, sm, w);
+    reg_dec<88>();
+    convert_role<D, false>(p, sm, w);
+  } else if (warp < 16) {
+    reg_dec<88>();
+    convert_role<D, true>(p, sm, w);
   } else {
     reg_dec<48>();
-    if (warp == 12) mma_role<D>(p, sm, w);
+    if (warp == 16) mma_role<D>(p, sm, w);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) tmem_dealloc(sm.tmem, 512);
+  if (warp == 16) tmem_dealloc(sm.tmem, 512);
 }
 
 // Join split items: block (c, y) adds the parts of 32 columns of the item that
