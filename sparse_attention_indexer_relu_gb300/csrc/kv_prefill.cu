@@ -38,28 +38,6 @@ constexpr long long kWaitNs = 2000000000LL;
 constexpr int kConverters = 128;
 constexpr int kBarConv = 1;               // named barriers of the two converter groups
 
-struct TileMeta {
-  float ks[8], lv[8];    // per 16 keys: key scale, log2 of the value scale
-  uint32_t hide[4];      // keys that no column sees (a page outside the pool)
-  uint32_t nan[4];       // keys whose values hold a NaN code
-};
-
-template <int D>
-struct Smem {
-  uint8_t q[2][128 * D * 2];
-  uint8_t k[kStagesKV][kKeys * D * 2];
-  uint8_t v[kStagesKV][kKeys * D * 2];
-  float cs[2][kCols];
-  TileMeta meta[kMeta];
-  int row[2][kMeta][8];  // keys', values': first row of each 16 keys in the pool, below 0: none
-  uint64_t q_full, q_empty, k_full[kStagesKV], k_empty[kStagesKV], v_full[kStagesKV], v_empty[kStagesKV];
-  uint64_t s_full[2], p_full[2], o_full[2], done;
-  uint32_t tmem;
-  int dead;
-  int found_seq;
-  long long found_at, scan[kThreads / 32];
-};
-
 // sum over 0 <= i < n of floor((a i + b) / m); a, b >= 0, m > 0.  Whole parts
 // first; what is left below the line is counted along the other axis.
 template <typename T>
@@ -123,7 +101,9 @@ struct Part {  // a part of an item: tiles [t0, t1) of tiles
   Seq q;
 };
 
-// The CTA's parts, one after another; every thread walks by itself.
+// The CTA's parts, one after another.  Each warp walks by itself; its state lies
+// in shared memory, where lane 0 moves it on (in registers it would crowd out
+// the tiles that are on their way).
 struct Walk {
   long long at, end;
   Part x;
@@ -153,6 +133,35 @@ struct Walk {
     return (int)min((long long)kCols, (long long)x.q.n * p.group - (long long)x.block * kCols);
   }
 };
+
+struct TileMeta {
+  float ks[8], lv[8];    // per 16 keys: key scale, log2 of the value scale
+  uint32_t hide[4];      // keys that no column sees (a page outside the pool)
+  uint32_t nan[4];       // keys whose values hold a NaN code
+};
+
+template <int D>
+struct Smem {
+  uint8_t q[2][128 * D * 2];
+  uint8_t k[kStagesKV][kKeys * D * 2];
+  uint8_t v[kStagesKV][kKeys * D * 2];
+  float cs[2][kCols];
+  TileMeta meta[kMeta];
+  int row[2][kMeta][8];  // keys', values': first row of each 16 keys in the pool, below 0: none
+  uint64_t q_full, q_empty, k_full[kStagesKV], k_empty[kStagesKV], v_full[kStagesKV], v_empty[kStagesKV];
+  uint64_t s_full[2], p_full[2], o_full[2], done;
+  Walk walk[kThreads / 32];
+  uint32_t tmem;
+  int dead;
+  int found_seq;
+  long long found_at, scan[kThreads / 32];
+};
+
+__device__ __forceinline__ void step_on(const AttnParams &p, Walk &w) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) w.next(p);
+  __syncwarp();
+}
 
 // ------------------------------------------------------------------ waits
 template <int D>
@@ -241,7 +250,8 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 // lanes are laid out so that 8 of them store to 8 different bank groups (4
 // chunks of two rows whose exchanges differ in the lowest bit).
 template <int D, bool VALUES>
-__device__ void convert_role(const AttnParams &p, Smem<D> &sm, Walk w) {
+__device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
+  Walk &w = sm.walk[threadIdx.x >> 5];
   constexpr int CH = D / 16;              // 16-byte chunks of a code row
   constexpr int RPS = kConverters / CH;   // rows per step: 16 (D = 128) or 32
   constexpr int STEPS = kKeys / RPS;
@@ -254,24 +264,24 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm, Walk w) {
   int(*rows)[8] = sm.row[VALUES];
   constexpr int kBar = kBarConv + VALUES;
   uint32_t tile_no = 0, q_no = 0;
-  for (; w.valid(); w.next(p)) {
+  for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p), ncols = w.cols(p);
-    const int lim = block_limit(p, w.x.q, w.x.block);
+    const int lim = block_limit(p, w.x.q, w.x.block), first = w.x.t0 * kKeys + tid * 16, head = w.x.head;
     const int32_t *table = p.c.table + (size_t)w.x.seq * p.c.max_pages;
     if (nt == 0) continue;  // softmax reads nothing either
     // lookups: threads 0 .. 7 hold 16 keys each, pages three tiles ahead, exponents two
     auto load_page = [&](int t) -> int {
-      const int pos = (w.x.t0 + t) * kKeys + tid * 16;
+      const int pos = first + t * kKeys;
       return tid < 8 && t < nt && pos < lim ? __ldg(table + (pos >> p.c.page_log2)) : -1;
     };
     auto row_of = [&](int t, int page) -> int {
-      const int pos = (w.x.t0 + t) * kKeys + tid * 16;
+      const int pos = first + t * kKeys;
       if (tid >= 8 || t >= nt || pos >= lim) return -2;  // nothing there
       if ((unsigned)page >= (unsigned)p.c.pages) {
         if (VALUES) atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
         return -1;
       }
-      return ((page * heads + w.x.head) << p.c.page_log2) + (pos & (p.c.page - 1));
+      return ((page * heads + head) << p.c.page_log2) + (pos & (p.c.page - 1));
     };
     // nothing is computed from a loaded value before it is published, an iteration later
     uint32_t ke1 = 127, ve1 = 127;
@@ -297,15 +307,11 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm, Walk w) {
       }
     };
     uint4 x[STEPS];
-    auto load = [&](uint32_t no) {
-      const int m = no % kMeta;
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int r = i * RPS + r0;
-        const int row = rows[m][r >> 4];
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)(row + (r & 15)) * D + ch * 16));
-      }
+    auto load = [&](uint32_t no, int i) {
+      const int r = i * RPS + r0;
+      const int row = rows[no % kMeta][r >> 4];
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)(row + (r & 15)) * D + ch * 16));
     };
     int pg2 = load_page(0);
     int row1 = row_of(0, pg2);
@@ -314,7 +320,8 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm, Walk w) {
     publish(tile_no, row1);
     row1 = row_of(1, pg2), load_exps(row1), pg2 = load_page(2);
     named_bar(kBar, kConverters);
-    load(tile_no);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) load(tile_no, i);
 
     for (int t = 0; t < nt; ++t, ++tile_no) {
       const int stage = tile_no % kStagesKV;
@@ -340,10 +347,10 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm, Walk w) {
             make_uint4(cvt2(ws[0]), cvt2_hi(ws[0]), cvt2(ws[1]), cvt2_hi(ws[1]));
         *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * ch + 1)) =
             make_uint4(cvt2(ws[2]), cvt2_hi(ws[2]), cvt2(ws[3]), cvt2_hi(ws[3]));
+        if (t + 1 < nt) load(tile_no + 1, i);  // on its way while the rest is converted
       }
       fence_async_smem();
       mbar_arrive(&full[stage]);
-      if (t + 1 < nt) load(tile_no + 1);
       if (t == 0) {
         // ---- this group's 128 query rows (the previous part's last scores must be
         // done): 8 components per lane, a row's largest magnitude by exchange
@@ -397,7 +404,8 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm, Walk w) {
 
 // ------------------------------------------------------------------ MMA issue
 template <int D>
-__device__ void mma_role(const AttnParams &p, Smem<D> &sm, Walk w) {
+__device__ void mma_role(const AttnParams &p, Smem<D> &sm) {
+  Walk &w = sm.walk[threadIdx.x >> 5];
   const uint32_t tmem = sm.tmem;
   const bool lead = (threadIdx.x & 31) == 0;
   constexpr uint32_t kQk = idesc_f16(128, kKeys, false), kPv = idesc_f16(128, D, true);
@@ -422,7 +430,7 @@ __device__ void mma_role(const AttnParams &p, Smem<D> &sm, Walk w) {
       umma_ts(tmem + x * 128, tmem + 256 + x * 128 + kk * 8, desc_mn(b + kk * 2048, 128 * 128), kPv,
               !first || kk > 0);
   };
-  for (; w.valid(); w.next(p)) {
+  for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p);
     const bool two = w.cols(p) > 128;
     if (nt == 0) continue;
@@ -485,6 +493,16 @@ __device__ __forceinline__ void hide_keys(uint32_t (&s)[32], const TileMeta &met
     if (b >= n) s[b] = 0xFF800000u;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, uint32_t c) { return max3(a, b, __uint_as_float(c)); }
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+  return max3(__uint_as_float(a), __uint_as_float(b), c);
+}
+
 // A column's largest score of the tile, and largest score plus value exponent.
 // The next 32 columns are on their way from TMEM while 32 are looked at.
 template <int MODE>
@@ -494,12 +512,10 @@ __device__ __forceinline__ void scan_scores(uint32_t ts, const TileMeta &meta, i
     hide_keys<MODE>(s, meta, j, room);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      float a[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) a[b] = __uint_as_float(s[16 * g + b]);
-#pragma unroll
-      for (int b = 4; b < 16; ++b) a[b & 3] = fmaxf(a[b & 3], __uint_as_float(s[16 * g + b]));
-      const float x = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * (cs * meta.ks[2 * j + g]);
+      const uint32_t *v = s + 16 * g;
+      const float a = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), v[6]);
+      const float b = max3(max3(v[7], v[8], v[9]), max3(v[10], v[11], v[12]), v[13]);
+      const float x = max3(fmaxf(a, __uint_as_float(v[14])), b, v[15]) * (cs * meta.ks[2 * j + g]);
       top = fmaxf(top, x);
       topw = fmaxf(topw, x + meta.lv[2 * j + g]);
     }
@@ -584,13 +600,14 @@ __device__ __forceinline__ float weigh(uint32_t ts, const TileMeta &meta, int ro
 }
 
 template <int D>
-__device__ void softmax_role(const AttnParams &p, Smem<D> &sm, Walk w, long long per) {
+__device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
+  Walk &w = sm.walk[threadIdx.x >> 5];
   const int x = threadIdx.x >> 7;        // tile of columns
   const int r = threadIdx.x & 127;       // its column
   const uint32_t lanes = (uint32_t)(r & ~31) << 16;
   const uint32_t ts = sm.tmem + 256 + x * 128 + lanes, to = sm.tmem + x * 128 + lanes;
   uint32_t tile_no = 0, q_no = 0, s_no = 0, o_no = 0;
-  for (; w.valid(); w.next(p)) {
+  for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p), ncols = w.cols(p);
     const int col = x * 128 + r;
     if (ncols <= x * 128) {  // this half is empty: it keeps step, so that it meets every phase of the barriers
@@ -607,6 +624,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, Walk w, long long
     const int lim = col < ncols ? (p.causal ? min(max(w.x.q.len - w.x.q.n + i + 1, 0), w.x.q.len) : w.x.q.len) : 0;
     float m = -INFINITY, wr = -INFINITY, l = 0.f;
     float cs = 0.f;
+    const int room0 = lim - w.x.t0 * kKeys;
     if (nt) {
       wait(sm, &sm.q_full, q_no & 1, p.c.status);
       cs = sm.cs[q_no & 1][col];
@@ -619,7 +637,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, Walk w, long long
       __syncwarp();
       tc_fence_after();
       const TileMeta &meta = sm.meta[tile_no % kMeta];
-      const int room = lim - (w.x.t0 + t) * kKeys;  // keys of the tile that the column sees
+      const int room = room0 - t * kKeys;  // keys of the tile that the column sees
       uint32_t odd = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) odd |= meta.hide[j] | meta.nan[j];
@@ -807,19 +825,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const AttnParam
     w.x.t0 = (int)(rest - tiles_before(p, w.x.q, lo));
     w.fit();
   }
+  if (lane == 0) sm.walk[warp] = w;
+  __syncwarp();
   // registers: 256 x 128 + 256 x 88 + 128 x 48 = 640 x 96, what the block was launched with
   if (warp < 8) {
     reg_inc<128>();
-    softmax_role<D>(p, sm, w, per);
+    softmax_role<D>(p, sm, per);
   } else if (warp < 12) {
     reg_dec<88>();
-    convert_role<D, false>(p, sm, w);
+    convert_role<D, false>(p, sm);
   } else if (warp < 16) {
     reg_dec<88>();
-    convert_role<D, true>(p, sm, w);
+    convert_role<D, true>(p, sm);
   } else {
     reg_dec<48>();
-    if (warp == 16) mma_role<D>(p, sm, w);
+    if (warp == 16) mma_role<D>(p, sm);
   }
   tc_fence_before();
   __syncthreads();
