@@ -207,7 +207,11 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
     p.max_cols = P.split ? kSplitCols : 0;
     p.desc = reinterpret_cast<int4 *>(ws + P.tiled_off);
     p.slots = reinterpret_cast<float *>(ws + P.tiled_slots_off);
-    rc = code(launch_kv_prefill(p, P.tiled_ctas, as_stream(stream)));
+    CUtensorMap map;
+    rc = encode_code_rows(&map, cache->k, (uint64_t)cache->num_pages * cache->kv_heads * cache->page_size,
+                          cache->head_dim, (uint32_t)cache->page_size);
+    if (rc != MQA_OK) return rc;
+    rc = code(launch_kv_prefill(p, map, P.tiled_ctas, as_stream(stream)));
     if (rc != MQA_OK || !P.split) return rc;
   }
   p.max_cols = P.tiled ? kSplitCols : INT_MAX;

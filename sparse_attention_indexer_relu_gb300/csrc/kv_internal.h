@@ -14,6 +14,9 @@ namespace mqa {
 int require_device(int *sms);
 // SM count of a device (any model).
 int device_sms(int device, int *sms);
+// Tensor map over `rows` rows of `dim` (64 or 128) codes, boxes of `box` rows,
+// swizzled by the row length.
+int encode_code_rows(CUtensorMap *map, const void *base, uint64_t rows, int dim, uint32_t box);
 
 // Cache fields as the kernels take them.
 struct KvView {
@@ -71,7 +74,8 @@ size_t attn_slot_floats(int nb, int dim);
 // more columns), and the fewest key tiles a CTA's part holds.
 constexpr int kTiledCols = 256;
 constexpr int kTiledMinTiles = 4;
-cudaError_t launch_kv_prefill(const AttnParams &p, int ctas, cudaStream_t stream);
+// map: the keys' codes as rows of head_dim bytes, boxes of one page.
+cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream);
 cudaError_t launch_kv_attention(const AttnParams &p, int nb, int ctas, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,

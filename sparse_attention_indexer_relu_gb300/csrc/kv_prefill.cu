@@ -3,16 +3,25 @@
 // (include/mqakv.h, mqa_kv_attention; the mathematics is kv_attn.cu's.)
 //
 // A CTA holds 256 columns of an item (query row x query head of one key/value
-// head) as two 128-row tiles and walks over 128-key tiles:
-//     S = Q K^T (Q, K fp16 in shared memory, S fp32 in TMEM),
+// head) as two 128-row halves and walks over 128-key tiles:
+//     S = Q K^T (kind::f8f6f4: the keys' codes as they lie in the pool, brought
+//         by TMA; each query value as a sum of e4m3 terms, below; S fp32 in TMEM),
 //     P = 2^(s + lv - w) rounded to fp16, written back over S in TMEM,
-//     O += P V (P from TMEM, V fp16 in shared memory, O fp32 in TMEM).
-// While one tile's scores are turned into weights the tensor cores work on the
-// other tile.  Roles: 2 x 4 softmax warps (a thread per column; it also moves
+//     O += P V (kind::f16: P from TMEM, V converted to fp16 in shared memory, O
+//         fp32 in TMEM).
+// Query terms: a row is multiplied by the power of two that brings its largest
+// magnitude to (224, 448]; x = t1 + t2 (+ t3), each term the e4m3 rounding of
+// what is left.  Two terms hold a bf16's 8 bits and three an fp16's 11 exactly,
+// down to e4m3's smallest step of 2^-9: what is lost is at most 2^-10 of 224,
+// 2^-17.8 of the row's largest value, and only in values below 2^-10 (bf16) or
+// 2^-7 (fp16) of it.  The products with two terms take as long as one fp16
+// product would, and no key has to be converted or stored twice.
+// While one half's scores are turned into weights the tensor cores work on the
+// other half.  Roles: 2 x 4 softmax warps (a thread per column; it also moves
 // its references and rescales its row of O when a score passes them by 2^8),
-// 2 x 4 converter warps (codes from global memory to fp16 in the swizzled
-// layouts that the MMAs read: K with its components contiguous, V as it lies,
-// which the MMA reads transposed), one issuing warp.
+// 4 converter warps (values to fp16, which the MMA reads transposed, and the
+// query terms), one warp that looks pages up and issues the keys' copies, one
+// that issues the MMAs.
 // Every wait has a time limit; once one has run out, all of them return at
 // once and the kernel runs to its end on whatever it finds in shared memory.
 //
@@ -28,15 +37,15 @@ namespace mqa {
 
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 512;
 constexpr int kKeys = 128;                // keys per tile
 constexpr int kCols = kTiledCols;         // columns per item
-constexpr int kStagesKV = 2;
-constexpr int kMeta = 4;                  // tile descriptions in flight (softmax is at most 3 behind)
+constexpr int kStagesK = 3, kStagesV = 2;
+constexpr int kMeta = 8;                  // tile descriptions in flight
+constexpr int kTerms = 3;                 // e4m3 terms of a query value (bf16: 2)
 constexpr float kSlack = 8.0f;
 constexpr long long kWaitNs = 2000000000LL;
 constexpr int kConverters = 128;
-constexpr int kBarConv = 1;               // named barriers of the two converter groups
 
 // sum over 0 <= i < n of floor((a i + b) / m); a, b >= 0, m > 0.  Whole parts
 // first; what is left below the line is counted along the other axis.
@@ -138,18 +147,19 @@ struct TileMeta {
   float ks[8], lv[8];    // per 16 keys: key scale, log2 of the value scale
   uint32_t hide[4];      // keys that no column sees (a page outside the pool)
   uint32_t nan[4];       // keys whose values hold a NaN code
+  int row[8];            // first row of each 16 keys in the pool; -1: page outside the pool, -2: no key needed
 };
+
 
 template <int D>
 struct Smem {
-  uint8_t q[2][128 * D * 2];
-  uint8_t k[kStagesKV][kKeys * D * 2];
-  uint8_t v[kStagesKV][kKeys * D * 2];
+  uint8_t q[2][kTerms][128 * D];
+  uint8_t k[kStagesK][kKeys * D];
+  uint8_t v[kStagesV][kKeys * D * 2];
   float cs[2][kCols];
   TileMeta meta[kMeta];
-  int row[2][kMeta][8];  // keys', values': first row of each 16 keys in the pool, below 0: none
-  uint64_t q_full, q_empty, k_full[kStagesKV], k_empty[kStagesKV], v_full[kStagesKV], v_empty[kStagesKV];
-  uint64_t s_full[2], p_full[2], o_full[2], done;
+  uint64_t q_full, q_empty, k_full[kStagesK], k_empty[kStagesK], v_full[kStagesV], v_empty[kStagesV];
+  uint64_t m_full[kMeta], m_empty[kMeta], s_full[2], p_full[2], o_full[2], done;
   Walk walk[kThreads / 32];
   uint32_t tmem;
   int dead;
@@ -183,39 +193,60 @@ __device__ __forceinline__ void wait(Smem<D> &sm, uint64_t *bar, uint32_t parity
   }
 }
 
-// ------------------------------------------------------------------ tcgen05
-// K-major operand: 128-byte rows of 64 fp16, 8-row groups of 1024 bytes.
-// MN-major (transposed) operand: the same bytes with the 64 contiguous values
-// along N: 1024 bytes between groups of 8 k, `block` bytes between blocks of 64 n.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t block) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(block >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// The same for copies in flight, also after another wait has run out.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kWaitNs) {
+  }
 }
+
+// ------------------------------------------------------------------ tcgen05
+// Shared-memory operand descriptors, in two words.  The low one is the address
+// in units of 16 bytes and the leading byte offset; it is all that changes from
+// one MMA to the next.  High word: stride byte offset, version, swizzle.
+//  codes (K-major): rows of D bytes (128: 128-byte swizzle, 64: 64-byte swizzle),
+//  8-row groups;
+//  values (transposed): 128-byte rows of 64 fp16 along N, 1024 bytes between
+//  groups of 8 k, 128 * 128 bytes between blocks of 64 n.
+template <int D>
+struct Desc {
+  static constexpr uint32_t codes_hi = ((8u * D) >> 4) | 1u << 14 | (D == 128 ? 2u : 4u) << 29;
+  static constexpr uint32_t values_hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+  static __device__ __forceinline__ uint32_t codes_lo(const void *p) {
+    return ((smem_u32(p) & 0x3FFFFu) >> 4) | 1u << 16;
+  }
+  static __device__ __forceinline__ uint32_t values_lo(const void *p) {
+    return ((smem_u32(p) & 0x3FFFFu) >> 4) | (128u * 128 >> 4) << 16;
+  }
+};
 // kind::f16, fp16 x fp16 -> fp32.
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t M, uint32_t N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_codes(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                           uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, "
+      "%3};\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_weights(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                             uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
 
 template <int R>
 __device__ __forceinline__ void reg_inc() {
@@ -226,6 +257,17 @@ __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// Four fp32 to four e4m3 codes (nearest even, NaN kept).
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tmov.b32 %0, {x, 0};\n\t}"
+      : "=r"(lo)
+      : "f"(a), "f"(b));
+  asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tmov.b32 %0, {x, 0};\n\t}"
+      : "=r"(hi)
+      : "f"(c), "f"(d));
+  return lo | hi << 16;
+}
 __device__ __forceinline__ uint32_t cvt2(uint32_t w) {
   uint32_t r;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
@@ -244,12 +286,83 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// Byte offset of 16-byte chunk c of row r in a [128][D] operand of codes.
+template <int D>
+__device__ __forceinline__ uint32_t code_at(int r, int c) {
+  return (uint32_t)(r * D + ((c ^ (D == 128 ? r & 7 : r >> 1 & 3)) << 4));
+}
+
+// ------------------------------------------------------------------ lookups and key copies
+// Four tiles at a time (lane = tile x 16 keys): page, row in the pool and
+// scales; then, tile by tile, the description and the keys' copies, one box
+// per page.
+template <int D>
+__device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, Smem<D> &sm) {
+  Walk &w = sm.walk[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31, g = lane & 7, heads = p.c.heads;
+  const int box = min(p.c.page, kKeys), per_box = box >> 4;
+  uint32_t tile_no = 0;
+  const uint64_t keep = policy_evict_last();  // other CTAs read the same keys
+  for (; w.valid(); step_on(p, w)) {
+    const int nt = w.needed(p);
+    const int lim = block_limit(p, w.x.q, w.x.block), first = w.x.t0 * kKeys + g * 16, head = w.x.head;
+    const int32_t *table = p.c.table + (size_t)w.x.seq * p.c.max_pages;
+    for (int tb = 0; tb < nt; tb += 4) {
+      const int t = tb + (lane >> 3), pos = first + t * kKeys;
+      int row = -2;
+      float ks = 1.f, lv = 0.f;
+      if (t < nt && pos < lim) {
+        const int page = __ldg(table + (pos >> p.c.page_log2));
+        if ((unsigned)page < (unsigned)p.c.pages) {
+          const int ph = page * heads + head;
+          row = (ph << p.c.page_log2) + (pos & (p.c.page - 1));
+          ks = exp_byte(__ldg(p.c.k_exps + ph));
+          lv = (float)(int)__ldg(p.c.v_exps + ph) - 127.f;
+        } else {
+          row = -1;
+          atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
+        }
+      }
+      const uint32_t bad = __ballot_sync(~0u, row == -1);
+      const uint32_t copies = __ballot_sync(~0u, row >= 0 && g % per_box == 0);
+      for (int u = 0; u < min(4, nt - tb); ++u, ++tile_no) {
+        const int slot = tile_no % kMeta, stage = tile_no % kStagesK;
+        wait(sm, &sm.m_empty[slot], (tile_no / kMeta & 1) ^ 1, p.c.status);
+        TileMeta &meta = sm.meta[slot];
+        if (lane >> 3 == u) {
+          meta.row[g] = row;
+          meta.ks[g] = ks;
+          meta.lv[g] = lv;
+          if (g < 4) {
+            const uint32_t two = bad >> (8 * u + 2 * g);
+            meta.hide[g] = (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
+            meta.nan[g] = 0;
+          }
+        }
+        wait(sm, &sm.k_empty[stage], (tile_no / kStagesK & 1) ^ 1, p.c.status);
+        const uint32_t mine = copies >> (8 * u) & 255u;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.m_full[slot]);
+          mbar_arrive_expect_tx(&sm.k_full[stage], (uint32_t)(__popc(mine) * box * D));
+        }
+        __syncwarp();
+        if (lane >> 3 == u && (mine >> g & 1))
+          tma_load_2d(sm.k[stage] + g * 16 * D, &map, &sm.k_full[stage], 0, row, keep);
+      }
+    }
+  }
+  // the copies must have landed before the CTA leaves
+  for (int i = 1; i <= kStagesK; ++i)
+    if (tile_no >= (uint32_t)i) drain(&sm.k_full[(tile_no - i) % kStagesK], (tile_no - i) / kStagesK & 1);
+  __syncwarp();
+}
+
 // ------------------------------------------------------------------ converters
-// One group of 4 warps converts the keys, another the values; each also loads
-// half of an item's queries.  A warp's load covers whole 128-byte lines; its
-// lanes are laid out so that 8 of them store to 8 different bank groups (4
-// chunks of two rows whose exchanges differ in the lowest bit).
-template <int D, bool VALUES>
+// A warp's load covers whole 128-byte lines; its lanes are laid out so that 8
+// of them store to 8 different bank groups (4 chunks of two rows whose
+// exchanges differ in the lowest bit).
+template <int D>
 __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   constexpr int CH = D / 16;              // 16-byte chunks of a code row
@@ -258,90 +371,102 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
   const int tid = threadIdx.x & (kConverters - 1), lane = tid & 31;
   const int ch = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3;
   const int r0 = D == 128 ? (tid >> 5) * 4 + (lane >> 2 & 3) : (tid >> 5) * 8 + (lane >> 2);
-  const int heads = p.c.heads;
-  const uint8_t *codes = VALUES ? p.c.v : p.c.k;
-  uint64_t *full = VALUES ? sm.v_full : sm.k_full, *empty = VALUES ? sm.v_empty : sm.k_empty;
-  int(*rows)[8] = sm.row[VALUES];
-  constexpr int kBar = kBarConv + VALUES;
   uint32_t tile_no = 0, q_no = 0;
+  uint4 x[STEPS];
+  auto load = [&](uint32_t no, int i) {
+    const int r = i * RPS + r0;
+    const int row = sm.meta[no % kMeta].row[r >> 4];
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(p.c.v + (size_t)(row + (r & 15)) * D + ch * 16));
+  };
   for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p), ncols = w.cols(p);
-    const int lim = block_limit(p, w.x.q, w.x.block), first = w.x.t0 * kKeys + tid * 16, head = w.x.head;
-    const int32_t *table = p.c.table + (size_t)w.x.seq * p.c.max_pages;
-    if (nt == 0) continue;  // softmax reads nothing either
-    // lookups: threads 0 .. 7 hold 16 keys each, pages three tiles ahead, exponents two
-    auto load_page = [&](int t) -> int {
-      const int pos = first + t * kKeys;
-      return tid < 8 && t < nt && pos < lim ? __ldg(table + (pos >> p.c.page_log2)) : -1;
-    };
-    auto row_of = [&](int t, int page) -> int {
-      const int pos = first + t * kKeys;
-      if (tid >= 8 || t >= nt || pos >= lim) return -2;  // nothing there
-      if ((unsigned)page >= (unsigned)p.c.pages) {
-        if (VALUES) atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
-        return -1;
-      }
-      return ((page * heads + head) << p.c.page_log2) + (pos & (p.c.page - 1));
-    };
-    // nothing is computed from a loaded value before it is published, an iteration later
-    uint32_t ke1 = 127, ve1 = 127;
-    auto load_exps = [&](int row) {
-      if (!VALUES || row < 0) return;
-      const int ph = row >> p.c.page_log2;
-      ke1 = __ldg(p.c.k_exps + ph);
-      ve1 = __ldg(p.c.v_exps + ph);
-    };
-    auto publish = [&](uint32_t no, int row) {
-      const int m = no % kMeta;
-      if (tid < 8) {
-        rows[m][tid] = row;
-        if (VALUES) {
-          sm.meta[m].ks[tid] = exp_byte(ke1);
-          sm.meta[m].lv[tid] = (float)(int)ve1 - 127.f;
-          const uint32_t bad = __ballot_sync(0xFFu, row == -1);
-          if (tid < 4) {
-            sm.meta[m].hide[tid] = (bad >> (2 * tid) & 1 ? 0xFFFFu : 0u) | (bad >> (2 * tid + 1) & 1 ? 0xFFFF0000u : 0u);
-            sm.meta[m].nan[tid] = 0;
-          }
-        }
-      }
-    };
-    uint4 x[STEPS];
-    auto load = [&](uint32_t no, int i) {
-      const int r = i * RPS + r0;
-      const int row = rows[no % kMeta][r >> 4];
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)(row + (r & 15)) * D + ch * 16));
-    };
-    int pg2 = load_page(0);
-    int row1 = row_of(0, pg2);
-    load_exps(row1);
-    pg2 = load_page(1);
-    publish(tile_no, row1);
-    row1 = row_of(1, pg2), load_exps(row1), pg2 = load_page(2);
-    named_bar(kBar, kConverters);
+    if (nt == 0) continue;  // nothing is read
+    wait(sm, &sm.m_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) load(tile_no, i);
 
+    // ---- the queries (the previous part's last scores must be done): 8
+    // components per lane, a row's largest magnitude by exchange
+    wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p.c.status);
+    {
+      constexpr int LPR = D / 8, QR = 32 / LPR;  // lanes per row, rows per warp step
+      constexpr int BATCH = 8;
+      const int part = lane % LPR;
+      const int r_first = w.x.q.r0, c_first = w.x.block * kCols, h_first = w.x.head * p.group;
+#pragma unroll 1
+      for (int b = 0; b < 64 / QR; b += BATCH) {
+        if ((tid >> 5) * 64 + b * QR >= ((ncols + 127) & ~127)) break;  // an empty half is not read by the MMAs
+        uint4 u[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int col = (tid >> 5) * 64 + (b + i) * QR + lane / LPR;
+          const int cc = c_first + col;
+          u[i] = make_uint4(0, 0, 0, 0);
+          if (col < ncols)
+            u[i] = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) +
+                                                         (size_t)(r_first + cc / p.group) * p.q_stride +
+                                                         (size_t)(h_first + cc % p.group) * D + part * 8));
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int col = (tid >> 5) * 64 + (b + i) * QR + lane / LPR;
+          const uint32_t ws[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+          float f[8];
+          float amax = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = p.bf16 ? bf16x2_to_float2(ws[j]) : half2_to_float2(ws[j]);
+            f[2 * j] = y.x, f[2 * j + 1] = y.y;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (!(fabsf(f[j]) <= FLT_MAX)) f[j] = NAN;  // infinities too: no softmax of theirs is a number
+            amax = fmaxf(amax, fabsf(f[j]));
+          }
+#pragma unroll
+          for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+          // power of two that brings the largest magnitude to (224, 448]
+          int e = 0;
+          if (amax > 0.f) e = ((__float_as_uint(amax) & 0x7FFFFFu) > 0x600000u ? 7 : 8) - exponent_of(amax);
+          e = max(-110, min(110, e));
+          const float up = pow2i(e);
+          if (part == 0) sm.cs[q_no & 1][col] = p.scale_log2 * pow2i(-e);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] *= up;
+          for (int term = 0; term < (p.bf16 ? 2 : 3); ++term) {
+            uint2 c;
+            c.x = to_e4m3x4(f[0], f[1], f[2], f[3]);
+            c.y = to_e4m3x4(f[4], f[5], f[6], f[7]);
+            *reinterpret_cast<uint2 *>(sm.q[col >> 7][term] + code_at<D>(col & 127, part >> 1) + (part & 1) * 8) = c;
+            const uint32_t back[4] = {cvt2(c.x), cvt2_hi(c.x), cvt2(c.y), cvt2_hi(c.y)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 y = half2_to_float2(back[j]);
+              f[2 * j] -= y.x, f[2 * j + 1] -= y.y;
+            }
+          }
+        }
+      }
+    }
+    fence_async_smem();
+    mbar_arrive(&sm.q_full);
+    ++q_no;
+
     for (int t = 0; t < nt; ++t, ++tile_no) {
-      const int stage = tile_no % kStagesKV;
-      const uint32_t round = tile_no / kStagesKV;
-      if (t + 1 < nt) publish(tile_no + 1, row1);
-      row1 = row_of(t + 2, pg2), load_exps(row1), pg2 = load_page(t + 3);
-      named_bar(kBar, kConverters);
-      wait(sm, &empty[stage], (round & 1) ^ 1, p.c.status);
-      uint8_t *dst = VALUES ? sm.v[stage] : sm.k[stage];
+      const int stage = tile_no % kStagesV;
+      if (t + 1 < nt) wait(sm, &sm.m_full[(tile_no + 1) % kMeta], (tile_no + 1) / kMeta & 1, p.c.status);
+      wait(sm, &sm.v_empty[stage], (tile_no / kStagesV & 1) ^ 1, p.c.status);
+      uint8_t *dst = sm.v[stage];
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
         const int r = i * RPS + r0;
         uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        if (VALUES) {
-          const uint32_t odd = nan_bytes(ws[0]) | nan_bytes(ws[1]) | nan_bytes(ws[2]) | nan_bytes(ws[3]);
-          if (odd) {  // taken out here; the scores of the columns that see the key become NaN
-            atomicOr(&sm.meta[tile_no % kMeta].nan[r >> 5], 1u << (r & 31));
+        const uint32_t odd = nan_bytes(ws[0]) | nan_bytes(ws[1]) | nan_bytes(ws[2]) | nan_bytes(ws[3]);
+        if (odd) {  // taken out here; the scores of the columns that see the key become NaN
+          atomicOr(&sm.meta[tile_no % kMeta].nan[r >> 5], 1u << (r & 31));
 #pragma unroll
-            for (int b = 0; b < 4; ++b) ws[b] &= ~((nan_bytes(ws[b]) >> 7) * 255u);
-          }
+          for (int b = 0; b < 4; ++b) ws[b] &= ~((nan_bytes(ws[b]) >> 7) * 255u);
         }
         *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * ch)) =
             make_uint4(cvt2(ws[0]), cvt2_hi(ws[0]), cvt2(ws[1]), cvt2_hi(ws[1]));
@@ -350,85 +475,37 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
         if (t + 1 < nt) load(tile_no + 1, i);  // on its way while the rest is converted
       }
       fence_async_smem();
-      mbar_arrive(&full[stage]);
-      if (t == 0) {
-        // ---- this group's 128 query rows (the previous part's last scores must be
-        // done): 8 components per lane, a row's largest magnitude by exchange
-        wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p.c.status);
-        constexpr int LPR = D / 8, QR = 32 / LPR;  // lanes per row, rows per warp step
-        const int part = lane % LPR;
-#pragma unroll 1
-        for (int b = 0; b < 32 / QR; b += 8) {
-          uint4 u[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = (tid >> 5) * 32 + (b + i) * QR + lane / LPR, col = VALUES * 128 + r;
-            const int cc = w.x.block * kCols + col;
-            u[i] = make_uint4(0, 0, 0, 0);
-            if (col < ncols)
-              u[i] = __ldg(reinterpret_cast<const uint4 *>(
-                  reinterpret_cast<const uint16_t *>(p.q) + (size_t)(w.x.q.r0 + cc / p.group) * p.q_stride +
-                  (size_t)(w.x.head * p.group + cc % p.group) * D + part * 8));
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = (tid >> 5) * 32 + (b + i) * QR + lane / LPR;
-            const uint32_t ws[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-            float2 f[4];
-            float amax = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              f[j] = p.bf16 ? bf16x2_to_float2(ws[j]) : half2_to_float2(ws[j]);
-              amax = fmaxf(amax, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
-            }
-#pragma unroll
-            for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-            int e = 0;
-            if (amax > 0.f && amax <= FLT_MAX) e = 10 - exponent_of(amax);
-            e = max(-100, min(100, e));
-            const float up = pow2i(e);
-            if (part == 0) sm.cs[q_no & 1][VALUES * 128 + r] = p.scale_log2 * pow2i(-e);
-            uint32_t h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = float2_to_half2(f[j].x * up, f[j].y * up);
-            *reinterpret_cast<uint4 *>(sm.q[VALUES] + chunk_at(r, part)) = make_uint4(h[0], h[1], h[2], h[3]);
-          }
-        }
-        fence_async_smem();
-        mbar_arrive(&sm.q_full);
-      }
+      mbar_arrive(&sm.v_full[stage]);
     }
-    ++q_no;
   }
 }
 
 // ------------------------------------------------------------------ MMA issue
+// The warp waits together, one elected lane issues, and the others wait for it
+// before the next barrier: lanes that poll hold up the one that issues.
 template <int D>
 __device__ void mma_role(const AttnParams &p, Smem<D> &sm) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   const uint32_t tmem = sm.tmem;
-  const bool lead = (threadIdx.x & 31) == 0;
-  constexpr uint32_t kQk = idesc_f16(128, kKeys, false), kPv = idesc_f16(128, D, true);
+  constexpr uint32_t kQk = idesc_f8_e4m3_f32(128, kKeys), kPv = idesc_f16(128, D, true);
+  const int terms = p.bf16 ? 2 : 3;
   uint32_t tile_no = 0, q_no = 0, p_no = 0;
-  auto qk = [&](int x, int stage, bool on) {
-    if (!lead) return;
-    const uint32_t a = smem_u32(sm.q[x]), b = smem_u32(sm.k[stage]);
-    if (on) {
+  const uint32_t q0 = Desc<D>::codes_lo(sm.q[0][0]), k0 = Desc<D>::codes_lo(sm.k[0]),
+                 v0 = Desc<D>::values_lo(sm.v[0]);
+  auto qk = [&](int x, int stage) {
+    uint32_t a = q0 + x * (kTerms * 128 * D / 16);
+    const uint32_t b = k0 + stage * (kKeys * D / 16), d = tmem + 256 + x * 128;
+#pragma unroll 1
+    for (int term = 0; term < terms; ++term, a += 128 * D / 16) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-        umma_ss(tmem + 256 + x * 128, sw128_kmajor_desc(a + off), sw128_kmajor_desc(b + off), kQk, kk > 0);
-      }
+      for (int kk = 0; kk < D / 32; ++kk) umma_codes(d, a + kk * 2, b + kk * 2, Desc<D>::codes_hi, kQk, term | kk);
     }
-    umma_commit(&sm.s_full[x]);
   };
   auto pv = [&](int x, int stage, bool first) {
-    if (!lead) return;
-    const uint32_t b = smem_u32(sm.v[stage]);
+    const uint32_t b = v0 + stage * (kKeys * D * 2 / 16), d = tmem + x * 128, a = tmem + 256 + x * 128;
 #pragma unroll
     for (int kk = 0; kk < kKeys / 16; ++kk)
-      umma_ts(tmem + x * 128, tmem + 256 + x * 128 + kk * 8, desc_mn(b + kk * 2048, 128 * 128), kPv,
-              !first || kk > 0);
+      umma_weights(d, a + kk * 8, b + kk * (2048 / 16), Desc<D>::values_hi, kPv, kk ? 1u : !first);
   };
   for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p);
@@ -437,62 +514,46 @@ __device__ void mma_role(const AttnParams &p, Smem<D> &sm) {
     for (int t = -1; t < nt; ++t) {
       // scores of tile t + 1, weights times values of tile t
       const uint32_t kn = tile_no + t + 1, vn = tile_no + t;
-      const int ks = kn % kStagesKV, vs = vn % kStagesKV;
+      const int ks = kn % kStagesK, vs = vn % kStagesV;
       const bool more = t + 1 < nt;
-      if (more) wait(sm, &sm.k_full[ks], kn / kStagesKV & 1, p.c.status);
+      if (more) wait(sm, &sm.k_full[ks], kn / kStagesK & 1, p.c.status);
       if (t < 0) wait(sm, &sm.q_full, q_no & 1, p.c.status);
-      else wait(sm, &sm.v_full[vs], vn / kStagesKV & 1, p.c.status);
+      else wait(sm, &sm.v_full[vs], vn / kStagesV & 1, p.c.status);
+#pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         const bool on = x == 0 || two;
-        if (t >= 0) {
-          wait(sm, &sm.p_full[x], p_no++ >> 1 & 1, p.c.status);
-          __syncwarp();
-          tc_fence_after();
-          if (on) pv(x, vs, t == 0);
-          if (on && !more && lead) umma_commit(&sm.o_full[x]);
-        }
+        if (t >= 0) wait(sm, &sm.p_full[x], p_no++ >> 1 & 1, p.c.status);
+        __syncwarp();
         tc_fence_after();
-        if (more) qk(x, ks, on);
+        if (elect_one()) {
+          if (t >= 0 && on) {
+            pv(x, vs, t == 0);
+            if (!more) umma_commit(&sm.o_full[x]);
+          }
+          if (more && on) qk(x, ks);
+          if (more) umma_commit(&sm.s_full[x]);
+          if (x == 1) {
+            if (t >= 0) {
+              umma_commit(&sm.v_empty[vs]);
+              umma_commit(&sm.m_empty[vn % kMeta]);
+            }
+            if (more) umma_commit(&sm.k_empty[ks]);
+            if (t + 2 == nt) umma_commit(&sm.q_empty);  // the last scores are under way
+          }
+        }
+        __syncwarp();
       }
-      if (lead) {
-        if (t >= 0) umma_commit(&sm.v_empty[vs]);
-        if (more) umma_commit(&sm.k_empty[ks]);
-        if (t + 2 == nt) umma_commit(&sm.q_empty);  // the last scores are under way
-      }
-      __syncwarp();
     }
     tile_no += nt;
     ++q_no;
   }
-  if (lead) {
-    umma_commit(&sm.done);
-    wait(sm, &sm.done, 0, p.c.status);
-  }
+  if (elect_one()) umma_commit(&sm.done);
+  __syncwarp();
+  wait(sm, &sm.done, 0, p.c.status);
   __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax
-// How a tile's scores are read: as they are; cut at the keys the column sees;
-// or with every rare case (pages outside the pool, NaN values, scales far apart).
-enum Mode { kPlain, kCut, kRare };
-
-template <int MODE>
-__device__ __forceinline__ void hide_keys(uint32_t (&s)[32], const TileMeta &meta, int j, int room) {
-  if (MODE == kPlain) return;
-  if (MODE == kRare) {
-    const uint32_t hide = meta.hide[j], nan = meta.nan[j];
-#pragma unroll
-    for (int b = 0; b < 32; ++b) {
-      if (nan >> b & 1) s[b] = 0x7FC00000u;
-      if (hide >> b & 1) s[b] = 0xFF800000u;  // -inf
-    }
-  }
-  const int n = room - 32 * j;
-#pragma unroll
-  for (int b = 0; b < 32; ++b)
-    if (b >= n) s[b] = 0xFF800000u;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -502,37 +563,6 @@ __device__ __forceinline__ float max3(float a, float b, uint32_t c) { return max
 __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
   return max3(__uint_as_float(a), __uint_as_float(b), c);
 }
-
-// A column's largest score of the tile, and largest score plus value exponent.
-// The next 32 columns are on their way from TMEM while 32 are looked at.
-template <int MODE>
-__device__ __forceinline__ void scan_scores(uint32_t ts, const TileMeta &meta, int room, float cs, float &top,
-                                            float &topw) {
-  auto look = [&](uint32_t(&s)[32], int j) {
-    hide_keys<MODE>(s, meta, j, room);
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const uint32_t *v = s + 16 * g;
-      const float a = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), v[6]);
-      const float b = max3(max3(v[7], v[8], v[9]), max3(v[10], v[11], v[12]), v[13]);
-      const float x = max3(fmaxf(a, __uint_as_float(v[14])), b, v[15]) * (cs * meta.ks[2 * j + g]);
-      top = fmaxf(top, x);
-      topw = fmaxf(topw, x + meta.lv[2 * j + g]);
-    }
-  };
-  uint32_t s0[32], s1[32];
-  tmem_ld_32x32b_x32(ts, s0);
-#pragma unroll 1
-  for (int j = 0; j < 4; j += 2) {
-    tmem_ld_wait();
-    tmem_ld_32x32b_x32(ts + 32 * j + 32, s1);
-    look(s0, j);
-    tmem_ld_wait();
-    if (j == 0) tmem_ld_32x32b_x32(ts + 64, s0);
-    look(s1, j + 1);
-  }
-}
-
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -552,53 +582,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Scores to weights, in place (fp16 over the first half of the fp32 columns);
-// returns the column's sum with this tile's.  A weight in the sum is 2^back of
-// the one that enters the product.
-template <int MODE>
-__device__ __forceinline__ float weigh(uint32_t ts, const TileMeta &meta, int room, float cs, float mr, float ww,
-                                       float l) {
-  auto turn = [&](uint32_t(&s)[32], int j) {
-    hide_keys<MODE>(s, meta, j, room);
-    uint32_t h[16];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const float f = cs * meta.ks[2 * j + g], lv = meta.lv[2 * j + g];
-      const float b = lv - ww, back = ww - lv - mr;
-      const uint64_t f2 = pack2(f, f), b2 = pack2(b, b);
-      if (MODE == kRare && back > 64.f) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) l += ex2(__uint_as_float(s[16 * g + k]) * f - mr);
-      }
-      uint64_t sum[2] = {0, 0};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float y, z;
-        unpack2(fma2(pack2(__uint_as_float(s[16 * g + 2 * k]), __uint_as_float(s[16 * g + 2 * k + 1])), f2, b2), y, z);
-        y = ex2(y), z = ex2(z);
-        sum[k & 1] = add2(sum[k & 1], pack2(y, z));
-        h[8 * g + k] = float2_to_half2(y, z);
-      }
-      float y, z;
-      unpack2(add2(sum[0], sum[1]), y, z);
-      if (MODE != kRare || !(back > 64.f)) l = fmaf(y + z, ex2(back), l);
-    }
-    tmem_st16(ts + 16 * j, h);
-  };
-  uint32_t s0[32], s1[32];
-  tmem_ld_32x32b_x32(ts, s0);
-#pragma unroll 1
-  for (int j = 0; j < 4; j += 2) {
-    tmem_ld_wait();
-    tmem_ld_32x32b_x32(ts + 32 * j + 32, s1);
-    turn(s0, j);
-    tmem_ld_wait();
-    if (j == 0) tmem_ld_32x32b_x32(ts + 64, s0);
-    turn(s1, j + 1);
-  }
-  return l;
-}
-
 template <int D>
 __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
   Walk &w = sm.walk[threadIdx.x >> 5];
@@ -613,7 +596,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
     if (ncols <= x * 128) {  // this half is empty: it keeps step, so that it meets every phase of the barriers
       if (nt) wait(sm, &sm.q_full, q_no++ & 1, p.c.status);
       for (int t = 0; t < nt; ++t, ++tile_no) {
-        wait(sm, &sm.v_full[tile_no % kStagesKV], tile_no / kStagesKV & 1, p.c.status);
+        wait(sm, &sm.v_full[tile_no % kStagesV], tile_no / kStagesV & 1, p.c.status);
         wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);  // without it this half could run ahead of the issuing warp
         mbar_arrive(&sm.p_full[x]);
       }
@@ -631,8 +614,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
       ++q_no;
     }
     for (int t = 0; t < nt; ++t, ++tile_no) {
-      const int stage = tile_no % kStagesKV;
-      wait(sm, &sm.v_full[stage], tile_no / kStagesKV & 1, p.c.status);
+      const int stage = tile_no % kStagesV;
+      wait(sm, &sm.v_full[stage], tile_no / kStagesV & 1, p.c.status);
       wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);
       __syncwarp();
       tc_fence_after();
@@ -641,12 +624,37 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
       uint32_t odd = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) odd |= meta.hide[j] | meta.nan[j];
-      const bool cut = __any_sync(~0u, room < kKeys);
-      // largest score, and largest score with the value scale
+      uint32_t s[128];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(ts + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
+      tmem_ld_wait();
+      if (odd) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t hide = meta.hide[j], nan = meta.nan[j];
+#pragma unroll
+          for (int b = 0; b < 32; ++b) {
+            if (nan >> b & 1) s[32 * j + b] = 0x7FC00000u;
+            if (hide >> b & 1) s[32 * j + b] = 0xFF800000u;  // -inf
+          }
+        }
+      }
+      if (__any_sync(~0u, room < kKeys)) {
+#pragma unroll
+        for (int b = 0; b < kKeys; ++b)
+          if (b >= room) s[b] = 0xFF800000u;
+      }
+      // largest score, and largest score plus value exponent
       float top = -INFINITY, topw = -INFINITY;
-      if (odd) scan_scores<kRare>(ts, meta, room, cs, top, topw);
-      else if (cut) scan_scores<kCut>(ts, meta, room, cs, top, topw);
-      else scan_scores<kPlain>(ts, meta, room, cs, top, topw);
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const uint32_t *v = s + 16 * g;
+        const float a = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), v[6]);
+        const float b = max3(max3(v[7], v[8], v[9]), max3(v[10], v[11], v[12]), v[13]);
+        const float y = max3(fmaxf(a, __uint_as_float(v[14])), b, v[15]) * (cs * meta.ks[g]);
+        top = fmaxf(top, y);
+        topw = fmaxf(topw, y + meta.lv[g]);
+      }
       const bool move = top > m + kSlack || topw > wr + kSlack;
       if (__any_sync(~0u, move)) {
         const float mn = fmaxf(m, top), wn = fmaxf(wr, topw);
@@ -666,14 +674,42 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
         }
       }
       const float mr = m == -INFINITY ? 0.f : m, ww = wr == -INFINITY ? 0.f : wr;
-      // values so small that their weights would leave fp32's range before they
-      // are scaled back: the sum takes a power of two of its own
+      // A weight in the sum is 2^back of the one that enters the product.  Where
+      // the values are so small that the latter would leave fp32's range, the sum
+      // takes powers of two of its own.
       bool far = false;
 #pragma unroll
       for (int g = 0; g < 8; ++g) far |= ww - meta.lv[g] - mr > 64.f;
-      if (odd || __any_sync(~0u, far)) l = weigh<kRare>(ts, meta, room, cs, mr, ww, l);
-      else if (cut) l = weigh<kCut>(ts, meta, room, cs, mr, ww, l);
-      else l = weigh<kPlain>(ts, meta, room, cs, mr, ww, l);
+      if (__any_sync(~0u, far)) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+          if (ww - meta.lv[g] - mr > 64.f) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) l += ex2(__uint_as_float(s[16 * g + k]) * (cs * meta.ks[g]) - mr);
+          }
+      }
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float f = cs * meta.ks[g], lv = meta.lv[g];
+        const float b = lv - ww;
+        float back = ww - lv - mr;
+        back = back > 64.f ? -INFINITY : back;
+        const uint64_t f2 = pack2(f, f), b2 = pack2(b, b);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float y, z;
+          unpack2(fma2(pack2(__uint_as_float(s[16 * g + 2 * k]), __uint_as_float(s[16 * g + 2 * k + 1])), f2, b2), y,
+                  z);
+          y = ex2(y), z = ex2(z);
+          sum[k & 1] = add2(sum[k & 1], pack2(y, z));
+          s[8 * g + k] = float2_to_half2(y, z);
+        }
+        float y, z;
+        unpack2(add2(sum[0], sum[1]), y, z);
+        l = fmaf(y + z, ex2(back), l);
+        if (g & 1) tmem_st16(ts + 8 * (g - 1), *reinterpret_cast<const uint32_t(*)[16]>(s + 8 * (g - 1)));
+      }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&sm.p_full[x]);
@@ -737,7 +773,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_prefill_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
   extern __shared__ uint8_t raw[];
   Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -786,13 +823,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const AttnParam
   }
   if (tid == 0) {
     sm.dead = 0;
-    mbar_init(&sm.q_full, 2 * kConverters);
+    mbar_init(&sm.q_full, kConverters);
     mbar_init(&sm.q_empty, 1);
-    for (int i = 0; i < kStagesKV; ++i) {
-      mbar_init(&sm.k_full[i], kConverters);
+    for (int i = 0; i < kStagesK; ++i) {
+      mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < kStagesV; ++i) {
       mbar_init(&sm.v_full[i], kConverters);
       mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < kMeta; ++i) {
+      mbar_init(&sm.m_full[i], 1);
+      mbar_init(&sm.m_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
@@ -802,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const AttnParam
     mbar_init(&sm.done, 1);
     fence_mbar_init();
   }
-  if (warp == 16) {
+  if (warp == 12) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
@@ -827,23 +870,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const AttnParam
   }
   if (lane == 0) sm.walk[warp] = w;
   __syncwarp();
-  // registers: 256 x 128 + 256 x 88 + 128 x 48 = 640 x 96, what the block was launched with
+  // registers: 256 x 176 + 128 x 104 + 128 x 56 = 512 x 128, what the block was launched with
   if (warp < 8) {
-    reg_inc<128>();
+    reg_inc<176>();
     softmax_role<D>(p, sm, per);
   } else if (warp < 12) {
-    reg_dec<88>();
-    convert_role<D, false>(p, sm);
-  } else if (warp < 16) {
-    reg_dec<88>();
-    convert_role<D, true>(p, sm);
+    reg_dec<104>();
+    convert_role<D>(p, sm);
   } else {
-    reg_dec<48>();
-    if (warp == 16) mma_role<D>(p, sm);
+    reg_dec<56>();
+    if (warp == 12) mma_role<D>(p, sm);
+    if (warp == 13) lookup_role<D>(p, map, sm);
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) tmem_dealloc(sm.tmem, 512);
+  if (warp == 12) tmem_dealloc(sm.tmem, 512);
 }
 
 // Join split items: block (c, y) adds the parts of 32 columns of the item that
@@ -890,12 +932,12 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const AttnParams p
 }
 
 template <int D>
-cudaError_t launch(const AttnParams &p, int ctas, cudaStream_t stream) {
+cudaError_t launch(const AttnParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream) {
   constexpr int bytes = (int)sizeof(Smem<D>) + 1024;
   auto *k = kv_prefill_kernel<D>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  k<<<ctas, kThreads, bytes, stream>>>(p);
+  k<<<ctas, kThreads, bytes, stream>>>(p, map);
   const cudaError_t le = cudaGetLastError();
   if (le != cudaSuccess) return le;
   kv_prefill_join_kernel<D><<<dim3(ctas, kCols / 32), 256, 0, stream>>>(p);
@@ -904,8 +946,8 @@ cudaError_t launch(const AttnParams &p, int ctas, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_kv_prefill(const AttnParams &p, int ctas, cudaStream_t stream) {
-  return p.c.dim == 64 ? launch<64>(p, ctas, stream) : launch<128>(p, ctas, stream);
+cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream) {
+  return p.c.dim == 64 ? launch<64>(p, map, ctas, stream) : launch<128>(p, map, ctas, stream);
 }
 
 }  // namespace mqa

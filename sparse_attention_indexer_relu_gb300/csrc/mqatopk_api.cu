@@ -172,6 +172,20 @@ int mqa::device_sms(int device, int *sms) {
   return rc;
 }
 
+int mqa::encode_code_rows(CUtensorMap *map, const void *base, uint64_t rows, int dim, uint32_t box_rows) {
+  const int rc = get_encoder();
+  if (rc != MQA_OK) return rc;
+  const cuuint64_t dims[2] = {(cuuint64_t)dim, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)dim};
+  const cuuint32_t box[2] = {(cuuint32_t)dim, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MQA_OK : MQA_ERR_CUDA;
+}
+
 FusedLayout mqa::fused_layout(int ctas, int cap, int split_max, int brows, int fold_rows) {
   FusedLayout L;
   L.done_off = kWsHeaderBytes;

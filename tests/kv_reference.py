@@ -103,6 +103,8 @@ class Cache:
                         # may lose 2^-22 of the magnitudes in it), then a product and a difference
                         mag = scale * (np.abs(kt) @ np.abs(q[r, x]))
                         ds = ((d / 16 + 2) * 2.0 ** -22 * mag + 2.0 ** -22 * (np.abs(sc) + abs(top))).max() + 2.0 ** -21
+                        # query values as sums of e4m3 terms: 2^-10 of a largest value of 224 or more is lost
+                        ds += (scale * np.abs(q[r, x]).max() * 2.0 ** -10 / 224 * np.abs(kt).sum(1)).max()
                         sums = (len(t) / 16 + 64) * 2.0 ** -22
                         mean = p @ np.abs(vt) / total
                         # a weight is rounded to fp16: 2^-11 of it, or 2^-25 of the largest weight times scale
