@@ -144,7 +144,9 @@ struct Walk {
 };
 
 struct TileMeta {
-  float ks[8], lv[8];    // per 16 keys: key scale, log2 of the value scale
+  float4 ks[2], lv[2];   // per 16 keys: key scale, log2 of the value scale
+  float lv_min;
+  uint32_t odd;          // nonzero where hide or nan is
   uint32_t hide[4];      // keys that no column sees (a page outside the pool)
   uint32_t nan[4];       // keys whose values hold a NaN code
   int row[8];            // first row of each 16 keys in the pool; -1: page outside the pool, -2: no key needed
@@ -323,6 +325,10 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, Smem<D>
           atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
         }
       }
+      float lv_min = lv;  // of the tile; groups that hold no key do not count
+      if (row < 0) lv_min = 128.f;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) lv_min = fminf(lv_min, __shfl_xor_sync(~0u, lv_min, o));
       const uint32_t bad = __ballot_sync(~0u, row == -1);
       const uint32_t copies = __ballot_sync(~0u, row >= 0 && g % per_box == 0);
       for (int u = 0; u < min(4, nt - tb); ++u, ++tile_no) {
@@ -331,12 +337,16 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, Smem<D>
         TileMeta &meta = sm.meta[slot];
         if (lane >> 3 == u) {
           meta.row[g] = row;
-          meta.ks[g] = ks;
-          meta.lv[g] = lv;
+          reinterpret_cast<float *>(meta.ks)[g] = ks;
+          reinterpret_cast<float *>(meta.lv)[g] = lv;
           if (g < 4) {
             const uint32_t two = bad >> (8 * u + 2 * g);
             meta.hide[g] = (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
             meta.nan[g] = 0;
+          }
+          if (g == 0) {
+            meta.lv_min = lv_min;
+            meta.odd = (bad >> (8 * u) & 255u) != 0;
           }
         }
         wait(sm, &sm.k_empty[stage], (tile_no / kStagesK & 1) ^ 1, p.c.status);
@@ -465,6 +475,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
         const uint32_t odd = nan_bytes(ws[0]) | nan_bytes(ws[1]) | nan_bytes(ws[2]) | nan_bytes(ws[3]);
         if (odd) {  // taken out here; the scores of the columns that see the key become NaN
           atomicOr(&sm.meta[tile_no % kMeta].nan[r >> 5], 1u << (r & 31));
+          sm.meta[tile_no % kMeta].odd = 1;
 #pragma unroll
           for (int b = 0; b < 4; ++b) ws[b] &= ~((nan_bytes(ws[b]) >> 7) * 255u);
         }
@@ -608,6 +619,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
     float m = -INFINITY, wr = -INFINITY, l = 0.f;
     float cs = 0.f;
     const int room0 = lim - w.x.t0 * kKeys;
+    const int whole_tiles = __reduce_min_sync(~0u, room0) / kKeys;  // tiles every column of the warp sees whole
     if (nt) {
       wait(sm, &sm.q_full, q_no & 1, p.c.status);
       cs = sm.cs[q_no & 1][col];
@@ -619,14 +631,19 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
       wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);
       __syncwarp();
       tc_fence_after();
-      const TileMeta &meta = sm.meta[tile_no % kMeta];
-      const int room = room0 - t * kKeys;  // keys of the tile that the column sees
-      uint32_t odd = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) odd |= meta.hide[j] | meta.nan[j];
       uint32_t s[128];
 #pragma unroll
       for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(ts + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
+      const TileMeta &meta = sm.meta[tile_no % kMeta];
+      const uint32_t odd = meta.odd;
+      const float lv_min = meta.lv_min;
+      float f[8], lv[8];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float4 a = meta.ks[g], b = meta.lv[g];
+        f[4 * g] = cs * a.x, f[4 * g + 1] = cs * a.y, f[4 * g + 2] = cs * a.z, f[4 * g + 3] = cs * a.w;
+        lv[4 * g] = b.x, lv[4 * g + 1] = b.y, lv[4 * g + 2] = b.z, lv[4 * g + 3] = b.w;
+      }
       tmem_ld_wait();
       if (odd) {
 #pragma unroll
@@ -639,7 +656,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
           }
         }
       }
-      if (__any_sync(~0u, room < kKeys)) {
+      if (t >= whole_tiles) {
+        const int room = room0 - t * kKeys;  // keys of the tile that the column sees
 #pragma unroll
         for (int b = 0; b < kKeys; ++b)
           if (b >= room) s[b] = 0xFF800000u;
@@ -651,12 +669,15 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
         const uint32_t *v = s + 16 * g;
         const float a = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), v[6]);
         const float b = max3(max3(v[7], v[8], v[9]), max3(v[10], v[11], v[12]), v[13]);
-        const float y = max3(fmaxf(a, __uint_as_float(v[14])), b, v[15]) * (cs * meta.ks[g]);
+        const float y = max3(fmaxf(a, __uint_as_float(v[14])), b, v[15]) * f[g];
         top = fmaxf(top, y);
-        topw = fmaxf(topw, y + meta.lv[g]);
+        topw = fmaxf(topw, y + lv[g]);
       }
-      const bool move = top > m + kSlack || topw > wr + kSlack;
-      if (__any_sync(~0u, move)) {
+      // A weight in the sum is 2^(wr - lv - m) of the one that enters the product.
+      // Where that is large, the values are so small that the latter may leave
+      // fp32's range: the sum then takes powers of two of its own.
+      auto far = [&] { return wr - lv_min - m > 64.f; };
+      if (__any_sync(~0u, top > m + kSlack || topw > wr + kSlack || far())) {
         const float mn = fmaxf(m, top), wn = fmaxf(wr, topw);
         const float fl = mn == m ? 1.f : ex2(m - mn), fo = wn == wr ? 1.f : ex2(wr - wn);
         m = mn, wr = wn;
@@ -672,29 +693,22 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
             tmem_st16(to + j, o);
           }
         }
+        if (far()) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            if (wr - lv[g] - m > 64.f) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) l += ex2(__uint_as_float(s[16 * g + k]) * f[g] - m);
+            }
+        }
       }
       const float mr = m == -INFINITY ? 0.f : m, ww = wr == -INFINITY ? 0.f : wr;
-      // A weight in the sum is 2^back of the one that enters the product.  Where
-      // the values are so small that the latter would leave fp32's range, the sum
-      // takes powers of two of its own.
-      bool far = false;
-#pragma unroll
-      for (int g = 0; g < 8; ++g) far |= ww - meta.lv[g] - mr > 64.f;
-      if (__any_sync(~0u, far)) {
-#pragma unroll
-        for (int g = 0; g < 8; ++g)
-          if (ww - meta.lv[g] - mr > 64.f) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) l += ex2(__uint_as_float(s[16 * g + k]) * (cs * meta.ks[g]) - mr);
-          }
-      }
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
-        const float f = cs * meta.ks[g], lv = meta.lv[g];
-        const float b = lv - ww;
-        float back = ww - lv - mr;
+        const float b = lv[g] - ww;
+        float back = -b - mr;
         back = back > 64.f ? -INFINITY : back;
-        const uint64_t f2 = pack2(f, f), b2 = pack2(b, b);
+        const uint64_t f2 = pack2(f[g], f[g]), b2 = pack2(b, b);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -702,7 +716,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
           unpack2(fma2(pack2(__uint_as_float(s[16 * g + 2 * k]), __uint_as_float(s[16 * g + 2 * k + 1])), f2, b2), y,
                   z);
           y = ex2(y), z = ex2(z);
-          sum[k & 1] = add2(sum[k & 1], pack2(y, z));
+          sum[k & 1] = k < 2 ? pack2(y, z) : add2(sum[k & 1], pack2(y, z));
           s[8 * g + k] = float2_to_half2(y, z);
         }
         float y, z;
@@ -870,15 +884,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (lane == 0) sm.walk[warp] = w;
   __syncwarp();
-  // registers: 256 x 176 + 128 x 104 + 128 x 56 = 512 x 128, what the block was launched with
+  // registers: 256 x 184 + 128 x 96 + 128 x 48 = 512 x 128, what the block was launched with
   if (warp < 8) {
-    reg_inc<176>();
+    reg_inc<184>();
     softmax_role<D>(p, sm, per);
   } else if (warp < 12) {
-    reg_dec<104>();
+    reg_dec<96>();
     convert_role<D>(p, sm);
   } else {
-    reg_dec<56>();
+    reg_dec<48>();
     if (warp == 12) mma_role<D>(p, sm);
     if (warp == 13) lookup_role<D>(p, map, sm);
   }
