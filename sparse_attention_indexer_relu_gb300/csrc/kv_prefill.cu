@@ -18,7 +18,7 @@
 // product would, and no key has to be converted or stored twice.
 // While one half's scores are turned into weights the tensor cores work on the
 // other half.  Roles: 2 x 4 softmax warps (a thread per column; it also moves
-// its references and rescales its row of O when a score passes them by 2^8),
+// its references and rescales its row of O when a score passes them too far),
 // 4 converter warps (values to fp16, which the MMA reads transposed, and the
 // query terms), one warp that looks pages up and issues the keys' copies, one
 // that issues the MMAs.
@@ -43,7 +43,6 @@ constexpr int kCols = kTiledCols;         // columns per item
 constexpr int kStagesK = 3, kStagesV = 2;
 constexpr int kMeta = 8;                  // tile descriptions in flight
 constexpr int kTerms = 3;                 // e4m3 terms of a query value (bf16: 2)
-constexpr float kSlack = 8.0f;
 constexpr long long kWaitNs = 2000000000LL;
 constexpr int kConverters = 128;
 
@@ -144,8 +143,9 @@ struct Walk {
 };
 
 struct TileMeta {
-  float4 ks[2], lv[2];   // per 16 keys: key scale, log2 of the value scale
-  float lv_min;
+  float2 kv[8];          // per 16 keys: key scale, log2 of the value scale
+  float lv_min;          // least of the latter,
+  float spread;          // and how far it lies below the largest of the part so far
   uint32_t odd;          // nonzero where hide or nan is
   uint32_t hide[4];      // keys that no column sees (a page outside the pool)
   uint32_t nan[4];       // keys whose values hold a NaN code
@@ -161,7 +161,7 @@ struct Smem {
   float cs[2][kCols];
   TileMeta meta[kMeta];
   uint64_t q_full, q_empty, k_full[kStagesK], k_empty[kStagesK], v_full[kStagesV], v_empty[kStagesV];
-  uint64_t m_full[kMeta], m_empty[kMeta], s_full[2], p_full[2], o_full[2], done;
+  uint64_t m_full[kMeta], m_empty[kMeta], n_full[kMeta], s_full[2], p_full[2], o_full[2], done;
   Walk walk[kThreads / 32];
   uint32_t tmem;
   int dead;
@@ -241,6 +241,17 @@ __device__ __forceinline__ void umma_weights(uint32_t d, uint32_t a, uint32_t b,
       "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -309,6 +320,7 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, Smem<D>
     const int nt = w.needed(p);
     const int lim = block_limit(p, w.x.q, w.x.block), first = w.x.t0 * kKeys + g * 16, head = w.x.head;
     const int32_t *table = p.c.table + (size_t)w.x.seq * p.c.max_pages;
+    float lv_max = -128.f;
     for (int tb = 0; tb < nt; tb += 4) {
       const int t = tb + (lane >> 3), pos = first + t * kKeys;
       int row = -2;
@@ -329,6 +341,9 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, Smem<D>
       if (row < 0) lv_min = 128.f;
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) lv_min = fminf(lv_min, __shfl_xor_sync(~0u, lv_min, o));
+      lv_max = fmaxf(lv_max, row < 0 ? -128.f : lv);  // over four tiles at once: never less than it must be
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) lv_max = fmaxf(lv_max, __shfl_xor_sync(~0u, lv_max, o));
       const uint32_t bad = __ballot_sync(~0u, row == -1);
       const uint32_t copies = __ballot_sync(~0u, row >= 0 && g % per_box == 0);
       for (int u = 0; u < min(4, nt - tb); ++u, ++tile_no) {
@@ -337,8 +352,7 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, Smem<D>
         TileMeta &meta = sm.meta[slot];
         if (lane >> 3 == u) {
           meta.row[g] = row;
-          reinterpret_cast<float *>(meta.ks)[g] = ks;
-          reinterpret_cast<float *>(meta.lv)[g] = lv;
+          meta.kv[g] = make_float2(ks, lv);
           if (g < 4) {
             const uint32_t two = bad >> (8 * u + 2 * g);
             meta.hide[g] = (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
@@ -346,6 +360,7 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, Smem<D>
           }
           if (g == 0) {
             meta.lv_min = lv_min;
+            meta.spread = lv_max - lv_min;
             meta.odd = (bad >> (8 * u) & 255u) != 0;
           }
         }
@@ -369,6 +384,25 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, Smem<D>
 }
 
 // ------------------------------------------------------------------ converters
+template <int STEPS, int RPS>
+__device__ void take_nan_out(uint4 (&x)[STEPS], TileMeta &meta, int r0) {
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    uint32_t *w = &x[i].x;
+    uint32_t odd = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint32_t n = nan_bytes(w[b]);
+      odd |= n;
+      w[b] &= ~((n >> 7) * 255u);
+    }
+    if (odd) {
+      const int r = i * RPS + r0;
+      atomicOr(&meta.nan[r >> 5], 1u << (r & 31));
+      meta.odd = 1;
+    }
+  }
+}
 // A warp's load covers whole 128-byte lines; its lanes are laid out so that 8
 // of them store to 8 different bank groups (4 chunks of two rows whose
 // exchanges differ in the lowest bit).
@@ -465,20 +499,21 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
 
     for (int t = 0; t < nt; ++t, ++tile_no) {
       const int stage = tile_no % kStagesV;
+      // NaN codes are taken out; the scores of the columns that see their key become
+      // NaN.  The softmax waits for this, not for the stage.
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i)
+        any |= nan_bytes(x[i].x) | nan_bytes(x[i].y) | nan_bytes(x[i].z) | nan_bytes(x[i].w);
+      if (any) take_nan_out<STEPS, RPS>(x, sm.meta[tile_no % kMeta], r0);
+      mbar_arrive(&sm.n_full[tile_no % kMeta]);
       if (t + 1 < nt) wait(sm, &sm.m_full[(tile_no + 1) % kMeta], (tile_no + 1) / kMeta & 1, p.c.status);
       wait(sm, &sm.v_empty[stage], (tile_no / kStagesV & 1) ^ 1, p.c.status);
       uint8_t *dst = sm.v[stage];
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
         const int r = i * RPS + r0;
-        uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        const uint32_t odd = nan_bytes(ws[0]) | nan_bytes(ws[1]) | nan_bytes(ws[2]) | nan_bytes(ws[3]);
-        if (odd) {  // taken out here; the scores of the columns that see the key become NaN
-          atomicOr(&sm.meta[tile_no % kMeta].nan[r >> 5], 1u << (r & 31));
-          sm.meta[tile_no % kMeta].odd = 1;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) ws[b] &= ~((nan_bytes(ws[b]) >> 7) * 255u);
-        }
+        const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * ch)) =
             make_uint4(cvt2(ws[0]), cvt2_hi(ws[0]), cvt2(ws[1]), cvt2_hi(ws[1]));
         *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * ch + 1)) =
@@ -593,6 +628,96 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Rare tiles, through TMEM so that their code stays small.  Scores of keys in a
+// page outside the pool become -inf, of keys with a NaN value NaN.
+__device__ __noinline__ void hide_keys(uint32_t ts, const TileMeta &meta) {
+#pragma unroll 1
+  for (int j = 0; j < kKeys / 16; ++j) {
+    uint32_t s[16];
+    tmem_ld16(ts + 16 * j, s);
+    const uint32_t nan = meta.nan[j >> 1] >> (16 * (j & 1)), hide = meta.hide[j >> 1] >> (16 * (j & 1));
+    tmem_ld_wait();
+#pragma unroll
+    for (int b = 0; b < 16; ++b) {
+      if (nan >> b & 1) s[b] = 0x7FC00000u;
+      if (hide >> b & 1) s[b] = 0xFF800000u;  // -inf
+    }
+    tmem_st16(ts + 16 * j, s);
+  }
+  tmem_st_wait();
+}
+// A column's largest score of 16 keys, and the largest with their value exponent.
+__device__ __forceinline__ void largest(const uint32_t *v, float f, float lv, float &top, float &topw) {
+  const float a = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), v[6]);
+  const float b = max3(max3(v[7], v[8], v[9]), max3(v[10], v[11], v[12]), v[13]);
+  const float y = max3(fmaxf(a, __uint_as_float(v[14])), b, v[15]) * f;
+  top = fmaxf(top, y);
+  topw = fmaxf(topw, y + lv);
+}
+
+// New references for a tile, the sum and the row of O brought to them.
+// A weight in the sum is 2^(w - lv - m) of the one that enters the product.
+// Where that is large (kFar), the values are so small that the latter may leave
+// fp32's range; w - m is at most the largest lv so far (plus the slack of the
+// references), so a tile's spread of lv tells when to look.
+constexpr float kFar = 64.f;
+template <int D>
+__device__ __noinline__ void settle(uint32_t ts, uint32_t to, const TileMeta &meta, int room, float cs, bool has_o,
+                                    float &m, float &w, float &l) {
+  float top = -INFINITY, topw = -INFINITY;
+#pragma unroll 1
+  for (int g = 0; g < 8; ++g) {
+    uint32_t s[16];
+    tmem_ld16(ts + 16 * g, s);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (16 * g + k >= room) s[k] = 0xFF800000u;
+    largest(s, cs * meta.kv[g].x, meta.kv[g].y, top, topw);
+  }
+  const float mn = fmaxf(m, top), wn = fmaxf(w, topw);
+  const float fl = mn == m ? 1.f : ex2(m - mn), fo = wn == w ? 1.f : ex2(w - wn);
+  m = mn, w = wn;
+  l *= fl;
+  if (has_o) {
+#pragma unroll 1
+    for (int j = 0; j < D; j += 16) {
+      uint32_t o[16];
+      tmem_ld16(to + j, o);
+      tmem_ld_wait();
+#pragma unroll
+      for (int b = 0; b < 16; ++b) o[b] = __float_as_uint(__uint_as_float(o[b]) * fo);
+      tmem_st16(to + j, o);
+    }
+  }
+}
+// Weights of a tile whose value scales are that far apart, 16 keys at a time.
+__device__ __noinline__ float weigh_far(uint32_t ts, const TileMeta &meta, int room, float cs, float m, float w,
+                                        float l) {
+  const float mr = m == -INFINITY ? 0.f : m, wr = w == -INFINITY ? 0.f : w;
+#pragma unroll 1
+  for (int g = 0; g < 8; ++g) {
+    uint32_t s[16];
+    tmem_ld16(ts + 16 * g, s);
+    const float f = cs * meta.kv[g].x, lv = meta.kv[g].y;
+    tmem_ld_wait();
+    uint32_t h[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float y[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const float x = 16 * g + 2 * k + b < room ? __uint_as_float(s[2 * k + b]) * f : -INFINITY;
+        l += ex2(x - mr);
+        y[b] = ex2(x + (lv - wr));
+      }
+      h[k] = float2_to_half2(y[0], y[1]);
+    }
+    tmem_st8(ts + 8 * g, h);
+  }
+  return l;
+}
+
 template <int D>
 __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
   Walk &w = sm.walk[threadIdx.x >> 5];
@@ -607,7 +732,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
     if (ncols <= x * 128) {  // this half is empty: it keeps step, so that it meets every phase of the barriers
       if (nt) wait(sm, &sm.q_full, q_no++ & 1, p.c.status);
       for (int t = 0; t < nt; ++t, ++tile_no) {
-        wait(sm, &sm.v_full[tile_no % kStagesV], tile_no / kStagesV & 1, p.c.status);
+        wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
         wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);  // without it this half could run ahead of the issuing warp
         mbar_arrive(&sm.p_full[x]);
       }
@@ -626,103 +751,85 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
       ++q_no;
     }
     for (int t = 0; t < nt; ++t, ++tile_no) {
-      const int stage = tile_no % kStagesV;
-      wait(sm, &sm.v_full[stage], tile_no / kStagesV & 1, p.c.status);
+      wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
       wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);
       __syncwarp();
       tc_fence_after();
-      uint32_t s[128];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(ts + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
       const TileMeta &meta = sm.meta[tile_no % kMeta];
-      const uint32_t odd = meta.odd;
-      const float lv_min = meta.lv_min;
-      float f[8], lv[8];
+      const int room = room0 - t * kKeys;  // keys of the tile that the column sees
+      if (meta.odd) hide_keys(ts, meta);
+      // The weights are formed with the references as they stand.  A tile in which
+      // 16 of them sum to more than 2^12 (or the scores pass m by as much) is done
+      // again with new references: its scores are still in TMEM then.  The first
+      // tile has its references set first.
+      if (t == 0) settle<D>(ts, to, meta, room, cs, false, m, wr, l);
+      bool apart = false;
+      if (meta.spread > kFar - 16.f) apart = __any_sync(~0u, wr - meta.lv_min - m > kFar);
+      if (apart) {
+        if (t > 0) settle<D>(ts, to, meta, room, cs, true, m, wr, l);
+        l = weigh_far(ts, meta, room, cs, m, wr, l);
+      } else {
+        uint32_t s[128];
+        while (true) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float4 a = meta.ks[g], b = meta.lv[g];
-        f[4 * g] = cs * a.x, f[4 * g + 1] = cs * a.y, f[4 * g + 2] = cs * a.z, f[4 * g + 3] = cs * a.w;
-        lv[4 * g] = b.x, lv[4 * g + 1] = b.y, lv[4 * g + 2] = b.z, lv[4 * g + 3] = b.w;
-      }
-      tmem_ld_wait();
-      if (odd) {
+          for (int j = 0; j < 2; ++j) tmem_ld_32x32b_x32(ts + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t hide = meta.hide[j], nan = meta.nan[j];
-#pragma unroll
-          for (int b = 0; b < 32; ++b) {
-            if (nan >> b & 1) s[32 * j + b] = 0x7FC00000u;
-            if (hide >> b & 1) s[32 * j + b] = 0xFF800000u;  // -inf
-          }
-        }
-      }
-      if (t >= whole_tiles) {
-        const int room = room0 - t * kKeys;  // keys of the tile that the column sees
-#pragma unroll
-        for (int b = 0; b < kKeys; ++b)
-          if (b >= room) s[b] = 0xFF800000u;
-      }
-      // largest score, and largest score plus value exponent
-      float top = -INFINITY, topw = -INFINITY;
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const uint32_t *v = s + 16 * g;
-        const float a = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), v[6]);
-        const float b = max3(max3(v[7], v[8], v[9]), max3(v[10], v[11], v[12]), v[13]);
-        const float y = max3(fmaxf(a, __uint_as_float(v[14])), b, v[15]) * f[g];
-        top = fmaxf(top, y);
-        topw = fmaxf(topw, y + lv[g]);
-      }
-      // A weight in the sum is 2^(wr - lv - m) of the one that enters the product.
-      // Where that is large, the values are so small that the latter may leave
-      // fp32's range: the sum then takes powers of two of its own.
-      auto far = [&] { return wr - lv_min - m > 64.f; };
-      if (__any_sync(~0u, top > m + kSlack || topw > wr + kSlack || far())) {
-        const float mn = fmaxf(m, top), wn = fmaxf(wr, topw);
-        const float fl = mn == m ? 1.f : ex2(m - mn), fo = wn == wr ? 1.f : ex2(wr - wn);
-        m = mn, wr = wn;
-        l *= fl;
-        if (t > 0) {
-#pragma unroll 1
-          for (int j = 0; j < D; j += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + j, o);
+          for (int j = 2; j < 4; ++j) tmem_ld_32x32b_x32(ts + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
+          const float mr = m == -INFINITY ? 0.f : m, ww = wr == -INFINITY ? 0.f : wr;
+          float lt = 0.f, most = 0.f;
+          if (t >= whole_tiles) {
             tmem_ld_wait();
 #pragma unroll
-            for (int b = 0; b < 16; ++b) o[b] = __float_as_uint(__uint_as_float(o[b]) * fo);
-            tmem_st16(to + j, o);
+            for (int b = 0; b < kKeys; ++b)
+              if (b >= room) s[b] = 0xFF800000u;
           }
-        }
-        if (far()) {
+          // Pairs of scores pass through three steps, kLag pairs apart, so that the
+          // exponentials of one overlap the products of another and the sums and
+          // roundings of a third: product and offset; 2^x; sum and fp16.
+          constexpr int kLag = 6;
+          uint64_t e[64], sum[2] = {0, 0};
+          uint64_t f2 = 0, b2 = 0;
+          float back[8];
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
-            if (wr - lv[g] - m > 64.f) {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) l += ex2(__uint_as_float(s[16 * g + k]) * f[g] - m);
+          for (int i = 0; i < 64 + 2 * kLag; ++i) {
+            if (i < 64) {
+              if (i == 32) tmem_ld_wait();
+              if (i % 8 == 0) {
+                const float2 kv = meta.kv[i / 8];
+                const float f = cs * kv.x, b = kv.y - ww;
+                f2 = pack2(f, f), b2 = pack2(b, b);
+                back[i / 8] = ex2(-b - mr);
+              }
+              e[i] = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), f2, b2);
             }
+            if (i >= kLag && i < 64 + kLag) {
+              float y, z;
+              unpack2(e[i - kLag], y, z);
+              e[i - kLag] = pack2(ex2(y), ex2(z));
+            }
+            if (i >= 2 * kLag) {
+              const int k = i - 2 * kLag;
+              float y, z;
+              unpack2(e[k], y, z);
+              s[k] = float2_to_half2(y, z);
+              sum[k & 1] = k % 8 < 2 ? e[k] : add2(sum[k & 1], e[k]);
+              if (k % 8 == 7) {
+                unpack2(add2(sum[0], sum[1]), y, z);
+                y += z;
+                most = fmaxf(most, y);
+                lt = fmaf(y, back[k / 8], lt);
+              }
+            }
+          }
+          if (!__any_sync(~0u, fmaxf(most, lt * 0.125f) > 4096.f)) {
+            l += lt;
+            break;
+          }
+          settle<D>(ts, to, meta, room, cs, t > 0, m, wr, l);
         }
-      }
-      const float mr = m == -INFINITY ? 0.f : m, ww = wr == -INFINITY ? 0.f : wr;
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const float b = lv[g] - ww;
-        float back = -b - mr;
-        back = back > 64.f ? -INFINITY : back;
-        const uint64_t f2 = pack2(f[g], f[g]), b2 = pack2(b, b);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float y, z;
-          unpack2(fma2(pack2(__uint_as_float(s[16 * g + 2 * k]), __uint_as_float(s[16 * g + 2 * k + 1])), f2, b2), y,
-                  z);
-          y = ex2(y), z = ex2(z);
-          sum[k & 1] = k < 2 ? pack2(y, z) : add2(sum[k & 1], pack2(y, z));
-          s[8 * g + k] = float2_to_half2(y, z);
-        }
-        float y, z;
-        unpack2(add2(sum[0], sum[1]), y, z);
-        l = fmaf(y + z, ex2(back), l);
-        if (g & 1) tmem_st16(ts + 8 * (g - 1), *reinterpret_cast<const uint32_t(*)[16]>(s + 8 * (g - 1)));
+        tmem_st32(ts, s);
+        tmem_st32(ts + 32, s + 32);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -850,6 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(&sm.m_full[i], 1);
       mbar_init(&sm.m_empty[i], 1);
+      mbar_init(&sm.n_full[i], kConverters);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
