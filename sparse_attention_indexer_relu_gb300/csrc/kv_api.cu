@@ -96,7 +96,7 @@ constexpr int kSplitCols = 16;
 struct AttnPlan {
   bool split, tiled;
   int nb, ctas, tiled_ctas;
-  size_t slots_off, tiled_off, tiled_slots_off, bytes;
+  size_t slots_off, tiled_off, tiled_slots_off, factor_off, terms_off, bytes;
 };
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, int q_heads, bool selected) {
@@ -112,15 +112,18 @@ AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, 
   p.tiled_off = up256(p.slots_off + (size_t)p.ctas * 2 * attn_slot_floats(p.nb, c->head_dim) * sizeof(float));
   p.tiled_ctas = sms;
   p.tiled_slots_off = p.tiled_off + up256((size_t)sms * sizeof(int4));
-  p.bytes = p.tiled ? p.tiled_slots_off + (size_t)sms * 2 * kTiledCols * (c->head_dim + 4) * sizeof(float)
-                    : p.tiled_off;
+  p.factor_off = p.tiled_slots_off + up256((size_t)sms * 2 * kTiledCols * (c->head_dim + 4) * sizeof(float));
+  p.terms_off = p.factor_off + up256((size_t)rows * q_heads * sizeof(float));
+  p.bytes = p.tiled ? p.terms_off + (size_t)kQueryTerms * rows * q_heads * c->head_dim : p.tiled_off;
   return p;
 }
 
 int check_attention(const mqa_kv_cache *c, int rows, int q_heads) {
   const int rc = check_cache(c, kTables);
   if (rc != MQA_OK) return rc;
-  if (rows < 0 || q_heads < 1 || q_heads % c->kv_heads != 0 || q_heads > 65536) return MQA_ERR_INVALID_ARGUMENT;
+  if (rows < 0 || q_heads < 1 || q_heads % c->kv_heads != 0 || q_heads > 65536 ||
+      (long long)rows * q_heads > INT_MAX / kQueryTerms)
+    return MQA_ERR_INVALID_ARGUMENT;
   return MQA_OK;
 }
 
@@ -207,11 +210,16 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
     p.max_cols = P.split ? kSplitCols : 0;
     p.desc = reinterpret_cast<int4 *>(ws + P.tiled_off);
     p.slots = reinterpret_cast<float *>(ws + P.tiled_slots_off);
-    CUtensorMap map;
+    CUtensorMap map, q_map;
+    uint8_t *terms = ws + P.terms_off;
+    float *factor = reinterpret_cast<float *>(ws + P.factor_off);
+    p.q_scale = factor;
     rc = encode_code_rows(&map, cache->k, (uint64_t)cache->num_pages * cache->kv_heads * cache->page_size,
                           cache->head_dim, (uint32_t)cache->page_size);
     if (rc != MQA_OK) return rc;
-    rc = code(launch_kv_prefill(p, map, P.tiled_ctas, as_stream(stream)));
+    rc = encode_code_rows(&q_map, terms, (uint64_t)(type == MQA_KV_BF16 ? 2 : 3) * rows * q_heads, cache->head_dim, 128);
+    if (rc != MQA_OK) return rc;
+    rc = code(launch_kv_prefill(p, map, q_map, terms, factor, P.tiled_ctas, as_stream(stream)));
     if (rc != MQA_OK || !P.split) return rc;
   }
   p.max_cols = P.tiled ? kSplitCols : INT_MAX;

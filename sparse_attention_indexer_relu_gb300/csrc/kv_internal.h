@@ -64,6 +64,7 @@ struct AttnParams {
   int max_cols;      // sequences of more (row, head of the group) columns go to the tiled kernel
   int4 *desc;        // per CTA: the split item it began, for the joining kernel
   float *slots;      // per CTA: two slots of partial results
+  const float *q_scale;  // tiled kernel: per column, what its products are multiplied with
 };
 
 // Column block sizes (8 * NB) of the split kernel, its CTAs per SM and threads.
@@ -74,8 +75,12 @@ size_t attn_slot_floats(int nb, int dim);
 // more columns), and the fewest key tiles a CTA's part holds.
 constexpr int kTiledCols = 256;
 constexpr int kTiledMinTiles = 4;
-// map: the keys' codes as rows of head_dim bytes, boxes of one page.
-cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream);
+constexpr int kQueryTerms = 3;  // e4m3 terms of an fp16 query value; a bf16 one has 2
+// map: the keys' codes as rows of head_dim bytes, boxes of one page; q_map: the
+// query terms (q8, workspace of kQueryTerms * rows * q_heads * head_dim bytes)
+// in boxes of 128 rows; factor: rows * q_heads floats, p.q_scale.
+cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8,
+                              float *factor, int ctas, cudaStream_t stream);
 cudaError_t launch_kv_attention(const AttnParams &p, int nb, int ctas, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,

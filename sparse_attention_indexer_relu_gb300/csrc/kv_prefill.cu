@@ -19,9 +19,11 @@
 // While one half's scores are turned into weights the tensor cores work on the
 // other half.  Roles: 2 x 4 softmax warps (a thread per column; it also moves
 // its references and rescales its row of O when a score passes them too far),
-// 4 converter warps (values to fp16, which the MMA reads transposed, and the
-// query terms), one warp that looks pages up and issues the keys' copies, one
-// that issues the MMAs.
+// 4 converter warps (values to fp16, which the MMA reads transposed), one warp
+// that looks pages up and issues the queries' and keys' copies, one that issues
+// the MMAs.  The query terms are formed once per call by a kernel of their own
+// (in the main kernel they cost 20,000 cycles per item), laid out so that an
+// item's columns are consecutive rows.
 // Every wait has a time limit; once one has run out, all of them return at
 // once and the kernel runs to its end on whatever it finds in shared memory.
 //
@@ -42,7 +44,7 @@ constexpr int kKeys = 128;                // keys per tile
 constexpr int kCols = kTiledCols;         // columns per item
 constexpr int kStagesK = 3, kStagesV = 2;
 constexpr int kMeta = 8;                  // tile descriptions in flight
-constexpr int kTerms = 3;                 // e4m3 terms of a query value (bf16: 2)
+constexpr int kTerms = kQueryTerms;       // e4m3 terms of a query value (bf16: 2)
 constexpr long long kWaitNs = 2000000000LL;
 constexpr int kConverters = 128;
 
@@ -158,7 +160,6 @@ struct Smem {
   uint8_t q[2][kTerms][128 * D];
   uint8_t k[kStagesK][kKeys * D];
   uint8_t v[kStagesV][kKeys * D * 2];
-  float cs[2][kCols];
   TileMeta meta[kMeta];
   uint64_t q_full, q_empty, k_full[kStagesK], k_empty[kStagesK], v_full[kStagesV], v_empty[kStagesV];
   uint64_t m_full[kMeta], m_empty[kMeta], n_full[kMeta], s_full[2], p_full[2], o_full[2], done;
@@ -261,6 +262,11 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+__device__ __forceinline__ void store32(void *p, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(p)), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 template <int R>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -310,12 +316,13 @@ __device__ __forceinline__ uint32_t code_at(int r, int c) {
 // scales; then, tile by tile, the description and the keys' copies, one box
 // per page.
 template <int D>
-__device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, Smem<D> &sm) {
+__device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, Smem<D> &sm) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31, g = lane & 7, heads = p.c.heads;
   const int box = min(p.c.page, kKeys), per_box = box >> 4;
-  uint32_t tile_no = 0;
-  const uint64_t keep = policy_evict_last();  // other CTAs read the same keys
+  uint32_t tile_no = 0, q_no = 0;
+  const uint64_t keep = policy_evict_last(), once = policy_evict_first();  // other CTAs read the same keys
+  const int terms = p.bf16 ? 2 : 3, planes = p.rows * p.group;  // rows of a head in a term's plane
   for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p);
     const int lim = block_limit(p, w.x.q, w.x.block), first = w.x.t0 * kKeys + g * 16, head = w.x.head;
@@ -374,10 +381,23 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, Smem<D>
         __syncwarp();
         if (lane >> 3 == u && (mine >> g & 1))
           tma_load_2d(sm.k[stage] + g * 16 * D, &map, &sm.k_full[stage], 0, row, keep);
+        if (tb + u == 0) {  // the queries, once the previous part's last scores are done
+          wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p.c.status);
+          const int halves = w.cols(p) > 128 ? 2 : 1, at = w.x.q.r0 * p.group + w.x.block * kCols;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(terms * halves * 128 * D));
+          __syncwarp();
+          if (lane < terms * halves) {
+            const int x = lane / terms, term = lane % terms;
+            tma_load_2d(sm.q[x][term], &q_map, &sm.q_full, 0, (term * heads + head) * planes + at + 128 * x, once);
+          }
+          ++q_no;
+        }
       }
     }
   }
   // the copies must have landed before the CTA leaves
+  if (q_no) drain(&sm.q_full, (q_no - 1) & 1);
   for (int i = 1; i <= kStagesK; ++i)
     if (tile_no >= (uint32_t)i) drain(&sm.k_full[(tile_no - i) % kStagesK], (tile_no - i) / kStagesK & 1);
   __syncwarp();
@@ -415,7 +435,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
   const int tid = threadIdx.x & (kConverters - 1), lane = tid & 31;
   const int ch = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3;
   const int r0 = D == 128 ? (tid >> 5) * 4 + (lane >> 2 & 3) : (tid >> 5) * 8 + (lane >> 2);
-  uint32_t tile_no = 0, q_no = 0;
+  uint32_t tile_no = 0;
   uint4 x[STEPS];
   auto load = [&](uint32_t no, int i) {
     const int r = i * RPS + r0;
@@ -424,78 +444,11 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
     if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(p.c.v + (size_t)(row + (r & 15)) * D + ch * 16));
   };
   for (; w.valid(); step_on(p, w)) {
-    const int nt = w.needed(p), ncols = w.cols(p);
+    const int nt = w.needed(p);
     if (nt == 0) continue;  // nothing is read
     wait(sm, &sm.m_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) load(tile_no, i);
-
-    // ---- the queries (the previous part's last scores must be done): 8
-    // components per lane, a row's largest magnitude by exchange
-    wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p.c.status);
-    {
-      constexpr int LPR = D / 8, QR = 32 / LPR;  // lanes per row, rows per warp step
-      constexpr int BATCH = 8;
-      const int part = lane % LPR;
-      const int r_first = w.x.q.r0, c_first = w.x.block * kCols, h_first = w.x.head * p.group;
-#pragma unroll 1
-      for (int b = 0; b < 64 / QR; b += BATCH) {
-        if ((tid >> 5) * 64 + b * QR >= ((ncols + 127) & ~127)) break;  // an empty half is not read by the MMAs
-        uint4 u[BATCH];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          const int col = (tid >> 5) * 64 + (b + i) * QR + lane / LPR;
-          const int cc = c_first + col;
-          u[i] = make_uint4(0, 0, 0, 0);
-          if (col < ncols)
-            u[i] = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) +
-                                                         (size_t)(r_first + cc / p.group) * p.q_stride +
-                                                         (size_t)(h_first + cc % p.group) * D + part * 8));
-        }
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          const int col = (tid >> 5) * 64 + (b + i) * QR + lane / LPR;
-          const uint32_t ws[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-          float f[8];
-          float amax = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 y = p.bf16 ? bf16x2_to_float2(ws[j]) : half2_to_float2(ws[j]);
-            f[2 * j] = y.x, f[2 * j + 1] = y.y;
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (!(fabsf(f[j]) <= FLT_MAX)) f[j] = NAN;  // infinities too: no softmax of theirs is a number
-            amax = fmaxf(amax, fabsf(f[j]));
-          }
-#pragma unroll
-          for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-          // power of two that brings the largest magnitude to (224, 448]
-          int e = 0;
-          if (amax > 0.f) e = ((__float_as_uint(amax) & 0x7FFFFFu) > 0x600000u ? 7 : 8) - exponent_of(amax);
-          e = max(-110, min(110, e));
-          const float up = pow2i(e);
-          if (part == 0) sm.cs[q_no & 1][col] = p.scale_log2 * pow2i(-e);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] *= up;
-          for (int term = 0; term < (p.bf16 ? 2 : 3); ++term) {
-            uint2 c;
-            c.x = to_e4m3x4(f[0], f[1], f[2], f[3]);
-            c.y = to_e4m3x4(f[4], f[5], f[6], f[7]);
-            *reinterpret_cast<uint2 *>(sm.q[col >> 7][term] + code_at<D>(col & 127, part >> 1) + (part & 1) * 8) = c;
-            const uint32_t back[4] = {cvt2(c.x), cvt2_hi(c.x), cvt2(c.y), cvt2_hi(c.y)};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 y = half2_to_float2(back[j]);
-              f[2 * j] -= y.x, f[2 * j + 1] -= y.y;
-            }
-          }
-        }
-      }
-    }
-    fence_async_smem();
-    mbar_arrive(&sm.q_full);
-    ++q_no;
 
     for (int t = 0; t < nt; ++t, ++tile_no) {
       const int stage = tile_no % kStagesV;
@@ -662,18 +615,22 @@ __device__ __forceinline__ void largest(const uint32_t *v, float f, float lv, fl
 // references), so a tile's spread of lv tells when to look.
 constexpr float kFar = 64.f;
 template <int D>
-__device__ __noinline__ void settle(uint32_t ts, uint32_t to, const TileMeta &meta, int room, float cs, bool has_o,
+__device__ __forceinline__ void settle(uint32_t ts, uint32_t to, const TileMeta &meta, int room, float cs, bool has_o,
                                     float &m, float &w, float &l) {
   float top = -INFINITY, topw = -INFINITY;
 #pragma unroll 1
-  for (int g = 0; g < 8; ++g) {
-    uint32_t s[16];
-    tmem_ld16(ts + 16 * g, s);
+  for (int j = 0; j < 2; ++j, room -= 64) {
+    uint32_t s[64];
+    tmem_ld_32x32b_x32(ts + 64 * j, *reinterpret_cast<uint32_t(*)[32]>(s));
+    tmem_ld_32x32b_x32(ts + 64 * j + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
     tmem_ld_wait();
+    if (__any_sync(~0u, room < 64)) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (16 * g + k >= room) s[k] = 0xFF800000u;
-    largest(s, cs * meta.kv[g].x, meta.kv[g].y, top, topw);
+      for (int b = 0; b < 64; ++b)
+        if (b >= room) s[b] = 0xFF800000u;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) largest(s + 16 * g, cs * meta.kv[4 * j + g].x, meta.kv[4 * j + g].y, top, topw);
   }
   const float mn = fmaxf(m, top), wn = fmaxf(w, topw);
   const float fl = mn == m ? 1.f : ex2(m - mn), fo = wn == w ? 1.f : ex2(w - wn);
@@ -725,12 +682,11 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
   const int r = threadIdx.x & 127;       // its column
   const uint32_t lanes = (uint32_t)(r & ~31) << 16;
   const uint32_t ts = sm.tmem + 256 + x * 128 + lanes, to = sm.tmem + x * 128 + lanes;
-  uint32_t tile_no = 0, q_no = 0, s_no = 0, o_no = 0;
+  uint32_t tile_no = 0, s_no = 0, o_no = 0;
   for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p), ncols = w.cols(p);
     const int col = x * 128 + r;
     if (ncols <= x * 128) {  // this half is empty: it keeps step, so that it meets every phase of the barriers
-      if (nt) wait(sm, &sm.q_full, q_no++ & 1, p.c.status);
       for (int t = 0; t < nt; ++t, ++tile_no) {
         wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
         wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);  // without it this half could run ahead of the issuing warp
@@ -738,18 +694,15 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
       }
       continue;
     }
-    const int c = w.x.block * kCols + col;
-    const int i = c / p.group;
-    const int lim = col < ncols ? (p.causal ? min(max(w.x.q.len - w.x.q.n + i + 1, 0), w.x.q.len) : w.x.q.len) : 0;
-    float m = -INFINITY, wr = -INFINITY, l = 0.f;
-    float cs = 0.f;
-    const int room0 = lim - w.x.t0 * kKeys;
-    const int whole_tiles = __reduce_min_sync(~0u, room0) / kKeys;  // tiles every column of the warp sees whole
-    if (nt) {
-      wait(sm, &sm.q_full, q_no & 1, p.c.status);
-      cs = sm.cs[q_no & 1][col];
-      ++q_no;
+    float m = -INFINITY, wr = -INFINITY, l = 0.f, cs = 0.f;
+    int room0 = 0;  // keys that the column sees from the part's first tile on
+    if (col < ncols) {
+      const int c = w.x.block * kCols + col;
+      room0 = p.causal ? min(max(w.x.q.len - w.x.q.n + c / p.group + 1, 0), w.x.q.len) : w.x.q.len;
+      cs = __ldg(p.q_scale + (size_t)w.x.head * p.rows * p.group + (size_t)w.x.q.r0 * p.group + c);
     }
+    room0 -= w.x.t0 * kKeys;
+    const int whole_tiles = __reduce_min_sync(~0u, room0) / kKeys;  // tiles every column of the warp sees whole
     for (int t = 0; t < nt; ++t, ++tile_no) {
       wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
       wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);
@@ -762,15 +715,16 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
       // 16 of them sum to more than 2^12 (or the scores pass m by as much) is done
       // again with new references: its scores are still in TMEM then.  The first
       // tile has its references set first.
-      if (t == 0) settle<D>(ts, to, meta, room, cs, false, m, wr, l);
-      bool apart = false;
-      if (meta.spread > kFar - 16.f) apart = __any_sync(~0u, wr - meta.lv_min - m > kFar);
-      if (apart) {
-        if (t > 0) settle<D>(ts, to, meta, room, cs, true, m, wr, l);
-        l = weigh_far(ts, meta, room, cs, m, wr, l);
-      } else {
+      const bool look = meta.spread > kFar - 16.f;
+      for (bool anew = t == 0;; anew = true) {
+        if (anew) settle<D>(ts, to, meta, room, cs, t > 0, m, wr, l);
+        if (look && __any_sync(~0u, wr - meta.lv_min - m > kFar)) {
+          if (!anew) continue;
+          l = weigh_far(ts, meta, room, cs, m, wr, l);
+          break;
+        }
         uint32_t s[128];
-        while (true) {
+        {
 #pragma unroll
           for (int j = 0; j < 2; ++j) tmem_ld_32x32b_x32(ts + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
           tmem_ld_wait();
@@ -822,14 +776,12 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
               }
             }
           }
-          if (!__any_sync(~0u, fmaxf(most, lt * 0.125f) > 4096.f)) {
-            l += lt;
-            break;
-          }
-          settle<D>(ts, to, meta, room, cs, t > 0, m, wr, l);
+          if (!anew && __any_sync(~0u, fmaxf(most, lt * 0.125f) > 4096.f)) continue;
+          l += lt;
         }
         tmem_st32(ts, s);
         tmem_st32(ts + 32, s + 32);
+        break;
       }
       tmem_st_wait();
       tc_fence_before();
@@ -843,39 +795,42 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
     }
     const bool whole = w.x.t0 == 0 && w.x.t1 == w.x.tiles;
     const bool none = m == -INFINITY && l == 0.f;
-    const float f = none ? 0.f : l != l ? NAN : ex2(wr - m) / l;
-    const int row = w.x.q.r0 + i, head = w.x.head * p.group + c % p.group;
+    const float f = none ? 1.f : l != l ? NAN : ex2(wr - m) / l;
+    const int c = w.x.block * kCols + col, ncols_now = w.cols(p);
+    const int row = w.x.q.r0 + c / p.group, head = w.x.head * p.group + c % p.group;
     float *slot = p.slots + ((size_t)blockIdx.x * 2 + (w.x.t0 == 0 ? 1 : 0)) * ((size_t)kCols * (D + 4));
-    uint4 *out = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + ((size_t)row * p.q_heads + head) * D);
+    uint8_t *out = reinterpret_cast<uint8_t *>(p.out) + ((size_t)row * p.q_heads + head) * D * 2;
 #pragma unroll 1
-    for (int j = 0; j < D; j += 16) {
-      uint32_t o[16];
+    for (int j = 0; j < D; j += 32) {
+      uint32_t o[32];
       if (nt) {
-        tmem_ld16(to + j, o);
+        tmem_ld_32x32b_x32(to + j, o);
         tmem_ld_wait();
       }
+      if (none) {
 #pragma unroll
-      for (int b = 0; b < 16; ++b) o[b] = none ? 0u : o[b];
-      if (col < ncols) {
+        for (int b = 0; b < 32; ++b) o[b] = 0;
+      }
+      if (col < ncols_now) {
+        // a lane writes its row by itself, in whole 32-byte sectors
         if (whole) {
-          uint32_t h[8];
 #pragma unroll
-          for (int b = 0; b < 8; ++b) {
-            const float y = __uint_as_float(o[2 * b]) * f, z = __uint_as_float(o[2 * b + 1]) * f;
-            h[b] = none ? 0u : p.bf16 ? float2_to_bf162(y, z) : float2_to_half2(y, z);
+          for (int k = 0; k < 32; k += 16) {
+            uint32_t h[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              const float y = __uint_as_float(o[k + 2 * b]) * f, z = __uint_as_float(o[k + 2 * b + 1]) * f;
+              h[b] = p.bf16 ? float2_to_bf162(y, z) : float2_to_half2(y, z);
+            }
+            store32(out + 2 * (j + k), h);
           }
-          out[j / 8] = make_uint4(h[0], h[1], h[2], h[3]);
-          out[j / 8 + 1] = make_uint4(h[4], h[5], h[6], h[7]);
         } else {
-          float4 *d = reinterpret_cast<float4 *>(slot + (size_t)col * D + j);
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-            d[b] = make_float4(__uint_as_float(o[4 * b]), __uint_as_float(o[4 * b + 1]), __uint_as_float(o[4 * b + 2]),
-                               __uint_as_float(o[4 * b + 3]));
+          for (int k = 0; k < 32; k += 8) store32(slot + (size_t)col * D + j + k, o + k);
         }
       }
     }
-    if (col < ncols) {
+    if (col < ncols_now) {
       if (whole) {
         if (p.lse)
           p.lse[(size_t)row * p.q_heads + head] = none ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
@@ -888,14 +843,15 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
     if (threadIdx.x == 0 && !whole && w.x.t0 == 0) {
       const long long rest = w.x.tiles - (w.x.t1 - w.x.t0);
       p.desc[blockIdx.x] = make_int4(w.x.q.r0, w.x.head, w.x.block * kCols,
-                                     (int)((rest + per - 1) / per) | ncols << 20);
+                                     (int)((rest + per - 1) / per) | ncols_now << 20);
     }
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv_prefill_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map) {
+    kv_prefill_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map,
+                      const __grid_constant__ CUtensorMap q_map) {
   extern __shared__ uint8_t raw[];
   Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -944,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     sm.dead = 0;
-    mbar_init(&sm.q_full, kConverters);
+    mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
     for (int i = 0; i < kStagesK; ++i) {
       mbar_init(&sm.k_full[i], 1);
@@ -992,17 +948,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (lane == 0) sm.walk[warp] = w;
   __syncwarp();
-  // registers: 256 x 184 + 128 x 96 + 128 x 48 = 512 x 128, what the block was launched with
+  // registers: 256 x 192 + 128 x 80 + 128 x 48 = 512 x 128, what the block was launched with
   if (warp < 8) {
-    reg_inc<184>();
+    reg_inc<192>();
     softmax_role<D>(p, sm, per);
   } else if (warp < 12) {
-    reg_dec<96>();
+    reg_dec<80>();
     convert_role<D>(p, sm);
   } else {
     reg_dec<48>();
     if (warp == 12) mma_role<D>(p, sm);
-    if (warp == 13) lookup_role<D>(p, map, sm);
+    if (warp == 13) lookup_role<D>(p, map, q_map, sm);
   }
   __syncwarp();
   tc_fence_before();
@@ -1053,13 +1009,73 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const AttnParams p
   }
 }
 
+// Query terms: D / 8 lanes per (row, head), 8 values each.  Terms go to planes
+// [term][key/value head][row][head of the group][D], factors to [key/value
+// head][row][head of the group].
 template <int D>
-cudaError_t launch(const AttnParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream) {
+__global__ void __launch_bounds__(256) kv_query_terms_kernel(const AttnParams p, uint8_t *__restrict__ q8,
+                                                            float *__restrict__ factor) {
+  constexpr int LPR = D / 8, PER = 256 / LPR;  // lanes per row, rows per CTA
+  const int part = threadIdx.x % LPR;
+  const long long total = (long long)p.rows * p.q_heads;
+  const int last = min(max(p.starts[p.c.seqs], 0), p.rows);
+  const long long i = (long long)blockIdx.x * PER + threadIdx.x / LPR;
+  const int row = (int)(i / p.q_heads), head = (int)(i % p.q_heads);
+  const bool on = i < total && row < last;  // rows of no sequence are not read
+  uint4 u = make_uint4(0, 0, 0, 0);
+  if (on)
+    u = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + (size_t)row * p.q_stride +
+                                              (size_t)head * D + part * 8));
+  const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+  float f[8];
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 y = p.bf16 ? bf16x2_to_float2(ws[j]) : half2_to_float2(ws[j]);
+    f[2 * j] = y.x, f[2 * j + 1] = y.y;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (!(fabsf(f[j]) <= FLT_MAX)) f[j] = NAN;  // infinities too: no softmax of theirs is a number
+    amax = fmaxf(amax, fabsf(f[j]));
+  }
+#pragma unroll
+  for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+  if (!on) return;
+  // power of two that brings the largest magnitude to (224, 448]
+  int e = 0;
+  if (amax > 0.f) e = ((__float_as_uint(amax) & 0x7FFFFFu) > 0x600000u ? 7 : 8) - exponent_of(amax);
+  e = max(-110, min(110, e));
+  const float up = pow2i(e);
+  const size_t at = ((size_t)(head / p.group) * p.rows + row) * p.group + head % p.group;
+  if (part == 0) factor[at] = p.scale_log2 * pow2i(-e);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] *= up;
+  const size_t plane = (size_t)total * D;
+  for (int term = 0; term < (p.bf16 ? 2 : 3); ++term) {
+    uint2 c;
+    c.x = to_e4m3x4(f[0], f[1], f[2], f[3]);
+    c.y = to_e4m3x4(f[4], f[5], f[6], f[7]);
+    *reinterpret_cast<uint2 *>(q8 + term * plane + at * D + part * 8) = c;
+    const uint32_t back[4] = {cvt2(c.x), cvt2_hi(c.x), cvt2(c.y), cvt2_hi(c.y)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 y = half2_to_float2(back[j]);
+      f[2 * j] -= y.x, f[2 * j + 1] -= y.y;
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8, float *factor,
+                   int ctas, cudaStream_t stream) {
   constexpr int bytes = (int)sizeof(Smem<D>) + 1024;
   auto *k = kv_prefill_kernel<D>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  k<<<ctas, kThreads, bytes, stream>>>(p, map);
+  const long long rows = (long long)p.rows * p.q_heads, per = 256 / (D / 8);
+  kv_query_terms_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, stream>>>(p, q8, factor);
+  k<<<ctas, kThreads, bytes, stream>>>(p, map, q_map);
   const cudaError_t le = cudaGetLastError();
   if (le != cudaSuccess) return le;
   kv_prefill_join_kernel<D><<<dim3(ctas, kCols / 32), 256, 0, stream>>>(p);
@@ -1068,8 +1084,10 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &map, int ctas, cudaSt
 
 }  // namespace
 
-cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, int ctas, cudaStream_t stream) {
-  return p.c.dim == 64 ? launch<64>(p, map, ctas, stream) : launch<128>(p, map, ctas, stream);
+cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8,
+                              float *factor, int ctas, cudaStream_t stream) {
+  return p.c.dim == 64 ? launch<64>(p, map, q_map, q8, factor, ctas, stream)
+                       : launch<128>(p, map, q_map, q8, factor, ctas, stream);
 }
 
 }  // namespace mqa
