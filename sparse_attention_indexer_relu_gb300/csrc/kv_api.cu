@@ -88,7 +88,7 @@ int code(cudaError_t e) {
 }
 
 // Which kernels a call runs and where their parts of the workspace lie.  The
-// split kernel (kv_attn.cu) takes blocks of 8, 16 or 32 columns; calls in which
+// split kernel (kv_attn.cu) takes blocks of 8 to 32 columns; calls in which
 // a sequence may have more than kTiledFrom columns run the tiled kernel
 // (kv_prefill.cu), and leave sequences of up to kSplitCols to the split kernel.
 constexpr int kTiledFrom = 64;
@@ -106,7 +106,7 @@ AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, 
   AttnPlan p;
   p.tiled = !selected && cols > kTiledFrom;
   p.split = !p.tiled || c->max_seqs > 1;
-  p.nb = cols <= 8 ? 1 : cols <= 16 || p.tiled ? 2 : 4;
+  p.nb = cols <= 8 ? 1 : cols <= 16 || p.tiled ? 2 : cols <= 24 ? 3 : 4;
   p.ctas = sms * attn_ctas_per_sm(p.nb);
   p.slots_off = up256((size_t)p.ctas * sizeof(int4));
   p.tiled_off = up256(p.slots_off + (size_t)p.ctas * 2 * attn_slot_floats(p.nb, c->head_dim) * sizeof(float));
@@ -220,12 +220,13 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
     rc = encode_code_rows(&q_map, terms, (uint64_t)(type == MQA_KV_BF16 ? 2 : 3) * rows * q_heads, cache->head_dim, 128);
     if (rc != MQA_OK) return rc;
     rc = code(launch_kv_prefill(p, map, q_map, terms, factor, P.tiled_ctas, as_stream(stream)));
+    if (rc == MQA_OK) rc = code(launch_kv_join_tiled(p, P.tiled_ctas, as_stream(stream)));
     if (rc != MQA_OK || !P.split) return rc;
   }
   p.max_cols = P.tiled ? kSplitCols : INT_MAX;
   p.desc = reinterpret_cast<int4 *>(ws);
   p.slots = reinterpret_cast<float *>(ws + P.slots_off);
-  return code(launch_kv_attention(p, P.nb, P.ctas, as_stream(stream)));
+  return code(launch_kv_attention(p, P.nb, P.ctas, P.tiled, as_stream(stream)));
 }
 
 int mqa_kv_reserve(const mqa_kv_cache *cache, const int32_t *counts, void *stream) {

@@ -14,7 +14,7 @@
 // relative to the largest weight TIMES scale that its column has seen (11
 // bits; a weight 2^-24 below it still has one).  The sum of the softmax is
 // kept in fp32 from unrounded weights against a second reference m.  Both
-// references move only when a value passes them by 2^8.
+// references move only when a weight passes 2^12.
 //
 // Layout.  S^T = K Q^T and O^T = V^T P^T: keys are the M dimension of the
 // first product and head components that of the second, so 8 columns fill an
@@ -39,7 +39,6 @@ namespace {
 
 constexpr int kWarps = kAttnThreads / 32;
 constexpr int kTile = 16 * kWarps;  // keys per unit of work: one 16-key sub-tile per warp
-constexpr float kSlack = 8.0f;      // a reference moves when a value passes it by 2^8: p' <= 2^8 in fp16
 constexpr int kStages = 3;          // sub-tiles in flight per warp: 2 x 16 warps x 4 KB ahead on an SM
 
 template <int NB>
@@ -82,7 +81,7 @@ struct Item {
 
 }  // namespace
 
-int attn_ctas_per_sm(int nb) { return nb == 1 ? Cfg<1>::ctas : nb == 2 ? Cfg<2>::ctas : Cfg<4>::ctas; }
+int attn_ctas_per_sm(int nb) { return nb == 1 ? Cfg<1>::ctas : nb == 2 ? Cfg<2>::ctas : nb == 3 ? Cfg<3>::ctas : Cfg<4>::ctas; }
 size_t attn_slot_floats(int nb, int dim) { return (size_t)8 * nb * (dim + 4); }
 
 namespace {
@@ -104,6 +103,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7
 
 template <int D, int NB, bool SEL>
 __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(const AttnParams p) {
+  grid_dependents();
   extern __shared__ __align__(128) uint8_t smem_raw[];
   using S = Smem<D, NB>;
   S &sm = *reinterpret_cast<S *>(smem_raw);
@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
   long long at = blockIdx.x * per;
   const long long end = min(total, at + per);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (at >= end) grid_wait();
   if (at >= end) return;  // the whole CTA leaves together
   Item it;
   int tile;  // first tile of the current segment
@@ -292,7 +293,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         cs[nb][c] = sm.cs[nb * 8 + 2 * t + c];
-        lim[nb][c] = sm.lim[nb * 8 + 2 * t + c];
+        // columns behind the last take part like the others (a query of zeros)
+        lim[nb][c] = nb * 8 + 2 * t + c < ncols ? sm.lim[nb * 8 + 2 * t + c] : lim_max;
       }
     const int32_t *sel = SEL ? p.selected + (size_t)it.seq * p.n_selected : nullptr;
 
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
             if (lane == (i & 31)) {
               meta.ks[stage][0] = d_ks;
               meta.lv[stage][0] = d_lv;
-              meta.pos[stage][0] = d_row < 0 ? INT32_MAX - 16 : base;
+              meta.pos[stage][0] = d_row < 0 ? INT32_MAX - 64 : base;
             }
           }
           const int first = SEL ? 0 : __shfl_sync(~0u, d_row, i & 31);
@@ -467,37 +469,90 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
             }
           bad_keys = __reduce_or_sync(~0u, bad_keys);
         }
-        // ---- weights
-        float s[NB][4], lv[2];
+        // ---- weights: formed with the references as they stand; a sub-tile in which
+        // one passes 2^12 (or that finds no references yet) moves them and starts over
+        uint32_t pf[NB][2];
+        float pl[NB][2][2];
         {
-          float ks[2];
-          int pos[2];
+          float ks[2], lv[2], none[2];
+          int room[2];  // by how much a column's limit lies behind the key
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int k = SEL ? g + 8 * r : 0;
+            const int k = SEL ? g + 8 * r : 0, pos = meta.pos[stage][k];
             ks[r] = meta.ks[stage][k];
             lv[r] = meta.lv[stage][k];
-            pos[r] = meta.pos[stage][k] + (SEL ? 0 : g + 8 * r);
+            none[r] = SEL && pos == INT32_MAX ? -INFINITY : 0.f;  // an entry that names no visible key
+            room[r] = SEL ? 0 : pos + g + 8 * r;
           }
-          bool move = false;
+          if (SEL) {
+            if (bad_keys) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+              for (int r = 0; r < 2; ++r)
+                if (bad_keys >> (g + 8 * r) & 1) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+                  for (int nb = 0; nb < NB; ++nb) acc[nb][2 * r] = acc[nb][2 * r + 1] = NAN;
+                }
+            }
+          } else if (bad_keys || __shfl_sync(~0u, room[0], 0) + 16 > lim_min) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  if (bad_keys >> (g + 8 * r) & 1) acc[nb][2 * r + c] = NAN;
+                  // (scales are positive: -inf stays -inf)
+                  if (room[r] >= lim[nb][c]) acc[nb][2 * r + c] = -INFINITY;
+                }
+          }
+          for (bool anew = false;; anew = true) {
+            bool move = false, far = false;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              float p2[2][2];
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                float x = acc[nb][2 * r + c] * (cs[nb][c] * ks[r]);
-                if (bad_keys >> (g + 8 * r) & 1) x = NAN;
-                x = pos[r] < lim[nb][c] ? x : -INFINITY;
-                s[nb][2 * r + c] = x;
-                move |= x > m[nb][c] + kSlack || x + lv[r] > w[nb][c] + kSlack;
+                const float mc = m[nb][c], wc = w[nb][c], mr = mc == -INFINITY ? 0.f : mc, wr = mc == -INFINITY ? 0.f : wc;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const float f = cs[nb][c] * ks[r];
+                  p2[r][c] = ex2(fmaf(acc[nb][2 * r + c], f, none[r] + (lv[r] - wr)));
+                  pl[nb][c][r] = SEL ? ex2(fmaf(acc[nb][2 * r + c], f, none[r] - mr)) : p2[r][c];
+                }
+                // dense: both keys have one value scale, and the weight in the sum is
+                // 2^back of the one that enters the product
+                const float back = wr - lv[0] - mr;
+                if (!SEL) {
+                  pl[nb][c][0] = (pl[nb][c][0] + pl[nb][c][1]) * ex2(back);
+                  pl[nb][c][1] = 0.f;
+                  far |= back > 64.f;
+                }
+                move |= fmaxf(fmaxf(p2[0][c], p2[1][c]), fmaxf(pl[nb][c][0], pl[nb][c][1]) * 0.125f) > 4096.f ||
+                        mc == -INFINITY;
               }
-          if (__any_sync(~0u, move)) {
+#pragma unroll
+              for (int r = 0; r < 2; ++r) pf[nb][r] = float2_to_half2(p2[r][0], p2[r][1]);
+            }
+            if (!__any_sync(~0u, move || far) || anew) {
+              if (!SEL && __any_sync(~0u, far)) {
+                // values so small that their weights may have left fp32's range
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    const float f = cs[nb][c] * ks[0], mr = m[nb][c] == -INFINITY ? 0.f : m[nb][c];
+                    pl[nb][c][0] = ex2(fmaf(acc[nb][c], f, -mr)) + ex2(fmaf(acc[nb][2 + c], f, -mr));
+                  }
+              }
+              break;
+            }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                float a = fmaxf(s[nb][c], s[nb][2 + c]), b = fmaxf(s[nb][c] + lv[0], s[nb][2 + c] + lv[1]);
+                const float s0 = fmaf(acc[nb][c], cs[nb][c] * ks[0], none[0]);
+                const float s1 = fmaf(acc[nb][2 + c], cs[nb][c] * ks[1], none[1]);
+                float a = fmaxf(s0, s1), b = fmaxf(s0 + lv[0], s1 + lv[1]);
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) {
                   a = fmaxf(a, __shfl_xor_sync(~0u, a, x));
@@ -511,22 +566,12 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
                 for (int j = 0; j < MT; ++j) o[j][nb][c] *= fo, o[j][nb][2 + c] *= fo;
               }
           }
-        }
-        uint32_t pf[NB][2];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          float mr[2], wr[2];
+          for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            mr[c] = m[nb][c] == -INFINITY ? 0.f : m[nb][c];
-            wr[c] = w[nb][c] == -INFINITY ? 0.f : w[nb][c];
-          }
+            for (int c = 0; c < 2; ++c) l[nb][c] += pl[nb][c][0] + pl[nb][c][1];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            l[nb][0] += ex2(s[nb][2 * r] - mr[0]);
-            l[nb][1] += ex2(s[nb][2 * r + 1] - mr[1]);
-            pf[nb][r] = transpose8x8(float2_to_half2(ex2(s[nb][2 * r] + (lv[r] - wr[0])),
-                                                     ex2(s[nb][2 * r + 1] + (lv[r] - wr[1]))));
+            for (int r = 0; r < 2; ++r) pf[nb][r] = transpose8x8(pf[nb][r]);
           }
         }
         // ---- O^T += V^T P^T; tile j holds components 4 * VW * g + 2j and + 2j + 1 in rows g and g + 8
@@ -648,92 +693,103 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
       }
     }
   }
+  grid_wait();
 }
 
 }  // namespace
 
-// Join split items: block (c, col) adds the parts of the item that CTA c
-// began, its own first, then the following CTAs' in order.
+// Join split items: a block adds the parts of kJoinCols columns of the item that
+// CTA blockIdx.x of the kernel before began, its own part first, then the
+// following CTAs' in order; WPC warps share a column's parts.
 namespace {
-template <int D>
-__global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int cb) {
+template <int D, int WPC>
+__global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb) {
+  constexpr int kJoinCols = 8 / WPC;
+  grid_wait();
   const int4 d = p.desc[blockIdx.x];
   const int more = d.w & 0xFFFFF, ncols = d.w >> 20;
-  const int col = blockIdx.y;
-  if (more == 0 || col >= ncols) return;
-  __shared__ float acc[4][D];
-  __shared__ float red[4][3];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % WPC;
+  const int col = blockIdx.y * kJoinCols + warp / WPC;
+  if (more == 0 || blockIdx.y * kJoinCols >= ncols) return;
+  __shared__ float acc[8][D];
+  __shared__ float red[8];
+  const bool on = col < ncols;
   const size_t pitch = (size_t)cb * (D + 4);
   auto slot = [&](int i) { return p.slots + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * pitch; };
   float mx = -INFINITY, wx = -INFINITY;
-  for (int i = lane; i <= more; i += 32) {
-    const float *s = slot(i) + cb * D;
-    mx = fmaxf(mx, s[col]);
-    wx = fmaxf(wx, s[cb + col]);
-  }
-#pragma unroll
-  for (int x = 16; x; x >>= 1) {
-    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
-    wx = fmaxf(wx, __shfl_xor_sync(~0u, wx, x));
-  }
   constexpr int E = D / 32;
   float o[E], ls = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i <= more; i += 4) {
-    const float *s = slot(i);
-    const float m = s[cb * D + col], w = s[cb * D + cb + col];
-    ls += s[cb * D + 2 * cb + col] * (m == mx ? 1.f : ex2(m - mx));
-    const float f = w == wx ? 1.f : ex2(w - wx);
+  if (on) {
+    for (int i = lane; i <= more; i += 32) {
+      const float *s = slot(i) + (size_t)cb * D;
+      mx = fmaxf(mx, s[col]);
+      wx = fmaxf(wx, s[cb + col]);
+    }
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += f * s[col * D + lane + 32 * e];
+    for (int x = 16; x; x >>= 1) {
+      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
+      wx = fmaxf(wx, __shfl_xor_sync(~0u, wx, x));
+    }
+#pragma unroll 8
+    for (int i = share; i <= more; i += WPC) {
+      const float *s = slot(i), *t = s + (size_t)cb * D;
+      const float m = t[col], w = t[cb + col];
+      ls += t[2 * cb + col] * (m == mx ? 1.f : ex2(m - mx));
+      const float f = w == wx ? 1.f : ex2(w - wx);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += f * s[(size_t)col * D + lane + 32 * e];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = o[e];
+    if (lane == 0) red[warp] = ls;
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = o[e];
-  if (lane == 0) red[warp][0] = ls;
   __syncthreads();
-  if (warp) return;
-  ls = red[0][0] + red[1][0] + red[2][0] + red[3][0];
+  if (!on || share) return;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int x = lane + 32 * e;
-    acc[0][x] = acc[0][x] + acc[1][x] + acc[2][x] + acc[3][x];
+  for (int k = 1; k < WPC; ++k) {
+    ls += red[warp + k];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] += acc[warp + k][lane + 32 * e];
   }
   __syncwarp();
   const bool sel = d.z < 0;
   const int c = (sel ? -d.z - 1 : d.z) + col;
   const int row = sel ? d.x : d.x + c / p.group, h = d.y * p.group + (sel ? c : c % p.group);
-  finish<D>(p, row, h, lane, acc[0], mx, wx, ls);
+  finish<D>(p, row, h, lane, acc[warp], mx, wx, ls);
 }
 
 template <int D, int NB, bool SEL>
-cudaError_t launch(const AttnParams &p, int ctas, cudaStream_t stream) {
+cudaError_t launch(const AttnParams &p, int ctas, bool follows, cudaStream_t stream) {
   constexpr size_t bytes = sizeof(Smem<D, NB>);
-  auto *k = kv_attn_kernel<D, NB, SEL>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  static DeviceFlags done{0};
+  cudaError_t e = allow_smem(kv_attn_kernel<D, NB, SEL>, bytes, done);
+  if (e == cudaSuccess) e = launch_after(kv_attn_kernel<D, NB, SEL>, dim3(ctas), kAttnThreads, bytes, stream, follows, p);
   if (e != cudaSuccess) return e;
-  k<<<ctas, kAttnThreads, bytes, stream>>>(p);
-  const cudaError_t le = cudaGetLastError();
-  if (le != cudaSuccess) return le;
-  kv_join_kernel<D><<<dim3(ctas, 8 * NB), 128, 0, stream>>>(p, 8 * NB);
-  return cudaGetLastError();
+  return launch_after(kv_join_kernel<D, 4>, dim3(ctas, 4 * NB), 256, 0, stream, true, p, 8 * NB);
 }
 
 template <int D>
-cudaError_t launch_d(const AttnParams &p, int nb, int ctas, cudaStream_t stream) {
+cudaError_t launch_d(const AttnParams &p, int nb, int ctas, bool follows, cudaStream_t stream) {
   const bool sel = p.selected != nullptr;
   switch (nb) {
-    case 1: return sel ? launch<D, 1, true>(p, ctas, stream) : launch<D, 1, false>(p, ctas, stream);
-    case 2: return sel ? launch<D, 2, true>(p, ctas, stream) : launch<D, 2, false>(p, ctas, stream);
-    default: return sel ? launch<D, 4, true>(p, ctas, stream) : launch<D, 4, false>(p, ctas, stream);
+    case 1: return sel ? launch<D, 1, true>(p, ctas, follows, stream) : launch<D, 1, false>(p, ctas, follows, stream);
+    case 2: return sel ? launch<D, 2, true>(p, ctas, follows, stream) : launch<D, 2, false>(p, ctas, follows, stream);
+    case 3: return sel ? launch<D, 3, true>(p, ctas, follows, stream) : launch<D, 3, false>(p, ctas, follows, stream);
+    default: return sel ? launch<D, 4, true>(p, ctas, follows, stream) : launch<D, 4, false>(p, ctas, follows, stream);
   }
 }
 }  // namespace
 
-cudaError_t launch_kv_attention(const AttnParams &p, int nb, int ctas, cudaStream_t stream) {
-  return p.c.dim == 64 ? launch_d<64>(p, nb, ctas, stream) : launch_d<128>(p, nb, ctas, stream);
+cudaError_t launch_kv_attention(const AttnParams &p, int nb, int ctas, bool follows, cudaStream_t stream) {
+  return p.c.dim == 64 ? launch_d<64>(p, nb, ctas, follows, stream) : launch_d<128>(p, nb, ctas, follows, stream);
+}
+
+cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream) {
+  const dim3 grid(ctas, kTiledCols / 8);
+  return p.c.dim == 64 ? launch_after(kv_join_kernel<64, 1>, grid, 256, 0, stream, true, p, kTiledCols)
+                       : launch_after(kv_join_kernel<128, 1>, grid, 256, 0, stream, true, p, kTiledCols);
 }
 
 }  // namespace mqa

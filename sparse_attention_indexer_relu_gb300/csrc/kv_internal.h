@@ -81,7 +81,10 @@ constexpr int kQueryTerms = 3;  // e4m3 terms of an fp16 query value; a bf16 one
 // in boxes of 128 rows; factor: rows * q_heads floats, p.q_scale.
 cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8,
                               float *factor, int ctas, cudaStream_t stream);
-cudaError_t launch_kv_attention(const AttnParams &p, int nb, int ctas, cudaStream_t stream);
+// Its joining pass (p.desc and p.slots are the tiled kernel's).
+cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream);
+// follows: another kernel of the same call is before it on the stream.
+cudaError_t launch_kv_attention(const AttnParams &p, int nb, int ctas, bool follows, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,
                              const int32_t *starts, int rows, int sms, cudaStream_t stream);

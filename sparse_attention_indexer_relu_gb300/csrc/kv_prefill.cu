@@ -852,6 +852,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_prefill_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map,
                       const __grid_constant__ CUtensorMap q_map) {
+  grid_dependents();
   extern __shared__ uint8_t raw[];
   Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -883,6 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   w.at = blockIdx.x * per;
   w.end = min(total, w.at + per);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (w.at >= w.end) grid_wait();
   if (w.at >= w.end) return;  // the whole CTA leaves together
   if (w.at >= before && w.at < before + mine) {
     long long b = before;
@@ -948,6 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (lane == 0) sm.walk[warp] = w;
   __syncwarp();
+  grid_wait();  // the query terms
   // registers: 256 x 192 + 128 x 80 + 128 x 48 = 512 x 128, what the block was launched with
   if (warp < 8) {
     reg_inc<192>();
@@ -966,66 +969,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 12) tmem_dealloc(sm.tmem, 512);
 }
 
-// Join split items: block (c, y) adds the parts of 32 columns of the item that
-// CTA c began; a warp per column in turn.
-template <int D>
-__global__ void __launch_bounds__(256) kv_prefill_join_kernel(const AttnParams p) {
-  const int4 d = p.desc[blockIdx.x];
-  const int more = d.w & 0xFFFFF, ncols = d.w >> 20;
-  if (more == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float acc[8][D];
-  constexpr size_t pitch = (size_t)kCols * (D + 4);
-  auto slot = [&](int i) { return p.slots + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * pitch; };
-  for (int col = blockIdx.y * 32 + warp; col < min(ncols, (int)blockIdx.y * 32 + 32); col += 8) {
-    float mx = -INFINITY, wx = -INFINITY, ls = 0.f, o[D / 32];
-    for (int i = lane; i <= more; i += 32) {
-      const float *s = slot(i) + (size_t)kCols * D;
-      mx = fmaxf(mx, s[col]);
-      wx = fmaxf(wx, s[kCols + col]);
-    }
-#pragma unroll
-    for (int k = 16; k; k >>= 1) {
-      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
-      wx = fmaxf(wx, __shfl_xor_sync(~0u, wx, k));
-    }
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i <= more; ++i) {
-      const float *s = slot(i), *t = s + (size_t)kCols * D;
-      const float m = t[col], w = t[kCols + col];
-      ls += t[2 * kCols + col] * (m == mx ? 1.f : ex2(m - mx));
-      const float f = w == wx ? 1.f : ex2(w - wx);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] += f * s[(size_t)col * D + lane + 32 * e];
-    }
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[warp][lane + 32 * e] = o[e];
-    __syncwarp();
-    const int c = d.z + col;
-    finish<D>(p, d.x + c / p.group, d.y * p.group + c % p.group, lane, acc[warp], mx, wx, ls);
-    __syncwarp();
-  }
-}
-
 // Query terms: D / 8 lanes per (row, head), 8 values each.  Terms go to planes
 // [term][key/value head][row][head of the group][D], factors to [key/value
 // head][row][head of the group].
 template <int D>
-__global__ void __launch_bounds__(256) kv_query_terms_kernel(const AttnParams p, uint8_t *__restrict__ q8,
-                                                            float *__restrict__ factor) {
-  constexpr int LPR = D / 8, PER = 256 / LPR;  // lanes per row, rows per CTA
-  const int part = threadIdx.x % LPR;
-  const long long total = (long long)p.rows * p.q_heads;
-  const int last = min(max(p.starts[p.c.seqs], 0), p.rows);
-  const long long i = (long long)blockIdx.x * PER + threadIdx.x / LPR;
-  const int row = (int)(i / p.q_heads), head = (int)(i % p.q_heads);
-  const bool on = i < total && row < last;  // rows of no sequence are not read
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (on)
-    u = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + (size_t)row * p.q_stride +
-                                              (size_t)head * D + part * 8));
+__device__ __forceinline__ void terms_of(const AttnParams &p, const uint4 u, int i, int last, int total, int part,
+                                         uint8_t *__restrict__ q8, float *__restrict__ factor) {
+  constexpr int LPR = D / 8;
   const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
   float f[8];
   float amax = 0.f;
@@ -1041,12 +991,13 @@ __global__ void __launch_bounds__(256) kv_query_terms_kernel(const AttnParams p,
   }
 #pragma unroll
   for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-  if (!on) return;
+  if (i >= last) return;
   // power of two that brings the largest magnitude to (224, 448]
   int e = 0;
   if (amax > 0.f) e = ((__float_as_uint(amax) & 0x7FFFFFu) > 0x600000u ? 7 : 8) - exponent_of(amax);
   e = max(-110, min(110, e));
   const float up = pow2i(e);
+  const int row = i / p.q_heads, head = i % p.q_heads;
   const size_t at = ((size_t)(head / p.group) * p.rows + row) * p.group + head % p.group;
   if (part == 0) factor[at] = p.scale_log2 * pow2i(-e);
 #pragma unroll
@@ -1067,19 +1018,38 @@ __global__ void __launch_bounds__(256) kv_query_terms_kernel(const AttnParams p,
 }
 
 template <int D>
+__global__ void __launch_bounds__(256) kv_query_terms_kernel(const AttnParams p, uint8_t *__restrict__ q8,
+                                                            float *__restrict__ factor) {
+  grid_dependents();
+  constexpr int LPR = D / 8, PER = 256 / LPR, BATCH = 4;  // lanes per row, rows per CTA and step, steps
+  const int part = threadIdx.x % LPR;
+  const int last = min(max(p.starts[p.c.seqs], 0), p.rows) * p.q_heads;  // rows of no sequence are not read
+  const int total = p.rows * p.q_heads, first = blockIdx.x * PER * BATCH + threadIdx.x / LPR;
+  uint4 u[BATCH];
+#pragma unroll
+  for (int i = 0; i < BATCH; ++i) {
+    const int at = first + i * PER;
+    u[i] = make_uint4(0, 0, 0, 0);
+    if (at < last)
+      u[i] = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) +
+                                                   (size_t)(at / p.q_heads) * p.q_stride +
+                                                   (size_t)(at % p.q_heads) * D + part * 8));
+  }
+#pragma unroll
+  for (int i = 0; i < BATCH; ++i) terms_of<D>(p, u[i], first + i * PER, last, total, part, q8, factor);
+}
+
+template <int D>
 cudaError_t launch(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8, float *factor,
                    int ctas, cudaStream_t stream) {
-  constexpr int bytes = (int)sizeof(Smem<D>) + 1024;
-  auto *k = kv_prefill_kernel<D>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr size_t bytes = sizeof(Smem<D>) + 1024;
+  static DeviceFlags done{0};
+  cudaError_t e = allow_smem(kv_prefill_kernel<D>, bytes, done);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)p.rows * p.q_heads, per = 256 / (D / 8);
-  kv_query_terms_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, stream>>>(p, q8, factor);
-  k<<<ctas, kThreads, bytes, stream>>>(p, map, q_map);
-  const cudaError_t le = cudaGetLastError();
-  if (le != cudaSuccess) return le;
-  kv_prefill_join_kernel<D><<<dim3(ctas, kCols / 32), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  const int rows = p.rows * p.q_heads, per = 4 * 256 / (D / 8);
+  e = launch_after(kv_query_terms_kernel<D>, dim3((rows + per - 1) / per), 256, 0, stream, false, p, q8, factor);
+  if (e != cudaSuccess) return e;
+  return launch_after(kv_prefill_kernel<D>, dim3(ctas), kThreads, bytes, stream, true, p, map, q_map);
 }
 
 }  // namespace

@@ -4,6 +4,7 @@
 #include "kv_internal.h"
 #include "ptx.cuh"
 
+#include <atomic>
 #include <cmath>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -19,8 +20,16 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 // floor(log2 |x|) of a finite nonzero fp32 (subnormals read as -127).
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
-// Scale of a UE8M0 byte: the fp32 with bit pattern e << 23.
-__device__ __forceinline__ float exp_byte(uint32_t e) { return __uint_as_float(e << 23); }
+// Scale of a UE8M0 byte, 1 <= e <= 254: the fp32 with bit pattern e << 23 (0 and
+// 255, which are not scales, read as their neighbours: never 0 or infinity).
+__device__ __forceinline__ float exp_byte(uint32_t e) { return __uint_as_float(min(max(e, 1u), 254u) << 23); }
+
+// Kernels of one call follow each other by programmatic dependent launch: each
+// lets the next one's blocks be scheduled at once, and waits for the one before
+// (its writes included) before it writes anything or reads what that one wrote.
+// Every block waits, so that a kernel's end means its predecessors' end too.
+__device__ __forceinline__ void grid_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // 16 bytes global -> shared without registers; zeros where !ok (nothing is read then).
 __device__ __forceinline__ void cp_async16(void *dst, const void *src, bool ok) {
@@ -97,6 +106,34 @@ __device__ __forceinline__ uint32_t float2_to_bf162(float a, float b) {
   uint32_t w;
   memcpy(&w, &h, 4);
   return w;
+}
+
+template <typename... Params, typename... Args>
+inline cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                bool follows, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &a;
+  cfg.numAttrs = follows ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+// A kernel's dynamic shared memory limit, raised once per device.
+typedef std::atomic<unsigned long long> DeviceFlags;
+template <typename K>
+inline cudaError_t allow_smem(K *kernel, size_t bytes, DeviceFlags &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ULL << dev, std::memory_order_release);
+  return e;
 }
 
 template <int CB, int D>

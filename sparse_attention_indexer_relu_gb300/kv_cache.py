@@ -56,9 +56,14 @@ def _api():
     return m
 
 
+_TYPES = {}
+
+
 def _types():
-    import torch
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    return _TYPES
 
 
 def _dense(t, dtypes, dim, name, device=None):
@@ -71,6 +76,10 @@ def _dense(t, dtypes, dim, name, device=None):
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     return t
+
+
+def _alike(a, b):
+    return (b is not None and a.dtype == b.dtype and a.shape == b.shape and a.device == b.device and a.is_contiguous())
 
 
 class KVCache:
@@ -128,9 +137,18 @@ class KVCache:
             c.extra[i] = _Pool(t.data_ptr(), t.numel() * t.element_size() // pages)
         self._c = c
         self._ref = ctypes.byref(c)
+        self._index = dev.index
 
     def replace(self, **changes):
         """A cache over the same tensors but for the given ones."""
+        if all(n in ("page_table", "seq_lens", "refcounts") and _alike(t, getattr(self, n)) for n, t in changes.items()):
+            other = object.__new__(KVCache)
+            other.__dict__.update(self.__dict__, **changes)
+            other._c = _Cache.from_buffer_copy(self._c)
+            for n, t in changes.items():
+                setattr(other._c, n, t.data_ptr())
+            other._ref = ctypes.byref(other._c)
+            return other
         now = {n: getattr(self, n) for n in ("k", "v", "k_exps", "v_exps", "page_table", "seq_lens", "refcounts",
                                              "scratch", "extra")}
         now.update(changes)
@@ -156,19 +174,38 @@ def alloc_kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int,
                    z(max_seqs, dtype=torch.int32), z(num_pages, dtype=torch.int32), extra=extra)
 
 
-@contextlib.contextmanager
+class _Here:
+    """The usual case of `_on`: the cache's device is current and its current stream is used."""
+
+    __slots__ = ("raw",)
+
+    def __init__(self, raw):
+        self.raw = raw
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *_):
+        return False
+
+
 def _on(cache, stream):
     """The cache's device current, `stream` (default: its current stream) as the stream of what is allocated."""
     import torch
-    if stream is None and torch.cuda.current_device() == cache.device.index:
-        yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        return
+    if stream is None and torch._C._cuda_getDevice() == cache._index:
+        return _Here(torch._C._cuda_getCurrentRawStream(cache._index))
+    return _on_other(cache, stream)
+
+
+@contextlib.contextmanager
+def _on_other(cache, stream):
+    import torch
     with torch.cuda.device(cache.device):
         s = torch.cuda.current_stream() if stream is None else stream
         if s.device != cache.device:
             raise ValueError(f"the stream is on {s.device}, the cache on {cache.device}")
         with torch.cuda.stream(s):
-            yield ctypes.c_void_p(s.cuda_stream)
+            yield s.cuda_stream
 
 
 def _list(t, cache, name, n=None):
