@@ -107,7 +107,7 @@ AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, 
   p.tiled = !selected && cols > kTiledFrom;
   p.split = !p.tiled || c->max_seqs > 1;
   p.nb = cols <= 8 ? 1 : cols <= 16 || p.tiled ? 2 : cols <= 24 ? 3 : 4;
-  p.ctas = sms * attn_ctas_per_sm(p.nb);
+  p.ctas = sms * attn_ctas_per_sm(p.nb, c->head_dim);
   p.slots_off = up256((size_t)p.ctas * sizeof(int4));
   p.tiled_off = up256(p.slots_off + (size_t)p.ctas * 2 * attn_slot_floats(p.nb, c->head_dim) * sizeof(float));
   p.tiled_ctas = sms;
@@ -226,7 +226,12 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
   p.max_cols = P.tiled ? kSplitCols : INT_MAX;
   p.desc = reinterpret_cast<int4 *>(ws);
   p.slots = reinterpret_cast<float *>(ws + P.slots_off);
-  return code(launch_kv_attention(p, P.nb, P.ctas, P.tiled, as_stream(stream)));
+  const uint64_t code_rows = (uint64_t)cache->num_pages * cache->kv_heads * cache->page_size;
+  CUtensorMap k_map, v_map;
+  rc = encode_code_rows(&k_map, cache->k, code_rows, cache->head_dim, selected ? 1 : 16);
+  if (rc == MQA_OK) rc = encode_code_rows(&v_map, cache->v, code_rows, cache->head_dim, selected ? 1 : 16);
+  if (rc != MQA_OK) return rc;
+  return code(launch_kv_attention(p, k_map, v_map, P.nb, P.ctas, P.tiled, as_stream(stream)));
 }
 
 int mqa_kv_reserve(const mqa_kv_cache *cache, const int32_t *counts, void *stream) {

@@ -41,9 +41,10 @@ constexpr int kWarps = kAttnThreads / 32;
 constexpr int kTile = 16 * kWarps;  // keys per unit of work: one 16-key sub-tile per warp
 constexpr int kStages = 3;          // sub-tiles in flight per warp: 2 x 16 warps x 4 KB ahead on an SM
 
-template <int NB>
+// CTAs per SM: what its registers allow without spilling in the loop.
+template <int D, int NB>
 struct Cfg {
-  static constexpr int ctas = NB == 1 ? 4 : NB == 2 ? 3 : 2;
+  static constexpr int ctas = D == 64 ? (NB == 1 ? 5 : NB <= 3 ? 3 : 2) : (NB == 1 ? 4 : NB == 2 ? 3 : 2);
 };
 
 template <int D>
@@ -56,19 +57,22 @@ struct Meta {
   float ks[kStages][16];
   float lv[kStages][16];
   int pos[kStages][16];
+  int any[kStages];
 };
 
 template <int D, int NB>
 struct Smem {
   union {
-    uint8_t ring[kWarps][kStages][2 * 16 * D];
+    uint8_t ring[kWarps][kStages][2 * 16 * D];  // 16 rows of keys, 16 of values
     float merge[8 * NB][D + 4];
   };
   Meta meta[kWarps];
+  uint64_t full[kWarps][kStages];
+  int dead;                     // a wait has run out
   float cs[8 * NB];             // per column: scale * log2(e) / (power of two q was multiplied with)
   int lim[8 * NB];              // positions the column sees: [0, lim)
   float wm[kWarps][8 * NB], ww[kWarps][8 * NB], wl[kWarps][8 * NB];
-  uint32_t qf[NB > 2 ? NB : 1][D / 8][32];  // q fragments (NB > 2)
+  uint4 qf[NB][D / 32][32];     // q fragments
   long long scan[kWarps];
   int found[2];
   long long found_at;
@@ -81,7 +85,10 @@ struct Item {
 
 }  // namespace
 
-int attn_ctas_per_sm(int nb) { return nb == 1 ? Cfg<1>::ctas : nb == 2 ? Cfg<2>::ctas : nb == 3 ? Cfg<3>::ctas : Cfg<4>::ctas; }
+int attn_ctas_per_sm(int nb, int dim) {
+  if (dim == 64) return nb == 1 ? Cfg<64, 1>::ctas : nb == 2 ? Cfg<64, 2>::ctas : nb == 3 ? Cfg<64, 3>::ctas : Cfg<64, 4>::ctas;
+  return nb == 1 ? Cfg<128, 1>::ctas : nb == 2 ? Cfg<128, 2>::ctas : nb == 3 ? Cfg<128, 3>::ctas : Cfg<128, 4>::ctas;
+}
 size_t attn_slot_floats(int nb, int dim) { return (size_t)8 * nb * (dim + 4); }
 
 namespace {
@@ -101,12 +108,35 @@ __device__ __forceinline__ uint32_t cvt2_hi(uint32_t w) {
 // Bytes of w that hold a NaN code (0x7F or 0xFF), as 0x80 bits.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
+// Wait for a warp's copies; once a wait has run out (2 s) the CTA's waits return
+// at once, and it runs to its end on what it finds.
+template <typename S>
+__device__ __forceinline__ void wait_full(S &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
+  if (mbar_try_wait(bar, parity)) return;
+  unsigned long long t0 = 0;
+  for (int i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((i & 15) == 15) {
+      if (*reinterpret_cast<volatile int *>(&sm.dead)) return;
+      const unsigned long long now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > 2000000000ULL) {
+        *reinterpret_cast<volatile int *>(&sm.dead) = 1;
+        atomicOr(status, MQA_KV_DEV_WAIT_TIMEOUT);
+        return;
+      }
+    }
+  }
+}
+
 template <int D, int NB, bool SEL>
-__global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
+    kv_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap k_map,
+                   const __grid_constant__ CUtensorMap v_map) {
   grid_dependents();
-  extern __shared__ __align__(128) uint8_t smem_raw[];
+  extern __shared__ uint8_t smem_raw[];
   using S = Smem<D, NB>;
-  S &sm = *reinterpret_cast<S *>(smem_raw);
+  S &sm = *reinterpret_cast<S *>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   constexpr int CB = 8 * NB;
   constexpr int KW = D / 16;   // words of a K row per lane (8 or 4)
   constexpr int VW = D / 32;   // words of a V row per lane (4 or 2)
@@ -116,6 +146,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
   const int nsel_tiles = SEL ? max(1, (p.n_selected + kTile - 1) / kTile) : 1;
   const int ncb_sel = (group + CB - 1) / CB;
 
+  const uint64_t policy = policy_evict_first();  // every key is read once, or few times
   // ---- this CTA's range of the line of work
   // sequence s: rows [r0, r1), length; units = heads * column blocks * tiles
   auto rows_of = [&](int s, int &r0, int &n) {
@@ -166,6 +197,12 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (at >= end) grid_wait();
   if (at >= end) return;  // the whole CTA leaves together
+  if (tid == 0) {
+    sm.dead = 0;
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&sm.full[0][0] + i, 1);
+    fence_mbar_init();
+  }
+  uint32_t copies = 0;  // sub-tiles whose copies this warp has issued, in all segments
   Item it;
   int tile;  // first tile of the current segment
   if (SEL) {
@@ -222,9 +259,10 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
     const int c0 = it.cb * CB;                          // first column of the block
     const int ncols = min(CB, (SEL ? group : n * group) - c0);
     if (tid == 0 && p.c.lens[seq] != len) atomicOr(p.c.status, MQA_KV_DEV_BAD_LENGTH);
-    __syncthreads();  // the previous segment's readers of cs / lim / merge are done
+    fence_async_smem();  // copies into what was read and written with ordinary accesses
+    __syncthreads();     // the previous segment's readers of cs / lim / merge are done
     if (tid < CB) {
-      int lim = 0;
+      int lim = SEL ? 0 : INT32_MAX;  // columns behind the last take part like the others (a query of zeros)
       if (tid < ncols) {
         const int i = SEL ? it.seq - r0 : (c0 + tid) / group;
         lim = p.causal ? min(max(len - n + i + 1, 0), len) : len;
@@ -236,15 +274,14 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
     int lim_max = 0, lim_min = INT32_MAX;
 #pragma unroll
     for (int i = 0; i < CB; ++i) {
-      lim_max = max(lim_max, sm.lim[i]);
+      lim_max = max(lim_max, i < ncols ? sm.lim[i] : 0);
       lim_min = min(lim_min, i < ncols ? sm.lim[i] : INT32_MAX);
     }
     // ---- q: column g of each 8-column block, the lane's components
     // k-step j: b0 = components KW*4*t + 4j, +1; b1 = +2, +3 (t's 4*KW bytes of a key row)
-    uint32_t qr[NB > 2 ? 1 : NB][2 * KW];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      if (NB > 2 && (nb & (kWarps - 1)) != warp) continue;  // shared through memory: one warp loads it
+      if (nb % kWarps != warp) continue;  // one warp loads a block for all
       const int col = nb * 8 + g;
       float f[4 * KW];
       float amax = 0.f;
@@ -277,24 +314,25 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
       if (amax > 0.f && amax <= FLT_MAX) e = 10 - exponent_of(amax);
       e = max(-100, min(100, e));
       const float up = pow2i(e);
-      if (t == 0) sm.cs[col] = p.scale_log2 * pow2i(-e);  // every warp writes the same value
+      if (t == 0) sm.cs[col] = p.scale_log2 * pow2i(-e);
 #pragma unroll
       for (int j = 0; j < 2 * KW; ++j) {
         const uint32_t h2 = float2_to_half2(f[2 * j] * up, f[2 * j + 1] * up);
-        if (NB > 2) sm.qf[NB > 2 ? nb : 0][j][lane] = h2;
-        else qr[NB > 2 ? 0 : nb][j] = h2;
+        reinterpret_cast<uint32_t *>(&sm.qf[nb][j >> 2][lane])[j & 3] = h2;
       }
     }
     __syncthreads();
+    uint4 qr[KW / 2];  // 8 columns: in registers; more are read with each sub-tile
+    if (NB == 1) {
+#pragma unroll
+      for (int j = 0; j < KW / 2; ++j) qr[j] = sm.qf[0][j][lane];
+    }
     float cs[NB][2];
-    int lim[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         cs[nb][c] = sm.cs[nb * 8 + 2 * t + c];
-        // columns behind the last take part like the others (a query of zeros)
-        lim[nb][c] = nb * 8 + 2 * t + c < ncols ? sm.lim[nb * 8 + 2 * t + c] : lim_max;
       }
     const int32_t *sel = SEL ? p.selected + (size_t)it.seq * p.n_selected : nullptr;
 
@@ -319,21 +357,19 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[j][nb][i] = 0.f;
 
-      // ---- loads.  Rows of D bytes; 16-byte chunks exchanged within 128 bytes
-      // so that both products' reads spread over the banks.
-      // Dense: lane j holds sub-tile it + j's first row, scale and exponent.
+      // ---- loads: TMA, 16 rows of keys and of values per sub-tile, the 16-byte
+      // chunks of a row exchanged by the copy's swizzle, so that both products'
+      // reads spread over the banks.  Nothing is computed from a loaded index
+      // before the refresh after the one that loaded it.
+      // Dense: lane j holds sub-tile i + j's first row and exponents.
       int d_row = -1;
-      float d_ks = 0.f, d_lv = 0.f;
-      // Selected: a chain three refreshes deep (position, page, exponents), 32 keys each.
-      int s_pos0 = -1, s_pos1 = -1, s_pos2 = -1, s_pos = -1;
-      int s_pg1 = -1, s_row2 = -1, s_row = -1;
-      uint32_t s_e2 = 0;
+      // Selected: 32 entries per refresh (two sub-tiles): position, page, exponents.
+      int s_raw = -1, s_pos1 = -1, s_pg1 = -1, s_pos2 = -1, s_row2 = -1, s_pos = -1, s_row = -1;
+      uint32_t ke = 127, ve = 127;
       float s_ks = 0.f, s_lv = 0.f;
-      auto load_pos = [&](int i) -> int {  // position of the lane's key among sub-tiles i, i + 1
+      auto load_raw = [&](int i) {  // the lane's entry among sub-tiles i, i + 1
         const int k = (t0 + i + (lane >> 4)) * kTile + warp * 16 + (lane & 15);
-        if (i + (lane >> 4) >= iters || k >= p.n_selected) return -1;
-        const int x = __ldg(sel + k);
-        return (unsigned)x < (unsigned)lim_max ? x : -1;
+        s_raw = i + (lane >> 4) < iters && k < p.n_selected ? __ldg(sel + k) : -1;
       };
       auto load_page = [&](int pos) -> int { return pos < 0 ? -1 : __ldg(table + (pos >> p.c.page_log2)); };
       auto row_of = [&](int pos, int pg) -> int {
@@ -344,73 +380,86 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
         }
         return ((pg * heads + it.head) << p.c.page_log2) + (pos & (p.c.page - 1));
       };
-      auto load_exps = [&](int row) -> uint32_t {
-        if (row < 0) return 127u | 127u << 8;
+      auto load_exps = [&](int row) {
+        if (row < 0) return;
         const int ph = row >> p.c.page_log2;
-        return (uint32_t)__ldg(p.c.k_exps + ph) | (uint32_t)__ldg(p.c.v_exps + ph) << 8;
+        ke = __ldg(p.c.k_exps + ph);
+        ve = __ldg(p.c.v_exps + ph);
       };
-      auto refresh_sel = [&](int i) {  // sub-tiles i, i + 1 become current
+      auto step_sel = [&](int i) {  // entries of sub-tile i enter the chain
         s_pos = s_pos2, s_row = s_row2;
-        s_ks = exp_byte(s_e2 & 255u), s_lv = (float)(int)(s_e2 >> 8) - 127.f;
-        s_pos2 = s_pos1, s_row2 = row_of(s_pos1, s_pg1), s_e2 = load_exps(s_row2);
-        s_pos1 = s_pos0, s_pg1 = load_page(s_pos0);
-        s_pos0 = load_pos(i + 6);
+        s_ks = exp_byte(ke), s_lv = (float)(int)ve - 127.f;
+        s_pos2 = s_pos1, s_row2 = row_of(s_pos1, s_pg1), load_exps(s_row2);
+        s_pos1 = (unsigned)s_raw < (unsigned)lim_max ? s_raw : -1, s_pg1 = load_page(s_pos1);
+        load_raw(i);
       };
       if (SEL) {
-        s_pos0 = load_pos(0);
-        s_pos1 = s_pos0, s_pg1 = load_page(s_pos0), s_pos0 = load_pos(2);
-        s_pos2 = s_pos1, s_row2 = row_of(s_pos1, s_pg1), s_e2 = load_exps(s_row2);
-        s_pos1 = s_pos0, s_pg1 = load_page(s_pos0), s_pos0 = load_pos(4);
+        step_sel(0);
+        step_sel(2);
+        step_sel(4);
       }
       auto issue = [&](int i) {
-        if (i < iters) {
-          const int stage = i % kStages;
-          const int base = (t0 + i) * kTile + warp * 16;
-          if (SEL) {
-            if ((i & 1) == 0) refresh_sel(i);
-            if ((lane >> 4) == (i & 1)) {
-              meta.ks[stage][lane & 15] = s_ks;
-              meta.lv[stage][lane & 15] = s_lv;
-              meta.pos[stage][lane & 15] = s_row < 0 ? INT32_MAX : s_pos;
-            }
-          } else {
-            if ((i & 31) == 0) {
-              const int pos = base + lane * kTile;
-              const bool want = i + lane < iters && pos < lim_max;
-              d_row = want ? row_of(pos, load_page(pos)) : -1;
-              const uint32_t e = load_exps(d_row);
-              d_ks = exp_byte(e & 255u), d_lv = (float)(int)(e >> 8) - 127.f;
-            }
-            if (lane == (i & 31)) {
-              meta.ks[stage][0] = d_ks;
-              meta.lv[stage][0] = d_lv;
-              meta.pos[stage][0] = d_row < 0 ? INT32_MAX - 64 : base;
-            }
+        if (i >= iters) return;
+        const uint32_t no = copies++;
+        const int stage = no % kStages;
+        const int base = (t0 + i) * kTile + warp * 16;
+        uint64_t *bar = &sm.full[warp][stage];
+        uint8_t *kd = sm.ring[warp][stage], *vd = kd + 16 * D;
+        if (SEL) {
+          if ((i & 1) == 0) step_sel(i + 6);
+          const int half = 16 * (i & 1);
+          const uint32_t ok = __ballot_sync(~0u, s_row >= 0) >> half & 0xFFFFu;
+          if ((lane >> 4) == (i & 1)) {
+            meta.ks[stage][lane & 15] = s_ks;
+            meta.lv[stage][lane & 15] = s_lv;
+            meta.pos[stage][lane & 15] = s_row < 0 ? INT32_MAX : s_pos;
           }
-          const int first = SEL ? 0 : __shfl_sync(~0u, d_row, i & 31);
-          constexpr int CH = D / 16;  // chunks per row
-          uint8_t *kd = sm.ring[warp][stage], *vd = kd + 16 * D;
+          // entries that name no visible key take the row of one that does
+          const int some = __shfl_sync(~0u, s_row, half + (ok ? __ffs(ok) - 1 : 0));
+          const int mine = s_row < 0 ? some : s_row;
+          int y[4];
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            const int id = c * 32 + lane, r = id / CH, ch = id % CH;
-            const int row = SEL ? __shfl_sync(~0u, s_row, r + 16 * (i & 1)) : first + r;
-            const bool ok = SEL ? row >= 0 : first >= 0 && base + r < lim_max;
-            const size_t src = ok ? (size_t)row * D + ch * 16 : 0;
-            const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
-            const int dst = r * D + ((ch ^ sw) << 4);
-            cp_async16(kd + dst, p.c.k + src, ok);
-            cp_async16(vd + dst, p.c.v + src, ok);
+          for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(~0u, mine, half + 4 * (lane & 3) + k);
+          if (lane == 0) mbar_arrive_expect_tx(bar, ok ? 2 * 16 * D : 0);
+          if (lane == 0) meta.any[stage] = ok != 0;
+          __syncwarp();
+          if (ok && lane < 8)
+            tma_gather4((lane < 4 ? kd : vd) + (lane & 3) * 4 * D, lane < 4 ? &k_map : &v_map, bar, y);
+        } else {
+          if ((i & 31) == 0) {
+            const int pos = base + lane * kTile;
+            const bool want = i + lane < iters && pos < lim_max;
+            d_row = want ? row_of(pos, load_page(pos)) : -1;
+            load_exps(d_row);
+          }
+          if (lane == (i & 31)) {
+            meta.ks[stage][0] = exp_byte(ke);
+            meta.lv[stage][0] = (float)(int)ve - 127.f;
+            meta.any[stage] = d_row >= 0;
+          }
+          const int row = __shfl_sync(~0u, d_row, i & 31);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, row >= 0 ? 2 * 16 * D : 0);
+            if (row >= 0) {
+              tma_load_2d(kd, &k_map, bar, 0, row, policy);
+              tma_load_2d(vd, &v_map, bar, 0, row, policy);
+            }
           }
         }
-        cp_async_commit();
       };
+      uint32_t done = copies;  // sub-tiles worked on
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-      for (int i = 0; i < iters; ++i) {
-        cp_async_wait<kStages - 2>();
+      for (int i = 0; i < iters; ++i, ++done) {
+        const int stage = done % kStages;
+        wait_full(sm, &sm.full[warp][stage], done / kStages & 1, p.c.status);
         __syncwarp();
-        const int stage = i % kStages;
+        if (!meta.any[stage]) {  // no key of the sub-tile is seen
+          __syncwarp();
+          issue(i + kStages - 1);
+          continue;
+        }
         const uint8_t *kd = sm.ring[warp][stage], *vd = kd + 16 * D;
         // ---- S^T = K Q^T
         float acc[NB][4];
@@ -429,16 +478,14 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
           kb[4 * h] = y.x, kb[4 * h + 1] = y.y, kb[4 * h + 2] = y.z, kb[4 * h + 3] = y.w;
         }
 #pragma unroll
-        for (int j = 0; j < KW; ++j) {
+        for (int j = 0; j < KW; j += 2) {
           const uint32_t a[4] = {cvt2(ka[j]), cvt2(kb[j]), cvt2_hi(ka[j]), cvt2_hi(kb[j])};
+          const uint32_t b[4] = {cvt2(ka[j + 1]), cvt2(kb[j + 1]), cvt2_hi(ka[j + 1]), cvt2_hi(kb[j + 1])};
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            if (NB > 2) {
-              const uint32_t b0 = sm.qf[NB > 2 ? nb : 0][2 * j][lane], b1 = sm.qf[NB > 2 ? nb : 0][2 * j + 1][lane];
-              mma_f16(acc[nb], a, b0, b1);
-            } else {
-              mma_f16(acc[nb], a, qr[NB > 2 ? 0 : nb][2 * j], qr[NB > 2 ? 0 : nb][2 * j + 1]);
-            }
+            const uint4 q = NB == 1 ? qr[j / 2] : sm.qf[nb][j / 2][lane];
+            mma_f16(acc[nb], a, q.x, q.y);
+            mma_f16(acc[nb], b, q.z, q.w);
           }
         }
         // ---- V words: keys 2t, 2t + 1, 2t + 8, 2t + 9, components 4 * VW * g ...
@@ -478,7 +525,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
           int room[2];  // by how much a column's limit lies behind the key
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int k = SEL ? g + 8 * r : 0, pos = meta.pos[stage][k];
+            const int k = SEL ? g + 8 * r : 0, pos = SEL ? meta.pos[stage][k] : (t0 + i) * kTile + warp * 16;
             ks[r] = meta.ks[stage][k];
             lv[r] = meta.lv[stage][k];
             none[r] = SEL && pos == INT32_MAX ? -INFINITY : 0.f;  // an entry that names no visible key
@@ -493,7 +540,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
                   for (int nb = 0; nb < NB; ++nb) acc[nb][2 * r] = acc[nb][2 * r + 1] = NAN;
                 }
             }
-          } else if (bad_keys || __shfl_sync(~0u, room[0], 0) + 16 > lim_min) {
+          } else if (bad_keys || (t0 + i) * kTile + warp * 16 + 16 > lim_min) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -502,7 +549,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
                 for (int c = 0; c < 2; ++c) {
                   if (bad_keys >> (g + 8 * r) & 1) acc[nb][2 * r + c] = NAN;
                   // (scales are positive: -inf stays -inf)
-                  if (room[r] >= lim[nb][c]) acc[nb][2 * r + c] = -INFINITY;
+                  if (room[r] >= min(sm.lim[nb * 8 + 2 * t + c], lim_max)) acc[nb][2 * r + c] = -INFINITY;
                 }
           }
           for (bool anew = false;; anew = true) {
@@ -590,7 +637,6 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<NB>::ctas) kv_attn_kernel(co
         __syncwarp();
         issue(i + kStages - 1);
       }
-      cp_async_wait<0>();
       bool bad = false;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
@@ -760,30 +806,41 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb
   finish<D>(p, row, h, lane, acc[warp], mx, wx, ls);
 }
 
-template <int D, int NB, bool SEL>
-cudaError_t launch(const AttnParams &p, int ctas, bool follows, cudaStream_t stream) {
-  constexpr size_t bytes = sizeof(Smem<D, NB>);
-  static DeviceFlags done{0};
-  cudaError_t e = allow_smem(kv_attn_kernel<D, NB, SEL>, bytes, done);
-  if (e == cudaSuccess) e = launch_after(kv_attn_kernel<D, NB, SEL>, dim3(ctas), kAttnThreads, bytes, stream, follows, p);
+template <int D, int NB>
+cudaError_t launch(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int ctas, bool follows,
+                   cudaStream_t stream) {
+  constexpr size_t bytes = sizeof(Smem<D, NB>) + 1024;
+  static DeviceFlags done[2];
+  cudaError_t e;
+  if (p.selected) {
+    e = allow_smem(kv_attn_kernel<D, NB, true>, bytes, done[0]);
+    if (e == cudaSuccess)
+      e = launch_after(kv_attn_kernel<D, NB, true>, dim3(ctas), kAttnThreads, bytes, stream, follows, p, k_map, v_map);
+  } else {
+    e = allow_smem(kv_attn_kernel<D, NB, false>, bytes, done[1]);
+    if (e == cudaSuccess)
+      e = launch_after(kv_attn_kernel<D, NB, false>, dim3(ctas), kAttnThreads, bytes, stream, follows, p, k_map, v_map);
+  }
   if (e != cudaSuccess) return e;
   return launch_after(kv_join_kernel<D, 4>, dim3(ctas, 4 * NB), 256, 0, stream, true, p, 8 * NB);
 }
 
 template <int D>
-cudaError_t launch_d(const AttnParams &p, int nb, int ctas, bool follows, cudaStream_t stream) {
-  const bool sel = p.selected != nullptr;
+cudaError_t launch_d(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int nb, int ctas,
+                     bool follows, cudaStream_t stream) {
   switch (nb) {
-    case 1: return sel ? launch<D, 1, true>(p, ctas, follows, stream) : launch<D, 1, false>(p, ctas, follows, stream);
-    case 2: return sel ? launch<D, 2, true>(p, ctas, follows, stream) : launch<D, 2, false>(p, ctas, follows, stream);
-    case 3: return sel ? launch<D, 3, true>(p, ctas, follows, stream) : launch<D, 3, false>(p, ctas, follows, stream);
-    default: return sel ? launch<D, 4, true>(p, ctas, follows, stream) : launch<D, 4, false>(p, ctas, follows, stream);
+    case 1: return launch<D, 1>(p, k_map, v_map, ctas, follows, stream);
+    case 2: return launch<D, 2>(p, k_map, v_map, ctas, follows, stream);
+    case 3: return launch<D, 3>(p, k_map, v_map, ctas, follows, stream);
+    default: return launch<D, 4>(p, k_map, v_map, ctas, follows, stream);
   }
 }
 }  // namespace
 
-cudaError_t launch_kv_attention(const AttnParams &p, int nb, int ctas, bool follows, cudaStream_t stream) {
-  return p.c.dim == 64 ? launch_d<64>(p, nb, ctas, follows, stream) : launch_d<128>(p, nb, ctas, follows, stream);
+cudaError_t launch_kv_attention(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int nb,
+                                int ctas, bool follows, cudaStream_t stream) {
+  return p.c.dim == 64 ? launch_d<64>(p, k_map, v_map, nb, ctas, follows, stream)
+                       : launch_d<128>(p, k_map, v_map, nb, ctas, follows, stream);
 }
 
 cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream) {

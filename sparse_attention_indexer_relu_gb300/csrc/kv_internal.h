@@ -69,7 +69,7 @@ struct AttnParams {
 
 // Column block sizes (8 * NB) of the split kernel, its CTAs per SM and threads.
 constexpr int kAttnThreads = 128;
-int attn_ctas_per_sm(int nb);
+int attn_ctas_per_sm(int nb, int dim);
 size_t attn_slot_floats(int nb, int dim);
 // Columns per item of the tiled kernel (p.max_cols: it takes the sequences of
 // more columns), and the fewest key tiles a CTA's part holds.
@@ -84,7 +84,10 @@ cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, const
 // Its joining pass (p.desc and p.slots are the tiled kernel's).
 cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream);
 // follows: another kernel of the same call is before it on the stream.
-cudaError_t launch_kv_attention(const AttnParams &p, int nb, int ctas, bool follows, cudaStream_t stream);
+// k_map, v_map: codes as rows of head_dim bytes, boxes of 16 rows (selected
+// keys: of one).
+cudaError_t launch_kv_attention(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int nb,
+                                int ctas, bool follows, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,
                              const int32_t *starts, int rows, int sms, cudaStream_t stream);

@@ -254,7 +254,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
