@@ -228,9 +228,13 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
   p.slots = reinterpret_cast<float *>(ws + P.slots_off);
   const uint64_t code_rows = (uint64_t)cache->num_pages * cache->kv_heads * cache->page_size;
   CUtensorMap k_map, v_map;
-  rc = encode_code_rows(&k_map, cache->k, code_rows, cache->head_dim, selected ? 1 : 16);
-  if (rc == MQA_OK) rc = encode_code_rows(&v_map, cache->v, code_rows, cache->head_dim, selected ? 1 : 16);
-  if (rc != MQA_OK) return rc;
+  std::memset(&k_map, 0, sizeof k_map);
+  std::memset(&v_map, 0, sizeof v_map);
+  if (!selected) {
+    rc = encode_code_rows(&k_map, cache->k, code_rows, cache->head_dim, 16);
+    if (rc == MQA_OK) rc = encode_code_rows(&v_map, cache->v, code_rows, cache->head_dim, 16);
+    if (rc != MQA_OK) return rc;
+  }
   return code(launch_kv_attention(p, k_map, v_map, P.nb, P.ctas, P.tiled, as_stream(stream)));
 }
 

@@ -21,17 +21,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kMaxRows = 16;  // rows a CTA looks at
 
-// Four fp32 to four e4m3 codes (nearest even, saturating, NaN kept).
-__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
-  uint32_t lo, hi;
-  asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tmov.b32 %0, {x, 0};\n\t}"
-      : "=r"(lo)
-      : "f"(a), "f"(b));
-  asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tmov.b32 %0, {x, 0};\n\t}"
-      : "=r"(hi)
-      : "f"(c), "f"(d));
-  return lo | hi << 16;
-}
 __device__ __forceinline__ float from_e4m3(uint32_t code) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);
   return __half2float(__half(h));

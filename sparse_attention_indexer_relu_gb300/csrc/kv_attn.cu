@@ -64,7 +64,7 @@ template <int D, int NB>
 struct Smem {
   union {
     uint8_t ring[kWarps][kStages][2 * 16 * D];  // 16 rows of keys, 16 of values
-    float merge[8 * NB][D + 4];
+    float merge[kWarps][8 * (NB < 2 ? NB : 2)][D + 4];
   };
   Meta meta[kWarps];
   uint64_t full[kWarps][kStages];
@@ -92,21 +92,6 @@ int attn_ctas_per_sm(int nb, int dim) {
 size_t attn_slot_floats(int nb, int dim) { return (size_t)8 * nb * (dim + 4); }
 
 namespace {
-
-// e4m3 code pair (low 16 bits) to fp16 pair.
-__device__ __forceinline__ uint32_t cvt2(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t cvt2_hi(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-
-// Bytes of w that hold a NaN code (0x7F or 0xFF), as 0x80 bits.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 // Wait for a warp's copies; once a wait has run out (2 s) the CTA's waits return
 // at once, and it runs to its end on what it finds.
@@ -277,6 +262,113 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
       lim_max = max(lim_max, i < ncols ? sm.lim[i] : 0);
       lim_min = min(lim_min, i < ncols ? sm.lim[i] : INT32_MAX);
     }
+    const int32_t *sel = SEL ? p.selected + (size_t)it.seq * p.n_selected : nullptr;
+    // the tiles this item needs: later ones hold no key that a column sees
+    const int t1e = SEL ? t1 : min(t1, (lim_max + kTile - 1) / kTile);
+    const int iters = max(0, t1e - t0);
+    // ---- loads, 16 rows of keys and of values per sub-tile, the 16-byte chunks
+    // of a row exchanged so that both products' reads spread over the banks:
+    // whole rows by TMA, whose swizzle is the same, selected ones 16 bytes per
+    // lane (as TMA gathers, 8 instructions of one lane each, they held their
+    // warp up for 1,200 cycles).  Nothing is computed from a loaded index
+    // before the refresh after the one that loaded it.
+    // Dense: lane j holds sub-tile i + j's first row and exponents.
+    int d_row = -1;
+    // Selected: 32 entries per refresh (two sub-tiles): position, page, exponents.
+    int s_raw = -1, s_pos1 = -1, s_pg1 = -1, s_pos2 = -1, s_row2 = -1, s_pos = -1, s_row = -1;
+    uint32_t ke = 127, ve = 127;
+    float s_ks = 0.f, s_lv = 0.f;
+    auto load_raw = [&](int i) {  // the lane's entry among sub-tiles i, i + 1
+      const int k = (t0 + i + (lane >> 4)) * kTile + warp * 16 + (lane & 15);
+      s_raw = i + (lane >> 4) < iters && k < p.n_selected ? __ldg(sel + k) : -1;
+    };
+    auto load_page = [&](int pos) -> int { return pos < 0 ? -1 : __ldg(table + (pos >> p.c.page_log2)); };
+    auto row_of = [&](int pos, int pg) -> int {
+      if (pos < 0) return -1;
+      if ((unsigned)pg >= (unsigned)p.c.pages) {
+        atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
+        return -1;
+      }
+      return ((pg * heads + it.head) << p.c.page_log2) + (pos & (p.c.page - 1));
+    };
+    auto load_exps = [&](int row) {
+      if (row < 0) return;
+      const int ph = row >> p.c.page_log2;
+      ke = __ldg(p.c.k_exps + ph);
+      ve = __ldg(p.c.v_exps + ph);
+    };
+    auto step_sel = [&](int i) {  // entries of sub-tile i enter the chain
+      s_pos = s_pos2, s_row = s_row2;
+      s_ks = exp_byte(ke), s_lv = (float)(int)ve - 127.f;
+      s_pos2 = s_pos1, s_row2 = row_of(s_pos1, s_pg1), load_exps(s_row2);
+      s_pos1 = (unsigned)s_raw < (unsigned)lim_max ? s_raw : -1, s_pg1 = load_page(s_pos1);
+      load_raw(i);
+    };
+    // the first indices are on their way while the queries are turned into terms
+    auto begin = [&] {
+      if (SEL) {
+        step_sel(0);
+        step_sel(2);
+        step_sel(4);
+      }
+    };
+    begin();
+    auto issue = [&](int i) {
+      if (i >= iters) {
+        if (SEL) cp_async_commit();
+        return;
+      }
+      const uint32_t no = copies++;
+      const int stage = no % kStages;
+      const int base = (t0 + i) * kTile + warp * 16;
+      uint64_t *bar = &sm.full[warp][stage];
+      uint8_t *kd = sm.ring[warp][stage], *vd = kd + 16 * D;
+      if (SEL) {
+        if ((i & 1) == 0) step_sel(i + 6);
+        const int half = 16 * (i & 1);
+        const uint32_t ok = __ballot_sync(~0u, s_row >= 0) >> half & 0xFFFFu;
+        if ((lane >> 4) == (i & 1)) {
+          meta.ks[stage][lane & 15] = s_ks;
+          meta.lv[stage][lane & 15] = s_lv;
+          meta.pos[stage][lane & 15] = s_row < 0 ? INT32_MAX : s_pos;
+        }
+        if (lane == 0) meta.any[stage] = ok != 0;
+        constexpr int CH = D / 16;  // chunks per row
+        const int ch = lane % CH, rl = lane / CH;
+        if (ok) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const int r = c * (32 / CH) + rl;
+            const int row = __shfl_sync(~0u, s_row, half + r);
+            const size_t src = (size_t)(unsigned)max(row, 0) * D + ch * 16;
+            const int dst = r * D + ((ch ^ (D == 128 ? r & 7 : r >> 1 & 3)) << 4);
+            cp_async16(kd + dst, p.c.k + src, row >= 0);  // zeros for entries that name no visible key
+            cp_async16(vd + dst, p.c.v + src, row >= 0);
+          }
+        }
+        cp_async_commit();
+      } else {
+        if ((i & 31) == 0) {
+          const int pos = base + lane * kTile;
+          const bool want = i + lane < iters && pos < lim_max;
+          d_row = want ? row_of(pos, load_page(pos)) : -1;
+          load_exps(d_row);
+        }
+        if (lane == (i & 31)) {
+          meta.ks[stage][0] = exp_byte(ke);
+          meta.lv[stage][0] = (float)(int)ve - 127.f;
+          meta.any[stage] = d_row >= 0;
+        }
+        const int row = __shfl_sync(~0u, d_row, i & 31);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, row >= 0 ? 2 * 16 * D : 0);
+          if (row >= 0) {
+            tma_load_2d(kd, &k_map, bar, 0, row, policy);
+            tma_load_2d(vd, &v_map, bar, 0, row, policy);
+          }
+        }
+      }
+    };
     // ---- q: column g of each 8-column block, the lane's components
     // k-step j: b0 = components KW*4*t + 4j, +1; b1 = +2, +3 (t's 4*KW bytes of a key row)
 #pragma unroll
@@ -306,20 +398,23 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
         for (int j = 0; j < 4 * KW; ++j) f[j] = 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < 4 * KW; ++j) amax = fmaxf(amax, fabsf(f[j]));
+      for (int j = 0; j < 4 * KW; ++j) {
+        if (!(fabsf(f[j]) <= FLT_MAX)) f[j] = NAN;  // infinities too: no softmax of theirs is a number
+        amax = fmaxf(amax, fabsf(f[j]));
+      }
       amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
       // power of two that brings the column's largest magnitude to [2^10, 2^11)
       int e = 0;
-      if (amax > 0.f && amax <= FLT_MAX) e = 10 - exponent_of(amax);
+      if (amax > 0.f) e = 10 - exponent_of(amax);
       e = max(-100, min(100, e));
       const float up = pow2i(e);
       if (t == 0) sm.cs[col] = p.scale_log2 * pow2i(-e);
 #pragma unroll
-      for (int j = 0; j < 2 * KW; ++j) {
-        const uint32_t h2 = float2_to_half2(f[2 * j] * up, f[2 * j + 1] * up);
-        reinterpret_cast<uint32_t *>(&sm.qf[nb][j >> 2][lane])[j & 3] = h2;
-      }
+      for (int j = 0; j < KW / 2; ++j)
+        sm.qf[nb][j][lane] = make_uint4(
+            float2_to_half2(f[8 * j] * up, f[8 * j + 1] * up), float2_to_half2(f[8 * j + 2] * up, f[8 * j + 3] * up),
+            float2_to_half2(f[8 * j + 4] * up, f[8 * j + 5] * up), float2_to_half2(f[8 * j + 6] * up, f[8 * j + 7] * up));
     }
     __syncthreads();
     uint4 qr[KW / 2];  // 8 columns: in registers; more are read with each sub-tile
@@ -334,13 +429,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
       for (int c = 0; c < 2; ++c) {
         cs[nb][c] = sm.cs[nb * 8 + 2 * t + c];
       }
-    const int32_t *sel = SEL ? p.selected + (size_t)it.seq * p.n_selected : nullptr;
 
     float m[NB][2], w[NB][2], l[NB][2];
     float o[MT][NB][4];
-    // the tiles this item needs: later ones hold no key that a column sees
-    const int t1e = SEL ? t1 : min(t1, (lim_max + kTile - 1) / kTile);
-    const int iters = max(0, t1e - t0);
 
     // A masked weight is zero, but zero times a NaN value is NaN: where the
     // result has one, the segment runs again with NaN codes of V taken out and
@@ -357,103 +448,15 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[j][nb][i] = 0.f;
 
-      // ---- loads: TMA, 16 rows of keys and of values per sub-tile, the 16-byte
-      // chunks of a row exchanged by the copy's swizzle, so that both products'
-      // reads spread over the banks.  Nothing is computed from a loaded index
-      // before the refresh after the one that loaded it.
-      // Dense: lane j holds sub-tile i + j's first row and exponents.
-      int d_row = -1;
-      // Selected: 32 entries per refresh (two sub-tiles): position, page, exponents.
-      int s_raw = -1, s_pos1 = -1, s_pg1 = -1, s_pos2 = -1, s_row2 = -1, s_pos = -1, s_row = -1;
-      uint32_t ke = 127, ve = 127;
-      float s_ks = 0.f, s_lv = 0.f;
-      auto load_raw = [&](int i) {  // the lane's entry among sub-tiles i, i + 1
-        const int k = (t0 + i + (lane >> 4)) * kTile + warp * 16 + (lane & 15);
-        s_raw = i + (lane >> 4) < iters && k < p.n_selected ? __ldg(sel + k) : -1;
-      };
-      auto load_page = [&](int pos) -> int { return pos < 0 ? -1 : __ldg(table + (pos >> p.c.page_log2)); };
-      auto row_of = [&](int pos, int pg) -> int {
-        if (pos < 0) return -1;
-        if ((unsigned)pg >= (unsigned)p.c.pages) {
-          atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
-          return -1;
-        }
-        return ((pg * heads + it.head) << p.c.page_log2) + (pos & (p.c.page - 1));
-      };
-      auto load_exps = [&](int row) {
-        if (row < 0) return;
-        const int ph = row >> p.c.page_log2;
-        ke = __ldg(p.c.k_exps + ph);
-        ve = __ldg(p.c.v_exps + ph);
-      };
-      auto step_sel = [&](int i) {  // entries of sub-tile i enter the chain
-        s_pos = s_pos2, s_row = s_row2;
-        s_ks = exp_byte(ke), s_lv = (float)(int)ve - 127.f;
-        s_pos2 = s_pos1, s_row2 = row_of(s_pos1, s_pg1), load_exps(s_row2);
-        s_pos1 = (unsigned)s_raw < (unsigned)lim_max ? s_raw : -1, s_pg1 = load_page(s_pos1);
-        load_raw(i);
-      };
-      if (SEL) {
-        step_sel(0);
-        step_sel(2);
-        step_sel(4);
-      }
-      auto issue = [&](int i) {
-        if (i >= iters) return;
-        const uint32_t no = copies++;
-        const int stage = no % kStages;
-        const int base = (t0 + i) * kTile + warp * 16;
-        uint64_t *bar = &sm.full[warp][stage];
-        uint8_t *kd = sm.ring[warp][stage], *vd = kd + 16 * D;
-        if (SEL) {
-          if ((i & 1) == 0) step_sel(i + 6);
-          const int half = 16 * (i & 1);
-          const uint32_t ok = __ballot_sync(~0u, s_row >= 0) >> half & 0xFFFFu;
-          if ((lane >> 4) == (i & 1)) {
-            meta.ks[stage][lane & 15] = s_ks;
-            meta.lv[stage][lane & 15] = s_lv;
-            meta.pos[stage][lane & 15] = s_row < 0 ? INT32_MAX : s_pos;
-          }
-          // entries that name no visible key take the row of one that does
-          const int some = __shfl_sync(~0u, s_row, half + (ok ? __ffs(ok) - 1 : 0));
-          const int mine = s_row < 0 ? some : s_row;
-          int y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(~0u, mine, half + 4 * (lane & 3) + k);
-          if (lane == 0) mbar_arrive_expect_tx(bar, ok ? 2 * 16 * D : 0);
-          if (lane == 0) meta.any[stage] = ok != 0;
-          __syncwarp();
-          if (ok && lane < 8)
-            tma_gather4((lane < 4 ? kd : vd) + (lane & 3) * 4 * D, lane < 4 ? &k_map : &v_map, bar, y);
-        } else {
-          if ((i & 31) == 0) {
-            const int pos = base + lane * kTile;
-            const bool want = i + lane < iters && pos < lim_max;
-            d_row = want ? row_of(pos, load_page(pos)) : -1;
-            load_exps(d_row);
-          }
-          if (lane == (i & 31)) {
-            meta.ks[stage][0] = exp_byte(ke);
-            meta.lv[stage][0] = (float)(int)ve - 127.f;
-            meta.any[stage] = d_row >= 0;
-          }
-          const int row = __shfl_sync(~0u, d_row, i & 31);
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar, row >= 0 ? 2 * 16 * D : 0);
-            if (row >= 0) {
-              tma_load_2d(kd, &k_map, bar, 0, row, policy);
-              tma_load_2d(vd, &v_map, bar, 0, row, policy);
-            }
-          }
-        }
-      };
+      if (careful) begin();
       uint32_t done = copies;  // sub-tiles worked on
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) issue(i);
 
       for (int i = 0; i < iters; ++i, ++done) {
         const int stage = done % kStages;
-        wait_full(sm, &sm.full[warp][stage], done / kStages & 1, p.c.status);
+        if (SEL) cp_async_wait<kStages - 2>();
+        else wait_full(sm, &sm.full[warp][stage], done / kStages & 1, p.c.status);
         __syncwarp();
         if (!meta.any[stage]) {  // no key of the sub-tile is seen
           __syncwarp();
@@ -637,6 +640,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
         __syncwarp();
         issue(i + kStages - 1);
       }
+      if (SEL) cp_async_wait<0>();
       bool bad = false;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
@@ -660,56 +664,58 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
           sm.wl[warp][nb * 8 + 2 * t + c] = l[nb][c];
         }
       }
-    __syncthreads();
+    __syncthreads();  // every warp is done with its ring
+    const bool whole = t0 == 0 && t1 == it.tiles;
+    float *slot = p.slots + ((size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * attn_slot_floats_dev<CB, D>();
+    // two blocks of columns at a time: every warp leaves its part, then a warp adds a column's
+    constexpr int NP = NB < 2 ? NB : 2;
+    for (int n0 = 0; n0 < NB; n0 += NP) {
+      if (n0) __syncthreads();
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) top = fmaxf(top, sm.ww[x][nb * 8 + 2 * t + c]);
-        const float f = w[nb][c] == top ? 1.f : ex2(w[nb][c] - top);
-#pragma unroll
-        for (int j = 0; j < MT; ++j) o[j][nb][c] *= f, o[j][nb][2 + c] *= f;
-      }
-    for (int x = 0; x < kWarps; ++x) {
-      if (warp == x) {
+      for (int nb = 0; nb < NB; ++nb) {
+        if (nb < n0 || nb >= n0 + NP) continue;
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float2 *d = reinterpret_cast<float2 *>(&sm.merge[nb * 8 + 2 * t + c][4 * VW * g + 2 * j]);
-              float2 val = make_float2(o[j][nb][c], o[j][nb][2 + c]);
-              if (x) {
-                const float2 was = *d;
-                val.x += was.x, val.y += was.y;
-              }
-              *d = val;
-            }
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<float2 *>(&sm.merge[warp][(nb - n0) * 8 + 2 * t + c][4 * VW * g + 2 * j]) =
+                make_float2(o[j][nb][c], o[j][nb][2 + c]);
       }
       __syncthreads();
-    }
-    const bool whole = t0 == 0 && t1 == it.tiles;
-    float *slot = p.slots + ((size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * attn_slot_floats_dev<CB, D>();
-    for (int col = warp; col < ncols; col += kWarps) {
-      float mx = -INFINITY, wx = -INFINITY, ls = 0.f;
+      for (int col = n0 * 8 + warp; col < min(ncols, (n0 + NP) * 8); col += kWarps) {
+        float mx = -INFINITY, wx = -INFINITY, ls = 0.f;
 #pragma unroll
-      for (int x = 0; x < kWarps; ++x) mx = fmaxf(mx, sm.wm[x][col]), wx = fmaxf(wx, sm.ww[x][col]);
+        for (int x = 0; x < kWarps; ++x) mx = fmaxf(mx, sm.wm[x][col]), wx = fmaxf(wx, sm.ww[x][col]);
 #pragma unroll
-      for (int x = 0; x < kWarps; ++x)
-        ls += sm.wl[x][col] * (sm.wm[x][col] == mx ? 1.f : ex2(sm.wm[x][col] - mx));
-      if (whole) {
-        const int row = SEL ? it.seq : r0 + (c0 + col) / group;
-        const int h = it.head * group + (SEL ? c0 + col : (c0 + col) % group);
-        finish<D>(p, row, h, lane, sm.merge[col], mx, wx, ls);
-      } else {
-        for (int d = lane; d < D; d += 32) slot[col * D + d] = sm.merge[col][d];
-        if (lane == 0) {
-          slot[CB * D + col] = mx;
-          slot[CB * D + CB + col] = wx;
-          slot[CB * D + 2 * CB + col] = ls;
+        for (int x = 0; x < kWarps; ++x)
+          ls += sm.wl[x][col] * (sm.wm[x][col] == mx ? 1.f : ex2(sm.wm[x][col] - mx));
+        constexpr int E = D / 32;  // components per lane
+        float sum[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] = 0.f;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+          const float f = sm.ww[x][col] == wx ? 1.f : ex2(sm.ww[x][col] - wx);
+          const float *part = &sm.merge[x][col - n0 * 8][lane * E];
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(part + e);
+            sum[e] += f * v.x, sum[e + 1] += f * v.y;
+          }
+        }
+        if (whole) {
+          const int row = SEL ? it.seq : r0 + (c0 + col) / group;
+          const int h = it.head * group + (SEL ? c0 + col : (c0 + col) % group);
+          finish_lane<E>(p, row, h, lane, sum, mx, wx, ls);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<float2 *>(slot + col * D + lane * E + e) = make_float2(sum[e], sum[e + 1]);
+          if (lane == 0) {
+            slot[CB * D + col] = mx;
+            slot[CB * D + CB + col] = wx;
+            slot[CB * D + 2 * CB + col] = ls;
+          }
         }
       }
     }
@@ -785,10 +791,13 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb
       ls += t[2 * cb + col] * (m == mx ? 1.f : ex2(m - mx));
       const float f = w == wx ? 1.f : ex2(w - wx);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f * s[(size_t)col * D + lane + 32 * e];
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(s + (size_t)col * D + lane * E + e);
+        o[e] += f * v.x, o[e + 1] += f * v.y;
+      }
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = o[e];
+    for (int e = 0; e < E; ++e) acc[warp][lane * E + e] = o[e];
     if (lane == 0) red[warp] = ls;
   }
   __syncthreads();
@@ -797,13 +806,12 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb
   for (int k = 1; k < WPC; ++k) {
     ls += red[warp + k];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] += acc[warp + k][lane + 32 * e];
+    for (int e = 0; e < E; ++e) o[e] += acc[warp + k][lane * E + e];
   }
-  __syncwarp();
   const bool sel = d.z < 0;
   const int c = (sel ? -d.z - 1 : d.z) + col;
   const int row = sel ? d.x : d.x + c / p.group, h = d.y * p.group + (sel ? c : c % p.group);
-  finish<D>(p, row, h, lane, acc[warp], mx, wx, ls);
+  finish_lane<E>(p, row, h, lane, o, mx, wx, ls);
 }
 
 template <int D, int NB>

@@ -84,8 +84,8 @@ cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, const
 // Its joining pass (p.desc and p.slots are the tiled kernel's).
 cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream);
 // follows: another kernel of the same call is before it on the stream.
-// k_map, v_map: codes as rows of head_dim bytes, boxes of 16 rows (selected
-// keys: of one).
+// k_map, v_map: codes as rows of head_dim bytes, boxes of 16 rows (not used for
+// selected keys).
 cudaError_t launch_kv_attention(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int nb,
                                 int ctas, bool follows, cudaStream_t stream);
 

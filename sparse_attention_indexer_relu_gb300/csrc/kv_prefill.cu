@@ -275,28 +275,6 @@ __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// Four fp32 to four e4m3 codes (nearest even, NaN kept).
-__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
-  uint32_t lo, hi;
-  asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tmov.b32 %0, {x, 0};\n\t}"
-      : "=r"(lo)
-      : "f"(a), "f"(b));
-  asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tmov.b32 %0, {x, 0};\n\t}"
-      : "=r"(hi)
-      : "f"(c), "f"(d));
-  return lo | hi << 16;
-}
-__device__ __forceinline__ uint32_t cvt2(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t cvt2_hi(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 // Byte offset of 16-byte chunk c (8 fp16) of row r in a [128][D] operand:
 // halves of 64 values, rows of 128 bytes, chunks exchanged within 8 rows.

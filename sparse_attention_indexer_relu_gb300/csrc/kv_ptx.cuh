@@ -31,6 +31,32 @@ __device__ __forceinline__ float exp_byte(uint32_t e) { return __uint_as_float(m
 __device__ __forceinline__ void grid_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// e4m3 code pair (low 16 bits) to fp16 pair.
+__device__ __forceinline__ uint32_t cvt2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t cvt2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// Four fp32 to four e4m3 codes (nearest even, saturating, NaN kept).
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tmov.b32 %0, {x, 0};\n\t}"
+      : "=r"(lo)
+      : "f"(a), "f"(b));
+  asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tmov.b32 %0, {x, 0};\n\t}"
+      : "=r"(hi)
+      : "f"(c), "f"(d));
+  return lo | hi << 16;
+}
+// Bytes of w that hold a NaN code (0x7F or 0xFF), as 0x80 bits.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16 operands.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -75,18 +101,20 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
                : "memory");
 }
 
-// Ordinary accesses to shared memory before, copies and MMAs after.
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// Four rows of a 2-D tensor (the map's box is one row) to consecutive rows of
-// shared memory.
-__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, uint64_t *bar, const int (&y)[4]) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
-      "%5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-      : "memory");
+// 16 bytes global -> shared without registers; zeros where !ok (nothing is read then).
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+               "l"(__cvta_generic_to_global(src)), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Ordinary accesses to shared memory before, copies and MMAs after.
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
@@ -141,23 +169,22 @@ __host__ __device__ constexpr size_t attn_slot_floats_dev() {
   return (size_t)CB * (D + 4);
 }
 
-// One warp writes a row of a head: acc = sum 2^(s + lv - w) E(v), ls = sum
-// 2^(s - m), so the result is acc / ls * 2^(w - m); zeros where nothing was
-// seen (m = -inf and no NaN).
-template <int D>
-__device__ __forceinline__ void finish(const AttnParams &p, int row, int head, int lane, const float *acc, float m,
-                                       float w, float ls) {
+// One warp writes a row of a head, a lane E consecutive components: acc = sum
+// 2^(s + lv - w) E(v), ls = sum 2^(s - m), so the result is acc / ls * 2^(w - m);
+// zeros where nothing was seen (m = -inf and no NaN).
+template <int E>
+__device__ __forceinline__ void finish_lane(const AttnParams &p, int row, int head, int lane, const float (&acc)[E],
+                                            float m, float w, float ls) {
   const bool none = m == -INFINITY && ls == 0.f;
   const float f = none ? 0.f : ls != ls ? NAN : ex2(w - m) / ls;
-  const size_t at = ((size_t)row * p.q_heads + head) * D;
-  uint32_t *o = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.out) + at);
+  const size_t at = (size_t)row * p.q_heads + head;
+  uint32_t *o = reinterpret_cast<uint32_t *>(p.out) + (at * 32 + lane) * (E / 2);
 #pragma unroll
-  for (int d = lane; d < D / 2; d += 32) {
-    const float a = none ? 0.f : acc[2 * d] * f, b = none ? 0.f : acc[2 * d + 1] * f;
-    o[d] = p.bf16 ? float2_to_bf162(a, b) : float2_to_half2(a, b);
+  for (int e = 0; e < E; e += 2) {
+    const float a = none ? 0.f : acc[e] * f, b = none ? 0.f : acc[e + 1] * f;
+    o[e / 2] = p.bf16 ? float2_to_bf162(a, b) : float2_to_half2(a, b);
   }
-  if (p.lse && lane == 0)
-    p.lse[(size_t)row * p.q_heads + head] = none ? -INFINITY : (m + log2f(ls)) * 0.693147180559945309f;
+  if (p.lse && lane == 0) p.lse[at] = none ? -INFINITY : (m + log2f(ls)) * 0.693147180559945309f;
 }
 
 }  // namespace mqa
