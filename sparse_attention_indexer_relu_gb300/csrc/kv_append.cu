@@ -7,9 +7,11 @@
 // the one to e4m3 (half a step: 2^-4 of the value).
 //
 // Bound by memory: rows * heads * dim * (input bytes + 1), twice (K and V).  A
-// CTA looks at a few consecutive rows, finds those that begin a page's new
-// positions (its leaders) and writes each leader's tile: one pass for the
-// magnitude, a second over the same bytes (from L1/L2) for the codes.
+// CTA looks at consecutive rows, finds those that begin a page's new positions
+// (its leaders) and writes each leader's tile: its rows are loaded into registers
+// at once, their largest magnitude found, and the codes written from there.  A
+// tile of more rows than that (calls of few rows, whose CTAs are small) is read
+// twice.
 #include "kv_ptx.cuh"
 
 #include <cuda_fp8.h>
@@ -18,8 +20,8 @@ namespace mqa {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kMaxRows = 16;  // rows a CTA looks at
+constexpr int kMaxRows = 128;    // rows a CTA looks at
+constexpr int kStarts = 1024;    // row bounds kept in shared memory
 
 __device__ __forceinline__ float from_e4m3(uint32_t code) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);
@@ -34,63 +36,91 @@ __device__ __forceinline__ int needed_exp(float amax) {
   return min(max(n, 7), 247);
 }
 
-// 8 elements of a row as fp32 (bf16, fp16: one 16-byte load; fp32: two).
+// 8 elements of a row: 16 bytes (bf16, fp16) or 32.
 template <int TYPE>
-__device__ __forceinline__ void load8(const void *base, size_t at, float (&f)[8]) {
-  if (TYPE == MQA_KV_FP32) {
-    const float4 *s = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + at);
-    const float4 x = __ldg(s), y = __ldg(s + 1);
-    f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
-  } else {
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + at));
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = TYPE == MQA_KV_BF16 ? bf16x2_to_float2(ws[i]) : half2_to_float2(ws[i]);
-      f[2 * i] = x.x, f[2 * i + 1] = x.y;
+struct Eight {
+  uint4 w[TYPE == MQA_KV_FP32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void *base, size_t at) {
+    if (TYPE == MQA_KV_FP32) {
+      const uint4 *s = reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(base) + at);
+      w[0] = __ldg(s);
+      w[TYPE == MQA_KV_FP32 ? 1 : 0] = __ldg(s + 1);
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + at));
     }
   }
-}
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (TYPE == MQA_KV_FP32) {
+        const uint4 &v = w[TYPE == MQA_KV_FP32 ? i >> 1 : 0];
+        f[2 * i] = __uint_as_float(i & 1 ? v.z : v.x), f[2 * i + 1] = __uint_as_float(i & 1 ? v.w : v.y);
+      } else {
+        const uint32_t v = i == 0 ? w[0].x : i == 1 ? w[0].y : i == 2 ? w[0].z : w[0].w;
+        const float2 x = TYPE == MQA_KV_BF16 ? bf16x2_to_float2(v) : half2_to_float2(v);
+        f[2 * i] = x.x, f[2 * i + 1] = x.y;
+      }
+    }
+  }
+};
 
-template <int D, int TYPE>
+// kThreads threads; tiles of up to STEPS times the rows they cover at once stay in registers.
+template <int D, int TYPE, int kThreads, int STEPS>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const void *__restrict__ kin,
                                                             const void *__restrict__ vin, long long ks, long long vs,
                                                             const int32_t *__restrict__ starts, int rows, int per) {
-  __shared__ int s_page[kMaxRows], s_slot[kMaxRows], s_count[kMaxRows], s_held[kMaxRows];
+  __shared__ int s_starts[kStarts + 1];
+  __shared__ int s_row[kMaxRows], s_page[kMaxRows], s_slot[kMaxRows], s_count[kMaxRows];
+  __shared__ int s_leaders[kMaxRows / 32];
   __shared__ float s_max[kThreads / 32];
   const int tid = threadIdx.x, head = blockIdx.y, values = blockIdx.z;
   const int row0 = blockIdx.x * per;
-  if (tid < per) {
-    const int r = row0 + tid;
-    int count = 0, page = -1, slot = 0, held = 0;
-    if (r < rows) {
-      int lo = 0, hi = c.seqs;  // the last sequence that starts at or before the row
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(starts + mid) <= r) lo = mid; else hi = mid;
-      }
-      const int a = max(__ldg(starts + lo), 0), b = min(__ldg(starts + lo + 1), rows);
-      const int len = __ldg(c.lens + lo);
-      const long long pos = (long long)len - (b - a) + (r - a);  // position of the row
-      if (r >= a && r < b && pos >= 0) {
-        slot = (int)(pos & (c.page - 1));
-        if (slot == 0 || r == a) {  // the first new position of its page
-          const long long col = pos >> c.page_log2;
-          if (col >= c.max_pages) {
-            if (head == 0 && !values) atomicOr(c.status, MQA_KV_DEV_BAD_LENGTH);
+  const bool near = c.seqs <= kStarts;
+  if (near) {
+    for (int i = tid; i <= c.seqs; i += kThreads) s_starts[i] = __ldg(starts + i);
+    __syncthreads();
+  }
+  auto start = [&](int s) { return near ? s_starts[s] : __ldg(starts + s); };
+  int count = 0, page = -1, slot = 0;
+  const int r = row0 + tid;
+  if (tid < per && r < rows) {
+    int lo = 0, hi = c.seqs;  // the last sequence that starts at or before the row
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start(mid) <= r) lo = mid; else hi = mid;
+    }
+    const int a = max(start(lo), 0), b = min(start(lo + 1), rows);
+    const long long pos = (long long)__ldg(c.lens + lo) - (b - a) + (r - a);  // position of the row
+    if (r >= a && r < b && pos >= 0) {
+      slot = (int)(pos & (c.page - 1));
+      if (slot == 0 || r == a) {  // the first new position of its page
+        const long long col = pos >> c.page_log2;
+        if (col >= c.max_pages) {
+          if (head == 0 && !values) atomicOr(c.status, MQA_KV_DEV_BAD_LENGTH);
+        } else {
+          page = __ldg(c.table + (size_t)lo * c.max_pages + col);
+          if ((unsigned)page >= (unsigned)c.pages) {
+            if (head == 0 && !values) atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
           } else {
-            page = __ldg(c.table + (size_t)lo * c.max_pages + col);
-            if ((unsigned)page >= (unsigned)c.pages) {
-              if (head == 0 && !values) atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
-            } else {
-              count = min(c.page - slot, b - r);
-              held = slot;
-            }
+            count = min(c.page - slot, b - r);
           }
         }
       }
     }
-    s_page[tid] = page, s_slot[tid] = slot, s_count[tid] = count, s_held[tid] = held;
+  }
+  // the leaders, in order
+  const uint32_t mine = __ballot_sync(~0u, count > 0);
+  if ((tid & 31) == 0 && tid < kMaxRows) s_leaders[tid >> 5] = __popc(mine);
+  __syncthreads();
+  int leaders = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < (kThreads < kMaxRows ? kThreads : kMaxRows) / 32; ++w) {
+    if (w < tid >> 5) before += s_leaders[w];
+    leaders += s_leaders[w];
+  }
+  if (count > 0) {
+    const int at = before + __popc(mine & lanemask_lt());
+    s_row[at] = r, s_page[at] = page, s_slot[at] = slot, s_count[at] = count;
   }
   __syncthreads();
   const void *in = values ? vin : kin;
@@ -99,66 +129,85 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, con
   uint8_t *exps = values ? c.v_exps : c.k_exps;
   constexpr int LPR = D / 8, RPS = kThreads / LPR;  // lanes per row, rows per step
   const int part = tid % LPR, step = tid / LPR;
-  for (int i = 0; i < per; ++i) {
-    const int count = s_count[i];
-    if (count == 0) continue;  // the same for the whole CTA
-    const size_t base = (size_t)(row0 + i) * stride + (size_t)head * D + part * 8;
+  for (int i = 0; i < leaders; ++i) {
+    const int n = s_count[i], held = s_slot[i];
+    const size_t base = (size_t)s_row[i] * stride + (size_t)head * D + part * 8;
+    const size_t ph = (size_t)s_page[i] * c.heads + head;
+    const int was = held ? exps[ph] : 0;
+    Eight<TYPE> x[STEPS];
     float amax = 0.f;
-#pragma unroll 4
-    for (int r = step; r < count; r += RPS) {
-      float f[8];
-      load8<TYPE>(in, base + (size_t)r * stride, f);
+    const bool kept = n <= STEPS * RPS;
+    for (int j0 = 0; j0 * RPS < n; j0 += STEPS) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = fabsf(f[j]);
-        amax = a <= 3.402823466e38f ? fmaxf(amax, a) : amax;  // infinities and NaN do not set the scale
-      }
+      for (int j = 0; j < STEPS; ++j)
+        if ((j0 + j) * RPS + step < n) x[j].load(in, base + (size_t)((j0 + j) * RPS + step) * stride);
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j)
+        if ((j0 + j) * RPS + step < n) {
+          float f[8];
+          x[j].values(f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float a = fabsf(f[k]);
+            amax = a <= 3.402823466e38f ? fmaxf(amax, a) : amax;  // infinities and NaN do not set the scale
+          }
+        }
     }
 #pragma unroll
-    for (int x = 16; x; x >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, x));
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
     if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-    const size_t ph = (size_t)s_page[i] * c.heads + head;
-    const int held = s_held[i], was = held ? exps[ph] : 0;
-    __syncthreads();  // s_max written, the old exponent read by all
-    amax = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    __syncthreads();  // the old exponent has been read by all, too
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
     const int e = max(needed_exp(amax), was);
     uint8_t *tile = codes + (ph << c.page_log2) * D;
     if (held && e > was) {  // earlier positions under the larger scale
       const float f = pow2i(max(was - e, -126));
       for (int j = tid; j < held * D / 4; j += kThreads) {
         uint32_t *w = reinterpret_cast<uint32_t *>(tile) + j;
-        const uint32_t x = *w;
-        *w = to_e4m3x4(from_e4m3(x & 255u) * f, from_e4m3(x >> 8 & 255u) * f, from_e4m3(x >> 16 & 255u) * f,
-                       from_e4m3(x >> 24) * f);
+        const uint32_t v = *w;
+        *w = to_e4m3x4(from_e4m3(v & 255u) * f, from_e4m3(v >> 8 & 255u) * f, from_e4m3(v >> 16 & 255u) * f,
+                       from_e4m3(v >> 24) * f);
       }
     }
     // 2^(127 - e); a page that was given a byte above 247 may need a subnormal
     const float up = e < 254 ? pow2i(127 - e) : __uint_as_float(0x00400000u >> (e - 254));
-#pragma unroll 4
-    for (int r = step; r < count; r += RPS) {
-      float f[8];
-      load8<TYPE>(in, base + (size_t)r * stride, f);
-      uint2 o;
-      o.x = to_e4m3x4(f[0] * up, f[1] * up, f[2] * up, f[3] * up);
-      o.y = to_e4m3x4(f[4] * up, f[5] * up, f[6] * up, f[7] * up);
-      *reinterpret_cast<uint2 *>(tile + (size_t)(s_slot[i] + r) * D + part * 8) = o;
+    for (int j0 = 0; j0 * RPS < n; j0 += STEPS) {
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) {
+        const int at = (j0 + j) * RPS + step;
+        if (at < n) {
+          if (!kept) x[j].load(in, base + (size_t)at * stride);
+          float f[8];
+          x[j].values(f);
+          uint2 o;
+          o.x = to_e4m3x4(f[0] * up, f[1] * up, f[2] * up, f[3] * up);
+          o.y = to_e4m3x4(f[4] * up, f[5] * up, f[6] * up, f[7] * up);
+          *reinterpret_cast<uint2 *>(tile + (size_t)(held + at) * D + part * 8) = o;
+        }
+      }
     }
     if (tid == 0) exps[ph] = (uint8_t)e;
     __syncthreads();  // s_max is free again
   }
 }
 
+template <int D, int TYPE>
+void launch(const KvView &c, const void *k, const void *v, long long ks, long long vs, const int32_t *starts, int rows,
+            dim3 grid, int per, cudaStream_t stream) {
+  if (per == 1)
+    kv_append_kernel<D, TYPE, 128, 1><<<grid, 128, 0, stream>>>(c, k, v, ks, vs, starts, rows, per);
+  else
+    kv_append_kernel<D, TYPE, 256, D / 16><<<grid, 256, 0, stream>>>(c, k, v, ks, vs, starts, rows, per);
+}
+
 template <int D>
 cudaError_t launch(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,
                    const int32_t *starts, int rows, dim3 grid, int per, cudaStream_t stream) {
   switch (type) {
-    case MQA_KV_BF16:
-      kv_append_kernel<D, MQA_KV_BF16><<<grid, kThreads, 0, stream>>>(c, k, v, ks, vs, starts, rows, per);
-      break;
-    case MQA_KV_FP16:
-      kv_append_kernel<D, MQA_KV_FP16><<<grid, kThreads, 0, stream>>>(c, k, v, ks, vs, starts, rows, per);
-      break;
-    default: kv_append_kernel<D, MQA_KV_FP32><<<grid, kThreads, 0, stream>>>(c, k, v, ks, vs, starts, rows, per);
+    case MQA_KV_BF16: launch<D, MQA_KV_BF16>(c, k, v, ks, vs, starts, rows, grid, per, stream); break;
+    case MQA_KV_FP16: launch<D, MQA_KV_FP16>(c, k, v, ks, vs, starts, rows, grid, per, stream); break;
+    default: launch<D, MQA_KV_FP32>(c, k, v, ks, vs, starts, rows, grid, per, stream);
   }
   return cudaGetLastError();
 }
@@ -167,11 +216,10 @@ cudaError_t launch(const KvView &c, const void *k, const void *v, long long ks, 
 
 cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,
                              const int32_t *starts, int rows, int sms, cudaStream_t stream) {
-  // one row per CTA while the rows fit a few waves (decode: every row is a
-  // leader); more rows per CTA for prompts, where one in page_size is
-  const long long units = (long long)rows * c.heads * 2;
-  int per = 1;
-  while (per < kMaxRows && units / per > 32LL * sms) per *= 2;
+  // one row per CTA of 128 threads while the rows fit a few waves (single tokens:
+  // every row is a leader); for prompts a page's rows per CTA of 256, so that
+  // every CTA has about one leader
+  const int per = (long long)rows * c.heads * 2 <= 32LL * sms ? 1 : c.page;
   const dim3 grid((rows + per - 1) / per, c.heads, 2);
   return c.dim == 64 ? launch<64>(c, k, v, ks, vs, type, starts, rows, grid, per, stream)
                      : launch<128>(c, k, v, ks, vs, type, starts, rows, grid, per, stream);
