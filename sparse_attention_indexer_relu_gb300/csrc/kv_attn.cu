@@ -750,13 +750,14 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
 
 }  // namespace
 
-// Join split items: a block adds the parts of kJoinCols columns of the item that
-// CTA blockIdx.x of the kernel before began, its own part first, then the
-// following CTAs' in order; WPC warps share a column's parts.
+// Join split items: a block adds the parts of two columns of the item that CTA
+// blockIdx.x of the kernel before began.  One long sequence is cut into one part
+// per CTA, so four warps share a column's parts, each its own in CTA order, and
+// are added in warp order: results do not depend on the timing.
 namespace {
-template <int D, int WPC>
+template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb) {
-  constexpr int kJoinCols = 8 / WPC;
+  constexpr int WPC = 4, kJoinCols = 8 / WPC;
   grid_wait();
   const int4 d = p.desc[blockIdx.x];
   const int more = d.w & 0xFFFFF, ncols = d.w >> 20;
@@ -814,6 +815,58 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb
   finish_lane<E>(p, row, h, lane, o, mx, wx, ls);
 }
 
+// The same for the tiled kernel's items: many columns, few parts.  A warp has 4
+// columns, one part's loads of all of them in flight (ragged prompts: 9 us,
+// against 13 with a warp per column and all parts' loads in a row).
+template <int D>
+__global__ void __launch_bounds__(256) kv_join_few_kernel(const AttnParams p) {
+  grid_wait();
+  const int4 d = p.desc[blockIdx.x];
+  const int more = d.w & 0xFFFFF, ncols = d.w >> 20;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.y * 32 + warp * 4;
+  if (more == 0 || c0 >= ncols) return;
+  constexpr int E = D / 32, CB = kTiledCols;
+  constexpr size_t pitch = (size_t)CB * (D + 4);
+  auto slot = [&](int i) { return p.slots + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * pitch; };
+  float mx[4], wx[4], ls[4], o[4][E];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    mx[k] = wx[k] = -INFINITY, ls[k] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[k][e] = 0.f;
+  }
+  for (int i = 0; i <= more; ++i) {
+    const float *s = slot(i), *t = s + (size_t)CB * D;
+    float m[4], w[4], l[4];
+    float2 v[4][E / 2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // columns behind the last hold what an earlier call left: not used
+      m[k] = t[c0 + k], w[k] = t[CB + c0 + k], l[k] = t[2 * CB + c0 + k];
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e)
+        v[k][e] = *reinterpret_cast<const float2 *>(s + (size_t)(c0 + k) * D + lane * E + 2 * e);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // references move as larger ones come
+      const float mn = fmaxf(mx[k], m[k]), wn = fmaxf(wx[k], w[k]);
+      const float fa = mx[k] == mn ? 1.f : ex2(mx[k] - mn), fb = m[k] == mn ? 1.f : ex2(m[k] - mn);
+      const float ga = wx[k] == wn ? 1.f : ex2(wx[k] - wn), gb = w[k] == wn ? 1.f : ex2(w[k] - wn);
+      ls[k] = ls[k] * fa + l[k] * fb;
+      mx[k] = mn, wx[k] = wn;
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        o[k][2 * e] = o[k][2 * e] * ga + v[k][e].x * gb;
+        o[k][2 * e + 1] = o[k][2 * e + 1] * ga + v[k][e].y * gb;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = d.z + c0 + k;
+    if (c0 + k < ncols) finish_lane<E>(p, d.x + c / p.group, d.y * p.group + c % p.group, lane, o[k], mx[k], wx[k], ls[k]);
+  }
+}
+
 template <int D, int NB>
 cudaError_t launch(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int ctas, bool follows,
                    cudaStream_t stream) {
@@ -830,7 +883,7 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &k_map, const CUtensor
       e = launch_after(kv_attn_kernel<D, NB, false>, dim3(ctas), kAttnThreads, bytes, stream, follows, p, k_map, v_map);
   }
   if (e != cudaSuccess) return e;
-  return launch_after(kv_join_kernel<D, 4>, dim3(ctas, 4 * NB), 256, 0, stream, true, p, 8 * NB);
+  return launch_after(kv_join_kernel<D>, dim3(ctas, 4 * NB), 256, 0, stream, true, p, 8 * NB);
 }
 
 template <int D>
@@ -852,9 +905,9 @@ cudaError_t launch_kv_attention(const AttnParams &p, const CUtensorMap &k_map, c
 }
 
 cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream) {
-  const dim3 grid(ctas, kTiledCols / 8);
-  return p.c.dim == 64 ? launch_after(kv_join_kernel<64, 1>, grid, 256, 0, stream, true, p, kTiledCols)
-                       : launch_after(kv_join_kernel<128, 1>, grid, 256, 0, stream, true, p, kTiledCols);
+  const dim3 grid(ctas, kTiledCols / 32);
+  return p.c.dim == 64 ? launch_after(kv_join_few_kernel<64>, grid, 256, 0, stream, true, p)
+                       : launch_after(kv_join_few_kernel<128>, grid, 256, 0, stream, true, p);
 }
 
 }  // namespace mqa

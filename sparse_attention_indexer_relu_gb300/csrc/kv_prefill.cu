@@ -46,6 +46,7 @@ constexpr int kStagesK = 3, kStagesV = 2;
 constexpr int kMeta = 8;                  // tile descriptions in flight
 constexpr int kTerms = kQueryTerms;       // e4m3 terms of a query value (bf16: 2)
 constexpr long long kWaitNs = 2000000000LL;
+constexpr int kNear = 2;                  // tiles by which a part's end may move (partial results cost about as much)
 constexpr int kConverters = 128;
 
 // sum over 0 <= i < n of floor((a i + b) / m); a, b >= 0, m > 0.  Whole parts
@@ -166,8 +167,8 @@ struct Smem {
   Walk walk[kThreads / 32];
   uint32_t tmem;
   int dead;
-  int found_seq;
-  long long found_at, scan[kThreads / 32];
+  int found_seq[2];
+  long long found_at[2], scan[kThreads / 32];
 };
 
 __device__ __forceinline__ void step_on(const AttnParams &p, Walk &w) {
@@ -653,7 +654,7 @@ __device__ __noinline__ float weigh_far(uint32_t ts, const TileMeta &meta, int r
 }
 
 template <int D>
-__device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
+__device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, long long near) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   const int x = threadIdx.x >> 7;        // tile of columns
   const int r = threadIdx.x & 127;       // its column
@@ -818,7 +819,9 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per) {
       }
     }
     if (threadIdx.x == 0 && !whole && w.x.t0 == 0) {
-      const long long rest = w.x.tiles - (w.x.t1 - w.x.t0);
+      // ends of parts that lie inside the item behind this one, each the beginning of
+      // a following CTA's part
+      const long long rest = w.x.tiles - w.x.t1 - near;
       p.desc[blockIdx.x] = make_int4(w.x.q.r0, w.x.head, w.x.block * kCols,
                                      (int)((rest + per - 1) / per) | ncols_now << 20);
     }
@@ -857,24 +860,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     total += sm.scan[i];
   }
   const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kTiledMinTiles);
-  Walk w;
-  w.at = blockIdx.x * per;
-  w.end = min(total, w.at + per);
+  // Even ends; one that lies within kNear tiles of an item's own end is
+  // moved there, which saves the item's partial results and their joining.
+  const long long near = min(per / 8, (long long)kNear), cut0 = min(blockIdx.x * per, total), cut1 = min(cut0 + per, total);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (w.at >= w.end) grid_wait();
-  if (w.at >= w.end) return;  // the whole CTA leaves together
-  if (w.at >= before && w.at < before + mine) {
-    long long b = before;
-    for (int i = 0; i < per_thread; ++i) {
-      const int s = tid * per_thread + i;
-      const Seq q = seq_of(p, s);
-      const long long u = q.blocks ? p.c.heads * tiles_before(p, q, q.blocks) : 0;
-      if (w.at < b + u) {
-        sm.found_seq = s;
-        sm.found_at = w.at - b;
-        break;
+  if (cut0 >= cut1) grid_wait();
+  if (cut0 >= cut1) return;  // the whole CTA leaves together
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const long long cut = k ? cut1 : cut0;
+    if (cut >= before && cut < before + mine) {
+      long long b = before;
+      for (int i = 0; i < per_thread; ++i) {
+        const int s = tid * per_thread + i;
+        const Seq q = seq_of(p, s);
+        const long long u = q.blocks ? p.c.heads * tiles_before(p, q, q.blocks) : 0;
+        if (cut < b + u) {
+          sm.found_seq[k] = s;
+          sm.found_at[k] = b;
+          break;
+        }
+        b += u;
       }
-      b += u;
     }
   }
   if (tid == 0) {
@@ -909,29 +916,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  {
-    w.x.seq = sm.found_seq;
+  // the end first, then the beginning, which stays in w
+  Walk w;
+  w.end = total;
+  for (int k = cut1 < total ? 1 : 0; k >= 0; --k) {
+    const long long cut = k ? cut1 : cut0;
+    w.x.seq = sm.found_seq[k];
     w.x.q = seq_of(p, w.x.seq);
     const long long per_head = tiles_before(p, w.x.q, w.x.q.blocks);
-    w.x.head = (int)(sm.found_at / per_head);
-    const long long rest = sm.found_at - w.x.head * per_head;
-    int lo = 0, hi = w.x.q.blocks;  // the last block that begins at or before `rest`
+    long long rest = cut - sm.found_at[k];
+    w.x.head = (int)(rest / per_head);
+    rest -= w.x.head * per_head;
+    int lo = 0, hi = w.x.q.blocks;  // the last block that begins at or before `rest`: 32 candidates at a time
     while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tiles_before(p, w.x.q, mid) <= rest) lo = mid; else hi = mid;
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const uint32_t ok = __ballot_sync(~0u, at < hi && tiles_before(p, w.x.q, at) <= rest);
+      lo += (31 - __clz(ok)) * step;  // lane 0's candidate always is
+      hi = min(hi, lo + step);
     }
     w.x.block = lo;
     w.x.tiles = block_tiles(p, w.x.q, lo);
     w.x.t0 = (int)(rest - tiles_before(p, w.x.q, lo));
-    w.fit();
+    const int off = w.x.t0, to_end = w.x.tiles - off;
+    if (k) {
+      w.end = off <= near ? cut - off : to_end <= near ? cut + to_end : cut;
+    } else if (off <= near) {
+      w.at = cut - off;
+      w.x.t0 = 0;
+    } else {
+      w.at = cut;
+      if (to_end <= near) {
+        w.x.t1 = w.x.tiles;
+        w.next(p);
+      }
+    }
   }
+  if (w.valid()) w.fit();
   if (lane == 0) sm.walk[warp] = w;
   __syncwarp();
   grid_wait();  // the query terms
   // registers: 256 x 192 + 128 x 80 + 128 x 48 = 512 x 128, what the block was launched with
   if (warp < 8) {
     reg_inc<192>();
-    softmax_role<D>(p, sm, per);
+    softmax_role<D>(p, sm, per, near);
   } else if (warp < 12) {
     reg_dec<80>();
     convert_role<D>(p, sm);

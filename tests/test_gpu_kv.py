@@ -279,6 +279,93 @@ def test_tiled_attention_bad_page(mqa):
     assert mqa.kv_status(dev) == 2
     check(got, None, c.attention(qd, np.array([0, 50]), 0.125, "fp16", sel))
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [3, 8])
+def test_one_workspace_holds_for_every_form(mqa, dim, group):
+    """alloc_kv_workspace(rows) serves calls of fewer rows, of any max_rows, and over selected keys."""
+    rng = np.random.default_rng(60)
+    c = ref.random_cache(rng, 20, 2, 16, dim, [90, 60], 8)
+    dev = ref.to_device(c, mqa)
+    q, qd = rows_of(rng, 8, 2 * group, dim, "bf16")
+    ws = mqa.alloc_kv_workspace(dev, 8, 2 * group)
+    for rows in ([8, 0], [4, 4], [1, 1], [0, 3]):
+        st = starts_of(rows)
+        n = int(st[-1])
+        sel = random_selection(rng, c, rows, 20)
+        for max_rows in (None, 1, 2, 3, 4, 7):
+            got = mqa.kv_attention(q[:n], dev, ints(st), max_rows=max_rows, workspace=ws)
+            check(got, None, c.attention(qd[:n], st, dim ** -0.5, "bf16"), (rows, max_rows))
+        got = mqa.kv_attention(q[:n], dev, ints(st), selected=ints(sel), workspace=ws)
+        check(got, None, c.attention(qd[:n], st, dim ** -0.5, "bf16", sel), rows)
+
+
+def test_short_sequences_beside_a_prompt(mqa):
+    """Sequences of one row, of none and of no position in one call with a prompt."""
+    rng = np.random.default_rng(61)
+    c = ref.random_cache(rng, 60, 2, 16, 128, [0, 400, 150, 7, 1], 26)
+    attend(mqa, c, rng, [0, 400, 1, 3, 1], 8, extra_rows=2)
+    attend(mqa, c, rng, [2, 300, 0, 1, 0], 8, "fp16", causal=False)
+
+
+def test_many_sequences(mqa):
+    """More sequences than the kernels hold bounds of at once, most of them without rows."""
+    rng = np.random.default_rng(62)
+    n = 1500
+    lens = rng.integers(0, 40, n)
+    rows = np.where(rng.random(n) < 0.1, np.minimum(rng.integers(1, 9, n), lens), 0)
+    rows[[0, 1023, 1024, 1025, n - 1]] = 1
+    lens[[0, 1023, 1024, 1025, n - 1]] = 17
+    c = ref.random_cache(rng, int((-(-lens // 16)).sum()) + 1, 1, 16, 64, lens, 3)
+    out, dev, q, st = attend(mqa, c, rng, rows, 4)
+    attend(mqa, c, rng, rows, 4, max_rows=1)
+    k, kd = rows_of(rng, int(st[-1]), 1, 64, "bf16")
+    mqa.kv_append(dev, k, k, ints(st))
+    c.append(kd, kd, st)
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+
+
+def test_offsets_past_32_bits(mqa):
+    """A pool of more than 2^32 bytes: its last pages are appended to, read in each form, copied and moved."""
+    import torch
+    rng = np.random.default_rng(63)
+    heads, page, dim = 8, 128, 128
+    pages = 2 ** 32 // (heads * page * dim) + 64
+    tail = 40  # the host holds the last pages only; page p of the pool is page p - (pages - tail) there
+    lens, width = [1000, 300], 12
+    c = ref.random_cache(rng, tail, heads, page, dim, lens, width)
+    base = pages - tail
+    z = lambda *s, t=torch.uint8: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    dev = mqa.KVCache(z(pages, heads, page, dim), z(pages, heads, page, dim), z(pages, heads), z(pages, heads),
+                      ints(c.table + base), ints(c.lens), z(pages, t=torch.int32))
+    for t, a in ((dev.k, c.k), (dev.v, c.v), (dev.k_exps, c.ke), (dev.v_exps, c.ve), (dev.refcounts, c.refs)):
+        t[base:] = torch.from_numpy(a).cuda()
+
+    def same():
+        return [n for n, a in (("k", c.k), ("v", c.v), ("k_exps", c.ke), ("v_exps", c.ve))
+                if not np.array_equal(getattr(dev, n)[base:].cpu().numpy(), a)]
+
+    for rows in ([1, 2], [40, 3]):
+        st = starts_of(rows)
+        n = int(st[-1])
+        k, kd = rows_of(rng, n, heads, dim, "bf16")
+        mqa.kv_append(dev, k, k, ints(st))
+        c.append(kd, kd, st)
+        assert same() == []
+        q, qd = rows_of(rng, n, heads * 4, dim, "bf16")
+        check(mqa.kv_attention(q, dev, ints(st)), None, c.attention(qd, st, dim ** -0.5, "bf16"))
+        sel = random_selection(rng, c, rows, 33)
+        check(mqa.kv_attention(q, dev, ints(st), selected=ints(sel)), None,
+              c.attention(qd, st, dim ** -0.5, "bf16", sel))
+    free = np.nonzero(c.refs == 0)[0][:2]
+    src = c.table[0, :2].copy()
+    mqa.kv_copy_pages(dev, ints(src + base), ints(free + base))
+    c.copy_pages(src, free)
+    assert same() == [] and not dev.k[:base].any() and not dev.v[:base].any()  # nothing landed 2^32 bytes lower
+    want = mqa.kv_attention(q, dev, ints(st))
+    mqa.kv_compact(dev)
+    assert mqa.kv_status(dev) == 0 and int(dev.page_table[0, :8].max()) < 64
+    assert torch.equal(mqa.kv_attention(q, dev, ints(st)), want)
+
 
 # ---------------------------------------------------------------- selected keys
 def random_selection(rng, c, rows, k, seen_only=False):
@@ -366,6 +453,63 @@ def test_two_streams_with_a_workspace_each(mqa):
     outs = [mqa.kv_attention(q, dev, st, stream=s) for _ in range(10) for s in streams]
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)  # and the same bits every time
+
+
+def test_tiled_attention_in_graphs(mqa):
+    """Two graphs of a call for many columns on one workspace, replayed on a side stream with other lengths."""
+    import torch
+    rng = np.random.default_rng(64)
+    c = ref.random_cache(rng, 60, 2, 16, 64, [300, 120], 24)
+    dev = ref.to_device(c, mqa)
+    q, qd = rows_of(rng, 90, 8, 64, "fp16")
+    bounds = [np.array([0, 60, 90]), np.array([0, 1, 90])]
+    st = [ints(b) for b in bounds]
+    ws = mqa.alloc_kv_workspace(dev, 90, 8)
+    outs = [torch.zeros_like(q) for _ in st]
+    mqa.kv_attention(q, dev, st[0], workspace=ws, out=outs[0])
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in st]
+    for g, s, o in zip(graphs, st, outs):
+        with torch.cuda.graph(g):
+            mqa.kv_attention(q, dev, s, workspace=ws, out=o)
+    side = torch.cuda.Stream()
+    for lens in ([300, 120], [60, 89], [5, 0], [257, 128]):
+        c.lens[:] = lens
+        dev.seq_lens.copy_(ints(lens))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for g in graphs:
+                g.replay()
+        side.synchronize()
+        for o, b in zip(outs, bounds):
+            check(o, None, c.attention(qd, b, 0.125, "fp16"), lens)
+
+
+def test_calls_follow_one_another_without_a_pause(mqa):
+    """Appending and attention for few and for many columns in turn on one workspace: each call reads what the call
+    before it wrote, and the answers are those of calls made one at a time."""
+    import torch
+    rng = np.random.default_rng(65)
+    c = ref.random_cache(rng, 90, 2, 16, 128, [500, 260], 36)
+    c.k &= 0x7E  # whatever the unused positions hold, no NaN
+    c.v &= 0x7E
+    ks = [rows_of(rng, n, 2, 128, "bf16")[0] for n in (3, 80, 3, 80)]
+    qs = [rows_of(rng, k.shape[0], 16, 128, "bf16")[0] for k in ks]
+    sts = [ints([0, k.shape[0] - 1, k.shape[0]]) for k in ks]
+
+    def run(pause):
+        dev, outs = ref.to_device(c, mqa), []
+        ws = mqa.alloc_kv_workspace(dev, 80, 16)
+        for k, q, st in list(zip(ks, qs, sts)) * 3:
+            mqa.kv_append(dev, k, k, st)
+            outs.append(mqa.kv_attention(q, dev, st, workspace=ws))
+            mqa.kv_reserve(dev, ints([1, 2]))
+            if pause:
+                torch.cuda.synchronize()
+        assert mqa.kv_status(dev) == 0
+        return outs
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
 
 
 # ---------------------------------------------------------------- appending
