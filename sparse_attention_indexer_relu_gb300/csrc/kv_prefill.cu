@@ -145,6 +145,12 @@ struct Walk {
   }
 };
 
+// Where an end of a CTA's part lies: `off` tiles into the item of x.
+struct Cut {
+  Part x;
+  int off;
+};
+
 struct TileMeta {
   float2 kv[8];          // per 16 keys: key scale, log2 of the value scale
   float lv_min;          // least of the latter,
@@ -168,7 +174,8 @@ struct Smem {
   uint32_t tmem;
   int dead;
   int found_seq[2];
-  long long found_at[2], scan[kThreads / 32];
+  long long found_at[2], found_per_head[2], scan[kThreads / 32];
+  Cut cut[2];
 };
 
 __device__ __forceinline__ void step_on(const AttnParams &p, Walk &w) {
@@ -306,6 +313,19 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
     const int lim = block_limit(p, w.x.q, w.x.block), first = w.x.t0 * kKeys + g * 16, head = w.x.head;
     const int32_t *table = p.c.table + (size_t)w.x.seq * p.c.max_pages;
     float lv_max = -128.f;
+    auto ask = [&] {  // the part's queries
+      const int halves = w.cols(p) > 128 ? 2 : 1, at = w.x.q.r0 * p.group + w.x.block * kCols;
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(terms * halves * 128 * D));
+      __syncwarp();
+      if (lane < terms * halves) {
+        const int x = lane / terms, term = lane % terms;
+        tma_load_2d(sm.q[x][term], &q_map, &sm.q_full, 0, (term * heads + head) * planes + at + 128 * x, once);
+      }
+      ++q_no;
+    };
+    const bool begins = q_no == 0;
+    if (begins && nt > 0) ask();  // the first part's before anything is looked up
     for (int tb = 0; tb < nt; tb += 4) {
       const int t = tb + (lane >> 3), pos = first + t * kKeys;
       int row = -2;
@@ -359,17 +379,9 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
         __syncwarp();
         if (lane >> 3 == u && (mine >> g & 1))
           tma_load_2d(sm.k[stage] + g * 16 * D, &map, &sm.k_full[stage], 0, row, keep);
-        if (tb + u == 0) {  // the queries, once the previous part's last scores are done
+        if (tb + u == 0 && !begins) {  // once the previous part's last scores are done
           wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p.c.status);
-          const int halves = w.cols(p) > 128 ? 2 : 1, at = w.x.q.r0 * p.group + w.x.block * kCols;
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(terms * halves * 128 * D));
-          __syncwarp();
-          if (lane < terms * halves) {
-            const int x = lane / terms, term = lane % terms;
-            tma_load_2d(sm.q[x][term], &q_map, &sm.q_full, 0, (term * heads + head) * planes + at + 128 * x, once);
-          }
-          ++q_no;
+          ask();
         }
       }
     }
@@ -874,9 +886,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < per_thread; ++i) {
         const int s = tid * per_thread + i;
         const Seq q = seq_of(p, s);
-        const long long u = q.blocks ? p.c.heads * tiles_before(p, q, q.blocks) : 0;
+        const long long per_head = q.blocks ? tiles_before(p, q, q.blocks) : 0, u = p.c.heads * per_head;
         if (cut < b + u) {
           sm.found_seq[k] = s;
+          sm.found_per_head[k] = per_head;
           sm.found_at[k] = b;
           break;
         }
@@ -916,43 +929,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // the end first, then the beginning, which stays in w
-  Walk w;
-  w.end = total;
-  for (int k = cut1 < total ? 1 : 0; k >= 0; --k) {
-    const long long cut = k ? cut1 : cut0;
-    w.x.seq = sm.found_seq[k];
-    w.x.q = seq_of(p, w.x.seq);
-    const long long per_head = tiles_before(p, w.x.q, w.x.q.blocks);
-    long long rest = cut - sm.found_at[k];
-    w.x.head = (int)(rest / per_head);
-    rest -= w.x.head * per_head;
-    int lo = 0, hi = w.x.q.blocks;  // the last block that begins at or before `rest`: 32 candidates at a time
+  // a warp finds the item of each end (each warp by itself took 11,000 cycles for both)
+  if (warp == 0 || (warp == 1 && cut1 < total)) {
+    Cut c;
+    c.x.seq = sm.found_seq[warp];
+    c.x.q = seq_of(p, c.x.seq);
+    long long rest = (warp ? cut1 : cut0) - sm.found_at[warp], begins = 0;
+    const long long per_head = sm.found_per_head[warp];
+    c.x.head = (int)(rest / per_head);
+    rest -= c.x.head * per_head;
+    int lo = 0, hi = c.x.q.blocks;  // the last block that begins at or before `rest`: 32 candidates at a time
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-      const uint32_t ok = __ballot_sync(~0u, at < hi && tiles_before(p, w.x.q, at) <= rest);
-      lo += (31 - __clz(ok)) * step;  // lane 0's candidate always is
+      const long long v = at < hi ? tiles_before(p, c.x.q, at) : 0;
+      const int pick = 31 - __clz(__ballot_sync(~0u, at < hi && v <= rest));  // lane 0's candidate always is one
+      begins = __shfl_sync(~0u, v, pick);
+      lo += pick * step;
       hi = min(hi, lo + step);
     }
-    w.x.block = lo;
-    w.x.tiles = block_tiles(p, w.x.q, lo);
-    w.x.t0 = (int)(rest - tiles_before(p, w.x.q, lo));
-    const int off = w.x.t0, to_end = w.x.tiles - off;
-    if (k) {
-      w.end = off <= near ? cut - off : to_end <= near ? cut + to_end : cut;
-    } else if (off <= near) {
-      w.at = cut - off;
-      w.x.t0 = 0;
-    } else {
-      w.at = cut;
-      if (to_end <= near) {
-        w.x.t1 = w.x.tiles;
-        w.next(p);
-      }
-    }
+    c.x.block = lo;
+    c.x.tiles = block_tiles(p, c.x.q, lo);
+    c.off = (int)(rest - begins);
+    if (lane == 0) sm.cut[warp] = c;
   }
-  if (w.valid()) w.fit();
-  if (lane == 0) sm.walk[warp] = w;
+  __syncthreads();
+  if (lane == 0) {
+    Walk w;
+    const Cut &c = sm.cut[0], &e = sm.cut[1];
+    w.end = cut1;
+    if (cut1 < total) {
+      const int to_end = e.x.tiles - e.off;
+      w.end = e.off <= near ? cut1 - e.off : to_end <= near ? cut1 + to_end : cut1;
+    }
+    w.at = cut0;
+    w.x = c.x;
+    w.x.t0 = c.off;
+    if (c.off <= near) {
+      w.at = cut0 - c.off;
+      w.x.t0 = 0;
+    } else if (c.x.tiles - c.off <= near) {
+      w.x.t1 = c.x.tiles;
+      w.next(p);
+    }
+    if (w.valid()) w.fit();
+    sm.walk[warp] = w;
+  }
   __syncwarp();
   grid_wait();  // the query terms
   // registers: 256 x 192 + 128 x 80 + 128 x 48 = 512 x 128, what the block was launched with
