@@ -998,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // [term][key/value head][row][head of the group][D], factors to [key/value
 // head][row][head of the group].
 template <int D>
-__device__ __forceinline__ void terms_of(const AttnParams &p, const uint4 u, int i, int last, int total, int part,
+__device__ __forceinline__ void terms_of(const AttnParams &p, const uint4 u, bool on, int row, int head, int part,
                                          uint8_t *__restrict__ q8, float *__restrict__ factor) {
   constexpr int LPR = D / 8;
   const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
@@ -1016,23 +1016,26 @@ __device__ __forceinline__ void terms_of(const AttnParams &p, const uint4 u, int
   }
 #pragma unroll
   for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-  if (i >= last) return;
+  if (!on) return;
   // power of two that brings the largest magnitude to (224, 448]
   int e = 0;
   if (amax > 0.f) e = ((__float_as_uint(amax) & 0x7FFFFFu) > 0x600000u ? 7 : 8) - exponent_of(amax);
   e = max(-110, min(110, e));
   const float up = pow2i(e);
-  const int row = i / p.q_heads, head = i % p.q_heads;
-  const size_t at = ((size_t)(head / p.group) * p.rows + row) * p.group + head % p.group;
+  // (exact: head < 2^16, so the quotient's error is below half of 1 / group)
+  const int kv_head = (int)(((float)head + 0.5f) * __frcp_rn((float)p.group));
+  const size_t at = ((size_t)kv_head * p.rows + row) * p.group + (head - kv_head * p.group);
   if (part == 0) factor[at] = p.scale_log2 * pow2i(-e);
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] *= up;
-  const size_t plane = (size_t)total * D;
-  for (int term = 0; term < (p.bf16 ? 2 : 3); ++term) {
+  const size_t plane = (size_t)p.rows * p.q_heads * D;
+  const int terms = p.bf16 ? 2 : 3;
+  for (int term = 0;;) {
     uint2 c;
     c.x = to_e4m3x4(f[0], f[1], f[2], f[3]);
     c.y = to_e4m3x4(f[4], f[5], f[6], f[7]);
     *reinterpret_cast<uint2 *>(q8 + term * plane + at * D + part * 8) = c;
+    if (++term == terms) break;
     const uint32_t back[4] = {cvt2(c.x), cvt2_hi(c.x), cvt2(c.y), cvt2_hi(c.y)};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -1049,19 +1052,25 @@ __global__ void __launch_bounds__(256) kv_query_terms_kernel(const AttnParams p,
   constexpr int LPR = D / 8, PER = 256 / LPR, BATCH = 4;  // lanes per row, rows per CTA and step, steps
   const int part = threadIdx.x % LPR;
   const int last = min(max(p.starts[p.c.seqs], 0), p.rows) * p.q_heads;  // rows of no sequence are not read
-  const int total = p.rows * p.q_heads, first = blockIdx.x * PER * BATCH + threadIdx.x / LPR;
+  const int first = blockIdx.x * PER * BATCH + threadIdx.x / LPR;
   uint4 u[BATCH];
+  int row[BATCH], head[BATCH];
 #pragma unroll
   for (int i = 0; i < BATCH; ++i) {
     const int at = first + i * PER;
+    if (i == 0 || p.q_heads < PER) {
+      row[i] = at / p.q_heads, head[i] = at - row[i] * p.q_heads;
+    } else {
+      row[i] = row[i - 1], head[i] = head[i - 1] + PER;
+      if (head[i] >= p.q_heads) ++row[i], head[i] -= p.q_heads;
+    }
     u[i] = make_uint4(0, 0, 0, 0);
     if (at < last)
       u[i] = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) +
-                                                   (size_t)(at / p.q_heads) * p.q_stride +
-                                                   (size_t)(at % p.q_heads) * D + part * 8));
+                                                   (size_t)row[i] * p.q_stride + (size_t)head[i] * D + part * 8));
   }
 #pragma unroll
-  for (int i = 0; i < BATCH; ++i) terms_of<D>(p, u[i], first + i * PER, last, total, part, q8, factor);
+  for (int i = 0; i < BATCH; ++i) terms_of<D>(p, u[i], first + i * PER < last, row[i], head[i], part, q8, factor);
 }
 
 template <int D>
