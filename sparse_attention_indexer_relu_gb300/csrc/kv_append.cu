@@ -49,6 +49,28 @@ struct Eight {
       w[0] = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + at));
     }
   }
+  __device__ __forceinline__ void clear() {
+    w[0] = make_uint4(0, 0, 0, 0);
+    if (TYPE == MQA_KV_FP32) w[TYPE == MQA_KV_FP32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
+  }
+  // The larger of m and the elements' magnitudes, as bit patterns (ordered like
+  // the values; two at a time for 16-bit types).
+  __device__ __forceinline__ uint32_t top(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < (TYPE == MQA_KV_FP32 ? 2 : 1); ++i) {
+      const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        m = TYPE == MQA_KV_FP32 ? max(m, v[k] & 0x7FFFFFFFu) : __vmaxu2(m, v[k] & 0x7FFF7FFFu);
+    }
+    return m;
+  }
+  // Its value; infinity or NaN where one of the elements is.
+  static __device__ __forceinline__ float value(uint32_t m) {
+    if (TYPE == MQA_KV_FP32) return __uint_as_float(m);
+    m = max(m & 0xFFFFu, m >> 16);
+    return TYPE == MQA_KV_BF16 ? __uint_as_float(m << 16) : half2_to_float2(m).x;
+  }
   __device__ __forceinline__ void values(float (&f)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -139,19 +161,28 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, con
     const bool kept = n <= STEPS * RPS;
     for (int j0 = 0; j0 * RPS < n; j0 += STEPS) {
 #pragma unroll
-      for (int j = 0; j < STEPS; ++j)
+      for (int j = 0; j < STEPS; ++j) {
+        x[j].clear();
         if ((j0 + j) * RPS + step < n) x[j].load(in, base + (size_t)((j0 + j) * RPS + step) * stride);
+      }
+      uint32_t m = 0;
 #pragma unroll
-      for (int j = 0; j < STEPS; ++j)
-        if ((j0 + j) * RPS + step < n) {
+      for (int j = 0; j < STEPS; ++j) m = x[j].top(m);
+      float a = Eight<TYPE>::value(m);
+      if (!(a <= 3.402823466e38f)) {  // infinities and NaN do not set the scale
+        a = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < STEPS; ++j) {
+          if ((j0 + j) * RPS + step >= n) continue;
+          Eight<TYPE> y;
+          y.load(in, base + (size_t)((j0 + j) * RPS + step) * stride);
           float f[8];
-          x[j].values(f);
+          y.values(f);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float a = fabsf(f[k]);
-            amax = a <= 3.402823466e38f ? fmaxf(amax, a) : amax;  // infinities and NaN do not set the scale
-          }
+          for (int k = 0; k < 8; ++k) a = fabsf(f[k]) <= 3.402823466e38f ? fmaxf(a, fabsf(f[k])) : a;
         }
+      }
+      amax = fmaxf(amax, a);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
