@@ -111,13 +111,23 @@ int mqa_kv_attention_workspace_bytes(int device, const mqa_kv_cache *cache, int 
  *            ignored; a position listed twice counts twice
  *  out       [rows, q_heads, head_dim] of q's type, contiguous, 16-byte aligned
  *  lse       NULL, or [rows, q_heads] fp32: the logarithm of the softmax's sum
+ *  scale     in (0, 65536]
  *  max_rows  the most rows any sequence has, if the caller knows it, else 0: it
  *            only chooses the kernels (any value gives correct results)
  * A row that sees nothing gives zeros and lse = -inf.  A NaN code in a key or
  * value that a row sees gives NaN in every component of the heads it serves,
- * and is without effect on rows that do not see it.  Dot products, softmax
- * statistics and sums are held in fp32; the softmax weights enter the product
- * with V in fp16.  `workspace` may be shared by calls that do not overlap. */
+ * and is without effect on rows that do not see it; an infinite or NaN query
+ * value does so for its row and head.  Dot products, softmax statistics and
+ * sums are held in fp32; the softmax weights enter the product with V in fp16
+ * (11 bits, down to 2^-24 of the largest weight times scale).  Query rows are
+ * scaled by a power of two and enter the product with K in fp16, or, where
+ * their sequence has more than 64 (row, head) pairs per key/value head, as sums
+ * of e4m3 terms: what is lost is below 2^-17 of the row's largest magnitude.
+ * Query magnitudes below 2^110 and scores within fp32's range are served.
+ * `out` must not overlap `q`.  `workspace` may be shared by calls that do not
+ * overlap; one for `rows` rows serves every call of fewer rows, whatever
+ * max_rows and `selected`.  Calls that do not write to the cache may overlap,
+ * each with a workspace of its own. */
 int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_stride, int type, int q_heads,
                      const int32_t *row_starts, int rows, int max_rows, const int32_t *selected, int n_selected,
                      int causal, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,

@@ -32,7 +32,8 @@ SOURCES = [("mqa_fused.cu", "mqa_fused.o", []), ("mqa_fused.cu", "mqa_fused_fold
            ("mqa_gather.cu", "mqa_gather.o", []), ("mqa_aux.cu", "mqa_aux.o", []),
            ("mqatopk_api.cu", "mqatopk_api.o", []),
            # the paged key/value cache
-           ("kv_attn.cu", "kv_attn.o", []), ("kv_prefill.cu", "kv_prefill.o", []), ("kv_append.cu", "kv_append.o", []), ("kv_pages.cu", "kv_pages.o", []),
+           ("kv_attn.cu", "kv_attn.o", []), ("kv_prefill.cu", "kv_prefill.o", []),
+           ("kv_append.cu", "kv_append.o", []), ("kv_pages.cu", "kv_pages.o", []),
            ("kv_api.cu", "kv_api.o", [])]
 HEADERS = ["mqa_internal.h", "ptx.cuh", "mqa_fold.h", "kv_internal.h", "kv_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -88,6 +88,8 @@ int code(cudaError_t e) {
   return MQA_ERR_CUDA;
 }
 
+// Times 2^110, the largest power of two that a small query takes, it stays within fp32.
+constexpr float kMaxScale = 65536.f;
 // Which kernels a call runs and where their parts of the workspace lie.  The
 // split kernel (kv_attn.cu) takes blocks of 8 to 32 columns; calls in which
 // a sequence may have more than kTiledFrom columns run the tiled kernel
@@ -189,7 +191,7 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
   int rc = check_attention(cache, rows, q_heads);
   if (rc != MQA_OK) return rc;
   if ((type != MQA_KV_BF16 && type != MQA_KV_FP16) || n_selected < 0 || (!selected && n_selected > 0) ||
-      !(scale > 0.f && scale < 3.4e38f))
+      !(scale > 0.f && scale <= kMaxScale))
     return MQA_ERR_INVALID_ARGUMENT;
   if (rows == 0) return MQA_OK;
   if (!q || !out || !row_starts || !workspace ||

@@ -93,27 +93,6 @@ size_t attn_slot_floats(int nb, int dim) { return (size_t)8 * nb * (dim + 4); }
 
 namespace {
 
-// Wait for a warp's copies; once a wait has run out (2 s) the CTA's waits return
-// at once, and it runs to its end on what it finds.
-template <typename S>
-__device__ __forceinline__ void wait_full(S &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
-  if (mbar_try_wait(bar, parity)) return;
-  unsigned long long t0 = 0;
-  for (int i = 0;; ++i) {
-    if (mbar_try_wait(bar, parity)) return;
-    if ((i & 15) == 15) {
-      if (*reinterpret_cast<volatile int *>(&sm.dead)) return;
-      const unsigned long long now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > 2000000000ULL) {
-        *reinterpret_cast<volatile int *>(&sm.dead) = 1;
-        atomicOr(status, MQA_KV_DEV_WAIT_TIMEOUT);
-        return;
-      }
-    }
-  }
-}
-
 template <int D, int NB, bool SEL>
 __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
     kv_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap k_map,
@@ -456,7 +435,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
       for (int i = 0; i < iters; ++i, ++done) {
         const int stage = done % kStages;
         if (SEL) cp_async_wait<kStages - 2>();
-        else wait_full(sm, &sm.full[warp][stage], done / kStages & 1, p.c.status);
+        else bounded_wait(sm, &sm.full[warp][stage], done / kStages & 1, p.c.status);
         __syncwarp();
         if (!meta.any[stage]) {  // no key of the sub-tile is seen
           __syncwarp();
@@ -745,6 +724,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
       }
     }
   }
+  if (!SEL)  // the copies have landed before the CTA leaves, also where a wait has run out
+    for (uint32_t i = 1; i <= kStages && i <= copies; ++i)
+      drain(&sm.full[warp][(copies - i) % kStages], (copies - i) / kStages & 1);
   grid_wait();
 }
 

@@ -45,7 +45,6 @@ constexpr int kCols = kTiledCols;         // columns per item
 constexpr int kStagesK = 3, kStagesV = 2;
 constexpr int kMeta = 8;                  // tile descriptions in flight
 constexpr int kTerms = kQueryTerms;       // e4m3 terms of a query value (bf16: 2)
-constexpr long long kWaitNs = 2000000000LL;
 constexpr int kNear = 2;                  // tiles by which a part's end may move (partial results cost about as much)
 constexpr int kConverters = 128;
 
@@ -182,33 +181,6 @@ __device__ __forceinline__ void step_on(const AttnParams &p, Walk &w) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) w.next(p);
   __syncwarp();
-}
-
-// ------------------------------------------------------------------ waits
-template <int D>
-__device__ __forceinline__ void wait(Smem<D> &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
-  if (mbar_try_wait(bar, parity)) return;
-  unsigned long long t0 = 0;
-  for (int i = 0;; ++i) {
-    if (mbar_try_wait(bar, parity)) return;
-    if ((i & 15) == 15) {
-      if (*reinterpret_cast<volatile int *>(&sm.dead)) return;
-      const unsigned long long now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitNs) {
-        *reinterpret_cast<volatile int *>(&sm.dead) = 1;
-        atomicOr(status, MQA_KV_DEV_WAIT_TIMEOUT);
-        return;
-      }
-    }
-  }
-}
-
-// The same for copies in flight, also after another wait has run out.
-__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
-  const unsigned long long t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kWaitNs) {
-  }
 }
 
 // ------------------------------------------------------------------ tcgen05
@@ -353,7 +325,7 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
       const uint32_t copies = __ballot_sync(~0u, row >= 0 && g % per_box == 0);
       for (int u = 0; u < min(4, nt - tb); ++u, ++tile_no) {
         const int slot = tile_no % kMeta, stage = tile_no % kStagesK;
-        wait(sm, &sm.m_empty[slot], (tile_no / kMeta & 1) ^ 1, p.c.status);
+        bounded_wait(sm, &sm.m_empty[slot], (tile_no / kMeta & 1) ^ 1, p.c.status);
         TileMeta &meta = sm.meta[slot];
         if (lane >> 3 == u) {
           meta.row[g] = row;
@@ -369,7 +341,7 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
             meta.odd = (bad >> (8 * u) & 255u) != 0;
           }
         }
-        wait(sm, &sm.k_empty[stage], (tile_no / kStagesK & 1) ^ 1, p.c.status);
+        bounded_wait(sm, &sm.k_empty[stage], (tile_no / kStagesK & 1) ^ 1, p.c.status);
         const uint32_t mine = copies >> (8 * u) & 255u;
         __syncwarp();
         if (lane == 0) {
@@ -380,7 +352,7 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
         if (lane >> 3 == u && (mine >> g & 1))
           tma_load_2d(sm.k[stage] + g * 16 * D, &map, &sm.k_full[stage], 0, row, keep);
         if (tb + u == 0 && !begins) {  // once the previous part's last scores are done
-          wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p.c.status);
+          bounded_wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p.c.status);
           ask();
         }
       }
@@ -436,7 +408,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
   for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p);
     if (nt == 0) continue;  // nothing is read
-    wait(sm, &sm.m_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
+    bounded_wait(sm, &sm.m_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) load(tile_no, i);
 
@@ -450,8 +422,8 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
         any |= nan_bytes(x[i].x) | nan_bytes(x[i].y) | nan_bytes(x[i].z) | nan_bytes(x[i].w);
       if (any) take_nan_out<STEPS, RPS>(x, sm.meta[tile_no % kMeta], r0);
       mbar_arrive(&sm.n_full[tile_no % kMeta]);
-      if (t + 1 < nt) wait(sm, &sm.m_full[(tile_no + 1) % kMeta], (tile_no + 1) / kMeta & 1, p.c.status);
-      wait(sm, &sm.v_empty[stage], (tile_no / kStagesV & 1) ^ 1, p.c.status);
+      if (t + 1 < nt) bounded_wait(sm, &sm.m_full[(tile_no + 1) % kMeta], (tile_no + 1) / kMeta & 1, p.c.status);
+      bounded_wait(sm, &sm.v_empty[stage], (tile_no / kStagesV & 1) ^ 1, p.c.status);
       uint8_t *dst = sm.v[stage];
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
@@ -505,13 +477,13 @@ __device__ void mma_role(const AttnParams &p, Smem<D> &sm) {
       const uint32_t kn = tile_no + t + 1, vn = tile_no + t;
       const int ks = kn % kStagesK, vs = vn % kStagesV;
       const bool more = t + 1 < nt;
-      if (more) wait(sm, &sm.k_full[ks], kn / kStagesK & 1, p.c.status);
-      if (t < 0) wait(sm, &sm.q_full, q_no & 1, p.c.status);
-      else wait(sm, &sm.v_full[vs], vn / kStagesV & 1, p.c.status);
+      if (more) bounded_wait(sm, &sm.k_full[ks], kn / kStagesK & 1, p.c.status);
+      if (t < 0) bounded_wait(sm, &sm.q_full, q_no & 1, p.c.status);
+      else bounded_wait(sm, &sm.v_full[vs], vn / kStagesV & 1, p.c.status);
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         const bool on = x == 0 || two;
-        if (t >= 0) wait(sm, &sm.p_full[x], p_no++ >> 1 & 1, p.c.status);
+        if (t >= 0) bounded_wait(sm, &sm.p_full[x], p_no++ >> 1 & 1, p.c.status);
         __syncwarp();
         tc_fence_after();
         if (elect_one()) {
@@ -538,7 +510,7 @@ __device__ void mma_role(const AttnParams &p, Smem<D> &sm) {
   }
   if (elect_one()) umma_commit(&sm.done);
   __syncwarp();
-  wait(sm, &sm.done, 0, p.c.status);
+  drain(&sm.done, 0);  // no product is under way when the CTA leaves
   __syncwarp();
 }
 
@@ -678,8 +650,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
     const int col = x * 128 + r;
     if (ncols <= x * 128) {  // this half is empty: it keeps step, so that it meets every phase of the barriers
       for (int t = 0; t < nt; ++t, ++tile_no) {
-        wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
-        wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);  // without it this half could run ahead of the issuing warp
+        bounded_wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
+        bounded_wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);  // without it this half could run ahead of the issuing warp
         mbar_arrive(&sm.p_full[x]);
       }
       continue;
@@ -694,8 +666,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
     room0 -= w.x.t0 * kKeys;
     const int whole_tiles = __reduce_min_sync(~0u, room0) / kKeys;  // tiles every column of the warp sees whole
     for (int t = 0; t < nt; ++t, ++tile_no) {
-      wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
-      wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);
+      bounded_wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
+      bounded_wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);
       __syncwarp();
       tc_fence_after();
       const TileMeta &meta = sm.meta[tile_no % kMeta];
@@ -779,7 +751,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
     }
     // ---- the part's result
     if (nt) {
-      wait(sm, &sm.o_full[x], o_no++ & 1, p.c.status);
+      bounded_wait(sm, &sm.o_full[x], o_no++ & 1, p.c.status);
       __syncwarp();
       tc_fence_after();
     }

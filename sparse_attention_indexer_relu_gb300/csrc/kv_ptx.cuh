@@ -136,6 +136,34 @@ __device__ __forceinline__ uint32_t float2_to_bf162(float a, float b) {
   return w;
 }
 
+// Wait for a barrier's phase.  Once a wait of the CTA has run out (2 s), its
+// waits return at once and it runs to its end on what it finds.
+constexpr unsigned long long kWaitNs = 2000000000ULL;
+template <typename S>
+__device__ __forceinline__ void bounded_wait(S &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
+  if (mbar_try_wait(bar, parity)) return;
+  unsigned long long t0 = 0;
+  for (int i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((i & 15) == 15) {
+      if (*reinterpret_cast<volatile int *>(&sm.dead)) return;
+      const unsigned long long now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitNs) {
+        *reinterpret_cast<volatile int *>(&sm.dead) = 1;
+        atomicOr(status, MQA_KV_DEV_WAIT_TIMEOUT);
+        return;
+      }
+    }
+  }
+}
+// The same for copies and products in flight, also after another wait has run out.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kWaitNs) {
+  }
+}
+
 template <typename... Params, typename... Args>
 inline cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                                 bool follows, Args &&...args) {

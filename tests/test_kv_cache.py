@@ -94,6 +94,7 @@ def attention(c=None, q=0x1000, stride=4096, type=0, heads=32, starts=0x2000, ro
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=-1), 1), (dict(type=2), 1), (dict(type=-1), 1), (dict(heads=30), 1), (dict(heads=0), 1),
     (dict(heads=1 << 17), 1), (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
+    (dict(scale=65537.0), 1), (dict(scale=-1.0), 1),
     (dict(nsel=-1, sel=0x1000), 1), (dict(nsel=5), 1), (dict(q=0), 1), (dict(out=0), 1), (dict(starts=0), 1),
     (dict(ws=0), 1), (dict(stride=4088), 1), (dict(stride=4100), 2), (dict(q=0x1008), 2), (dict(out=0x3004), 2),
     (dict(starts=0x2002), 2), (dict(sel=0x1002, nsel=5), 2), (dict(lse=0x1002), 2), (dict(ws=0x100010), 2)])
