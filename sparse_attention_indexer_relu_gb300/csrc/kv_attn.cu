@@ -27,7 +27,16 @@
 // Split.  All items' key tiles form one line that is cut evenly between the
 // CTAs of a fixed grid, whatever the lengths; a CTA's range begins and ends
 // inside items, for which it leaves partial results in its two workspace
-// slots, and a second kernel joins them in CTA order.
+// slots, and a second kernel joins them in a fixed order.
+//
+// What bounds it.  Single tokens over long caches: HBM (32 sequences of 16K to
+// 64K positions, 8 key/value heads of 128: 2.68 GB in 400 us, 6.7 TB/s, 99% of
+// the measured copy rate; 310 instructions per 16 keys, issue slots 42% busy).
+// More columns, or keys picked one by one: instructions and their latencies at
+// the 12 warps per SM that the accumulators leave room for (16 x 5 fp16 rows, 4
+// heads per key/value head of 64: 372 per 16 keys, 33 us, 1.35 TB/s; 2,492 rows
+// with 512 selected keys each, 16 heads per key/value head of 128: 690 per 16
+// keys, issue slots 52% busy, 180 us, 116 TFLOP/s out of L2).
 #include "kv_internal.h"
 #include "kv_ptx.cuh"
 
@@ -39,9 +48,13 @@ namespace {
 
 constexpr int kWarps = kAttnThreads / 32;
 constexpr int kTile = 16 * kWarps;  // keys per unit of work: one 16-key sub-tile per warp
-constexpr int kStages = 3;          // sub-tiles in flight per warp: 2 x 16 warps x 4 KB ahead on an SM
+// Sub-tiles in flight per warp: 2 x 16 warps x 4 KB ahead on an SM.  Long caches
+// take 396 us with three stages and 429 with two (or with five CTAs of two: 460).
+constexpr int kStages = 3;
 
-// CTAs per SM: what its registers allow without spilling in the loop.
+// CTAs per SM: what its registers allow without much spilling in the loop (16
+// columns of 128, four CTAs of 128 registers instead of three: 180 -> 275 us for
+// selected prompts; 24 of 64, four instead of three: 34 -> 38 us).
 template <int D, int NB>
 struct Cfg {
   static constexpr int ctas = D == 64 ? (NB == 1 ? 5 : NB <= 3 ? 3 : 2) : (NB == 1 ? 4 : NB == 2 ? 3 : 2);
@@ -798,8 +811,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb
 }
 
 // The same for the tiled kernel's items: many columns, few parts.  A warp has 4
-// columns, one part's loads of all of them in flight (ragged prompts: 9 us,
-// against 13 with a warp per column and all parts' loads in a row).
+// columns, one part's loads of all of them in flight (9 us after 5 prompts of up
+// to 1,531 rows, latency).
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_few_kernel(const AttnParams p) {
   grid_wait();

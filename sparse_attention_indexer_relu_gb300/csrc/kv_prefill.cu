@@ -27,6 +27,14 @@
 // Every wait has a time limit; once one has run out, all of them return at
 // once and the kernel runs to its end on whatever it finds in shared memory.
 //
+// What bounds it: the softmax of a 128 x 128 half tile, about 2,500 cycles of
+// two maxima, two exponentials' arguments, one exponential and a rounding per
+// score, against 2,048 of its MMAs; the clock under that load is about 1.5 GHz.
+// 2,048 rows at the end of 32K positions (32 heads, 8 key/value heads of 128):
+// 924 us, 1.15 PFLOP/s, 59% of the measured bf16 rate.  Five prompts of up to
+// 1,531 rows: 95 us, of which 13 for the query terms, 5 to find the parts, 7
+// until the first scores are there, 9 to join.
+//
 // Work is cut like kv_attn.cu's: the key tiles of all items in one line, even
 // parts per CTA, partial results in two slots per CTA and a joining pass.  The
 // position of a part is found from the exact number of tiles that causal
@@ -45,7 +53,10 @@ constexpr int kCols = kTiledCols;         // columns per item
 constexpr int kStagesK = 3, kStagesV = 2;
 constexpr int kMeta = 8;                  // tile descriptions in flight
 constexpr int kTerms = kQueryTerms;       // e4m3 terms of a query value (bf16: 2)
-constexpr int kNear = 2;                  // tiles by which a part's end may move (partial results cost about as much)
+// Tiles by which a part's end may move to its item's: partial results and their
+// joining cost about as much.  (Up to an eighth of the part: the chunk of 32K
+// positions 925 -> 1,071 us, for want of balance.)
+constexpr int kNear = 2;
 constexpr int kConverters = 128;
 
 // sum over 0 <= i < n of floor((a i + b) / m); a, b >= 0, m > 0.  Whole parts
@@ -700,7 +711,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
             for (int b = 0; b < kKeys; ++b)
               if (b >= room) s[b] = 0xFF800000u;
           }
-          // Pairs of scores pass through three steps, kLag pairs apart, so that the
+          // Pairs of scores pass through three steps, kLag pairs apart (6 or 8: 923 us
+          // for the chunk of 32K positions; 4: 945), so that the
           // exponentials of one overlap the products of another and the sums and
           // roundings of a third: product and offset; 2^x; sum and fp16.
           constexpr int kLag = 6;
@@ -948,7 +960,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   grid_wait();  // the query terms
-  // registers: 256 x 192 + 128 x 80 + 128 x 48 = 512 x 128, what the block was launched with
+  // Registers: 256 x 192 + 128 x 80 + 128 x 48 = 512 x 128, what the block was
+  // launched with.  (Chunk of 32K positions: 924 us; with 184, 96 and 48: 1,007;
+  // with 208, 56 and 40: 1,416.)
   if (warp < 8) {
     reg_inc<192>();
     softmax_role<D>(p, sm, per, near);
@@ -966,7 +980,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 12) tmem_dealloc(sm.tmem, 512);
 }
 
-// Query terms: D / 8 lanes per (row, head), 8 values each.  Terms go to planes
+// Query terms: D / 8 lanes per (row, head), 8 values each (90K rows of 128: 13.4 us, 3.4
+// TB/s).  Terms go to planes
 // [term][key/value head][row][head of the group][D], factors to [key/value
 // head][row][head of the group].
 template <int D>
