@@ -73,7 +73,7 @@ typedef struct mqa_kv_cache {
   int kv_heads;             /* 1 .. 256 */
   int head_dim;             /* 64 or 128 */
   int max_seqs;             /* 1 .. MQA_KV_MAX_SEQS */
-  int max_pages;            /* columns of page_table; max_pages * page_size < 2^31 */
+  int max_pages;            /* columns of page_table; max_pages * page_size <= 2^30 */
   int n_extra;              /* further pools whose pages move along (an indexer's keys and scales) */
   mqa_kv_pool extra[MQA_KV_MAX_EXTRA];
 } mqa_kv_cache;

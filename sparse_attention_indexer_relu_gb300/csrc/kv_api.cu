@@ -25,7 +25,7 @@ int check_cache(const mqa_kv_cache *c, int needs) {
       c->max_pages < 1 || c->n_extra < 0 || c->n_extra > MQA_KV_MAX_EXTRA)
     return MQA_ERR_INVALID_ARGUMENT;
   if ((long long)c->num_pages * c->kv_heads * c->page_size > INT_MAX ||
-      (long long)c->max_pages * c->page_size > INT_MAX)
+      (long long)c->max_pages * c->page_size > 1 << 30)  // positions, with room for a tile behind the last
     return MQA_ERR_INVALID_ARGUMENT;
   if (!c->k || !c->v || !c->k_exps || !c->v_exps || !c->scratch) return MQA_ERR_INVALID_ARGUMENT;
   if ((needs & kTables) && (!c->page_table || !c->seq_lens)) return MQA_ERR_INVALID_ARGUMENT;

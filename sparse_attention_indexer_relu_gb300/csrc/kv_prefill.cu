@@ -672,7 +672,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
     if (col < ncols) {
       const int c = w.x.block * kCols + col;
       room0 = p.causal ? min(max(w.x.q.len - w.x.q.n + c / p.group + 1, 0), w.x.q.len) : w.x.q.len;
-      cs = __ldg(p.q_scale + (size_t)w.x.head * p.rows * p.group + (size_t)w.x.q.r0 * p.group + c);
+      cs = __ldcg(p.q_scale + (size_t)w.x.head * p.rows * p.group + (size_t)w.x.q.r0 * p.group + c);
     }
     room0 -= w.x.t0 * kKeys;
     const int whole_tiles = __reduce_min_sync(~0u, room0) / kKeys;  // tiles every column of the warp sees whole
