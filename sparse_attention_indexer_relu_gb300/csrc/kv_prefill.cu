@@ -414,7 +414,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
     const int r = i * RPS + r0;
     const int row = sm.meta[no % kMeta].row[r >> 4];
     x[i] = make_uint4(0, 0, 0, 0);
-    if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(p.c.v + (size_t)(row + (r & 15)) * D + ch * 16));
+    if (row >= 0) x[i] = __ldcg(reinterpret_cast<const uint4 *>(p.c.v + (size_t)(row + (r & 15)) * D + ch * 16));
   };
   for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p);
