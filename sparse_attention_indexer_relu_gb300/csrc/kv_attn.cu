@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
                 const float mc = m[nb][c], wc = w[nb][c], mr = mc == -INFINITY ? 0.f : mc, wr = mc == -INFINITY ? 0.f : wc;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                  const float f = cs[nb][c] * ks[r];
+                  const float f = score_factor(cs[nb][c], ks[r]);
                   p2[r][c] = ex2(fmaf(acc[nb][2 * r + c], f, none[r] + (lv[r] - wr)));
                   pl[nb][c][r] = SEL ? ex2(fmaf(acc[nb][2 * r + c], f, none[r] - mr)) : p2[r][c];
                 }
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                   for (int c = 0; c < 2; ++c) {
-                    const float f = cs[nb][c] * ks[0], mr = m[nb][c] == -INFINITY ? 0.f : m[nb][c];
+                    const float f = score_factor(cs[nb][c], ks[0]), mr = m[nb][c] == -INFINITY ? 0.f : m[nb][c];
                     pl[nb][c][0] = ex2(fmaf(acc[nb][c], f, -mr)) + ex2(fmaf(acc[nb][2 + c], f, -mr));
                   }
               }
@@ -592,8 +592,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const float s0 = fmaf(acc[nb][c], cs[nb][c] * ks[0], none[0]);
-                const float s1 = fmaf(acc[nb][2 + c], cs[nb][c] * ks[1], none[1]);
+                const float s0 = fmaf(acc[nb][c], score_factor(cs[nb][c], ks[0]), none[0]);
+                const float s1 = fmaf(acc[nb][2 + c], score_factor(cs[nb][c], ks[1]), none[1]);
                 float a = fmaxf(s0, s1), b = fmaxf(s0 + lv[0], s1 + lv[1]);
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) {

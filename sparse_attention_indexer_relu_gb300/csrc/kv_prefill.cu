@@ -588,22 +588,17 @@ __device__ __forceinline__ void largest(const uint32_t *v, float f, float lv, fl
 // references), so a tile's spread of lv tells when to look.
 constexpr float kFar = 64.f;
 template <int D>
-__device__ __forceinline__ void settle(uint32_t ts, uint32_t to, const TileMeta &meta, int room, float cs, bool has_o,
+__device__ __forceinline__ void settle(uint32_t ts, uint32_t to, const TileMeta &meta, float cs, bool has_o,
                                     float &m, float &w, float &l) {
   float top = -INFINITY, topw = -INFINITY;
 #pragma unroll 1
-  for (int j = 0; j < 2; ++j, room -= 64) {
+  for (int j = 0; j < 2; ++j) {
     uint32_t s[64];
     tmem_ld_32x32b_x32(ts + 64 * j, *reinterpret_cast<uint32_t(*)[32]>(s));
     tmem_ld_32x32b_x32(ts + 64 * j + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
     tmem_ld_wait();
-    if (__any_sync(~0u, room < 64)) {
 #pragma unroll
-      for (int b = 0; b < 64; ++b)
-        if (b >= room) s[b] = 0xFF800000u;
-    }
-#pragma unroll
-    for (int g = 0; g < 4; ++g) largest(s + 16 * g, cs * meta.kv[4 * j + g].x, meta.kv[4 * j + g].y, top, topw);
+    for (int g = 0; g < 4; ++g) largest(s + 16 * g, score_factor(cs, meta.kv[4 * j + g].x), meta.kv[4 * j + g].y, top, topw);
   }
   const float mn = fmaxf(m, top), wn = fmaxf(w, topw);
   const float fl = mn == m ? 1.f : ex2(m - mn), fo = wn == w ? 1.f : ex2(w - wn);
@@ -622,14 +617,13 @@ __device__ __forceinline__ void settle(uint32_t ts, uint32_t to, const TileMeta 
   }
 }
 // Weights of a tile whose value scales are that far apart, 16 keys at a time.
-__device__ __noinline__ float weigh_far(uint32_t ts, const TileMeta &meta, int room, float cs, float m, float w,
-                                        float l) {
+__device__ __noinline__ float weigh_far(uint32_t ts, const TileMeta &meta, float cs, float m, float w, float l) {
   const float mr = m == -INFINITY ? 0.f : m, wr = w == -INFINITY ? 0.f : w;
 #pragma unroll 1
   for (int g = 0; g < 8; ++g) {
     uint32_t s[16];
     tmem_ld16(ts + 16 * g, s);
-    const float f = cs * meta.kv[g].x, lv = meta.kv[g].y;
+    const float f = score_factor(cs, meta.kv[g].x), lv = meta.kv[g].y;
     tmem_ld_wait();
     uint32_t h[8];
 #pragma unroll
@@ -637,7 +631,7 @@ __device__ __noinline__ float weigh_far(uint32_t ts, const TileMeta &meta, int r
       float y[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const float x = 16 * g + 2 * k + b < room ? __uint_as_float(s[2 * k + b]) * f : -INFINITY;
+        const float x = __uint_as_float(s[2 * k + b]) * f;
         l += ex2(x - mr);
         y[b] = ex2(x + (lv - wr));
       }
@@ -646,6 +640,22 @@ __device__ __noinline__ float weigh_far(uint32_t ts, const TileMeta &meta, int r
     tmem_st8(ts + 8 * g, h);
   }
   return l;
+}
+
+// Scores of keys at or behind the column's limit, in TMEM.
+__device__ __noinline__ void hide_behind(uint32_t ts, int room) {
+#pragma unroll 1
+  for (int j = 0; j < kKeys; j += 32) {
+    if (__all_sync(~0u, room >= j + 32)) continue;
+    uint32_t s[32];
+    tmem_ld_32x32b_x32(ts + j, s);
+    tmem_ld_wait();
+#pragma unroll
+    for (int b = 0; b < 32; ++b)
+      if (j + b >= room) s[b] = 0xFF800000u;
+    tmem_st32(ts + j, s);
+  }
+  tmem_st_wait();
 }
 
 template <int D>
@@ -684,16 +694,17 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
       const TileMeta &meta = sm.meta[tile_no % kMeta];
       const int room = room0 - t * kKeys;  // keys of the tile that the column sees
       if (meta.odd) hide_keys(ts, meta);
+      if (t >= whole_tiles) hide_behind(ts, room);
       // The weights are formed with the references as they stand.  A tile in which
       // 16 of them sum to more than 2^12 (or the scores pass m by as much) is done
       // again with new references: its scores are still in TMEM then.  The first
       // tile has its references set first.
       const bool look = meta.spread > kFar - 16.f;
       for (bool anew = t == 0;; anew = true) {
-        if (anew) settle<D>(ts, to, meta, room, cs, t > 0, m, wr, l);
+        if (anew) settle<D>(ts, to, meta, cs, t > 0, m, wr, l);
         if (look && __any_sync(~0u, wr - meta.lv_min - m > kFar)) {
           if (!anew) continue;
-          l = weigh_far(ts, meta, room, cs, m, wr, l);
+          l = weigh_far(ts, meta, cs, m, wr, l);
           break;
         }
         uint32_t s[128];
@@ -705,12 +716,6 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
           for (int j = 2; j < 4; ++j) tmem_ld_32x32b_x32(ts + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
           const float mr = m == -INFINITY ? 0.f : m, ww = wr == -INFINITY ? 0.f : wr;
           float lt = 0.f, most = 0.f;
-          if (t >= whole_tiles) {
-            tmem_ld_wait();
-#pragma unroll
-            for (int b = 0; b < kKeys; ++b)
-              if (b >= room) s[b] = 0xFF800000u;
-          }
           // Pairs of scores pass through three steps, kLag pairs apart (6 or 8: 923 us
           // for the chunk of 32K positions; 4: 945), so that the
           // exponentials of one overlap the products of another and the sums and
@@ -725,7 +730,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
               if (i == 32) tmem_ld_wait();
               if (i % 8 == 0) {
                 const float2 kv = meta.kv[i / 8];
-                const float f = cs * kv.x, b = kv.y - ww;
+                const float f = score_factor(cs, kv.x), b = kv.y - ww;
                 f2 = pack2(f, f), b2 = pack2(b, b);
                 back[i / 8] = ex2(-b - mr);
               }

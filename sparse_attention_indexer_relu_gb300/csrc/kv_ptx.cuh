@@ -31,6 +31,11 @@ __device__ __forceinline__ float exp_byte(uint32_t e) { return __uint_as_float(m
 __device__ __forceinline__ void grid_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Factor of a product's scores: what a column's are multiplied with times a
+// block's scale.  Never zero, which would turn a masked score (-inf) into NaN
+// (the least normal number that is added changes no factor above 2^-101).
+__device__ __forceinline__ float score_factor(float column, float block) { return fmaf(column, block, 0x1p-126f); }
+
 // e4m3 code pair (low 16 bits) to fp16 pair.
 __device__ __forceinline__ uint32_t cvt2(uint32_t w) {
   uint32_t r;

@@ -367,6 +367,16 @@ def test_offsets_past_32_bits(mqa):
     assert torch.equal(mqa.kv_attention(q, dev, ints(st)), want)
 
 
+@pytest.mark.parametrize("rows", [3, 70])
+def test_tiny_queries_and_scales(mqa, rows):
+    """Scores whose factor leaves fp32's range: all alike, and masked keys stay masked."""
+    rng = np.random.default_rng(66)
+    c = ref.random_cache(rng, 12, 1, 16, 64, [100], 8)
+    c.ke[:] = 7
+    attend(mqa, c, rng, [rows], 4, q_scale=1e-30)
+    attend(mqa, c, rng, [rows], 4, q_scale=1e-30, selected=random_selection(rng, c, [rows], 20))
+
+
 # ---------------------------------------------------------------- selected keys
 def random_selection(rng, c, rows, k, seen_only=False):
     sel = []
