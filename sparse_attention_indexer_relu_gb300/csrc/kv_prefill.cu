@@ -27,12 +27,14 @@
 // Every wait has a time limit; once one has run out, all of them return at
 // once and the kernel runs to its end on whatever it finds in shared memory.
 //
-// What bounds it: the softmax of a 128 x 128 half tile, about 2,500 cycles of
-// two maxima, two exponentials' arguments, one exponential and a rounding per
-// score, against 2,048 of its MMAs; the clock under that load is about 1.5 GHz.
+// What bounds it: a half's chain of weights (about 1,750 cycles for 128 x 128),
+// their product and the next scores (1,024), 3,100 cycles per tile with its
+// waits, against 2,048 of both halves' MMAs.  (Scores of 64 keys per MMA, the
+// upper ones ahead of the product, would break the chain, but then the queries
+// are read from shared memory twice as often: 894 us instead of 718.)
 // 2,048 rows at the end of 32K positions (32 heads, 8 key/value heads of 128):
-// 924 us, 1.15 PFLOP/s, 59% of the measured bf16 rate.  Five prompts of up to
-// 1,531 rows: 95 us, of which 13 for the query terms, 5 to find the parts, 7
+// 720 us, 1.48 PFLOP/s, 76% of the measured bf16 rate.  Five prompts of up to
+// 1,531 rows: 90 us, of which 13 for the query terms, 5 to find the parts, 7
 // until the first scores are there, 9 to join.
 //
 // Work is cut like kv_attn.cu's: the key tiles of all items in one line, even
@@ -54,8 +56,8 @@ constexpr int kStagesK = 3, kStagesV = 2;
 constexpr int kMeta = 8;                  // tile descriptions in flight
 constexpr int kTerms = kQueryTerms;       // e4m3 terms of a query value (bf16: 2)
 // Tiles by which a part's end may move to its item's: partial results and their
-// joining cost about as much.  (Up to an eighth of the part: the chunk of 32K
-// positions 925 -> 1,071 us, for want of balance.)
+// joining cost about as much.  (Up to an eighth of the part made the chunk of 32K
+// positions 16% slower, for want of balance.)
 constexpr int kNear = 2;
 constexpr int kConverters = 128;
 
@@ -414,6 +416,8 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
     const int r = i * RPS + r0;
     const int row = sm.meta[no % kMeta].row[r >> 4];
     x[i] = make_uint4(0, 0, 0, 0);
+    // (past the L1, of which shared memory leaves little: spills live there, and the
+    // chunk of 32K positions takes 799 us so and 920 with loads that allocate in it)
     if (row >= 0) x[i] = __ldcg(reinterpret_cast<const uint4 *>(p.c.v + (size_t)(row + (r & 15)) * D + ch * 16));
   };
   for (; w.valid(); step_on(p, w)) {
@@ -694,7 +698,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
       const TileMeta &meta = sm.meta[tile_no % kMeta];
       const int room = room0 - t * kKeys;  // keys of the tile that the column sees
       if (meta.odd) hide_keys(ts, meta);
-      if (t >= whole_tiles) hide_behind(ts, room);
+      if (t >= whole_tiles) hide_behind(ts, room);  // (not below: 128 live scores and a branch spill)
       // The weights are formed with the references as they stand.  A tile in which
       // 16 of them sum to more than 2^12 (or the scores pass m by as much) is done
       // again with new references: its scores are still in TMEM then.  The first
@@ -716,8 +720,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
           for (int j = 2; j < 4; ++j) tmem_ld_32x32b_x32(ts + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
           const float mr = m == -INFINITY ? 0.f : m, ww = wr == -INFINITY ? 0.f : wr;
           float lt = 0.f, most = 0.f;
-          // Pairs of scores pass through three steps, kLag pairs apart (6 or 8: 923 us
-          // for the chunk of 32K positions; 4: 945), so that the
+          // Pairs of scores pass through three steps, kLag pairs apart (4, 6 or 8
+          // are alike within 1%), so that the
           // exponentials of one overlap the products of another and the sums and
           // roundings of a third: product and offset; 2^x; sum and fp16.
           constexpr int kLag = 6;
@@ -966,8 +970,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   grid_wait();  // the query terms
   // Registers: 256 x 192 + 128 x 80 + 128 x 48 = 512 x 128, what the block was
-  // launched with.  (Chunk of 32K positions: 924 us; with 184, 96 and 48: 1,007;
-  // with 208, 56 and 40: 1,416.)
+  // launched with.  (Chunk of 32K positions: 720 us; with 184, 96 and 48: 735; with
+  // 200, 72 and 40 the converters spill: 1,360 instead of 799 at the time.)
   if (warp < 8) {
     reg_inc<192>();
     softmax_role<D>(p, sm, per, near);
