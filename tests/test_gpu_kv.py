@@ -522,6 +522,36 @@ def test_calls_follow_one_another_without_a_pause(mqa):
         assert torch.equal(a, b)
 
 
+def test_prompts_on_two_streams_from_two_threads(mqa):
+    """Calls for many columns that overlap, a workspace each: the same bits as one at a time."""
+    import threading
+
+    import torch
+    rng = np.random.default_rng(67)
+    c = ref.random_cache(rng, 130, 2, 32, 128, [2000, 700, 900], 70)
+    dev = ref.to_device(c, mqa)
+    q, _ = rows_of(rng, 500, 8, 128, "bf16")
+    st = ints([0, 300, 301, 500])
+    want = mqa.kv_attention(q, dev, st)
+    torch.cuda.synchronize()
+    outs = [[], []]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            ws = mqa.alloc_kv_workspace(dev, 500, 8)
+            for _ in range(20):
+                outs[i].append(mqa.kv_attention(q, dev, st, workspace=ws))
+        s.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(outs[0]) == len(outs[1]) == 20
+    assert all(torch.equal(o, want) for o in outs[0] + outs[1]) and mqa.kv_status(dev) == 0
+
+
 # ---------------------------------------------------------------- appending
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("case", [(16, 1, 128, [1], [1]), (64, 2, 64, [64, 65, 200, 5], [1, 2, 130, 0]),
