@@ -121,7 +121,7 @@ int mqa_kv_attention_workspace_bytes(int device, const mqa_kv_cache *cache, int 
  * sums are held in fp32; the softmax weights enter the product with V in fp16
  * (11 bits, down to 2^-24 of the largest weight times scale).  Query rows are
  * scaled by a power of two and enter the product with K in fp16, or, where
- * their sequence has more than 64 (row, head) pairs per key/value head, as sums
+ * their sequence has more than 32 (row, head) pairs per key/value head, as sums
  * of e4m3 terms: what is lost is below 2^-17 of the row's largest magnitude.
  * Query magnitudes below 2^110 and scores within fp32's range are served.
  * `out` must not overlap `q`.  `workspace` may be shared by calls that do not

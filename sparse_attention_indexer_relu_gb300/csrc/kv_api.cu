@@ -91,14 +91,17 @@ int code(cudaError_t e) {
 // Times 2^110, the largest power of two that a small query takes, it stays within fp32.
 constexpr float kMaxScale = 65536.f;
 // Which kernels a call runs and where their parts of the workspace lie.  The
-// split kernel (kv_attn.cu) takes blocks of 8 to 32 columns; calls in which
-// a sequence may have more than kTiledFrom columns run the tiled kernel
-// (kv_prefill.cu), and leave sequences of up to kSplitCols to the split kernel:
-// beside a prompt of 2,048 rows, 63 single tokens at 32K positions take 0.81 ms
-// so, and 2.46 ms with every sequence in the tiled kernel.  The host does not
-// know whether there are such sequences; a call without any pays the 5 us of
+// split kernel (kv_attn.cu) takes blocks of 8 to 32 columns; calls in which a
+// sequence may have more, for which it would read the cache twice, run the tiled
+// kernel (kv_prefill.cu).  8 sequences of 8K positions, 8 heads of 128, split
+// and tiled: 32 columns 60 and 88 us, 48: 94 and 88, 64: 95 and 87, 128: 167 and
+// 77; one of 32K: 44 and 62, 58 and 63, 60 and 63, 93 and 59.  Such calls leave
+// sequences of up to kSplitCols to the split kernel (16 columns: 40 and 46 us):
+// beside a prompt of 2,048 rows, 63 single tokens at 32K positions take 0.80 ms
+// so, and 1.90 ms with every sequence in the tiled kernel.  The host does not
+// know whether there are such sequences; a call without any pays the 6 us of
 // two launches that find no work.
-constexpr int kTiledFrom = 64;
+constexpr int kTiledFrom = 32;
 constexpr int kSplitCols = 16;
 struct AttnPlan {
   bool split, tiled;
