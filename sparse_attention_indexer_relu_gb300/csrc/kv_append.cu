@@ -8,16 +8,16 @@
 //
 // At least rows * heads * dim * (input bytes + 1) bytes move, twice (K and V); what
 // bounds it is the chain bounds -> length -> page -> rows of each CTA, four CTAs
-// to an SM (9.3K bf16 rows of 8 heads of 128 to 4 sequences: 16.5 us, 3.5 TB/s;
-// one row for each of 128 sequences: 5 us).  A
-// CTA looks at consecutive rows, finds those that begin a page's new positions
-// (its leaders) and writes each leader's tile: its rows are loaded into registers
-// at once, their largest magnitude found, and the codes written from there.  A
-// tile of more rows than that (calls of few rows, whose CTAs are small) is read
-// twice.
+// to an SM (9.3K bf16 rows of 8 heads of 128 to 4 sequences: 16.8 us, 3.4 TB/s;
+// one row for each of 128 sequences: 5 us).  A CTA looks at consecutive rows,
+// finds those that begin a page's new positions (its leaders) and writes each
+// leader's tile: its rows are loaded into registers at once, their largest
+// magnitude found, and the codes written from there.  A tile of more rows than
+// that (by a warp, or by a small CTA) is read twice.
 #include "kv_ptx.cuh"
 
 #include <cuda_fp8.h>
+#include <type_traits>
 
 namespace mqa {
 
@@ -89,7 +89,88 @@ struct Eight {
   }
 };
 
-// kThreads threads; tiles of up to STEPS times the rows they cover at once stay in registers.
+// A page's new positions of one head: `count` rows from `row` on, behind the
+// `held` positions of the page, by kThreads threads (a CTA, or a warp); up to
+// STEPS times the rows they cover at once stay in registers.
+template <int D, int TYPE, int kThreads, int STEPS>
+__device__ __forceinline__ void write_tile(const KvView &c, const void *__restrict__ in, long long stride,
+                                           uint8_t *codes, uint8_t *exps, int head, int row, int page, int held, int n,
+                                           float *s_max) {
+  constexpr int LPR = D / 8, RPS = kThreads / LPR;  // lanes per row, rows per step
+  const int tid = threadIdx.x % kThreads, part = tid % LPR, step = tid / LPR;
+  const size_t base = (size_t)row * stride + (size_t)head * D + part * 8;
+  const size_t ph = (size_t)page * c.heads + head;
+  const int was = held ? exps[ph] : 0;
+  Eight<TYPE> x[STEPS];
+  float amax = 0.f;
+  const bool kept = n <= STEPS * RPS;
+  for (int j0 = 0; j0 * RPS < n; j0 += STEPS) {
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      x[j].clear();
+      if ((j0 + j) * RPS + step < n) x[j].load(in, base + (size_t)((j0 + j) * RPS + step) * stride);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) m = x[j].top(m);
+    float a = Eight<TYPE>::value(m);
+    if (!(a <= 3.402823466e38f)) {  // infinities and NaN do not set the scale
+      a = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < STEPS; ++j) {
+        if ((j0 + j) * RPS + step >= n) continue;
+        Eight<TYPE> y;
+        y.load(in, base + (size_t)((j0 + j) * RPS + step) * stride);
+        float f[8];
+        y.values(f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a = fabsf(f[k]) <= 3.402823466e38f ? fmaxf(a, fabsf(f[k])) : a;
+      }
+    }
+    amax = fmaxf(amax, a);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+  if (kThreads > 32) {
+    if ((tid & 31) == 0) s_max[tid >> 5] = amax;
+    __syncthreads();  // the old exponent has been read by all, too
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+  } else {
+    __syncwarp();
+  }
+  const int e = max(needed_exp(amax), was);
+  uint8_t *tile = codes + (ph << c.page_log2) * D;
+  if (held && e > was) {  // earlier positions under the larger scale
+    const float f = pow2i(max(was - e, -126));
+    for (int j = tid; j < held * D / 4; j += kThreads) {
+      uint32_t *w = reinterpret_cast<uint32_t *>(tile) + j;
+      const uint32_t v = *w;
+      *w = to_e4m3x4(from_e4m3(v & 255u) * f, from_e4m3(v >> 8 & 255u) * f, from_e4m3(v >> 16 & 255u) * f,
+                     from_e4m3(v >> 24) * f);
+    }
+  }
+  // 2^(127 - e); a page that was given a byte above 247 may need a subnormal
+  const float up = e < 254 ? pow2i(127 - e) : __uint_as_float(0x00400000u >> (e - 254));
+  for (int j0 = 0; j0 * RPS < n; j0 += STEPS) {
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      const int at = (j0 + j) * RPS + step;
+      if (at < n) {
+        if (!kept) x[j].load(in, base + (size_t)at * stride);
+        float f[8];
+        x[j].values(f);
+        uint2 o;
+        o.x = to_e4m3x4(f[0] * up, f[1] * up, f[2] * up, f[3] * up);
+        o.y = to_e4m3x4(f[4] * up, f[5] * up, f[6] * up, f[7] * up);
+        *reinterpret_cast<uint2 *>(tile + (size_t)(held + at) * D + part * 8) = o;
+      }
+    }
+  }
+  if (tid == 0) exps[ph] = (uint8_t)e;
+  if (kThreads > 32) __syncthreads();  // s_max is free again
+}
+
 template <int D, int TYPE, int kThreads, int STEPS>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const void *__restrict__ kin,
                                                             const void *__restrict__ vin, long long ks, long long vs,
@@ -152,77 +233,16 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, con
   const long long stride = values ? vs : ks;
   uint8_t *codes = values ? c.v : c.k;
   uint8_t *exps = values ? c.v_exps : c.k_exps;
-  constexpr int LPR = D / 8, RPS = kThreads / LPR;  // lanes per row, rows per step
-  const int part = tid % LPR, step = tid / LPR;
-  for (int i = 0; i < leaders; ++i) {
-    const int n = s_count[i], held = s_slot[i];
-    const size_t base = (size_t)s_row[i] * stride + (size_t)head * D + part * 8;
-    const size_t ph = (size_t)s_page[i] * c.heads + head;
-    const int was = held ? exps[ph] : 0;
-    Eight<TYPE> x[STEPS];
-    float amax = 0.f;
-    const bool kept = n <= STEPS * RPS;
-    for (int j0 = 0; j0 * RPS < n; j0 += STEPS) {
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        x[j].clear();
-        if ((j0 + j) * RPS + step < n) x[j].load(in, base + (size_t)((j0 + j) * RPS + step) * stride);
-      }
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) m = x[j].top(m);
-      float a = Eight<TYPE>::value(m);
-      if (!(a <= 3.402823466e38f)) {  // infinities and NaN do not set the scale
-        a = 0.f;
-#pragma unroll 1
-        for (int j = 0; j < STEPS; ++j) {
-          if ((j0 + j) * RPS + step >= n) continue;
-          Eight<TYPE> y;
-          y.load(in, base + (size_t)((j0 + j) * RPS + step) * stride);
-          float f[8];
-          y.values(f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) a = fabsf(f[k]) <= 3.402823466e38f ? fmaxf(a, fabsf(f[k])) : a;
-        }
-      }
-      amax = fmaxf(amax, a);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-    if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-    __syncthreads();  // the old exponent has been read by all, too
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
-    const int e = max(needed_exp(amax), was);
-    uint8_t *tile = codes + (ph << c.page_log2) * D;
-    if (held && e > was) {  // earlier positions under the larger scale
-      const float f = pow2i(max(was - e, -126));
-      for (int j = tid; j < held * D / 4; j += kThreads) {
-        uint32_t *w = reinterpret_cast<uint32_t *>(tile) + j;
-        const uint32_t v = *w;
-        *w = to_e4m3x4(from_e4m3(v & 255u) * f, from_e4m3(v >> 8 & 255u) * f, from_e4m3(v >> 16 & 255u) * f,
-                       from_e4m3(v >> 24) * f);
-      }
-    }
-    // 2^(127 - e); a page that was given a byte above 247 may need a subnormal
-    const float up = e < 254 ? pow2i(127 - e) : __uint_as_float(0x00400000u >> (e - 254));
-    for (int j0 = 0; j0 * RPS < n; j0 += STEPS) {
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        const int at = (j0 + j) * RPS + step;
-        if (at < n) {
-          if (!kept) x[j].load(in, base + (size_t)at * stride);
-          float f[8];
-          x[j].values(f);
-          uint2 o;
-          o.x = to_e4m3x4(f[0] * up, f[1] * up, f[2] * up, f[3] * up);
-          o.y = to_e4m3x4(f[4] * up, f[5] * up, f[6] * up, f[7] * up);
-          *reinterpret_cast<uint2 *>(tile + (size_t)(held + at) * D + part * 8) = o;
-        }
-      }
-    }
-    if (tid == 0) exps[ph] = (uint8_t)e;
-    __syncthreads();  // s_max is free again
+  auto tile = [&](int i, auto group) {
+    write_tile<D, TYPE, decltype(group)::value, STEPS>(c, in, stride, codes, exps, head, s_row[i], s_page[i], s_slot[i],
+                                                       s_count[i], s_max);
+  };
+  // Few tiles: one after another by the whole CTA.  Many (single tokens of many
+  // sequences): one per warp (2,048 tokens of 8 heads: 15.7 us, against 123).
+  if (kThreads > 128 && leaders > 2) {
+    for (int i = tid >> 5; i < leaders; i += kThreads / 32) tile(i, std::integral_constant<int, 32>());
+  } else {
+    for (int i = 0; i < leaders; ++i) tile(i, std::integral_constant<int, kThreads>());
   }
 }
 
@@ -231,6 +251,8 @@ void launch(const KvView &c, const void *k, const void *v, long long ks, long lo
             dim3 grid, int per, cudaStream_t stream) {
   if (per == 1)
     kv_append_kernel<D, TYPE, 128, 1><<<grid, 128, 0, stream>>>(c, k, v, ks, vs, starts, rows, per);
+  else if (c.page <= 64)  // registers for a page's rows: of 64, or of 128 (9.3K rows: 16.8 us, with room for 128 17.9)
+    kv_append_kernel<D, TYPE, 256, D / 32><<<grid, 256, 0, stream>>>(c, k, v, ks, vs, starts, rows, per);
   else
     kv_append_kernel<D, TYPE, 256, D / 16><<<grid, 256, 0, stream>>>(c, k, v, ks, vs, starts, rows, per);
 }
@@ -250,10 +272,12 @@ cudaError_t launch(const KvView &c, const void *k, const void *v, long long ks, 
 
 cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,
                              const int32_t *starts, int rows, int sms, cudaStream_t stream) {
-  // one row per CTA of 128 threads while the rows fit a few waves (single tokens:
-  // every row is a leader); for prompts a page's rows per CTA of 256, so that
-  // every CTA has about one leader
-  const int per = (long long)rows * c.heads * 2 <= 32LL * sms ? 1 : c.page;
+  // Rows per CTA.  Few: one, by 128 threads (32 tokens of 8 heads 3.0 us, with 16 per
+  // CTA 4.4).  More: 16, by 256 (512 tokens 5.8 us, with one 12.9, with a page of 64
+  // 11; a prompt of 300 rows 3.6, 6.7 and 4.5).  Many: a page's, so that a prompt's
+  // CTA has about one tile (2,000 rows 5.4 us, with 16 7.6).
+  const long long work = (long long)rows * c.heads * 2;
+  const int per = work <= 4LL * sms ? 1 : work <= 96LL * sms ? 16 : c.page;
   const dim3 grid((rows + per - 1) / per, c.heads, 2);
   return c.dim == 64 ? launch<64>(c, k, v, ks, vs, type, starts, rows, grid, per, stream)
                      : launch<128>(c, k, v, ks, vs, type, starts, rows, grid, per, stream);
