@@ -72,9 +72,8 @@ constexpr int kAttnThreads = 128;
 int attn_ctas_per_sm(int nb, int dim);
 size_t attn_slot_floats(int nb, int dim);
 // Columns per item of the tiled kernel (p.max_cols: it takes the sequences of
-// more columns), and the fewest key tiles a CTA's part holds.
+// more columns).
 constexpr int kTiledCols = 256;
-constexpr int kTiledMinTiles = 4;
 constexpr int kQueryTerms = 3;  // e4m3 terms of an fp16 query value; a bf16 one has 2
 // map: the keys' codes as rows of head_dim bytes, boxes of one page; q_map: the
 // query terms (q8, workspace of kQueryTerms * rows * q_heads * head_dim bytes)
