@@ -47,25 +47,40 @@ __device__ int block_scan(int v, int &excl, int *warp_sums) {
 }
 
 // The lowest `need` free pages, ascending, into list; returns how many there
-// are (at most need).  One CTA; stops as soon as it has them.
+// are (at most need).  One CTA; stops as soon as it has them.  A step looks at
+// 16K counts, with the next step's on their way, and costs one vote where none
+// is free (behind 2M used pages).
 __device__ int lowest_free(const KvView &c, int need, int32_t *list, int *warp_sums) {
-  int found = 0;
-  for (int base = 0; base < c.pages && found < need; base += kPlan * 8) {
-    int r[8], n = 0;
-    const int at = base + threadIdx.x * 8;
+  constexpr int kRun = 16, kStep = kPlan * kRun;
+  const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 32 * kRun + lane;
+  int found = 0, refs[kRun];
+  auto load = [&](int base) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = at + i < c.pages ? c.refs[at + i] : 1;
+    for (int i = 0; i < kRun; ++i) {
+      const int page = base + first + 32 * i;
+      refs[i] = page < c.pages ? c.refs[page] : 1;
+    }
+  };
+  load(0);
+  for (int base = 0; base < c.pages && found < need; base += kStep) {
+    uint32_t free[kRun];
+    int n = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n += r[i] == 0;
+    for (int i = 0; i < kRun; ++i) {
+      free[i] = __ballot_sync(~0u, refs[i] == 0);
+      n += __popc(free[i]);
+    }
+    load(base + kStep);
+    if (!__syncthreads_or(n)) continue;
     int excl;
-    const int total = block_scan(n, excl, warp_sums);
-    excl += found;
+    const int total = block_scan(lane == 0 ? n : 0, excl, warp_sums);
+    int at = found + __shfl_sync(~0u, excl, 0);  // free pages before the warp's
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (r[i] == 0) {
-        if (excl < need) list[excl] = at + i;
-        ++excl;
-      }
+    for (int i = 0; i < kRun; ++i) {
+      const int mine = at + __popc(free[i] & ((1u << lane) - 1));
+      if ((free[i] >> lane & 1) && mine < need) list[mine] = base + first + 32 * i;
+      at += __popc(free[i]);
+    }
     found += total;
   }
   __syncthreads();

@@ -686,6 +686,24 @@ def test_too_few_pages_change_nothing(mqa):
         assert c.fork(parents, children) == want and mqa.kv_status(dev) == want and ref.same(c, dev) == []
 
 
+@pytest.mark.parametrize("pages", [16384, 40001])
+def test_reserve_in_large_pools(mqa, pages):
+    """Free pages far apart and far behind are found lowest first, over all steps of the search."""
+    rng = np.random.default_rng(pages)
+    c = ref.random_cache(rng, pages, 1, 16, 64, [0] * 6, 1000, garbage=False)
+    c.refs[:] = rng.random(pages) < 0.97
+    c.refs[:pages // 2] = 1
+    c.refs[[5, pages - 1]] = 0
+    dev = ref.to_device(c, mqa)
+    free = int((c.refs == 0).sum())
+    for counts, want in (([16, 0, 0, 33, 0, 1], 0), ([0, 16 * (free // 2), 0, 0, 15, 0], 0), ([0, 0, 16 * free, 0, 0, 0], 1),
+                         ([0, 0, 16 * (free - free // 2 - 6), 0, 0, 0], 0), ([0, 0, 0, 0, 16, 0], 1)):
+        counts = np.array(counts, np.int32)
+        assert c.reserve(counts) == want
+        mqa.kv_reserve(dev, ints(counts))
+        assert mqa.kv_status(dev) == want and ref.same(c, dev) == [], counts
+
+
 @pytest.mark.parametrize("pages", [1, 7, 4096, 5000, 12289])
 def test_compact_sizes(mqa, pages):
     rng = np.random.default_rng(pages)
