@@ -139,26 +139,23 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
     tiles = ncb ? max(1, (length_of(s) + kTile - 1) / kTile) : 0;
   };
   long long total;
-  const int per_thread = (p.c.seqs + kAttnThreads - 1) / kAttnThreads;
-  long long mine = 0, before = 0;
+  // a warp has a run of sequences, 32 at a time
+  const int per_warp = (p.c.seqs + kAttnThreads - 1) / kAttnThreads * 32, s0 = warp * per_warp + lane;
+  auto units_of = [&](int s) -> long long {
+    int ncb = 0, tiles = 0;
+    if (s < p.c.seqs) shape_of(s, ncb, tiles);
+    return (long long)heads * ncb * tiles;
+  };
+  long long mine = 0, before = 0;  // of the warp, and of the warps before it
   if (SEL) {
     int last = min(max(p.starts[p.c.seqs], 0), p.rows);
     total = (long long)last * heads * ncb_sel * nsel_tiles;
   } else {
-    for (int i = 0; i < per_thread; ++i) {
-      const int s = tid * per_thread + i;
-      if (s >= p.c.seqs) break;
-      int ncb, tiles;
-      shape_of(s, ncb, tiles);
-      mine += (long long)heads * ncb * tiles;
-    }
-    long long incl = mine;
+#pragma unroll 4
+    for (int i = 0; i < per_warp; i += 32) mine += units_of(s0 + i);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(~0u, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) sm.scan[warp] = incl;
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
+    if (lane == 0) sm.scan[warp] = mine;
     __syncthreads();
     total = 0;
 #pragma unroll
@@ -166,7 +163,6 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
       if (w < warp) before += sm.scan[w];
       total += sm.scan[w];
     }
-    before += incl - mine;
   }
   const long long per = (total + gridDim.x - 1) / gridDim.x;
   long long at = blockIdx.x * per;
@@ -192,17 +188,19 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
   } else {
     if (at >= before && at < before + mine) {
       long long b = before;
-      for (int i = 0; i < per_thread; ++i) {
-        const int s = tid * per_thread + i;
-        int ncb, tiles;
-        shape_of(s, ncb, tiles);
-        const long long u = (long long)heads * ncb * tiles;
-        if (at < b + u) {
-          sm.found[0] = s;
-          sm.found_at = at - b;
-          break;
+      for (int i = 0; i < per_warp && b <= at; i += 32) {
+        const long long u = units_of(s0 + i);
+        long long incl = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(~0u, incl, o);
+          if (lane >= o) incl += v;
         }
-        b += u;
+        if (at >= b + incl - u && at < b + incl) {
+          sm.found[0] = s0 + i;
+          sm.found_at = at - (b + incl - u);
+        }
+        b += __shfl_sync(~0u, incl, 31);
       }
     }
     __syncthreads();
