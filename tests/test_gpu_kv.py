@@ -794,3 +794,51 @@ def test_prompt_selection_attention_fork_and_decode(mqa):
     c.compact()
     assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
     assert torch.equal(mqa.kv_attention(q, dev, ints(st)), want)
+
+
+# ---------------------------------------------------------------- the least alignment
+def shifted(t, by):
+    """A copy of t that begins `by` elements behind an aligned address, and the elements before it."""
+    import torch
+    flat = torch.zeros(t.numel() + by, dtype=t.dtype, device="cuda")
+    flat[by:].copy_(t.reshape(-1))
+    return flat[by:].view(t.shape), flat[:by]
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,max_rows", [([60, 1, 300], None), ([40, 0, 0], None), ([2, 1, 3], 3)])
+def test_least_alignment(mqa, dim, rows, max_rows):
+    """Rows, outputs and codes at 16 bytes behind a multiple of 32, counts and tables at 4, exponents at 1: every form
+    of attention, appending and the page operations answer as ever and write nothing before their outputs."""
+    import torch
+    rng = np.random.default_rng(70)
+    c = ref.random_cache(rng, 60, 2, 16, dim, [300, 41, 310], 24)
+    dev = mqa.KVCache(*(shifted(torch.from_numpy(a).cuda(), by)[0]
+                        for a, by in ((c.k, 16), (c.v, 16), (c.ke, 1), (c.ve, 1), (c.table, 1), (c.lens, 1), (c.refs, 1))))
+    assert dev.k.data_ptr() % 32 == 16
+    st = starts_of(rows)
+    n = int(st[-1])
+    k, kd = rows_of(rng, n, 2, dim, "bf16")
+    k, _ = shifted(k, 8)
+    starts, _ = shifted(ints(st), 1)
+    mqa.kv_append(dev, k, k, starts)
+    c.append(kd, kd, st)
+    assert ref.same(c, dev) == []
+    for dtype in ("bf16", "fp16"):
+        q, qd = rows_of(rng, n, 8, dim, dtype)
+        q, _ = shifted(q, 8)
+        for sel in (None, random_selection(rng, c, rows, 20)):
+            out, before = shifted(torch.zeros_like(q), 8)
+            lse, lse_before = shifted(torch.zeros((n, 8), device="cuda"), 1)
+            assert q.data_ptr() % 32 == 16 and out.data_ptr() % 32 == 16 and lse.data_ptr() % 8 == 4
+            mqa.kv_attention(q, dev, starts, selected=None if sel is None else shifted(ints(sel), 1)[0],
+                             max_rows=max_rows, out=out, lse=lse)
+            check(out, lse, c.attention(qd, st, dim ** -0.5, dtype, sel))
+            assert not before.any() and not lse_before.any()
+    c.free([0])
+    mqa.kv_free(dev, ints([0]))
+    mqa.kv_fork(dev, ints([2]), ints([0]))
+    assert c.fork(np.array([2]), np.array([0])) == 0
+    mqa.kv_compact(dev)
+    c.compact()
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
