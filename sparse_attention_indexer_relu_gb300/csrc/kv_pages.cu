@@ -20,23 +20,24 @@ namespace {
 constexpr int kPlan = 1024;  // threads of a planning CTA
 constexpr int kCopy = 256;   // threads of a copying CTA
 
-// Exclusive scan of one int per thread over the CTA; returns the total.
-__device__ int block_scan(int v, int &excl, int *warp_sums) {
+// Exclusive scan of one value per thread over the CTA; returns the total.
+template <typename T>
+__device__ T block_scan(T v, T &excl, T *warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int incl = v;
+  T incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(~0u, incl, o);
+    const T x = __shfl_up_sync(~0u, incl, o);
     if (lane >= o) incl += x;
   }
   __syncthreads();
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    int x = lane < warps ? warp_sums[lane] : 0;
+    T x = lane < warps ? warp_sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(~0u, x, o);
+      const T y = __shfl_up_sync(~0u, x, o);
       if (lane >= o) x += y;
     }
     if (lane < warps) warp_sums[lane] = x;
@@ -132,13 +133,16 @@ __device__ void copy_line(const KvPools &p, const int32_t *src, const int32_t *d
 __global__ void __launch_bounds__(kPlan) reserve_kernel(const KvView c, const KvLists l,
                                                        const int32_t *__restrict__ counts) {
   __shared__ int sums[32];
+  __shared__ long long wide_sums[32];
   __shared__ int bad;
   if (threadIdx.x == 0) bad = 0;
   __syncthreads();
-  long long total = 0;  // the same in every thread
+  // The same in every thread.  In 64 bits, a step's sum as well: a sequence may ask
+  // for 2^26 pages, and 32 such requests sum to 2^31.
+  long long total = 0;
   for (int base = 0; base < c.seqs; base += kPlan) {
     const int s = base + threadIdx.x;
-    int need = 0;
+    long long need = 0;
     if (s < c.seqs) {
       const int len = c.lens[s], add = counts[s];
       const long long now = (long long)len + add;
@@ -146,8 +150,8 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const KvView c, const Kv
       else if (!length_ok(c, len) || now > (long long)(c.max_pages << c.page_log2)) atomicOr(&bad, MQA_KV_DEV_BAD_LENGTH);
       else need = pages_of(c, (int)now) - pages_of(c, len);
     }
-    int excl;
-    const int sum = block_scan(need, excl, sums);
+    long long excl;
+    const long long sum = block_scan(need, excl, wide_sums);
     if (s < c.seqs) l.seq_a[s] = (int)min(total + excl, (long long)INT32_MAX);
     total += sum;
   }

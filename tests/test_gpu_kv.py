@@ -842,3 +842,26 @@ def test_least_alignment(mqa, dim, rows, max_rows):
     mqa.kv_compact(dev)
     c.compact()
     assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+
+
+# ---------------------------------------------------------------- requests far past the pool
+def test_reserve_requests_whose_pages_pass_32_bits(mqa):
+    """Requests of up to 2^26 pages each, whose sum passes 2^31 and 2^32 pages, in a pool of 40: too few pages, and
+    nothing changes.  (Sums in 32 bits would read as negative, as zero and as three pages.)"""
+    import torch
+    pages, seqs, width = 40, 65, 1 << 26
+    z = lambda *s, t=torch.uint8: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    dev = mqa.KVCache(z(pages, 1, 16, 64), z(pages, 1, 16, 64), z(pages, 1), z(pages, 1),
+                      torch.full((seqs, width), -1, dtype=torch.int32, device="cuda"), z(seqs, t=torch.int32),
+                      z(pages, t=torch.int32))
+    full = 1 << 30  # positions of 2^26 pages of 16
+    for counts in ([full] * 32 + [0] * 33, [0] * 33 + [full] * 32, [full] * 64 + [0], [full] * 64 + [40], [full] * 65):
+        need = sum(-(-n // 16) for n in counts)
+        assert need >= 1 << 31
+        mqa.kv_reserve(dev, ints(counts))
+        assert mqa.kv_status(dev) == 1, need
+        assert not dev.seq_lens.any() and not dev.refcounts.any()
+        assert int(dev.page_table.max()) == -1 and int(dev.page_table.min()) == -1
+    mqa.kv_reserve(dev, ints([0] * 64 + [40]))
+    assert mqa.kv_status(dev) == 0 and dev.page_table[64, :4].tolist() == [0, 1, 2, -1] and int(dev.seq_lens[64]) == 40
+    assert int(dev.refcounts.sum()) == 3
