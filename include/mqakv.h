@@ -52,7 +52,7 @@ extern "C" {
 #define MQA_KV_DEV_BAD_INDEX 2    /* a page or sequence index outside its range was skipped */
 #define MQA_KV_DEV_BAD_LIST 4     /* a list the call refuses (see each call): it changed nothing */
 #define MQA_KV_DEV_BAD_LENGTH 8   /* a length that is negative or longer than the page table */
-#define MQA_KV_DEV_WAIT_TIMEOUT 16 /* a bounded wait expired: outputs are undefined */
+#define MQA_KV_DEV_WAIT_TIMEOUT 16 /* a bounded wait expired: the call's outputs are undefined, later calls are not affected */
 
 typedef struct mqa_kv_pool {
   void *data;        /* [num_pages, page_bytes] */
@@ -132,6 +132,22 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
                      const int32_t *row_starts, int rows, int max_rows, const int32_t *selected, int n_selected,
                      int causal, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
                      void *stream);
+
+/* Test-only knobs for mqa_kv_attention_debug.  Zero-initialise for defaults. */
+typedef struct mqa_kv_debug_options {
+  int stall;           /* nonzero: dense attention waits for something that never
+                          comes: 1 the copies of keys (and values), 2 the lookups
+                          (where sequences of few columns are served: 1).  The
+                          time limit ends the waits, the kernels leave and
+                          MQA_KV_DEV_WAIT_TIMEOUT is recorded */
+  int wait_timeout_ms; /* limit of every wait in the kernels, up to 10000; 0 = default (2000) */
+} mqa_kv_debug_options;
+
+/* mqa_kv_attention with test-only knobs (opt may be NULL). */
+int mqa_kv_attention_debug(const mqa_kv_cache *cache, const void *q, long long q_row_stride, int type, int q_heads,
+                           const int32_t *row_starts, int rows, int max_rows, const int32_t *selected, int n_selected,
+                           int causal, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                           void *stream, const mqa_kv_debug_options *opt);
 
 /* Extend sequences: sequence s grows by counts[s] >= 0 positions, with new
  * pages (the lowest free ones, in sequence order, then position order) behind

@@ -191,8 +191,18 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
                      const int32_t *row_starts, int rows, int max_rows, const int32_t *selected, int n_selected,
                      int causal, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
                      void *stream) {
+  return mqa_kv_attention_debug(cache, q, q_row_stride, type, q_heads, row_starts, rows, max_rows, selected,
+                                n_selected, causal, scale, out, lse, workspace, workspace_bytes, stream, nullptr);
+}
+
+int mqa_kv_attention_debug(const mqa_kv_cache *cache, const void *q, long long q_row_stride, int type, int q_heads,
+                           const int32_t *row_starts, int rows, int max_rows, const int32_t *selected, int n_selected,
+                           int causal, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                           void *stream, const mqa_kv_debug_options *opt) {
   int rc = check_attention(cache, rows, q_heads);
   if (rc != MQA_OK) return rc;
+  if (opt && (opt->stall < 0 || opt->stall > 2 || opt->wait_timeout_ms < 0 || opt->wait_timeout_ms > 10000))
+    return MQA_ERR_INVALID_ARGUMENT;
   if ((type != MQA_KV_BF16 && type != MQA_KV_FP16) || n_selected < 0 || (!selected && n_selected > 0) ||
       !(scale > 0.f && scale <= kMaxScale))
     return MQA_ERR_INVALID_ARGUMENT;
@@ -224,6 +234,9 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
   p.causal = causal != 0;
   p.bf16 = type == MQA_KV_BF16;
   p.scale_log2 = scale * 1.44269504088896341f;
+  p.wait_ns = (opt && opt->wait_timeout_ms ? opt->wait_timeout_ms : 2000) * 1000000ULL;
+  p.stall = opt ? opt->stall : 0;
+  p.test = p.stall || (opt && opt->wait_timeout_ms);
   uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
   if (P.tiled) {
     p.max_cols = P.split ? kSplitCols : 0;

@@ -73,14 +73,16 @@ struct Meta {
   int any[kStages];
 };
 
-template <int D, int NB>
+template <int D, int NB, bool TEST>
 struct Smem {
+  static constexpr bool test = TEST;
   union {
     uint8_t ring[kWarps][kStages][2 * 16 * D];  // 16 rows of keys, 16 of values
     float merge[kWarps][8 * (NB < 2 ? NB : 2)][D + 4];
   };
   Meta meta[kWarps];
   uint64_t full[kWarps][kStages];
+  uint64_t never[kStages];      // tests: nothing arrives here
   int dead;                     // a wait has run out
   float cs[8 * NB];             // per column: scale * log2(e) / (power of two q was multiplied with)
   int lim[8 * NB];              // positions the column sees: [0, lim)
@@ -106,13 +108,13 @@ size_t attn_slot_floats(int nb, int dim) { return (size_t)8 * nb * (dim + 4); }
 
 namespace {
 
-template <int D, int NB, bool SEL>
+template <int D, int NB, bool SEL, bool TEST>
 __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
     kv_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap k_map,
                    const __grid_constant__ CUtensorMap v_map) {
   grid_dependents();
   extern __shared__ uint8_t smem_raw[];
-  using S = Smem<D, NB>;
+  using S = Smem<D, NB, TEST>;
   S &sm = *reinterpret_cast<S *>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   constexpr int CB = 8 * NB;
   constexpr int KW = D / 16;   // words of a K row per lane (8 or 4)
@@ -173,9 +175,11 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
   if (tid == 0) {
     sm.dead = 0;
     for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&sm.full[0][0] + i, 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(sm.never + i, 1);
     fence_mbar_init();
   }
   uint32_t copies = 0;  // sub-tiles whose copies this warp has issued, in all segments
+  uint64_t *const full = TEST && p.stall ? sm.never : sm.full[warp];  // what it waits for
   Item it;
   int tile;  // first tile of the current segment
   if (SEL) {
@@ -423,6 +427,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
     float m[NB][2], w[NB][2], l[NB][2];
     float o[MT][NB][4];
 
+    bool lost = false;  // a wait has run out
     // A masked weight is zero, but zero times a NaN value is NaN: where the
     // result has one, the segment runs again with NaN codes of V taken out and
     // every visible key that has one scored NaN.
@@ -445,9 +450,13 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
 
       for (int i = 0; i < iters; ++i, ++done) {
         const int stage = done % kStages;
-        if (SEL) cp_async_wait<kStages - 2>();
-        else bounded_wait(sm, &sm.full[warp][stage], done / kStages & 1, p.c.status);
-        __syncwarp();
+        if (SEL) {
+          cp_async_wait<kStages - 2>();
+          __syncwarp();
+        } else if (!warp_wait(sm, full + stage, done / kStages & 1, p)) {
+          lost = true;
+          break;
+        }
         if (!meta.any[stage]) {  // no key of the sub-tile is seen
           __syncwarp();
           issue(i + kStages - 1);
@@ -638,7 +647,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int i = 0; i < 4; ++i) bad |= o[j][nb][i] != o[j][nb][i];
-      if (careful || !__any_sync(~0u, bad)) break;
+      if (careful || lost || !__any_sync(~0u, bad)) break;
     }
 
     // ---- join the warps: common references, then sums in warp order
@@ -715,10 +724,11 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
       p.desc[blockIdx.x] = make_int4(SEL ? it.seq : r0, it.head, SEL ? -c0 - 1 : c0, (int)((rest + per - 1) / per) |
                                      ncols << 20);
     }
-    // ---- next item
+    // ---- next item (none after a wait that has run out: every warp sees that, as
+    // none waits between the barriers above and the next item's)
     at += t1 - t0;
     tile = 0;
-    if (at >= end) break;
+    if (at >= end || (!SEL && *reinterpret_cast<volatile int *>(&sm.dead))) break;
     if (++it.cb == ncb) {
       it.cb = 0;
       if (++it.head == heads) {
@@ -863,18 +873,16 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(const AttnParams p) {
 template <int D, int NB>
 cudaError_t launch(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int ctas, bool follows,
                    cudaStream_t stream) {
-  constexpr size_t bytes = sizeof(Smem<D, NB>) + 1024;
-  static DeviceFlags done[2];
-  cudaError_t e;
-  if (p.selected) {
-    e = allow_smem(kv_attn_kernel<D, NB, true>, bytes, done[0]);
-    if (e == cudaSuccess)
-      e = launch_after(kv_attn_kernel<D, NB, true>, dim3(ctas), kAttnThreads, bytes, stream, follows, p, k_map, v_map);
-  } else {
-    e = allow_smem(kv_attn_kernel<D, NB, false>, bytes, done[1]);
-    if (e == cudaSuccess)
-      e = launch_after(kv_attn_kernel<D, NB, false>, dim3(ctas), kAttnThreads, bytes, stream, follows, p, k_map, v_map);
-  }
+  constexpr size_t bytes = sizeof(Smem<D, NB, false>) + 1024;
+  static DeviceFlags done[3];
+  auto run = [&](auto *kernel, DeviceFlags &flags) {
+    const cudaError_t e = allow_smem(kernel, bytes, flags);
+    return e != cudaSuccess ? e
+                            : launch_after(kernel, dim3(ctas), kAttnThreads, bytes, stream, follows, p, k_map, v_map);
+  };
+  const cudaError_t e = p.selected ? run(kv_attn_kernel<D, NB, true, false>, done[0])
+                        : p.test   ? run(kv_attn_kernel<D, NB, false, true>, done[1])
+                                   : run(kv_attn_kernel<D, NB, false, false>, done[2]);
   if (e != cudaSuccess) return e;
   return launch_after(kv_join_kernel<D>, dim3(ctas, 4 * NB), 256, 0, stream, true, p, 8 * NB);
 }

@@ -65,6 +65,11 @@ struct AttnParams {
   int4 *desc;        // per CTA: the split item it began, for the joining kernel
   float *slots;      // per CTA: two slots of partial results
   const float *q_scale;  // tiled kernel: per column, what its products are multiplied with
+  // tests only (mqa_kv_debug_options): their compilations are to run, with this
+  // limit of a wait, and waits that nothing ends
+  int test;
+  unsigned long long wait_ns;
+  int stall;
 };
 
 // Column block sizes (8 * NB) of the split kernel, its CTAs per SM and threads.

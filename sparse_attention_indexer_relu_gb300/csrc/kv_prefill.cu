@@ -25,7 +25,9 @@
 // (in the main kernel they cost 20,000 cycles per item), laid out so that an
 // item's columns are consecutive rows.
 // Every wait has a time limit; once one has run out, all of them return at
-// once and the kernel runs to its end on whatever it finds in shared memory.
+// once: the lookup warp leaves after the copies it has under way, and the other
+// roles run to their end on whatever they find in shared memory (rows are
+// checked before they are read).
 //
 // What bounds it: a half's chain of weights (about 1,750 cycles for 128 x 128),
 // their product and the next scores (1,024), 3,100 cycles per tile with its
@@ -174,14 +176,16 @@ struct TileMeta {
 };
 
 
-template <int D>
+template <int D, bool TEST>
 struct Smem {
+  static constexpr bool test = TEST;
   uint8_t q[2][kTerms][128 * D];
   uint8_t k[kStagesK][kKeys * D];
   uint8_t v[kStagesV][kKeys * D * 2];
   TileMeta meta[kMeta];
   uint64_t q_full, q_empty, k_full[kStagesK], k_empty[kStagesK], v_full[kStagesV], v_empty[kStagesV];
   uint64_t m_full[kMeta], m_empty[kMeta], n_full[kMeta], s_full[2], p_full[2], o_full[2], done;
+  uint64_t never[kStagesK];  // tests: nothing arrives here
   Walk walk[kThreads / 32];
   uint32_t tmem;
   int dead;
@@ -296,92 +300,97 @@ __device__ __forceinline__ uint32_t code_at(int r, int c) {
 // Four tiles at a time (lane = tile x 16 keys): page, row in the pool and
 // scales; then, tile by tile, the description and the keys' copies, one box
 // per page.
-template <int D>
-__device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, Smem<D> &sm) {
+template <int D, bool TEST>
+__device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, Smem<D, TEST> &sm) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31, g = lane & 7, heads = p.c.heads;
   const int box = min(p.c.page, kKeys), per_box = box >> 4;
   uint32_t tile_no = 0, q_no = 0;
   const uint64_t keep = policy_evict_last(), once = policy_evict_first();  // other CTAs read the same keys
   const int terms = p.bf16 ? 2 : 3, planes = p.rows * p.group;  // rows of a head in a term's plane
-  for (; w.valid(); step_on(p, w)) {
-    const int nt = w.needed(p);
-    const int lim = block_limit(p, w.x.q, w.x.block), first = w.x.t0 * kKeys + g * 16, head = w.x.head;
-    const int32_t *table = p.c.table + (size_t)w.x.seq * p.c.max_pages;
-    float lv_max = -128.f;
-    auto ask = [&] {  // the part's queries
-      const int halves = w.cols(p) > 128 ? 2 : 1, at = w.x.q.r0 * p.group + w.x.block * kCols;
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(terms * halves * 128 * D));
-      __syncwarp();
-      if (lane < terms * halves) {
-        const int x = lane / terms, term = lane % terms;
-        tma_load_2d(sm.q[x][term], &q_map, &sm.q_full, 0, (term * heads + head) * planes + at + 128 * x, once);
-      }
-      ++q_no;
-    };
-    const bool begins = q_no == 0;
-    if (begins && nt > 0) ask();  // the first part's before anything is looked up
-    for (int tb = 0; tb < nt; tb += 4) {
-      const int t = tb + (lane >> 3), pos = first + t * kKeys;
-      int row = -2;
-      float ks = 1.f, lv = 0.f;
-      if (t < nt && pos < lim) {
-        const int page = __ldg(table + (pos >> p.c.page_log2));
-        if ((unsigned)page < (unsigned)p.c.pages) {
-          const int ph = page * heads + head;
-          row = (ph << p.c.page_log2) + (pos & (p.c.page - 1));
-          ks = exp_byte(__ldg(p.c.k_exps + ph));
-          lv = (float)(int)__ldg(p.c.v_exps + ph) - 127.f;
-        } else {
-          row = -1;
-          atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
+  auto walk = [&] {
+    for (; w.valid(); step_on(p, w)) {
+      const int nt = w.needed(p);
+      const int lim = block_limit(p, w.x.q, w.x.block), first = w.x.t0 * kKeys + g * 16, head = w.x.head;
+      const int32_t *table = p.c.table + (size_t)w.x.seq * p.c.max_pages;
+      float lv_max = -128.f;
+      auto ask = [&] {  // the part's queries
+        const int halves = w.cols(p) > 128 ? 2 : 1, at = w.x.q.r0 * p.group + w.x.block * kCols;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(terms * halves * 128 * D));
+        __syncwarp();
+        if (lane < terms * halves) {
+          const int x = lane / terms, term = lane % terms;
+          tma_load_2d(sm.q[x][term], &q_map, &sm.q_full, 0, (term * heads + head) * planes + at + 128 * x, once);
         }
-      }
-      float lv_min = lv;  // of the tile; groups that hold no key do not count
-      if (row < 0) lv_min = 128.f;
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) lv_min = fminf(lv_min, __shfl_xor_sync(~0u, lv_min, o));
-      lv_max = fmaxf(lv_max, row < 0 ? -128.f : lv);  // over four tiles at once: never less than it must be
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) lv_max = fmaxf(lv_max, __shfl_xor_sync(~0u, lv_max, o));
-      const uint32_t bad = __ballot_sync(~0u, row == -1);
-      const uint32_t copies = __ballot_sync(~0u, row >= 0 && g % per_box == 0);
-      for (int u = 0; u < min(4, nt - tb); ++u, ++tile_no) {
-        const int slot = tile_no % kMeta, stage = tile_no % kStagesK;
-        bounded_wait(sm, &sm.m_empty[slot], (tile_no / kMeta & 1) ^ 1, p.c.status);
-        TileMeta &meta = sm.meta[slot];
-        if (lane >> 3 == u) {
-          meta.row[g] = row;
-          meta.kv[g] = make_float2(ks, lv);
-          if (g < 4) {
-            const uint32_t two = bad >> (8 * u + 2 * g);
-            meta.hide[g] = (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
-            meta.nan[g] = 0;
-          }
-          if (g == 0) {
-            meta.lv_min = lv_min;
-            meta.spread = lv_max - lv_min;
-            meta.odd = (bad >> (8 * u) & 255u) != 0;
+        ++q_no;
+      };
+      const bool begins = q_no == 0;
+      if (begins && nt > 0) ask();  // the first part's before anything is looked up
+      for (int tb = 0; tb < nt; tb += 4) {
+        const int t = tb + (lane >> 3), pos = first + t * kKeys;
+        int row = -2;
+        float ks = 1.f, lv = 0.f;
+        if (t < nt && pos < lim) {
+          const int page = __ldg(table + (pos >> p.c.page_log2));
+          if ((unsigned)page < (unsigned)p.c.pages) {
+            const int ph = page * heads + head;
+            row = (ph << p.c.page_log2) + (pos & (p.c.page - 1));
+            ks = exp_byte(__ldg(p.c.k_exps + ph));
+            lv = (float)(int)__ldg(p.c.v_exps + ph) - 127.f;
+          } else {
+            row = -1;
+            atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
           }
         }
-        bounded_wait(sm, &sm.k_empty[stage], (tile_no / kStagesK & 1) ^ 1, p.c.status);
-        const uint32_t mine = copies >> (8 * u) & 255u;
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.m_full[slot]);
-          mbar_arrive_expect_tx(&sm.k_full[stage], (uint32_t)(__popc(mine) * box * D));
-        }
-        __syncwarp();
-        if (lane >> 3 == u && (mine >> g & 1))
-          tma_load_2d(sm.k[stage] + g * 16 * D, &map, &sm.k_full[stage], 0, row, keep);
-        if (tb + u == 0 && !begins) {  // once the previous part's last scores are done
-          bounded_wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p.c.status);
-          ask();
+        float lv_min = lv;  // of the tile; groups that hold no key do not count
+        if (row < 0) lv_min = 128.f;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) lv_min = fminf(lv_min, __shfl_xor_sync(~0u, lv_min, o));
+        lv_max = fmaxf(lv_max, row < 0 ? -128.f : lv);  // over four tiles at once: never less than it must be
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) lv_max = fmaxf(lv_max, __shfl_xor_sync(~0u, lv_max, o));
+        const uint32_t bad = __ballot_sync(~0u, row == -1);
+        const uint32_t copies = __ballot_sync(~0u, row >= 0 && g % per_box == 0);
+        for (int u = 0; u < min(4, nt - tb); ++u, ++tile_no) {
+          const int slot = tile_no % kMeta, stage = tile_no % kStagesK;
+          if (!warp_wait(sm, &sm.m_empty[slot], (tile_no / kMeta & 1) ^ 1, p)) return;
+          TileMeta &meta = sm.meta[slot];
+          if (lane >> 3 == u) {
+            meta.row[g] = row;
+            meta.kv[g] = make_float2(ks, lv);
+            if (g < 4) {
+              const uint32_t two = bad >> (8 * u + 2 * g);
+              meta.hide[g] = (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
+              meta.nan[g] = 0;
+            }
+            if (g == 0) {
+              meta.lv_min = lv_min;
+              meta.spread = lv_max - lv_min;
+              meta.odd = (bad >> (8 * u) & 255u) != 0;
+            }
+          }
+          const uint32_t mine = copies >> (8 * u) & 255u;
+          if (!warp_wait(sm, &sm.k_empty[stage], (tile_no / kStagesK & 1) ^ 1, p)) return;
+          if (lane == 0) {
+            mbar_arrive(&sm.m_full[slot]);
+            mbar_arrive_expect_tx(&sm.k_full[stage], (uint32_t)(__popc(mine) * box * D));
+          }
+          __syncwarp();
+          if (lane >> 3 == u && (mine >> g & 1))
+            tma_load_2d(sm.k[stage] + g * 16 * D, &map, &sm.k_full[stage], 0, row, keep);
+          if (tb + u == 0 && !begins) {  // once the previous part's last scores are done
+            if (!warp_wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p)) {
+              ++tile_no;  // its copies are under way
+              return;
+            }
+            ask();
+          }
         }
       }
     }
-  }
+  };
+  if (!TEST || p.stall != 2 || warp_wait(sm, &sm.never[0], 0, p)) walk();
   // the copies must have landed before the CTA leaves
   if (q_no) drain(&sm.q_full, (q_no - 1) & 1);
   for (int i = 1; i <= kStagesK; ++i)
@@ -412,8 +421,8 @@ __device__ void take_nan_out(uint4 (&x)[STEPS], TileMeta &meta, int r0) {
 // A warp's load covers whole 128-byte lines; its lanes are laid out so that 8
 // of them store to 8 different bank groups (4 chunks of two rows whose
 // exchanges differ in the lowest bit).
-template <int D>
-__device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
+template <int D, bool TEST>
+__device__ void convert_role(const AttnParams &p, Smem<D, TEST> &sm) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   constexpr int CH = D / 16;              // 16-byte chunks of a code row
   constexpr int RPS = kConverters / CH;   // rows per step: 16 (D = 128) or 32
@@ -421,6 +430,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
   const int tid = threadIdx.x & (kConverters - 1), lane = tid & 31;
   const int ch = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3;
   const int r0 = D == 128 ? (tid >> 5) * 4 + (lane >> 2 & 3) : (tid >> 5) * 8 + (lane >> 2);
+  const uint32_t last_row = ((uint32_t)p.c.pages * p.c.heads << p.c.page_log2) - 16;  // begins the pool's last 16 rows
   uint32_t tile_no = 0;
   uint4 x[STEPS];
   auto load = [&](uint32_t no, int i) {
@@ -429,12 +439,12 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
     x[i] = make_uint4(0, 0, 0, 0);
     // (past the L1, of which shared memory leaves little: spills live there, and the
     // chunk of 32K positions takes 799 us so and 920 with loads that allocate in it)
-    if (row >= 0) x[i] = __ldcg(reinterpret_cast<const uint4 *>(p.c.v + (size_t)(row + (r & 15)) * D + ch * 16));
+    if ((uint32_t)row <= last_row) x[i] = __ldcg(reinterpret_cast<const uint4 *>(p.c.v + (size_t)(row + (r & 15)) * D + ch * 16));
   };
   for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p);
     if (nt == 0) continue;  // nothing is read
-    bounded_wait(sm, &sm.m_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
+    bounded_wait(sm, &sm.m_full[tile_no % kMeta], tile_no / kMeta & 1, p);
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) load(tile_no, i);
 
@@ -448,8 +458,8 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
         any |= nan_bytes(x[i].x) | nan_bytes(x[i].y) | nan_bytes(x[i].z) | nan_bytes(x[i].w);
       if (any) take_nan_out<STEPS, RPS>(x, sm.meta[tile_no % kMeta], r0);
       mbar_arrive(&sm.n_full[tile_no % kMeta]);
-      if (t + 1 < nt) bounded_wait(sm, &sm.m_full[(tile_no + 1) % kMeta], (tile_no + 1) / kMeta & 1, p.c.status);
-      bounded_wait(sm, &sm.v_empty[stage], (tile_no / kStagesV & 1) ^ 1, p.c.status);
+      if (t + 1 < nt) bounded_wait(sm, &sm.m_full[(tile_no + 1) % kMeta], (tile_no + 1) / kMeta & 1, p);
+      bounded_wait(sm, &sm.v_empty[stage], (tile_no / kStagesV & 1) ^ 1, p);
       uint8_t *dst = sm.v[stage];
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
@@ -470,12 +480,13 @@ __device__ void convert_role(const AttnParams &p, Smem<D> &sm) {
 // ------------------------------------------------------------------ MMA issue
 // The warp waits together, one elected lane issues, and the others wait for it
 // before the next barrier: lanes that poll hold up the one that issues.
-template <int D>
-__device__ void mma_role(const AttnParams &p, Smem<D> &sm) {
+template <int D, bool TEST>
+__device__ void mma_role(const AttnParams &p, Smem<D, TEST> &sm) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   const uint32_t tmem = sm.tmem;
   constexpr uint32_t kQk = idesc_f8_e4m3_f32(128, kKeys), kPv = idesc_f16(128, D, true);
   const int terms = p.bf16 ? 2 : 3;
+  uint64_t *const k_full = TEST && p.stall == 1 ? sm.never : sm.k_full;
   uint32_t tile_no = 0, q_no = 0, p_no = 0;
   const uint32_t q0 = Desc<D>::codes_lo(sm.q[0][0]), k0 = Desc<D>::codes_lo(sm.k[0]),
                  v0 = Desc<D>::values_lo(sm.v[0]);
@@ -503,13 +514,13 @@ __device__ void mma_role(const AttnParams &p, Smem<D> &sm) {
       const uint32_t kn = tile_no + t + 1, vn = tile_no + t;
       const int ks = kn % kStagesK, vs = vn % kStagesV;
       const bool more = t + 1 < nt;
-      if (more) bounded_wait(sm, &sm.k_full[ks], kn / kStagesK & 1, p.c.status);
-      if (t < 0) bounded_wait(sm, &sm.q_full, q_no & 1, p.c.status);
-      else bounded_wait(sm, &sm.v_full[vs], vn / kStagesV & 1, p.c.status);
+      if (more) bounded_wait(sm, k_full + ks, kn / kStagesK & 1, p);
+      if (t < 0) bounded_wait(sm, &sm.q_full, q_no & 1, p);
+      else bounded_wait(sm, &sm.v_full[vs], vn / kStagesV & 1, p);
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         const bool on = x == 0 || two;
-        if (t >= 0) bounded_wait(sm, &sm.p_full[x], p_no++ >> 1 & 1, p.c.status);
+        if (t >= 0) bounded_wait(sm, &sm.p_full[x], p_no++ >> 1 & 1, p);
         __syncwarp();
         tc_fence_after();
         if (elect_one()) {
@@ -673,8 +684,8 @@ __device__ __noinline__ void hide_behind(uint32_t ts, int room) {
   tmem_st_wait();
 }
 
-template <int D>
-__device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, long long near) {
+template <int D, bool TEST>
+__device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long per, long long near) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   const int x = threadIdx.x >> 7;        // tile of columns
   const int r = threadIdx.x & 127;       // its column
@@ -686,8 +697,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
     const int col = x * 128 + r;
     if (ncols <= x * 128) {  // this half is empty: it keeps step, so that it meets every phase of the barriers
       for (int t = 0; t < nt; ++t, ++tile_no) {
-        bounded_wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
-        bounded_wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);  // without it this half could run ahead of the issuing warp
+        bounded_wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p);
+        bounded_wait(sm, &sm.s_full[x], s_no++ & 1, p);  // without it this half could run ahead of the issuing warp
         mbar_arrive(&sm.p_full[x]);
       }
       continue;
@@ -702,8 +713,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
     room0 -= w.x.t0 * kKeys;
     const int whole_tiles = __reduce_min_sync(~0u, room0) / kKeys;  // tiles every column of the warp sees whole
     for (int t = 0; t < nt; ++t, ++tile_no) {
-      bounded_wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p.c.status);
-      bounded_wait(sm, &sm.s_full[x], s_no++ & 1, p.c.status);
+      bounded_wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p);
+      bounded_wait(sm, &sm.s_full[x], s_no++ & 1, p);
       __syncwarp();
       tc_fence_after();
       const TileMeta &meta = sm.meta[tile_no % kMeta];
@@ -783,7 +794,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
     }
     // ---- the part's result
     if (nt) {
-      bounded_wait(sm, &sm.o_full[x], o_no++ & 1, p.c.status);
+      bounded_wait(sm, &sm.o_full[x], o_no++ & 1, p);
       __syncwarp();
       tc_fence_after();
     }
@@ -845,13 +856,14 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> &sm, long long per, lo
   }
 }
 
-template <int D>
+template <int D, bool TEST>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_prefill_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map,
                       const __grid_constant__ CUtensorMap q_map) {
   grid_dependents();
   extern __shared__ uint8_t raw[];
-  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
+  using S = Smem<D, TEST>;
+  S &sm = *reinterpret_cast<S *>(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // ---- this CTA's part of the line
   const int per_thread = (p.c.seqs + kThreads - 1) / kThreads;
@@ -927,6 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.o_full[i], 1);
     }
     mbar_init(&sm.done, 1);
+    for (int i = 0; i < kStagesK; ++i) mbar_init(&sm.never[i], 1);
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -988,14 +1001,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // 200, 72 and 40 the converters spill: 1,360 instead of 799 at the time.)
   if (warp < 8) {
     reg_inc<192>();
-    softmax_role<D>(p, sm, per, near);
+    softmax_role<D, TEST>(p, sm, per, near);
   } else if (warp < 12) {
     reg_dec<80>();
-    convert_role<D>(p, sm);
+    convert_role<D, TEST>(p, sm);
   } else {
     reg_dec<48>();
-    if (warp == 12) mma_role<D>(p, sm);
-    if (warp == 13) lookup_role<D>(p, map, q_map, sm);
+    if (warp == 12) mma_role<D, TEST>(p, sm);
+    if (warp == 13) lookup_role<D, TEST>(p, map, q_map, sm);
   }
   __syncwarp();
   tc_fence_before();
@@ -1083,25 +1096,28 @@ __global__ void __launch_bounds__(256) kv_query_terms_kernel(const AttnParams p,
   for (int i = 0; i < BATCH; ++i) terms_of<D>(p, u[i], first + i * PER < last, row[i], head[i], part, q8, factor);
 }
 
-template <int D>
+template <int D, bool TEST>
 cudaError_t launch(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8, float *factor,
                    int ctas, cudaStream_t stream) {
-  constexpr size_t bytes = sizeof(Smem<D>) + 1024;
+  constexpr size_t bytes = sizeof(Smem<D, TEST>) + 1024;
   static DeviceFlags done{0};
-  cudaError_t e = allow_smem(kv_prefill_kernel<D>, bytes, done);
+  cudaError_t e = allow_smem(kv_prefill_kernel<D, TEST>, bytes, done);
   if (e != cudaSuccess) return e;
   const int rows = p.rows * p.q_heads, per = 4 * 256 / (D / 8);
   e = launch_after(kv_query_terms_kernel<D>, dim3((rows + per - 1) / per), 256, 0, stream, false, p, q8, factor);
   if (e != cudaSuccess) return e;
-  return launch_after(kv_prefill_kernel<D>, dim3(ctas), kThreads, bytes, stream, true, p, map, q_map);
+  return launch_after(kv_prefill_kernel<D, TEST>, dim3(ctas), kThreads, bytes, stream, true, p, map, q_map);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8,
                               float *factor, int ctas, cudaStream_t stream) {
-  return p.c.dim == 64 ? launch<64>(p, map, q_map, q8, factor, ctas, stream)
-                       : launch<128>(p, map, q_map, q8, factor, ctas, stream);
+  if (p.test)
+    return p.c.dim == 64 ? launch<64, true>(p, map, q_map, q8, factor, ctas, stream)
+                         : launch<128, true>(p, map, q_map, q8, factor, ctas, stream);
+  return p.c.dim == 64 ? launch<64, false>(p, map, q_map, q8, factor, ctas, stream)
+                       : launch<128, false>(p, map, q_map, q8, factor, ctas, stream);
 }
 
 }  // namespace mqa

@@ -141,28 +141,39 @@ __device__ __forceinline__ uint32_t float2_to_bf162(float a, float b) {
   return w;
 }
 
-// Wait for a barrier's phase.  Once a wait of the CTA has run out (2 s), its
-// waits return at once and it runs to its end on what it finds.
+// Wait for a barrier's phase: true once it is complete.  Once a wait of the CTA
+// has run out (2 s), every wait for what has not come returns false at once.
+// The warps that issue copies then leave: a barrier never counts the bytes of
+// more than one phase, and the last phase's can be waited for (drain).  The
+// others may run to their end, on whatever lies in shared memory: none of it
+// may reach an address unchecked.  (A vote per wait that lets them leave, too,
+// costs the tiled kernel 6% of a chunk of 32K positions.)
+// S::test: compilation for tests, with a limit of its own.
 constexpr unsigned long long kWaitNs = 2000000000ULL;
 template <typename S>
-__device__ __forceinline__ void bounded_wait(S &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
-  if (mbar_try_wait(bar, parity)) return;
+__device__ __forceinline__ bool bounded_wait(S &sm, uint64_t *bar, uint32_t parity, const AttnParams &p) {
+  if (mbar_try_wait(bar, parity)) return true;
   unsigned long long t0 = 0;
   for (int i = 0;; ++i) {
-    if (mbar_try_wait(bar, parity)) return;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((i & 15) == 15) {
-      if (*reinterpret_cast<volatile int *>(&sm.dead)) return;
+      if (*reinterpret_cast<volatile int *>(&sm.dead)) return false;
       const unsigned long long now = globaltimer_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitNs) {
+      if (now - t0 > (S::test ? p.wait_ns : kWaitNs)) {
         *reinterpret_cast<volatile int *>(&sm.dead) = 1;
-        atomicOr(status, MQA_KV_DEV_WAIT_TIMEOUT);
-        return;
+        atomicOr(p.c.status, MQA_KV_DEV_WAIT_TIMEOUT);
+        return false;
       }
     }
   }
 }
-// The same for copies and products in flight, also after another wait has run out.
+// The same for the whole warp.
+template <typename S>
+__device__ __forceinline__ bool warp_wait(S &sm, uint64_t *bar, uint32_t parity, const AttnParams &p) {
+  return __all_sync(~0u, bounded_wait(sm, bar, parity, p));
+}
+// For copies and products under way, also after a wait has run out.
 __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kWaitNs) {

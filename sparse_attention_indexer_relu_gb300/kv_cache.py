@@ -14,6 +14,7 @@ import math
 from typing import Optional, Sequence
 
 KV_EXPORTS = ("mqa_kv_scratch_bytes", "mqa_kv_append", "mqa_kv_attention_workspace_bytes", "mqa_kv_attention",
+              "mqa_kv_attention_debug",
               "mqa_kv_reserve", "mqa_kv_fork", "mqa_kv_free", "mqa_kv_compact", "mqa_kv_copy_pages",
               "mqa_kv_get_status")
 KV_STATUS_BITS = {1: "out_of_pages", 2: "bad_index", 4: "bad_list", 8: "bad_length", 16: "wait_timeout"}
@@ -33,6 +34,10 @@ class _Cache(ctypes.Structure):
                                              "max_pages", "n_extra")] + [("extra", _Pool * _MAX_EXTRA)])
 
 
+class KVDebugOptions(ctypes.Structure):
+    _fields_ = [("stall", ctypes.c_int), ("wait_timeout_ms", ctypes.c_int)]
+
+
 def declare(L):
     """Argument types of the cache's entries (called when the library is loaded)."""
     P, I, S, Q, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float
@@ -41,6 +46,7 @@ def declare(L):
     L.mqa_kv_append.argtypes = [C, P, P, Q, Q, I, P, I, P]
     L.mqa_kv_attention_workspace_bytes.argtypes = [I, C, I, I, ctypes.POINTER(S)]
     L.mqa_kv_attention.argtypes = [C, P, Q, I, I, P, I, I, P, I, I, F, P, P, P, S, P]
+    L.mqa_kv_attention_debug.argtypes = L.mqa_kv_attention.argtypes + [ctypes.POINTER(KVDebugOptions)]
     L.mqa_kv_reserve.argtypes = [C, P, P]
     L.mqa_kv_fork.argtypes = [C, P, P, I, P]
     L.mqa_kv_free.argtypes = [C, P, I, P]
@@ -257,14 +263,16 @@ def kv_append(cache: KVCache, k, v, row_starts, stream=None):
 
 
 def kv_attention(q, cache: KVCache, row_starts, selected=None, causal: bool = True, scale: Optional[float] = None,
-                 max_rows: Optional[int] = None, workspace=None, out=None, lse=None, stream=None):
+                 max_rows: Optional[int] = None, workspace=None, out=None, lse=None, stream=None,
+                 debug: Optional[dict] = None):
     """Attention of rows q [rows, q_heads, head_dim] (bf16 or fp16) over the cache; returns out, of q's shape.
 
     Row i of the n rows of a sequence is its position seq_len - n + i and sees the positions up to its own (every
     position of the sequence where not `causal`); with `selected` [rows, k] int32, the listed ones among them (the
     answer of `mqa_topk_prefill`).  scale defaults to head_dim ** -0.5.  max_rows: the most rows of one sequence, if
     known (it only helps to choose the kernels).  lse [rows, q_heads] float32 receives the logarithm of each
-    softmax's sum.  Rows at or behind row_starts[-1] are left as they are in `out` and `lse`."""
+    softmax's sum.  Rows at or behind row_starts[-1] are left as they are in `out` and `lse`.  debug: test-only
+    knobs (KVDebugOptions)."""
     import torch
     m, types = _api(), _types()
     qp, qs = _rows(q, cache, (torch.bfloat16, torch.float16), None, "q")
@@ -291,11 +299,15 @@ def kv_attention(q, cache: KVCache, row_starts, selected=None, causal: bool = Tr
             workspace = alloc_kv_workspace(cache, rows, heads)
         elif workspace.device != cache.device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {cache.device}")
-        m._check(m.lib().mqa_kv_attention(cache._ref, qp, qs, types[q.dtype], heads, rs, rows, int(max_rows or 0), sp,
-                                          n_sel, int(bool(causal)),
-                                          cache.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
-                                          None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), s), "mqa_kv_attention")
+        args = (cache._ref, qp, qs, types[q.dtype], heads, rs, rows, int(max_rows or 0), sp, n_sel, int(bool(causal)),
+                cache.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
+                None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), s)
+        if debug is None:
+            m._check(m.lib().mqa_kv_attention(*args), "mqa_kv_attention")
+        else:
+            m._check(m.lib().mqa_kv_attention_debug(*args, ctypes.byref(KVDebugOptions(**debug))),
+                     "mqa_kv_attention_debug")
     return out
 
 

@@ -865,3 +865,28 @@ def test_reserve_requests_whose_pages_pass_32_bits(mqa):
     mqa.kv_reserve(dev, ints([0] * 64 + [40]))
     assert mqa.kv_status(dev) == 0 and dev.page_table[64, :4].tolist() == [0, 1, 2, -1] and int(dev.seq_lens[64]) == 40
     assert int(dev.refcounts.sum()) == 3
+
+
+# ---------------------------------------------------------------- the waits' time limit
+@pytest.mark.parametrize("stall", [1, 2])
+@pytest.mark.parametrize("rows,max_rows", [([1, 1, 2], 2), ([150, 0, 90], None), ([400, 1, 300], None)])
+def test_waits_end_at_their_limit(mqa, rows, max_rows, stall):
+    """A wait for what never comes runs out (of few columns, of many, and of both in one call): the status says so,
+    nothing but the outputs has changed, and the next call on the same workspace answers as if nothing had been."""
+    import torch
+    rng = np.random.default_rng(71)
+    c = ref.random_cache(rng, 130, 2, 16, 128, [900, 40, 700], 60)
+    dev = ref.to_device(c, mqa)
+    st = starts_of(rows)
+    q, _ = rows_of(rng, int(st[-1]), 8, 128, "bf16")
+    ws = mqa.alloc_kv_workspace(dev, int(st[-1]), 8)
+    ws.fill_(0xAB)
+    want = mqa.kv_attention(q, dev, ints(st), max_rows=max_rows, workspace=ws)
+    assert mqa.kv_status(dev) == 0
+    for _ in range(2):
+        got = mqa.kv_attention(q, dev, ints(st), max_rows=max_rows, workspace=ws,
+                               debug={"stall": stall, "wait_timeout_ms": 30})
+        assert got.shape == q.shape and mqa.kv_status(dev) == 16
+        assert ref.same(c, dev) == []
+        got = mqa.kv_attention(q, dev, ints(st), max_rows=max_rows, workspace=ws, debug={"wait_timeout_ms": 500})
+        assert torch.equal(got, want) and mqa.kv_status(dev) == 0

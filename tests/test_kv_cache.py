@@ -150,3 +150,12 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError):
         mqa.KVCache(z(4, 2, 16, 64), z(4, 2, 16, 64), z(4, 2), z(4, 2), z(2, 3, dtype=torch.int32),
                     z(2, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("opt,code", [(dict(stall=3), 1), (dict(stall=-1), 1), (dict(wait_timeout_ms=-1), 1),
+                                      (dict(wait_timeout_ms=10001), 1), (dict(stall=2, wait_timeout_ms=10000), 0)])
+def test_debug_options_are_checked(opt, code):
+    rc = mqa.lib().mqa_kv_attention_debug(ctypes.byref(cache()), P(0x1000), 4096, 0, 32, P(0x2000), 0 if code == 0 else 8,
+                                          0, None, 0, 1, 0.1, P(0x3000), None, P(0x100000), 1 << 40, None,
+                                          ctypes.byref(kv.KVDebugOptions(**opt)))
+    assert rc == code
