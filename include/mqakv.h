@@ -25,9 +25,9 @@
  * Rows.  row_starts [max_seqs + 1] int32 (non-decreasing) says which rows of a
  * call belong to which sequence: rows [row_starts[s], row_starts[s + 1]) are
  * the LAST positions of sequence s: row i of n is position seq_lens[s] - n + i
- * (seq_lens already counts them; mqa_kv_reserve does that).  Rows at or behind
- * row_starts[max_seqs] belong to no sequence: nothing is read for them, and
- * their outputs are left as they were.
+ * (seq_lens already counts them; mqa_kv_reserve does that).  Rows before
+ * row_starts[0] and at or behind row_starts[max_seqs] belong to no sequence:
+ * nothing is read for them, and their outputs are left as they were.
  */
 #ifndef MQAKV_H_
 #define MQAKV_H_

@@ -149,9 +149,11 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
     return (long long)heads * ncb * tiles;
   };
   long long mine = 0, before = 0;  // of the warp, and of the warps before it
+  int first = 0;                   // selected keys: the first row of a sequence
   if (SEL) {
-    int last = min(max(p.starts[p.c.seqs], 0), p.rows);
-    total = (long long)last * heads * ncb_sel * nsel_tiles;
+    first = min(max(p.starts[0], 0), p.rows);
+    const int last = min(max(p.starts[p.c.seqs], first), p.rows);
+    total = (long long)(last - first) * heads * ncb_sel * nsel_tiles;
   } else {
 #pragma unroll 4
     for (int i = 0; i < per_warp; i += 32) mine += units_of(s0 + i);
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
     tile = (int)(at - item * nsel_tiles);
     it.cb = (int)(item % ncb_sel);
     it.head = (int)(item / ncb_sel % heads);
-    it.seq = (int)(item / ((long long)ncb_sel * heads));  // the row
+    it.seq = first + (int)(item / ((long long)ncb_sel * heads));  // the row
   } else {
     if (at >= before && at < before + mine) {
       long long b = before;

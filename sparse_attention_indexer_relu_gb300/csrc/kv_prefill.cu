@@ -1074,7 +1074,8 @@ __global__ void __launch_bounds__(256) kv_query_terms_kernel(const AttnParams p,
   grid_dependents();
   constexpr int LPR = D / 8, PER = 256 / LPR, BATCH = 4;  // lanes per row, rows per CTA and step, steps
   const int part = threadIdx.x % LPR;
-  const int last = min(max(p.starts[p.c.seqs], 0), p.rows) * p.q_heads;  // rows of no sequence are not read
+  const int from = min(max(p.starts[0], 0), p.rows) * p.q_heads;  // rows of no sequence are not read
+  const int last = min(max(p.starts[p.c.seqs], 0), p.rows) * p.q_heads;
   const int first = blockIdx.x * PER * BATCH + threadIdx.x / LPR;
   uint4 u[BATCH];
   int row[BATCH], head[BATCH];
@@ -1088,12 +1089,15 @@ __global__ void __launch_bounds__(256) kv_query_terms_kernel(const AttnParams p,
       if (head[i] >= p.q_heads) ++row[i], head[i] -= p.q_heads;
     }
     u[i] = make_uint4(0, 0, 0, 0);
-    if (at < last)
+    if (at >= from && at < last)
       u[i] = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) +
                                                    (size_t)row[i] * p.q_stride + (size_t)head[i] * D + part * 8));
   }
 #pragma unroll
-  for (int i = 0; i < BATCH; ++i) terms_of<D>(p, u[i], first + i * PER < last, row[i], head[i], part, q8, factor);
+  for (int i = 0; i < BATCH; ++i) {
+    const int at = first + i * PER;
+    terms_of<D>(p, u[i], at >= from && at < last, row[i], head[i], part, q8, factor);
+  }
 }
 
 template <int D, bool TEST>

@@ -271,8 +271,8 @@ def kv_attention(q, cache: KVCache, row_starts, selected=None, causal: bool = Tr
     position of the sequence where not `causal`); with `selected` [rows, k] int32, the listed ones among them (the
     answer of `mqa_topk_prefill`).  scale defaults to head_dim ** -0.5.  max_rows: the most rows of one sequence, if
     known (it only helps to choose the kernels).  lse [rows, q_heads] float32 receives the logarithm of each
-    softmax's sum.  Rows at or behind row_starts[-1] are left as they are in `out` and `lse`.  debug: test-only
-    knobs (KVDebugOptions)."""
+    softmax's sum.  Rows before row_starts[0] and at or behind row_starts[-1] are left as they are in `out`
+    and `lse`.  debug: test-only knobs (KVDebugOptions)."""
     import torch
     m, types = _api(), _types()
     qp, qs = _rows(q, cache, (torch.bfloat16, torch.float16), None, "q")

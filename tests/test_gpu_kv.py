@@ -890,3 +890,33 @@ def test_waits_end_at_their_limit(mqa, rows, max_rows, stall):
         assert ref.same(c, dev) == []
         got = mqa.kv_attention(q, dev, ints(st), max_rows=max_rows, workspace=ws, debug={"wait_timeout_ms": 500})
         assert torch.equal(got, want) and mqa.kv_status(dev) == 0
+
+
+# ---------------------------------------------------------------- rows of no sequence
+@pytest.mark.parametrize("form", ["dense", "selected"])
+@pytest.mark.parametrize("rows", [[1, 2], [40, 9], [0, 3], [0, 0]])
+def test_rows_before_the_first_bound(mqa, rows, form):
+    """A first bound above zero: the rows before it belong to no sequence, in no form of the call."""
+    import torch
+    rng = np.random.default_rng(72)
+    c = ref.random_cache(rng, 20, 2, 16, 64, [90, 70], 8)
+    dev = ref.to_device(c, mqa)
+    before, behind, n = 3, 2, sum(rows)
+    st = starts_of(rows) + before
+    q, qd = rows_of(rng, before + n + behind, 8, 64, "bf16")
+    q[:before] = float("nan")
+    sel = random_selection(rng, c, rows, 20)
+    pad = lambda k: np.zeros((k, 20), np.int32)  # noqa: E731
+    sel = np.concatenate([pad(before), sel, pad(behind)]) if form == "selected" else None
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    mqa.kv_attention(q, dev, ints(st), selected=None if sel is None else ints(sel), out=out, lse=lse)
+    assert mqa.kv_status(dev) == 0
+    at = slice(before, before + n)
+    for t in (out, lse):
+        assert (t[:before] == 7).all() and (t[before + n:] == 7).all()
+    check(out[at], lse[at], c.attention(qd[at], st - before, 0.125, "bf16", None if sel is None else sel[at]))
+    k, kd = rows_of(rng, before + n + behind, 2, 64, "bf16")
+    mqa.kv_append(dev, k, k, ints(st))
+    c.append(kd[at], kd[at], st - before)
+    assert ref.same(c, dev) == []
