@@ -227,8 +227,12 @@ def _list(t, cache, name, n=None):
 
 def _rows(t, cache, dtypes, heads, name):
     """A [rows, heads, head_dim] tensor whose rows may be strided (a slice of a wider projection)."""
+    import torch
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which the cache's operators do not have: detach it, or call "
+                         "them under torch.no_grad()")
     d = cache.head_dim
     if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (rows, {heads or 'heads'}, {d})")

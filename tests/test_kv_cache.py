@@ -159,3 +159,54 @@ def test_debug_options_are_checked(opt, code):
                                           0, None, 0, 1, 0.1, P(0x3000), None, P(0x100000), 1 << 40, None,
                                           ctypes.byref(kv.KVDebugOptions(**opt)))
     assert rc == code
+
+
+class OnDevice:
+    """What the binding reads of a CUDA tensor, at a made-up address."""
+    is_cuda = True
+    device = torch.device("cuda", 0)
+    requires_grad = False
+
+    def __init__(self, *shape, dtype=torch.uint8, at=0x10000):
+        self.shape, self.dtype, self.at = torch.Size(shape), dtype, at
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return self.at
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self, i):
+        return self.shape[i + 1:].numel()
+
+
+def fake_cache(**kw):
+    i32 = torch.int32
+    a = dict(k=OnDevice(9, 2, 16, 64), v=OnDevice(9, 2, 16, 64), k_exps=OnDevice(9, 2), v_exps=OnDevice(9, 2),
+             page_table=OnDevice(3, 4, dtype=i32), seq_lens=OnDevice(3, dtype=i32), refcounts=OnDevice(9, dtype=i32),
+             scratch=OnDevice(mqa.kv_scratch_bytes(9, 3)))
+    a.update(kw)
+    return mqa.KVCache(**a)
+
+
+def test_rows_that_require_a_gradient_are_refused():
+    """The operators have no backward pass: an answer without history would lose the gradient silently."""
+    c, starts = fake_cache(), OnDevice(4, dtype=torch.int32)
+    x, y = (OnDevice(5, 2, 64, dtype=torch.bfloat16) for _ in range(2))
+    y.requires_grad = True
+    with pytest.raises(ValueError, match="q requires a gradient"):
+        mqa.kv_attention(y, c, starts)
+    for k, v, name in ((y, x, "k"), (x, y, "v")):
+        with pytest.raises(ValueError, match=name + " requires a gradient"):
+            mqa.kv_append(c, k, v, starts)
+    with torch.no_grad():
+        assert kv._rows(y, c, (torch.bfloat16,), None, "q") == (0x10000, 128)
