@@ -85,7 +85,8 @@ def _dense(t, dtypes, dim, name, device=None):
 
 
 def _alike(a, b):
-    return (b is not None and a.dtype == b.dtype and a.shape == b.shape and a.device == b.device and a.is_contiguous())
+    return (a is not None and b is not None and a.dtype == b.dtype and a.shape == b.shape and a.device == b.device and
+            a.is_contiguous())
 
 
 class KVCache:

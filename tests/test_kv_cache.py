@@ -210,3 +210,15 @@ def test_rows_that_require_a_gradient_are_refused():
             mqa.kv_append(c, k, v, starts)
     with torch.no_grad():
         assert kv._rows(y, c, (torch.bfloat16,), None, "q") == (0x10000, 128)
+
+
+def test_replace_without_refcounts():
+    c = fake_cache()
+    bare = c.replace(refcounts=None)
+    assert bare.refcounts is None and bare._c.refcounts is None
+    again = bare.replace(refcounts=OnDevice(9, dtype=torch.int32, at=0x80000))
+    assert again._c.refcounts == 0x80000
+    with pytest.raises(ValueError):
+        bare.replace(refcounts=OnDevice(8, dtype=torch.int32))
+    with pytest.raises((TypeError, ValueError, AttributeError)):
+        c.replace(page_table=None)
