@@ -99,9 +99,24 @@ class KVCache:
     scratch         uint8, `kv_scratch_bytes` long and zeroed (made here if None)
     extra           up to 4 further tensors [num_pages, ...] whose pages move along
 
-    The object keeps references and changes nothing by itself.  Calls that
-    change the cache, and calls that overlap such a call, are the caller's to
-    order."""
+    The object keeps references and changes nothing by itself; its calls use
+    the addresses taken here, so its tensors are not exchanged but by
+    `replace`.  Calls that change the cache, and calls that overlap such a
+    call, are the caller's to order; handles that share a scratch (those of
+    `replace`) count as one cache there."""
+
+    def _fixed(self, name):
+        if name in self.__dict__.get("_held", ()):
+            raise AttributeError(f"{name} of a KVCache is fixed: its calls use the address of the tensor that it was made "
+                                 "of; replace() makes a handle over another one")
+
+    def __setattr__(self, name, value):
+        self._fixed(name)
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        self._fixed(name)
+        object.__delattr__(self, name)
 
     def __init__(self, k, v, k_exps, v_exps, page_table, seq_lens, refcounts=None, scratch=None, extra: Sequence = ()):
         import torch
@@ -145,16 +160,17 @@ class KVCache:
         self._c = c
         self._ref = ctypes.byref(c)
         self._index = dev.index
+        self._held = frozenset(self.__dict__)
 
     def replace(self, **changes):
-        """A cache over the same tensors but for the given ones."""
+        """A cache over the same tensors (the scratch included) but for the given ones."""
         if all(n in ("page_table", "seq_lens", "refcounts") and _alike(t, getattr(self, n)) for n, t in changes.items()):
             other = object.__new__(KVCache)
             other.__dict__.update(self.__dict__, **changes)
-            other._c = _Cache.from_buffer_copy(self._c)
+            other.__dict__["_c"] = _Cache.from_buffer_copy(self._c)
             for n, t in changes.items():
                 setattr(other._c, n, t.data_ptr())
-            other._ref = ctypes.byref(other._c)
+            other.__dict__["_ref"] = ctypes.byref(other._c)
             return other
         now = {n: getattr(self, n) for n in ("k", "v", "k_exps", "v_exps", "page_table", "seq_lens", "refcounts",
                                              "scratch", "extra")}

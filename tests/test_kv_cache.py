@@ -222,3 +222,22 @@ def test_replace_without_refcounts():
         bare.replace(refcounts=OnDevice(8, dtype=torch.int32))
     with pytest.raises((TypeError, ValueError, AttributeError)):
         c.replace(page_table=None)
+
+
+def test_a_handle_keeps_the_tensors_it_was_made_of():
+    """The C entries read the addresses taken when the handle was made: another tensor under a name of the handle would
+    not be used, and the one in use could be freed."""
+    c = fake_cache()
+    for name in ("k", "v", "k_exps", "v_exps", "page_table", "seq_lens", "refcounts", "scratch", "extra", "device",
+                 "num_pages", "max_pages"):
+        with pytest.raises(AttributeError, match="replace"):
+            setattr(c, name, getattr(c, name))
+        with pytest.raises(AttributeError, match="replace"):
+            delattr(c, name)
+    other = c.replace(seq_lens=OnDevice(3, dtype=torch.int32, at=0x90000))
+    assert other._c.seq_lens == 0x90000 == other.seq_lens.data_ptr() and c._c.seq_lens == 0x10000
+    assert other._c.k == c._c.k and other._c.scratch == c._c.scratch
+    with pytest.raises(AttributeError, match="replace"):
+        other.seq_lens = c.seq_lens
+    c.note = "a program's own attributes are its business"
+    assert c.note
