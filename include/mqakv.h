@@ -17,8 +17,8 @@
  * Conventions are those of mqatopk.h: device pointers of the current device,
  * caller-owned memory, work enqueued on `stream`, MQA_* return codes, argument
  * errors found on the host before any work, no allocation, no synchronisation
- * except in mqa_kv_get_status.  Every call may be captured into a CUDA graph;
- * replays read the buffers' current contents.  Lengths, tables and lists are
+ * except in mqa_kv_get_status.  Every other call may be captured into a CUDA
+ * graph; replays read the buffers' current contents.  Lengths, tables and lists are
  * read on the device: an index there that leaves its range is never followed,
  * and is recorded in the status word.
  *
@@ -180,7 +180,8 @@ int mqa_kv_compact(const mqa_kv_cache *cache, void *stream);
 int mqa_kv_copy_pages(const mqa_kv_cache *cache, const int32_t *src, const int32_t *dst, int n, void *stream);
 
 /* The status bits collected since the last call; clears them.  Synchronises
- * `stream`. */
+ * `stream`; one that is being captured is refused (MQA_ERR_INVALID_ARGUMENT),
+ * and its capture goes on. */
 int mqa_kv_get_status(const mqa_kv_cache *cache, int32_t *status, void *stream);
 
 #ifdef __cplusplus

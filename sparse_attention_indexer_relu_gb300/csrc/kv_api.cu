@@ -338,7 +338,10 @@ int mqa_kv_get_status(const mqa_kv_cache *cache, int32_t *status, void *stream) 
   rc = require_device(&sms);
   if (rc != MQA_OK) return rc;
   int32_t *word = reinterpret_cast<int32_t *>(cache->scratch) + kKvStatus;
-  cudaError_t e = cudaMemcpyAsync(status, word, sizeof(int32_t), cudaMemcpyDeviceToHost, as_stream(stream));
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(as_stream(stream), &capture);
+  if (e == cudaSuccess && capture != cudaStreamCaptureStatusNone) return MQA_ERR_INVALID_ARGUMENT;
+  if (e == cudaSuccess) e = cudaMemcpyAsync(status, word, sizeof(int32_t), cudaMemcpyDeviceToHost, as_stream(stream));
   if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof(int32_t), as_stream(stream));
   if (e == cudaSuccess) e = cudaStreamSynchronize(as_stream(stream));
   return code(e);

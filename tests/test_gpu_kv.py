@@ -920,3 +920,31 @@ def test_rows_before_the_first_bound(mqa, rows, form):
     mqa.kv_append(dev, k, k, ints(st))
     c.append(kd[at], kd[at], st - before)
     assert ref.same(c, dev) == []
+
+
+# ---------------------------------------------------------------- the status word and captures
+def test_status_is_refused_in_a_capture(mqa):
+    """Reading the status waits for the stream, which a capture does not allow: the call is refused, and the capture
+    is not lost."""
+    import torch
+    rng = np.random.default_rng(73)
+    c = ref.random_cache(rng, 12, 2, 16, 64, [100], 8)
+    dev = ref.to_device(c, mqa)
+    q, qd = rows_of(rng, 2, 8, 64, "bf16")
+    st = ints([0, 2])
+    ws = mqa.alloc_kv_workspace(dev, 2, 8)
+    out = torch.zeros_like(q)
+    mqa.kv_attention(q, dev, st, workspace=ws, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mqa.kv_attention(q, dev, st, workspace=ws, out=out)
+        with pytest.raises(mqa.MQAError) as e:
+            mqa.kv_status(dev)
+        assert e.value.code == 1
+    dev.page_table[0, 1] = -7
+    out.zero_()
+    g.replay()
+    assert mqa.kv_status(dev) == 2 and mqa.kv_status(dev) == 0
+    sel = np.array([[t for t in range(100) if t // 16 != 1]] * 2, np.int32)
+    check(out, None, c.attention(qd, np.array([0, 2]), 0.125, "bf16", sel))
