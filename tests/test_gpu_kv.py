@@ -948,3 +948,182 @@ def test_status_is_refused_in_a_capture(mqa):
     assert mqa.kv_status(dev) == 2 and mqa.kv_status(dev) == 0
     sel = np.array([[t for t in range(100) if t // 16 != 1]] * 2, np.int32)
     check(out, None, c.attention(qd, np.array([0, 2]), 0.125, "bf16", sel))
+
+
+# ---------------------------------------------------------------- forms that only few columns had been tested in
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,lens", [([3, 2], [100, 60]), ([90, 40], [400, 60]), ([30, 70], [2900, 70])], ids=str)
+def test_infinite_and_nan_query_values(mqa, rows, lens, dtype):
+    """A query value that is no finite number gives NaN in every component and the lse of its row and head, and
+    nothing else: in both kernels, whole and joined from parts, over selected keys, and zeros where the row sees
+    nothing."""
+    import torch
+    rng = np.random.default_rng(74)
+    c = ref.random_cache(rng, sum(-(-n // 16) for n in lens) + 2, 2, 16, 64, lens, 190)
+    dev = ref.to_device(c, mqa)
+    st = starts_of(rows)
+    n = int(st[-1])
+    q, _ = rows_of(rng, n, 8, 64, dtype)
+    marks = [(1, 2, 5, float("nan")), (2, 4, 0, float("inf")), (n - 1, 7, 63, float("-inf")), (n - 2, 0, 8, float("inf"))]
+    for r, h, d, x in marks:
+        q[r, h, d] = x
+    q[0, 1] = float("nan")
+    qd = q.double().cpu().numpy()
+    for sel in (None, random_selection(rng, c, rows, 30)):
+        if sel is not None:
+            sel[n - 1] = -1  # sees nothing: zeros
+        lse = torch.zeros((n, 8), device="cuda")
+        out = mqa.kv_attention(q, dev, ints(st), selected=None if sel is None else ints(sel), lse=lse)
+        want = c.attention(qd, st, 0.125, dtype, sel)
+        for r, h in [m[:2] for m in marks] + [(0, 1)]:
+            assert np.isnan(want[0][r, h]).all() or (sel is not None and not want[0][r, h].any())
+        assert np.isnan(want[0]).any()
+        check(out, lse, want)
+    assert mqa.kv_status(dev) == 0
+
+
+@pytest.mark.parametrize("rows,max_rows", [([90, 40, 1], None), ([3, 2, 1], 3)])
+def test_strided_queries_in_every_kernel(mqa, rows, max_rows):
+    """Queries that are a slice of a wider projection."""
+    import torch
+    rng = np.random.default_rng(75)
+    c = ref.random_cache(rng, 40, 2, 32, 128, [400, 60, 70], 14)
+    dev = ref.to_device(c, mqa)
+    st = starts_of(rows)
+    wide = torch.from_numpy(rng.standard_normal((int(st[-1]), 14, 128))).to(torch.float16).cuda()
+    q = wide[:, 3:11]
+    qd = q.double().cpu().numpy()
+    sel = random_selection(rng, c, rows, 30)
+    check(mqa.kv_attention(q, dev, ints(st), max_rows=max_rows), None, c.attention(qd, st, 128 ** -0.5, "fp16"))
+    check(mqa.kv_attention(q, dev, ints(st), selected=ints(sel)), None, c.attention(qd, st, 128 ** -0.5, "fp16", sel))
+
+
+@pytest.mark.parametrize("case", [(1, 72, 64, [90, 3], [2, 1]), (2, 128, 128, [300, 40], [1, 5]),
+                                  (1, 300, 64, [200, 129], [1, 3]), (256, 1, 64, [20, 33], [1, 20])], ids=str)
+def test_many_query_heads(mqa, case):
+    """Groups beyond a block's columns (one row in several blocks), and many key/value heads."""
+    heads, group, dim, lens, rows = case
+    rng = np.random.default_rng(76)
+    c = ref.random_cache(rng, 40, heads, 16, dim, lens, 20)
+    for max_rows in (None, 1):
+        attend(mqa, c, rng, rows, group, "bf16", max_rows=max_rows)
+    attend(mqa, c, rng, rows, group, "fp16", selected=random_selection(rng, c, rows, 25))
+    attend(mqa, c, rng, rows, group, "fp16", False, selected=random_selection(rng, c, rows, 25))
+
+
+def test_decreasing_bounds_give_the_others_their_rows(mqa):
+    """A bound below the one before it leaves its sequence without rows; the others' rows are answered."""
+    import torch
+    rng = np.random.default_rng(77)
+    c = ref.random_cache(rng, 30, 1, 16, 64, [50, 40, 30], 8)
+    dev = ref.to_device(c, mqa)
+    for n, group in ((4, 4), (70, 4)):
+        q, qd = rows_of(rng, n, group, 64, "bf16")
+        out = torch.zeros_like(q)
+        mqa.kv_attention(q, dev, ints([3, 1, n, n]), out=out)  # sequence 1: rows [1, n)
+        want = c.attention(qd[1:], np.array([0, 0, n - 1, n - 1]), 0.125, "bf16")
+        check(out[1:], None, want)
+        assert not out[0].any() and mqa.kv_status(dev) == 0
+
+
+def test_rows_past_32_bits(mqa):
+    """More than 2^32 bytes of queries, outputs and new rows: the last of them are read and written where they lie."""
+    import torch
+    rng = np.random.default_rng(78)
+    base, rows = (1 << 24) + 3, [40, 1]
+    c = ref.random_cache(rng, 30, 1, 64, 128, [300, 129], 6)
+    dev = ref.to_device(c, mqa)
+    n = sum(rows)
+    st = starts_of(rows)
+    starts = ints(st + base)
+    k = torch.zeros((base + n, 1, 128), dtype=torch.bfloat16, device="cuda")
+    kn, kd = rows_of(rng, n, 1, 128, "bf16")
+    k[base:] = kn
+    mqa.kv_append(dev, k, k, starts)
+    c.append(kd, kd, st)
+    assert ref.same(c, dev) == []
+    del k
+    q = torch.zeros((base + n, 2, 128), dtype=torch.bfloat16, device="cuda")
+    qn, qd = rows_of(rng, n, 2, 128, "bf16")
+    q[base:] = qn
+    sel = random_selection(rng, c, rows, 20)
+    out = torch.zeros_like(q)
+    for max_rows, s in ((None, None), (1, None), (None, sel)):
+        wide = None
+        if s is not None:
+            wide = torch.zeros((base + n, 20), dtype=torch.int32, device="cuda")
+            wide[base:] = ints(s)
+        out.zero_()
+        mqa.kv_attention(q, dev, starts, selected=wide, max_rows=max_rows, out=out)
+        check(out[base:], None, c.attention(qd, st, 128 ** -0.5, "bf16", s))
+        assert not out[:base].any() and mqa.kv_status(dev) == 0
+
+
+def test_as_many_sequences_as_there_may_be(mqa):
+    import torch
+    rng = np.random.default_rng(79)
+    n = 65536
+    lens, rows = np.zeros(n, np.int64), np.zeros(n, np.int64)
+    pick = rng.choice(n, 60, replace=False)
+    pick[:2] = 0, n - 1
+    lens[pick] = rng.integers(1, 90, 60)
+    rows[pick] = np.minimum(lens[pick], rng.integers(1, 60, 60))
+    lens[pick[5]], rows[pick[5]] = 700, 300
+    c = ref.random_cache(rng, 600, 1, 16, 64, lens, 45)
+    _, dev, _, st = attend(mqa, c, rng, rows, 4)
+    attend(mqa, c, rng, rows, 4, "fp16", max_rows=2)
+    attend(mqa, c, rng, rows, 4, selected=random_selection(rng, c, rows, 20))
+    counts = np.zeros(n, np.int32)
+    counts[pick] = rng.integers(0, 9, 60)
+    mqa.kv_reserve(dev, ints(counts))
+    assert c.reserve(counts) == 0 and mqa.kv_status(dev) == 0
+    k, kd = rows_of(rng, int(counts.sum()), 1, 64, "fp32")
+    st = starts_of(counts)
+    mqa.kv_append(dev, k, k, ints(st))
+    c.append(kd, kd, st)
+    assert ref.same(c, dev) == []
+
+
+def test_a_decode_step_in_a_graph(mqa):
+    """Room, a token's keys and values and its attention, captured once on a stream of its own and replayed while the
+    sequences grow over their pages; then a fork, a return and a packing, captured as well."""
+    import torch
+    rng = np.random.default_rng(80)
+    c = ref.random_cache(rng, 60, 2, 16, 64, [14, 31, 0, 1], 8)
+    dev = ref.to_device(c, mqa)
+    counts = np.array([1, 1, 0, 2], np.int32)
+    st = starts_of(counts)
+    k, v, q = (torch.zeros((4, h, 64), dtype=torch.bfloat16, device="cuda") for h in (2, 2, 8))
+    dcounts, dst = ints(counts), ints(st)
+    ws, out = mqa.alloc_kv_workspace(dev, 4, 8), torch.zeros_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step, pages = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    mqa.kv_attention(q, dev, dst, workspace=ws, out=out, stream=side)
+    side.synchronize()
+    with torch.cuda.graph(step, stream=side):
+        mqa.kv_reserve(dev, dcounts)
+        mqa.kv_append(dev, k, v, dst)
+        mqa.kv_attention(q, dev, dst, workspace=ws, out=out)
+    parents, children, gone = ints([1]), ints([2]), ints([0])
+    with torch.cuda.graph(pages, stream=side):
+        mqa.kv_fork(dev, parents, children)
+        mqa.kv_free(dev, gone)
+        mqa.kv_compact(dev)
+    torch.cuda.synchronize()
+    for i in range(20):
+        kn, vn, qn = (rows_of(rng, 4, h, 64, "bf16") for h in (2, 2, 8))
+        for t, x in ((k, kn), (v, vn), (q, qn)):
+            t.copy_(x[0])
+        step.replay()
+        torch.cuda.synchronize()
+        assert c.reserve(counts) == 0
+        c.append(kn[1], vn[1], st)
+        assert ref.same(c, dev) == [], i
+        check(out, None, c.attention(qn[1], st, 0.125, "bf16"), i)
+    pages.replay()
+    torch.cuda.synchronize()
+    assert c.fork(np.array([1]), np.array([2])) == 0
+    c.free([0])
+    c.compact()
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
