@@ -244,10 +244,9 @@ def _list(t, cache, name, n=None):
 
 def _rows(t, cache, dtypes, heads, name):
     """A [rows, heads, head_dim] tensor whose rows may be strided (a slice of a wider projection)."""
-    import torch
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.requires_grad and torch.is_grad_enabled():
+    if t.requires_grad and _api()._torch().is_grad_enabled():
         raise ValueError(f"{name} requires a gradient, which the cache's operators do not have: detach it, or call "
                          "them under torch.no_grad()")
     d = cache.head_dim
