@@ -74,7 +74,7 @@ typedef struct mqa_kv_cache {
   int head_dim;             /* 64 or 128 */
   int max_seqs;             /* 1 .. MQA_KV_MAX_SEQS */
   int max_pages;            /* columns of page_table; max_pages * page_size <= 2^30 */
-  int n_extra;              /* further pools whose pages move along (an indexer's keys and scales) */
+  int n_extra;              /* further pools of the program's, whose pages move along */
   mqa_kv_pool extra[MQA_KV_MAX_EXTRA];
 } mqa_kv_cache;
 
@@ -113,17 +113,21 @@ int mqa_kv_attention_workspace_bytes(int device, const mqa_kv_cache *cache, int 
  *  lse       NULL, or [rows, q_heads] fp32: the logarithm of the softmax's sum
  *  scale     in (0, 65536]
  *  max_rows  the most rows any sequence has, if the caller knows it, else 0: it
- *            only chooses the kernels (any value gives correct results)
+ *            only chooses the kernels (any value gives correct results).  Calls
+ *            for single tokens should give it: without it one sequence may have
+ *            all rows, and the kernels for prompts run as well (6 to 55 us)
  * A row that sees nothing gives zeros and lse = -inf.  A NaN code in a key or
  * value that a row sees gives NaN in every component of the heads it serves,
  * and is without effect on rows that do not see it; an infinite or NaN query
  * value does so for its row and head.  Dot products, softmax statistics and
  * sums are held in fp32; the softmax weights enter the product with V in fp16
  * (11 bits, down to 2^-24 of the largest weight times scale).  Query rows are
- * scaled by a power of two and enter the product with K in fp16, or, where
- * their sequence has more than 32 (row, head) pairs per key/value head, as sums
- * of e4m3 terms: what is lost is below 2^-17 of the row's largest magnitude.
- * Query magnitudes below 2^110 and scores within fp32's range are served.
+ * scaled by a power of two and enter the product with K in fp16, or as sums of
+ * e4m3 terms (by the call's and the sequences' sizes): in either form what is
+ * lost is below 2^-17 of the row's largest magnitude.  Query magnitudes below
+ * 2^110 and scores within fp32's range are served, as long as scale times the
+ * row's largest magnitude (1 for a row of zeros) times a page's key scale stays
+ * below 2^127, whatever the codes there.
  * `out` must not overlap `q`.  `workspace` may be shared by calls that do not
  * overlap; one for `rows` rows serves every call of fewer rows, whatever
  * max_rows and `selected`.  Calls that do not write to the cache may overlap,

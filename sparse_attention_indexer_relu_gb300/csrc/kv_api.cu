@@ -93,14 +93,21 @@ constexpr float kMaxScale = 65536.f;
 // Which kernels a call runs and where their parts of the workspace lie.  The
 // split kernel (kv_attn.cu) takes blocks of 8 to 32 columns; calls in which a
 // sequence may have more, for which it would read the cache twice, run the tiled
-// kernel (kv_prefill.cu).  8 sequences of 8K positions, 8 heads of 128, split
-// and tiled: 32 columns 60 and 88 us, 48: 94 and 88, 64: 95 and 87, 128: 167 and
-// 77; one of 32K: 44 and 62, 58 and 63, 60 and 63, 93 and 59.  Such calls leave
-// sequences of up to kSplitCols to the split kernel (16 columns: 40 and 46 us):
-// beside a prompt of 2,048 rows, 63 single tokens at 32K positions take 0.80 ms
-// so, and 1.90 ms with every sequence in the tiled kernel.  The host does not
-// know whether there are such sequences; a call without any pays the 6 us of
-// two launches that find no work.
+// kernel (kv_prefill.cu).  In graphs, split and tiled, 8 heads of 128: 32
+// sequences of up to 8K positions, 40 columns 236 and 190 us, 64: 248 and 186; 8
+// of them 73 and 73, 76 and 72; heads of 64: 183 and 155, 194 and 153; 59 and 58,
+// 62 and 59.  (The host knows neither lengths nor sequences with rows: one
+// sequence of 32K positions would be better off in the split kernel up to 64
+// columns, 57 to 59 us against 61 to 63, heads of 64 45 to 47 against 50.)
+// Tiled calls leave sequences of up to kSplitCols to the split kernel (16
+// columns: 40 and 46 us): beside a prompt of 2,048 rows, 63 single tokens at 32K
+// positions take 0.80 ms so, and 1.90 ms with every sequence in the tiled kernel.
+// The host does not know whether there are such sequences; a call without any
+// pays the 6 us of two launches that find no work.  Nor does it know that there
+// is nothing else where max_rows is missing: 32 single tokens over up to 16K
+// positions take 107 us with max_rows = 1 and 130 without (4 query heads per
+// key/value head of 128; 32 query heads: 70 and 108, as their 32 columns go to
+// the tiled kernel then).
 constexpr int kTiledFrom = 32;
 constexpr int kSplitCols = 16;
 struct AttnPlan {

@@ -8,8 +8,9 @@
 //
 // At least rows * heads * dim * (input bytes + 1) bytes move, twice (K and V); what
 // bounds it is the chain bounds -> length -> page -> rows of each CTA, four CTAs
-// to an SM (9.3K bf16 rows of 8 heads of 128 to 4 sequences: 16.8 us, 3.4 TB/s;
-// one row for each of 128 sequences: 5 us).  A CTA looks at consecutive rows,
+// to an SM (9.3K bf16 rows of 8 heads of 128 to 4 sequences: 17 us, 3.3 TB/s, in a
+// graph; one row for each of 128 sequences: 4.6 us in a graph.  Calls by
+// themselves, with new inputs each time, take 24 and 17 to 19 us).  A CTA looks at consecutive rows,
 // finds those that begin a page's new positions (its leaders) and writes each
 // leader's tile: its rows are loaded into registers at once, their largest
 // magnitude found, and the codes written from there.  A tile of more rows than

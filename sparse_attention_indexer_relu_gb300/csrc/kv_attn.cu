@@ -31,12 +31,12 @@
 //
 // What bounds it.  Single tokens over long caches: HBM (32 sequences of 16K to
 // 64K positions, 8 key/value heads of 128: 2.68 GB in 400 us, 6.7 TB/s, 99% of
-// the measured copy rate; 310 instructions per 16 keys, issue slots 42% busy).
+// the measured copy rate; 323 instructions per 16 keys, issue slots 44% busy).
 // More columns, or keys picked one by one: instructions and their latencies at
 // the 12 warps per SM that the accumulators leave room for (16 x 5 fp16 rows, 4
-// heads per key/value head of 64: 372 per 16 keys, 33 us, 1.35 TB/s; 2,492 rows
-// with 512 selected keys each, 16 heads per key/value head of 128: 690 per 16
-// keys, issue slots 52% busy, 180 us, 116 TFLOP/s out of L2).
+// heads per key/value head of 64: 591 per 16 keys and 24 columns, 33 us, 1.33
+// TB/s; 2,505 rows with 512 selected keys each, 16 heads per key/value head of
+// 128: 683 per 16 keys, issue slots 52% busy, 180 us, 116 TFLOP/s out of L2).
 #include "kv_internal.h"
 #include "kv_ptx.cuh"
 

@@ -35,9 +35,11 @@
 // upper ones ahead of the product, would break the chain, but then the queries
 // are read from shared memory twice as often: 894 us instead of 718.)
 // 2,048 rows at the end of 32K positions (32 heads, 8 key/value heads of 128):
-// 720 us, 1.48 PFLOP/s, 76% of the measured bf16 rate.  Five prompts of up to
-// 1,531 rows: 90 us, of which 13 for the query terms, 5 to find the parts, 7
-// until the first scores are there, 9 to join.
+// 735 to 745 us a pass, 1.43 to 1.45 PFLOP/s, 74% of the measured bf16 rate; fp16
+// queries, whose third term lengthens the scores' product by half, 831 us in a
+// run where bf16 took 725.  Five prompts of up to 1,531 rows: 90 us, of which 13
+// for the query terms, 5 to find the parts, 7 until the first scores are there, 9
+// to join.
 //
 // Work is cut like kv_attn.cu's: the key tiles of all items in one line, even
 // parts per CTA, partial results in two slots per CTA and a joining pass.  The
@@ -439,7 +441,8 @@ __device__ void convert_role(const AttnParams &p, Smem<D, TEST> &sm) {
     x[i] = make_uint4(0, 0, 0, 0);
     // (past the L1, of which shared memory leaves little: spills live there, and the
     // chunk of 32K positions takes 799 us so and 920 with loads that allocate in it)
-    if ((uint32_t)row <= last_row) x[i] = __ldcg(reinterpret_cast<const uint4 *>(p.c.v + (size_t)(row + (r & 15)) * D + ch * 16));
+    if ((uint32_t)row <= last_row)
+      x[i] = __ldcg(reinterpret_cast<const uint4 *>(p.c.v + (size_t)(row + (r & 15)) * D + ch * 16));
   };
   for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p);
@@ -997,8 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   grid_wait();  // the query terms
   // Registers: 256 x 192 + 128 x 80 + 128 x 48 = 512 x 128, what the block was
-  // launched with.  (Chunk of 32K positions: 720 us; with 184, 96 and 48: 735; with
-  // 200, 72 and 40 the converters spill: 1,360 instead of 799 at the time.)
+  // launched with.  (Chunk of 32K positions, at the time: 720 us; with 184, 96 and 48
+  // 735; with 200, 72 and 40 the converters spill: 1,360 instead of 799.)
   if (warp < 8) {
     reg_inc<192>();
     softmax_role<D, TEST>(p, sm, per, near);

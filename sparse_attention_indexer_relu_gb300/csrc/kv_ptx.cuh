@@ -26,7 +26,9 @@ __device__ __forceinline__ float exp_byte(uint32_t e) { return __uint_as_float(m
 
 // Kernels of one call follow each other by programmatic dependent launch: each
 // lets the next one's blocks be scheduled at once, and waits for the one before
-// (its writes included) before it writes anything or reads what that one wrote.
+// (its writes included) before it reads what that one wrote.  What a kernel
+// writes before it waits, no earlier kernel of the call touches: the split
+// kernel, which waits at its end, has rows, descriptions and slots of its own.
 // Every block waits, so that a kernel's end means its predecessors' end too.
 __device__ __forceinline__ void grid_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -147,7 +149,7 @@ __device__ __forceinline__ uint32_t float2_to_bf162(float a, float b) {
 // more than one phase, and the last phase's can be waited for (drain).  The
 // others may run to their end, on whatever lies in shared memory: none of it
 // may reach an address unchecked.  (A vote per wait that lets them leave, too,
-// costs the tiled kernel 6% of a chunk of 32K positions.)
+// costs the tiled kernel 5% of a chunk of 32K positions.)
 // S::test: compilation for tests, with a limit of its own.
 constexpr unsigned long long kWaitNs = 2000000000ULL;
 template <typename S>
