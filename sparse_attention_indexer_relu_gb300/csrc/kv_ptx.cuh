@@ -170,10 +170,13 @@ __device__ __forceinline__ bool bounded_wait(S &sm, uint64_t *bar, uint32_t pari
     }
   }
 }
-// The same for the whole warp.
+// The same for the whole warp; what its lanes wrote before, all of them see (a
+// vote alone orders no memory).
 template <typename S>
 __device__ __forceinline__ bool warp_wait(S &sm, uint64_t *bar, uint32_t parity, const AttnParams &p) {
-  return __all_sync(~0u, bounded_wait(sm, bar, parity, p));
+  const bool ok = __all_sync(~0u, bounded_wait(sm, bar, parity, p));
+  __syncwarp();
+  return ok;
 }
 // For copies and products under way, also after a wait has run out.
 __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
