@@ -137,6 +137,59 @@ int mqa_kv_attention(const mqa_kv_cache *cache, const void *q, long long q_row_s
                      int causal, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
                      void *stream);
 
+/* What the rows of mqa_kv_attention_view see.  Zero-initialised: every position
+ * up to the row's own.
+ *  window      > 0: the row at position p sees t <= p with t > p - window
+ *  sinks       and, with a window, the sequence's first `sinks` positions t <= p
+ *  tree        NULL, or [rows, tree_words] int32, for drafted rows that hang on one
+ *              another: the row sees every position before its sequence's first
+ *              row, and the position of the sequence's row j where bit j % 32 of
+ *              word j / 32 is set (its own only if its own bit is); rows behind the
+ *              last word are not seen.  Not together with a window */
+typedef struct mqa_kv_view {
+  int window, sinks;
+  const int32_t *tree;
+  int tree_words;
+} mqa_kv_view;
+
+/* mqa_kv_attention over the positions that `view` says; everything else is as
+ * there, the workspace included. */
+int mqa_kv_attention_view(const mqa_kv_cache *cache, const void *q, long long q_row_stride, int type, int q_heads,
+                          const int32_t *row_starts, int rows, int max_rows, const mqa_kv_view *view, float scale,
+                          void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Masks and positions of drafted rows.
+ *  parents    [rows] int32: the row that a row hangs on, as its number among its
+ *             sequence's rows, which comes before it; -1: on the position before
+ *             them.  Anything else counts as -1 and is recorded
+ *             (MQA_KV_DEV_BAD_INDEX)
+ *  mask       [rows, words] int32: bits of the row itself and of all it hangs on, as
+ *             mqa_kv_view.tree has them; rows from 32 * words on have no bit
+ *  positions  NULL, or [rows] int32: seq_lens[s] - n + the number of drafted rows
+ *             above the row, which is where it will be if it is accepted
+ * Rows of no sequence are left as they were. */
+int mqa_kv_tree_mask(const mqa_kv_cache *cache, const int32_t *parents, const int32_t *row_starts, int rows,
+                     int32_t *mask, int words, int32_t *positions, void *stream);
+
+/* Keep accepted rows and give the rest back: of the n last positions of sequence s
+ * (its rows, see Rows), counts[s] stay, behind one another; the sequence gets that
+ * much shorter, and pages that it no longer needs are given back as mqa_kv_free
+ * does.
+ *  counts    [max_seqs] int32, 0 <= counts[s] <= n (not looked at where n is 0)
+ *  accepted  NULL: the first counts[s] rows stay.  Or [rows] int32: entry
+ *            row_starts[s] + i, i < counts[s], is the number among the sequence's
+ *            rows of the one that becomes its i-th, ascending; entries behind
+ *            counts[s] are not looked at
+ * Rows that change places are written as mqa_kv_append would write their values: a
+ * page's scale becomes the least that holds what moves into it, but not less than
+ * it was where earlier positions stay in the page; when it grows, those are
+ * rounded again.  A sequence whose list is not ascending or leaves its rows
+ * (MQA_KV_DEV_BAD_LIST), or whose length does not hold its rows
+ * (MQA_KV_DEV_BAD_LENGTH), is left as it was.  Two sequences must not share a page
+ * that rows move into.  Extra pools are not touched. */
+int mqa_kv_accept(const mqa_kv_cache *cache, const int32_t *row_starts, int rows, const int32_t *counts,
+                  const int32_t *accepted, void *stream);
+
 /* Test-only knobs for mqa_kv_attention_debug.  Zero-initialise for defaults. */
 typedef struct mqa_kv_debug_options {
   int stall;           /* nonzero: dense attention waits for something that never

@@ -14,8 +14,11 @@ from typing import Optional
 
 from . import kv_cache as _kv
 from . import plan  # noqa: F401  (host-side sizing rules)
-from .kv_cache import (KV_STATUS_BITS, KVCache, alloc_kv_cache, alloc_kv_workspace, kv_append, kv_attention,  # noqa: F401
-                       kv_compact, kv_copy_pages, kv_fork, kv_free, kv_reserve, kv_scratch_bytes, kv_status)
+from . import qk_rope as _qk
+from .kv_cache import (KV_STATUS_BITS, KVCache, alloc_kv_cache, alloc_kv_workspace, kv_accept, kv_append,  # noqa: F401
+                       kv_attention, kv_compact, kv_copy_pages, kv_fork, kv_free, kv_reserve, kv_scratch_bytes,
+                       kv_status, kv_tree_mask)
+from .qk_rope import qk_norm_rope, rope_turns  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmqatopk.so")
@@ -93,6 +96,7 @@ def lib():
     for name in EXPORTS[:-1]:
         getattr(L, name).restype = I
     _kv.declare(L)
+    _qk.declare(L)
     _lib = L
     return L
 

@@ -33,6 +33,10 @@ SOURCES = [("mqa_fused.cu", "mqa_fused.o", []), ("mqa_fused.cu", "mqa_fused_fold
            ("mqatopk_api.cu", "mqatopk_api.o", []),
            # the paged key/value cache
            ("kv_attn.cu", "kv_attn.o", []), ("kv_prefill.cu", "kv_prefill.o", []),
+           ("kv_attn.cu", "kv_attn_window.o", ["-DMQA_KV_KIND=2"]), ("kv_attn.cu", "kv_attn_tree.o", ["-DMQA_KV_KIND=3"]),
+           ("kv_prefill.cu", "kv_prefill_window.o", ["-DMQA_KV_KIND=2"]),
+           ("kv_prefill.cu", "kv_prefill_tree.o", ["-DMQA_KV_KIND=3"]),
+           ("kv_tree.cu", "kv_tree.o", []), ("qk_rope.cu", "qk_rope.o", []),
            ("kv_append.cu", "kv_append.o", []), ("kv_pages.cu", "kv_pages.o", []),
            ("kv_api.cu", "kv_api.o", [])]
 HEADERS = ["mqa_internal.h", "ptx.cuh", "mqa_fold.h", "kv_internal.h", "kv_ptx.cuh"]
@@ -61,6 +65,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     # the compile flags live in this file: a change to it rebuilds every object
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "mqatopk.h"),
                                                        os.path.join(ROOT, "include", "mqakv.h"),
+                                                       os.path.join(ROOT, "include", "mqaqk.h"),
                                                        os.path.abspath(__file__)]
     objs, jobs = [], []
     for src, obj, defs in SOURCES:

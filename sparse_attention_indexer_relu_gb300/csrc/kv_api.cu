@@ -144,6 +144,20 @@ AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, 
   return p;
 }
 
+// Kernels by what their rows see.
+cudaError_t launch_tiled(KvKind kind, const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8,
+                         float *factor, int ctas, cudaStream_t stream) {
+  return kind == kWindow ? launch_kv_prefill<kWindow>(p, map, q_map, q8, factor, ctas, stream)
+         : kind == kTree ? launch_kv_prefill<kTree>(p, map, q_map, q8, factor, ctas, stream)
+                         : launch_kv_prefill<kDense>(p, map, q_map, q8, factor, ctas, stream);
+}
+cudaError_t launch_split(KvKind kind, const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int nb,
+                         int ctas, bool follows, cudaStream_t stream) {
+  return kind == kWindow ? launch_kv_attention<kWindow>(p, k_map, v_map, nb, ctas, follows, stream)
+         : kind == kTree ? launch_kv_attention<kTree>(p, k_map, v_map, nb, ctas, follows, stream)
+                         : launch_kv_attention<kDense>(p, k_map, v_map, nb, ctas, follows, stream);
+}
+
 int check_attention(const mqa_kv_cache *c, int rows, int q_heads) {
   const int rc = check_cache(c, kTables);
   if (rc != MQA_OK) return rc;
@@ -151,6 +165,90 @@ int check_attention(const mqa_kv_cache *c, int rows, int q_heads) {
       (long long)rows * q_heads > INT_MAX / kQueryTerms)
     return MQA_ERR_INVALID_ARGUMENT;
   return MQA_OK;
+}
+
+// The call behind every attention entry; view may be null.
+int attention(const mqa_kv_cache *cache, const void *q, long long q_row_stride, int type, int q_heads,
+              const int32_t *row_starts, int rows, int max_rows, const int32_t *selected, int n_selected, int causal,
+              const mqa_kv_view *view, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+              void *stream, const mqa_kv_debug_options *opt) {
+  int rc = check_attention(cache, rows, q_heads);
+  if (rc != MQA_OK) return rc;
+  if (opt && (opt->stall < 0 || opt->stall > 2 || opt->wait_timeout_ms < 0 || opt->wait_timeout_ms > 10000))
+    return MQA_ERR_INVALID_ARGUMENT;
+  if ((type != MQA_KV_BF16 && type != MQA_KV_FP16) || n_selected < 0 || (!selected && n_selected > 0) ||
+      !(scale > 0.f && scale <= kMaxScale))
+    return MQA_ERR_INVALID_ARGUMENT;
+  // a window of 0 sees everything up to the row's position; a mask goes without a window
+  if (view && (view->window < 0 || view->sinks < 0 || (view->sinks > 0 && view->window == 0) ||
+               (view->tree ? view->tree_words < 1 || view->window != 0 : view->tree_words != 0)))
+    return MQA_ERR_INVALID_ARGUMENT;
+  const KvKind kind = view && view->tree ? kTree : view && view->window ? kWindow : kDense;
+  if (rows == 0) return MQA_OK;
+  if (!q || !out || !row_starts || !workspace ||
+      (rows > 1 && q_row_stride < (long long)q_heads * cache->head_dim))
+    return MQA_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(out, 16) || q_row_stride % 8 || !aligned(row_starts, 4) || !aligned(selected, 4) ||
+      !aligned(lse, 4) || !aligned(workspace, 256) || (kind == kTree && !aligned(view->tree, 4)))
+    return MQA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = require_device(&sms);
+  if (rc != MQA_OK) return rc;
+  const AttnPlan P = plan_attention(sms, cache, rows, max_rows, q_heads, selected != nullptr);
+  if (workspace_bytes < P.bytes) return MQA_ERR_WORKSPACE_TOO_SMALL;
+  AttnParams p;
+  std::memset(&p, 0, sizeof p);
+  p.c = view_of(cache);
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.starts = row_starts;
+  p.selected = selected;
+  p.q_stride = q_row_stride;
+  p.rows = rows;
+  p.q_heads = q_heads;
+  p.group = q_heads / cache->kv_heads;
+  p.n_selected = n_selected;
+  p.causal = causal != 0 && kind != kTree;  // a mask alone says what is seen behind the first row
+  // (positions stay below 2^30)
+  if (kind == kWindow) p.window = std::min(view->window, 1 << 30), p.sinks = std::min(view->sinks, 1 << 30);
+  if (kind == kTree) p.tree = view->tree, p.tree_words = view->tree_words;
+  p.bf16 = type == MQA_KV_BF16;
+  p.scale_log2 = scale * 1.44269504088896341f;
+  p.wait_ns = (opt && opt->wait_timeout_ms ? opt->wait_timeout_ms : 2000) * 1000000ULL;
+  p.stall = opt ? opt->stall : 0;
+  p.test = p.stall || (opt && opt->wait_timeout_ms);
+  uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
+  if (P.tiled) {
+    p.max_cols = P.split ? kSplitCols : 0;
+    p.desc = reinterpret_cast<int4 *>(ws + P.tiled_off);
+    p.slots = reinterpret_cast<float *>(ws + P.tiled_slots_off);
+    CUtensorMap map, q_map;
+    uint8_t *terms = ws + P.terms_off;
+    float *factor = reinterpret_cast<float *>(ws + P.factor_off);
+    p.q_scale = factor;
+    rc = encode_code_rows(&map, cache->k, (uint64_t)cache->num_pages * cache->kv_heads * cache->page_size,
+                          cache->head_dim, (uint32_t)cache->page_size);
+    if (rc != MQA_OK) return rc;
+    rc = encode_code_rows(&q_map, terms, (uint64_t)(type == MQA_KV_BF16 ? 2 : 3) * rows * q_heads, cache->head_dim, 128);
+    if (rc != MQA_OK) return rc;
+    rc = code(launch_tiled(kind, p, map, q_map, terms, factor, P.tiled_ctas, as_stream(stream)));
+    if (rc == MQA_OK) rc = code(launch_kv_join_tiled(p, P.tiled_ctas, as_stream(stream)));
+    if (rc != MQA_OK || !P.split) return rc;
+  }
+  p.max_cols = P.tiled ? kSplitCols : INT_MAX;
+  p.desc = reinterpret_cast<int4 *>(ws);
+  p.slots = reinterpret_cast<float *>(ws + P.slots_off);
+  const uint64_t code_rows = (uint64_t)cache->num_pages * cache->kv_heads * cache->page_size;
+  CUtensorMap k_map, v_map;
+  std::memset(&k_map, 0, sizeof k_map);
+  std::memset(&v_map, 0, sizeof v_map);
+  if (!selected) {
+    rc = encode_code_rows(&k_map, cache->k, code_rows, cache->head_dim, 16);
+    if (rc == MQA_OK) rc = encode_code_rows(&v_map, cache->v, code_rows, cache->head_dim, 16);
+    if (rc != MQA_OK) return rc;
+  }
+  return code(launch_split(kind, p, k_map, v_map, P.nb, P.ctas, P.tiled, as_stream(stream)));
 }
 
 }  // namespace
@@ -206,75 +304,45 @@ int mqa_kv_attention_debug(const mqa_kv_cache *cache, const void *q, long long q
                            const int32_t *row_starts, int rows, int max_rows, const int32_t *selected, int n_selected,
                            int causal, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
                            void *stream, const mqa_kv_debug_options *opt) {
-  int rc = check_attention(cache, rows, q_heads);
+  return attention(cache, q, q_row_stride, type, q_heads, row_starts, rows, max_rows, selected, n_selected, causal,
+                   nullptr, scale, out, lse, workspace, workspace_bytes, stream, opt);
+}
+
+int mqa_kv_attention_view(const mqa_kv_cache *cache, const void *q, long long q_row_stride, int type, int q_heads,
+                          const int32_t *row_starts, int rows, int max_rows, const mqa_kv_view *view, float scale,
+                          void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+  if (!view) return MQA_ERR_INVALID_ARGUMENT;
+  return attention(cache, q, q_row_stride, type, q_heads, row_starts, rows, max_rows, nullptr, 0, 1, view, scale, out,
+                   lse, workspace, workspace_bytes, stream, nullptr);
+}
+
+int mqa_kv_tree_mask(const mqa_kv_cache *cache, const int32_t *parents, const int32_t *row_starts, int rows,
+                     int32_t *mask, int words, int32_t *positions, void *stream) {
+  int rc = check_cache(cache, kTables);
   if (rc != MQA_OK) return rc;
-  if (opt && (opt->stall < 0 || opt->stall > 2 || opt->wait_timeout_ms < 0 || opt->wait_timeout_ms > 10000))
-    return MQA_ERR_INVALID_ARGUMENT;
-  if ((type != MQA_KV_BF16 && type != MQA_KV_FP16) || n_selected < 0 || (!selected && n_selected > 0) ||
-      !(scale > 0.f && scale <= kMaxScale))
-    return MQA_ERR_INVALID_ARGUMENT;
+  if (rows < 0 || words < 1) return MQA_ERR_INVALID_ARGUMENT;
   if (rows == 0) return MQA_OK;
-  if (!q || !out || !row_starts || !workspace ||
-      (rows > 1 && q_row_stride < (long long)q_heads * cache->head_dim))
-    return MQA_ERR_INVALID_ARGUMENT;
-  if (!aligned(q, 16) || !aligned(out, 16) || q_row_stride % 8 || !aligned(row_starts, 4) || !aligned(selected, 4) ||
-      !aligned(lse, 4) || !aligned(workspace, 256))
+  if (!parents || !row_starts || !mask) return MQA_ERR_INVALID_ARGUMENT;
+  if (!aligned(parents, 4) || !aligned(row_starts, 4) || !aligned(mask, 4) || !aligned(positions, 4))
     return MQA_ERR_MISALIGNED;
   int sms = 0;
   rc = require_device(&sms);
   if (rc != MQA_OK) return rc;
-  const AttnPlan P = plan_attention(sms, cache, rows, max_rows, q_heads, selected != nullptr);
-  if (workspace_bytes < P.bytes) return MQA_ERR_WORKSPACE_TOO_SMALL;
-  AttnParams p;
-  std::memset(&p, 0, sizeof p);
-  p.c = view_of(cache);
-  p.q = q;
-  p.out = out;
-  p.lse = lse;
-  p.starts = row_starts;
-  p.selected = selected;
-  p.q_stride = q_row_stride;
-  p.rows = rows;
-  p.q_heads = q_heads;
-  p.group = q_heads / cache->kv_heads;
-  p.n_selected = n_selected;
-  p.causal = causal != 0;
-  p.bf16 = type == MQA_KV_BF16;
-  p.scale_log2 = scale * 1.44269504088896341f;
-  p.wait_ns = (opt && opt->wait_timeout_ms ? opt->wait_timeout_ms : 2000) * 1000000ULL;
-  p.stall = opt ? opt->stall : 0;
-  p.test = p.stall || (opt && opt->wait_timeout_ms);
-  uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
-  if (P.tiled) {
-    p.max_cols = P.split ? kSplitCols : 0;
-    p.desc = reinterpret_cast<int4 *>(ws + P.tiled_off);
-    p.slots = reinterpret_cast<float *>(ws + P.tiled_slots_off);
-    CUtensorMap map, q_map;
-    uint8_t *terms = ws + P.terms_off;
-    float *factor = reinterpret_cast<float *>(ws + P.factor_off);
-    p.q_scale = factor;
-    rc = encode_code_rows(&map, cache->k, (uint64_t)cache->num_pages * cache->kv_heads * cache->page_size,
-                          cache->head_dim, (uint32_t)cache->page_size);
-    if (rc != MQA_OK) return rc;
-    rc = encode_code_rows(&q_map, terms, (uint64_t)(type == MQA_KV_BF16 ? 2 : 3) * rows * q_heads, cache->head_dim, 128);
-    if (rc != MQA_OK) return rc;
-    rc = code(launch_kv_prefill(p, map, q_map, terms, factor, P.tiled_ctas, as_stream(stream)));
-    if (rc == MQA_OK) rc = code(launch_kv_join_tiled(p, P.tiled_ctas, as_stream(stream)));
-    if (rc != MQA_OK || !P.split) return rc;
-  }
-  p.max_cols = P.tiled ? kSplitCols : INT_MAX;
-  p.desc = reinterpret_cast<int4 *>(ws);
-  p.slots = reinterpret_cast<float *>(ws + P.slots_off);
-  const uint64_t code_rows = (uint64_t)cache->num_pages * cache->kv_heads * cache->page_size;
-  CUtensorMap k_map, v_map;
-  std::memset(&k_map, 0, sizeof k_map);
-  std::memset(&v_map, 0, sizeof v_map);
-  if (!selected) {
-    rc = encode_code_rows(&k_map, cache->k, code_rows, cache->head_dim, 16);
-    if (rc == MQA_OK) rc = encode_code_rows(&v_map, cache->v, code_rows, cache->head_dim, 16);
-    if (rc != MQA_OK) return rc;
-  }
-  return code(launch_kv_attention(p, k_map, v_map, P.nb, P.ctas, P.tiled, as_stream(stream)));
+  return code(launch_kv_tree_mask(view_of(cache), parents, row_starts, rows, mask, words, positions, as_stream(stream)));
+}
+
+int mqa_kv_accept(const mqa_kv_cache *cache, const int32_t *row_starts, int rows, const int32_t *counts,
+                  const int32_t *accepted, void *stream) {
+  int rc = check_cache(cache, kTables | kRefs);
+  if (rc != MQA_OK) return rc;
+  if (rows < 0) return MQA_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return MQA_OK;
+  if (!row_starts || !counts) return MQA_ERR_INVALID_ARGUMENT;
+  if (!aligned(row_starts, 4) || !aligned(counts, 4) || !aligned(accepted, 4)) return MQA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = require_device(&sms);
+  if (rc != MQA_OK) return rc;
+  return code(launch_kv_accept(view_of(cache), row_starts, counts, accepted, rows, sms, as_stream(stream)));
 }
 
 int mqa_kv_reserve(const mqa_kv_cache *cache, const int32_t *counts, void *stream) {

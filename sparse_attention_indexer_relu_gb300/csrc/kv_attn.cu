@@ -42,6 +42,12 @@
 
 #include <cfloat>
 
+// Compiled once for dense and selected attention (with the joining kernels), once
+// for windows and once for trees.
+#ifndef MQA_KV_KIND
+#define MQA_KV_KIND 0
+#endif
+
 namespace mqa {
 
 namespace {
@@ -73,7 +79,7 @@ struct Meta {
   int any[kStages];
 };
 
-template <int D, int NB, bool TEST>
+template <int D, int NB, int KIND, bool TEST>
 struct Smem {
   static constexpr bool test = TEST;
   union {
@@ -86,6 +92,7 @@ struct Smem {
   int dead;                     // a wait has run out
   float cs[8 * NB];             // per column: scale * log2(e) / (power of two q was multiplied with)
   int lim[8 * NB];              // positions the column sees: [0, lim)
+  int lo[KIND >= kWindow ? 8 * NB : 1];  // windows: where the column's begins; trees: its row (-1: none)
   float wm[kWarps][8 * NB], ww[kWarps][8 * NB], wl[kWarps][8 * NB];
   uint4 qf[NB][D / 32][32];     // q fragments
   long long scan[kWarps];
@@ -100,21 +107,24 @@ struct Item {
 
 }  // namespace
 
+#if MQA_KV_KIND == 0
 int attn_ctas_per_sm(int nb, int dim) {
   if (dim == 64) return nb == 1 ? Cfg<64, 1>::ctas : nb == 2 ? Cfg<64, 2>::ctas : nb == 3 ? Cfg<64, 3>::ctas : Cfg<64, 4>::ctas;
   return nb == 1 ? Cfg<128, 1>::ctas : nb == 2 ? Cfg<128, 2>::ctas : nb == 3 ? Cfg<128, 3>::ctas : Cfg<128, 4>::ctas;
 }
 size_t attn_slot_floats(int nb, int dim) { return (size_t)8 * nb * (dim + 4); }
+#endif
 
 namespace {
 
-template <int D, int NB, bool SEL, bool TEST>
+template <int D, int NB, int KIND, bool TEST>
 __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
     kv_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap k_map,
                    const __grid_constant__ CUtensorMap v_map) {
   grid_dependents();
   extern __shared__ uint8_t smem_raw[];
-  using S = Smem<D, NB, TEST>;
+  constexpr bool SEL = KIND == kSelected, WIN = KIND == kWindow, TREE = KIND == kTree;
+  using S = Smem<D, NB, KIND, TEST>;
   S &sm = *reinterpret_cast<S *>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   constexpr int CB = 8 * NB;
   constexpr int KW = D / 16;   // words of a K row per lane (8 or 4)
@@ -138,7 +148,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
     rows_of(s, r0, n);
     const long long cols = (long long)n * group;
     ncb = cols > p.max_cols ? 0 : (int)((cols + CB - 1) / CB);
-    tiles = ncb ? max(1, (length_of(s) + kTile - 1) / kTile) : 0;
+    const int len = length_of(s);
+    tiles = ncb ? max(1, (len + kTile - 1) / kTile - (WIN ? skipped_tiles<kTile>(p, len - n + 1) : 0)) : 0;
   };
   long long total;
   // a warp has a run of sequences, 32 at a time
@@ -244,23 +255,39 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
     __syncthreads();     // the previous segment's readers of cs / lim / merge are done
     if (tid < CB) {
       int lim = SEL ? 0 : INT32_MAX;  // columns behind the last take part like the others (a query of zeros)
+      int lo = TREE ? -1 : INT32_MIN;
       if (tid < ncols) {
         const int i = SEL ? it.seq - r0 : (c0 + tid) / group;
         lim = p.causal ? min(max(len - n + i + 1, 0), len) : len;
         if (SEL && (i < 0 || i >= n)) lim = 0;
+        if (WIN) lo = lim - p.window;
+        if (TREE) lo = r0 + i;
       }
       sm.lim[tid] = lim;
+      if (WIN || TREE) sm.lo[tid] = lo;
     }
     __syncthreads();
     int lim_max = 0, lim_min = INT32_MAX;
+    int lo_max = 0, lo_min = INT32_MAX;  // windows
 #pragma unroll
     for (int i = 0; i < CB; ++i) {
       lim_max = max(lim_max, i < ncols ? sm.lim[i] : 0);
       lim_min = min(lim_min, i < ncols ? sm.lim[i] : INT32_MAX);
+      if (WIN) {
+        lo_max = max(lo_max, i < ncols ? sm.lo[i] : 0);
+        lo_min = min(lo_min, i < ncols ? sm.lo[i] : INT32_MAX);
+      }
     }
+    const int own0 = len - n;  // trees: position of the sequence's first row
+    // first position of the warp's 16 in tile i of the segment
+    const int sinks_end = WIN ? sink_tiles<kTile>(p) : 0, skip = WIN ? skipped_tiles<kTile>(p, len - n + 1) : 0;
+    auto base_of = [&](int i) {
+      const int t = t0 + i;
+      return (WIN && t >= sinks_end ? t + skip : t) * kTile + warp * 16;
+    };
     const int32_t *sel = SEL ? p.selected + (size_t)it.seq * p.n_selected : nullptr;
     // the tiles this item needs: later ones hold no key that a column sees
-    const int t1e = SEL ? t1 : min(t1, (lim_max + kTile - 1) / kTile);
+    const int t1e = SEL ? t1 : min(t1, (lim_max + kTile - 1) / kTile - skip);
     const int iters = max(0, t1e - t0);
     // ---- loads, 16 rows of keys and of values per sub-tile, the 16-byte chunks
     // of a row exchanged so that both products' reads spread over the banks:
@@ -316,7 +343,6 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
       }
       const uint32_t no = copies++;
       const int stage = no % kStages;
-      const int base = (t0 + i) * kTile + warp * 16;
       uint64_t *bar = &sm.full[warp][stage];
       uint8_t *kd = sm.ring[warp][stage], *vd = kd + 16 * D;
       if (SEL) {
@@ -345,8 +371,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
         cp_async_commit();
       } else {
         if ((i & 31) == 0) {
-          const int pos = base + lane * kTile;
-          const bool want = i + lane < iters && pos < lim_max;
+          const int pos = base_of(i + lane);
+          const bool want = i + lane < iters && pos < lim_max && (!WIN || pos < p.sinks || pos + 16 > lo_min);
           d_row = want ? row_of(pos, load_page(pos)) : -1;
           load_exps(d_row);
         }
@@ -529,7 +555,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
           int room[2];  // by how much a column's limit lies behind the key
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int k = SEL ? g + 8 * r : 0, pos = SEL ? meta.pos[stage][k] : (t0 + i) * kTile + warp * 16;
+            const int k = SEL ? g + 8 * r : 0, pos = SEL ? meta.pos[stage][k] : base_of(i);
             ks[r] = meta.ks[stage][k];
             lv[r] = meta.lv[stage][k];
             none[r] = SEL && pos == INT32_MAX ? -INFINITY : 0.f;  // an entry that names no visible key
@@ -544,7 +570,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
                   for (int nb = 0; nb < NB; ++nb) acc[nb][2 * r] = acc[nb][2 * r + 1] = NAN;
                 }
             }
-          } else if (bad_keys || (t0 + i) * kTile + warp * 16 + 16 > lim_min) {
+          } else if (bad_keys || base_of(i) + 16 > (TREE ? own0 : lim_min) ||
+                     (WIN && base_of(i) < lo_max && base_of(i) + 16 > p.sinks)) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -553,7 +580,12 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
                 for (int c = 0; c < 2; ++c) {
                   if (bad_keys >> (g + 8 * r) & 1) acc[nb][2 * r + c] = NAN;
                   // (scales are positive: -inf stays -inf)
-                  if (room[r] >= min(sm.lim[nb * 8 + 2 * t + c], lim_max)) acc[nb][2 * r + c] = -INFINITY;
+                  const int col = nb * 8 + 2 * t + c;
+                  if (room[r] >= min(sm.lim[col], lim_max)) acc[nb][2 * r + c] = -INFINITY;
+                  if (WIN && room[r] < sm.lo[col] && room[r] >= p.sinks) acc[nb][2 * r + c] = -INFINITY;
+                  if (TREE && sm.lo[col] >= 0 &&
+                      !(tree_bits(p.tree + (size_t)sm.lo[col] * p.tree_words, p.tree_words, room[r] - own0) & 1))
+                    acc[nb][2 * r + c] = -INFINITY;
                 }
           }
           for (bool anew = false;; anew = true) {
@@ -755,6 +787,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
 
 }  // namespace
 
+#if MQA_KV_KIND == 0
 // Join split items: a block adds the parts of two columns of the item that CTA
 // blockIdx.x of the kernel before began.  One long sequence is cut into one part
 // per CTA, so four warps share a column's parts, each its own in CTA order, and
@@ -872,21 +905,42 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(const AttnParams p) {
   }
 }
 
+}  // namespace
+
+cudaError_t launch_kv_join(const AttnParams &p, int nb, int ctas, cudaStream_t stream) {
+  const dim3 grid(ctas, 4 * nb);
+  return p.c.dim == 64 ? launch_after(kv_join_kernel<64>, grid, 256, 0, stream, true, p, 8 * nb)
+                       : launch_after(kv_join_kernel<128>, grid, 256, 0, stream, true, p, 8 * nb);
+}
+
+cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream) {
+  const dim3 grid(ctas, kTiledCols / 32);
+  return p.c.dim == 64 ? launch_after(kv_join_few_kernel<64>, grid, 256, 0, stream, true, p)
+                       : launch_after(kv_join_few_kernel<128>, grid, 256, 0, stream, true, p);
+}
+
+#endif  // MQA_KV_KIND == 0
+
+namespace {
+
 template <int D, int NB>
 cudaError_t launch(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int ctas, bool follows,
                    cudaStream_t stream) {
-  constexpr size_t bytes = sizeof(Smem<D, NB, false>) + 1024;
+  constexpr size_t bytes = sizeof(Smem<D, NB, MQA_KV_KIND, false>) + 1024;
   static DeviceFlags done[3];
   auto run = [&](auto *kernel, DeviceFlags &flags) {
     const cudaError_t e = allow_smem(kernel, bytes, flags);
     return e != cudaSuccess ? e
                             : launch_after(kernel, dim3(ctas), kAttnThreads, bytes, stream, follows, p, k_map, v_map);
   };
-  const cudaError_t e = p.selected ? run(kv_attn_kernel<D, NB, true, false>, done[0])
-                        : p.test   ? run(kv_attn_kernel<D, NB, false, true>, done[1])
-                                   : run(kv_attn_kernel<D, NB, false, false>, done[2]);
-  if (e != cudaSuccess) return e;
-  return launch_after(kv_join_kernel<D>, dim3(ctas, 4 * NB), 256, 0, stream, true, p, 8 * NB);
+#if MQA_KV_KIND == 0
+  const cudaError_t e = p.selected ? run(kv_attn_kernel<D, NB, kSelected, false>, done[0])
+                        : p.test   ? run(kv_attn_kernel<D, NB, kDense, true>, done[1])
+                                   : run(kv_attn_kernel<D, NB, kDense, false>, done[2]);
+#else
+  const cudaError_t e = run(kv_attn_kernel<D, NB, MQA_KV_KIND, false>, done[0]);
+#endif
+  return e != cudaSuccess ? e : launch_kv_join(p, NB, ctas, stream);
 }
 
 template <int D>
@@ -901,16 +955,11 @@ cudaError_t launch_d(const AttnParams &p, const CUtensorMap &k_map, const CUtens
 }
 }  // namespace
 
-cudaError_t launch_kv_attention(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int nb,
-                                int ctas, bool follows, cudaStream_t stream) {
+template <>
+cudaError_t launch_kv_attention<MQA_KV_KIND>(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                             int nb, int ctas, bool follows, cudaStream_t stream) {
   return p.c.dim == 64 ? launch_d<64>(p, k_map, v_map, nb, ctas, follows, stream)
                        : launch_d<128>(p, k_map, v_map, nb, ctas, follows, stream);
-}
-
-cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream) {
-  const dim3 grid(ctas, kTiledCols / 32);
-  return p.c.dim == 64 ? launch_after(kv_join_few_kernel<64>, grid, 256, 0, stream, true, p)
-                       : launch_after(kv_join_few_kernel<128>, grid, 256, 0, stream, true, p);
 }
 
 }  // namespace mqa

@@ -50,6 +50,11 @@ inline KvScratch kv_scratch(int pages, int seqs) {
   return s;
 }
 
+// Which positions rows see: up to their own (or all), the selected ones, a window
+// and first positions, or the ones before the sequence's rows and those of the
+// rows that the mask names.  Kernels are compiled for each.
+enum KvKind : int { kDense = 0, kSelected = 1, kWindow = 2, kTree = 3 };
+
 // Attention call.
 struct AttnParams {
   KvView c;
@@ -61,6 +66,9 @@ struct AttnParams {
   long long q_stride;
   int rows, q_heads, group, n_selected, causal, bf16;
   float scale_log2;  // softmax scale * log2(e)
+  int window, sinks;    // kWindow: a row sees the last `window` positions up to its own, and the first `sinks`
+  const int32_t *tree;  // kTree: [rows, tree_words], bit j: the row sees its sequence's row j
+  int tree_words;
   int max_cols;      // sequences of more (row, head of the group) columns go to the tiled kernel
   int4 *desc;        // per CTA: the split item it began, for the joining kernel
   float *slots;      // per CTA: two slots of partial results
@@ -83,18 +91,29 @@ constexpr int kQueryTerms = 3;  // e4m3 terms of an fp16 query value; a bf16 one
 // map: the keys' codes as rows of head_dim bytes, boxes of one page; q_map: the
 // query terms (q8, workspace of kQueryTerms * rows * q_heads * head_dim bytes)
 // in boxes of 128 rows; factor: rows * q_heads floats, p.q_scale.
+// KIND: not kSelected.
+template <int KIND>
 cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8,
                               float *factor, int ctas, cudaStream_t stream);
 // Its joining pass (p.desc and p.slots are the tiled kernel's).
 cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream);
 // follows: another kernel of the same call is before it on the stream.
 // k_map, v_map: codes as rows of head_dim bytes, boxes of 16 rows (not used for
-// selected keys).
+// selected keys).  KIND: kDense serves selected keys as well.
+template <int KIND>
 cudaError_t launch_kv_attention(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int nb,
                                 int ctas, bool follows, cudaStream_t stream);
+// The split kernel's joining pass.
+cudaError_t launch_kv_join(const AttnParams &p, int nb, int ctas, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,
                              const int32_t *starts, int rows, int sms, cudaStream_t stream);
+
+cudaError_t launch_kv_tree_mask(const KvView &c, const int32_t *parents, const int32_t *starts, int rows, int32_t *mask,
+                                int words, int32_t *positions, cudaStream_t stream);
+// accepted may be null: the first counts[s] rows stay.
+cudaError_t launch_kv_accept(const KvView &c, const int32_t *starts, const int32_t *counts, const int32_t *accepted,
+                             int rows, int sms, cudaStream_t stream);
 
 struct KvPools {
   uint8_t *data[4 + MQA_KV_MAX_EXTRA];

@@ -49,10 +49,16 @@
 
 #include <cfloat>
 
+// Compiled once for dense attention, once for windows and once for trees.
+#ifndef MQA_KV_KIND
+#define MQA_KV_KIND 0
+#endif
+
 namespace mqa {
 
 namespace {
 
+constexpr int kKind = MQA_KV_KIND;
 constexpr int kThreads = 512;
 constexpr int kKeys = 128;                // keys per tile
 constexpr int kCols = kTiledCols;         // columns per item
@@ -109,10 +115,16 @@ __device__ __forceinline__ int block_limit(const AttnParams &p, const Seq &q, in
   const int last = min(q.n - 1, (block * kCols + kCols - 1) / p.group);
   return p.causal ? min(max(q.len - q.n + last + 1, 0), q.len) : q.len;
 }
+// Windows: the tiles that none of a block's columns sees, between the first
+// positions and the window of the block's first row.
+__device__ __forceinline__ int block_skip(const AttnParams &p, const Seq &q, int block) {
+  if (kKind != kWindow || q.len < q.n) return 0;
+  return skipped_tiles<kKeys>(p, q.len - q.n + 1 + (int)((long long)block * kCols / p.group));
+}
 // Tiles of a block, and of all blocks before it.  (More rows than positions:
 // every block counts as the whole length.)
 __device__ __forceinline__ int block_tiles(const AttnParams &p, const Seq &q, int block) {
-  return tiles_for(p.causal && q.len >= q.n ? block_limit(p, q, block) : q.len);
+  return tiles_for(p.causal && q.len >= q.n ? block_limit(p, q, block) : q.len) - block_skip(p, q, block);
 }
 __device__ long long tiles_before(const AttnParams &p, const Seq &q, int block) {
   if (!p.causal || q.len < q.n) return (long long)block * tiles_for(q.len);
@@ -120,13 +132,24 @@ __device__ long long tiles_before(const AttnParams &p, const Seq &q, int block) 
   const long long g = p.group;
   long long sum = floor_sum(inner, kKeys * g, kCols, kCols - 1 + g * (q.len - q.n + kKeys));
   if (block > inner) sum += tiles_for(q.len);
+  if (kKind == kWindow) {
+    // less block_skip(b) = max(0, floor((kCols b + c g) / (kKeys g))), from the first b whose numerator is not negative
+    const long long cg = g * (q.len - q.n + 1LL - p.window - (long long)kKeys * sink_tiles<kKeys>(p));
+    const long long b0 = cg < 0 ? (-cg + kCols - 1) / kCols : 0;
+    if (block > b0) sum -= floor_sum(block - b0, kKeys * g, kCols, kCols * b0 + cg);
+  }
   return sum;
 }
 
 struct Part {  // a part of an item: tiles [t0, t1) of tiles
   int seq, head, block, tiles, t0, t1;
+  int skip;  // windows: block_skip
   Seq q;
 };
+// First position of tile t.
+__device__ __forceinline__ int tile_at(const AttnParams &p, const Part &x, int t) {
+  return (kKind == kWindow && t >= sink_tiles<kKeys>(p) ? t + x.skip : t) * kKeys;
+}
 
 // The CTA's parts, one after another.  Each warp walks by itself; its state lies
 // in shared memory, where lane 0 moves it on (in registers it would crowd out
@@ -149,12 +172,13 @@ struct Walk {
       }
     }
     x.tiles = block_tiles(p, x.q, x.block);
+    x.skip = block_skip(p, x.q, x.block);
     fit();
   }
   // key tiles that hold a key some column sees
   __device__ __forceinline__ int needed(const AttnParams &p) const {
     const int lim = block_limit(p, x.q, x.block);
-    return max(0, min(x.t1, (lim + kKeys - 1) / kKeys) - x.t0);
+    return max(0, min(x.t1, (lim + kKeys - 1) / kKeys - (kKind == kWindow ? x.skip : 0)) - x.t0);
   }
   __device__ __forceinline__ int cols(const AttnParams &p) const {
     return (int)min((long long)kCols, (long long)x.q.n * p.group - (long long)x.block * kCols);
@@ -314,6 +338,9 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
     for (; w.valid(); step_on(p, w)) {
       const int nt = w.needed(p);
       const int lim = block_limit(p, w.x.q, w.x.block), first = w.x.t0 * kKeys + g * 16, head = w.x.head;
+      // windows: positions before the first column's window, and behind the first positions, are not needed
+      const int lo = kKind == kWindow ? w.x.q.len - w.x.q.n + 1 + (int)((long long)w.x.block * kCols / p.group) - p.window
+                                      : 0;
       const int32_t *table = p.c.table + (size_t)w.x.seq * p.c.max_pages;
       float lv_max = -128.f;
       auto ask = [&] {  // the part's queries
@@ -330,10 +357,11 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
       const bool begins = q_no == 0;
       if (begins && nt > 0) ask();  // the first part's before anything is looked up
       for (int tb = 0; tb < nt; tb += 4) {
-        const int t = tb + (lane >> 3), pos = first + t * kKeys;
+        const int t = tb + (lane >> 3), pos = kKind == kWindow ? tile_at(p, w.x, w.x.t0 + t) + g * 16 : first + t * kKeys;
         int row = -2;
         float ks = 1.f, lv = 0.f;
-        if (t < nt && pos < lim) {
+        const int at = pos - g % per_box * 16;  // of the box: it is copied whole, from its first 16 keys' row on
+        if (t < nt && pos < lim && (kKind != kWindow || at < p.sinks || at + box > lo)) {
           const int page = __ldg(table + (pos >> p.c.page_log2));
           if ((unsigned)page < (unsigned)p.c.pages) {
             const int ph = page * heads + head;
@@ -671,6 +699,41 @@ __device__ __noinline__ float weigh_far(uint32_t ts, const TileMeta &meta, float
   return l;
 }
 
+// Windows: scores of the keys of a tile at `base` that the column [lo, lim) does
+// not see.
+__device__ __noinline__ void hide_outside(uint32_t ts, int base, int lo, int lim, int sinks) {
+#pragma unroll 1
+  for (int j = base; j < base + kKeys; j += 32) {
+    if (__all_sync(~0u, j + 32 <= lim && (j >= lo || j + 32 <= sinks))) continue;
+    uint32_t s[32];
+    tmem_ld_32x32b_x32(ts + (j - base), s);
+    tmem_ld_wait();
+#pragma unroll
+    for (int b = 0; b < 32; ++b)
+      if (j + b >= lim || (j + b < lo && j + b >= sinks)) s[b] = 0xFF800000u;
+    tmem_st32(ts + (j - base), s);
+  }
+  tmem_st_wait();
+}
+// Trees: scores of the keys of a tile at `base` that the mask of the column's row
+// (bit 0: position `own`) leaves out, and of those behind the sequence.
+__device__ __noinline__ void hide_others(uint32_t ts, int base, int own, int len, const int32_t *mask, int words) {
+#pragma unroll 1
+  for (int j = base; j < base + kKeys; j += 32) {
+    uint32_t see = mask ? tree_bits(mask, words, j - own) : 0u;
+    if (j + 32 > len) see = j >= len ? 0u : see & ((1u << (len - j)) - 1);
+    if (__all_sync(~0u, see == ~0u)) continue;
+    uint32_t s[32];
+    tmem_ld_32x32b_x32(ts + (j - base), s);
+    tmem_ld_wait();
+#pragma unroll
+    for (int b = 0; b < 32; ++b)
+      if (!(see >> b & 1)) s[b] = 0xFF800000u;
+    tmem_st32(ts + (j - base), s);
+  }
+  tmem_st_wait();
+}
+
 // Scores of keys at or behind the column's limit, in TMEM.
 __device__ __noinline__ void hide_behind(uint32_t ts, int room) {
 #pragma unroll 1
@@ -713,6 +776,14 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
       room0 = p.causal ? min(max(w.x.q.len - w.x.q.n + c / p.group + 1, 0), w.x.q.len) : w.x.q.len;
       cs = __ldcg(p.q_scale + (size_t)w.x.head * p.rows * p.group + (size_t)w.x.q.r0 * p.group + c);
     }
+    // windows: the column sees [lo, lim) and the first positions; trees: its row's mask
+    const int lim = room0, lo = kKind == kWindow ? lim - p.window : 0;
+    const int lim_min = kKind == kWindow ? __reduce_min_sync(~0u, lim) : 0;
+    const int lo_max = kKind == kWindow ? __reduce_max_sync(~0u, lo) : 0;
+    const int own = w.x.q.len - w.x.q.n;
+    const int32_t *mask = nullptr;
+    if (kKind == kTree && col < ncols)
+      mask = p.tree + (size_t)(w.x.q.r0 + (w.x.block * kCols + col) / p.group) * p.tree_words;
     room0 -= w.x.t0 * kKeys;
     const int whole_tiles = __reduce_min_sync(~0u, room0) / kKeys;  // tiles every column of the warp sees whole
     for (int t = 0; t < nt; ++t, ++tile_no) {
@@ -723,13 +794,25 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
       const TileMeta &meta = sm.meta[tile_no % kMeta];
       const int room = room0 - t * kKeys;  // keys of the tile that the column sees
       if (meta.odd) hide_keys(ts, meta);
-      if (t >= whole_tiles) hide_behind(ts, room);  // (not below: 128 live scores and a branch spill)
+      // (not below: 128 live scores and a branch spill)
+      if (kKind == kWindow) {
+        const int base = tile_at(p, w.x, w.x.t0 + t);
+        if (base + kKeys > lim_min || (base < lo_max && base + kKeys > p.sinks))
+          hide_outside(ts, base, lo, lim, p.sinks);
+      } else if (kKind == kTree) {
+        const int base = (w.x.t0 + t) * kKeys;
+        if (base + kKeys > own) hide_others(ts, base, own, w.x.q.len, mask, p.tree_words);
+      } else if (t >= whole_tiles) {
+        hide_behind(ts, room);
+      }
       // The weights are formed with the references as they stand.  A tile in which
       // 16 of them sum to more than 2^12 (or the scores pass m by as much) is done
       // again with new references: its scores are still in TMEM then.  The first
       // tile has its references set first.
       const bool look = meta.spread > kFar - 16.f;
-      for (bool anew = t == 0;; anew = true) {
+      // (Columns of a window or tree may see nothing of it; theirs are set with the
+      // first key that they see.)
+      for (bool anew = t == 0 || (kKind != kDense && __any_sync(~0u, m == -INFINITY && col < ncols));; anew = true) {
         if (anew) settle<D>(ts, to, meta, cs, t > 0, m, wr, l);
         if (look && __any_sync(~0u, wr - meta.lv_min - m > kFar)) {
           if (!anew) continue;
@@ -972,6 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     c.x.block = lo;
     c.x.tiles = block_tiles(p, c.x.q, lo);
+    c.x.skip = block_skip(p, c.x.q, lo);
     c.off = (int)(rest - begins);
     if (lane == 0) sm.cut[warp] = c;
   }
@@ -1118,11 +1202,14 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &map, const CUtensorMa
 
 }  // namespace
 
-cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8,
-                              float *factor, int ctas, cudaStream_t stream) {
+template <>
+cudaError_t launch_kv_prefill<MQA_KV_KIND>(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map,
+                                           uint8_t *q8, float *factor, int ctas, cudaStream_t stream) {
+#if MQA_KV_KIND == 0
   if (p.test)
     return p.c.dim == 64 ? launch<64, true>(p, map, q_map, q8, factor, ctas, stream)
                          : launch<128, true>(p, map, q_map, q8, factor, ctas, stream);
+#endif
   return p.c.dim == 64 ? launch<64, false>(p, map, q_map, q8, factor, ctas, stream)
                        : launch<128, false>(p, map, q_map, q8, factor, ctas, stream);
 }

@@ -213,6 +213,23 @@ inline cudaError_t allow_smem(K *kernel, size_t bytes, DeviceFlags &done) {
   return e;
 }
 
+// Tiles of kKeys positions that window rows do not read: the ones behind the first
+// positions' tiles and before the tile in which the window of the first row begins,
+// whose last seen position is `lim` - 1.
+template <int kKeys>
+__device__ __forceinline__ int sink_tiles(const AttnParams &p) { return (int)(((long long)p.sinks + kKeys - 1) / kKeys); }
+template <int kKeys>
+__device__ __forceinline__ int skipped_tiles(const AttnParams &p, int lim) {
+  return max(max(lim - p.window, 0) / kKeys - sink_tiles<kKeys>(p), 0);
+}
+// Bits j0 .. j0 + 31 of a row's mask; the positions before bit 0 are seen, those
+// behind the last word are not.
+__device__ __forceinline__ uint32_t tree_bits(const int32_t *row, int words, int j0) {
+  const int a = j0 >> 5;
+  auto word = [&](int i) { return i < 0 ? ~0u : i < words ? (uint32_t)__ldg(row + i) : 0u; };
+  return __funnelshift_r(word(a), word(a + 1), j0 & 31);
+}
+
 template <int CB, int D>
 __host__ __device__ constexpr size_t attn_slot_floats_dev() {
   return (size_t)CB * (D + 4);

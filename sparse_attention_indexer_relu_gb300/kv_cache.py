@@ -2,9 +2,10 @@
 
 A `KVCache` holds the cache's tensors (the caller's) and passes them to the C
 entries: `kv_reserve` makes room, `kv_append` writes new keys and values,
-`kv_attention` reads them (all visible keys, or the ones `mqa_topk_prefill`
-selected), and `kv_fork`, `kv_free`, `kv_compact` and `kv_copy_pages` manage
-the pages.  As in the rest of the package only arguments are marshalled here.
+`kv_attention` reads them (all visible keys, a window and the first ones, or
+the ones `mqa_topk_prefill` selected), `kv_tree_mask` and `kv_accept` serve
+drafted tokens, and `kv_fork`, `kv_free`, `kv_compact` and `kv_copy_pages`
+manage the pages.  As in the rest of the package only arguments are marshalled here.
 """
 from __future__ import annotations
 
@@ -14,7 +15,7 @@ import math
 from typing import Optional, Sequence
 
 KV_EXPORTS = ("mqa_kv_scratch_bytes", "mqa_kv_append", "mqa_kv_attention_workspace_bytes", "mqa_kv_attention",
-              "mqa_kv_attention_debug",
+              "mqa_kv_attention_debug", "mqa_kv_attention_view", "mqa_kv_tree_mask", "mqa_kv_accept",
               "mqa_kv_reserve", "mqa_kv_fork", "mqa_kv_free", "mqa_kv_compact", "mqa_kv_copy_pages",
               "mqa_kv_get_status")
 KV_STATUS_BITS = {1: "out_of_pages", 2: "bad_index", 4: "bad_list", 8: "bad_length", 16: "wait_timeout"}
@@ -34,6 +35,11 @@ class _Cache(ctypes.Structure):
                                              "max_pages", "n_extra")] + [("extra", _Pool * _MAX_EXTRA)])
 
 
+class _View(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int), ("sinks", ctypes.c_int), ("tree", ctypes.c_void_p),
+                ("tree_words", ctypes.c_int)]
+
+
 class KVDebugOptions(ctypes.Structure):
     _fields_ = [("stall", ctypes.c_int), ("wait_timeout_ms", ctypes.c_int)]
 
@@ -47,6 +53,9 @@ def declare(L):
     L.mqa_kv_attention_workspace_bytes.argtypes = [I, C, I, I, ctypes.POINTER(S)]
     L.mqa_kv_attention.argtypes = [C, P, Q, I, I, P, I, I, P, I, I, F, P, P, P, S, P]
     L.mqa_kv_attention_debug.argtypes = L.mqa_kv_attention.argtypes + [ctypes.POINTER(KVDebugOptions)]
+    L.mqa_kv_attention_view.argtypes = [C, P, Q, I, I, P, I, I, ctypes.POINTER(_View), F, P, P, P, S, P]
+    L.mqa_kv_tree_mask.argtypes = [C, P, P, I, P, I, P, P]
+    L.mqa_kv_accept.argtypes = [C, P, I, P, P, P]
     L.mqa_kv_reserve.argtypes = [C, P, P]
     L.mqa_kv_fork.argtypes = [C, P, P, I, P]
     L.mqa_kv_free.argtypes = [C, P, I, P]
@@ -226,7 +235,7 @@ def _on_other(cache, stream):
     with torch.cuda.device(cache.device):
         s = torch.cuda.current_stream() if stream is None else stream
         if s.device != cache.device:
-            raise ValueError(f"the stream is on {s.device}, the cache on {cache.device}")
+            raise ValueError(f"the stream is on {s.device}, the call's tensors on {cache.device}")
         with torch.cuda.stream(s):
             yield s.cuda_stream
 
@@ -282,9 +291,26 @@ def kv_append(cache: KVCache, k, v, row_starts, stream=None):
                  "mqa_kv_append")
 
 
+def _view_of(cache, rows, selected, causal, debug, window, sinks, tree):
+    import torch
+    if selected is not None or debug is not None or not causal:
+        raise ValueError("window and tree go with causal calls over all positions, without selected and debug")
+    if tree is not None:
+        if window is not None or sinks:
+            raise ValueError("window and tree do not go together")
+        _dense(tree, (torch.int32,), 2, "tree", cache.device)
+        if tree.shape[0] != rows or tree.shape[1] < 1:
+            raise ValueError(f"tree has shape {tuple(tree.shape)}, expected ({rows}, words)")
+        # (a tensor without rows has no address)
+        return _View(0, 0, tree.data_ptr() or cache.seq_lens.data_ptr(), int(tree.shape[1]))
+    if window is None or not 1 <= int(window) < 2 ** 31 or not 0 <= int(sinks) < 2 ** 31:
+        raise ValueError(f"window {window} and sinks {sinks}: a window of at least one position is expected")
+    return _View(int(window), int(sinks), None, 0)
+
+
 def kv_attention(q, cache: KVCache, row_starts, selected=None, causal: bool = True, scale: Optional[float] = None,
                  max_rows: Optional[int] = None, workspace=None, out=None, lse=None, stream=None,
-                 debug: Optional[dict] = None):
+                 debug: Optional[dict] = None, window: Optional[int] = None, sinks: int = 0, tree=None):
     """Attention of rows q [rows, q_heads, head_dim] (bf16 or fp16) over the cache; returns out, of q's shape.
 
     Row i of the n rows of a sequence is its position seq_len - n + i and sees the positions up to its own (every
@@ -292,7 +318,12 @@ def kv_attention(q, cache: KVCache, row_starts, selected=None, causal: bool = Tr
     answer of `mqa_topk_prefill`).  scale defaults to head_dim ** -0.5.  max_rows: the most rows of one sequence, if
     known (it only helps to choose the kernels).  lse [rows, q_heads] float32 receives the logarithm of each
     softmax's sum.  Rows before row_starts[0] and at or behind row_starts[-1] are left as they are in `out`
-    and `lse`.  debug: test-only knobs (KVDebugOptions)."""
+    and `lse`.  debug: test-only knobs (KVDebugOptions).
+
+    window: a row sees the last `window` positions up to its own, and of the earlier ones the sequence's first `sinks`.
+    tree [rows, words] int32: the rows are drafted tokens that hang on one another; a row sees every position before its
+    sequence's rows, and those of the rows whose bits are set in its mask (`kv_tree_mask`).  One of selected, window and
+    tree at most, the latter two of causal calls."""
     import torch
     m, types = _api(), _types()
     qp, qs = _rows(q, cache, (torch.bfloat16, torch.float16), None, "q")
@@ -307,6 +338,9 @@ def kv_attention(q, cache: KVCache, row_starts, selected=None, causal: bool = Tr
             raise ValueError(f"selected has {selected.shape[0]} rows, q {rows}")
         n_sel = int(selected.shape[1])
         sp = selected.data_ptr() or rs  # an empty list still is a list
+    view = None
+    if window is not None or tree is not None or sinks:
+        view = _view_of(cache, rows, selected, causal, debug, window, sinks, tree)
     with _on(cache, stream) as s:
         if out is None:
             out = torch.empty((rows, heads, cache.head_dim), dtype=q.dtype, device=cache.device)
@@ -319,16 +353,67 @@ def kv_attention(q, cache: KVCache, row_starts, selected=None, causal: bool = Tr
             workspace = alloc_kv_workspace(cache, rows, heads)
         elif workspace.device != cache.device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {cache.device}")
-        args = (cache._ref, qp, qs, types[q.dtype], heads, rs, rows, int(max_rows or 0), sp, n_sel, int(bool(causal)),
-                cache.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
+        head = (cache._ref, qp, qs, types[q.dtype], heads, rs, rows, int(max_rows or 0))
+        tail = (cache.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
                 None if lse is None else lse.data_ptr(), workspace.data_ptr(),
                 workspace.numel() * workspace.element_size(), s)
-        if debug is None:
+        args = head + (sp, n_sel, int(bool(causal))) + tail
+        if view is not None:
+            m._check(m.lib().mqa_kv_attention_view(*head, ctypes.byref(view), *tail), "mqa_kv_attention_view")
+        elif debug is None:
             m._check(m.lib().mqa_kv_attention(*args), "mqa_kv_attention")
         else:
             m._check(m.lib().mqa_kv_attention_debug(*args, ctypes.byref(KVDebugOptions(**debug))),
                      "mqa_kv_attention_debug")
     return out
+
+
+def kv_tree_mask(cache: KVCache, parents, row_starts, max_rows: int, mask=None, positions=None, stream=None):
+    """Masks and positions of drafted rows, for `kv_attention(tree=)` and the rotation of their heads.
+
+    parents [rows] int32: the row that each row hangs on, as its number among its sequence's rows (an earlier one), or -1
+    for the position before them.  max_rows: the most rows of one sequence.  Returns (mask [rows, ceil(max_rows / 32)]
+    int32, positions [rows] int32); a row's position is where it will be if it is accepted.  Rows of no sequence are left
+    as they were (zeros in tensors made here)."""
+    import torch
+    m = _api()
+    p = _list(parents, cache, "parents")
+    rows = int(parents.shape[0])
+    if int(max_rows) < 1:
+        raise ValueError(f"max_rows {max_rows}: at least one row is expected")
+    words = -(-int(max_rows) // 32)
+    rs = _list(row_starts, cache, "row_starts", cache.max_seqs + 1)
+    if mask is not None and tuple(_dense(mask, (torch.int32,), 2, "mask", cache.device).shape) != (rows, words):
+        raise ValueError(f"mask has shape {tuple(mask.shape)}, expected {(rows, words)}")
+    if positions is not None:
+        _list(positions, cache, "positions", rows)
+    with _on(cache, stream) as s:
+        if mask is None:
+            mask = torch.zeros((rows, words), dtype=torch.int32, device=cache.device)
+        if positions is None:
+            positions = torch.zeros(rows, dtype=torch.int32, device=cache.device)
+        m._check(m.lib().mqa_kv_tree_mask(cache._ref, p, rs, rows, mask.data_ptr(), words, positions.data_ptr(), s),
+                 "mqa_kv_tree_mask")
+    return mask, positions
+
+
+def kv_accept(cache: KVCache, row_starts, counts, accepted=None, rows: Optional[int] = None, stream=None):
+    """Keep counts[s] (int32 [max_seqs]) of the rows that are sequence s's last positions, and give the rest back: the
+    sequence gets shorter, pages that it no longer needs become free.
+
+    accepted [rows] int32: entry row_starts[s] + i, i < counts[s], is the number among the sequence's rows of the one
+    that becomes its i-th, ascending; without it the first ones stay, and `rows` says how many there are in all."""
+    m = _api()
+    ap = None
+    if accepted is not None:
+        ap = _list(accepted, cache, "accepted", rows)
+        rows = int(accepted.shape[0])
+    elif rows is None:
+        raise ValueError("rows is needed where accepted is not given")
+    cp = _list(counts, cache, "counts", cache.max_seqs)
+    rs = _list(row_starts, cache, "row_starts", cache.max_seqs + 1)
+    with _on(cache, stream) as s:
+        m._check(m.lib().mqa_kv_accept(cache._ref, rs, int(rows), cp, ap, s), "mqa_kv_accept")
 
 
 def kv_reserve(cache: KVCache, counts, stream=None):

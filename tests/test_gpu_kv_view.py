@@ -1,0 +1,434 @@
+"""Windows and trees over the paged 8-bit cache, the trees' masks and accepted rows, against plain 64-bit forms."""
+import numpy as np
+import pytest
+
+import kv_reference as ref
+import view_reference as view
+from test_gpu_kv import check, ints, mqa, rows_of, starts_of  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(mqa, c, rng, rows, group, dtype="bf16", max_rows=None, extra_rows=0, mask=None, **sees):  # noqa: F811
+    import torch
+    st = starts_of(rows)
+    m, n = int(st[-1]), int(st[-1]) + extra_rows
+    q, qd = rows_of(rng, n, c.heads * group, c.dim, dtype)
+    dev = ref.to_device(c, mqa)
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    if mask is not None:
+        wide = np.concatenate([mask, np.full((extra_rows, mask.shape[1]), -1, np.int32)])
+        mqa.kv_attention(q, dev, ints(st), tree=ints(wide), max_rows=max_rows, out=out, lse=lse)
+        seen = view.tree_seen(c, st, mask)
+    else:
+        mqa.kv_attention(q, dev, ints(st), max_rows=max_rows, out=out, lse=lse, **sees)
+        seen = view.window_seen(c, st, sees["window"], sees.get("sinks", 0))
+    assert mqa.kv_status(dev) == 0
+    assert (out[m:] == 7).all() and (lse[m:] == 7).all()  # rows behind the last sequence
+    check(out[:m], lse[:m], c.attention(qd[:m], st, c.dim ** -0.5, dtype, seen, causal=mask is None))
+    return out, lse, dev, q, st
+
+
+CASES = [  # page, heads, group, dim, lens, rows
+    (16, 1, 1, 128, [1], [1]),
+    (64, 2, 4, 128, [0, 1, 63, 64, 65, 700], [1, 1, 1, 1, 1, 1]),
+    (32, 2, 8, 64, [0, 5, 333, 0], [0, 3, 2, 1]),
+    (16, 3, 3, 64, [100, 257], [5, 7]),
+    (128, 1, 16, 128, [129, 1000], [1, 2]),
+    (64, 2, 5, 128, [700], [9]),
+    (32, 2, 2, 128, [2, 40], [5, 40]),            # more rows than positions
+    (64, 1, 4, 128, [130, 77, 64], [130, 77, 1]),
+    (16, 2, 8, 128, [700], [70]),
+    (128, 1, 3, 64, [400, 0, 90, 513], [200, 0, 90, 9]),
+    (64, 2, 1, 128, [1500], [600]),
+    (64, 1, 7, 64, [100, 260], [150, 200]),
+    (16, 3, 5, 64, [257, 256, 255], [255, 256, 100]),
+]
+WINDOWS = [(1, 0), (1, 1), (16, 0), (64, 4), (100, 17), (128, 128), (300, 0), (257, 200), (5000, 3), (7, 5000),
+           (2 ** 31 - 1, 2 ** 31 - 1)]
+
+
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_window(mqa, case, window, sinks):  # noqa: F811
+    page, heads, group, dim, lens, rows = case
+    rng = np.random.default_rng(len(lens) * 100 + group + window % 1000)
+    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 2, heads, page, dim, lens, 100)
+    dtype = "bf16" if (window + dim) % 3 else "fp16"
+    attend(mqa, c, rng, rows, group, dtype, extra_rows=3, window=window, sinks=sinks)
+    attend(mqa, c, rng, rows, group, dtype, max_rows=1, window=window, sinks=sinks)  # every sequence on the split kernel
+
+
+@pytest.mark.parametrize("window,sinks", [(1000, 4), (4096, 0), (129, 300)])
+@pytest.mark.parametrize("rows", [1, 8, 300])
+def test_window_far_behind_the_first_positions(mqa, rows, window, sinks):  # noqa: F811
+    rng = np.random.default_rng(rows + window)
+    c = ref.random_cache(rng, 200, 1, 64, 128, [9001, 2500], 160)
+    attend(mqa, c, rng, [rows, 2 * rows // 3], 4, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("rows,max_rows", [([9, 1], 1), ([90, 40], None)])
+def test_a_window_as_long_as_the_sequences_is_no_window(mqa, rows, max_rows):  # noqa: F811
+    """Bit by bit what the call without one gives."""
+    import torch
+    rng = np.random.default_rng(5)
+    c = ref.random_cache(rng, 40, 2, 16, 128, [300, 200], 30)
+    out, lse, dev, q, st = attend(mqa, c, rng, rows, 4, window=300, max_rows=max_rows)
+    l2 = torch.zeros_like(lse)
+    assert torch.equal(out, mqa.kv_attention(q, dev, ints(st), max_rows=max_rows, lse=l2)) and torch.equal(lse, l2)
+
+
+def test_nan_codes_outside_a_window(mqa):  # noqa: F811
+    """A NaN key or value counts for the rows whose window holds it, in tiles that other rows see as well."""
+    for rows in ([6, 5], [100, 90]):
+        for window, sinks in ((20, 0), (20, 3)):
+            rng = np.random.default_rng(14)
+            c = ref.random_cache(rng, 30, 2, 16, 128, [170, 140], 12)
+            c.v[c.table[0, 150 // 16], 0, 150 % 16, 3] = 127
+            c.k[c.table[1, 110 // 16], 1, 110 % 16, 100] = 255
+            c.v[c.table[1, 0], 0, 1, 0] = 127
+            out, *_ = attend(mqa, c, rng, rows, 4, window=window, sinks=sinks)
+            assert out.isnan().any() == (rows[0] == 100 or sinks > 0 or rows[1] > 5) or not out.isnan().all()
+
+
+def test_a_window_over_bad_tables(mqa):  # noqa: F811
+    """Pages that no row's window needs are not looked at; one that is needed and outside the pool is not followed."""
+    rng = np.random.default_rng(17)
+    c = ref.random_cache(rng, 30, 2, 16, 64, [300], 30)
+    dev = ref.to_device(c, mqa)
+    dev.page_table[0, 3:9] = 1 << 30
+    for n in (2, 60):
+        q, qd = rows_of(rng, n, 8, 64, "fp16")
+        st = np.array([0, n])
+        got = mqa.kv_attention(q, dev, ints(st), window=90, sinks=20)
+        assert mqa.kv_status(dev) == 0
+        check(got, None, c.attention(qd, st, 0.125, "fp16", view.window_seen(c, st, 90, 20)))
+    dev.page_table[0, 17] = -5
+    seen = view.window_seen(c, st, 90, 20)
+    seen[(seen >= 272) & (seen < 288)] = -1
+    got = mqa.kv_attention(q, dev, ints(st), window=90, sinks=20)
+    assert mqa.kv_status(dev) == 2
+    check(got, None, c.attention(qd, st, 0.125, "fp16", seen))
+
+
+TREES = CASES + [(64, 2, 4, 128, [1000, 900], [64, 37]), (16, 1, 1, 64, [400], [333]), (32, 1, 32, 128, [500], [12])]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", TREES, ids=str)
+def test_tree(mqa, case, dtype):  # noqa: F811
+    page, heads, group, dim, lens, rows = case
+    rng = np.random.default_rng(len(lens) * 100 + group)
+    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 2, heads, page, dim, lens, 100)
+    parents = view.random_parents(rng, rows)
+    mask, _ = view.tree_mask(c, starts_of(rows), parents, -(-max(rows) // 32))
+    attend(mqa, c, rng, rows, group, dtype, mask=mask, extra_rows=3)
+    attend(mqa, c, rng, rows, group, dtype, mask=mask, max_rows=1)
+
+
+@pytest.mark.parametrize("max_rows", [1, None])
+@pytest.mark.parametrize("words", [1, 2, 5])
+def test_tree_masks_of_any_kind(mqa, words, max_rows):  # noqa: F811
+    """Random bits (later rows and rows behind the sequence's last among them), no bit at all, too few words."""
+    rng = np.random.default_rng(words)
+    c = ref.random_cache(rng, 60, 2, 16, 64, [0, 100, 7, 300], 20)
+    rows = [3, 70, 7, 40]  # sequence 0 has no positions, sequence 2 none before its rows
+    mask = rng.integers(-2 ** 31, 2 ** 31, (120, words)).astype(np.int32)
+    mask[5] = 0
+    mask[74:77] = 0
+    out, lse, *_ = attend(mqa, c, rng, rows, 4, mask=mask, max_rows=max_rows)
+    assert not out[:3].any() and not out[74:77].any() and lse[74:77].isneginf().all()
+
+
+def test_a_chain_is_causal(mqa):  # noqa: F811
+    """Rows that hang on the one before them see what they see without a mask."""
+    rng = np.random.default_rng(9)
+    c = ref.random_cache(rng, 40, 2, 16, 128, [300, 200], 30)
+    rows = [40, 33]
+    parents = np.concatenate([np.arange(n) - 1 for n in rows])
+    mask, pos = view.tree_mask(c, starts_of(rows), parents, 2)
+    assert np.array_equal(pos, np.concatenate([np.arange(260, 300), np.arange(167, 200)]))
+    out, _, dev, q, st = attend(mqa, c, rng, rows, 4, mask=mask)
+    check(mqa.kv_attention(q, dev, ints(st)), None, c.attention(q.double().cpu().numpy(), st, 128 ** -0.5, "bf16"))
+
+
+def test_tree_nan_codes(mqa):  # noqa: F811
+    """A drafted row with a NaN value counts for the rows that hang on it."""
+    rng = np.random.default_rng(10)
+    for rows in ([6, 4], [60, 50]):
+        c = ref.random_cache(rng, 40, 2, 16, 128, [200, 150], 13)
+        p = 200 - rows[0] + 2
+        c.v[c.table[0, p // 16], 1, p % 16, 9] = 127
+        parents = view.random_parents(rng, rows)
+        mask, _ = view.tree_mask(c, starts_of(rows), parents, 2)
+        attend(mqa, c, rng, rows, 4, mask=mask)
+
+
+def test_least_alignment_of_masks_and_strided_rows(mqa):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(11)
+    c = ref.random_cache(rng, 40, 2, 16, 64, [200], 13)
+    for n in (5, 50):
+        wide = torch.from_numpy(rng.standard_normal((n, 12, 64))).to(torch.bfloat16).cuda()
+        q, st = wide[:, 2:10], np.array([0, n])
+        mask, _ = view.tree_mask(c, st, view.random_parents(rng, [n]), 2)
+        odd = torch.zeros(2 * n + 1, dtype=torch.int32, device="cuda")[1:].view(n, 2)
+        odd.copy_(ints(mask))
+        dev = ref.to_device(c, mqa)
+        qd = q.double().cpu().numpy()
+        check(mqa.kv_attention(q, dev, ints(st), tree=odd), None,
+              c.attention(qd, st, 0.125, "bf16", view.tree_seen(c, st, mask), causal=False))
+        check(mqa.kv_attention(q, dev, ints(st), window=60, sinks=2), None,
+              c.attention(qd, st, 0.125, "bf16", view.window_seen(c, st, 60, 2)))
+
+
+# ---------------------------------------------------------------- masks
+@pytest.mark.parametrize("rows", [[1], [5, 0, 33], [64] * 7, [300, 2, 1], [1500, 40]], ids=str)
+def test_masks_and_positions(mqa, rows):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(sum(rows))
+    lens = [n + int(rng.integers(0, 50)) for n in rows]
+    c = ref.random_cache(rng, sum(-(-n // 16) for n in lens) + 2, 1, 16, 64, lens, 200)
+    dev, st = ref.to_device(c, mqa), starts_of(rows)
+    parents = view.random_parents(rng, rows)
+    for max_rows in (max(rows), 32, 700):
+        mask, pos = mqa.kv_tree_mask(dev, ints(parents), ints(st), max_rows)
+        want = view.tree_mask(c, st, parents, -(-max_rows // 32))
+        assert np.array_equal(mask.cpu().numpy(), want[0]) and np.array_equal(pos.cpu().numpy(), want[1])
+    # rows of no sequence are left alone; bounds that leave the rows are cut to them
+    n = int(st[-1])
+    held = torch.full((n + 3, 2), 5, dtype=torch.int32, device="cuda")
+    pos = torch.full((n + 3,), 5, dtype=torch.int32, device="cuda")
+    more = np.concatenate([[0, 0], parents, [9]]).astype(np.int32)
+    mqa.kv_tree_mask(dev, ints(more), ints(st + 2), 64, mask=held, positions=pos)
+    want = view.tree_mask(c, st, parents, 2)
+    assert np.array_equal(held[2:-1].cpu().numpy(), want[0]) and np.array_equal(pos[2:-1].cpu().numpy(), want[1])
+    assert (held[:2] == 5).all() and (held[-1] == 5).all() and (pos[:2] == 5).all() and pos[-1] == 5
+    assert mqa.kv_status(dev) == 0
+
+
+def test_parents_that_are_no_earlier_rows(mqa):  # noqa: F811
+    rng = np.random.default_rng(3)
+    c = ref.random_cache(rng, 10, 1, 16, 64, [50], 5)
+    dev, st = ref.to_device(c, mqa), np.array([0, 6])
+    for bad in (3, 5, 2 ** 31 - 1, -2, -2 ** 31):
+        parents = np.array([-1, 0, 1, bad, 3, 1], np.int32)
+        mask, pos = mqa.kv_tree_mask(dev, ints(parents), ints(st), 6)
+        assert mqa.kv_status(dev) == 2
+        want = view.tree_mask(c, st, parents, 1)
+        assert np.array_equal(mask.cpu().numpy(), want[0]) and np.array_equal(pos.cpu().numpy(), want[1])
+
+
+# ---------------------------------------------------------------- accepting
+ACCEPT = [  # page, heads, dim, lens, rows
+    (16, 1, 64, [1], [1]),
+    (16, 2, 128, [40, 33, 16, 100], [7, 16, 16, 50]),
+    (64, 3, 64, [200, 90, 0, 64], [64, 1, 0, 64]),
+    (128, 1, 128, [500, 129], [300, 129]),
+    (32, 2, 64, [333] * 9, [20] * 9),
+]
+
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("case", ACCEPT, ids=str)
+def test_accept(mqa, case, seed):  # noqa: F811
+    page, heads, dim, lens, rows = case
+    rng = np.random.default_rng(seed * 100 + page)
+    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 2, heads, page, dim, lens, 40, spread=1 + 3 * seed)
+    dev, st = ref.to_device(c, mqa), starts_of(rows)
+    counts, accepted = view.random_accepted(rng, rows)
+    if seed == 3:  # everything stays
+        counts = np.array(rows, np.int32)
+        accepted = np.concatenate([np.arange(n) for n in rows]).astype(np.int32)
+    mqa.kv_accept(dev, ints(st), ints(counts), ints(accepted))
+    view.accept(c, st, counts, accepted)
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+    mqa.kv_accept(dev, ints(st * 0), ints(counts), ints(accepted))  # no rows: nothing changes
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+
+
+def test_accept_the_first_rows(mqa):  # noqa: F811
+    """Without a list: a plain roll-back; shared pages are given back once."""
+    rng = np.random.default_rng(4)
+    lens, rows = [40, 33, 16, 100], [7, 16, 16, 50]
+    c = ref.random_cache(rng, 30, 2, 16, 64, lens, 9)
+    c.refs[c.table[3, 4]] = 2
+    dev, st = ref.to_device(c, mqa), starts_of(rows)
+    counts = np.array([7, 0, 0, 3], np.int32)
+    mqa.kv_accept(dev, ints(st), ints(counts), rows=int(st[-1]))
+    view.accept(c, st, counts)
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+
+
+def test_accept_nan_and_extreme_scales(mqa):  # noqa: F811
+    """NaN codes move and set no scale; scales up to both ends of their range."""
+    rng = np.random.default_rng(6)
+    lens, rows = [60, 61], [30, 40]
+    c = ref.random_cache(rng, 12, 2, 16, 64, lens, 5, spread=100)
+    for s in (0, 1):
+        p = lens[s] - 3
+        c.k[c.table[s, p // 16], 0, p % 16, :7] = 127
+        c.v[c.table[s, p // 16], 1, p % 16, :] = 127
+    dev, st = ref.to_device(c, mqa), starts_of(rows)
+    counts = np.array([20, 11], np.int32)
+    accepted = np.zeros(70, np.int32)
+    accepted[:20] = np.sort(rng.choice(27, 20, replace=False))
+    accepted[19] = 27
+    accepted[30:41] = [0, 1, 5, 7, 8, 20, 30, 35, 36, 37, 39]
+    mqa.kv_accept(dev, ints(st), ints(counts), ints(accepted))
+    view.accept(c, st, counts, accepted)
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(counts=[8, 2, 1]), 4), (dict(counts=[-1, 2, 1]), 4), (dict(accepted=[1, 1, 2]), 4),
+    (dict(accepted=[2, 1, 3]), 4), (dict(accepted=[-1, 0, 1]), 4), (dict(accepted=[0, 1, 7]), 4),
+    (dict(len=6), 8), (dict(len=10 ** 6), 8), (dict(len=-1), 8)])
+def test_a_refused_list_changes_its_sequence_not_the_others(mqa, change, status):  # noqa: F811
+    rng = np.random.default_rng(7)
+    c = ref.random_cache(rng, 20, 2, 16, 64, [40, 33, 20], 9)
+    rows = [7, 16, 3]
+    counts, accepted = np.array([3, 2, 1], np.int32), np.arange(26, dtype=np.int32) % 7
+    accepted[:3], accepted[7:9], accepted[23] = [1, 3, 6], [4, 15], 2
+    if "counts" in change:
+        counts[:] = change["counts"]
+    if "accepted" in change:
+        accepted[:3] = change["accepted"]
+    st = starts_of(rows)
+    if "len" in change:
+        c.lens[0] = change["len"]
+    dev = ref.to_device(c, mqa)
+    mqa.kv_accept(dev, ints(st), ints(counts), ints(accepted))
+    others = st.copy()
+    others[0] = 7  # sequence 0 without rows
+    view.accept(c, others, counts, accepted)
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == status
+
+
+def test_accept_over_bad_tables(mqa):  # noqa: F811
+    """Pages outside the pool are not followed: nothing moves from them, to them or into their place."""
+    rng = np.random.default_rng(8)
+    c = ref.random_cache(rng, 20, 1, 16, 64, [60, 60], 6)
+    dev, st = ref.to_device(c, mqa), np.array([0, 40, 80])
+    dev.page_table[0, 2] = 99
+    dev.page_table[1, 3] = -1
+    accepted = np.concatenate([np.arange(0, 40, 3), np.zeros(26), np.arange(1, 40, 2), np.zeros(20)]).astype(np.int32)
+    before = dev.page_table.clone()
+    mqa.kv_accept(dev, ints(st), ints([14, 20]), ints(accepted))
+    assert mqa.kv_status(dev) == 2 and dev.seq_lens.tolist() == [34, 40]
+    assert (dev.page_table[:, :2] == before[:, :2]).all() and (dev.page_table[:, 3] == -1).all()
+
+
+# ---------------------------------------------------------------- together
+def test_a_speculative_step(mqa):  # noqa: F811
+    """Prompt; then rounds of: room for a draft, its masks and positions, rotated heads appended and attended, what was
+    accepted taken over.  Against the plain forms, and the kept rows against a cache that never held the others."""
+    import torch
+    rng = np.random.default_rng(20)
+    heads, group, dim, page = 2, 4, 64, 16
+    c = ref.random_cache(rng, 40, heads, page, dim, [0, 0], 16, garbage=False)
+    dev = ref.to_device(c, mqa)
+    turns = mqa.rope_turns(10000.0 ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim))
+    ws = mqa.alloc_kv_workspace(dev, 100, heads * group)
+    for step, rows in enumerate(([37, 50], [9, 13], [16, 1], [5, 20])):
+        st, n = starts_of(rows), sum(rows)
+        mqa.kv_reserve(dev, ints(rows))
+        assert c.reserve(np.array(rows)) == 0
+        parents = view.random_parents(rng, rows) if step else np.concatenate([np.arange(k) - 1 for k in rows])
+        mask, pos = mqa.kv_tree_mask(dev, ints(parents), ints(st), max(rows))
+        want = view.tree_mask(c, st, parents, mask.shape[1])
+        assert np.array_equal(mask.cpu().numpy(), want[0]) and np.array_equal(pos.cpu().numpy(), want[1])
+        qkv, _ = rows_of(rng, n, heads * (group + 2), dim, "bf16")
+        q, k = mqa.qk_norm_rope(qkv[:, :heads * group], qkv[:, heads * group:heads * (group + 1)], turns, pos)
+        v = qkv[:, heads * (group + 1):]
+        mqa.kv_append(dev, k, v, ints(st))
+        c.append(k.double().cpu().numpy(), v.double().cpu().numpy(), st)
+        assert ref.same(c, dev) == []
+        qd = q.double().cpu().numpy()
+        got = mqa.kv_attention(q, dev, ints(st), tree=mask, max_rows=max(rows), workspace=ws)
+        check(got, None, c.attention(qd, st, dim ** -0.5, "bf16", view.tree_seen(c, st, want[0]), causal=False))
+        got = mqa.kv_attention(q, dev, ints(st), window=20, sinks=2, max_rows=max(rows), workspace=ws)
+        check(got, None, c.attention(qd, st, dim ** -0.5, "bf16", view.window_seen(c, st, 20, 2)))
+        if step:  # a path from a random row up
+            counts, accepted = np.zeros(2, np.int32), np.zeros(n, np.int32)
+            for s, r in enumerate(rows):
+                path, at = [], int(rng.integers(0, r))
+                while at >= 0:
+                    path.append(at)
+                    at = int(parents[st[s] + at])
+                counts[s] = len(path)
+                accepted[st[s]:st[s] + len(path)] = path[::-1]
+            mqa.kv_accept(dev, ints(st), ints(counts), ints(accepted))
+            view.accept(c, st, counts, accepted)
+            assert ref.same(c, dev) == []
+    assert mqa.kv_status(dev) == 0
+
+
+def test_a_speculative_step_in_a_graph(mqa):  # noqa: F811
+    """Reserve, masks, attention in both forms and acceptance captured once, replayed with other contents."""
+    import torch
+    rng = np.random.default_rng(21)
+    heads, group, dim, page = 2, 4, 64, 16
+    c = ref.random_cache(rng, 60, heads, page, dim, [30, 100], 30)
+    dev = ref.to_device(c, mqa)
+    rows = np.array([12, 20], np.int32)
+    st, n = starts_of(rows), 32
+    drows, dst = ints(rows), ints(st)
+    q, k, v = (torch.zeros((n, h, dim), dtype=torch.bfloat16, device="cuda") for h in (heads * group, heads, heads))
+    parents, counts, accepted = ints(np.zeros(n) - 1), ints([0, 0]), ints(np.zeros(n))
+    mask, pos = ints(np.zeros((n, 1))), ints(np.zeros(n))
+    ws = [mqa.alloc_kv_workspace(dev, n, heads * group) for _ in range(2)]
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        mqa.kv_reserve(dev, drows)
+        mqa.kv_tree_mask(dev, parents, dst, 32, mask=mask, positions=pos)
+        mqa.kv_append(dev, k, v, dst)
+        mqa.kv_attention(q, dev, dst, tree=mask, workspace=ws[0], out=outs[0])
+        mqa.kv_attention(q, dev, dst, window=40, sinks=4, workspace=ws[1], out=outs[1])
+        mqa.kv_accept(dev, dst, counts, accepted)
+    torch.cuda.synchronize()
+    for i in range(8):
+        qn, kn, vn = (rows_of(rng, n, h, dim, "bf16") for h in (heads * group, heads, heads))
+        pn = view.random_parents(rng, rows)
+        cn, an = view.random_accepted(rng, rows)
+        cn = np.minimum(cn, 15)
+        for t, x in ((q, qn[0]), (k, kn[0]), (v, vn[0]), (parents, ints(pn)), (counts, ints(cn)), (accepted, ints(an))):
+            t.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert c.reserve(rows) == 0
+        want = view.tree_mask(c, st, pn, 1)
+        assert np.array_equal(mask.cpu().numpy(), want[0]) and np.array_equal(pos.cpu().numpy(), want[1])
+        c.append(kn[1], vn[1], st)
+        check(outs[0], None, c.attention(qn[1], st, 0.125, "bf16", view.tree_seen(c, st, want[0]), causal=False), i)
+        check(outs[1], None, c.attention(qn[1], st, 0.125, "bf16", view.window_seen(c, st, 40, 4)), i)
+        view.accept(c, st, cn, an)
+        assert ref.same(c, dev) == [], i
+    assert mqa.kv_status(dev) == 0
+
+
+def test_as_many_sequences_as_there_may_be(mqa):  # noqa: F811
+    rng = np.random.default_rng(79)
+    n = 65536
+    lens, rows = np.zeros(n, np.int64), np.zeros(n, np.int64)
+    pick = rng.choice(n, 40, replace=False)
+    pick[:2] = 0, n - 1
+    lens[pick] = rng.integers(1, 90, 40)
+    rows[pick] = np.minimum(lens[pick], rng.integers(1, 60, 40))
+    lens[pick[5]], rows[pick[5]] = 700, 300
+    c = ref.random_cache(rng, 600, 1, 16, 64, lens, 45)
+    st = starts_of(rows)
+    attend(mqa, c, rng, rows, 4, window=33, sinks=4)
+    attend(mqa, c, rng, rows, 4, "fp16", max_rows=2, window=33, sinks=4)
+    parents = view.random_parents(rng, rows)
+    mask, pos = view.tree_mask(c, st, parents, 10)
+    _, _, dev, _, _ = attend(mqa, c, rng, rows, 4, mask=mask)
+    got = mqa.kv_tree_mask(dev, ints(parents), ints(st), 300)
+    assert np.array_equal(got[0].cpu().numpy(), mask) and np.array_equal(got[1].cpu().numpy(), pos)
+    counts, accepted = view.random_accepted(rng, rows)
+    mqa.kv_accept(dev, ints(st), ints(counts), ints(accepted))
+    view.accept(c, st, counts, accepted)
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
