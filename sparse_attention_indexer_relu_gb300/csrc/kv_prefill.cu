@@ -699,9 +699,14 @@ __device__ __noinline__ float weigh_far(uint32_t ts, const TileMeta &meta, float
   return l;
 }
 
-// Windows: scores of the keys of a tile at `base` that the column [lo, lim) does
-// not see.
-__device__ __noinline__ void hide_outside(uint32_t ts, int base, int lo, int lim, int sinks) {
+// Windows: scores of the part's tile t that the column does not see.  (What says so
+// is formed here, anew for each of these few tiles, and not held over all tiles.)
+__device__ __noinline__ void hide_outside(uint32_t ts, const Part &x, int t, int col, int ncols, int group, int window,
+                                          int sinks) {
+  const int first_tiles = (int)(((long long)sinks + kKeys - 1) / kKeys), v = x.t0 + t;
+  const int base = (v >= first_tiles ? v + x.skip : v) * kKeys;
+  const int lim = col < ncols ? min(max(x.q.len - x.q.n + (x.block * kCols + col) / group + 1, 0), x.q.len) : 0;
+  const int lo = lim - window;
 #pragma unroll 1
   for (int j = base; j < base + kKeys; j += 32) {
     if (__all_sync(~0u, j + 32 <= lim && (j >= lo || j + 32 <= sinks))) continue;
@@ -715,12 +720,15 @@ __device__ __noinline__ void hide_outside(uint32_t ts, int base, int lo, int lim
   }
   tmem_st_wait();
 }
-// Trees: scores of the keys of a tile at `base` that the mask of the column's row
-// (bit 0: position `own`) leaves out, and of those behind the sequence.
-__device__ __noinline__ void hide_others(uint32_t ts, int base, int own, int len, const int32_t *mask, int words) {
+// Trees: scores of the part's tile t that the mask of the column's row leaves out,
+// and of those behind the sequence.
+__device__ __noinline__ void hide_others(uint32_t ts, const Part &x, int t, int col, int ncols, int group,
+                                         const int32_t *tree, int words) {
+  const int base = (x.t0 + t) * kKeys, own = x.q.len - x.q.n, len = x.q.len;
+  const int32_t *mask = tree + (size_t)(x.q.r0 + (x.block * kCols + col) / group) * words;
 #pragma unroll 1
   for (int j = base; j < base + kKeys; j += 32) {
-    uint32_t see = mask ? tree_bits(mask, words, j - own) : 0u;
+    uint32_t see = col < ncols ? tree_bits(mask, words, j - own) : 0u;
     if (j + 32 > len) see = j >= len ? 0u : see & ((1u << (len - j)) - 1);
     if (__all_sync(~0u, see == ~0u)) continue;
     uint32_t s[32];
@@ -776,43 +784,42 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
       room0 = p.causal ? min(max(w.x.q.len - w.x.q.n + c / p.group + 1, 0), w.x.q.len) : w.x.q.len;
       cs = __ldcg(p.q_scale + (size_t)w.x.head * p.rows * p.group + (size_t)w.x.q.r0 * p.group + c);
     }
-    // windows: the column sees [lo, lim) and the first positions; trees: its row's mask
-    const int lim = room0, lo = kKind == kWindow ? lim - p.window : 0;
-    const int lim_min = kKind == kWindow ? __reduce_min_sync(~0u, lim) : 0;
-    const int lo_max = kKind == kWindow ? __reduce_max_sync(~0u, lo) : 0;
-    const int own = w.x.q.len - w.x.q.n;
-    const int32_t *mask = nullptr;
-    if (kKind == kTree && col < ncols)
-      mask = p.tree + (size_t)(w.x.q.r0 + (w.x.block * kCols + col) / p.group) * p.tree_words;
-    room0 -= w.x.t0 * kKeys;
-    const int whole_tiles = __reduce_min_sync(~0u, room0) / kKeys;  // tiles every column of the warp sees whole
+    // Tiles [from, whole_tiles) every column of the warp sees whole (dense: from the
+    // first on; windows: positions from the latest window's begin to the first limit;
+    // trees: before the sequence's rows).
+    int from = 0, whole_tiles;
+    if (kKind == kWindow) {
+      whole_tiles = (__reduce_min_sync(~0u, col < ncols ? room0 : INT32_MAX) >> 7) - w.x.skip - w.x.t0;
+      from = __reduce_max_sync(~0u, col < ncols ? room0 - p.window : 0);
+      from = from > 0 ? (from + kKeys - 1) / kKeys - w.x.skip - w.x.t0 : 0;
+    } else if (kKind == kTree) {
+      whole_tiles = max(w.x.q.len - w.x.q.n, 0) / kKeys - w.x.t0;
+    } else {
+      room0 -= w.x.t0 * kKeys;
+      whole_tiles = __reduce_min_sync(~0u, room0) / kKeys;
+    }
     for (int t = 0; t < nt; ++t, ++tile_no) {
       bounded_wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p);
       bounded_wait(sm, &sm.s_full[x], s_no++ & 1, p);
       __syncwarp();
       tc_fence_after();
       const TileMeta &meta = sm.meta[tile_no % kMeta];
-      const int room = room0 - t * kKeys;  // keys of the tile that the column sees
       if (meta.odd) hide_keys(ts, meta);
-      // (not below: 128 live scores and a branch spill)
-      if (kKind == kWindow) {
-        const int base = tile_at(p, w.x, w.x.t0 + t);
-        if (base + kKeys > lim_min || (base < lo_max && base + kKeys > p.sinks))
-          hide_outside(ts, base, lo, lim, p.sinks);
-      } else if (kKind == kTree) {
-        const int base = (w.x.t0 + t) * kKeys;
-        if (base + kKeys > own) hide_others(ts, base, own, w.x.q.len, mask, p.tree_words);
-      } else if (t >= whole_tiles) {
-        hide_behind(ts, room);
+      const bool edge = t >= whole_tiles || (kKind == kWindow && t < from);
+      if (edge) {  // (not below: 128 live scores and a branch spill)
+        if (kKind == kWindow) hide_outside(ts, w.x, t, col, ncols, p.group, p.window, p.sinks);
+        else if (kKind == kTree) hide_others(ts, w.x, t, col, ncols, p.group, p.tree, p.tree_words);
+        else hide_behind(ts, room0 - t * kKeys);  // keys of the tile that the column sees
       }
       // The weights are formed with the references as they stand.  A tile in which
       // 16 of them sum to more than 2^12 (or the scores pass m by as much) is done
       // again with new references: its scores are still in TMEM then.  The first
       // tile has its references set first.
       const bool look = meta.spread > kFar - 16.f;
-      // (Columns of a window or tree may see nothing of it; theirs are set with the
-      // first key that they see.)
-      for (bool anew = t == 0 || (kKind != kDense && __any_sync(~0u, m == -INFINITY && col < ncols));; anew = true) {
+      // (Columns of a window or tree may see nothing of it and of more tiles behind it;
+      // theirs are set in the tile of the first key that they see.)
+      for (bool anew = t == 0 || (kKind != kDense && (edge || t == from) &&
+                                  __any_sync(~0u, m == -INFINITY && col < ncols));; anew = true) {
         if (anew) settle<D>(ts, to, meta, cs, t > 0, m, wr, l);
         if (look && __any_sync(~0u, wr - meta.lv_min - m > kFar)) {
           if (!anew) continue;
