@@ -110,20 +110,39 @@ constexpr float kMaxScale = 65536.f;
 // the tiled kernel then).
 constexpr int kTiledFrom = 32;
 constexpr int kSplitCols = 16;
+// Windows and trees run the split kernel, in blocks of 16 columns, for more: where
+// the call's rows x query heads x positions that a row may see stay below
+// kSplitWork, as the tiled kernel's start (terms, parts, joining) takes longer than
+// that work (heads of 128, 4 query heads for each of 8 key/value heads: windows of
+// 1,024, 9 rows 15.5 us against 26.6 tiled, 64: 24.7 and 31.8, 16 x 16: 44.5 and 47.4,
+// work 8.5 M; windows of 4,096, 64 rows: 39.7 and 47.2, work 8.5 M, 128: 62.6 and 46.1,
+// 17 M; heads of 64 alike); and trees of up to kSplitTree columns in all, whose
+// lengths the host does not know (13 rows after 3,001 positions: 21.7 and 27.3, after
+// 32K: 57.6 and 53.0; 104 columns of two sequences of 9,000: 39.2 and 41.2, 208 of four
+// of 3,001: 33.1 and 31.2).
+constexpr long long kSplitWork = 10000000;
+constexpr int kSplitTree = 64;
 struct AttnPlan {
   bool split, tiled;
   int nb, ctas, tiled_ctas;
   size_t slots_off, tiled_off, tiled_slots_off, factor_off, terms_off, bytes;
 };
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, int q_heads, bool selected) {
+AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, int q_heads, bool selected,
+                        const mqa_kv_view *view = nullptr) {
   const int group = q_heads / c->kv_heads;
   if (max_rows <= 0 || max_rows > rows) max_rows = rows;
   const long long cols = selected ? group : (long long)group * max_rows;
   AttnPlan p;
-  p.tiled = !selected && cols > kTiledFrom;
+  bool little = false;
+  if (view && (view->window || view->tree)) {
+    long long sees = (long long)c->max_pages * c->page_size;
+    if (view->window) sees = std::min(sees, (long long)view->window + view->sinks + max_rows);
+    little = (long long)rows * q_heads * sees <= kSplitWork || (view->tree && (long long)rows * group <= kSplitTree);
+  }
+  p.tiled = !selected && cols > kTiledFrom && !little;
   p.split = !p.tiled || c->max_seqs > 1;
-  p.nb = cols <= 8 ? 1 : cols <= 16 || p.tiled ? 2 : cols <= 24 ? 3 : 4;
+  p.nb = cols <= 8 ? 1 : cols <= 16 || p.tiled || little ? 2 : cols <= 24 ? 3 : 4;
   p.ctas = sms * attn_ctas_per_sm(p.nb, c->head_dim);
   // Room for whichever block width needs most: a workspace holds for every
   // max_rows and for selected keys as well.
@@ -194,7 +213,7 @@ int attention(const mqa_kv_cache *cache, const void *q, long long q_row_stride, 
   int sms = 0;
   rc = require_device(&sms);
   if (rc != MQA_OK) return rc;
-  const AttnPlan P = plan_attention(sms, cache, rows, max_rows, q_heads, selected != nullptr);
+  const AttnPlan P = plan_attention(sms, cache, rows, max_rows, q_heads, selected != nullptr, view);
   if (workspace_bytes < P.bytes) return MQA_ERR_WORKSPACE_TOO_SMALL;
   AttnParams p;
   std::memset(&p, 0, sizeof p);

@@ -9,7 +9,9 @@ from test_gpu_kv import check, ints, mqa, rows_of, starts_of  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 
-def attend(mqa, c, rng, rows, group, dtype="bf16", max_rows=None, extra_rows=0, mask=None, **sees):  # noqa: F811
+def attend(mqa, c, rng, rows, group, dtype="bf16", max_rows=None, extra_rows=0, mask=None, only=None,  # noqa: F811
+           **sees):
+    """only: how many rows of each sequence are compared (its first and last among them)."""
     import torch
     st = starts_of(rows)
     m, n = int(st[-1]), int(st[-1]) + extra_rows
@@ -26,8 +28,16 @@ def attend(mqa, c, rng, rows, group, dtype="bf16", max_rows=None, extra_rows=0, 
         seen = view.window_seen(c, st, sees["window"], sees.get("sinks", 0))
     assert mqa.kv_status(dev) == 0
     assert (out[m:] == 7).all() and (lse[m:] == 7).all()  # rows behind the last sequence
-    check(out[:m], lse[:m], c.attention(qd[:m], st, c.dim ** -0.5, dtype, seen, causal=mask is None))
+    pick, part = np.arange(m), st
+    if only is not None:
+        at = [np.unique(np.concatenate([rng.integers(0, n, only), np.arange(n)[:3], np.arange(n)[-3:]])) if n else
+              np.arange(0) for n in rows]
+        pick, part = np.concatenate([a + s for a, s in zip(at, st)]), starts_of([len(a) for a in at])
+    check(out[pick], lse[pick], c.attention(qd[pick], part, c.dim ** -0.5, dtype, seen[pick], causal=False))
     return out, lse, dev, q, st
+
+
+LITTLE = 10 ** 7  # rows x query heads x positions seen: views of more go to the tiled kernel
 
 
 CASES = [  # page, heads, group, dim, lens, rows
@@ -60,56 +70,82 @@ def test_window(mqa, case, window, sinks):  # noqa: F811
     attend(mqa, c, rng, rows, group, dtype, max_rows=1, window=window, sinks=sinks)  # every sequence on the split kernel
 
 
+TILED = [  # page, heads, group, dim, lens, rows
+    (16, 2, 8, 128, [2500, 900], [1400, 900]),
+    (64, 1, 4, 64, [3000], [2900]),
+    (128, 3, 5, 128, [1700, 1000, 130], [1000, 700, 1]),
+    (32, 1, 7, 64, [1200, 2000], [1500, 1000]),   # more rows than positions
+]
+
+
+@pytest.mark.parametrize("window,sinks", WINDOWS + [(700, 3), (900, 400)])
+@pytest.mark.parametrize("case", TILED, ids=str)
+def test_window_in_the_tiled_kernel(mqa, case, window, sinks):  # noqa: F811
+    page, heads, group, dim, lens, rows = case
+    assert sum(rows) * heads * group * max(rows) > LITTLE
+    rng = np.random.default_rng(len(lens) * 100 + group + window % 1000)
+    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 2, heads, page, dim, lens, 200)
+    attend(mqa, c, rng, rows, group, "bf16" if (window + dim) % 3 else "fp16", extra_rows=3, only=20, window=window,
+           sinks=sinks)
+
+
 @pytest.mark.parametrize("window,sinks", [(1000, 4), (4096, 0), (129, 300)])
-@pytest.mark.parametrize("rows", [1, 8, 300])
+@pytest.mark.parametrize("rows", [1, 8, 300, 2400])
 def test_window_far_behind_the_first_positions(mqa, rows, window, sinks):  # noqa: F811
     rng = np.random.default_rng(rows + window)
     c = ref.random_cache(rng, 200, 1, 64, 128, [9001, 2500], 160)
-    attend(mqa, c, rng, [rows, 2 * rows // 3], 4, window=window, sinks=sinks)
+    attend(mqa, c, rng, [rows, 2 * rows // 3], 4, only=40, window=window, sinks=sinks)
 
 
-@pytest.mark.parametrize("rows,max_rows", [([9, 1], 1), ([90, 40], None)])
+@pytest.mark.parametrize("rows,max_rows", [([9, 1], 1), ([1100, 40], None)])
 def test_a_window_as_long_as_the_sequences_is_no_window(mqa, rows, max_rows):  # noqa: F811
     """Bit by bit what the call without one gives."""
     import torch
     rng = np.random.default_rng(5)
-    c = ref.random_cache(rng, 40, 2, 16, 128, [300, 200], 30)
-    out, lse, dev, q, st = attend(mqa, c, rng, rows, 4, window=300, max_rows=max_rows)
+    c = ref.random_cache(rng, 100, 2, 16, 128, [1300, 200], 90)
+    out, lse, dev, q, st = attend(mqa, c, rng, rows, 4, window=1300, max_rows=max_rows, only=20)
     l2 = torch.zeros_like(lse)
     assert torch.equal(out, mqa.kv_attention(q, dev, ints(st), max_rows=max_rows, lse=l2)) and torch.equal(lse, l2)
 
 
 def test_nan_codes_outside_a_window(mqa):  # noqa: F811
     """A NaN key or value counts for the rows whose window holds it, in tiles that other rows see as well."""
-    for rows in ([6, 5], [100, 90]):
+    for rows in ([6, 5], [1100, 1000]):
         for window, sinks in ((20, 0), (20, 3)):
             rng = np.random.default_rng(14)
-            c = ref.random_cache(rng, 30, 2, 16, 128, [170, 140], 12)
-            c.v[c.table[0, 150 // 16], 0, 150 % 16, 3] = 127
-            c.k[c.table[1, 110 // 16], 1, 110 % 16, 100] = 255
-            c.v[c.table[1, 0], 0, 1, 0] = 127
-            out, *_ = attend(mqa, c, rng, rows, 4, window=window, sinks=sinks)
-            assert out.isnan().any() == (rows[0] == 100 or sinks > 0 or rows[1] > 5) or not out.isnan().all()
+            c = ref.random_cache(rng, 150, 2, 16, 128, [1170, 1140], 80)
+            c.v[c.table[0, 1150 // 16], 0, 1150 % 16, 3] = 127
+            c.k[c.table[1, 1120 // 16], 1, 1120 % 16, 100] = 255
+            if sinks:
+                c.v[c.table[1, 0], 0, 1, 0] = 127
+            out, _, _, _, st = attend(mqa, c, rng, rows, 4, window=window, sinks=sinks, only=60)
+            o, a, b = out.isnan().any(2).cpu().numpy(), int(st[1]), int(st[2])
+            sees = np.arange(1170 - rows[0], 1170)
+            assert np.array_equal(o[:a, 0], (sees >= 1150) & (sees < 1170)) and not o[:a, 4:].any()
+            sees = np.arange(1140 - rows[1], 1140)
+            assert np.array_equal(o[a:b, 4], sees >= 1120) and o[a:b, 0].all() == (sinks > 0)
 
 
 def test_a_window_over_bad_tables(mqa):  # noqa: F811
     """Pages that no row's window needs are not looked at; one that is needed and outside the pool is not followed."""
     rng = np.random.default_rng(17)
-    c = ref.random_cache(rng, 30, 2, 16, 64, [300], 30)
-    dev = ref.to_device(c, mqa)
-    dev.page_table[0, 3:9] = 1 << 30
-    for n in (2, 60):
-        q, qd = rows_of(rng, n, 8, 64, "fp16")
-        st = np.array([0, n])
+    for n, heads in ((2, 8), (60, 8), (1200, 8)):
+        length = n + 240
+        c = ref.random_cache(rng, 100, 2, 16, 64, [length], 100)
+        dev = ref.to_device(c, mqa)
+        dev.page_table[0, 3:9] = 1 << 30
+        q, qd = rows_of(rng, n, heads, 64, "fp16")
+        st, pick = np.array([0, n]), np.unique(rng.integers(0, n, 40))
+        part = np.array([0, len(pick)])
         got = mqa.kv_attention(q, dev, ints(st), window=90, sinks=20)
         assert mqa.kv_status(dev) == 0
-        check(got, None, c.attention(qd, st, 0.125, "fp16", view.window_seen(c, st, 90, 20)))
-    dev.page_table[0, 17] = -5
-    seen = view.window_seen(c, st, 90, 20)
-    seen[(seen >= 272) & (seen < 288)] = -1
-    got = mqa.kv_attention(q, dev, ints(st), window=90, sinks=20)
-    assert mqa.kv_status(dev) == 2
-    check(got, None, c.attention(qd, st, 0.125, "fp16", seen))
+        seen = view.window_seen(c, st, 90, 20)
+        check(got[pick], None, c.attention(qd[pick], part, 0.125, "fp16", seen[pick], causal=False))
+        dev.page_table[0, (length - 20) // 16] = -5
+        seen[seen // 16 == (length - 20) // 16] = -1
+        got = mqa.kv_attention(q, dev, ints(st), window=90, sinks=20)
+        assert mqa.kv_status(dev) == 2
+        check(got[pick], None, c.attention(qd[pick], part, 0.125, "fp16", seen[pick], causal=False))
 
 
 TREES = CASES + [(64, 2, 4, 128, [1000, 900], [64, 37]), (16, 1, 1, 64, [400], [333]), (32, 1, 32, 128, [500], [12])]
@@ -125,6 +161,10 @@ def test_tree(mqa, case, dtype):  # noqa: F811
     mask, _ = view.tree_mask(c, starts_of(rows), parents, -(-max(rows) // 32))
     attend(mqa, c, rng, rows, group, dtype, mask=mask, extra_rows=3)
     attend(mqa, c, rng, rows, group, dtype, mask=mask, max_rows=1)
+    # a table long enough for the tiled kernel
+    c.table = np.concatenate([c.table, np.full((len(lens), LITTLE // (sum(rows) * heads * group * page) + 1), -1,
+                                               np.int32)], 1)
+    attend(mqa, c, rng, rows, group, dtype, mask=mask, extra_rows=3, only=30)
 
 
 @pytest.mark.parametrize("max_rows", [1, None])
@@ -132,7 +172,7 @@ def test_tree(mqa, case, dtype):  # noqa: F811
 def test_tree_masks_of_any_kind(mqa, words, max_rows):  # noqa: F811
     """Random bits (later rows and rows behind the sequence's last among them), no bit at all, too few words."""
     rng = np.random.default_rng(words)
-    c = ref.random_cache(rng, 60, 2, 16, 64, [0, 100, 7, 300], 20)
+    c = ref.random_cache(rng, 60, 2, 16, 64, [0, 100, 7, 300], 20 if words == 2 else 2000)
     rows = [3, 70, 7, 40]  # sequence 0 has no positions, sequence 2 none before its rows
     mask = rng.integers(-2 ** 31, 2 ** 31, (120, words)).astype(np.int32)
     mask[5] = 0
@@ -157,7 +197,7 @@ def test_tree_nan_codes(mqa):  # noqa: F811
     """A drafted row with a NaN value counts for the rows that hang on it."""
     rng = np.random.default_rng(10)
     for rows in ([6, 4], [60, 50]):
-        c = ref.random_cache(rng, 40, 2, 16, 128, [200, 150], 13)
+        c = ref.random_cache(rng, 40, 2, 16, 128, [200, 150], 1000)
         p = 200 - rows[0] + 2
         c.v[c.table[0, p // 16], 1, p % 16, 9] = 127
         parents = view.random_parents(rng, rows)
