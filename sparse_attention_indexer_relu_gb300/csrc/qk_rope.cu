@@ -6,9 +6,24 @@
 // wrap is the angle's, so the fraction is exact whatever the position; its upper
 // 32 bits become the argument of sincospi.
 //
-// Split.  A unit is a head of a row, D / 8 lanes with 8 components each.  A CTA has
-// consecutive units, all of whose loads are on their way while the angles of its
-// rows are formed once for all heads into shared memory.
+// With the weights taken in, a pair (a, b) becomes
+//     r (w_a cos a - w_b sin b),  r (w_b cos b + w_a sin a),   r = rsqrt(...):
+// the four factors belong to the row, so they are formed once for all heads that a
+// warp takes of it, and a component costs an unpacking, a square, and a product, a
+// fused product and a product by r, two components to an instruction.
+//
+// Split.  A head is D / 8 lanes with four pairs each (of those that are not turned,
+// any two components make a pair), a step of a warp 32 / (D / 8) heads of a row.  A warp
+// takes a row's heads, q's, then k's, or a share of them where rows are few, with
+// several steps' loads on their way; the angles of the CTA's rows are formed together
+// into shared memory.
+//
+// What bounds it.  HBM: each component is read once and written once.  16,384 rows of
+// 32 and 8 heads of 128 in bf16: 336 MB in 58.5 us, 5.74 TB/s, 85% of the measured copy
+// rate; fp32, 8,192 rows: 5.96 TB/s.  Rows of few heads are bound by what a row costs
+// by itself (its angles and factors: 60,000 rows of 2 and 1 heads of 128, 92 MB, 53 us;
+// several rows to a warp: 59).  A kernel in which every head fetched its cosines from
+// shared memory took 113 us (256 instructions per step of two heads, now 113).
 #include "../../include/mqaqk.h"
 #include "kv_ptx.cuh"
 
@@ -18,74 +33,95 @@ namespace {
 
 using namespace mqa;
 
-constexpr int kThreads = 256;
+// (16,384 rows of 32 and 8 heads of 128: 58.5 us with CTAs of 128 and six of them on an
+// SM, 60.3 with three of 256, 67 with as many registers as the compiler likes; 64.5
+// with two steps ahead and eight CTAs, 81 with one and ten.)
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 
 struct QkParams {
   mqa_qk_heads q, k;
-  int rows, heads, half, interleaved, norm, weight_type, held;  // heads: of q and k; held: rows a CTA may touch
-  unsigned units;
+  int rows, half, norm, weight_type;
+  int steps, q_steps;    // of a row, and those of its query heads
+  int per_warp, shares;  // steps that a warp takes, warps that share a row
   float eps;
   const long long *turns;
   const int32_t *positions;
 };
 
-// 8 elements: 16 bytes, or 32 of fp32.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Four elements: 8 bytes, or 16 of fp32.
 template <int TYPE>
-struct Octet {
-  uint4 w[TYPE == MQA_QK_FP32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void *base, size_t at) {
+struct Four {
+  static constexpr int words = TYPE == MQA_QK_FP32 ? 4 : 2;
+  static constexpr int bytes = 4 * words;
+  uint32_t w[words];
+  __device__ __forceinline__ void load(const char *at) {
     if (TYPE == MQA_QK_FP32) {
-      const uint4 *s = reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(base) + at);
-      w[0] = s[0], w[TYPE == MQA_QK_FP32 ? 1 : 0] = s[1];
+      const uint4 v = *reinterpret_cast<const uint4 *>(at);
+      w[0] = v.x, w[1] = v.y, w[words - 2] = v.z, w[words - 1] = v.w;
     } else {
-      w[0] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + at);
+      const uint2 v = *reinterpret_cast<const uint2 *>(at);
+      w[0] = v.x, w[1] = v.y;
     }
   }
-  __device__ __forceinline__ void values(float (&f)[8]) const {
+  __device__ __forceinline__ void values(float (&f)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       if (TYPE == MQA_QK_FP32) {
-        const uint4 &v = w[TYPE == MQA_QK_FP32 ? i >> 1 : 0];
-        f[2 * i] = __uint_as_float(i & 1 ? v.z : v.x), f[2 * i + 1] = __uint_as_float(i & 1 ? v.w : v.y);
+        f[2 * i] = __uint_as_float(w[(2 * i) % words]), f[2 * i + 1] = __uint_as_float(w[(2 * i + 1) % words]);
       } else {
-        const uint32_t v = i == 0 ? w[0].x : i == 1 ? w[0].y : i == 2 ? w[0].z : w[0].w;
-        const float2 x = TYPE == MQA_QK_BF16 ? bf16x2_to_float2(v) : half2_to_float2(v);
+        const float2 x = TYPE == MQA_QK_BF16 ? bf16x2_to_float2(w[i]) : half2_to_float2(w[i]);
         f[2 * i] = x.x, f[2 * i + 1] = x.y;
       }
     }
   }
-  static __device__ __forceinline__ void store(void *base, size_t at, const float (&f)[8]) {
-    if (TYPE == MQA_QK_FP32) {
-      float4 *d = reinterpret_cast<float4 *>(reinterpret_cast<float *>(base) + at);
-      d[0] = make_float4(f[0], f[1], f[2], f[3]);
-      d[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-      uint32_t v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = TYPE == MQA_QK_BF16 ? float2_to_bf162(f[2 * i], f[2 * i + 1]) : float2_to_half2(f[2 * i], f[2 * i + 1]);
-      *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(base) + at) = make_uint4(v[0], v[1], v[2], v[3]);
-    }
+  static __device__ __forceinline__ void store(char *at, float a, float b, float c, float d) {
+    if (TYPE == MQA_QK_FP32)
+      *reinterpret_cast<float4 *>(at) = make_float4(a, b, c, d);
+    else
+      *reinterpret_cast<uint2 *>(at) = TYPE == MQA_QK_BF16
+                                           ? make_uint2(float2_to_bf162(a, b), float2_to_bf162(c, d))
+                                           : make_uint2(float2_to_half2(a, b), float2_to_half2(c, d));
   }
 };
 
-__device__ __forceinline__ void load_weight(const void *w, int type, int at, float (&f)[8]) {
-  if (!w) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = 1.f;
-  } else if (type == MQA_QK_FP32) {
-    Octet<MQA_QK_FP32> o;
-    o.load(w, at);
-    o.values(f);
-  } else if (type == MQA_QK_FP16) {
-    Octet<MQA_QK_FP16> o;
-    o.load(w, at);
-    o.values(f);
-  } else {
-    Octet<MQA_QK_BF16> o;
-    o.load(w, at);
-    o.values(f);
-  }
+template <int TYPE>
+__device__ __forceinline__ void weights_of(const void *w, int at, float (&f)[4]) {
+  Four<TYPE> o;
+  o.load(reinterpret_cast<const char *>(w) + (size_t)at * (Four<TYPE>::bytes / 4));
+  o.values(f);
+}
+__device__ __forceinline__ void load_weights(const void *w, int type, int at, float (&f)[4]) {
+  if (!w) f[0] = f[1] = f[2] = f[3] = 1.f;
+  else if (type == MQA_QK_FP32) weights_of<MQA_QK_FP32>(w, at, f);
+  else if (type == MQA_QK_FP16) weights_of<MQA_QK_FP16>(w, at, f);
+  else weights_of<MQA_QK_BF16>(w, at, f);
+}
+// From the order of memory (two runs of four) to pairs (a_0 .. a_3), (b_0 .. b_3), and back.
+template <bool NEIGHBOURS>
+__device__ __forceinline__ void to_pairs(const float (&x)[4], const float (&y)[4], uint64_t (&a)[2], uint64_t (&b)[2]) {
+  a[0] = NEIGHBOURS ? pack2(x[0], x[2]) : pack2(x[0], x[1]);
+  a[1] = NEIGHBOURS ? pack2(y[0], y[2]) : pack2(x[2], x[3]);
+  b[0] = NEIGHBOURS ? pack2(x[1], x[3]) : pack2(y[0], y[1]);
+  b[1] = NEIGHBOURS ? pack2(y[1], y[3]) : pack2(y[2], y[3]);
 }
 
 template <int LPH>
@@ -94,144 +130,193 @@ __device__ __forceinline__ float sum_lanes(float v) {
   for (int o = LPH / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
-template <int LPH>
-__device__ __forceinline__ float max_lanes(float v) {
-#pragma unroll
-  for (int o = LPH / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-  return v;
+__device__ __forceinline__ float square_sum(const uint64_t (&f)[2], const uint64_t (&g)[2]) {
+  float a, b;
+  unpack2(fma2(g[1], g[1], fma2(g[0], g[0], fma2(f[1], f[1], mul2(f[0], f[0])))), a, b);
+  return a + b;
+}
+__device__ __forceinline__ float rsqrt_of(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// Squares that leave fp32's range: the head times a power of two first (the whole
-// warp comes here; heads for which `odd` is false keep their factor).
+// Heads whose squares leave fp32's range: the power of two that the components are
+// multiplied with first, and r for those.  (The whole warp comes here; others keep
+// theirs.)
 template <int LPH, int D>
-__device__ __noinline__ float rescued(float amax, float ss, float eps, bool odd, const float (&f)[8]) {
-  amax = max_lanes<LPH>(amax);
-  const int e = max(-100, min(100, exponent_of(amax)));
-  const float down = pow2i(-e);
-  float s = 0.f;
+__device__ __noinline__ float2 rescued(uint64_t f0, uint64_t f1, uint64_t g0, uint64_t g1, float r, float eps, bool odd) {
+  uint64_t f[4] = {f0, f1, g0, g1};
+  float amax = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float x = f[j] * down;
-    s = fmaf(x, x, s);
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack2(f[i], a, b);
+    amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
   }
-  s = sum_lanes<LPH>(s);
-  const float r = rsqrtf(s * (1.f / D) + eps * down * down) * down;
-  return odd && amax > 0.f && amax <= 3.402823466e38f ? r : rsqrtf(ss * (1.f / D) + eps);
+#pragma unroll
+  for (int o = LPH / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+  const bool able = odd && amax > 0.f && amax <= 3.402823466e38f;
+  const float down = able ? pow2i(-max(-100, min(100, exponent_of(amax)))) : 1.f;
+  uint64_t a[2], b[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) a[i] = mul2(f[i], pack2(down, down)), b[i] = mul2(f[2 + i], pack2(down, down));
+  const float s = sum_lanes<LPH>(square_sum(a, b));
+  return make_float2(down, able ? rsqrt_of(s * (1.f / D) + eps * down * down) : r);
 }
 
-// UNITS units per group of lanes.
-template <int D, int TYPE, int UNITS>
-__global__ void __launch_bounds__(kThreads) qk_kernel(const QkParams p) {
-  constexpr int LPH = D / 8, GROUPS = kThreads / LPH;
-  extern __shared__ float4 s_turn[];  // [row][pair of pairs j][lane of the head]: cos, sin, cos, sin
-  const int lane = threadIdx.x % LPH, group = threadIdx.x / LPH;
-  const unsigned first = blockIdx.x * (unsigned)(GROUPS * UNITS);
-  const int row0 = (int)(first / (unsigned)p.heads);
-  Octet<TYPE> x[UNITS];
-  int row[UNITS], head[UNITS];
+template <int D, int TYPE, bool NEIGHBOURS>
+__global__ void __launch_bounds__(kThreads, 6) qk_kernel(const QkParams p) {
+  constexpr int LPH = D / 8, HEADS = 32 / LPH, AHEAD = TYPE == MQA_QK_FP32 ? 2 : 4;
+  constexpr int SIZE = Four<TYPE>::bytes / 4, STEP = HEADS * D * SIZE;  // bytes of an element and from step to step
+  extern __shared__ float4 s_angles[];                                  // [row][pair]: cos, sin
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane % LPH, sub = lane / LPH;
+  const unsigned item0 = blockIdx.x * kWarps, item = item0 + warp, shares = p.shares;
+  const int row0 = (int)(item0 / shares), row = (int)(item / shares);
+  const int begin = (int)(item - row * shares) * p.per_warp;
+  const int end = row < p.rows ? min(begin + p.per_warp, p.steps) : begin;
+  // the lane's two runs of four components
+  const bool turned = part < p.half / 4;
+  const int lo = NEIGHBOURS || !turned ? part * 8 : part * 4, hi = NEIGHBOURS || !turned ? lo + 4 : lo + p.half;
+  const float tiny = p.eps < 0x1p-90f ? 0x1p-90f : 0.f;
+  Four<TYPE> x[AHEAD], y[AHEAD];
+  // steps [s0, s1) of a row's heads of one kind, s1 - s0 of which hold one for the lane's part of the warp
+  struct Run {
+    const char *in;
+    char *out;
+    int steps, mine;
+  };
+  auto run_of = [&](const mqa_qk_heads &h, int s0, int s1) {
+    Run r;
+    const int head = s0 * HEADS + sub;
+    r.in = reinterpret_cast<const char *>(h.in) + ((size_t)row * h.in_stride + (size_t)head * D + lo) * SIZE;
+    r.out = reinterpret_cast<char *>(h.out) + ((size_t)row * h.out_stride + (size_t)head * D + lo) * SIZE;
+    r.steps = max(s1 - s0, 0);
+    r.mine = min(r.steps, (h.heads - head + HEADS - 1) / HEADS);
+    return r;
+  };
+  const int apart = (hi - lo) * SIZE;
+  auto load = [&](const Run &r, int i, int step) {
+    if (step < r.mine) {
+      x[i].load(r.in + (size_t)step * STEP);
+      y[i].load(r.in + (size_t)step * STEP + apart);
+    } else {
 #pragma unroll
-  for (int i = 0; i < UNITS; ++i) {
-    const unsigned u = first + i * GROUPS + group;
-    row[i] = (int)(u / (unsigned)p.heads);
-    head[i] = (int)(u - (unsigned)row[i] * p.heads);
-    const bool is_q = head[i] < p.q.heads;
-    const mqa_qk_heads &h = is_q ? p.q : p.k;
-    if (u < p.units)
-      x[i].load(h.in, (size_t)row[i] * h.in_stride + (size_t)(is_q ? head[i] : head[i] - p.q.heads) * D + lane * 8);
-    else
-      x[i].w[0] = x[i].w[TYPE == MQA_QK_FP32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
-  }
-  // ---- angles of the rows: a lane of a head turns 8 pairs (halves, with the lane
-  // that has the other component) or 4 (neighbours)
-  const int ppl = p.interleaved ? 4 : 8, slots = p.half / ppl;
-  for (int i = threadIdx.x; i < p.held * p.half; i += kThreads) {
+      for (int k = 0; k < Four<TYPE>::words; ++k) x[i].w[k] = y[i].w[k] = 0;
+    }
+  };
+  const Run q = run_of(p.q, min(begin, p.q_steps), min(end, p.q_steps));
+  const Run k = run_of(p.k, max(begin - p.q_steps, 0), end - p.q_steps);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) load(q.steps ? q : k, i, i);
+  const int rows_here = min((int)((item0 + kWarps - 1) / shares), p.rows - 1) - row0 + 1;
+  for (int i = threadIdx.x; i < rows_here * p.half; i += kThreads) {
     const int r = i / p.half, pair = i - r * p.half;
-    if (row0 + r >= p.rows) break;
     const unsigned long long phase =
         (unsigned long long)(long long)__ldg(p.positions + row0 + r) * (unsigned long long)__ldg(p.turns + pair);
     float s, c;
     sincospif((float)(int)(phase >> 32) * 0x1p-31f, &s, &c);
-    float2 *at = reinterpret_cast<float2 *>(s_turn + r * (p.half / 2) + (pair % ppl >> 1) * slots + pair / ppl);
-    at[pair & 1] = make_float2(c, s);
+    reinterpret_cast<float2 *>(s_angles)[i] = make_float2(c, s);
   }
-  float wq[8], wk[8];
-  load_weight(p.q.heads ? p.q.weight : nullptr, p.weight_type, lane * 8, wq);
-  load_weight(p.k.heads ? p.k.weight : nullptr, p.weight_type, lane * 8, wk);
   __syncthreads();
+  auto work = [&](const mqa_qk_heads &h, const Run &r) {
+    uint64_t ca[2], sa[2], cb[2], sb[2];  // a' = r (ca a + sa b), b' = r (cb b + sb a)
+    {
+      float u[4], v[4], c[4], s[4];
+      uint64_t wa[2], wb[2];
+      load_weights(h.weight, p.weight_type, lo, u);
+      load_weights(h.weight, p.weight_type, hi, v);
+      to_pairs<NEIGHBOURS>(u, v, wa, wb);
+      const float4 *t = s_angles + ((row - row0) * p.half + part * 4) / 2;
 #pragma unroll
-  for (int i = 0; i < UNITS; ++i) {
-    const unsigned u = first + i * GROUPS + group;
-    float f[8];
-    x[i].values(f);
-    const bool is_q = head[i] < p.q.heads;
-    if (p.norm) {
-      float ss = 0.f, amax = 0.f;
+      for (int i = 0; i < 2; ++i) {
+        const float4 cs = turned ? t[i] : make_float4(1.f, 0.f, 1.f, 0.f);
+        c[2 * i] = cs.x, s[2 * i] = cs.y, c[2 * i + 1] = cs.z, s[2 * i + 1] = cs.w;
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss), amax = fmaxf(amax, fabsf(f[j]));
-      ss = sum_lanes<LPH>(ss);
-      float rs = rsqrtf(ss * (1.f / D) + p.eps);
-      const bool odd = !(ss <= 3e38f) || (ss < 0x1p-90f && p.eps < 0x1p-90f);
-      if (__any_sync(~0u, odd)) rs = rescued<LPH, D>(amax, ss, p.eps, odd, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = f[j] * rs * (is_q ? wq[j] : wk[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= is_q ? wq[j] : wk[j];
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t c2 = pack2(c[2 * i], c[2 * i + 1]), s2 = pack2(s[2 * i], s[2 * i + 1]);
+        ca[i] = mul2(wa[i], c2), cb[i] = mul2(wb[i], c2);
+        sb[i] = mul2(wa[i], s2), sa[i] = mul2(wb[i], pack2(-s[2 * i], -s[2 * i + 1]));
+      }
     }
-    const float4 *turn = s_turn + (row[i] - row0) * (p.half / 2);
-    if (p.interleaved) {
-      if (lane < slots && u < p.units) {
+    for (int step = 0; step < r.steps; step += AHEAD) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (step + i >= r.steps) break;
+        float u[4], v[4];
+        uint64_t a[2], b[2];
+        x[i].values(u);
+        y[i].values(v);
+        to_pairs<NEIGHBOURS>(u, v, a, b);
+        load(r, i, step + i + AHEAD);
+        float f = 1.f;
+        if (p.norm) {
+          const float ss = sum_lanes<LPH>(square_sum(a, b));
+          f = rsqrt_of(fmaf(ss, 1.f / D, p.eps));
+          const bool odd = !(ss <= 3e38f) || ss < tiny;
+          if (__any_sync(~0u, odd)) {
+            const float2 by = rescued<LPH, D>(a[0], a[1], b[0], b[1], f, p.eps, odd);
+            f = by.y;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) a[j] = mul2(a[j], pack2(by.x, by.x)), b[j] = mul2(b[j], pack2(by.x, by.x));
+          }
+        }
+        float e[4], g[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float4 t = turn[j * slots + lane];
-          const float a = f[4 * j], b = f[4 * j + 1], c = f[4 * j + 2], d = f[4 * j + 3];
-          f[4 * j] = a * t.x - b * t.y, f[4 * j + 1] = b * t.x + a * t.y;
-          f[4 * j + 2] = c * t.z - d * t.w, f[4 * j + 3] = d * t.z + c * t.w;
+          uint64_t aa = mul2(ca[j], a[j]), bb = mul2(cb[j], b[j]);
+          if (turned) aa = fma2(sa[j], b[j], aa), bb = fma2(sb[j], a[j], bb);
+          unpack2(mul2(aa, pack2(f, f)), e[2 * j], e[2 * j + 1]);
+          unpack2(mul2(bb, pack2(f, f)), g[2 * j], g[2 * j + 1]);
         }
-      }
-    } else if (p.half) {
-      const int base = threadIdx.x & 31 & ~(LPH - 1), mine = lane < slots ? lane : lane - slots;
-      const int other = lane < slots ? lane + slots : lane < 2 * slots ? lane - slots : lane;
-      float g[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = __shfl_sync(~0u, f[j], base + other);
-      if (lane < 2 * slots && u < p.units) {
-        const float sign = lane < slots ? -1.f : 1.f;  // (a cos - b sin, b cos + a sin)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 t = turn[j * slots + mine];
-          f[2 * j] = f[2 * j] * t.x + sign * g[2 * j] * t.y;
-          f[2 * j + 1] = f[2 * j + 1] * t.z + sign * g[2 * j + 1] * t.w;
+        if (step + i < r.mine) {
+          char *out = r.out + (size_t)(step + i) * STEP;
+          if (NEIGHBOURS) {
+            Four<TYPE>::store(out, e[0], g[0], e[1], g[1]);
+            Four<TYPE>::store(out + apart, e[2], g[2], e[3], g[3]);
+          } else {
+            Four<TYPE>::store(out, e[0], e[1], e[2], e[3]);
+            Four<TYPE>::store(out + apart, g[0], g[1], g[2], g[3]);
+          }
         }
       }
     }
-    if (u < p.units) {
-      const mqa_qk_heads &h = is_q ? p.q : p.k;
-      Octet<TYPE>::store(h.out, (size_t)row[i] * h.out_stride + (size_t)(is_q ? head[i] : head[i] - p.q.heads) * D +
-                                    lane * 8, f);
+  };
+  if (q.steps) work(p.q, q);
+  if (k.steps) {
+    if (q.steps) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) load(k, i, i);
     }
+    work(p.k, k);
   }
 }
 
 template <int D, int TYPE>
-cudaError_t launch(QkParams &p, int sms, cudaStream_t stream) {
-  constexpr int kGroups = kThreads / (D / 8);
-  auto run = [&](auto *kernel, int units) {
-    const unsigned per = kGroups * units, ctas = (p.units + per - 1) / per;
-    p.held = (int)((per - 1) / p.heads + 2);
-    if (p.held > p.rows) p.held = p.rows;
-    kernel<<<ctas, kThreads, (size_t)p.held * p.half * 8, stream>>>(p);
-    return cudaGetLastError();
-  };
-  const bool few = p.units <= (unsigned)(sms * 4 * kGroups);
-  return few ? run(qk_kernel<D, TYPE, 1>, 1) : run(qk_kernel<D, TYPE, 4>, 4);
+cudaError_t launch(QkParams &p, bool neighbours, int sms, cudaStream_t stream) {
+  constexpr int kHeads = 32 / (D / 8);
+  p.q_steps = (p.q.heads + kHeads - 1) / kHeads;
+  p.steps = p.q_steps + (p.k.heads + kHeads - 1) / kHeads;
+  // a row for each warp, or so many that every SM has 32
+  const long long want = (32LL * sms + p.rows - 1) / p.rows;
+  p.shares = (int)(want < p.steps ? want : p.steps);
+  p.per_warp = (p.steps + p.shares - 1) / p.shares;
+  p.shares = (p.steps + p.per_warp - 1) / p.per_warp;
+  const long long items = (long long)p.rows * p.shares, ctas = (items + kWarps - 1) / kWarps;
+  const size_t smem = (size_t)((kWarps - 1) / p.shares + 2) * p.half * sizeof(float2);
+  if (neighbours)
+    qk_kernel<D, TYPE, true><<<(unsigned)ctas, kThreads, smem, stream>>>(p);
+  else
+    qk_kernel<D, TYPE, false><<<(unsigned)ctas, kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch(QkParams &p, int type, int sms, cudaStream_t stream) {
-  return type == MQA_QK_BF16   ? launch<D, MQA_QK_BF16>(p, sms, stream)
-         : type == MQA_QK_FP16 ? launch<D, MQA_QK_FP16>(p, sms, stream)
-                               : launch<D, MQA_QK_FP32>(p, sms, stream);
+cudaError_t launch(QkParams &p, int type, bool neighbours, int sms, cudaStream_t stream) {
+  return type == MQA_QK_BF16   ? launch<D, MQA_QK_BF16>(p, neighbours, sms, stream)
+         : type == MQA_QK_FP16 ? launch<D, MQA_QK_FP16>(p, neighbours, sms, stream)
+                               : launch<D, MQA_QK_FP32>(p, neighbours, sms, stream);
 }
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -273,19 +358,16 @@ extern "C" int mqa_qk_norm_rope(const mqa_qk_heads *q, const mqa_qk_heads *k, in
   p.q = *q;
   p.k = *k;
   p.rows = rows;
-  p.heads = q->heads + k->heads;
   p.half = rotary / 2;
-  p.interleaved = interleaved != 0;
   p.norm = norm != 0;
   p.weight_type = weight_type;
-  p.units = (unsigned)rows * p.heads;
   p.eps = eps;
   p.turns = reinterpret_cast<const long long *>(turns);
   p.positions = positions;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = head_dim == 64    ? launch<64>(p, type, sms, s)
-                        : head_dim == 128 ? launch<128>(p, type, sms, s)
-                                          : launch<256>(p, type, sms, s);
+  const cudaError_t e = head_dim == 64    ? launch<64>(p, type, interleaved != 0, sms, s)
+                        : head_dim == 128 ? launch<128>(p, type, interleaved != 0, sms, s)
+                                          : launch<256>(p, type, interleaved != 0, sms, s);
   if (e == cudaSuccess) return MQA_OK;
   cudaGetLastError();
   return MQA_ERR_CUDA;
