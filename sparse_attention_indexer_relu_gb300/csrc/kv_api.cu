@@ -347,7 +347,8 @@ int mqa_kv_tree_mask(const mqa_kv_cache *cache, const int32_t *parents, const in
   int sms = 0;
   rc = require_device(&sms);
   if (rc != MQA_OK) return rc;
-  return code(launch_kv_tree_mask(view_of(cache), parents, row_starts, rows, mask, words, positions, as_stream(stream)));
+  return code(launch_kv_tree_mask(view_of(cache), parents, row_starts, rows, mask, words, positions, sms,
+                                  as_stream(stream)));
 }
 
 int mqa_kv_accept(const mqa_kv_cache *cache, const int32_t *row_starts, int rows, const int32_t *counts,

@@ -110,7 +110,7 @@ cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long
                              const int32_t *starts, int rows, int sms, cudaStream_t stream);
 
 cudaError_t launch_kv_tree_mask(const KvView &c, const int32_t *parents, const int32_t *starts, int rows, int32_t *mask,
-                                int words, int32_t *positions, cudaStream_t stream);
+                                int words, int32_t *positions, int sms, cudaStream_t stream);
 // accepted may be null: the first counts[s] rows stay.
 cudaError_t launch_kv_accept(const KvView &c, const int32_t *starts, const int32_t *counts, const int32_t *accepted,
                              int rows, int sms, cudaStream_t stream);

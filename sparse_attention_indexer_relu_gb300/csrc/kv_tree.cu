@@ -30,37 +30,42 @@ constexpr int kMaskHeld = 1024;  // parents of a sequence kept in shared memory
 __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const KvView c, const int32_t *__restrict__ parents,
                                                                  const int32_t *__restrict__ starts, int rows,
                                                                  int32_t *__restrict__ mask, int words,
-                                                                 int32_t *__restrict__ positions) {
+                                                                 int32_t *__restrict__ positions, int per) {
   __shared__ int s_parent[kMaskHeld];
-  const int s = blockIdx.x;
-  const Rows r = rows_of(starts, s, rows);
-  if (r.n == 0) return;
-  const int first = min(max(__ldg(c.lens + s), 0), c.max_pages << c.page_log2) - r.n;
-  // a parent that is no earlier row counts as none
-  auto checked = [&](int i) {
-    const int up = __ldg(parents + r.r0 + i);
-    if (up >= -1 && up < i) return up;
-    atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
-    return -1;
-  };
-  for (int i = threadIdx.x; i < min(r.n, kMaskHeld); i += kMaskThreads) s_parent[i] = checked(i);
-  __syncthreads();
-  for (int i = threadIdx.x; i < r.n; i += kMaskThreads) {
-    int32_t *row = mask + (size_t)(r.r0 + i) * words;
-    int w = i >> 5, depth = 0;
-    for (int k = words - 1; k > w; --k) row[k] = 0;
-    uint32_t bits = 1u << (i & 31);
-    for (int at = i;;) {
-      at = at < kMaskHeld ? s_parent[at] : checked(at);
-      if (at < 0) break;
-      ++depth;
-      for (; w > at >> 5; bits = 0, --w)
+  const int lane = threadIdx.x & 31, s0 = blockIdx.x * per;
+  bool on = false;
+  if (lane < per && s0 + lane < c.seqs) on = rows_of(starts, s0 + lane, rows).n > 0;
+  for (uint32_t left = __ballot_sync(~0u, on); left; left &= left - 1) {
+    const int s = s0 + __ffs(left) - 1;
+    const Rows r = rows_of(starts, s, rows);
+    const int first = min(max(__ldg(c.lens + s), 0), c.max_pages << c.page_log2) - r.n;
+    // a parent that is no earlier row counts as none
+    auto checked = [&](int i) {
+      const int up = __ldg(parents + r.r0 + i);
+      if (up >= -1 && up < i) return up;
+      atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
+      return -1;
+    };
+    for (int i = threadIdx.x; i < min(r.n, kMaskHeld); i += kMaskThreads) s_parent[i] = checked(i);
+    __syncthreads();
+    for (int i = threadIdx.x; i < r.n; i += kMaskThreads) {
+      int32_t *row = mask + (size_t)(r.r0 + i) * words;
+      int w = i >> 5, depth = 0;
+      for (int k = words - 1; k > w; --k) row[k] = 0;
+      uint32_t bits = 1u << (i & 31);
+      for (int at = i;;) {
+        at = at < kMaskHeld ? s_parent[at] : checked(at);
+        if (at < 0) break;
+        ++depth;
+        for (; w > at >> 5; bits = 0, --w)
+          if (w < words) row[w] = (int32_t)bits;
+        bits |= 1u << (at & 31);
+      }
+      for (; w >= 0; bits = 0, --w)
         if (w < words) row[w] = (int32_t)bits;
-      bits |= 1u << (at & 31);
+      if (positions) positions[r.r0 + i] = first + depth;
     }
-    for (; w >= 0; bits = 0, --w)
-      if (w < words) row[w] = (int32_t)bits;
-    if (positions) positions[r.r0 + i] = first + depth;
+    __syncthreads();  // the parents have been read
   }
 }
 
@@ -107,166 +112,181 @@ __device__ __forceinline__ int needed_exp(uint32_t code, int e) {
   const uint32_t b = __float_as_uint(from_e4m3(code));
   return code ? e + (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0) : 0;
 }
-// Four codes times f.
+// Codes times f.
 __device__ __forceinline__ uint32_t scaled(uint32_t w, float f) {
-  return to_e4m3x4(from_e4m3(w & 255u) * f, from_e4m3(w >> 8 & 255u) * f, from_e4m3(w >> 16 & 255u) * f,
-                   from_e4m3(w >> 24) * f);
+  const float2 a = half2_to_float2(cvt2(w)), b = half2_to_float2(cvt2_hi(w));
+  return to_e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
+}
+__device__ __forceinline__ uint4 scaled(uint4 v, float f) {
+  return make_uint4(scaled(v.x, f), scaled(v.y, f), scaled(v.z, f), scaled(v.w, f));
 }
 // 2^d, of as much of d as matters for a product with a code.
 __device__ __forceinline__ float step_by(int d) { return pow2i(min(max(d, -60), 60)); }
 
-// Moves the kept rows behind each other: a CTA has a head's keys or values of a few
-// sequences, and goes over the pages that rows move into, in order.  A page's rows
-// come from its own places or later ones, so that a page is read (into registers)
-// before anything of it is overwritten, and what later pages need lies in pages
-// that have not been written yet.
-constexpr int kMoveThreads = 128;
+// A CTA has a sequence (of a few, those that have rows): it looks up where its kept
+// rows come from and go to, a warp moves a head's keys or values, and then the length
+// and the pages behind it follow.
+//
+// A warp goes over the pages that rows move into, in order.  A page's scale depends on
+// all that moves into it, so its rows are read for their largest magnitude first; few
+// enough stay in registers, others are read again.  In both cases a row is read
+// before its source is overwritten: rows come from their own places or later ones, in
+// order, so that what is written at any time lies before all sources still to be read,
+// and the scales of pages behind this one have not changed yet.
+constexpr int kAcceptWarps = 16;
+constexpr int kMoved = 1024;  // rows looked up at once
+
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) accept_move_kernel(const KvView c, const int32_t *__restrict__ starts,
+__global__ void __launch_bounds__(32 * kAcceptWarps) accept_kernel(const KvView c, const int32_t *__restrict__ starts,
                                                                    const int32_t *__restrict__ counts,
                                                                    const int32_t *__restrict__ accepted, int rows,
                                                                    int per) {
-  constexpr int LPR = D / 16, RPS = kMoveThreads / LPR, STEPS = 128 / RPS;  // lanes per row, rows per step, steps
-  __shared__ int s_need[kMoveThreads / 32];
-  grid_dependents();
-  const int tid = threadIdx.x, head = blockIdx.y;
-  uint8_t *codes = blockIdx.z ? c.v : c.k, *exps = blockIdx.z ? c.v_exps : c.k_exps;
-  for (int s = blockIdx.x * per; s < min(c.seqs, (int)(blockIdx.x + 1) * per); ++s) {
-    const Asked a = asked_of(c, starts, counts, s, rows, nullptr);
-    if (a.keep <= 0) continue;
-    const int32_t *list = accepted + a.r0, *table = c.table + (size_t)s * c.max_pages;
-    bool ok = true;
-    int stay = 0;  // rows that are where they belong: the first ones
-    for (int i = tid; i < a.keep; i += kMoveThreads) {
-      ok &= entry_ok(list, i, a.n);
-      stay += __ldg(list + i) == i;
-    }
-    if (__syncthreads_or(!ok)) continue;
-    stay = __reduce_add_sync(~0u, stay);
-    if ((tid & 31) == 0) s_need[tid >> 5] = stay;
-    __syncthreads();
-    stay = 0;
-#pragma unroll
-    for (int w = 0; w < kMoveThreads / 32; ++w) stay += s_need[w];
-    for (int i = stay; i < a.keep;) {
-      const int to = a.first + i, slot = to & (c.page - 1), m = min(c.page - slot, a.keep - i);
-      const int to_page = __ldg(table + (to >> c.page_log2));
-      bool in = (unsigned)to_page < (unsigned)c.pages;
-      uint4 x[STEPS];
-      int e[STEPS];
-      int need = 0;
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        const int row = j * RPS + tid / LPR;
-        x[j] = make_uint4(0, 0, 0, 0);
-        e[j] = 0;
-        if (row < m) {
-          const int from = a.first + __ldg(list + i + row), page = __ldg(table + (from >> c.page_log2));
-          if ((unsigned)page < (unsigned)c.pages) {
+  constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = 4, HELD = RPS * STEPS;  // lanes per row, rows per step, rows held
+  __shared__ int s_src[kMoved], s_dst[kMoved / 16 + 1];  // source rows (page * page size + slot, or -1), pages
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads / 32;
+  const int s0 = blockIdx.x * per;
+  bool on = false;
+  if (lane < per && s0 + lane < c.seqs) on = rows_of(starts, s0 + lane, rows).n > 0;
+  for (uint32_t left = __ballot_sync(~0u, on); left; left &= left - 1) {
+    const int s = s0 + __ffs(left) - 1;
+    const Asked a = asked_of(c, starts, counts, s, rows, tid == 0 ? c.status : nullptr);
+    if (a.keep < 0) continue;
+    const int32_t *list = accepted + a.r0;
+    int32_t *table = c.table + (size_t)s * c.max_pages;
+    if (accepted) {
+      bool bad = false;
+      int stay = 0;  // rows that are where they belong: the first ones
+      for (int i0 = 0; i0 < a.keep; i0 += threads) {
+        const int i = i0 + tid;
+        if (i < a.keep) bad |= !entry_ok(list, i, a.n);
+        stay += __syncthreads_count(i < a.keep && __ldg(list + i) == i);
+      }
+      if (__syncthreads_or(bad)) {
+        if (tid == 0) atomicOr(c.status, MQA_KV_DEV_BAD_LIST);
+        continue;
+      }
+      // rows looked up at once end with a page's last one
+      for (int from = stay, to; from < a.keep; from = to) {
+        const int begin = a.first + from;
+        to = min(a.keep, ((begin + kMoved) & ~(c.page - 1)) - a.first);
+        __syncthreads();  // the last ones' readers are done
+        for (int i = tid; i < to - from; i += threads) {
+          const int pos = a.first + __ldg(list + from + i), page = table[pos >> c.page_log2];
+          s_src[i] = (unsigned)page < (unsigned)c.pages ? (page << c.page_log2) + (pos & (c.page - 1)) : -1;
+        }
+        const int pages = ((a.first + to - 1) >> c.page_log2) - (begin >> c.page_log2) + 1;
+        for (int i = tid; i < pages; i += threads) s_dst[i] = table[(begin >> c.page_log2) + i];
+        __syncthreads();
+        for (int item = warp; item < 2 * c.heads; item += warps) {
+          const int head = item >> 1;
+          uint8_t *codes = item & 1 ? c.v : c.k, *exps = item & 1 ? c.v_exps : c.k_exps;
+          for (int i = from, n = 0; i < to; ++n) {
+            const int slot = (a.first + i) & (c.page - 1), m = min(c.page - slot, to - i), page = s_dst[n];
+            const int *src = s_src + (i - from);
+            i += m;
+            bool in = (unsigned)page < (unsigned)c.pages;
+            for (int r = lane; r < m; r += 32) in &= src[r] >= 0;
+            if (!__all_sync(~0u, in)) {  // a page outside the pool: nothing moves into this one
+              if (lane == 0) atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
+              continue;
+            }
             const size_t ph = (size_t)page * c.heads + head;
-            e[j] = exps[ph];
-            x[j] = *reinterpret_cast<const uint4 *>(codes + ((ph << c.page_log2) + (from & (c.page - 1))) * D +
-                                                    tid % LPR * 16);
-            uint32_t top = top_code(top_code(top_code(top_code(0, x[j].x), x[j].y), x[j].z), x[j].w);
-            top = __vmaxu4(top, top >> 16);
-            top = __vmaxu4(top, top >> 8) & 255u;
-            need = max(need, needed_exp(top, e[j]));
-          } else {
-            in = false;
+            const int was = exps[ph];
+            uint4 x[STEPS];
+            int e[STEPS];
+            auto load = [&](int r0) {
+#pragma unroll
+              for (int j = 0; j < STEPS; ++j) {
+                const int r = r0 + j * RPS + lane / LPR;
+                x[j] = make_uint4(0, 0, 0, 0), e[j] = 0;
+                if (r < m) {
+                  const int at = src[r];
+                  const size_t row = ((size_t)(at >> c.page_log2) * c.heads + head);
+                  e[j] = at >> c.page_log2 == page ? was : exps[row];
+                  x[j] = *reinterpret_cast<const uint4 *>(codes + ((row << c.page_log2) + (at & (c.page - 1))) * D +
+                                                          lane % LPR * 16);
+                }
+              }
+            };
+            int need = 0;
+            for (int r0 = 0; r0 < m; r0 += HELD) {
+              load(r0);
+#pragma unroll
+              for (int j = 0; j < STEPS; ++j) {
+                if (r0 + j * RPS >= m) break;
+                uint32_t top = top_code(top_code(top_code(top_code(0, x[j].x), x[j].y), x[j].z), x[j].w);
+                top = __vmaxu4(top, top >> 16);
+                top = __vmaxu4(top, top >> 8) & 255u;
+                need = max(need, needed_exp(top, e[j]));
+              }
+            }
+            need = min(max(__reduce_max_sync(~0u, need), 7), 247);
+            const int now = slot ? max(need, was) : need;
+            uint8_t *tile = codes + (ph << c.page_log2) * D;
+            if (slot && now > was) {  // earlier positions under the larger scale
+              const float f = pow2i(max(was - now, -126));
+              for (int j = lane; j < slot * D / 16; j += 32) {
+                uint4 *w = reinterpret_cast<uint4 *>(tile) + j;
+                *w = scaled(*w, f);
+              }
+            }
+            for (int r0 = 0; r0 < m; r0 += HELD) {
+              if (m > HELD) load(r0);
+              __syncwarp();  // read, before any lane writes
+#pragma unroll
+              for (int j = 0; j < STEPS; ++j) {
+                const int r = r0 + j * RPS + lane / LPR;
+                if (r < m) {
+                  if (e[j] != now) x[j] = scaled(x[j], step_by(e[j] - now));
+                  *reinterpret_cast<uint4 *>(tile + (size_t)(slot + r) * D + lane % LPR * 16) = x[j];
+                }
+              }
+              __syncwarp();
+            }
+            if (lane == 0) exps[ph] = (uint8_t)now;
           }
         }
       }
-      need = __reduce_max_sync(~0u, need);
-      __syncthreads();  // what s_need held has been read
-      if ((tid & 31) == 0) s_need[tid >> 5] = need;
-      const size_t ph = (size_t)max(to_page, 0) * c.heads + head;
-      const int was = slot && (unsigned)to_page < (unsigned)c.pages ? exps[ph] : 0;
-      if (__syncthreads_or(!in)) {  // a page outside the pool: nothing moves into this one
-        if (tid == 0) atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
-        i += m;
-        continue;
-      }
-#pragma unroll
-      for (int w = 0; w < kMoveThreads / 32; ++w) need = max(need, s_need[w]);
-      const int now = max(min(max(need, 7), 247), was);
-      uint8_t *tile = codes + (ph << c.page_log2) * D;
-      if (slot && now > was) {  // earlier positions under the larger scale
-        const float f = pow2i(max(was - now, -126));
-        for (int j = tid; j < slot * D / 4; j += kMoveThreads) {
-          uint32_t *w = reinterpret_cast<uint32_t *>(tile) + j;
-          *w = scaled(*w, f);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        const int row = j * RPS + tid / LPR;
-        if (row < m) {
-          const float f = step_by(e[j] - now);
-          *reinterpret_cast<uint4 *>(tile + (size_t)(slot + row) * D + tid % LPR * 16) =
-              make_uint4(scaled(x[j].x, f), scaled(x[j].y, f), scaled(x[j].z, f), scaled(x[j].w, f));
-        }
-      }
-      if (tid == 0) exps[ph] = (uint8_t)now;
-      i += m;
+      __syncthreads();  // the table has been read
     }
-  }
-  grid_wait();
-}
-
-// Lengths and pages: a warp per sequence.
-__global__ void __launch_bounds__(256) accept_trim_kernel(const KvView c, const int32_t *__restrict__ starts,
-                                                          const int32_t *__restrict__ counts,
-                                                          const int32_t *__restrict__ accepted, int rows) {
-  grid_wait();
-  const int s = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (s >= c.seqs) return;
-  const Asked a = asked_of(c, starts, counts, s, rows, lane == 0 ? c.status : nullptr);
-  if (a.keep < 0) return;
-  bool ok = true;
-  if (accepted)
-    for (int i = lane; i < a.keep; i += 32) ok &= entry_ok(accepted + a.r0, i, a.n);
-  if (!__all_sync(~0u, ok)) {
-    if (lane == 0) atomicOr(c.status, MQA_KV_DEV_BAD_LIST);
-    return;
-  }
-  const int now = a.first + a.keep, held = (now + c.page - 1) >> c.page_log2;
-  int32_t *table = c.table + (size_t)s * c.max_pages;
-  for (int j = held + lane; j < (a.first + a.n + c.page - 1) >> c.page_log2; j += 32) {
-    const int page = table[j];
-    table[j] = -1;
-    if ((unsigned)page >= (unsigned)c.pages) {
-      atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
-    } else if (atomicSub(c.refs + page, 1) <= 0) {  // not in use: the count stays
-      atomicAdd(c.refs + page, 1);
-      atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
+    const int now = a.first + a.keep, held = (now + c.page - 1) >> c.page_log2;
+    for (int j = held + tid; j < (a.first + a.n + c.page - 1) >> c.page_log2; j += threads) {
+      const int page = table[j];
+      table[j] = -1;
+      if ((unsigned)page >= (unsigned)c.pages) {
+        atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
+      } else if (atomicSub(c.refs + page, 1) <= 0) {  // not in use: the count stays
+        atomicAdd(c.refs + page, 1);
+        atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
+      }
     }
+    if (tid == 0) c.lens[s] = now;
   }
-  if (lane == 0) c.lens[s] = now;
 }
 
 }  // namespace
 
+// Sequences that a CTA looks through: one, or up to 32 of a large table, most of which
+// have no rows.
+static int sequences_per_cta(const KvView &c, int sms) { return std::min(std::max(c.seqs / (sms * 16), 1), 32); }
+
 cudaError_t launch_kv_tree_mask(const KvView &c, const int32_t *parents, const int32_t *starts, int rows, int32_t *mask,
-                                int words, int32_t *positions, cudaStream_t stream) {
-  tree_mask_kernel<<<c.seqs, kMaskThreads, 0, stream>>>(c, parents, starts, rows, mask, words, positions);
+                                int words, int32_t *positions, int sms, cudaStream_t stream) {
+  const int per = sequences_per_cta(c, sms);
+  tree_mask_kernel<<<(c.seqs + per - 1) / per, kMaskThreads, 0, stream>>>(c, parents, starts, rows, mask, words, positions,
+                                                                         per);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_accept(const KvView &c, const int32_t *starts, const int32_t *counts, const int32_t *accepted,
                              int rows, int sms, cudaStream_t stream) {
-  if (accepted) {
-    const long long ctas = (long long)c.seqs * c.heads * 2;
-    const int per = (int)std::min(std::max(ctas / (sms * 8LL), 1LL), 32LL);
-    const dim3 grid((c.seqs + per - 1) / per, c.heads, 2);
-    const cudaError_t e =
-        c.dim == 64 ? launch_after(accept_move_kernel<64>, grid, kMoveThreads, 0, stream, false, c, starts, counts,
-                                   accepted, rows, per)
-                    : launch_after(accept_move_kernel<128>, grid, kMoveThreads, 0, stream, false, c, starts, counts,
-                                   accepted, rows, per);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_after(accept_trim_kernel, dim3((c.seqs + 7) / 8), 256, 0, stream, accepted != nullptr, c, starts, counts,
-                      accepted, rows);
+  const int warps = accepted ? std::min(2 * c.heads, kAcceptWarps) : 1, per = sequences_per_cta(c, sms);
+  const int ctas = (c.seqs + per - 1) / per;
+  if (c.dim == 64)
+    accept_kernel<64><<<ctas, 32 * warps, 0, stream>>>(c, starts, counts, accepted, rows, per);
+  else
+    accept_kernel<128><<<ctas, 32 * warps, 0, stream>>>(c, starts, counts, accepted, rows, per);
+  return cudaGetLastError();
 }
 
 }  // namespace mqa

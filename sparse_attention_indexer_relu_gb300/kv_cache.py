@@ -374,7 +374,7 @@ def kv_tree_mask(cache: KVCache, parents, row_starts, max_rows: int, mask=None, 
     parents [rows] int32: the row that each row hangs on, as its number among its sequence's rows (an earlier one), or -1
     for the position before them.  max_rows: the most rows of one sequence.  Returns (mask [rows, ceil(max_rows / 32)]
     int32, positions [rows] int32); a row's position is where it will be if it is accepted.  Rows of no sequence are left
-    as they were (zeros in tensors made here)."""
+    as they were."""
     import torch
     m = _api()
     p = _list(parents, cache, "parents")
@@ -389,9 +389,9 @@ def kv_tree_mask(cache: KVCache, parents, row_starts, max_rows: int, mask=None, 
         _list(positions, cache, "positions", rows)
     with _on(cache, stream) as s:
         if mask is None:
-            mask = torch.zeros((rows, words), dtype=torch.int32, device=cache.device)
+            mask = torch.empty((rows, words), dtype=torch.int32, device=cache.device)
         if positions is None:
-            positions = torch.zeros(rows, dtype=torch.int32, device=cache.device)
+            positions = torch.empty(rows, dtype=torch.int32, device=cache.device)
         m._check(m.lib().mqa_kv_tree_mask(cache._ref, p, rs, rows, mask.data_ptr(), words, positions.data_ptr(), s),
                  "mqa_kv_tree_mask")
     return mask, positions
