@@ -37,10 +37,15 @@ def _api():
 class _Place:
     """Where a call runs, as the cache's calls know it."""
 
-    __slots__ = ("device", "_index")
+    __slots__ = ("_index",)
 
-    def __init__(self, device):
-        self.device, self._index = device, device.index
+    def __init__(self, index):
+        self._index = index
+
+    @property
+    def device(self):
+        import torch
+        return torch.device("cuda", self._index)
 
 
 def rope_turns(inv_freq, device=None):
@@ -59,34 +64,50 @@ def rope_turns(inv_freq, device=None):
     return torch.tensor(turns, dtype=torch.int64, device=dev)
 
 
-def _heads(t, out, weight, dim, dtype, weight_type, device, name):
-    """The struct of q or k; its tensors checked."""
-    import torch
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name} requires a gradient, which qk_norm_rope does not have: detach it, or call it under "
-                         "torch.no_grad()")
-    for x, what in ((t, name), (out, name + "_out")):
-        if x.dtype != dtype:
-            raise TypeError(f"{what} must be {dtype}, got {x.dtype}")
-        if x.shape != t.shape or x.dim() != 3 or x.shape[2] != dim:
-            raise ValueError(f"{what} has shape {tuple(x.shape)}, expected (rows, heads, {dim})")
-        if x.device != device or not x.is_cuda or (x.numel() and (x.stride(2) != 1 or
-                                                                  (x.shape[1] > 1 and x.stride(1) != dim))):
-            raise ValueError(f"{what} must be on {device} with its heads contiguous in a row")
+def _check(t, dtype, shape, where, name):
+    """A tensor [rows, heads, dim] on device `where` whose heads lie side by side in a row; its row stride."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    rows, heads, dim = shape
+    across, beside, within = t.stride()
+    if t.get_device() != where or (rows and heads and (within != 1 or (heads > 1 and beside != dim))):
+        raise ValueError(f"{name} must be on cuda:{where} with its heads contiguous in a row")
+    return across if rows > 1 else heads * dim
+
+
+def _heads(t, out, weight, dtype, weight_type, where, name):
+    """The struct of q or k; its tensors checked (out is None: made by the caller)."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected (rows, heads, dim)")
+    if t.requires_grad or (weight is not None and weight.requires_grad):
+        if _api()._torch().is_grad_enabled():
+            raise ValueError(f"{name if t.requires_grad else name + '_weight'} requires a gradient, which qk_norm_rope does "
+                             "not have: detach it, or call it under torch.no_grad()")
+    heads, dim = shape[1], shape[2]
+    stride = _check(t, dtype, shape, where, name)
+    op, os = None, heads * dim
+    if out is not None:
+        os = _check(out, dtype, shape, where, name + "_out")
+        op = out.data_ptr()
     wp = None
     if weight is not None:
-        if weight.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{name}_weight requires a gradient, which qk_norm_rope does not have: detach it, or call it "
-                             "under torch.no_grad()")
         if weight.dtype != weight_type:
             raise TypeError(f"{name}_weight must be {weight_type}, got {weight.dtype}")
-        if tuple(weight.shape) != (dim,) or weight.device != device or not weight.is_contiguous():
-            raise ValueError(f"{name}_weight must be a contiguous tensor ({dim},) on {device}")
+        if weight.shape != (dim,) or weight.get_device() != where or not weight.is_contiguous():
+            raise ValueError(f"{name}_weight must be a contiguous tensor ({dim},) on cuda:{where}")
         wp = weight.data_ptr()
-    width = int(t.shape[1]) * dim
-    many = t.shape[0] > 1
-    return _Heads(t.data_ptr(), out.data_ptr(), wp, t.stride(0) if many else width, out.stride(0) if many else width,
-                  int(t.shape[1]))
+    return _Heads(t.data_ptr(), op, wp, stride, os, heads)
+
+
+def _list(t, dtype, n, where, name):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (n,) or t.get_device() != where or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor ({n},) on cuda:{where}")
+    return t.data_ptr()
 
 
 def qk_norm_rope(q, k, turns, positions, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
@@ -104,39 +125,35 @@ def qk_norm_rope(q, k, turns, positions, q_weight=None, k_weight=None, eps: floa
     Computed in 32 bits (positions times frequencies in 64), rounded once."""
     import torch
     m, types = _api(), _types()
-    if q.dtype not in types:
-        raise TypeError(f"q must be bfloat16, float16 or float32, got {q.dtype}")
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] not in QK_HEAD_DIMS:
+    dtype, where = q.dtype, q.get_device()
+    if dtype not in types:
+        raise TypeError(f"q must be bfloat16, float16 or float32, got {dtype}")
+    if where < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2] or \
+            q.shape[2] not in QK_HEAD_DIMS:
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)}: (rows, heads, {QK_HEAD_DIMS}) are expected")
-    rows, dim, dev = int(q.shape[0]), int(q.shape[2]), q.device
-    w = q_weight if q_weight is not None else k_weight
-    wt = q.dtype if w is None else w.dtype
-    if wt not in types:
-        raise TypeError(f"weights must be bfloat16, float16 or float32, got {wt}")
-    rotary = 0
+    weight = k_weight if q_weight is None else q_weight
+    weight_type = dtype if weight is None else weight.dtype
+    if weight_type not in types:
+        raise TypeError(f"weights must be bfloat16, float16 or float32, got {weight_type}")
+    rows, rotary, tp, pp = q.shape[0], 0, None, None
     if (turns is None) != (positions is None):
         raise ValueError("turns and positions go together")
     if turns is not None:
-        rotary = 2 * int(turns.shape[0])
-        for t, dt, shape, name in ((turns, torch.int64, (rotary // 2,), "turns"),
-                                   (positions, torch.int32, (rows,), "positions")):
-            if t.dtype != dt:
-                raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-            if tuple(t.shape) != shape or t.device != dev or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous tensor {shape} on {dev}")
-    if not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
-    hq = _heads(q, q if q_out is None else q_out, q_weight, dim, q.dtype, wt, dev, "q")
-    hk = _heads(k, k if k_out is None else k_out, k_weight, dim, q.dtype, wt, dev, "k")
-    with _on(_Place(dev), stream) as s:
+        rotary = 2 * turns.shape[0]
+        tp = _list(turns, torch.int64, rotary // 2, where, "turns")
+        pp = _list(positions, torch.int32, rows, where, "positions")
+    hq = _heads(q, q_out, q_weight, dtype, weight_type, where, "q")
+    hk = _heads(k, k_out, k_weight, dtype, weight_type, where, "k")
+    with _on(_Place(where), stream) as s:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            hq.out, hq.out_stride = q_out.data_ptr(), hq.heads * dim
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            hq.out = q_out.data_ptr()
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
-            hk.out, hk.out_stride = k_out.data_ptr(), hk.heads * dim
-        m._check(m.lib().mqa_qk_norm_rope(ctypes.byref(hq), ctypes.byref(hk), rows, types[q.dtype], types[wt], dim, rotary,
-                                          int(bool(interleaved)), int(bool(norm)), float(eps),
-                                          turns.data_ptr() if rotary else None, positions.data_ptr() if rotary else None,
-                                          s), "mqa_qk_norm_rope")
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            hk.out = k_out.data_ptr()
+        m._check(m.lib().mqa_qk_norm_rope(hq, hk, rows, types[dtype], types[weight_type], q.shape[2], rotary,
+                                          int(bool(interleaved)), int(bool(norm)), eps, tp if rotary else None,
+                                          pp if rotary else None, s), "mqa_qk_norm_rope")
     return q_out, k_out

@@ -146,20 +146,28 @@ def test_binding_refuses_bad_lists():
             mqa.kv_accept(*args, **kw)
 
 
+class Rows(OnDevice):
+    def get_device(self):
+        return 0
+
+    def stride(self, i=None):
+        return [self.shape[j + 1:].numel() for j in range(len(self.shape))] if i is None else super().stride(i)
+
+
 def test_binding_refuses_bad_heads():
     bf, f32 = torch.bfloat16, torch.float32
-    on = lambda *s, dtype=bf: OnDevice(*s, dtype=dtype)  # noqa: E731
-    turns, pos = OnDevice(64, dtype=torch.int64), OnDevice(5, dtype=torch.int32)
+    on = lambda *s, dtype=bf: Rows(*s, dtype=dtype)  # noqa: E731
+    turns, pos = Rows(64, dtype=torch.int64), Rows(5, dtype=torch.int32)
     q, k = on(5, 4, 128), on(5, 2, 128)
     f = lambda q=q, k=k, t=turns, p=pos, **kw: mqa.qk_norm_rope(q, k, t, p, **kw)  # noqa: E731
     out = dict(q_out=on(5, 4, 128), k_out=on(5, 2, 128))
     for bad in (dict(q=on(5, 4, 96), k=on(5, 2, 96)), dict(k=on(4, 2, 128)), dict(k=on(5, 2, 64)), dict(t=None),
-                dict(p=None), dict(p=OnDevice(4, dtype=torch.int32)), dict(q_weight=on(64)),
+                dict(p=None), dict(p=Rows(4, dtype=torch.int32)), dict(q_weight=on(64)),
                 dict(q_out=on(5, 3, 128), k_out=on(5, 2, 128))):
         with pytest.raises(ValueError):
             f(**{**out, **bad})
     for bad in (dict(q=on(5, 4, 128, dtype=torch.int32)), dict(k=on(5, 2, 128, dtype=f32)),
-                dict(t=OnDevice(64, dtype=f32)), dict(p=OnDevice(5, dtype=torch.int64)),
+                dict(t=Rows(64, dtype=f32)), dict(p=Rows(5, dtype=torch.int64)),
                 dict(q_weight=on(128), k_weight=on(128, dtype=f32)), dict(k_weight=on(128, dtype=torch.int32))):
         with pytest.raises(TypeError):
             f(**{**out, **bad})
@@ -171,6 +179,9 @@ def test_binding_refuses_bad_heads():
     w.requires_grad = True
     with pytest.raises(ValueError, match="k_weight requires a gradient"):
         f(k_weight=w, **out)
+    host = torch.zeros((5, 4, 128), dtype=bf)
+    with pytest.raises(ValueError, match="CUDA"):
+        mqa.qk_norm_rope(host, host, None, None)
 
 
 def test_turns():
