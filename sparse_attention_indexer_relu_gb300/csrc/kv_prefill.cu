@@ -119,7 +119,7 @@ __device__ __forceinline__ int block_limit(const AttnParams &p, const Seq &q, in
 // positions and the window of the block's first row.
 __device__ __forceinline__ int block_skip(const AttnParams &p, const Seq &q, int block) {
   if (kKind != kWindow || q.len < q.n) return 0;
-  return skipped_tiles<kKeys>(p, q.len - q.n + 1 + (int)((long long)block * kCols / p.group));
+  return skipped_tiles<kKeys>(p, q.len - q.n + 1 + block * kCols / p.group);  // (columns are fewer than 2^31)
 }
 // Tiles of a block, and of all blocks before it.  (More rows than positions:
 // every block counts as the whole length.)
@@ -339,8 +339,7 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
       const int nt = w.needed(p);
       const int lim = block_limit(p, w.x.q, w.x.block), first = w.x.t0 * kKeys + g * 16, head = w.x.head;
       // windows: positions before the first column's window, and behind the first positions, are not needed
-      const int lo = kKind == kWindow ? w.x.q.len - w.x.q.n + 1 + (int)((long long)w.x.block * kCols / p.group) - p.window
-                                      : 0;
+      const int lo = kKind == kWindow ? w.x.q.len - w.x.q.n + 1 + w.x.block * kCols / p.group - p.window : 0;
       const int32_t *table = p.c.table + (size_t)w.x.seq * p.c.max_pages;
       float lv_max = -128.f;
       auto ask = [&] {  // the part's queries
@@ -699,6 +698,24 @@ __device__ __noinline__ float weigh_far(uint32_t ts, const TileMeta &meta, float
   return l;
 }
 
+// Scores of 32 keys in TMEM, those without a bit in `see` hidden.
+__device__ __forceinline__ void hide_32(uint32_t ts, uint32_t see) {
+  if (__all_sync(~0u, see == ~0u)) return;
+  uint32_t s[32];
+  if (__all_sync(~0u, see == 0)) {
+#pragma unroll
+    for (int b = 0; b < 32; ++b) s[b] = 0xFF800000u;
+  } else {
+    tmem_ld_32x32b_x32(ts, s);
+    tmem_ld_wait();
+#pragma unroll
+    for (int b = 0; b < 32; ++b)
+      if (!(see >> b & 1)) s[b] = 0xFF800000u;
+  }
+  tmem_st32(ts, s);
+}
+// Bits of the n lowest of 32 positions (none below 0, all above 32).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 // Windows: scores of the part's tile t that the column does not see.  (What says so
 // is formed here, anew for each of these few tiles, and not held over all tiles.)
 __device__ __noinline__ void hide_outside(uint32_t ts, const Part &x, int t, int col, int ncols, int group, int window,
@@ -708,15 +725,9 @@ __device__ __noinline__ void hide_outside(uint32_t ts, const Part &x, int t, int
   const int lim = col < ncols ? min(max(x.q.len - x.q.n + (x.block * kCols + col) / group + 1, 0), x.q.len) : 0;
   const int lo = lim - window;
 #pragma unroll 1
-  for (int j = base; j < base + kKeys; j += 32) {
-    if (__all_sync(~0u, j + 32 <= lim && (j >= lo || j + 32 <= sinks))) continue;
-    uint32_t s[32];
-    tmem_ld_32x32b_x32(ts + (j - base), s);
-    tmem_ld_wait();
-#pragma unroll
-    for (int b = 0; b < 32; ++b)
-      if (j + b >= lim || (j + b < lo && j + b >= sinks)) s[b] = 0xFF800000u;
-    tmem_st32(ts + (j - base), s);
+  for (int j = 0; j < kKeys; j += 32) {
+    const int at = base + j;
+    hide_32(ts + j, below(lim - at) & (~below(lo - at) | below(sinks - at)));
   }
   tmem_st_wait();
 }
@@ -724,20 +735,12 @@ __device__ __noinline__ void hide_outside(uint32_t ts, const Part &x, int t, int
 // and of those behind the sequence.
 __device__ __noinline__ void hide_others(uint32_t ts, const Part &x, int t, int col, int ncols, int group,
                                          const int32_t *tree, int words) {
-  const int base = (x.t0 + t) * kKeys, own = x.q.len - x.q.n, len = x.q.len;
+  const int base = (x.t0 + t) * kKeys, own = x.q.len - x.q.n;
   const int32_t *mask = tree + (size_t)(x.q.r0 + (x.block * kCols + col) / group) * words;
 #pragma unroll 1
-  for (int j = base; j < base + kKeys; j += 32) {
-    uint32_t see = col < ncols ? tree_bits(mask, words, j - own) : 0u;
-    if (j + 32 > len) see = j >= len ? 0u : see & ((1u << (len - j)) - 1);
-    if (__all_sync(~0u, see == ~0u)) continue;
-    uint32_t s[32];
-    tmem_ld_32x32b_x32(ts + (j - base), s);
-    tmem_ld_wait();
-#pragma unroll
-    for (int b = 0; b < 32; ++b)
-      if (!(see >> b & 1)) s[b] = 0xFF800000u;
-    tmem_st32(ts + (j - base), s);
+  for (int j = 0; j < kKeys; j += 32) {
+    const int at = base + j;
+    hide_32(ts + j, col < ncols ? tree_bits(mask, words, at - own) & below(x.q.len - at) : 0u);
   }
   tmem_st_wait();
 }
@@ -960,12 +963,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // ---- this CTA's part of the line
   const int per_thread = (p.c.seqs + kThreads - 1) / kThreads;
-  long long mine = 0;
+  long long mine = 0, one = 0;  // the thread's, and a head's of its last sequence
   for (int i = 0; i < per_thread; ++i) {
     const int s = tid * per_thread + i;
     if (s >= p.c.seqs) break;
     const Seq q = seq_of(p, s);
-    if (q.blocks) mine += p.c.heads * tiles_before(p, q, q.blocks);
+    one = q.blocks ? tiles_before(p, q, q.blocks) : 0;
+    mine += p.c.heads * one;
     if (blockIdx.x == 0 && p.c.lens[s] != q.len) atomicOr(p.c.status, MQA_KV_DEV_BAD_LENGTH);
   }
   long long incl = mine;
@@ -997,8 +1001,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long b = before;
       for (int i = 0; i < per_thread; ++i) {
         const int s = tid * per_thread + i;
-        const Seq q = seq_of(p, s);
-        const long long per_head = q.blocks ? tiles_before(p, q, q.blocks) : 0, u = p.c.heads * per_head;
+        long long per_head = one;
+        if (per_thread > 1) {
+          const Seq q = seq_of(p, s);
+          per_head = q.blocks ? tiles_before(p, q, q.blocks) : 0;
+        }
+        const long long u = p.c.heads * per_head;
         if (cut < b + u) {
           sm.found_seq[k] = s;
           sm.found_per_head[k] = per_head;
