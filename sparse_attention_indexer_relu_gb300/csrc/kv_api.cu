@@ -252,9 +252,10 @@ int attention(const mqa_kv_cache *cache, const void *q, long long q_row_stride, 
     rc = encode_code_rows(&q_map, terms, (uint64_t)(type == MQA_KV_BF16 ? 2 : 3) * rows * q_heads, cache->head_dim, 128);
     if (rc != MQA_OK) return rc;
     rc = code(launch_tiled(kind, p, map, q_map, terms, factor, P.tiled_ctas, as_stream(stream)));
-    if (rc == MQA_OK) rc = code(launch_kv_join_tiled(p, P.tiled_ctas, as_stream(stream)));
+    if (rc == MQA_OK && !P.split) rc = code(launch_kv_join_tiled(p, P.tiled_ctas, as_stream(stream)));
     if (rc != MQA_OK || !P.split) return rc;
   }
+  const AttnParams tiled = p;
   p.max_cols = P.tiled ? kSplitCols : INT_MAX;
   p.desc = reinterpret_cast<int4 *>(ws);
   p.slots = reinterpret_cast<float *>(ws + P.slots_off);
@@ -267,7 +268,10 @@ int attention(const mqa_kv_cache *cache, const void *q, long long q_row_stride, 
     if (rc == MQA_OK) rc = encode_code_rows(&v_map, cache->v, code_rows, cache->head_dim, 16);
     if (rc != MQA_OK) return rc;
   }
-  return code(launch_split(kind, p, k_map, v_map, P.nb, P.ctas, P.tiled, as_stream(stream)));
+  rc = code(launch_split(kind, p, k_map, v_map, P.nb, P.ctas, P.tiled, as_stream(stream)));
+  if (rc != MQA_OK) return rc;
+  return code(P.tiled ? launch_kv_join_both(tiled, P.tiled_ctas, p, P.nb, P.ctas, as_stream(stream))
+                      : launch_kv_join(p, P.nb, P.ctas, as_stream(stream)));
 }
 
 }  // namespace

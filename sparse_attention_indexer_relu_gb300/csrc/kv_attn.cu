@@ -789,15 +789,14 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
 
 #if MQA_KV_KIND == 0
 // Join split items: a block adds the parts of two columns of the item that CTA
-// blockIdx.x of the kernel before began.  One long sequence is cut into one part
+// `cta` of the kernel before began.  One long sequence is cut into one part
 // per CTA, so four warps share a column's parts, each its own in CTA order, and
 // are added in warp order: results do not depend on the timing.
 namespace {
 template <int D>
-__global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb) {
+__device__ __forceinline__ void join_many(const AttnParams &p, int cb, int cta) {
   constexpr int WPC = 4, kJoinCols = 8 / WPC;
-  grid_wait();
-  const int4 d = p.desc[blockIdx.x];
+  const int4 d = p.desc[cta];
   const int more = d.w & 0xFFFFF, ncols = d.w >> 20;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % WPC;
   const int col = blockIdx.y * kJoinCols + warp / WPC;
@@ -806,7 +805,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb
   __shared__ float red[8];
   const bool on = col < ncols;
   const size_t pitch = (size_t)cb * (D + 4);
-  auto slot = [&](int i) { return p.slots + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * pitch; };
+  auto slot = [&](int i) { return p.slots + ((size_t)(cta + i) * 2 + (i == 0 ? 1 : 0)) * pitch; };
   float mx = -INFINITY, wx = -INFINITY;
   constexpr int E = D / 32;
   float o[E], ls = 0.f;
@@ -857,8 +856,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb
 // columns, one part's loads of all of them in flight (9 us after 5 prompts of up
 // to 1,531 rows, latency).
 template <int D>
-__global__ void __launch_bounds__(256) kv_join_few_kernel(const AttnParams p) {
-  grid_wait();
+__device__ __forceinline__ void join_few(const AttnParams &p) {
   const int4 d = p.desc[blockIdx.x];
   const int more = d.w & 0xFFFFF, ncols = d.w >> 20;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.y * 32 + warp * 4;
@@ -905,6 +903,26 @@ __global__ void __launch_bounds__(256) kv_join_few_kernel(const AttnParams p) {
   }
 }
 
+
+template <int D>
+__global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb) {
+  grid_wait();
+  join_many<D>(p, cb, blockIdx.x);
+}
+template <int D>
+__global__ void __launch_bounds__(256) kv_join_few_kernel(const AttnParams p) {
+  grid_wait();
+  join_few<D>(p);
+}
+// Of a call that ran both kernels: the first `tiled` blocks of a row join the tiled
+// one's items.  (In a launch of their own the split kernel's, of which such a call may
+// have none, took 3 us more.)
+template <int D>
+__global__ void __launch_bounds__(256) kv_join_both_kernel(const AttnParams t, const AttnParams p, int tiled, int cb) {
+  grid_wait();
+  if ((int)blockIdx.x < tiled) join_few<D>(t);
+  else join_many<D>(p, cb, blockIdx.x - tiled);
+}
 }  // namespace
 
 cudaError_t launch_kv_join(const AttnParams &p, int nb, int ctas, cudaStream_t stream) {
@@ -917,6 +935,14 @@ cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t str
   const dim3 grid(ctas, kTiledCols / 32);
   return p.c.dim == 64 ? launch_after(kv_join_few_kernel<64>, grid, 256, 0, stream, true, p)
                        : launch_after(kv_join_few_kernel<128>, grid, 256, 0, stream, true, p);
+}
+
+cudaError_t launch_kv_join_both(const AttnParams &t, int tiled_ctas, const AttnParams &p, int nb, int ctas,
+                                cudaStream_t stream) {
+  const dim3 grid(tiled_ctas + ctas, kTiledCols / 32 > 4 * nb ? kTiledCols / 32 : 4 * nb);
+  return p.c.dim == 64
+             ? launch_after(kv_join_both_kernel<64>, grid, 256, 0, stream, true, t, p, tiled_ctas, 8 * nb)
+             : launch_after(kv_join_both_kernel<128>, grid, 256, 0, stream, true, t, p, tiled_ctas, 8 * nb);
 }
 
 #endif  // MQA_KV_KIND == 0
@@ -934,13 +960,12 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &k_map, const CUtensor
                             : launch_after(kernel, dim3(ctas), kAttnThreads, bytes, stream, follows, p, k_map, v_map);
   };
 #if MQA_KV_KIND == 0
-  const cudaError_t e = p.selected ? run(kv_attn_kernel<D, NB, kSelected, false>, done[0])
-                        : p.test   ? run(kv_attn_kernel<D, NB, kDense, true>, done[1])
-                                   : run(kv_attn_kernel<D, NB, kDense, false>, done[2]);
+  return p.selected ? run(kv_attn_kernel<D, NB, kSelected, false>, done[0])
+         : p.test   ? run(kv_attn_kernel<D, NB, kDense, true>, done[1])
+                    : run(kv_attn_kernel<D, NB, kDense, false>, done[2]);
 #else
-  const cudaError_t e = run(kv_attn_kernel<D, NB, MQA_KV_KIND, false>, done[0]);
+  return run(kv_attn_kernel<D, NB, MQA_KV_KIND, false>, done[0]);
 #endif
-  return e != cudaSuccess ? e : launch_kv_join(p, NB, ctas, stream);
 }
 
 template <int D>

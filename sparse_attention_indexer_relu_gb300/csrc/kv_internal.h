@@ -103,8 +103,10 @@ cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t str
 template <int KIND>
 cudaError_t launch_kv_attention(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int nb,
                                 int ctas, bool follows, cudaStream_t stream);
-// The split kernel's joining pass.
+// The split kernel's joining pass, and that of a call that ran both kernels (t: the tiled one's).
 cudaError_t launch_kv_join(const AttnParams &p, int nb, int ctas, cudaStream_t stream);
+cudaError_t launch_kv_join_both(const AttnParams &t, int tiled_ctas, const AttnParams &p, int nb, int ctas,
+                                cudaStream_t stream);
 
 cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,
                              const int32_t *starts, int rows, int sms, cudaStream_t stream);
