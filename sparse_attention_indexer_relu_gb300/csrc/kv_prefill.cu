@@ -141,9 +141,26 @@ __device__ long long tiles_before(const AttnParams &p, const Seq &q, int block) 
   return sum;
 }
 
+// Windows and trees: a block of at most 128 columns has them in both halves, and the
+// halves take its tiles in turns; what a half has found of a column is added in the
+// end.  Such a tile takes half the time (drafts of 21 to 29 rows x 4 heads: 1.5 us a
+// tile when the other half had nothing to do, as long as tiles of 256 columns), so
+// work is counted in units of it.
+constexpr int kUnits = kKind == kDense ? 1 : 2;  // of a tile of more columns
+__device__ __forceinline__ bool in_turns(int cols) { return kKind != kDense && cols <= 128; }
+__device__ __forceinline__ int block_units(const AttnParams &p, const Seq &q, int block) {
+  return in_turns(q.n * p.group - block * kCols) ? 1 : kUnits;
+}
+__device__ __forceinline__ long long units_before(const AttnParams &p, const Seq &q, int block) {
+  if (kKind == kDense || block < q.blocks) return kUnits * tiles_before(p, q, block);
+  return kUnits * tiles_before(p, q, block - 1) +
+         (long long)block_units(p, q, block - 1) * block_tiles(p, q, block - 1);
+}
+
 struct Part {  // a part of an item: tiles [t0, t1) of tiles
   int seq, head, block, tiles, t0, t1;
-  int skip;  // windows: block_skip
+  int skip;   // windows: block_skip
+  int units;  // of a tile
   Seq q;
 };
 // First position of tile t.
@@ -155,12 +172,13 @@ __device__ __forceinline__ int tile_at(const AttnParams &p, const Part &x, int t
 // in shared memory, where lane 0 moves it on (in registers it would crowd out
 // the tiles that are on their way).
 struct Walk {
-  long long at, end;
+  long long at, end;  // in units
   Part x;
   __device__ __forceinline__ bool valid() const { return at < end; }
-  __device__ void fit() { x.t1 = (int)min((long long)x.tiles, x.t0 + (end - at)); }
+  __device__ __forceinline__ int units() const { return kKind == kDense ? 1 : x.units; }
+  __device__ void fit() { x.t1 = (int)min((long long)x.tiles, x.t0 + (end - at) / units()); }
   __device__ void next(const AttnParams &p) {
-    at += x.t1 - x.t0;
+    at += (x.t1 - x.t0) * units();
     if (at >= end) return;
     x.t0 = 0;
     if (++x.block == x.q.blocks) {
@@ -173,6 +191,7 @@ struct Walk {
     }
     x.tiles = block_tiles(p, x.q, x.block);
     x.skip = block_skip(p, x.q, x.block);
+    x.units = block_units(p, x.q, x.block);
     fit();
   }
   // key tiles that hold a key some column sees
@@ -185,10 +204,11 @@ struct Walk {
   }
 };
 
-// Where an end of a CTA's part lies: `off` tiles into the item of x.
+// Where an end of a CTA's part lies: `off` whole tiles, `units` units into the item of x.
 struct Cut {
   Part x;
   int off;
+  long long units;
 };
 
 struct TileMeta {
@@ -218,6 +238,7 @@ struct Smem {
   int found_seq[2];
   long long found_at[2], found_per_head[2], scan[kThreads / 32];
   Cut cut[2];
+  float turns[kKind == kDense ? 1 : 3][128];  // the second half's references and sums
 };
 
 __device__ __forceinline__ void step_on(const AttnParams &p, Walk &w) {
@@ -343,13 +364,14 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
       const int32_t *table = p.c.table + (size_t)w.x.seq * p.c.max_pages;
       float lv_max = -128.f;
       auto ask = [&] {  // the part's queries
-        const int halves = w.cols(p) > 128 ? 2 : 1, at = w.x.q.r0 * p.group + w.x.block * kCols;
+        const int cols = w.cols(p), halves = cols > 128 || in_turns(cols) ? 2 : 1;
+        const int at = w.x.q.r0 * p.group + w.x.block * kCols, apart = in_turns(cols) ? 0 : 128;
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(terms * halves * 128 * D));
         __syncwarp();
         if (lane < terms * halves) {
           const int x = lane / terms, term = lane % terms;
-          tma_load_2d(sm.q[x][term], &q_map, &sm.q_full, 0, (term * heads + head) * planes + at + 128 * x, once);
+          tma_load_2d(sm.q[x][term], &q_map, &sm.q_full, 0, (term * heads + head) * planes + at + apart * x, once);
         }
         ++q_no;
       };
@@ -517,7 +539,7 @@ __device__ void mma_role(const AttnParams &p, Smem<D, TEST> &sm) {
   constexpr uint32_t kQk = idesc_f8_e4m3_f32(128, kKeys), kPv = idesc_f16(128, D, true);
   const int terms = p.bf16 ? 2 : 3;
   uint64_t *const k_full = TEST && p.stall == 1 ? sm.never : sm.k_full;
-  uint32_t tile_no = 0, q_no = 0, p_no = 0;
+  uint32_t tile_no = 0, q_no = 0, p_no = 0;  // p_no: the phase of each half's weights
   const uint32_t q0 = Desc<D>::codes_lo(sm.q[0][0]), k0 = Desc<D>::codes_lo(sm.k[0]),
                  v0 = Desc<D>::values_lo(sm.v[0]);
   auto qk = [&](int x, int stage) {
@@ -539,6 +561,46 @@ __device__ void mma_role(const AttnParams &p, Smem<D, TEST> &sm) {
     const int nt = w.needed(p);
     const bool two = w.cols(p) > 128;
     if (nt == 0) continue;
+    if (in_turns(w.cols(p))) {
+      // half x: scores of tile 2 (t + 1) + x, weights times values of tile 2 t + x
+      for (int t = -1; 2 * t < nt; ++t) {
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          const int q = 2 * (t + 1) + x, v = 2 * t + x;
+          const bool has_q = q < nt, has_v = t >= 0 && v < nt;
+          if (!has_q && !has_v) continue;
+          const uint32_t kn = tile_no + q, vn = tile_no + v;
+          const int ks = kn % kStagesK, vs = vn % kStagesV;
+          if (has_q) bounded_wait(sm, k_full + ks, kn / kStagesK & 1, p);
+          if (q == 0) bounded_wait(sm, &sm.q_full, q_no & 1, p);
+          if (has_v) {
+            bounded_wait(sm, &sm.v_full[vs], vn / kStagesV & 1, p);
+            bounded_wait(sm, &sm.p_full[x], p_no >> x & 1, p);
+            p_no ^= 1u << x;
+          }
+          __syncwarp();
+          tc_fence_after();
+          if (elect_one()) {
+            if (has_v) {
+              pv(x, vs, t == 0);
+              if (v + 2 >= nt) umma_commit(&sm.o_full[x]);
+              umma_commit(&sm.v_empty[vs]);
+              umma_commit(&sm.m_empty[vn % kMeta]);
+            }
+            if (has_q) {
+              qk(x, ks);
+              umma_commit(&sm.s_full[x]);
+              umma_commit(&sm.k_empty[ks]);
+              if (q + 1 == nt) umma_commit(&sm.q_empty);  // the last scores are under way
+            }
+          }
+          __syncwarp();
+        }
+      }
+      tile_no += nt;
+      ++q_no;
+      continue;
+    }
     for (int t = -1; t < nt; ++t) {
       // scores of tile t + 1, weights times values of tile t
       const uint32_t kn = tile_no + t + 1, vn = tile_no + t;
@@ -550,7 +612,8 @@ __device__ void mma_role(const AttnParams &p, Smem<D, TEST> &sm) {
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         const bool on = x == 0 || two;
-        if (t >= 0) bounded_wait(sm, &sm.p_full[x], p_no++ >> 1 & 1, p);
+        if (t >= 0) bounded_wait(sm, &sm.p_full[x], p_no >> x & 1, p);
+        if (t >= 0) p_no ^= 1u << x;
         __syncwarp();
         tc_fence_after();
         if (elect_one()) {
@@ -762,7 +825,7 @@ __device__ __noinline__ void hide_behind(uint32_t ts, int room) {
 }
 
 template <int D, bool TEST>
-__device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long per, long long near) {
+__device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long per, long long near, long long cut1) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   const int x = threadIdx.x >> 7;        // tile of columns
   const int r = threadIdx.x & 127;       // its column
@@ -771,8 +834,10 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
   uint32_t tile_no = 0, s_no = 0, o_no = 0;
   for (; w.valid(); step_on(p, w)) {
     const int nt = w.needed(p), ncols = w.cols(p);
-    const int col = x * 128 + r;
-    if (ncols <= x * 128) {  // this half is empty: it keeps step, so that it meets every phase of the barriers
+    const bool turns = in_turns(ncols);
+    const int begin = turns ? x : 0, step = turns ? 2 : 1;  // the half's tiles
+    const int col = turns ? r : x * 128 + r;
+    if (kKind == kDense && ncols <= x * 128) {  // this half is empty: it keeps step, so that it meets every phase of the barriers
       for (int t = 0; t < nt; ++t, ++tile_no) {
         bounded_wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p);
         bounded_wait(sm, &sm.s_full[x], s_no++ & 1, p);  // without it this half could run ahead of the issuing warp
@@ -801,7 +866,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
       room0 -= w.x.t0 * kKeys;
       whole_tiles = __reduce_min_sync(~0u, room0) / kKeys;
     }
-    for (int t = 0; t < nt; ++t, ++tile_no) {
+    tile_no += begin;
+    for (int t = begin; t < nt; t += step, tile_no += step) {
       bounded_wait(sm, &sm.n_full[tile_no % kMeta], tile_no / kMeta & 1, p);
       bounded_wait(sm, &sm.s_full[x], s_no++ & 1, p);
       __syncwarp();
@@ -821,9 +887,9 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
       const bool look = meta.spread > kFar - 16.f;
       // (Columns of a window or tree may see nothing of it and of more tiles behind it;
       // theirs are set in the tile of the first key that they see.)
-      for (bool anew = t == 0 || (kKind != kDense && (edge || t == from) &&
-                                  __any_sync(~0u, m == -INFINITY && col < ncols));; anew = true) {
-        if (anew) settle<D>(ts, to, meta, cs, t > 0, m, wr, l);
+      for (bool anew = t == begin || (kKind != kDense && (edge || t < from + step) &&
+                                      __any_sync(~0u, m == -INFINITY && col < ncols));; anew = true) {
+        if (anew) settle<D>(ts, to, meta, cs, t > begin, m, wr, l);
         if (look && __any_sync(~0u, wr - meta.lv_min - m > kFar)) {
           if (!anew) continue;
           l = weigh_far(ts, meta, cs, m, wr, l);
@@ -889,10 +955,29 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
       mbar_arrive(&sm.p_full[x]);
     }
     // ---- the part's result
-    if (nt) {
+    if (turns) tile_no += nt - begin - (nt - begin + 1) / 2 * 2;  // behind the part's tiles
+    if (nt > begin) {
       bounded_wait(sm, &sm.o_full[x], o_no++ & 1, p);
       __syncwarp();
       tc_fence_after();
+    }
+    float f0 = 1.f, f1 = 0.f;  // what the halves' sums are multiplied with
+    if (turns) {
+      float *with = &sm.turns[0][r];
+      if (x == 1) {
+        with[0] = m, with[kKind == kDense ? 0 : 128] = wr, with[kKind == kDense ? 0 : 256] = l;
+        tc_fence_before();
+        named_bar(1, 256);
+        named_bar(2, 256);  // its O has been read
+        continue;
+      }
+      named_bar(1, 256);
+      tc_fence_after();
+      const float m1 = with[0], w1 = with[kKind == kDense ? 0 : 128], l1 = with[kKind == kDense ? 0 : 256];
+      const float mx = fmaxf(m, m1), wx = fmaxf(wr, w1);
+      l = l * (m == mx ? 1.f : ex2(m - mx)) + l1 * (m1 == mx ? 1.f : ex2(m1 - mx));
+      f0 = wr == wx ? 1.f : ex2(wr - wx), f1 = w1 == wx ? 1.f : ex2(w1 - wx);
+      m = mx, wr = wx;
     }
     const bool whole = w.x.t0 == 0 && w.x.t1 == w.x.tiles;
     const bool none = m == -INFINITY && l == 0.f;
@@ -908,6 +993,14 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
       if (nt) {
         tmem_ld_32x32b_x32(to + j, o);
         tmem_ld_wait();
+      }
+      if (turns && nt > 1) {
+        uint32_t o1[32];
+        tmem_ld_32x32b_x32(to + 128 + j, o1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int b = 0; b < 32; ++b)
+          o[b] = __float_as_uint(fmaf(__uint_as_float(o[b]), f0, __uint_as_float(o1[b]) * f1));
       }
       if (none) {
 #pragma unroll
@@ -932,6 +1025,10 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
         }
       }
     }
+    if (turns) {
+      tc_fence_before();
+      named_bar(2, 256);
+    }
     if (col < ncols_now) {
       if (whole) {
         if (p.lse)
@@ -945,7 +1042,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
     if (threadIdx.x == 0 && !whole && w.x.t0 == 0) {
       // ends of parts that lie inside the item behind this one, each the beginning of
       // a following CTA's part
-      const long long rest = w.x.tiles - w.x.t1 - near;
+      const long long rest = w.at + (long long)(w.x.tiles - near - w.x.t0) * w.units() - cut1;
       p.desc[blockIdx.x] = make_int4(w.x.q.r0, w.x.head, w.x.block * kCols,
                                      (int)((rest + per - 1) / per) | ncols_now << 20);
     }
@@ -968,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = tid * per_thread + i;
     if (s >= p.c.seqs) break;
     const Seq q = seq_of(p, s);
-    one = q.blocks ? tiles_before(p, q, q.blocks) : 0;
+    one = q.blocks ? units_before(p, q, q.blocks) : 0;
     mine += p.c.heads * one;
     if (blockIdx.x == 0 && p.c.lens[s] != q.len) atomicOr(p.c.status, MQA_KV_DEV_BAD_LENGTH);
   }
@@ -987,10 +1084,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // (One tile is enough for a part: a prompt of 128 rows takes 15 us so, 21 with two
   // tiles or more and 31 with four.)
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  // (Whole tiles of more columns, so that none of the parts of an item is empty.)
+  const long long per = (total + gridDim.x * kUnits - 1) / (gridDim.x * kUnits) * kUnits;
   // Even ends; one that lies within kNear tiles of an item's own end is
   // moved there, which saves the item's partial results and their joining.
-  const long long near = min(per / 8, (long long)kNear), cut0 = min(blockIdx.x * per, total), cut1 = min(cut0 + per, total);
+  const long long near = min(per / (8 * kUnits), (long long)kNear), cut0 = min(blockIdx.x * per, total), cut1 = min(cut0 + per, total);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (cut0 >= cut1) grid_wait();
   if (cut0 >= cut1) return;  // the whole CTA leaves together
@@ -1004,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long per_head = one;
         if (per_thread > 1) {
           const Seq q = seq_of(p, s);
-          per_head = q.blocks ? tiles_before(p, q, q.blocks) : 0;
+          per_head = q.blocks ? units_before(p, q, q.blocks) : 0;
         }
         const long long u = p.c.heads * per_head;
         if (cut < b + u) {
@@ -1062,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int lo = 0, hi = c.x.q.blocks;  // the last block that begins at or before `rest`: 32 candidates at a time
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-      const long long v = at < hi ? tiles_before(p, c.x.q, at) : 0;
+      const long long v = at < hi ? units_before(p, c.x.q, at) : 0;
       const int pick = 31 - __clz(__ballot_sync(~0u, at < hi && v <= rest));  // lane 0's candidate always is one
       begins = __shfl_sync(~0u, v, pick);
       lo += pick * step;
@@ -1071,7 +1169,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     c.x.block = lo;
     c.x.tiles = block_tiles(p, c.x.q, lo);
     c.x.skip = block_skip(p, c.x.q, lo);
-    c.off = (int)(rest - begins);
+    c.x.units = block_units(p, c.x.q, lo);
+    c.units = rest - begins;
+    c.off = (int)(c.units / c.x.units);
     if (lane == 0) sm.cut[warp] = c;
   }
   __syncthreads();
@@ -1081,13 +1181,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.end = cut1;
     if (cut1 < total) {
       const int to_end = e.x.tiles - e.off;
-      w.end = e.off <= near ? cut1 - e.off : to_end <= near ? cut1 + to_end : cut1;
+      w.end = cut1 - e.units + (long long)(e.off <= near ? 0 : to_end <= near ? e.x.tiles : e.off) * e.x.units;
     }
-    w.at = cut0;
+    w.at = cut0 - c.units + (long long)c.off * c.x.units;
     w.x = c.x;
     w.x.t0 = c.off;
     if (c.off <= near) {
-      w.at = cut0 - c.off;
+      w.at = cut0 - c.units;
       w.x.t0 = 0;
     } else if (c.x.tiles - c.off <= near) {
       w.x.t1 = c.x.tiles;
@@ -1103,7 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // 735; with 200, 72 and 40 the converters spill: 1,360 instead of 799.)
   if (warp < 8) {
     reg_inc<192>();
-    softmax_role<D, TEST>(p, sm, per, near);
+    softmax_role<D, TEST>(p, sm, per, near, cut1);
   } else if (warp < 12) {
     reg_dec<80>();
     convert_role<D, TEST>(p, sm);
