@@ -70,6 +70,7 @@ constexpr int kTerms = kQueryTerms;       // e4m3 terms of a query value (bf16: 
 // positions 16% slower, for want of balance.)
 constexpr int kNear = 2;
 constexpr int kConverters = 128;
+constexpr int kNoPage = INT32_MIN;  // no key of a page is needed
 
 // sum over 0 <= i < n of floor((a i + b) / m); a, b >= 0, m > 0.  Whole parts
 // first; what is left below the line is counted along the other axis.
@@ -143,13 +144,12 @@ __device__ long long tiles_before(const AttnParams &p, const Seq &q, int block) 
 
 // Windows and trees: a block of at most 128 columns has them in both halves, and the
 // halves take its tiles in turns; what a half has found of a column is added in the
-// end.  Such a tile takes half the time (drafts of 21 to 29 rows x 4 heads: 1.5 us a
-// tile when the other half had nothing to do, as long as tiles of 256 columns), so
-// work is counted in units of it.
-constexpr int kUnits = kKind == kDense ? 1 : 2;  // of a tile of more columns
+// end.  Such a tile takes two thirds of the time (drafts of 16 sequences: 2,300 cycles
+// and 3,500; with one half idle as long as the others), so work is counted in thirds.
+constexpr int kUnits = kKind == kDense ? 1 : 3, kTurnUnits = 2;  // of a tile of more columns, of one in turns
 __device__ __forceinline__ bool in_turns(int cols) { return kKind != kDense && cols <= 128; }
 __device__ __forceinline__ int block_units(const AttnParams &p, const Seq &q, int block) {
-  return in_turns(q.n * p.group - block * kCols) ? 1 : kUnits;
+  return in_turns(q.n * p.group - block * kCols) ? kTurnUnits : kUnits;
 }
 __device__ __forceinline__ long long units_before(const AttnParams &p, const Seq &q, int block) {
   if (kKind == kDense || block < q.blocks) return kUnits * tiles_before(p, q, block);
@@ -211,14 +211,14 @@ struct Cut {
   long long units;
 };
 
-struct TileMeta {
+struct alignas(16) TileMeta {
   float2 kv[8];          // per 16 keys: key scale, log2 of the value scale
+  int row[8];            // first row of each 16 keys in the pool; -1: page outside the pool, -2: no key needed
   float lv_min;          // least of the latter,
   float spread;          // and how far it lies below the largest of the part so far
   uint32_t odd;          // nonzero where hide or nan is
   uint32_t hide[4];      // keys that no column sees (a page outside the pool)
   uint32_t nan[4];       // keys whose values hold a NaN code
-  int row[8];            // first row of each 16 keys in the pool; -1: page outside the pool, -2: no key needed
 };
 
 
@@ -377,23 +377,43 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
       };
       const bool begins = q_no == 0;
       if (begins && nt > 0) ask();  // the first part's before anything is looked up
-      for (int tb = 0; tb < nt; tb += 4) {
-        const int t = tb + (lane >> 3), pos = kKind == kWindow ? tile_at(p, w.x, w.x.t0 + t) + g * 16 : first + t * kKeys;
-        int row = -2;
-        float ks = 1.f, lv = 0.f;
+      // Pages are looked up two steps of four tiles ahead, scales one.
+      auto pos_of = [&](int tb) {
+        const int t = tb + (lane >> 3);
+        return kKind == kWindow ? tile_at(p, w.x, w.x.t0 + t) + g * 16 : first + t * kKeys;
+      };
+      auto page_of = [&](int tb) {
+        const int pos = pos_of(tb);
         const int at = pos - g % per_box * 16;  // of the box: it is copied whole, from its first 16 keys' row on
-        if (t < nt && pos < lim && (kKind != kWindow || at < p.sinks || at + box > lo)) {
-          const int page = __ldg(table + (pos >> p.c.page_log2));
-          if ((unsigned)page < (unsigned)p.c.pages) {
-            const int ph = page * heads + head;
-            row = (ph << p.c.page_log2) + (pos & (p.c.page - 1));
-            ks = exp_byte(__ldg(p.c.k_exps + ph));
-            lv = (float)(int)__ldg(p.c.v_exps + ph) - 127.f;
-          } else {
-            row = -1;
-            atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
-          }
+        if (tb + (lane >> 3) >= nt || pos >= lim || (kKind == kWindow && at >= p.sinks && at + box <= lo)) return kNoPage;
+        return max(__ldg(table + (pos >> p.c.page_log2)), -1);
+      };
+      struct Found {
+        int row;
+        uint32_t ke, ve;
+      };
+      auto rows_of = [&](int tb, int page) {
+        Found f{-2, 127, 127};
+        if (page == kNoPage) return f;
+        if ((unsigned)page < (unsigned)p.c.pages) {
+          const int ph = page * heads + head;
+          f.row = (ph << p.c.page_log2) + (pos_of(tb) & (p.c.page - 1));
+          f.ke = __ldg(p.c.k_exps + ph);
+          f.ve = __ldg(p.c.v_exps + ph);
+        } else {
+          f.row = -1;
+          atomicOr(p.c.status, MQA_KV_DEV_BAD_INDEX);
         }
+        return f;
+      };
+      Found next = rows_of(0, page_of(0));
+      int page = page_of(4);
+      for (int tb = 0; tb < nt; tb += 4) {
+        const Found now = next;
+        next = rows_of(tb + 4, page);
+        page = page_of(tb + 8);
+        const int row = now.row;
+        const float ks = exp_byte(now.ke), lv = (float)(int)now.ve - 127.f;
         float lv_min = lv;  // of the tile; groups that hold no key do not count
         if (row < 0) lv_min = 128.f;
 #pragma unroll
@@ -403,9 +423,11 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
         for (int o = 1; o < 32; o <<= 1) lv_max = fmaxf(lv_max, __shfl_xor_sync(~0u, lv_max, o));
         const uint32_t bad = __ballot_sync(~0u, row == -1);
         const uint32_t copies = __ballot_sync(~0u, row >= 0 && g % per_box == 0);
-        for (int u = 0; u < min(4, nt - tb); ++u, ++tile_no) {
-          const int slot = tile_no % kMeta, stage = tile_no % kStagesK;
-          if (!warp_wait(sm, &sm.m_empty[slot], (tile_no / kMeta & 1) ^ 1, p)) return;
+        const int some = min(4, nt - tb);
+        // all descriptions first: the converters may go ahead of the keys' copies
+        for (int u = 0; u < some; ++u) {
+          const int slot = (tile_no + u) % kMeta;
+          if (!warp_wait(sm, &sm.m_empty[slot], ((tile_no + u) / kMeta & 1) ^ 1, p)) return;
           TileMeta &meta = sm.meta[slot];
           if (lane >> 3 == u) {
             meta.row[g] = row;
@@ -421,12 +443,14 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
               meta.odd = (bad >> (8 * u) & 255u) != 0;
             }
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.m_full[slot]);
+        }
+        for (int u = 0; u < some; ++u, ++tile_no) {
+          const int stage = tile_no % kStagesK;
           const uint32_t mine = copies >> (8 * u) & 255u;
           if (!warp_wait(sm, &sm.k_empty[stage], (tile_no / kStagesK & 1) ^ 1, p)) return;
-          if (lane == 0) {
-            mbar_arrive(&sm.m_full[slot]);
-            mbar_arrive_expect_tx(&sm.k_full[stage], (uint32_t)(__popc(mine) * box * D));
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[stage], (uint32_t)(__popc(mine) * box * D));
           __syncwarp();
           if (lane >> 3 == u && (mine >> g & 1))
             tma_load_2d(sm.k[stage] + g * 16 * D, &map, &sm.k_full[stage], 0, row, keep);
@@ -469,10 +493,23 @@ __device__ void take_nan_out(uint4 (&x)[STEPS], TileMeta &meta, int r0) {
     }
   }
 }
+// NaN codes are taken out; the scores of the columns that see their key become NaN.
+// The softmax waits for this, not for the stage.
+template <int STEPS, int RPS, int D, bool TEST>
+__device__ __forceinline__ void take_out(uint4 (&x)[STEPS], Smem<D, TEST> &sm, uint32_t tile_no, int r0) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i)
+    any |= nan_bits(x[i].x) | nan_bits(x[i].y) | nan_bits(x[i].z) | nan_bits(x[i].w);
+  if (any & 0x80808080u) take_nan_out<STEPS, RPS>(x, sm.meta[tile_no % kMeta], r0);
+  mbar_arrive(&sm.n_full[tile_no % kMeta]);
+}
 // A warp's load covers whole 128-byte lines; its lanes are laid out so that 8
 // of them store to 8 different bank groups (4 chunks of two rows whose
 // exchanges differ in the lowest bit).
-template <int D, bool TEST>
+// STAGED: values that come from HBM (drafts read the cache once), whose latency one tile
+// ahead in registers does not cover.
+template <int D, bool TEST, bool STAGED>
 __device__ void convert_role(const AttnParams &p, Smem<D, TEST> &sm) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   constexpr int CH = D / 16;              // 16-byte chunks of a code row
@@ -484,6 +521,57 @@ __device__ void convert_role(const AttnParams &p, Smem<D, TEST> &sm) {
   const uint32_t last_row = ((uint32_t)p.c.pages * p.c.heads << p.c.page_log2) - 16;  // begins the pool's last 16 rows
   uint32_t tile_no = 0;
   uint4 x[STEPS];
+  if (STAGED) {
+    // Two tiles on their way into shared memory (where a third query term would lie),
+    // each 16 bytes to a place of the thread's own, so that nobody else waits for them.
+    uint8_t *const raw[2] = {sm.q[0][2] + tid * 16, sm.q[1][2] + tid * 16};
+    const uint8_t *const values = p.c.v + (r0 & 15) * D + ch * 16;
+    auto fetch = [&](uint32_t no, bool on) {
+      if (on) {
+        bounded_wait(sm, &sm.m_full[no % kMeta], no / kMeta & 1, p);
+        uint8_t *const to = no & 1 ? raw[1] : raw[0];
+        const int4 *const rows = reinterpret_cast<const int4 *>(sm.meta[no % kMeta].row);
+        const int4 a = rows[0], b = rows[1];
+        const int at[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const int row = D == 128 ? at[i % 8] : r0 < 16 ? at[2 * i % 8] : at[(2 * i + 1) % 8];
+          const bool ok = (uint32_t)row <= last_row;
+          cp_async16(to + i * kConverters * 16, values + (size_t)(ok ? (uint32_t)row : 0u) * D, ok);
+        }
+      }
+      cp_async_commit();
+    };
+    for (; w.valid(); step_on(p, w)) {
+      const int nt = w.needed(p);
+      if (nt == 0) continue;  // nothing is read
+      fetch(tile_no, true);
+      fetch(tile_no + 1, nt > 1);
+      for (int t = 0; t < nt; ++t, ++tile_no) {
+        const int stage = tile_no % kStagesV;
+        cp_async_wait<1>();
+        const uint8_t *const at = tile_no & 1 ? raw[1] : raw[0];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) x[i] = *reinterpret_cast<const uint4 *>(at + i * kConverters * 16);
+        take_out<STEPS, RPS>(x, sm, tile_no, r0);
+        fetch(tile_no + 2, t + 2 < nt);
+        bounded_wait(sm, &sm.v_empty[stage], (tile_no / kStagesV & 1) ^ 1, p);
+        uint8_t *dst = sm.v[stage];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const int r = i * RPS + r0;
+          *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * ch)) =
+              make_uint4(cvt2(x[i].x), cvt2_hi(x[i].x), cvt2(x[i].y), cvt2_hi(x[i].y));
+          *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * ch + 1)) =
+              make_uint4(cvt2(x[i].z), cvt2_hi(x[i].z), cvt2(x[i].w), cvt2_hi(x[i].w));
+        }
+        fence_async_smem();
+        mbar_arrive(&sm.v_full[stage]);
+      }
+    }
+    cp_async_wait<0>();
+    return;
+  }
   auto load = [&](uint32_t no, int i) {
     const int r = i * RPS + r0;
     const int row = sm.meta[no % kMeta].row[r >> 4];
@@ -502,14 +590,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D, TEST> &sm) {
 
     for (int t = 0; t < nt; ++t, ++tile_no) {
       const int stage = tile_no % kStagesV;
-      // NaN codes are taken out; the scores of the columns that see their key become
-      // NaN.  The softmax waits for this, not for the stage.
-      uint32_t any = 0;
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i)
-        any |= nan_bytes(x[i].x) | nan_bytes(x[i].y) | nan_bytes(x[i].z) | nan_bytes(x[i].w);
-      if (any) take_nan_out<STEPS, RPS>(x, sm.meta[tile_no % kMeta], r0);
-      mbar_arrive(&sm.n_full[tile_no % kMeta]);
+      take_out<STEPS, RPS>(x, sm, tile_no, r0);
       if (t + 1 < nt) bounded_wait(sm, &sm.m_full[(tile_no + 1) % kMeta], (tile_no + 1) / kMeta & 1, p);
       bounded_wait(sm, &sm.v_empty[stage], (tile_no / kStagesV & 1) ^ 1, p);
       uint8_t *dst = sm.v[stage];
@@ -1084,8 +1165,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // (One tile is enough for a part: a prompt of 128 rows takes 15 us so, 21 with two
   // tiles or more and 31 with four.)
-  // (Whole tiles of more columns, so that none of the parts of an item is empty.)
-  const long long per = (total + gridDim.x * kUnits - 1) / (gridDim.x * kUnits) * kUnits;
+  // (A tile at least, so that none of the parts of an item is empty.)
+  const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kUnits);
   // Even ends; one that lies within kNear tiles of an item's own end is
   // moved there, which saves the item's partial results and their joining.
   const long long near = min(per / (8 * kUnits), (long long)kNear), cut0 = min(blockIdx.x * per, total), cut1 = min(cut0 + per, total);
@@ -1206,7 +1287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     softmax_role<D, TEST>(p, sm, per, near, cut1);
   } else if (warp < 12) {
     reg_dec<80>();
-    convert_role<D, TEST>(p, sm);
+    if (kKind == kTree && p.bf16) convert_role<D, TEST, kKind == kTree>(p, sm);
+    else convert_role<D, TEST, false>(p, sm);
   } else {
     reg_dec<48>();
     if (warp == 12) mma_role<D, TEST>(p, sm);

@@ -62,7 +62,8 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
   return lo | hi << 16;
 }
 // Bytes of w that hold a NaN code (0x7F or 0xFF), as 0x80 bits.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }  // among others
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return nan_bits(w) & 0x80808080u; }
 
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16 operands.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
