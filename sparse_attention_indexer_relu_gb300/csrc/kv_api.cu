@@ -125,7 +125,7 @@ constexpr int kSplitTree = 64;
 struct AttnPlan {
   bool split, tiled;
   int nb, ctas, tiled_ctas;
-  size_t slots_off, tiled_off, tiled_slots_off, factor_off, terms_off, bytes;
+  size_t slots_off, tiled_off, cuts_off, tiled_slots_off, factor_off, terms_off, bytes;
 };
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, int q_heads, bool selected,
@@ -156,7 +156,8 @@ AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, 
   p.slots_off = up256((size_t)most_ctas * sizeof(int4));
   p.tiled_off = up256(p.slots_off + most_floats * sizeof(float));
   p.tiled_ctas = sms;
-  p.tiled_slots_off = p.tiled_off + up256((size_t)sms * sizeof(int4));
+  p.cuts_off = p.tiled_off + up256((size_t)sms * sizeof(int4));
+  p.tiled_slots_off = p.cuts_off + up256((size_t)(sms + 1) * kCutBytes);
   p.factor_off = p.tiled_slots_off + up256((size_t)sms * 2 * kTiledCols * (c->head_dim + 4) * sizeof(float));
   p.terms_off = p.factor_off + up256((size_t)rows * q_heads * sizeof(float));
   p.bytes = p.tiled ? p.terms_off + (size_t)kQueryTerms * rows * q_heads * c->head_dim : p.tiled_off;
@@ -242,6 +243,7 @@ int attention(const mqa_kv_cache *cache, const void *q, long long q_row_stride, 
     p.max_cols = P.split ? kSplitCols : 0;
     p.desc = reinterpret_cast<int4 *>(ws + P.tiled_off);
     p.slots = reinterpret_cast<float *>(ws + P.tiled_slots_off);
+    p.cuts = ws + P.cuts_off;
     CUtensorMap map, q_map;
     uint8_t *terms = ws + P.terms_off;
     float *factor = reinterpret_cast<float *>(ws + P.factor_off);

@@ -71,6 +71,7 @@ struct AttnParams {
   int tree_words;
   int max_cols;      // sequences of more (row, head of the group) columns go to the tiled kernel
   int4 *desc;        // per CTA: the split item it began, for the joining kernel
+  uint8_t *cuts;     // tiled kernel: the line's length and the parts' (two 64-bit words), then where each part's end lies
   float *slots;      // per CTA: two slots of partial results
   const float *q_scale;  // tiled kernel: per column, what its products are multiplied with
   // tests only (mqa_kv_debug_options): their compilations are to run, with this
@@ -87,6 +88,7 @@ size_t attn_slot_floats(int nb, int dim);
 // Columns per item of the tiled kernel (p.max_cols: it takes the sequences of
 // more columns).
 constexpr int kTiledCols = 256;
+constexpr int kCutBytes = 64;  // of an entry of p.cuts, and of its head
 constexpr int kQueryTerms = 3;  // e4m3 terms of an fp16 query value; a bf16 one has 2
 // map: the keys' codes as rows of head_dim bytes, boxes of one page; q_map: the
 // query terms (q8, workspace of kQueryTerms * rows * q_heads * head_dim bytes)

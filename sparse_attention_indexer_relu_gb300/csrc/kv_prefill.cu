@@ -210,6 +210,16 @@ struct Cut {
   int off;
   long long units;
 };
+static_assert(sizeof(Cut) == kCutBytes);
+__device__ __forceinline__ Cut load_cut(const AttnParams &p, int i) {
+  int4 w[sizeof(Cut) / 16];
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(Cut) / 16; ++k)
+    w[k] = __ldcg(reinterpret_cast<const int4 *>(p.cuts + kCutBytes * (i + 1)) + k);
+  Cut c;
+  memcpy(&c, w, sizeof c);
+  return c;
+}
 
 struct alignas(16) TileMeta {
   float2 kv[8];          // per 16 keys: key scale, log2 of the value scale
@@ -228,16 +238,16 @@ struct Smem {
   uint8_t q[2][kTerms][128 * D];
   uint8_t k[kStagesK][kKeys * D];
   uint8_t v[kStagesV][kKeys * D * 2];
+  uint8_t raw[2][kKind == kTree && D == 64 ? kKeys * D : 16];  // values on their way to the converters
   TileMeta meta[kMeta];
   uint64_t q_full, q_empty, k_full[kStagesK], k_empty[kStagesK], v_full[kStagesV], v_empty[kStagesV];
   uint64_t m_full[kMeta], m_empty[kMeta], n_full[kMeta], s_full[2], p_full[2], o_full[2], done;
   uint64_t never[kStagesK];  // tests: nothing arrives here
   Walk walk[kThreads / 32];
+  long long per, near, cut1;  // of the parts: their length, by how far an end is moved, this one's even end
   uint32_t tmem;
   int dead;
-  int found_seq[2];
-  long long found_at[2], found_per_head[2], scan[kThreads / 32];
-  Cut cut[2];
+  int2 whole[kKind == kWindow ? 8 : 1];  // per softmax warp: the part's tiles [x, y) that all of its columns see whole
   float turns[kKind == kDense ? 1 : 3][128];  // the second half's references and sums
 };
 
@@ -379,8 +389,8 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
       if (begins && nt > 0) ask();  // the first part's before anything is looked up
       // Pages are looked up two steps of four tiles ahead, scales one.
       auto pos_of = [&](int tb) {
-        const int t = tb + (lane >> 3);
-        return kKind == kWindow ? tile_at(p, w.x, w.x.t0 + t) + g * 16 : first + t * kKeys;
+        const int pos = first + (tb + (lane >> 3)) * kKeys;
+        return kKind == kWindow && pos >= sink_tiles<kKeys>(p) * kKeys ? pos + w.x.skip * kKeys : pos;
       };
       auto page_of = [&](int tb) {
         const int pos = pos_of(tb);
@@ -522,9 +532,10 @@ __device__ void convert_role(const AttnParams &p, Smem<D, TEST> &sm) {
   uint32_t tile_no = 0;
   uint4 x[STEPS];
   if (STAGED) {
-    // Two tiles on their way into shared memory (where a third query term would lie),
-    // each 16 bytes to a place of the thread's own, so that nobody else waits for them.
-    uint8_t *const raw[2] = {sm.q[0][2] + tid * 16, sm.q[1][2] + tid * 16};
+    // Two tiles on their way into shared memory (heads of 128: where a third query term
+    // would lie), each 16 bytes to a place of the thread's own, so that nobody else
+    // waits for them.
+    uint8_t *const raw[2] = {(D == 128 ? sm.q[0][2] : sm.raw[0]) + tid * 16, (D == 128 ? sm.q[1][2] : sm.raw[1]) + tid * 16};
     const uint8_t *const values = p.c.v + (r0 & 15) * D + ch * 16;
     auto fetch = [&](uint32_t no, bool on) {
       if (on) {
@@ -864,7 +875,7 @@ __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 
 // is formed here, anew for each of these few tiles, and not held over all tiles.)
 __device__ __noinline__ void hide_outside(uint32_t ts, const Part &x, int t, int col, int ncols, int group, int window,
                                           int sinks) {
-  const int first_tiles = (int)(((long long)sinks + kKeys - 1) / kKeys), v = x.t0 + t;
+  const int first_tiles = (int)((unsigned)(sinks + kKeys - 1) / kKeys), v = x.t0 + t;
   const int base = (v >= first_tiles ? v + x.skip : v) * kKeys;
   const int lim = col < ncols ? min(max(x.q.len - x.q.n + (x.block * kCols + col) / group + 1, 0), x.q.len) : 0;
   const int lo = lim - window;
@@ -906,7 +917,7 @@ __device__ __noinline__ void hide_behind(uint32_t ts, int room) {
 }
 
 template <int D, bool TEST>
-__device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long per, long long near, long long cut1) {
+__device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm) {
   Walk &w = sm.walk[threadIdx.x >> 5];
   const int x = threadIdx.x >> 7;        // tile of columns
   const int r = threadIdx.x & 127;       // its column
@@ -936,11 +947,14 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
     // Tiles [from, whole_tiles) every column of the warp sees whole (dense: from the
     // first on; windows: positions from the latest window's begin to the first limit;
     // trees: before the sequence's rows).
-    int from = 0, whole_tiles;
-    if (kKind == kWindow) {
-      whole_tiles = (__reduce_min_sync(~0u, col < ncols ? room0 : INT32_MAX) >> 7) - w.x.skip - w.x.t0;
-      from = __reduce_max_sync(~0u, col < ncols ? room0 - p.window : 0);
-      from = from > 0 ? (from + kKeys - 1) / kKeys - w.x.skip - w.x.t0 : 0;
+    int whole_tiles = 0;
+    if (kKind == kWindow) {  // (kept in shared memory: the loop has no register to spare)
+      const int lim = __reduce_min_sync(~0u, col < ncols ? room0 : INT32_MAX) / kKeys;
+      const int lo = __reduce_max_sync(~0u, col < ncols ? room0 - p.window : 0);
+      if ((threadIdx.x & 31) == 0)
+        sm.whole[threadIdx.x >> 5] = make_int2(lo > 0 ? (lo + kKeys - 1) / kKeys - w.x.skip - w.x.t0 : 0,
+                                               lim - w.x.skip - w.x.t0);
+      __syncwarp();
     } else if (kKind == kTree) {
       whole_tiles = max(w.x.q.len - w.x.q.n, 0) / kKeys - w.x.t0;
     } else {
@@ -955,7 +969,9 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
       tc_fence_after();
       const TileMeta &meta = sm.meta[tile_no % kMeta];
       if (meta.odd) hide_keys(ts, meta);
-      const bool edge = t >= whole_tiles || (kKind == kWindow && t < from);
+      const int2 whole = kKind == kWindow ? sm.whole[threadIdx.x >> 5] : make_int2(0, whole_tiles);
+      const int from = whole.x;
+      const bool edge = t >= whole.y || t < from;
       if (edge) {  // (not below: 128 live scores and a branch spill)
         if (kKind == kWindow) hide_outside(ts, w.x, t, col, ncols, p.group, p.window, p.sinks);
         else if (kKind == kTree) hide_others(ts, w.x, t, col, ncols, p.group, p.tree, p.tree_words);
@@ -1123,7 +1139,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm, long long p
     if (threadIdx.x == 0 && !whole && w.x.t0 == 0) {
       // ends of parts that lie inside the item behind this one, each the beginning of
       // a following CTA's part
-      const long long rest = w.at + (long long)(w.x.tiles - near - w.x.t0) * w.units() - cut1;
+      const long long per = sm.per, rest = w.at + (long long)(w.x.tiles - sm.near - w.x.t0) * w.units() - sm.cut1;
       p.desc[blockIdx.x] = make_int4(w.x.q.r0, w.x.head, w.x.block * kCols,
                                      (int)((rest + per - 1) / per) | ncols_now << 20);
     }
@@ -1139,63 +1155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Smem<D, TEST>;
   S &sm = *reinterpret_cast<S *>(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // ---- this CTA's part of the line
-  const int per_thread = (p.c.seqs + kThreads - 1) / kThreads;
-  long long mine = 0, one = 0;  // the thread's, and a head's of its last sequence
-  for (int i = 0; i < per_thread; ++i) {
-    const int s = tid * per_thread + i;
-    if (s >= p.c.seqs) break;
-    const Seq q = seq_of(p, s);
-    one = q.blocks ? units_before(p, q, q.blocks) : 0;
-    mine += p.c.heads * one;
-    if (blockIdx.x == 0 && p.c.lens[s] != q.len) atomicOr(p.c.status, MQA_KV_DEV_BAD_LENGTH);
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) sm.scan[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = incl - mine;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += sm.scan[i];
-    total += sm.scan[i];
-  }
-  // (One tile is enough for a part: a prompt of 128 rows takes 15 us so, 21 with two
-  // tiles or more and 31 with four.)
-  // (A tile at least, so that none of the parts of an item is empty.)
-  const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kUnits);
-  // Even ends; one that lies within kNear tiles of an item's own end is
-  // moved there, which saves the item's partial results and their joining.
-  const long long near = min(per / (8 * kUnits), (long long)kNear), cut0 = min(blockIdx.x * per, total), cut1 = min(cut0 + per, total);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (cut0 >= cut1) grid_wait();
-  if (cut0 >= cut1) return;  // the whole CTA leaves together
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const long long cut = k ? cut1 : cut0;
-    if (cut >= before && cut < before + mine) {
-      long long b = before;
-      for (int i = 0; i < per_thread; ++i) {
-        const int s = tid * per_thread + i;
-        long long per_head = one;
-        if (per_thread > 1) {
-          const Seq q = seq_of(p, s);
-          per_head = q.blocks ? units_before(p, q, q.blocks) : 0;
-        }
-        const long long u = p.c.heads * per_head;
-        if (cut < b + u) {
-          sm.found_seq[k] = s;
-          sm.found_per_head[k] = per_head;
-          sm.found_at[k] = b;
-          break;
-        }
-        b += u;
-      }
-    }
-  }
   if (tid == 0) {
     sm.dead = 0;
     mbar_init(&sm.q_full, 1);
@@ -1229,38 +1189,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // a warp finds the item of each end (each warp by itself took 11,000 cycles for both)
-  if (warp == 0 || (warp == 1 && cut1 < total)) {
-    Cut c;
-    c.x.seq = sm.found_seq[warp];
-    c.x.q = seq_of(p, c.x.seq);
-    long long rest = (warp ? cut1 : cut0) - sm.found_at[warp], begins = 0;
-    const long long per_head = sm.found_per_head[warp];
-    c.x.head = (int)(rest / per_head);
-    rest -= c.x.head * per_head;
-    int lo = 0, hi = c.x.q.blocks;  // the last block that begins at or before `rest`: 32 candidates at a time
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-      const long long v = at < hi ? units_before(p, c.x.q, at) : 0;
-      const int pick = 31 - __clz(__ballot_sync(~0u, at < hi && v <= rest));  // lane 0's candidate always is one
-      begins = __shfl_sync(~0u, v, pick);
-      lo += pick * step;
-      hi = min(hi, lo + step);
-    }
-    c.x.block = lo;
-    c.x.tiles = block_tiles(p, c.x.q, lo);
-    c.x.skip = block_skip(p, c.x.q, lo);
-    c.x.units = block_units(p, c.x.q, lo);
-    c.units = rest - begins;
-    c.off = (int)(c.units / c.x.units);
-    if (lane == 0) sm.cut[warp] = c;
+  grid_wait();  // the query terms and the ends of the parts
+  long long total, per;
+  {
+    const longlong2 line = __ldcg(reinterpret_cast<const longlong2 *>(p.cuts));
+    total = line.x, per = line.y;
   }
-  __syncthreads();
+  // Even ends; one that lies within kNear tiles of an item's own end is
+  // moved there, which saves the item's partial results and their joining.
+  const long long near = min(per / (8 * kUnits), (long long)kNear), cut0 = min(blockIdx.x * per, total), cut1 = min(cut0 + per, total);
+  if (tid == 0) sm.per = per, sm.near = near, sm.cut1 = cut1;
+  if (cut0 >= cut1) {  // the whole CTA leaves together
+    if (warp == 12) tmem_dealloc(sm.tmem, 512);
+    return;
+  }
   if (lane == 0) {
     Walk w;
-    const Cut &c = sm.cut[0], &e = sm.cut[1];
+    const Cut c = load_cut(p, blockIdx.x);
     w.end = cut1;
     if (cut1 < total) {
+      const Cut e = load_cut(p, blockIdx.x + 1);
       const int to_end = e.x.tiles - e.off;
       w.end = cut1 - e.units + (long long)(e.off <= near ? 0 : to_end <= near ? e.x.tiles : e.off) * e.x.units;
     }
@@ -1278,16 +1226,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.walk[warp] = w;
   }
   __syncwarp();
-  grid_wait();  // the query terms
   // Registers: 256 x 192 + 128 x 80 + 128 x 48 = 512 x 128, what the block was
   // launched with.  (Chunk of 32K positions, at the time: 720 us; with 184, 96 and 48
   // 735; with 200, 72 and 40 the converters spill: 1,360 instead of 799.)
   if (warp < 8) {
     reg_inc<192>();
-    softmax_role<D, TEST>(p, sm, per, near, cut1);
+    softmax_role<D, TEST>(p, sm);
   } else if (warp < 12) {
     reg_dec<80>();
-    if (kKind == kTree && p.bf16) convert_role<D, TEST, kKind == kTree>(p, sm);
+    if (kKind == kTree && (D == 64 || p.bf16)) convert_role<D, TEST, kKind == kTree>(p, sm);
     else convert_role<D, TEST, false>(p, sm);
   } else {
     reg_dec<48>();
@@ -1298,6 +1245,101 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 12) tmem_dealloc(sm.tmem, 512);
+}
+
+// The even ends of the CTAs' parts: 8 to a CTA, a warp each.  They are found beside the
+// query terms: the tiled kernel's CTAs, which need whole SMs, begin when those are
+// done, and took 4.5 us for it.
+constexpr int kFind = 8;
+__device__ void find_cuts(const AttnParams &p, int ctas) {
+  __shared__ long long s_scan[kFind], s_at[kFind], s_head[kFind];
+  __shared__ int s_seq[kFind];
+  constexpr int kSpan = 32 * kFind;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per_thread = (p.c.seqs + kSpan - 1) / kSpan;
+  long long mine = 0, one = 0;  // the thread's, and a head's of its last sequence
+  for (int i = 0; i < per_thread; ++i) {
+    const int s = tid * per_thread + i;
+    if (s >= p.c.seqs) break;
+    const Seq q = seq_of(p, s);
+    one = q.blocks ? units_before(p, q, q.blocks) : 0;
+    mine += p.c.heads * one;
+    if (blockIdx.x == 0 && p.c.lens[s] != q.len) atomicOr(p.c.status, MQA_KV_DEV_BAD_LENGTH);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  long long total = 0, before = incl - mine;
+  for (int i = 0; i < kFind; ++i) {
+    if (i < warp) before += s_scan[i];
+    total += s_scan[i];
+  }
+  // (One tile is enough for a part, and the least, so that none of the parts of an item
+  // is empty: a prompt of 128 rows takes 15 us so, 21 with two tiles or more and 31
+  // with four.)
+  const long long per = max((total + ctas - 1) / ctas, (long long)kUnits);
+  if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<longlong2 *>(p.cuts) = make_longlong2(total, per);
+  for (int k = 0; k < kFind; ++k) {
+    const long long cut = (blockIdx.x * kFind + k) * per;
+    if (cut < before || cut >= before + mine) continue;
+    long long b = before;
+    for (int i = 0; i < per_thread; ++i) {
+      const int s = tid * per_thread + i;
+      long long per_head = one;
+      if (per_thread > 1) {
+        const Seq q = seq_of(p, s);
+        per_head = q.blocks ? units_before(p, q, q.blocks) : 0;
+      }
+      const long long u = p.c.heads * per_head;
+      if (cut < b + u) {
+        s_seq[k] = s;
+        s_head[k] = per_head;
+        s_at[k] = b;
+        break;
+      }
+      b += u;
+    }
+  }
+  __syncthreads();
+  const int i = blockIdx.x * kFind + warp;
+  if (i >= ctas || i * per >= total) return;
+  Cut c;
+  c.x.seq = s_seq[warp];
+  c.x.q = seq_of(p, c.x.seq);
+  c.x.t0 = c.x.t1 = 0;
+  long long rest = i * per - s_at[warp], begins = 0;
+  const long long per_head = s_head[warp];
+  c.x.head = (int)(rest / per_head);
+  rest -= c.x.head * per_head;
+  int lo = 0, hi = c.x.q.blocks;  // the last block that begins at or before `rest`: 32 candidates at a time
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const long long v = at < hi ? units_before(p, c.x.q, at) : 0;
+    const int pick = 31 - __clz(__ballot_sync(~0u, at < hi && v <= rest));  // lane 0's candidate always is one
+    begins = __shfl_sync(~0u, v, pick);
+    lo += pick * step;
+    hi = min(hi, lo + step);
+  }
+  c.x.block = lo;
+  c.x.tiles = block_tiles(p, c.x.q, lo);
+  c.x.skip = block_skip(p, c.x.q, lo);
+  c.x.units = block_units(p, c.x.q, lo);
+  c.units = rest - begins;
+  c.off = (int)(c.units / c.x.units);
+  if (lane < (int)sizeof(Cut) / 16) {
+    int4 w[sizeof(Cut) / 16];
+    memcpy(w, &c, sizeof c);
+    int4 mine4 = w[0];
+#pragma unroll
+    for (int k = 1; k < (int)sizeof(Cut) / 16; ++k)
+      if (lane == k) mine4 = w[k];
+    reinterpret_cast<int4 *>(p.cuts + kCutBytes * (i + 1))[lane] = mine4;
+  }
 }
 
 // Query terms: D / 8 lanes per (row, head), 8 values each (90K rows of 128: 13.4 us, 3.4
@@ -1354,13 +1396,17 @@ __device__ __forceinline__ void terms_of(const AttnParams &p, const uint4 u, boo
 
 template <int D>
 __global__ void __launch_bounds__(256) kv_query_terms_kernel(const AttnParams p, uint8_t *__restrict__ q8,
-                                                            float *__restrict__ factor) {
+                                                            float *__restrict__ factor, int finders, int ctas) {
   grid_dependents();
+  if ((int)blockIdx.x < finders) {
+    find_cuts(p, ctas);
+    return;
+  }
   constexpr int LPR = D / 8, PER = 256 / LPR, BATCH = 4;  // lanes per row, rows per CTA and step, steps
   const int part = threadIdx.x % LPR;
   const int from = min(max(p.starts[0], 0), p.rows) * p.q_heads;  // rows of no sequence are not read
   const int last = min(max(p.starts[p.c.seqs], 0), p.rows) * p.q_heads;
-  const int first = blockIdx.x * PER * BATCH + threadIdx.x / LPR;
+  const int first = (blockIdx.x - finders) * PER * BATCH + threadIdx.x / LPR;
   uint4 u[BATCH];
   int row[BATCH], head[BATCH];
 #pragma unroll
@@ -1392,7 +1438,9 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &map, const CUtensorMa
   cudaError_t e = allow_smem(kv_prefill_kernel<D, TEST>, bytes, done);
   if (e != cudaSuccess) return e;
   const int rows = p.rows * p.q_heads, per = 4 * 256 / (D / 8);
-  e = launch_after(kv_query_terms_kernel<D>, dim3((rows + per - 1) / per), 256, 0, stream, false, p, q8, factor);
+  const int finders = (ctas + kFind - 1) / kFind;
+  e = launch_after(kv_query_terms_kernel<D>, dim3(finders + (rows + per - 1) / per), 256, 0, stream, false, p, q8,
+                   factor, finders, ctas);
   if (e != cudaSuccess) return e;
   return launch_after(kv_prefill_kernel<D, TEST>, dim3(ctas), kThreads, bytes, stream, true, p, map, q_map);
 }

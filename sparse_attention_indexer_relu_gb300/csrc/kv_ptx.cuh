@@ -218,7 +218,7 @@ inline cudaError_t allow_smem(K *kernel, size_t bytes, DeviceFlags &done) {
 // positions' tiles and before the tile in which the window of the first row begins,
 // whose last seen position is `lim` - 1.
 template <int kKeys>
-__device__ __forceinline__ int sink_tiles(const AttnParams &p) { return (int)(((long long)p.sinks + kKeys - 1) / kKeys); }
+__device__ __forceinline__ int sink_tiles(const AttnParams &p) { return (int)((unsigned)(p.sinks + kKeys - 1) / kKeys); }
 template <int kKeys>
 __device__ __forceinline__ int skipped_tiles(const AttnParams &p, int lim) {
   return max(max(lim - p.window, 0) / kKeys - sink_tiles<kKeys>(p), 0);
