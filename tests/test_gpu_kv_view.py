@@ -477,3 +477,138 @@ def test_as_many_sequences_as_there_may_be(mqa):  # noqa: F811
     mqa.kv_accept(dev, ints(st), ints(counts), ints(accepted))
     view.accept(c, st, counts, accepted)
     assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+
+
+# ---------------------------------------------------------------- values that are hard, in every kernel
+HARD = [  # heads, group, lens, rows: split kernel; tiled, halves in turns; tiled, two halves
+    (2, 4, [300], [6]), (1, 4, [700, 400], [30, 25]), (1, 8, [700, 300], [60, 31])]
+
+
+def both_views(mqa, c, rng, rows, group, q, qd, st, scale=None, dtype="bf16"):  # noqa: F811
+    """A tree and a window call, each in the kernel that the sizes choose, and their plain answers."""
+    parents = view.random_parents(rng, rows)
+    mask, _ = view.tree_mask(c, st, parents, -(-max(rows) // 32))
+    dev = ref.to_device(c, mqa)
+    scale = c.dim ** -0.5 if scale is None else scale
+    got = mqa.kv_attention(q, dev, ints(st), tree=ints(mask), scale=scale)
+    yield got, c.attention(qd, st, scale, dtype, view.tree_seen(c, st, mask), causal=False)
+    got = mqa.kv_attention(q, dev, ints(st), window=100, sinks=3, scale=scale)
+    yield got, c.attention(qd, st, scale, dtype, view.window_seen(c, st, 100, 3))
+    assert mqa.kv_status(dev) == 0
+
+
+def long_tables(c, rows, group):
+    """Tables so long that trees go to the tiled kernel."""
+    c.table = np.concatenate([c.table, np.full((len(c.lens), LITTLE // (sum(rows) * c.heads * group * c.page) + 1), -1,
+                                               np.int32)], 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", HARD, ids=str)
+def test_infinite_and_nan_queries(mqa, case, dtype):  # noqa: F811
+    heads, group, lens, rows = case
+    rng = np.random.default_rng(30)
+    c = ref.random_cache(rng, 100, heads, 16, 128, lens, 60)
+    if sum(rows) > 10:
+        long_tables(c, rows, group)
+    st, n = starts_of(rows), sum(rows)
+    q, _ = rows_of(rng, n, heads * group, 128, dtype)
+    q[0, 1, 5], q[n - 1, 0, 0], q[n // 2, 2, 127] = float("nan"), float("inf"), -float("inf")
+    for got, want in both_views(mqa, c, rng, rows, group, q, q.double().cpu().numpy(), st, dtype=dtype):
+        check(got, None, want)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("case", HARD, ids=str)
+def test_scales_far_apart_and_sharp_softmax(mqa, case, dim):  # noqa: F811
+    heads, group, lens, rows = case
+    rng = np.random.default_rng(31)
+    st, n = starts_of(rows), sum(rows)
+    c = ref.random_cache(rng, 100, heads, 16, dim, lens, 60, spread=20)
+    if sum(rows) > 10:
+        long_tables(c, rows, group)
+    q, qd = rows_of(rng, n, heads * group, dim, "fp16")
+    for got, (out, _, tol, _) in both_views(mqa, c, rng, rows, group, q, qd, st, scale=1e-6, dtype="fp16"):
+        g = got.double().cpu().numpy()
+        fine, past = np.abs(out) + tol < 65504, np.abs(out) - tol >= 65520  # what rounds to fp16's infinity
+        assert fine.any() and (np.abs(g - out)[fine] <= tol[fine]).all()
+        assert np.array_equal(g[past], np.copysign(np.inf, out[past]))
+    c.ke[:] = 127
+    q, qd = rows_of(rng, n, heads * group, dim, "bf16", 200.0)  # scores of thousands
+    for got, want in both_views(mqa, c, rng, rows, group, q, qd, st):
+        check(got, None, want)
+    # values whose scales span 2^120: those within bf16's range are compared
+    c.ve[:] = rng.integers(60, 180, c.ve.shape)
+    q, qd = rows_of(rng, n, heads * group, dim, "bf16")
+    for got, (out, _, tol, _) in both_views(mqa, c, rng, rows, group, q, qd, st, scale=0.01):
+        fine = np.abs(out) < 3e38
+        assert fine.any() and (np.abs(got.double().cpu().numpy() - out)[fine] <= tol[fine]).all()
+
+
+@pytest.mark.parametrize("case", HARD, ids=str)
+def test_a_tree_over_bad_tables(mqa, case):  # noqa: F811
+    heads, group, lens, rows = case
+    rng = np.random.default_rng(32)
+    c = ref.random_cache(rng, 100, heads, 16, 64, lens, 60)
+    if sum(rows) > 10:
+        long_tables(c, rows, group)
+    st, n = starts_of(rows), sum(rows)
+    q, qd = rows_of(rng, n, heads * group, 64, "fp16")
+    mask, _ = view.tree_mask(c, st, view.random_parents(rng, rows), 2)
+    seen = view.tree_seen(c, st, mask)
+    dev = ref.to_device(c, mqa)
+    for col, bad in ((2, 1 << 30), (9, -5), (17, -2 ** 31)):
+        dev.page_table[0, col] = bad
+        seen[:rows[0]][seen[:rows[0]] // 16 == col] = -1
+    got = mqa.kv_attention(q, dev, ints(st), tree=ints(mask))
+    assert mqa.kv_status(dev) == 2
+    check(got, None, c.attention(qd, st, 0.125, "fp16", seen, causal=False))
+
+
+def test_on_streams_of_their_own(mqa):  # noqa: F811
+    """Each operator on a stream that is not the current one, outputs made there; two layers' calls at once."""
+    import torch
+    rng = np.random.default_rng(33)
+    c = ref.random_cache(rng, 60, 1, 16, 128, [400, 300], 2000)
+    rows = [40, 33]
+    st, n = starts_of(rows), sum(rows)
+    parents = view.random_parents(rng, rows)
+    want = view.tree_mask(c, st, parents, 2)
+    dev, pd, sd = ref.to_device(c, mqa), ints(parents), ints(st)
+    q, qd = rows_of(rng, n, 8, 128, "bf16")
+    counts, accepted = view.random_accepted(rng, rows)
+    cd, ad = ints(counts), ints(accepted)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    mask, pos = mqa.kv_tree_mask(dev, pd, sd, 40, stream=sides[0])
+    a = mqa.kv_attention(q, dev, sd, tree=mask, stream=sides[0])
+    b = mqa.kv_attention(q, dev, sd, window=50, sinks=1, stream=sides[1])
+    for s in sides:
+        s.synchronize()
+    assert np.array_equal(mask.cpu().numpy(), want[0]) and np.array_equal(pos.cpu().numpy(), want[1])
+    check(a, None, c.attention(qd, st, 128 ** -0.5, "bf16", view.tree_seen(c, st, want[0]), causal=False))
+    check(b, None, c.attention(qd, st, 128 ** -0.5, "bf16", view.window_seen(c, st, 50, 1)))
+    mqa.kv_accept(dev, sd, cd, ad, stream=sides[1])
+    sides[1].synchronize()
+    view.accept(c, st, counts, accepted)
+    assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+
+
+def test_results_do_not_depend_on_the_run(mqa):  # noqa: F811
+    """The same call again and again gives the same bits, whatever ran before on its workspace."""
+    import torch
+    rng = np.random.default_rng(34)
+    c = ref.random_cache(rng, 300, 2, 16, 128, [2000, 1500], 2000)
+    rows = [30, 60]
+    st, n = starts_of(rows), sum(rows)
+    q, _ = rows_of(rng, n, 8, 128, "bf16")
+    dev, sd = ref.to_device(c, mqa), ints(st)
+    mask, _ = mqa.kv_tree_mask(dev, ints(view.random_parents(rng, rows)), sd, 60)
+    ws = mqa.alloc_kv_workspace(dev, n, 8)
+    first = None
+    for i in range(20):
+        ws.random_(0, 256)
+        got = (mqa.kv_attention(q, dev, sd, tree=mask, workspace=ws), mqa.kv_attention(q, dev, sd, window=900, sinks=5,
+                                                                                       workspace=ws))
+        first = got if first is None else first
+        assert all(torch.equal(x, y) for x, y in zip(got, first)), i
