@@ -34,6 +34,13 @@ def _api():
     return m
 
 
+def _entry(*args):
+    """The C entry; loads the library at the first call."""
+    global _entry
+    _entry = _api().lib().mqa_qk_norm_rope
+    return _entry(*args)
+
+
 class _Place:
     """Where a call runs, as the cache's calls know it."""
 
@@ -64,36 +71,36 @@ def rope_turns(inv_freq, device=None):
     return torch.tensor(turns, dtype=torch.int64, device=dev)
 
 
-def _check(t, dtype, shape, where, name):
-    """A tensor [rows, heads, dim] on device `where` whose heads lie side by side in a row; its row stride."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _layout(t, dtype, shape, where, name):
+    """Row stride of a tensor [rows, heads, dim] on device `where` whose heads lie side by side in a row."""
     rows, heads, dim = shape
     across, beside, within = t.stride()
     if t.get_device() != where or (rows and heads and (within != 1 or (heads > 1 and beside != dim))):
         raise ValueError(f"{name} must be on cuda:{where} with its heads contiguous in a row")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return across if rows > 1 else heads * dim
 
 
-def _heads(t, out, weight, dtype, weight_type, where, name):
+def _no_gradient(t, name):
+    if t.requires_grad and _api()._torch().is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which qk_norm_rope does not have: detach it, or call it under "
+                         "torch.no_grad()")
+
+
+def _heads(t, shape, out, weight, dtype, weight_type, where, name):
     """The struct of q or k; its tensors checked (out is None: made by the caller)."""
-    shape = t.shape
-    if len(shape) != 3:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected (rows, heads, dim)")
-    if t.requires_grad or (weight is not None and weight.requires_grad):
-        if _api()._torch().is_grad_enabled():
-            raise ValueError(f"{name if t.requires_grad else name + '_weight'} requires a gradient, which qk_norm_rope does "
-                             "not have: detach it, or call it under torch.no_grad()")
-    heads, dim = shape[1], shape[2]
-    stride = _check(t, dtype, shape, where, name)
-    op, os = None, heads * dim
+    _no_gradient(t, name)
+    stride = _layout(t, dtype, shape, where, name)
+    _, heads, dim = shape
+    op, os, wp = None, heads * dim, None
     if out is not None:
-        os = _check(out, dtype, shape, where, name + "_out")
+        if out.shape != shape:
+            raise ValueError(f"{name}_out has shape {tuple(out.shape)}, expected {tuple(shape)}")
+        os = _layout(out, dtype, shape, where, name + "_out")
         op = out.data_ptr()
-    wp = None
     if weight is not None:
+        _no_gradient(weight, name + "_weight")
         if weight.dtype != weight_type:
             raise TypeError(f"{name}_weight must be {weight_type}, got {weight.dtype}")
         if weight.shape != (dim,) or weight.get_device() != where or not weight.is_contiguous():
@@ -125,27 +132,28 @@ def qk_norm_rope(q, k, turns, positions, q_weight=None, k_weight=None, eps: floa
     Computed in 32 bits (positions times frequencies in 64), rounded once."""
     import torch
     m, types = _api(), _types()
-    dtype, where = q.dtype, q.get_device()
+    dtype, where, qs, ks = q.dtype, q.get_device(), q.shape, k.shape
     if dtype not in types:
         raise TypeError(f"q must be bfloat16, float16 or float32, got {dtype}")
     if where < 0:
         raise ValueError("q must be a CUDA tensor")
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2] or \
-            q.shape[2] not in QK_HEAD_DIMS:
-        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)}: (rows, heads, {QK_HEAD_DIMS}) are expected")
+    if len(qs) != 3 or len(ks) != 3 or qs[0] != ks[0] or qs[2] != ks[2] or qs[2] not in QK_HEAD_DIMS:
+        raise ValueError(f"q {tuple(qs)} and k {tuple(ks)}: (rows, heads, {QK_HEAD_DIMS}) are expected")
     weight = k_weight if q_weight is None else q_weight
     weight_type = dtype if weight is None else weight.dtype
     if weight_type not in types:
         raise TypeError(f"weights must be bfloat16, float16 or float32, got {weight_type}")
-    rows, rotary, tp, pp = q.shape[0], 0, None, None
+    rotary, tp, pp = 0, None, None
     if (turns is None) != (positions is None):
         raise ValueError("turns and positions go together")
     if turns is not None:
-        rotary = 2 * turns.shape[0]
-        tp = _list(turns, torch.int64, rotary // 2, where, "turns")
-        pp = _list(positions, torch.int32, rows, where, "positions")
-    hq = _heads(q, q_out, q_weight, dtype, weight_type, where, "q")
-    hk = _heads(k, k_out, k_weight, dtype, weight_type, where, "k")
+        half = turns.shape[0]
+        rotary = 2 * half
+        tp, pp = _list(turns, torch.int64, half, where, "turns"), _list(positions, torch.int32, qs[0], where, "positions")
+        if not rotary:
+            tp = pp = None
+    hq = _heads(q, qs, q_out, q_weight, dtype, weight_type, where, "q")
+    hk = _heads(k, ks, k_out, k_weight, dtype, weight_type, where, "k")
     with _on(_Place(where), stream) as s:
         if q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -153,7 +161,8 @@ def qk_norm_rope(q, k, turns, positions, q_weight=None, k_weight=None, eps: floa
         if k_out is None:
             k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
             hk.out = k_out.data_ptr()
-        m._check(m.lib().mqa_qk_norm_rope(hq, hk, rows, types[dtype], types[weight_type], q.shape[2], rotary,
-                                          int(bool(interleaved)), int(bool(norm)), eps, tp if rotary else None,
-                                          pp if rotary else None, s), "mqa_qk_norm_rope")
+        rc = _entry(hq, hk, qs[0], types[dtype], types[weight_type], qs[2], rotary, 1 if interleaved else 0,
+                    1 if norm else 0, eps, tp, pp, s)
+    if rc:
+        m._check(rc, "mqa_qk_norm_rope")
     return q_out, k_out
