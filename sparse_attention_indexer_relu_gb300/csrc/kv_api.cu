@@ -103,7 +103,8 @@ constexpr float kMaxScale = 65536.f;
 // columns: 40 and 46 us): beside a prompt of 2,048 rows, 63 single tokens at 32K
 // positions take 0.80 ms so, and 1.90 ms with every sequence in the tiled kernel.
 // The host does not know whether there are such sequences; a call without any
-// pays the 6 us of two launches that find no work.  Nor does it know that there
+// pays for a launch that finds no work (3 us; joining is one launch for both
+// kernels).  Nor does it know that there
 // is nothing else where max_rows is missing: 32 single tokens over up to 16K
 // positions take 107 us with max_rows = 1 and 130 without (4 query heads per
 // key/value head of 128; 32 query heads: 70 and 108, as their 32 columns go to

@@ -29,9 +29,17 @@
 // inside items, for which it leaves partial results in its two workspace
 // slots, and a second kernel joins them in a fixed order.
 //
+// Windows and trees (MQA_KV_KIND) are this kernel with other limits.  A window's items
+// have the tiles of the first positions and those from its sequence's first row's
+// window on, one number of tiles for the whole sequence; a tree's rows see what
+// their masks say behind the sequence's rows.  Sub-tiles that no column sees are not
+// read, and only those that some column sees in part look at limits or masks.
+//
 // What bounds it.  Single tokens over long caches: HBM (32 sequences of 16K to
 // 64K positions, 8 key/value heads of 128: 2.68 GB in 400 us, 6.7 TB/s, 99% of
-// the measured copy rate; 323 instructions per 16 keys, issue slots 44% busy).
+// the measured copy rate; 323 instructions per 16 keys, issue slots 44% busy; 128 with
+// a window of 4,096 over up to 32K positions: 1.08 GB in 168 us, 6.4 TB/s, 95%).  One
+// token with a window of 1,024: 11.4 us in a graph, two dependent kernels' latencies.
 // More columns, or keys picked one by one: instructions and their latencies at
 // the 12 warps per SM that the accumulators leave room for (16 x 5 fp16 rows, 4
 // heads per key/value head of 64: 591 per 16 keys and 24 columns, 33 us, 1.33

@@ -37,14 +37,30 @@
 // 2,048 rows at the end of 32K positions (32 heads, 8 key/value heads of 128):
 // 735 to 745 us a pass, 1.43 to 1.45 PFLOP/s, 74% of the measured bf16 rate; fp16
 // queries, whose third term lengthens the scores' product by half, 831 us in a
-// run where bf16 took 725.  Five prompts of up to 1,531 rows: 90 us, of which 13
-// for the query terms, 5 to find the parts, 7 until the first scores are there, 9
-// to join.
+// run where bf16 took 725.  Five prompts of up to 1,531 rows: 88 us, of which 13
+// for the query terms (the parts are found meanwhile), 7 until the first scores are
+// there, 9 to join.
 //
 // Work is cut like kv_attn.cu's: the key tiles of all items in one line, even
 // parts per CTA, partial results in two slots per CTA and a joining pass.  The
 // position of a part is found from the exact number of tiles that causal
 // column blocks need (a sum of floors).
+//
+// Windows and trees (MQA_KV_KIND) are this kernel, compiled for them.  A window's block
+// has the tiles of the first positions and those between its first row's window's
+// begin and its last row's position, again a difference of sums of floors; a tree's
+// rows see every tile before the sequence's rows and their masks' bits behind.
+// Scores that a column does not see are hidden in TMEM, in the few tiles that some
+// column sees in part.  Blocks of at most 128 columns have their halves take tiles in
+// turns (in_turns).  A chunk of 2,048 rows, window 4,096, 32 and 8 heads of 128: 157
+// us, 873 TFLOP/s; a tile takes 1.6 us as in dense chunks, but a CTA has 58 of them,
+// 35 to an item, so that the start (10 us for the terms, 7 until the first scores),
+// 2.7 parts of 5 us each (last product, result, next part, first references) and 10
+// us to join are 40% of it.  Five prompts of up to 1,531 rows, window 301, fp16, heads
+// of 64: 62 us, 11 tiles in 3.3 parts per CTA.  Drafts of 16 sequences of up to 64 rows
+// after up to 32K positions: 222 us, 865 TFLOP/s, 2.7 TB/s: 3,500 cycles per tile of
+// 256 columns against 2,048 of its MMAs, where values come from HBM and the
+// converters' instructions stand in the softmax's way.
 #include "kv_ptx.cuh"
 
 #include <cfloat>
@@ -534,7 +550,10 @@ __device__ void convert_role(const AttnParams &p, Smem<D, TEST> &sm) {
   if (STAGED) {
     // Two tiles on their way into shared memory (heads of 128: where a third query term
     // would lie), each 16 bytes to a place of the thread's own, so that nobody else
-    // waits for them.
+    // waits for them.  (Drafts of 16 sequences 222 us; as TMA copies with barriers 237,
+    // and 264 where a warp of its own, whose polling holds the others up, issues them.
+    // With work counted otherwise, at the time: 258 us so, 321 with loads to registers
+    // one tile ahead, 296 with those asked for into the L2 before.)
     uint8_t *const raw[2] = {(D == 128 ? sm.q[0][2] : sm.raw[0]) + tid * 16, (D == 128 ? sm.q[1][2] : sm.raw[1]) + tid * 16};
     const uint8_t *const values = p.c.v + (r0 & 15) * D + ch * 16;
     auto fetch = [&](uint32_t no, bool on) {
