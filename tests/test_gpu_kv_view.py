@@ -612,3 +612,26 @@ def test_results_do_not_depend_on_the_run(mqa):  # noqa: F811
                                                                                        workspace=ws))
         first = got if first is None else first
         assert all(torch.equal(x, y) for x, y in zip(got, first)), i
+
+
+@pytest.mark.parametrize("case", HARD + [(1, 8, [1300], [1200])], ids=str)
+def test_values_near_the_top_of_the_range(mqa, case):  # noqa: F811
+    """Value scales of 2^118: results within bf16's range come out, also in tiles of which some keys are not needed."""
+    heads, group, lens, rows = case
+    rng = np.random.default_rng(35)
+    c = ref.random_cache(rng, 130, heads, 16, 128, lens, 90)
+    c.v[:] = ref.round_e4m3(rng.standard_normal(c.v.shape))
+    c.ve[:] = 127 + 118
+    if sum(rows) > 10:
+        long_tables(c, rows, group)
+    st, n = starts_of(rows), sum(rows)
+    q, qd = rows_of(rng, n, heads * group, 128, "bf16", 0.01)
+    pick = np.arange(n) if n < 1000 else np.unique(np.concatenate([np.arange(5), rng.integers(0, n, 20), [n - 1]]))
+    part = st if n < 1000 else np.array([0, len(pick)])
+    dev = ref.to_device(c, mqa)
+    mask, _ = view.tree_mask(c, st, view.random_parents(rng, rows), -(-max(rows) // 32))
+    for kw, seen in ((dict(tree=ints(mask)), view.tree_seen(c, st, mask)),
+                     (dict(window=100, sinks=3), view.window_seen(c, st, 100, 3)),
+                     (dict(), view.window_seen(c, st, 10 ** 6, 0))):
+        got = mqa.kv_attention(q, dev, ints(st), **kw)
+        check(got[pick], None, c.attention(qd[pick], part, 128 ** -0.5, "bf16", seen[pick], causal=False), sorted(kw))
