@@ -344,8 +344,7 @@ def kv_attention(q, cache: KVCache, row_starts, selected=None, causal: bool = Tr
     with _on(cache, stream) as s:
         if out is None:
             out = torch.empty((rows, heads, cache.head_dim), dtype=q.dtype, device=cache.device)
-        _dense(out, (q.dtype,), 3, "out", cache.device)
-        if out.shape != q.shape:
+        elif _dense(out, (q.dtype,), 3, "out", cache.device).shape != q.shape:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
         if lse is not None and tuple(_dense(lse, (torch.float32,), 2, "lse", cache.device).shape) != (rows, heads):
             raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(rows, heads)}")
