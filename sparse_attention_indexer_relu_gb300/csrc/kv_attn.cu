@@ -39,7 +39,7 @@
 // 64K positions, 8 key/value heads of 128: 2.68 GB in 400 us, 6.7 TB/s, 99% of
 // the measured copy rate; 323 instructions per 16 keys, issue slots 44% busy; 128 with
 // a window of 4,096 over up to 32K positions: 1.08 GB in 168 us, 6.4 TB/s, 95%).  One
-// token with a window of 1,024: 11.4 us in a graph, two dependent kernels' latencies.
+// token with a window of 1,024: 10.6 us in a graph, two dependent kernels' latencies.
 // More columns, or keys picked one by one: instructions and their latencies at
 // the 12 warps per SM that the accumulators leave room for (16 x 5 fp16 rows, 4
 // heads per key/value head of 64: 591 per 16 keys and 24 columns, 33 us, 1.33
@@ -187,7 +187,10 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NB>::ctas)
       total += sm.scan[w];
     }
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  // (Windows and trees: two tiles at least, for fewer parts to join.  A window of 1,024:
+  // one token 10.8 us with one, 10.6 with two, 11.0 with three and 13.9 with four, 9
+  // rows 15.1, 14.0, 14.4 and 17.5; a window of 4,096 15.0, 13.0, 13.0 and 15.5.)
+  const long long per = max((total + gridDim.x - 1) / gridDim.x, WIN || TREE ? 2LL : 1LL);
   long long at = blockIdx.x * per;
   const long long end = min(total, at + per);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);

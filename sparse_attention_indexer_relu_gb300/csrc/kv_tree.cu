@@ -137,9 +137,9 @@ __device__ __forceinline__ float step_by(int d) { return pow2i(min(max(d, -60), 
 //
 // Bound by the chain of loads bounds -> lengths -> list -> table -> scales and rows, all
 // from HBM, and for kept rows of more than a page by their order (256 sequences of up
-// to 64 rows, a third of them kept, 8 heads of 128, 15 MB moved: 19 us in a graph with
-// three copies of tables before it; a CTA per head and sequence, with a launch of its
-// own for the lengths, 23.6).
+// to 64 rows, a third of them kept, 8 heads of 128, 15 MB moved: 17 us in a graph with
+// three copies of tables before it, 19 where every row is read for its magnitude
+// first; a CTA per head and sequence, with a launch of its own for the lengths, 23.6).
 constexpr int kAcceptWarps = 16;
 constexpr int kMoved = 1024;  // rows looked up at once
 
@@ -215,8 +215,19 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) accept_kernel(const KvView 
                 }
               }
             };
+            // more rows than registers hold, behind positions that stay: where the page's
+            // scale is no less than those of all rows, it holds them
+            bool fits = false;
+            if (m > HELD && slot && was >= 7) {
+              int most = 0;
+              for (int r = lane; r < m; r += 32) {
+                const int at = src[r] >> c.page_log2;
+                if (at != page) most = max(most, (int)exps[(size_t)at * c.heads + head]);
+              }
+              fits = __all_sync(~0u, most <= was);
+            }
             int need = 0;
-            for (int r0 = 0; r0 < m; r0 += HELD) {
+            for (int r0 = 0; r0 < m && !fits; r0 += HELD) {
               load(r0);
 #pragma unroll
               for (int j = 0; j < STEPS; ++j) {
@@ -228,7 +239,7 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) accept_kernel(const KvView 
               }
             }
             need = min(max(__reduce_max_sync(~0u, need), 7), 247);
-            const int now = slot ? max(need, was) : need;
+            const int now = fits ? was : slot ? max(need, was) : need;
             uint8_t *tile = codes + (ph << c.page_log2) * D;
             if (slot && now > was) {  // earlier positions under the larger scale
               const float f = pow2i(max(was - now, -126));
