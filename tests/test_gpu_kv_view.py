@@ -272,6 +272,9 @@ ACCEPT = [  # page, heads, dim, lens, rows
     (64, 3, 64, [200, 90, 0, 64], [64, 1, 0, 64]),
     (128, 1, 128, [500, 129], [300, 129]),
     (32, 2, 64, [333] * 9, [20] * 9),
+    (16, 20, 64, [50, 21], [30, 5]),              # more heads than a CTA has warps for
+    (16, 1, 128, [3001, 5], [2500, 5]),           # more rows than are looked up at once
+    (128, 1, 64, [4000], [3900]),
 ]
 
 
@@ -280,7 +283,7 @@ ACCEPT = [  # page, heads, dim, lens, rows
 def test_accept(mqa, case, seed):  # noqa: F811
     page, heads, dim, lens, rows = case
     rng = np.random.default_rng(seed * 100 + page)
-    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 2, heads, page, dim, lens, 40, spread=1 + 3 * seed)
+    c = ref.random_cache(rng, sum(-(-n // page) for n in lens) + 2, heads, page, dim, lens, 200, spread=1 + 3 * seed)
     dev, st = ref.to_device(c, mqa), starts_of(rows)
     counts, accepted = view.random_accepted(rng, rows)
     if seed == 3:  # everything stays
