@@ -58,9 +58,9 @@
 // 2.7 parts of 5 us each (last product, result, next part, first references) and 10
 // us to join are 40% of it.  Five prompts of up to 1,531 rows, window 301, fp16, heads
 // of 64: 62 us, 11 tiles in 3.3 parts per CTA.  Drafts of 16 sequences of up to 64 rows
-// after up to 32K positions: 222 us, 865 TFLOP/s, 2.7 TB/s: 3,500 cycles per tile of
-// 256 columns against 2,048 of its MMAs, where values come from HBM and the
-// converters' instructions stand in the softmax's way.
+// after up to 32K positions: 222 us, 865 TFLOP/s, 2.7 TB/s: 3,300 cycles per tile of
+// 256 columns (the same chain as in dense chunks) and 2,150 per tile taken in turns,
+// which the converters bound.
 #include "kv_ptx.cuh"
 
 #include <cfloat>
@@ -160,8 +160,9 @@ __device__ long long tiles_before(const AttnParams &p, const Seq &q, int block) 
 
 // Windows and trees: a block of at most 128 columns has them in both halves, and the
 // halves take its tiles in turns; what a half has found of a column is added in the
-// end.  Such a tile takes two thirds of the time (drafts of 16 sequences: 2,300 cycles
-// and 3,500; with one half idle as long as the others), so work is counted in thirds.
+// end.  Such a tile takes two thirds of the time (drafts of 16 sequences: 2,150 cycles
+// and 3,300; with one half idle 2,900), so work is counted in thirds (222 us; as 1 to 2
+// 247, as 3 to 4 228).
 constexpr int kUnits = kKind == kDense ? 1 : 3, kTurnUnits = 2;  // of a tile of more columns, of one in turns
 __device__ __forceinline__ bool in_turns(int cols) { return kKind != kDense && cols <= 128; }
 __device__ __forceinline__ int block_units(const AttnParams &p, const Seq &q, int block) {
