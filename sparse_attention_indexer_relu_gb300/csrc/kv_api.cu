@@ -124,7 +124,7 @@ constexpr int kSplitCols = 16;
 constexpr long long kSplitWork = 10000000;
 constexpr int kSplitTree = 64;
 struct AttnPlan {
-  bool split, tiled;
+  bool split, tiled, many;
   int nb, ctas, tiled_ctas;
   size_t slots_off, tiled_off, cuts_off, tiled_slots_off, factor_off, terms_off, bytes;
 };
@@ -143,6 +143,9 @@ AttnPlan plan_attention(int sms, const mqa_kv_cache *c, int rows, int max_rows, 
   }
   p.tiled = !selected && cols > kTiledFrom && !little;
   p.split = !p.tiled || c->max_seqs > 1;
+  // how the tiled kernel's parts are joined: items, were all rows one sequence's, are
+  // so few that each has four parts or more
+  p.many = (long long)c->kv_heads * (((long long)rows * group + kTiledCols - 1) / kTiledCols) * 4 <= sms;
   p.nb = cols <= 8 ? 1 : cols <= 16 || p.tiled || little ? 2 : cols <= 24 ? 3 : 4;
   p.ctas = sms * attn_ctas_per_sm(p.nb, c->head_dim);
   // Room for whichever block width needs most: a workspace holds for every
@@ -255,7 +258,7 @@ int attention(const mqa_kv_cache *cache, const void *q, long long q_row_stride, 
     rc = encode_code_rows(&q_map, terms, (uint64_t)(type == MQA_KV_BF16 ? 2 : 3) * rows * q_heads, cache->head_dim, 128);
     if (rc != MQA_OK) return rc;
     rc = code(launch_tiled(kind, p, map, q_map, terms, factor, P.tiled_ctas, as_stream(stream)));
-    if (rc == MQA_OK && !P.split) rc = code(launch_kv_join_tiled(p, P.tiled_ctas, as_stream(stream)));
+    if (rc == MQA_OK && !P.split) rc = code(launch_kv_join_tiled(p, P.tiled_ctas, P.many, as_stream(stream)));
     if (rc != MQA_OK || !P.split) return rc;
   }
   const AttnParams tiled = p;
@@ -273,7 +276,7 @@ int attention(const mqa_kv_cache *cache, const void *q, long long q_row_stride, 
   }
   rc = code(launch_split(kind, p, k_map, v_map, P.nb, P.ctas, P.tiled, as_stream(stream)));
   if (rc != MQA_OK) return rc;
-  return code(P.tiled ? launch_kv_join_both(tiled, P.tiled_ctas, p, P.nb, P.ctas, as_stream(stream))
+  return code(P.tiled ? launch_kv_join_both(tiled, P.tiled_ctas, P.many, p, P.nb, P.ctas, as_stream(stream))
                       : launch_kv_join(p, P.nb, P.ctas, as_stream(stream)));
 }
 

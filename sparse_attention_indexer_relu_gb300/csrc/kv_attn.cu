@@ -863,52 +863,66 @@ __device__ __forceinline__ void join_many(const AttnParams &p, int cb, int cta) 
   finish_lane<E>(p, row, h, lane, o, mx, wx, ls);
 }
 
-// The same for the tiled kernel's items: many columns, few parts.  A warp has 4
-// columns, one part's loads of all of them in flight (9 us after 5 prompts of up
-// to 1,531 rows, latency).
-template <int D>
+// The same for the tiled kernel's items: many columns.  A warp has kFewCols columns,
+// PARTS parts' loads of all of them in flight.  Mostly there are two or three parts,
+// and registers decide (9 us after 5 prompts of up to 1,531 rows; with two in flight
+// 12).  Calls of few items are cut into many parts: 18 drafts of 141 rows x 2 heads
+// after 8K positions take 47 us with three in flight, 48 with two, 54 with four and 51
+// with one; 3 of 58 rows x 16 heads of 64 after 30K 53, 55, 51 and 64.
+constexpr int kFewCols = 4, kManyParts = 3;
+template <int D, int PARTS>
 __device__ __forceinline__ void join_few(const AttnParams &p) {
   const int4 d = p.desc[blockIdx.x];
   const int more = d.w & 0xFFFFF, ncols = d.w >> 20;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.y * 32 + warp * 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = (blockIdx.y * 8 + warp) * kFewCols;
   if (more == 0 || c0 >= ncols) return;
   constexpr int E = D / 32, CB = kTiledCols;
   constexpr size_t pitch = (size_t)CB * (D + 4);
   auto slot = [&](int i) { return p.slots + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * pitch; };
-  float mx[4], wx[4], ls[4], o[4][E];
+  float mx[kFewCols], wx[kFewCols], ls[kFewCols], o[kFewCols][E];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < kFewCols; ++k) {
     mx[k] = wx[k] = -INFINITY, ls[k] = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[k][e] = 0.f;
   }
-  for (int i = 0; i <= more; ++i) {
-    const float *s = slot(i), *t = s + (size_t)CB * D;
-    float m[4], w[4], l[4];
-    float2 v[4][E / 2];
+  for (int i0 = 0; i0 <= more; i0 += PARTS) {
+    float m[PARTS][4], w[PARTS][4], l[PARTS][4];
+    float2 v[PARTS][kFewCols][E / 2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {  // columns behind the last hold what an earlier call left: not used
-      m[k] = t[c0 + k], w[k] = t[CB + c0 + k], l[k] = t[2 * CB + c0 + k];
+    for (int b = 0; b < PARTS; ++b) {
+      if (i0 + b > more) break;
+      const float *s = slot(i0 + b), *t = s + (size_t)CB * D + c0;  // columns behind the last hold anything: not used
+      *reinterpret_cast<float4 *>(m[b]) = *reinterpret_cast<const float4 *>(t);
+      *reinterpret_cast<float4 *>(w[b]) = *reinterpret_cast<const float4 *>(t + CB);
+      *reinterpret_cast<float4 *>(l[b]) = *reinterpret_cast<const float4 *>(t + 2 * CB);
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e)
-        v[k][e] = *reinterpret_cast<const float2 *>(s + (size_t)(c0 + k) * D + lane * E + 2 * e);
+      for (int k = 0; k < kFewCols; ++k)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e)
+          v[b][k][e] = *reinterpret_cast<const float2 *>(s + (size_t)(c0 + k) * D + lane * E + 2 * e);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {  // references move as larger ones come
-      const float mn = fmaxf(mx[k], m[k]), wn = fmaxf(wx[k], w[k]);
-      const float fa = mx[k] == mn ? 1.f : ex2(mx[k] - mn), fb = m[k] == mn ? 1.f : ex2(m[k] - mn);
-      const float ga = wx[k] == wn ? 1.f : ex2(wx[k] - wn), gb = w[k] == wn ? 1.f : ex2(w[k] - wn);
-      ls[k] = ls[k] * fa + l[k] * fb;
-      mx[k] = mn, wx[k] = wn;
+    for (int b = 0; b < PARTS; ++b) {
+      if (i0 + b > more) break;
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        o[k][2 * e] = o[k][2 * e] * ga + v[k][e].x * gb;
-        o[k][2 * e + 1] = o[k][2 * e + 1] * ga + v[k][e].y * gb;
+      for (int k = 0; k < kFewCols; ++k) {  // references move as larger ones come
+        const float pm = m[b][k], pw = w[b][k], pl = l[b][k];
+        const float mn = fmaxf(mx[k], pm), wn = fmaxf(wx[k], pw);
+        const float fa = mx[k] == mn ? 1.f : ex2(mx[k] - mn), fb = pm == mn ? 1.f : ex2(pm - mn);
+        const float ga = wx[k] == wn ? 1.f : ex2(wx[k] - wn), gb = pw == wn ? 1.f : ex2(pw - wn);
+        ls[k] = ls[k] * fa + pl * fb;
+        mx[k] = mn, wx[k] = wn;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          o[k][2 * e] = o[k][2 * e] * ga + v[b][k][e].x * gb;
+          o[k][2 * e + 1] = o[k][2 * e + 1] * ga + v[b][k][e].y * gb;
+        }
       }
     }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < kFewCols; ++k) {
     const int c = d.z + c0 + k;
     if (c0 + k < ncols) finish_lane<E>(p, d.x + c / p.group, d.y * p.group + c % p.group, lane, o[k], mx[k], wx[k], ls[k]);
   }
@@ -920,18 +934,18 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnParams p, int cb
   grid_wait();
   join_many<D>(p, cb, blockIdx.x);
 }
-template <int D>
+template <int D, int PARTS>
 __global__ void __launch_bounds__(256) kv_join_few_kernel(const AttnParams p) {
   grid_wait();
-  join_few<D>(p);
+  join_few<D, PARTS>(p);
 }
 // Of a call that ran both kernels: the first `tiled` blocks of a row join the tiled
 // one's items.  (In a launch of their own the split kernel's, of which such a call may
 // have none, took 3 us more.)
-template <int D>
+template <int D, int PARTS>
 __global__ void __launch_bounds__(256) kv_join_both_kernel(const AttnParams t, const AttnParams p, int tiled, int cb) {
   grid_wait();
-  if ((int)blockIdx.x < tiled) join_few<D>(t);
+  if ((int)blockIdx.x < tiled) join_few<D, PARTS>(t);
   else join_many<D>(p, cb, blockIdx.x - tiled);
 }
 }  // namespace
@@ -942,18 +956,20 @@ cudaError_t launch_kv_join(const AttnParams &p, int nb, int ctas, cudaStream_t s
                        : launch_after(kv_join_kernel<128>, grid, 256, 0, stream, true, p, 8 * nb);
 }
 
-cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream) {
-  const dim3 grid(ctas, kTiledCols / 32);
-  return p.c.dim == 64 ? launch_after(kv_join_few_kernel<64>, grid, 256, 0, stream, true, p)
-                       : launch_after(kv_join_few_kernel<128>, grid, 256, 0, stream, true, p);
+cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, bool many, cudaStream_t stream) {
+  const dim3 grid(ctas, kTiledCols / (8 * kFewCols));
+  auto run = [&](auto *kernel) { return launch_after(kernel, grid, 256, 0, stream, true, p); };
+  if (p.c.dim == 64) return many ? run(kv_join_few_kernel<64, kManyParts>) : run(kv_join_few_kernel<64, 1>);
+  return many ? run(kv_join_few_kernel<128, kManyParts>) : run(kv_join_few_kernel<128, 1>);
 }
 
-cudaError_t launch_kv_join_both(const AttnParams &t, int tiled_ctas, const AttnParams &p, int nb, int ctas,
+cudaError_t launch_kv_join_both(const AttnParams &t, int tiled_ctas, bool many, const AttnParams &p, int nb, int ctas,
                                 cudaStream_t stream) {
-  const dim3 grid(tiled_ctas + ctas, kTiledCols / 32 > 4 * nb ? kTiledCols / 32 : 4 * nb);
-  return p.c.dim == 64
-             ? launch_after(kv_join_both_kernel<64>, grid, 256, 0, stream, true, t, p, tiled_ctas, 8 * nb)
-             : launch_after(kv_join_both_kernel<128>, grid, 256, 0, stream, true, t, p, tiled_ctas, 8 * nb);
+  constexpr int kRows = kTiledCols / (8 * kFewCols);
+  const dim3 grid(tiled_ctas + ctas, kRows > 4 * nb ? kRows : 4 * nb);
+  auto run = [&](auto *kernel) { return launch_after(kernel, grid, 256, 0, stream, true, t, p, tiled_ctas, 8 * nb); };
+  if (p.c.dim == 64) return many ? run(kv_join_both_kernel<64, kManyParts>) : run(kv_join_both_kernel<64, 1>);
+  return many ? run(kv_join_both_kernel<128, kManyParts>) : run(kv_join_both_kernel<128, 1>);
 }
 
 #endif  // MQA_KV_KIND == 0

@@ -97,8 +97,8 @@ constexpr int kQueryTerms = 3;  // e4m3 terms of an fp16 query value; a bf16 one
 template <int KIND>
 cudaError_t launch_kv_prefill(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map, uint8_t *q8,
                               float *factor, int ctas, cudaStream_t stream);
-// Its joining pass (p.desc and p.slots are the tiled kernel's).
-cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, cudaStream_t stream);
+// Its joining pass (p.desc and p.slots are the tiled kernel's).  many: an item has many parts.
+cudaError_t launch_kv_join_tiled(const AttnParams &p, int ctas, bool many, cudaStream_t stream);
 // follows: another kernel of the same call is before it on the stream.
 // k_map, v_map: codes as rows of head_dim bytes, boxes of 16 rows (not used for
 // selected keys).  KIND: kDense serves selected keys as well.
@@ -107,7 +107,7 @@ cudaError_t launch_kv_attention(const AttnParams &p, const CUtensorMap &k_map, c
                                 int ctas, bool follows, cudaStream_t stream);
 // The split kernel's joining pass, and that of a call that ran both kernels (t: the tiled one's).
 cudaError_t launch_kv_join(const AttnParams &p, int nb, int ctas, cudaStream_t stream);
-cudaError_t launch_kv_join_both(const AttnParams &t, int tiled_ctas, const AttnParams &p, int nb, int ctas,
+cudaError_t launch_kv_join_both(const AttnParams &t, int tiled_ctas, bool many, const AttnParams &p, int nb, int ctas,
                                 cudaStream_t stream);
 
 cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long long ks, long long vs, int type,
