@@ -906,17 +906,17 @@ __device__ __forceinline__ void join_few(const AttnParams &p) {
     for (int b = 0; b < PARTS; ++b) {
       if (i0 + b > more) break;
 #pragma unroll
-      for (int k = 0; k < kFewCols; ++k) {  // references move as larger ones come
+      for (int k = 0; k < kFewCols; ++k) {  // references move as larger ones come; fmaf: the same bits for any PARTS
         const float pm = m[b][k], pw = w[b][k], pl = l[b][k];
         const float mn = fmaxf(mx[k], pm), wn = fmaxf(wx[k], pw);
         const float fa = mx[k] == mn ? 1.f : ex2(mx[k] - mn), fb = pm == mn ? 1.f : ex2(pm - mn);
         const float ga = wx[k] == wn ? 1.f : ex2(wx[k] - wn), gb = pw == wn ? 1.f : ex2(pw - wn);
-        ls[k] = ls[k] * fa + pl * fb;
+        ls[k] = fmaf(ls[k], fa, pl * fb);
         mx[k] = mn, wx[k] = wn;
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
-          o[k][2 * e] = o[k][2 * e] * ga + v[b][k][e].x * gb;
-          o[k][2 * e + 1] = o[k][2 * e + 1] * ga + v[b][k][e].y * gb;
+          o[k][2 * e] = fmaf(o[k][2 * e], ga, v[b][k][e].x * gb);
+          o[k][2 * e + 1] = fmaf(o[k][2 * e + 1], ga, v[b][k][e].y * gb);
         }
       }
     }
