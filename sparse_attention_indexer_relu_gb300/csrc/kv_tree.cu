@@ -81,7 +81,7 @@ __device__ __forceinline__ Asked asked_of(const KvView &c, const int32_t *starts
   const Rows r = rows_of(starts, s, rows);
   Asked a{r.r0, r.n, 0, -1};
   if (r.n == 0) return a;
-  const int len = __ldg(c.lens + s), keep = __ldg(counts + s);
+  const int len = c.lens[s], keep = __ldg(counts + s);  // (the kernel writes lengths: an ordinary load)
   if (len < r.n || len > c.max_pages << c.page_log2) {
     if (status) atomicOr(status, MQA_KV_DEV_BAD_LENGTH);
   } else if (keep < 0 || keep > r.n) {
@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) accept_kernel(const KvView 
           }
         }
       }
-      __syncthreads();  // the table has been read
     }
+    __syncthreads();  // the length and the table have been read, by every thread
     const int now = a.first + a.keep, held = (now + c.page - 1) >> c.page_log2;
     for (int j = held + tid; j < (a.first + a.n + c.page - 1) >> c.page_log2; j += threads) {
       const int page = table[j];

@@ -309,6 +309,22 @@ def test_accept_the_first_rows(mqa):  # noqa: F811
     assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
 
 
+def test_roll_backs_of_many_sequences(mqa):  # noqa: F811
+    """Without a list, again and again: every thread reads a sequence's length before it changes."""
+    rng = np.random.default_rng(41)
+    n = 700
+    rows = rng.integers(0, 30, n)
+    c = ref.random_cache(rng, 3 * n, 1, 16, 64, rows + rng.integers(0, 12, n), 3)
+    dev, st = ref.to_device(c, mqa), starts_of(rows)
+    for _ in range(20):
+        counts = np.array([rng.integers(0, k + 1) for k in rows], np.int32)
+        mqa.kv_accept(dev, ints(st), ints(counts), rows=int(st[-1]))
+        view.accept(c, st, counts)
+        assert ref.same(c, dev) == [] and mqa.kv_status(dev) == 0
+        mqa.kv_reserve(dev, ints(rows - counts))
+        assert c.reserve(rows - counts) == 0
+
+
 def test_accept_nan_and_extreme_scales(mqa):  # noqa: F811
     """NaN codes move and set no scale; scales up to both ends of their range."""
     rng = np.random.default_rng(6)
