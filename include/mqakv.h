@@ -48,7 +48,7 @@ extern "C" {
 
 /* Device-side status bits, collected in the cache's scratch until
  * mqa_kv_get_status reads and clears them. */
-#define MQA_KV_DEV_OUT_OF_PAGES 1 /* too few free pages: the call changed nothing */
+#define MQA_KV_DEV_OUT_OF_PAGES 1 /* too few free pages: the call changed nothing (see mqa_kv_accept) */
 #define MQA_KV_DEV_BAD_INDEX 2    /* a page or sequence index outside its range was skipped */
 #define MQA_KV_DEV_BAD_LIST 4     /* a list the call refuses (see each call): it changed nothing */
 #define MQA_KV_DEV_BAD_LENGTH 8   /* a length that is negative or longer than the page table */
@@ -185,8 +185,13 @@ int mqa_kv_tree_mask(const mqa_kv_cache *cache, const int32_t *parents, const in
  * it was where earlier positions stay in the page; when it grows, those are
  * rounded again.  A sequence whose list is not ascending or leaves its rows
  * (MQA_KV_DEV_BAD_LIST), or whose length does not hold its rows
- * (MQA_KV_DEV_BAD_LENGTH), is left as it was.  Two sequences must not share a page
- * that rows move into.  Extra pools are not touched. */
+ * (MQA_KV_DEV_BAD_LENGTH), is left as it was.
+ * Shared pages (refcounts above 1 before the call) that rows move into, or in which a
+ * shortened sequence ends without filling it, are replaced in its table by copies of
+ * its own, extra pools included, as mqa_kv_fork copies a page that is not full: the
+ * lowest pages that were free before the call, by sequence, then position.  Where there are
+ * too few for all (MQA_KV_DEV_OUT_OF_PAGES), the sequences that need one are left as they
+ * were.  Apart from that extra pools are not touched: their rows do not move. */
 int mqa_kv_accept(const mqa_kv_cache *cache, const int32_t *row_starts, int rows, const int32_t *counts,
                   const int32_t *accepted, void *stream);
 

@@ -39,7 +39,7 @@ SOURCES = [("mqa_fused.cu", "mqa_fused.o", []), ("mqa_fused.cu", "mqa_fused_fold
            ("kv_tree.cu", "kv_tree.o", []), ("qk_rope.cu", "qk_rope.o", []),
            ("kv_append.cu", "kv_append.o", []), ("kv_pages.cu", "kv_pages.o", []),
            ("kv_api.cu", "kv_api.o", [])]
-HEADERS = ["mqa_internal.h", "ptx.cuh", "mqa_fold.h", "kv_internal.h", "kv_ptx.cuh"]
+HEADERS = ["mqa_internal.h", "ptx.cuh", "mqa_fold.h", "kv_internal.h", "kv_ptx.cuh", "kv_pages.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -372,7 +372,8 @@ int mqa_kv_accept(const mqa_kv_cache *cache, const int32_t *row_starts, int rows
   int sms = 0;
   rc = require_device(&sms);
   if (rc != MQA_OK) return rc;
-  return code(launch_kv_accept(view_of(cache), row_starts, counts, accepted, rows, sms, as_stream(stream)));
+  return code(launch_kv_accept(view_of(cache), lists_of(cache), pools_of(cache), row_starts, counts, accepted, rows, sms,
+                               as_stream(stream)));
 }
 
 int mqa_kv_reserve(const mqa_kv_cache *cache, const int32_t *counts, void *stream) {

@@ -31,6 +31,7 @@ enum KvWord : int {
   kKvOk = 1,      // the planned page operation goes ahead
   kKvCount = 2,   // pages to move
   kKvLive = 3,    // compact: pages in use
+  kKvTicket = 4,  // accept, 64 bits: CTAs that have planned, and the pages to copy; 0 between calls
 };
 constexpr size_t kKvHeaderBytes = 256;
 constexpr int kCompactPages = 4096;  // pages per block of the compaction's scans
@@ -115,10 +116,6 @@ cudaError_t launch_kv_append(const KvView &c, const void *k, const void *v, long
 
 cudaError_t launch_kv_tree_mask(const KvView &c, const int32_t *parents, const int32_t *starts, int rows, int32_t *mask,
                                 int words, int32_t *positions, int sms, cudaStream_t stream);
-// accepted may be null: the first counts[s] rows stay.
-cudaError_t launch_kv_accept(const KvView &c, const int32_t *starts, const int32_t *counts, const int32_t *accepted,
-                             int rows, int sms, cudaStream_t stream);
-
 struct KvPools {
   uint8_t *data[4 + MQA_KV_MAX_EXTRA];
   unsigned long long bytes[4 + MQA_KV_MAX_EXTRA];
@@ -127,6 +124,9 @@ struct KvPools {
 struct KvLists {
   int32_t *head, *src, *dst, *rank, *seq_a, *seq_b, *sums;
 };
+// accepted may be null: the first counts[s] rows stay.
+cudaError_t launch_kv_accept(const KvView &c, const KvLists &l, const KvPools &pools, const int32_t *starts,
+                             const int32_t *counts, const int32_t *accepted, int rows, int sms, cudaStream_t stream);
 cudaError_t launch_kv_reserve(const KvView &c, const KvLists &l, const int32_t *counts, cudaStream_t stream);
 cudaError_t launch_kv_fork(const KvView &c, const KvLists &l, const KvPools &pools, const int32_t *parents,
                            const int32_t *children, int n, int sms, cudaStream_t stream);

@@ -14,7 +14,7 @@
 // Order.  Free pages are taken lowest first and lists are worked in order, so
 // results do not depend on timing; refcounts change by integer atomics, whose
 // sums do not depend on order either.
-#include "kv_internal.h"
+#include "kv_pages.cuh"
 
 namespace mqa {
 
@@ -22,74 +22,6 @@ namespace {
 
 constexpr int kPlan = 1024;  // threads of a planning CTA
 constexpr int kCopy = 256;   // threads of a copying CTA
-
-// Exclusive scan of one value per thread over the CTA; returns the total.
-template <typename T>
-__device__ T block_scan(T v, T &excl, T *warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  T incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T x = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += x;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    T x = lane < warps ? warp_sums[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const T y = __shfl_up_sync(~0u, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane < warps) warp_sums[lane] = x;
-  }
-  __syncthreads();
-  excl = incl - v + (warp ? warp_sums[warp - 1] : 0);
-  return warp_sums[warps - 1];
-}
-
-// The lowest `need` free pages, ascending, into list; returns how many there
-// are (at most need).  One CTA; stops as soon as it has them.  A step looks at
-// 16K counts, with the next step's on their way, and costs one vote where none
-// is free (a page behind 2M used ones: 125 us).
-__device__ int lowest_free(const KvView &c, int need, int32_t *list, int *warp_sums) {
-  constexpr int kRun = 16, kStep = kPlan * kRun;
-  const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 32 * kRun + lane;
-  int found = 0, refs[kRun];
-  auto load = [&](int base) {
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const int page = base + first + 32 * i;
-      refs[i] = page < c.pages ? c.refs[page] : 1;
-    }
-  };
-  load(0);
-  for (int base = 0; base < c.pages && found < need; base += kStep) {
-    uint32_t free[kRun];
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      free[i] = __ballot_sync(~0u, refs[i] == 0);
-      n += __popc(free[i]);
-    }
-    load(base + kStep);
-    if (!__syncthreads_or(n)) continue;
-    int excl;
-    const int total = block_scan(lane == 0 ? n : 0, excl, warp_sums);
-    int at = found + __shfl_sync(~0u, excl, 0);  // free pages before the warp's
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const int mine = at + __popc(free[i] & ((1u << lane) - 1));
-      if ((free[i] >> lane & 1) && mine < need) list[mine] = base + first + 32 * i;
-      at += __popc(free[i]);
-    }
-    found += total;
-  }
-  __syncthreads();
-  return min(found, need);
-}
 
 __device__ __forceinline__ int pages_of(const KvView &c, int len) { return (len + c.page - 1) >> c.page_log2; }
 // A length the table can hold; false (and 0) otherwise.
@@ -161,7 +93,7 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const KvView c, const Kv
   __syncthreads();
   if (bad == 0 && total > c.pages && threadIdx.x == 0) bad = MQA_KV_DEV_OUT_OF_PAGES;
   __syncthreads();
-  if (bad == 0 && lowest_free(c, (int)total, l.dst, sums) < total && threadIdx.x == 0) bad = MQA_KV_DEV_OUT_OF_PAGES;
+  if (bad == 0 && lowest_free<kPlan>(c, (int)total, l.dst, sums) < total && threadIdx.x == 0) bad = MQA_KV_DEV_OUT_OF_PAGES;
   __syncthreads();
   if (bad) {
     if (threadIdx.x == 0) atomicOr(c.status, bad);
@@ -223,7 +155,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const KvView c, const 
     total += sum;
   }
   __syncthreads();
-  if (bad == 0 && lowest_free(c, total, l.dst, sums) < total && threadIdx.x == 0) bad = MQA_KV_DEV_OUT_OF_PAGES;
+  if (bad == 0 && lowest_free<kPlan>(c, total, l.dst, sums) < total && threadIdx.x == 0) bad = MQA_KV_DEV_OUT_OF_PAGES;
   __syncthreads();
   if (threadIdx.x == 0) {
     l.head[kKvOk] = bad == 0;
@@ -276,12 +208,8 @@ __global__ void __launch_bounds__(kCopy) free_kernel(const KvView c, const int32
   for (int j = threadIdx.x; j < pages_of(c, len); j += kCopy) {
     const int page = row[j];
     row[j] = -1;
-    if ((unsigned)page >= (unsigned)c.pages) {
-      atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
-    } else if (atomicSub(c.refs + page, 1) <= 0) {  // not in use: the count stays
-      atomicAdd(c.refs + page, 1);
-      atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
-    }
+    if ((unsigned)page < (unsigned)c.pages) drop_page(c, page);
+    else atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
   }
 }
 

@@ -1,6 +1,7 @@
 // Drafted tokens over the paged 8-bit cache (include/mqakv.h): the masks and
 // positions of a tree of drafts (mqa_kv_tree_mask), and taking over the accepted
 // ones (mqa_kv_accept).
+#include "kv_pages.cuh"
 #include "kv_ptx.cuh"
 
 #include <algorithm>
@@ -92,10 +93,30 @@ __device__ __forceinline__ Asked asked_of(const KvView &c, const int32_t *starts
   }
   return a;
 }
-// Whether entry i of a sequence's list is where it may be: ascending rows.
-__device__ __forceinline__ bool entry_ok(const int32_t *list, int i, int n) {
-  const int at = __ldg(list + i);
-  return at < n && at > (i ? __ldg(list + i - 1) : -1);
+// A thread's entry of a sequence's list and the one before it, asked for beside the length
+// and the count (entries behind the kept ones are rows of the sequence as well).
+struct Entry {
+  int at, prev;
+};
+__device__ __forceinline__ Entry entry_of(const int32_t *starts, const int32_t *accepted, int s, int rows) {
+  const Rows r = rows_of(starts, s, rows);
+  const int32_t *at = accepted + r.r0 + threadIdx.x;
+  const bool on = accepted && (int)threadIdx.x < r.n;
+  return {on ? __ldg(at) : 0, on && threadIdx.x > 0 ? __ldg(at - 1) : -1};
+}
+// How many of a sequence's kept rows are where they belong (the first ones); -1, and bad, where
+// the list does not ascend within the sequence's rows.  By the CTA.
+__device__ __forceinline__ int settled(const Asked &a, const int32_t *accepted, Entry e, int threads, bool &bad) {
+  if (!accepted) return a.keep;
+  int stay = 0;
+  bool odd = false;
+  for (int i = threadIdx.x; i - (int)threadIdx.x < a.keep; i += threads) {
+    if (i >= threads && i < a.keep) e = {__ldg(accepted + a.r0 + i), __ldg(accepted + a.r0 + i - 1)};
+    odd |= i < a.keep && (e.at >= a.n || e.at <= e.prev || e.at < 0);
+    stay += __syncthreads_count(i < a.keep && e.at == i);
+  }
+  bad = __syncthreads_or(odd);
+  return bad ? -1 : stay;
 }
 
 __device__ __forceinline__ float from_e4m3(uint32_t code) {
@@ -124,9 +145,144 @@ __device__ __forceinline__ uint4 scaled(uint4 v, float f) {
 // 2^d, of as much of d as matters for a product with a code.
 __device__ __forceinline__ float step_by(int d) { return pow2i(min(max(d, -60), 60)); }
 
-// A CTA has a sequence (of a few, those that have rows): it looks up where its kept
-// rows come from and go to, a warp moves a head's keys or values, and then the length
-// and the pages behind it follow.
+// ---- plan
+// What a call does is decided before anything changes, for what one sequence gives back
+// another may look at: lists are checked, and pages that rows move into, or in which a
+// shortened sequence ends without filling it, are the sequence's own afterwards.  Where
+// such a page is shared (its count is above 1) the sequence gets a copy, as kv_fork makes
+// of a page that is not full; otherwise appending would write over the others' positions.
+//
+// A CTA per sequence (of a few, those that have rows) leaves in seq_a how many of its
+// rows are where they belong (-1: the sequence is left alone) and in seq_b the number
+// of pages to copy (-1: none).  The CTA that is done last deals free pages out, lowest first, by
+// sequence, then position, which seldom is needed: src, dst and rank then hold the pairs and the
+// places in the table, a sequence's from seq_b on, the sign bit marking its last.
+constexpr int kAcceptPlan = 128;
+
+// The places in the table of pages that are to be the sequence's own: [lo, hi).
+struct Own {
+  int lo, hi;
+};
+__device__ __forceinline__ Own own_of(const KvView &c, const Asked &a, int stay) {
+  const int now = a.first + a.keep, end = (now + c.page - 1) >> c.page_log2;
+  if (a.keep == a.n) return {end, end};  // nothing changes
+  if (stay < a.keep) return {(a.first + stay) >> c.page_log2, end};
+  return {now >> c.page_log2, end};  // empty where the last page is full
+}
+__device__ __forceinline__ bool shared(const KvView &c, int page) {
+  return (unsigned)page < (unsigned)c.pages && c.refs[page] > 1;
+}
+
+__device__ __noinline__ void deal_pages(const KvView &c, const KvLists &l, const int32_t *starts, const int32_t *counts,
+                                        int rows, int need, int *sums) {
+  const bool enough = need <= c.pages && lowest_free<kAcceptPlan>(c, need, l.dst, sums) == need;
+  if (!enough && threadIdx.x == 0) atomicOr(c.status, MQA_KV_DEV_OUT_OF_PAGES);
+  int total = 0;
+  for (int base = 0; base < c.seqs; base += kAcceptPlan) {
+    const int s = base + threadIdx.x;
+    const int n = s < c.seqs && rows_of(starts, s, rows).n > 0 ? max(__ldcg(l.seq_b + s), 0) : 0;
+    int excl;
+    const int sum = block_scan(n, excl, sums);
+    if (n > 0 && enough) {
+      const Own own = own_of(c, asked_of(c, starts, counts, s, rows, nullptr), __ldcg(l.seq_a + s));
+      const int32_t *table = c.table + (size_t)s * c.max_pages;
+      int k = total + excl;
+      for (int j = own.lo; j < own.hi; ++j)
+        if (shared(c, table[j])) l.src[k] = table[j], l.rank[k++] = j;
+      l.rank[k - 1] |= INT32_MIN;
+      l.seq_b[s] = k - n;
+    } else if (n > 0) {
+      l.seq_a[s] = l.seq_b[s] = -1;
+    }
+    total += sum;
+  }
+  __syncthreads();  // the counts have been read
+  if (!enough) return;
+  for (int s = threadIdx.x; s < c.seqs; s += kAcceptPlan) {
+    int k = rows_of(starts, s, rows).n > 0 ? __ldcg(l.seq_b + s) : -1;
+    for (bool more = k >= 0; more; ++k) {
+      more = l.rank[k] >= 0;
+      c.table[(size_t)s * c.max_pages + (l.rank[k] & INT32_MAX)] = l.dst[k];
+      c.refs[l.dst[k]] = 1;
+      drop_page(c, l.src[k]);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kAcceptPlan) accept_plan_kernel(const KvView c, const KvLists l,
+                                                                  const int32_t *__restrict__ starts,
+                                                                  const int32_t *__restrict__ counts,
+                                                                  const int32_t *__restrict__ accepted, int rows, int per) {
+  grid_dependents();
+  __shared__ int sums[32], s_need;
+  const int tid = threadIdx.x, lane = tid & 31, s0 = blockIdx.x * per;
+  bool on = false;
+  int need = 0;  // pages to copy
+  if (lane < per && s0 + lane < c.seqs) on = rows_of(starts, s0 + lane, rows).n > 0;
+  for (uint32_t left = __ballot_sync(~0u, on); left; left &= left - 1) {
+    const int s = s0 + __ffs(left) - 1;
+    const Entry entry = entry_of(starts, accepted, s, rows);
+    const Asked a = asked_of(c, starts, counts, s, rows, tid == 0 ? c.status : nullptr);
+    const int32_t *table = c.table + (size_t)s * c.max_pages;
+    // the first pages' counts are on their way while the list is checked
+    const int at = (a.first >> c.page_log2) + tid;
+    const bool is_shared = a.keep >= 0 && at << c.page_log2 < a.first + a.n && shared(c, table[at]);
+    bool bad = false;
+    const int stay = a.keep < 0 ? -1 : settled(a, accepted, entry, kAcceptPlan, bad);
+    int pages = 0;
+    if (bad) {
+      if (tid == 0) atomicOr(c.status, MQA_KV_DEV_BAD_LIST);
+    } else if (a.keep >= 0) {
+      const Own own = own_of(c, a, stay);
+      pages = __syncthreads_count(is_shared && at >= own.lo && at < own.hi);
+      for (int j = max(own.lo, at - tid + kAcceptPlan) + tid; j - tid < own.hi; j += kAcceptPlan)
+        pages += __syncthreads_count(j < own.hi && shared(c, table[j]));
+    }
+    if (tid == 0) {
+      l.seq_a[s] = stay;
+      l.seq_b[s] = pages ? pages : -1;
+    }
+    need += pages;
+  }
+  if (gridDim.x > 1) {  // the one that comes last learns the sum
+    if (tid == 0) {
+      unsigned long long *const ticket = reinterpret_cast<unsigned long long *>(l.head + kKvTicket);
+      if (need) __threadfence();
+      const unsigned long long was = atomicAdd(ticket, (unsigned long long)need << 32 | 1);
+      s_need = 0;
+      if ((uint32_t)was == gridDim.x - 1) {
+        *ticket = 0;
+        s_need = (int)(was >> 32) + need;
+        if (s_need) __threadfence();
+      }
+    }
+    __syncthreads();
+    need = s_need;
+  } else {
+    __syncthreads();
+  }
+  if (need) deal_pages(c, l, starts, counts, rows, need, sums);
+}
+
+// ---- moving
+// Contents of a page, by the CTA.
+__device__ __noinline__ void copy_page(const KvPools &p, int from, int to) {
+  for (int i = 0; i < p.n; ++i) {
+    const unsigned long long size = p.bytes[i];
+    const uint8_t *s = p.data[i] + (unsigned long long)from * size;
+    uint8_t *d = p.data[i] + (unsigned long long)to * size;
+    if (((reinterpret_cast<uintptr_t>(s) | reinterpret_cast<uintptr_t>(d) | size) & 15) == 0) {
+      for (unsigned long long x = threadIdx.x; x < size / 16; x += blockDim.x)
+        reinterpret_cast<uint4 *>(d)[x] = reinterpret_cast<const uint4 *>(s)[x];
+    } else {
+      for (unsigned long long x = threadIdx.x; x < size; x += blockDim.x) d[x] = s[x];
+    }
+  }
+}
+
+// A CTA has a sequence (of a few, those that have rows): it makes the copies that the
+// plan names, looks up where its kept rows come from and go to, a warp moves a head's
+// keys or values, and then the length and the pages behind it follow.
 //
 // A warp goes over the pages that rows move into, in order.  A page's scale depends on
 // all that moves into it, so its rows are read for their largest magnitude first; few
@@ -135,16 +291,18 @@ __device__ __forceinline__ float step_by(int d) { return pow2i(min(max(d, -60), 
 // order, so that what is written at any time lies before all sources still to be read,
 // and the scales of pages behind this one have not changed yet.
 //
-// Bound by the chain of loads bounds -> lengths -> list -> table -> scales and rows, all
+// Bound by the chain of loads bounds -> lengths, list -> table -> scales and rows, all
 // from HBM, and for kept rows of more than a page by their order (256 sequences of up
-// to 64 rows, a third of them kept, 8 heads of 128, 15 MB moved: 17 us in a graph with
-// three copies of tables before it, 19 where every row is read for its magnitude
-// first; a CTA per head and sequence, with a launch of its own for the lengths, 23.6).
+// to 64 rows, a third of them kept, 8 heads of 128, 15 MB moved: 20 us in a graph with
+// three copies of tables before it, 13 rows of one sequence 9.2; of it 3.0 and 2.3 for the
+// plan's kernel, beside which this one looks its places up; 21.3 and 10.4 where it waits
+// for the plan first).
 constexpr int kAcceptWarps = 16;
 constexpr int kMoved = 1024;  // rows looked up at once
 
 template <int D>
-__global__ void __launch_bounds__(32 * kAcceptWarps) accept_kernel(const KvView c, const int32_t *__restrict__ starts,
+__global__ void __launch_bounds__(32 * kAcceptWarps) accept_kernel(const KvView c, const KvLists l, const KvPools pools,
+                                                                   const int32_t *__restrict__ starts,
                                                                    const int32_t *__restrict__ counts,
                                                                    const int32_t *__restrict__ accepted, int rows,
                                                                    int per) {
@@ -154,36 +312,46 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) accept_kernel(const KvView 
   const int s0 = blockIdx.x * per;
   bool on = false;
   if (lane < per && s0 + lane < c.seqs) on = rows_of(starts, s0 + lane, rows).n > 0;
+  bool planned = false;
+  // What is only looked up does not wait for the plan.
   for (uint32_t left = __ballot_sync(~0u, on); left; left &= left - 1) {
     const int s = s0 + __ffs(left) - 1;
-    const Asked a = asked_of(c, starts, counts, s, rows, tid == 0 ? c.status : nullptr);
-    if (a.keep < 0) continue;
+    const Entry entry = entry_of(starts, accepted, s, rows);
+    const Asked a = asked_of(c, starts, counts, s, rows, nullptr);
+    bool bad = false;
+    const int stay = a.keep < 0 ? -1 : settled(a, accepted, entry, threads, bad);
+    if (stay < 0) continue;
     const int32_t *list = accepted + a.r0;
     int32_t *table = c.table + (size_t)s * c.max_pages;
-    if (accepted) {
-      bool bad = false;
-      int stay = 0;  // rows that are where they belong: the first ones
-      for (int i0 = 0; i0 < a.keep; i0 += threads) {
-        const int i = i0 + tid;
-        if (i < a.keep) bad |= !entry_ok(list, i, a.n);
-        stay += __syncthreads_count(i < a.keep && __ldg(list + i) == i);
+    // Places of the kept rows from `from` on; those looked up at once end with a page's last one.
+    auto look_up = [&](int from) {
+      const int begin = a.first + from, to = min(a.keep, ((begin + kMoved) & ~(c.page - 1)) - a.first);
+      for (int i = tid; i < to - from; i += threads) {
+        const int pos = a.first + __ldg(list + from + i), page = __ldcg(table + (pos >> c.page_log2));
+        s_src[i] = (unsigned)page < (unsigned)c.pages ? (page << c.page_log2) + (pos & (c.page - 1)) : -1;
       }
-      if (__syncthreads_or(bad)) {
-        if (tid == 0) atomicOr(c.status, MQA_KV_DEV_BAD_LIST);
-        continue;
+      const int pages = ((a.first + to - 1) >> c.page_log2) - (begin >> c.page_log2) + 1;
+      for (int i = tid; i < pages; i += threads) s_dst[i] = __ldcg(table + (begin >> c.page_log2) + i);
+      __syncthreads();
+      return to;
+    };
+    const bool moves = stay < a.keep;
+    int to = 0;
+    if (moves) to = look_up(stay);
+    if (!planned) grid_wait();
+    planned = true;
+    if (__ldcg(l.seq_a + s) < 0) continue;  // too few pages
+    int pair = __ldcg(l.seq_b + s);
+    if (pair >= 0) {
+      for (bool more = true; more; ++pair) {
+        more = __ldcg(l.rank + pair) >= 0;
+        copy_page(pools, __ldcg(l.src + pair), __ldcg(l.dst + pair));
       }
-      // rows looked up at once end with a page's last one
-      for (int from = stay, to; from < a.keep; from = to) {
-        const int begin = a.first + from;
-        to = min(a.keep, ((begin + kMoved) & ~(c.page - 1)) - a.first);
-        __syncthreads();  // the last ones' readers are done
-        for (int i = tid; i < to - from; i += threads) {
-          const int pos = a.first + __ldg(list + from + i), page = table[pos >> c.page_log2];
-          s_src[i] = (unsigned)page < (unsigned)c.pages ? (page << c.page_log2) + (pos & (c.page - 1)) : -1;
-        }
-        const int pages = ((a.first + to - 1) >> c.page_log2) - (begin >> c.page_log2) + 1;
-        for (int i = tid; i < pages; i += threads) s_dst[i] = table[(begin >> c.page_log2) + i];
-        __syncthreads();
+      __syncthreads();
+      if (moves) look_up(stay);  // anew, in the copies
+    }
+    if (moves) {
+      for (int from = stay;;) {
         for (int item = warp; item < 2 * c.heads; item += warps) {
           const int head = item >> 1;
           uint8_t *codes = item & 1 ? c.v : c.k, *exps = item & 1 ? c.v_exps : c.k_exps;
@@ -264,22 +432,23 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) accept_kernel(const KvView 
             if (lane == 0) exps[ph] = (uint8_t)now;
           }
         }
+        if (to == a.keep) break;
+        __syncthreads();  // the places have been read
+        from = to;
+        to = look_up(from);
       }
     }
-    __syncthreads();  // the length and the table have been read, by every thread
+    __syncthreads();  // the length, the table and the places have been read, by every thread
     const int now = a.first + a.keep, held = (now + c.page - 1) >> c.page_log2;
     for (int j = held + tid; j < (a.first + a.n + c.page - 1) >> c.page_log2; j += threads) {
       const int page = table[j];
       table[j] = -1;
-      if ((unsigned)page >= (unsigned)c.pages) {
-        atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
-      } else if (atomicSub(c.refs + page, 1) <= 0) {  // not in use: the count stays
-        atomicAdd(c.refs + page, 1);
-        atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
-      }
+      if ((unsigned)page < (unsigned)c.pages) drop_page(c, page);
+      else atomicOr(c.status, MQA_KV_DEV_BAD_INDEX);
     }
     if (tid == 0) c.lens[s] = now;
   }
+  if (!planned) grid_wait();
 }
 
 }  // namespace
@@ -296,15 +465,17 @@ cudaError_t launch_kv_tree_mask(const KvView &c, const int32_t *parents, const i
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv_accept(const KvView &c, const int32_t *starts, const int32_t *counts, const int32_t *accepted,
-                             int rows, int sms, cudaStream_t stream) {
-  const int warps = accepted ? std::min(2 * c.heads, kAcceptWarps) : 1, per = sequences_per_cta(c, sms);
+cudaError_t launch_kv_accept(const KvView &c, const KvLists &l, const KvPools &pools, const int32_t *starts,
+                             const int32_t *counts, const int32_t *accepted, int rows, int sms, cudaStream_t stream) {
+  const int warps = accepted ? std::min(2 * c.heads, kAcceptWarps) : 4, per = sequences_per_cta(c, sms);
   const int ctas = (c.seqs + per - 1) / per;
-  if (c.dim == 64)
-    accept_kernel<64><<<ctas, 32 * warps, 0, stream>>>(c, starts, counts, accepted, rows, per);
-  else
-    accept_kernel<128><<<ctas, 32 * warps, 0, stream>>>(c, starts, counts, accepted, rows, per);
-  return cudaGetLastError();
+  cudaError_t e = launch_after(accept_plan_kernel, dim3(ctas), kAcceptPlan, 0, stream, false, c, l, starts, counts, accepted,
+                               rows, per);
+  if (e != cudaSuccess) return e;
+  auto run = [&](auto *kernel) {
+    return launch_after(kernel, dim3(ctas), 32 * warps, 0, stream, true, c, l, pools, starts, counts, accepted, rows, per);
+  };
+  return c.dim == 64 ? run(accept_kernel<64>) : run(accept_kernel<128>);
 }
 
 }  // namespace mqa

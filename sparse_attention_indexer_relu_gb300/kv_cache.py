@@ -401,7 +401,11 @@ def kv_accept(cache: KVCache, row_starts, counts, accepted=None, rows: Optional[
     sequence gets shorter, pages that it no longer needs become free.
 
     accepted [rows] int32: entry row_starts[s] + i, i < counts[s], is the number among the sequence's rows of the one
-    that becomes its i-th, ascending; without it the first ones stay, and `rows` says how many there are in all."""
+    that becomes its i-th, ascending; without it the first ones stay, and `rows` says how many there are in all.
+
+    Pages that a fork shares and that rows move into, or in which the shorter sequence ends without filling it, become
+    the sequence's own (copies in free pages, `extra` pools included); too few free pages leave the sequences that need
+    one as they were.  `extra` pools hold per-position data at their old places otherwise: rows do not move there."""
     m = _api()
     ap = None
     if accepted is not None:
