@@ -957,7 +957,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm) {
       }
       continue;
     }
-    float m = -INFINITY, wr = -INFINITY, l = 0.f, cs = 0.f;
+    float m = col < ncols ? -INFINITY : 0.f, wr = -INFINITY, l = 0.f, cs = 0.f;  // (others ask for no references)
     int room0 = 0;  // keys that the column sees from the part's first tile on
     if (col < ncols) {
       const int c = w.x.block * kCols + col;
@@ -1002,10 +1002,9 @@ __device__ void softmax_role(const AttnParams &p, Smem<D, TEST> &sm) {
       // again with new references: its scores are still in TMEM then.  The first
       // tile has its references set first.
       const bool look = meta.spread > kFar - 16.f;
-      // (Columns of a window or tree may see nothing of it and of more tiles behind it;
-      // theirs are set in the tile of the first key that they see.)
-      for (bool anew = t == begin || (kKind != kDense && (edge || t < from + step) &&
-                                      __any_sync(~0u, m == -INFINITY && col < ncols));; anew = true) {
+      // Columns may see nothing of it and of more tiles behind it (windows, trees, pages outside
+      // the pool): while one of the warp has no references, each tile has them set first.
+      for (bool anew = __any_sync(~0u, m == -INFINITY && l == 0.f);; anew = true) {
         if (anew) settle<D>(ts, to, meta, cs, t > begin, m, wr, l);
         if (look && __any_sync(~0u, wr - meta.lv_min - m > kFar)) {
           if (!anew) continue;

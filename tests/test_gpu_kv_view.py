@@ -654,3 +654,53 @@ def test_values_near_the_top_of_the_range(mqa, case):  # noqa: F811
                      (dict(), view.window_seen(c, st, 10 ** 6, 0))):
         got = mqa.kv_attention(q, dev, ints(st), **kw)
         check(got[pick], None, c.attention(qd[pick], part, 128 ** -0.5, "bf16", seen[pick], causal=False), sorted(kw))
+
+
+# ---------------------------------------------------------------- pages outside the pool, whole tiles of them
+OUTSIDE = [  # what rows see, heads, group, lens, rows: in the tiled kernel parts of several tiles, in both forms
+    ("split", 1, 8, [1500, 700], [3, 1]), ("dense", 1, 8, [2600, 900], [700, 20]), ("all", 8, 8, [1700, 700], [130, 77]),
+    ("window", 1, 8, [2600, 1500], [1200, 900]), ("tree", 32, 4, [3000, 700], [30, 25]),
+    ("tree", 8, 8, [2900, 900], [60, 31])]
+
+
+@pytest.mark.parametrize("size", ["large", "small", "low"])
+@pytest.mark.parametrize("page,dim", [(16, 128), (128, 64)])
+@pytest.mark.parametrize("kind,heads,group,lens,rows", OUTSIDE, ids=str)
+def test_tiles_of_pages_outside_the_pool(mqa, kind, heads, group, lens, rows, page, dim, size):  # noqa: F811
+    """Runs of 128 and 256 positions in pages outside the pool, the first ones among them, so that parts begin with tiles
+    in which nothing is seen; in the tiled kernel as in the split one they count as not seen.  size: of the scores; low:
+    about -270 in powers of two, whose weights vanish unless the references follow."""
+    import torch
+    rng = np.random.default_rng(page + dim + len(kind))
+    n, st = sum(rows), starts_of(rows)
+    c = ref.random_cache(rng, sum(-(-k // page) for k in lens) + 2, heads, page, dim, lens, 4096 // page)
+    q, _ = rows_of(rng, n, heads * group, dim, "bf16", 1.5 if size == "large" else 0.003)
+    scale = dim ** -0.5
+    if size == "low":
+        c.k[:], c.ke[:], scale = 56, 127, 1.0  # keys of 1
+        q = (q - 187.0 / dim).to(torch.bfloat16)
+    qd = q.double().cpu().numpy()
+    pick = np.unique(np.concatenate([rng.integers(0, n, 16 if heads == 1 else 2), [0, n - 1, rows[0] - 1, rows[0]]]))
+    part = np.array([0, (pick < rows[0]).sum(), len(pick)])
+    if kind == "tree":
+        long_tables(c, rows, group)
+        mask, _ = view.tree_mask(c, st, view.random_parents(rng, rows), 2)
+        kw, seen = dict(tree=ints(mask)), view.tree_seen(c, st, mask)
+    elif kind == "window":
+        assert n * group * max(rows) > LITTLE
+        kw, seen = dict(window=400), view.window_seen(c, st, 400, 0)
+    elif kind == "all":
+        kw, seen = dict(causal=False), np.stack([np.where(np.arange(max(lens)) < lens[s], np.arange(max(lens)), -1)
+                                                 for s, _ in enumerate(rows) for _ in range(rows[s])])
+    else:
+        kw, seen = dict(max_rows=1 if kind == "split" else None), view.window_seen(c, st, 10 ** 6, 0)
+    for bad in (lambda t: (t >= 0) & (t < 256), lambda t: (t >= 0) & (t // 128 % 3 != 2)):
+        dev = ref.to_device(c, mqa)
+        at = np.arange(c.table.shape[1]) * page
+        for s, k in enumerate(lens):
+            dev.page_table[s, torch.from_numpy((at < k) & bad(at)).cuda()] = (1 << 30) - 3 * s
+        sees = np.where(bad(seen), -1, seen)[pick]
+        lse = torch.zeros((n, heads * group), device="cuda")
+        got = mqa.kv_attention(q, dev, ints(st), lse=lse, scale=scale, **kw)
+        assert mqa.kv_status(dev) == 2
+        check(got[pick], lse[pick], c.attention(qd[pick], part, scale, "bf16", sees, causal=False), kind)
