@@ -6,11 +6,12 @@
 // wrap is the angle's, so the fraction is exact whatever the position; its upper
 // 32 bits become the argument of sincospi.
 //
-// With the weights taken in, a pair (a, b) becomes
-//     r (w_a cos a - w_b sin b),  r (w_b cos b + w_a sin a),   r = rsqrt(...):
+// With r = rsqrt(...) and the weights taken in, a pair (a, b) becomes
+//     (w_a cos) (r a) - (w_b sin) (r b),  (w_b cos) (r b) + (w_a sin) (r a):
 // the four factors belong to the row, so they are formed once for all heads that a
-// warp takes of it, and a component costs an unpacking, a square, and a product, a
-// fused product and a product by r, two components to an instruction.
+// warp takes of it, and a component costs an unpacking, a square, a product by r, a product
+// and a fused product, two components to an instruction.  (r first: |r a| is at most
+// sqrt(D), so nothing leaves fp32's range that the answer does not.)
 //
 // Split.  A head is D / 8 lanes with four pairs each (of those that are not turned,
 // any two components make a pair), a step of a warp 32 / (D / 8) heads of a row.  A warp
@@ -20,7 +21,7 @@
 //
 // What bounds it.  HBM: each component is read once and written once.  16,384 rows of
 // 32 and 8 heads of 128 in bf16: 336 MB in 58.5 us, 5.74 TB/s, 85% of the measured copy
-// rate; fp32, 8,192 rows: 5.96 TB/s.  Rows of few heads are bound by what a row costs
+// rate; fp32, 8,192 rows: 5.9 TB/s.  Rows of few heads are bound by what a row costs
 // by itself (its angles and factors: 60,000 rows of 2 and 1 heads of 128, 92 MB, 53 us;
 // several rows to a warp: 59).  A kernel in which every head fetched its cosines from
 // shared memory took 113 us (256 instructions per step of two heads, now 113).
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_kernel(const QkParams p) {
   }
   __syncthreads();
   auto work = [&](const mqa_qk_heads &h, const Run &r) {
-    uint64_t ca[2], sa[2], cb[2], sb[2];  // a' = r (ca a + sa b), b' = r (cb b + sb a)
+    uint64_t ca[2], sa[2], cb[2], sb[2];  // a' = ca (r a) + sa (r b), b' = cb (r b) + sb (r a)
     {
       float u[4], v[4], c[4], s[4];
       uint64_t wa[2], wb[2];
@@ -265,10 +266,11 @@ __global__ void __launch_bounds__(kThreads, 6) qk_kernel(const QkParams p) {
         float e[4], g[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+          a[j] = mul2(a[j], pack2(f, f)), b[j] = mul2(b[j], pack2(f, f));
           uint64_t aa = mul2(ca[j], a[j]), bb = mul2(cb[j], b[j]);
           if (turned) aa = fma2(sa[j], b[j], aa), bb = fma2(sb[j], a[j], bb);
-          unpack2(mul2(aa, pack2(f, f)), e[2 * j], e[2 * j + 1]);
-          unpack2(mul2(bb, pack2(f, f)), g[2 * j], g[2 * j + 1]);
+          unpack2(aa, e[2 * j], e[2 * j + 1]);
+          unpack2(bb, g[2 * j], g[2 * j + 1]);
         }
         if (step + i < r.mine) {
           char *out = r.out + (size_t)(step + i) * STEP;

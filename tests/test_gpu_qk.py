@@ -152,3 +152,21 @@ def test_rows_past_32_bits(mqa):
     q, k = mqa.qk_norm_rope(x[:, :n], x[:, n:n + 1], turns, pos)
     few = mqa.qk_norm_rope(x[-3:, :n], x[-3:, n:n + 1], turns, pos[-3:])
     assert torch.equal(q[-3:], few[0]) and torch.equal(k[-3:], few[1]) and not q[:-3].any() and few[0].any()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("scale,weight", [(1e18, 1e21), (1e-25, 1e-20), (1.0, 1e37), (1e12, 1e-37)])
+def test_weights_whose_products_with_rows_leave_the_range(mqa, dtype, scale, weight):
+    """The norm's answer times the weight stays in fp32's range although row times weight does not."""
+    import torch
+    rng = np.random.default_rng(3)
+    t = getattr(torch, dtype)
+    q = (torch.from_numpy(rng.standard_normal((9, 6, 64))) * scale).to(t).cuda()
+    k = q[:, :2].clone()
+    w = [(torch.from_numpy(1 + 0.3 * rng.random(64)) * weight).to(t).cuda() for _ in range(2)]
+    inv, pos = 10000.0 ** (-np.arange(0, 64, 2) / 64), np.arange(9) * 100
+    turns, positions = mqa.rope_turns(torch.from_numpy(inv)), torch.from_numpy(pos.astype(np.int32)).cuda()
+    got = mqa.qk_norm_rope(q, k, turns, positions, *w, eps=0.0)
+    for x, y, v in zip((q, k), got, w):
+        out, tol = plain(x.double().cpu().numpy(), v.double().cpu().numpy(), 0.0, True, inv, pos, False, dtype)
+        assert np.abs(out).max() < 1e39 and (np.abs(y.double().cpu().numpy() - out) <= tol).all()
