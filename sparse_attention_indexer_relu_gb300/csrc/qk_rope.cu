@@ -163,6 +163,7 @@ __device__ __noinline__ float2 rescued(uint64_t f0, uint64_t f1, uint64_t g0, ui
 #pragma unroll
   for (int i = 0; i < 2; ++i) a[i] = mul2(f[i], pack2(down, down)), b[i] = mul2(f[2 + i], pack2(down, down));
   const float s = sum_lanes<LPH>(square_sum(a, b));
+  if (odd && amax == 0.f && eps > 0.f) return make_float2(1.f, 0.f);  // (rsqrt reads the least eps as zero)
   return make_float2(down, able ? rsqrt_of(s * (1.f / D) + eps * down * down) : r);
 }
 

@@ -170,3 +170,17 @@ def test_weights_whose_products_with_rows_leave_the_range(mqa, dtype, scale, wei
     for x, y, v in zip((q, k), got, w):
         out, tol = plain(x.double().cpu().numpy(), v.double().cpu().numpy(), 0.0, True, inv, pos, False, dtype)
         assert np.abs(out).max() < 1e39 and (np.abs(y.double().cpu().numpy() - out) <= tol).all()
+
+
+@pytest.mark.parametrize("eps", [1e-40, 2.0 ** -149, 1e-38, 1e-30])
+def test_heads_of_zeros_under_the_least_eps(mqa, eps):
+    """0 / sqrt(0 + eps) is 0 for every eps above 0, and heads of such sizes are divided as the formula has it."""
+    import torch
+    q = torch.zeros((5, 3, 64), device="cuda")
+    q[1] = torch.from_numpy(np.random.default_rng(4).standard_normal((3, 64)) * eps ** 0.5).float().cuda()
+    got, _ = mqa.qk_norm_rope(q, q[:, :1], None, None, eps=eps)
+    eps = float(np.float32(eps))
+    out, tol = plain(q.double().cpu().numpy(), 1.0, eps, True, None, None, False, "float32")
+    assert (np.abs(got.double().cpu().numpy() - out) <= tol).all() and not got[0].any() and not got[2:].any()
+    zeros = mqa.qk_norm_rope(q, q[:, :1], None, None, eps=0.0)[0]
+    assert zeros[0].isnan().all() and zeros[1].isfinite().all()
