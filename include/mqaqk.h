@@ -38,7 +38,8 @@ typedef struct mqa_qk_heads {
  * interleaved; components from `rotary` on are not turned.  t is 2 pi times the
  * fraction of positions[r] * turns[i] / 2^64: turns[i] is the pair's frequency in
  * turns per position as a 64-bit fraction, so the product wraps as the angle does
- * and far positions are turned as exactly as near ones (to 2^-32 of a turn).
+ * and far positions are turned as exactly as near ones (the angle is rounded to fp32,
+ * by at most 2^-26 of a turn).
  * All the rest is held in fp32 and rounded once to the rows' type.
  *  type         of rows in and out, MQA_QK_*;  weight_type of both weights
  *  head_dim     64, 128 or 256

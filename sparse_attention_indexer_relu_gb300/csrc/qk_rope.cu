@@ -4,7 +4,7 @@
 // Mathematics.  y = x rsqrt(mean x^2 + eps) w; each pair of y is turned by t = 2 pi
 // frac(position * turns / 2^64).  The product is formed in 64-bit integers, whose
 // wrap is the angle's, so the fraction is exact whatever the position; its upper
-// 32 bits become the argument of sincospi.
+// 32 bits, rounded to fp32 (by at most 2^-26 of a turn), become the argument of sincospi.
 //
 // With r = rsqrt(...) and the weights taken in, a pair (a, b) becomes
 //     (w_a cos) (r a) - (w_b sin) (r b),  (w_b cos) (r b) + (w_a sin) (r a):
