@@ -180,11 +180,6 @@ struct Part {  // a part of an item: tiles [t0, t1) of tiles
   int units;  // of a tile
   Seq q;
 };
-// First position of tile t.
-__device__ __forceinline__ int tile_at(const AttnParams &p, const Part &x, int t) {
-  return (kKind == kWindow && t >= sink_tiles<kKeys>(p) ? t + x.skip : t) * kKeys;
-}
-
 // The CTA's parts, one after another.  Each warp walks by itself; its state lies
 // in shared memory, where lane 0 moves it on (in registers it would crowd out
 // the tiles that are on their way).
