@@ -704,3 +704,91 @@ def test_tiles_of_pages_outside_the_pool(mqa, kind, heads, group, lens, rows, pa
         got = mqa.kv_attention(q, dev, ints(st), lse=lse, scale=scale, **kw)
         assert mqa.kv_status(dev) == 2
         check(got[pick], lse[pick], c.attention(qd[pick], part, scale, "bf16", sees, causal=False), kind)
+
+
+# ---------------------------------------------------------------- windows in the tiled kernel: hard values, repeated, replayed
+BROAD = [  # heads, group, lens, rows: the last block has 128 columns, whose halves take turns; blocks of two full halves
+    (1, 8, [1300], [1200]), (2, 4, [1500, 1400], [700, 640])]
+
+
+def broad(case, window, sinks, rng, dim=128, spread=2):
+    """A cache, and rows whose windows are so much work that the tiled kernel serves them; a sample of the rows."""
+    heads, group, lens, rows = case
+    assert sum(rows) * heads * group * min(1600, window + sinks + sum(rows)) > LITTLE
+    c = ref.random_cache(rng, 200, heads, 16, dim, lens, 100, spread=spread)
+    st, n = starts_of(rows), sum(rows)
+    pick = np.unique(np.concatenate([np.arange(3), rng.integers(0, n, 16), [rows[0] - 1, n - 1]]))
+    part = np.concatenate([[0], np.searchsorted(pick, st[1:])])
+    return c, st, n, pick, part, view.window_seen(c, st, window, sinks)[pick]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", BROAD, ids=str)
+def test_infinite_and_nan_queries_in_broad_windows(mqa, case, dtype):  # noqa: F811
+    rng = np.random.default_rng(50)
+    c, st, n, pick, part, seen = broad(case, 100, 3, rng)
+    q, _ = rows_of(rng, n, c.heads * case[1], 128, dtype)
+    q[0, 1, 5], q[n - 1, 0, 0], q[pick[8], 2, 127] = float("nan"), float("inf"), -float("inf")
+    dev = ref.to_device(c, mqa)
+    got = mqa.kv_attention(q, dev, ints(st), window=100, sinks=3)
+    check(got[pick], None, c.attention(q.double().cpu().numpy()[pick], part, 128 ** -0.5, dtype, seen, causal=False))
+    assert mqa.kv_status(dev) == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("case", BROAD, ids=str)
+def test_scales_far_apart_and_sharp_softmax_in_broad_windows(mqa, case, dim):  # noqa: F811
+    rng = np.random.default_rng(51)
+    c, st, n, pick, part, seen = broad(case, 300, 20, rng, dim, spread=20)
+    attention = lambda q, scale: mqa.kv_attention(q, ref.to_device(c, mqa), ints(st), window=300, sinks=20,  # noqa: E731
+                                                  scale=scale)[pick]
+    plain = lambda qd, scale, dtype: c.attention(qd[pick], part, scale, dtype, seen, causal=False)  # noqa: E731
+    heads = c.heads * case[1]
+    q, qd = rows_of(rng, n, heads, dim, "fp16")
+    g, (out, _, tol, _) = attention(q, 1e-6).double().cpu().numpy(), plain(qd, 1e-6, "fp16")
+    fine, past = np.abs(out) + tol < 65504, np.abs(out) - tol >= 65520  # what rounds to fp16's infinity
+    assert fine.any() and (np.abs(g - out)[fine] <= tol[fine]).all()
+    assert np.array_equal(g[past], np.copysign(np.inf, out[past]))
+    c.ke[:] = 127
+    q, qd = rows_of(rng, n, heads, dim, "bf16", 200.0)  # scores of thousands
+    check(attention(q, dim ** -0.5), None, plain(qd, dim ** -0.5, "bf16"))
+    # values whose scales span 2^120: those within bf16's range are compared
+    c.ve[:] = rng.integers(60, 180, c.ve.shape)
+    q, qd = rows_of(rng, n, heads, dim, "bf16")
+    out, _, tol, _ = plain(qd, 0.01, "bf16")
+    fine = np.abs(out) < 3e38
+    assert fine.any() and (np.abs(attention(q, 0.01).double().cpu().numpy() - out)[fine] <= tol[fine]).all()
+
+
+@pytest.mark.parametrize("case", BROAD, ids=str)
+def test_broad_windows_give_the_same_bits_again(mqa, case):  # noqa: F811
+    """Whatever ran on the workspace before, on two streams at once, and in a graph whose lengths and queries change."""
+    import torch
+    rng = np.random.default_rng(52)
+    c, st, n, pick, part, seen = broad(case, 500, 5, rng)
+    q, qd = rows_of(rng, n, c.heads * case[1], 128, "bf16")
+    dev, sd = ref.to_device(c, mqa), ints(st)
+    ws = [mqa.alloc_kv_workspace(dev, n, c.heads * case[1]) for _ in range(2)]
+    call = lambda q=q, **kw: mqa.kv_attention(q, dev, sd, window=500, sinks=5, **kw)  # noqa: E731
+    first = call(workspace=ws[0])
+    check(first[pick], None, c.attention(qd[pick], part, 128 ** -0.5, "bf16", seen, causal=False))
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for w in ws:
+            w.random_(0, 256)
+        torch.cuda.synchronize()
+        got = [call(workspace=w, stream=s) for w, s in zip(ws, sides)]
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], first) and torch.equal(got[1], first)
+    held, out, graph = torch.zeros_like(q), torch.zeros_like(q), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(held, workspace=ws[0], out=out)
+    for cut in (0, 77, 1):
+        c.lens[:] -= cut
+        dev.seq_lens.copy_(ints(c.lens))
+        held.copy_(q)
+        graph.replay()
+        assert torch.equal(out, call(workspace=ws[1]))
+        seen = view.window_seen(c, st, 500, 5)[pick]
+        check(out[pick], None, c.attention(qd[pick], part, 128 ** -0.5, "bf16", seen, causal=False), cut)
+    assert mqa.kv_status(dev) == 0
