@@ -449,7 +449,7 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
         // all descriptions first: the converters may go ahead of the keys' copies
         for (int u = 0; u < some; ++u) {
           const int slot = (tile_no + u) % kMeta;
-          if (!warp_wait(sm, &sm.m_empty[slot], ((tile_no + u) / kMeta & 1) ^ 1, p)) return;
+          if (!copy_wait(sm, &sm.m_empty[slot], ((tile_no + u) / kMeta & 1) ^ 1, p)) return;
           TileMeta &meta = sm.meta[slot];
           if (lane >> 3 == u) {
             meta.row[g] = row;
@@ -471,13 +471,13 @@ __device__ void lookup_role(const AttnParams &p, const CUtensorMap &map, const C
         for (int u = 0; u < some; ++u, ++tile_no) {
           const int stage = tile_no % kStagesK;
           const uint32_t mine = copies >> (8 * u) & 255u;
-          if (!warp_wait(sm, &sm.k_empty[stage], (tile_no / kStagesK & 1) ^ 1, p)) return;
+          if (!copy_wait(sm, &sm.k_empty[stage], (tile_no / kStagesK & 1) ^ 1, p)) return;
           if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[stage], (uint32_t)(__popc(mine) * box * D));
           __syncwarp();
           if (lane >> 3 == u && (mine >> g & 1))
             tma_load_2d(sm.k[stage] + g * 16 * D, &map, &sm.k_full[stage], 0, row, keep);
           if (tb + u == 0 && !begins) {  // once the previous part's last scores are done
-            if (!warp_wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p)) {
+            if (!copy_wait(sm, &sm.q_empty, (q_no & 1) ^ 1, p)) {
               ++tile_no;  // its copies are under way
               return;
             }

@@ -179,6 +179,15 @@ __device__ __forceinline__ bool warp_wait(S &sm, uint64_t *bar, uint32_t parity,
   __syncwarp();
   return ok;
 }
+// The same for a warp that begins copies once the wait is over: not after a wait of the
+// CTA has run out, for then nobody waits for what is under way, and a barrier could be
+// given a phase's bytes before it has counted those of the one before.
+template <typename S>
+__device__ __forceinline__ bool copy_wait(S &sm, uint64_t *bar, uint32_t parity, const AttnParams &p) {
+  const bool ok = __all_sync(~0u, bounded_wait(sm, bar, parity, p) && *reinterpret_cast<volatile int *>(&sm.dead) == 0);
+  __syncwarp();
+  return ok;
+}
 // For copies and products under way, also after a wait has run out.
 __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
