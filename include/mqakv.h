@@ -195,7 +195,7 @@ int mqa_kv_tree_mask(const mqa_kv_cache *cache, const int32_t *parents, const in
 int mqa_kv_accept(const mqa_kv_cache *cache, const int32_t *row_starts, int rows, const int32_t *counts,
                   const int32_t *accepted, void *stream);
 
-/* Test-only knobs for mqa_kv_attention_debug.  Zero-initialise for defaults. */
+/* Test-only knobs for the entries below.  Zero-initialise for defaults. */
 typedef struct mqa_kv_debug_options {
   int stall;           /* nonzero: dense attention waits for something that never
                           comes: 1 the copies of keys (and values), 2 the lookups
@@ -210,6 +210,13 @@ int mqa_kv_attention_debug(const mqa_kv_cache *cache, const void *q, long long q
                            const int32_t *row_starts, int rows, int max_rows, const int32_t *selected, int n_selected,
                            int causal, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
                            void *stream, const mqa_kv_debug_options *opt);
+
+/* The same of mqa_kv_attention_view: the waits of the kernel for prompts (those of
+ * few columns are the ones of mqa_kv_attention's, and do not stall here). */
+int mqa_kv_attention_view_debug(const mqa_kv_cache *cache, const void *q, long long q_row_stride, int type, int q_heads,
+                                const int32_t *row_starts, int rows, int max_rows, const mqa_kv_view *view, float scale,
+                                void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream,
+                                const mqa_kv_debug_options *opt);
 
 /* Extend sequences: sequence s grows by counts[s] >= 0 positions, with new
  * pages (the lowest free ones, in sequence order, then position order) behind

@@ -340,9 +340,17 @@ int mqa_kv_attention_debug(const mqa_kv_cache *cache, const void *q, long long q
 int mqa_kv_attention_view(const mqa_kv_cache *cache, const void *q, long long q_row_stride, int type, int q_heads,
                           const int32_t *row_starts, int rows, int max_rows, const mqa_kv_view *view, float scale,
                           void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+  return mqa_kv_attention_view_debug(cache, q, q_row_stride, type, q_heads, row_starts, rows, max_rows, view, scale, out,
+                                     lse, workspace, workspace_bytes, stream, nullptr);
+}
+
+int mqa_kv_attention_view_debug(const mqa_kv_cache *cache, const void *q, long long q_row_stride, int type, int q_heads,
+                                const int32_t *row_starts, int rows, int max_rows, const mqa_kv_view *view, float scale,
+                                void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream,
+                                const mqa_kv_debug_options *opt) {
   if (!view) return MQA_ERR_INVALID_ARGUMENT;
   return attention(cache, q, q_row_stride, type, q_heads, row_starts, rows, max_rows, nullptr, 0, 1, view, scale, out,
-                   lse, workspace, workspace_bytes, stream, nullptr);
+                   lse, workspace, workspace_bytes, stream, opt);
 }
 
 int mqa_kv_tree_mask(const mqa_kv_cache *cache, const int32_t *parents, const int32_t *row_starts, int rows,

@@ -1464,11 +1464,9 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &map, const CUtensorMa
 template <>
 cudaError_t launch_kv_prefill<MQA_KV_KIND>(const AttnParams &p, const CUtensorMap &map, const CUtensorMap &q_map,
                                            uint8_t *q8, float *factor, int ctas, cudaStream_t stream) {
-#if MQA_KV_KIND == 0
   if (p.test)
     return p.c.dim == 64 ? launch<64, true>(p, map, q_map, q8, factor, ctas, stream)
                          : launch<128, true>(p, map, q_map, q8, factor, ctas, stream);
-#endif
   return p.c.dim == 64 ? launch<64, false>(p, map, q_map, q8, factor, ctas, stream)
                        : launch<128, false>(p, map, q_map, q8, factor, ctas, stream);
 }

@@ -15,8 +15,8 @@ import math
 from typing import Optional, Sequence
 
 KV_EXPORTS = ("mqa_kv_scratch_bytes", "mqa_kv_append", "mqa_kv_attention_workspace_bytes", "mqa_kv_attention",
-              "mqa_kv_attention_debug", "mqa_kv_attention_view", "mqa_kv_tree_mask", "mqa_kv_accept",
-              "mqa_kv_reserve", "mqa_kv_fork", "mqa_kv_free", "mqa_kv_compact", "mqa_kv_copy_pages",
+              "mqa_kv_attention_debug", "mqa_kv_attention_view", "mqa_kv_attention_view_debug", "mqa_kv_tree_mask",
+              "mqa_kv_accept", "mqa_kv_reserve", "mqa_kv_fork", "mqa_kv_free", "mqa_kv_compact", "mqa_kv_copy_pages",
               "mqa_kv_get_status")
 KV_STATUS_BITS = {1: "out_of_pages", 2: "bad_index", 4: "bad_list", 8: "bad_length", 16: "wait_timeout"}
 KV_PAGE_SIZES = (16, 32, 64, 128)
@@ -54,6 +54,7 @@ def declare(L):
     L.mqa_kv_attention.argtypes = [C, P, Q, I, I, P, I, I, P, I, I, F, P, P, P, S, P]
     L.mqa_kv_attention_debug.argtypes = L.mqa_kv_attention.argtypes + [ctypes.POINTER(KVDebugOptions)]
     L.mqa_kv_attention_view.argtypes = [C, P, Q, I, I, P, I, I, ctypes.POINTER(_View), F, P, P, P, S, P]
+    L.mqa_kv_attention_view_debug.argtypes = L.mqa_kv_attention_view.argtypes + [ctypes.POINTER(KVDebugOptions)]
     L.mqa_kv_tree_mask.argtypes = [C, P, P, I, P, I, P, P]
     L.mqa_kv_accept.argtypes = [C, P, I, P, P, P]
     L.mqa_kv_reserve.argtypes = [C, P, P]

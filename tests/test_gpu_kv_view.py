@@ -792,3 +792,49 @@ def test_broad_windows_give_the_same_bits_again(mqa, case):  # noqa: F811
         seen = view.window_seen(c, st, 500, 5)[pick]
         check(out[pick], None, c.attention(qd[pick], part, 128 ** -0.5, "bf16", seen, causal=False), cut)
     assert mqa.kv_status(dev) == 0
+
+
+# ---------------------------------------------------------------- the waits' time limit
+LIMITS = [  # what rows see, heads, group, dim, type, lens, rows: halves in turns, values staged or not, full halves
+    ("tree", 1, 4, 128, "bf16", [900, 700], [30, 25]), ("tree", 1, 4, 64, "fp16", [900, 700], [30, 25]),
+    ("tree", 1, 4, 128, "fp16", [900, 700], [30, 25]), ("tree", 2, 8, 64, "bf16", [900, 0, 700], [60, 0, 1]),
+    ("window", 1, 8, 128, "bf16", [1300], [1200]), ("window", 2, 4, 64, "fp16", [1500, 1400], [700, 640])]
+
+
+@pytest.mark.parametrize("stall", [1, 2])
+@pytest.mark.parametrize("case", LIMITS, ids=str)
+def test_waits_of_views_end_at_their_limit(mqa, case, stall):  # noqa: F811
+    """A wait for what never comes runs out: the status says so, nothing but the outputs has changed, and the next call on
+    the same workspace answers as if nothing had been."""
+    import ctypes
+
+    import torch
+    from sparse_attention_indexer_relu_gb300 import kv_cache as kv
+    kind, heads, group, dim, dtype, lens, rows = case
+    rng = np.random.default_rng(60)
+    c = ref.random_cache(rng, 220, heads, 16, dim, lens, 100)
+    n, st = sum(rows), ints(starts_of(rows))
+    if kind == "tree":
+        long_tables(c, rows, group)
+        mask = ints(view.tree_mask(c, starts_of(rows), view.random_parents(rng, rows), 2)[0])
+        seen, kw = kv._View(0, 0, mask.data_ptr(), 2), dict(tree=mask)
+    else:
+        assert n * heads * group * min(1600, 103 + n) > LITTLE
+        seen, kw = kv._View(100, 3, None, 0), dict(window=100, sinks=3)
+    dev = ref.to_device(c, mqa)
+    q, _ = rows_of(rng, n, heads * group, dim, dtype)
+    ws = mqa.alloc_kv_workspace(dev, n, heads * group)
+    ws.fill_(0xAB)
+    want, got = mqa.kv_attention(q, dev, st, workspace=ws, **kw), torch.empty_like(q)
+    assert mqa.kv_status(dev) == 0
+
+    def call(**options):
+        mqa._check(mqa.lib().mqa_kv_attention_view_debug(
+            dev._ref, q.data_ptr(), heads * group * dim, kv._types()[q.dtype], heads * group, st.data_ptr(), n, 0,
+            ctypes.byref(seen), dim ** -0.5, got.data_ptr(), None, ws.data_ptr(), ws.numel(),
+            torch.cuda.current_stream().cuda_stream, ctypes.byref(kv.KVDebugOptions(**options))), "view")
+        return mqa.kv_status(dev)
+
+    for _ in range(2):
+        assert call(stall=stall, wait_timeout_ms=30) == 16 and ref.same(c, dev) == []
+        assert call(wait_timeout_ms=500) == 0 and torch.equal(got, want)

@@ -197,3 +197,13 @@ def test_turns():
         mqa.rope_turns(torch.zeros(4, dtype=torch.int64))
     with pytest.raises(TypeError):
         mqa.rope_turns(torch.zeros(4, 2))
+
+
+@pytest.mark.parametrize("opt,code", [(dict(stall=3), 1), (dict(stall=-1), 1), (dict(wait_timeout_ms=10001), 1),
+                                      (dict(wait_timeout_ms=-1), 1)])
+def test_debug_options_of_views_are_checked(opt, code):
+    v = kv._View(5, 0, None, 0)
+    entry = lambda view: mqa.lib().mqa_kv_attention_view_debug(  # noqa: E731
+        ctypes.byref(cache()), P(0x1000), 4096, 0, 32, P(0x2000), 8, 0, view, 0.1, P(0x3000), P(0), P(0x100000), 1 << 40,
+        None, ctypes.byref(kv.KVDebugOptions(**opt)))
+    assert entry(ctypes.byref(v)) == code and entry(None) == 1
