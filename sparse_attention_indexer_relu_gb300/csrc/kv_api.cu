@@ -117,10 +117,13 @@ constexpr int kSplitCols = 16;
 // that work (heads of 128, 4 query heads for each of 8 key/value heads: windows of
 // 1,024, 9 rows 15.5 us against 26.6 tiled, 64: 24.7 and 31.8, 16 x 16: 44.5 and 47.4,
 // work 8.5 M; windows of 4,096, 64 rows: 39.7 and 47.2, work 8.5 M, 128: 62.6 and 46.1,
-// 17 M; heads of 64 alike); and trees of up to kSplitTree columns in all, whose
-// lengths the host does not know (13 rows after 3,001 positions: 21.7 and 27.3, after
-// 32K: 57.6 and 53.0; 104 columns of two sequences of 9,000: 39.2 and 41.2, 208 of four
-// of 3,001: 33.1 and 31.2).
+// 17 M; heads of 64 alike).  How far a tree's rows see the host does not know: the page
+// table's width stands for it, and trees of up to kSplitTree columns in all go to the
+// split kernel under any table (13 rows of 4 query heads per key/value head, 52 columns,
+// after 3,001 positions: 21.7 us against 27.3 tiled; after 32K they lose, 57.6 against
+// 53.0).  A wide table sends larger drafts to the tiled kernel whatever their lengths: 104
+// columns of two sequences of 9,000 take 41.2 us there and 39.2 split, 208 of four of
+// 3,001 31.2 and 33.1.
 constexpr long long kSplitWork = 10000000;
 constexpr int kSplitTree = 64;
 struct AttnPlan {

@@ -53,14 +53,15 @@
 // Scores that a column does not see are hidden in TMEM, in the few tiles that some
 // column sees in part.  Blocks of at most 128 columns have their halves take tiles in
 // turns (in_turns).  A chunk of 2,048 rows, window 4,096, 32 and 8 heads of 128: 157
-// us, 873 TFLOP/s; a tile takes 1.6 us as in dense chunks, but a CTA has 58 of them,
-// 35 to an item, so that the start (10 us for the terms, 7 until the first scores),
-// 2.7 parts of 5 us each (last product, result, next part, first references) and 10
-// us to join are 40% of it.  Five prompts of up to 1,531 rows, window 301, fp16, heads
+// us, 873 TFLOP/s; a tile takes 1.6 us as in dense chunks, and a CTA has 58 of them (93
+// us), 35 to an item; the start (10 us for the terms, 7 until the first scores), 2.7 parts
+// of 5 us each (last product, result, next part, first references) and 10 us to join make
+// it 133, and the rest was not found.  Five prompts of up to 1,531 rows, window 301, fp16, heads
 // of 64: 62 us, 11 tiles in 3.3 parts per CTA.  Drafts of 16 sequences of up to 64 rows
 // after up to 32K positions: 222 us, 865 TFLOP/s, 2.7 TB/s: 3,300 cycles per tile of
 // 256 columns (the same chain as in dense chunks) and 2,150 per tile taken in turns,
-// which the converters bound.
+// which the converters bound.  In fp16 266 us: the third term takes the room in which the
+// others' values are staged.
 #include "kv_ptx.cuh"
 
 #include <cfloat>

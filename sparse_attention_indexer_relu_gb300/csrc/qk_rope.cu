@@ -21,10 +21,11 @@
 //
 // What bounds it.  HBM: each component is read once and written once.  16,384 rows of
 // 32 and 8 heads of 128 in bf16: 336 MB in 58.5 us, 5.74 TB/s, 85% of the measured copy
-// rate; fp32, 8,192 rows: 5.9 TB/s.  Rows of few heads are bound by what a row costs
-// by itself (its angles and factors: 60,000 rows of 2 and 1 heads of 128, 92 MB, 53 us;
-// several rows to a warp: 59).  A kernel in which every head fetched its cosines from
-// shared memory took 113 us (256 instructions per step of two heads, now 113).
+// rate; fp32, 8,192 rows: 5.9 TB/s.  Rows of few heads are bound by latency: a warp
+// has two or three steps of work behind its CTA's chain positions -> angles -> barrier ->
+// weights -> factors (60,000 rows of 2 and 1 heads of 128, 92 MB, 53 us, 1.7 TB/s; several
+// rows to a warp, one after another, which keeps the chain: 59).  A kernel in which every head fetched its cosines from
+// shared memory took 113 us (256 instructions per step of two heads, now 112).
 #include "../../include/mqaqk.h"
 #include "kv_ptx.cuh"
 
