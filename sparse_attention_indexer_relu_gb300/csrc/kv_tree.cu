@@ -94,7 +94,7 @@ __device__ __forceinline__ Asked asked_of(const KvView &c, const int32_t *starts
   return a;
 }
 // A thread's entry of a sequence's list and the one before it, asked for beside the length
-// and the count (entries behind the kept ones are rows of the sequence as well).
+// and the count (those behind the kept ones, which mean nothing, are within the list too).
 struct Entry {
   int at, prev;
 };

@@ -373,9 +373,9 @@ def kv_tree_mask(cache: KVCache, parents, row_starts, max_rows: int, mask=None, 
 
     parents [rows] int32: the row that each row hangs on, as its number among its sequence's rows (an earlier one), or -1
     for the position before them.  max_rows: the most rows of one sequence; the mask has room for as many (up to the next
-    multiple of 32), and rows behind them have no bit, not even in their own masks.  Returns (mask [rows, ceil(max_rows / 32)]
-    int32, positions [rows] int32); a row's position is where it will be if it is accepted.  Rows of no sequence are left
-    as they were."""
+    multiple of 32), and rows behind them have no bit, not even in their own masks.  Returns (mask
+    [rows, ceil(max_rows / 32)] int32, positions [rows] int32); a row's position is where it will be if it is accepted.
+    Rows of no sequence are left as they were."""
     import torch
     m = _api()
     p = _list(parents, cache, "parents")
